@@ -11,6 +11,12 @@ from ._native import (  # noqa: F401
     attn_get_device_status,
     attn_splitkv_workspace_size,
     decode,
+    decode_paged_fp8,
     forward,
+    kvcache_append_paged,
+    kvcache_append_paged_fp8,
+    qk_norm_rope,
+    qk_norm_rope_bwd,
+    rope_table,
     status_string,
 )

@@ -77,6 +77,24 @@ def _open(path):
     L.attn_fwd_splitkv_paged.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, f, i, vp, sz, vp]
     L.attn_fwd_splitkv_noalloc.restype = i
     L.attn_fwd_splitkv_noalloc.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, i, i, f, i, vp]
+    ll = ctypes.c_longlong
+    L.attn_qk_norm_rope.restype = i
+    L.attn_qk_norm_rope.argtypes = [vp, ll, vp, ll, vp, vp, f, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, i, vp]
+    L.attn_qk_norm_rope_bwd_workspace_size.restype = sz
+    L.attn_qk_norm_rope_bwd_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_qk_norm_rope_bwd.restype = i
+    L.attn_qk_norm_rope_bwd.argtypes = [vp, vp, vp, ll, vp, ll, vp, vp, f, vp, vp, i, i, i, vp, vp, vp, vp, vp,
+                                        i, i, i, i, i, vp, sz, vp]
+    append = [vp, ll, vp, ll, vp, vp, vp, i, i, i, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp]
+    L.attn_kvcache_append_paged.restype = i
+    L.attn_kvcache_append_paged.argtypes = append
+    L.attn_kvcache_append_paged_fp8.restype = i
+    L.attn_kvcache_append_paged_fp8.argtypes = append[:6] + [vp, vp] + append[6:]
+    L.attn_splitkv_fp8_chunk.restype = i
+    L.attn_splitkv_fp8_chunk.argtypes = [i, i, i, i, i]
+    L.attn_fwd_splitkv_paged_fp8.restype = i
+    L.attn_fwd_splitkv_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, i, f, i, vp, sz,
+                                             vp]
     L.attn_get_device_status.restype = i
     L.attn_get_device_status.argtypes = [vp]
     L.attn_selftest_wait_timeout.restype = i
@@ -239,6 +257,215 @@ def attn_fwd_splitkv_noalloc(q, k_cache, v_cache, seqlens, o, lse, scale, chunk,
     return lib().attn_fwd_splitkv_noalloc(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), max_seqlen,
                                           _ptr(o), _ptr(lse), B, Hq, Hkv, d, float(scale), int(chunk),
                                           _stream_handle(stream))
+
+
+# --------------------------------------------------------------------------- operators around the attention kernels
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def _call(name, device, stream, *args):
+    """The C call `name` on `device`, whichever is current, on `stream` (None: that device's current stream).
+    Returns the status."""
+    fn = getattr(lib(), name)
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)
+
+
+def _need(name, t, dtype, shape, device):
+    """t is a contiguous tensor of this type and shape on the device; returns its address."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s %s)"
+                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, device):
+    """t [B, N, H, d] bf16 with dense heads and one distance between its token rows (a part of a fused projection's
+    rows); returns (address, that distance)."""
+    B, N, H, d = shape
+    if t.dtype != _BF16 or t.shape != shape or t.device != device:
+        raise ValueError("%s must be a bf16 tensor of shape %s on %s (got %s %s %s)"
+                         % (name, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
+    sb, sn, sh, sd = t.stride()
+    row = sn if N > 1 else (sb if B > 1 else H * d)  # distance of neighbouring tokens, whatever sizes of one say
+    if sd != 1 or (sh != d and H > 1) or (N > 1 and B > 1 and sb != N * sn):
+        raise ValueError("%s must have dense heads and evenly spaced token rows (strides %s)" % (name, t.stride()))
+    return t.data_ptr(), row
+
+
+def _rope_args(rope, interleaved, device):
+    """(cos, sin, max_pos, rot_dim, interleaved) of the C calls; rope: None or (cos, sin) fp32 [max_pos, rot_dim/2]."""
+    if rope is None:
+        return None, None, 0, 0, 0
+    cos, sin = rope
+    shape = cos.shape
+    if len(shape) != 2:
+        raise ValueError("rope tables must be [max_pos, rot_dim / 2]")
+    return (_need("rope cos", cos, _F32, shape, device), _need("rope sin", sin, _F32, shape, device), shape[0],
+            2 * shape[1], int(bool(interleaved)))
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError("a CUDA tensor is wanted (got %s)" % t.device)
+    return t.device
+
+
+def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
+    """Tables (cos, sin) fp32 [max_pos, rot_dim / 2] of the rotation by t * base^(-2i / rot_dim); the angles are
+    formed in 64 bits, so those of far positions keep their accuracy."""
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return a.cos().float(), a.sin().float()
+
+
+def _weight(name, w, d, device):
+    return None if w is None else _need(name, w, _F32, (d,), device)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, interleaved=False, out=None,
+                 stream=None):
+    """Norms of q and k for each head (weights fp32 [d]; None: no norm) and the position rotation, in one pass
+    (attn_qk_norm_rope).  q [B,N,Hq,d], k [B,N,Hkv,d] (or None) bf16, possibly parts of a fused projection's rows;
+    rope: (cos, sin) from rope_table, or None; positions int32 [B,N], or None for 0 .. N-1; out: (q_out, k_out) to
+    write to (q and k themselves where dense), or None.  Returns (q_out, k_out)."""
+    dev = _cuda_device(q)
+    B, N, Hq, d = q.shape
+    Hkv = 0 if k is None else k.shape[2]
+    qp, qs = _rows("q", q, (B, N, Hq, d), dev)
+    kp, ks = (None, 0) if k is None else _rows("k", k, (B, N, Hkv, d), dev)
+    if out is None:
+        qo = torch.empty((B, N, Hq, d), dtype=_BF16, device=dev)
+        ko = None if k is None else torch.empty((B, N, Hkv, d), dtype=_BF16, device=dev)
+    else:
+        qo, ko = out
+        _need("q_out", qo, _BF16, (B, N, Hq, d), dev)
+        if k is not None:
+            _need("k_out", ko, _BF16, (B, N, Hkv, d), dev)
+    pos = None if positions is None else _need("positions", positions, _I32, (B, N), dev)
+    rc = _call("attn_qk_norm_rope", dev, stream, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
+               _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, qo.data_ptr(),
+               None if ko is None else ko.data_ptr(), B, N, Hq, Hkv, d)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_qk_norm_rope")
+    return qo, ko
+
+
+def attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d):
+    return int(lib().attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d))
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None,
+                     interleaved=False, workspace=None, stream=None):
+    """Gradients of qk_norm_rope (attn_qk_norm_rope_bwd): dq_out, dk_out are the gradients of its outputs, the other
+    arguments its own (q, k may be None without a norm).  Returns (dq, dk, dq_weight, dk_weight), None where there
+    is nothing to differentiate."""
+    dev = _cuda_device(dq_out)
+    B, N, Hq, d = dq_out.shape
+    Hkv = 0 if dk_out is None else dk_out.shape[2]
+    gq = _need("dq_out", dq_out, _BF16, (B, N, Hq, d), dev)
+    gk = None if dk_out is None else _need("dk_out", dk_out, _BF16, (B, N, Hkv, d), dev)
+    qp, qs = (None, 0) if q_weight is None else _rows("q", q, (B, N, Hq, d), dev)
+    kp, ks = (None, 0) if k_weight is None else _rows("k", k, (B, N, Hkv, d), dev)
+    dq = torch.empty((B, N, Hq, d), dtype=_BF16, device=dev)
+    dk = None if dk_out is None else torch.empty((B, N, Hkv, d), dtype=_BF16, device=dev)
+    dwq = None if q_weight is None else torch.empty((d,), dtype=_F32, device=dev)
+    dwk = None if k_weight is None else torch.empty((d,), dtype=_F32, device=dev)
+    ws, nbytes = None, 0
+    if dwq is not None or dwk is not None:
+        if workspace is None:
+            nbytes = attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
+        ws = workspace.data_ptr()
+    pos = None if positions is None else _need("positions", positions, _I32, (B, N), dev)
+    rc = _call("attn_qk_norm_rope_bwd", dev, stream, gq, gk, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
+               _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, dq.data_ptr(),
+               None if dk is None else dk.data_ptr(), None if dwq is None else dwq.data_ptr(),
+               None if dwk is None else dwk.data_ptr(), B, N, Hq, Hkv, d, ws, nbytes)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def _append(name, k, v, k_pages, v_pages, scales, block_table, seqlens, rope, interleaved, new_lens, seqlens_out,
+            stream):
+    dev = _cuda_device(k_pages)
+    B, Nn, Hkv, d = k.shape
+    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
+    kp, ks = _rows("k", k, (B, Nn, Hkv, d), dev)
+    vp, vs = _rows("v", v, (B, Nn, Hkv, d), dev)
+    pools = (num_pages, page_size, Hkv, d)
+    dtype = _E4M3 if scales else _BF16
+    args = [kp, ks, vp, vs, _need("k_pages", k_pages, dtype, pools, dev), _need("v_pages", v_pages, dtype, pools, dev)]
+    for what, s in zip(("k_scales", "v_scales"), scales):
+        args.append(_need(what, s, _F32, (num_pages, Hkv), dev))
+    max_blocks = block_table.shape[-1]
+    rc = _call(name, dev, stream, *args, _need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks,
+               page_size, num_pages, _need("seqlens", seqlens, _I32, (B,), dev),
+               None if new_lens is None else _need("new_lens", new_lens, _I32, (B,), dev),
+               None if seqlens_out is None else _need("seqlens_out", seqlens_out, _I32, (B,), dev),
+               *_rope_args(rope, interleaved, dev), B, Nn, Hkv, d)
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+
+
+def kvcache_append_paged(k, v, k_pages, v_pages, block_table, seqlens, rope=None, interleaved=False, new_lens=None,
+                         seqlens_out=None, stream=None):
+    """Appends new tokens' keys (rotated to their position if rope = (cos, sin) is given) and values
+    [B,Nn,Hkv,d] bf16 to a paged bf16 cache in place (attn_kvcache_append_paged); seqlens int32 [B]: the lengths
+    before; new_lens int32 [B]: the real ones of the Nn rows; seqlens_out int32 [B]: receives the lengths after."""
+    _append("attn_kvcache_append_paged", k, v, k_pages, v_pages, (), block_table, seqlens, rope, interleaved,
+            new_lens, seqlens_out, stream)
+
+
+def kvcache_append_paged_fp8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens, rope=None,
+                             interleaved=False, new_lens=None, seqlens_out=None, stream=None):
+    """kvcache_append_paged for float8_e4m3fn pages with fp32 scales [num_pages, Hkv], both updated in place
+    (attn_kvcache_append_paged_fp8)."""
+    _append("attn_kvcache_append_paged_fp8", k, v, k_pages, v_pages, (k_scales, v_scales), block_table, seqlens,
+            rope, interleaved, new_lens, seqlens_out, stream)
+
+
+def attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, max_seqlen):
+    return int(lib().attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, max_seqlen))
+
+
+def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens, scale, chunk=None,
+                     workspace=None, stream=None):
+    """Attention of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over a paged float8_e4m3fn cache with
+    fp32 scales [num_pages, Hkv] (attn_fwd_splitkv_paged_fp8); chunk None: attn_splitkv_fp8_chunk's.
+    Returns (o, lse [B,Hq,Nq])."""
+    dev = _cuda_device(q)
+    B, Nq, Hq, d = q.shape
+    num_pages, page_size, Hkv = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
+    max_blocks = block_table.shape[-1]
+    pools = (num_pages, page_size, Hkv, d)
+    args = (_need("q", q, _BF16, (B, Nq, Hq, d), dev), _need("k_pages", k_pages, _E4M3, pools, dev),
+            _need("v_pages", v_pages, _E4M3, pools, dev), _need("k_scales", k_scales, _F32, (num_pages, Hkv), dev),
+            _need("v_scales", v_scales, _F32, (num_pages, Hkv), dev),
+            _need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks, page_size, num_pages,
+            _need("seqlens", seqlens, _I32, (B,), dev))
+    L = lib()
+    cap = max_blocks * page_size
+    if chunk is None:
+        chunk = L.attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, min(cap, 0x7fffffff))
+    o = torch.empty((B, Nq, Hq, d), dtype=_BF16, device=dev)
+    lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
+    if workspace is None:
+        n = L.attn_splitkv_workspace_size(B, Nq * Hq, min(cap, 0x7fffffff), d, chunk)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    rc = _call("attn_fwd_splitkv_paged_fp8", dev, stream, *args, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
+               scale, chunk, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_splitkv_paged_fp8")
+    return o, lse
 
 
 def attn_get_device_status(stream=None):

@@ -43,6 +43,26 @@ bool make_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace attn {
+
+bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)Hkv * d, (cuuint64_t)page_size * Hkv * d};
+  const cuuint32_t box[4] = {(cuuint32_t)d, 1u, (cuuint32_t)box_rows, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace attn
+
+namespace {
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr double kLog2e = 1.4426950408889634;
@@ -288,16 +308,22 @@ attn_status attn_probe_read_bandwidth(const void* buf, size_t bytes, unsigned lo
 attn_status attn_get_device_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  uint32_t w_prefill = 0, w_decode = 0, w_selftest = 0;
+  uint32_t w_prefill = 0, w_decode = 0, w_selftest = 0, w_rope = 0, w_append = 0, w_fp8 = 0;
   if (attn::fetch_status_prefill(s, &w_prefill) != cudaSuccess) return ATTN_ERR_LAUNCH;
   if (attn::fetch_status_decode(s, &w_decode) != cudaSuccess) return ATTN_ERR_LAUNCH;
   if (attn::fetch_status_selftest(s, &w_selftest) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  const uint32_t w = w_prefill ? w_prefill : (w_decode ? w_decode : w_selftest);
+  if (attn::fetch_status_rope(s, &w_rope) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  if (attn::fetch_status_append(s, &w_append) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  if (attn::fetch_status_decode_fp8(s, &w_fp8) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  uint32_t w = 0;
+  for (uint32_t x : {w_prefill, w_decode, w_selftest, w_fp8, w_append, w_rope})
+    if (!w) w = x;
   switch (w & 0xffu) {
     case 0: return ATTN_OK;
     case attn::kDevTimeout: return ATTN_ERR_TIMEOUT;
     case attn::kDevBadSeqlen:
-    case attn::kDevBadPage: return ATTN_ERR_DEVICE_ARG;
+    case attn::kDevBadPage:
+    case attn::kDevBadPosition: return ATTN_ERR_DEVICE_ARG;
     default: return ATTN_ERR_LAUNCH;
   }
 }

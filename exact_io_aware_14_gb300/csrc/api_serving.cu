@@ -1,0 +1,300 @@
+// extern "C" boundary of the operators around the attention kernels: norms
+// and rotation of queries and keys, appending to a paged cache, decode over a
+// paged e4m3 cache.  Argument checks and dispatch; declared in include/attn.h.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "launch.h"
+
+namespace {
+
+constexpr long long kIntMax = 0x7fffffffLL;
+constexpr double kLog2e = 1.4426950408889634;
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+attn_status check_rope(const float* cosv, const float* sinv, int max_pos, int rot_dim, int interleaved, int d) {
+  if (rot_dim < 0 || rot_dim > d || interleaved < 0 || interleaved > 1) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim == 0) return ATTN_OK;
+  if (!cosv || !sinv || max_pos < 1) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (off16(cosv) || off16(sinv)) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+attn::RopeParams rope_params(const float* cosv, const float* sinv, int max_pos, int rot_dim, int interleaved) {
+  return {cosv, sinv, max_pos, rot_dim, interleaved};
+}
+
+// One of the two tensors of the norm-and-rotation calls: H heads, rows
+// `stride` elements apart.  `read`: whether the call reads x.
+attn_status check_rows(const void* x, long long stride, int H, int d, bool read) {
+  if (!read) return ATTN_OK;
+  if (!x || stride < static_cast<long long>(H) * d) return ATTN_ERR_INVALID_ARG;
+  if (stride % 8 != 0 || off16(x)) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+// Sizes shared by the forward and backward norm-and-rotation calls.
+attn_status check_qk_sizes(int B, int N, int Hq, int Hkv, int d) {
+  if (B < 1 || N < 0 || Hq < 1 || Hkv < 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const long long tokens = static_cast<long long>(B) * N;
+  if (tokens > kIntMax || static_cast<long long>(Hq) + Hkv > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  // grid: one block per 256 threads, d/16 threads a row at most
+  if (tokens * (static_cast<long long>(Hq) + Hkv) > kIntMax * 16) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status check_append(const void* k, long long k_stride, const void* v, long long v_stride, const void* k_pages,
+                         const void* v_pages, const int* block_table, int max_blocks, int page_size, int num_pages,
+                         const int* seqlens, const int* new_lens, const int* seqlens_out, int B, int Nn, int Hkv,
+                         int d) {
+  if (B < 1 || Nn < 0 || Hkv < 1 || max_blocks < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (page_size < 64 || page_size % 64 != 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  const long long cap = static_cast<long long>(max_blocks) * page_size;
+  if (cap + Nn + page_size > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if ((static_cast<long long>(Nn) / page_size + 2) * Hkv > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(Nn) * Hkv * (d / 16) > kIntMax * 256) return ATTN_ERR_UNSUPPORTED;
+  if (!seqlens || !block_table || !k_pages || !v_pages) return ATTN_ERR_INVALID_ARG;
+  if (seqlens_out && seqlens_out == seqlens) return ATTN_ERR_INVALID_ARG;
+  if (Nn > 0) {
+    attn_status st = check_rows(k, k_stride, Hkv, d, true);
+    if (st == ATTN_OK) st = check_rows(v, v_stride, Hkv, d, true);
+    if (st != ATTN_OK) return st;
+  }
+  if (off16(k_pages) || off16(v_pages) || off4(block_table) || off4(seqlens) || (new_lens && off4(new_lens)) ||
+      (seqlens_out && off4(seqlens_out)))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+attn_status append(const void* k, long long k_stride, const void* v, long long v_stride, void* k_pages, void* v_pages,
+                   float* k_scales, float* v_scales, const int* block_table, int max_blocks, int page_size,
+                   int num_pages, const int* seqlens, const int* new_lens, int* seqlens_out, const float* rope_cos,
+                   const float* rope_sin, int max_pos, int rot_dim, int interleaved, int B, int Nn, int Hkv, int d,
+                   void* stream) {
+  attn_status st = check_append(k, k_stride, v, v_stride, k_pages, v_pages, block_table, max_blocks, page_size,
+                                num_pages, seqlens, new_lens, seqlens_out, B, Nn, Hkv, d);
+  if (st == ATTN_OK) st = check_rope(rope_cos, rope_sin, max_pos, rot_dim, interleaved, d);
+  if (st != ATTN_OK) return st;
+  attn::AppendParams p;
+  std::memset(&p, 0, sizeof p);
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.new_lens = new_lens;
+  p.seqlens_out = seqlens_out;
+  p.rope = rope_params(rope_cos, rope_sin, max_pos, rot_dim, interleaved);
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nn = Nn;
+  p.Hkv = Hkv;
+  p.d = d;
+  return attn::launch_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                              const float* q_weight, const float* k_weight, float eps, const float* rope_cos,
+                              const float* rope_sin, int max_pos, int rot_dim, int interleaved, const int* positions,
+                              void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int d, void* stream) {
+  attn_status st = check_qk_sizes(B, N, Hq, Hkv, d);
+  if (st == ATTN_OK) st = check_rope(rope_cos, rope_sin, max_pos, rot_dim, interleaved, d);
+  if (st != ATTN_OK) return st;
+  if ((q_weight || k_weight) && !(std::isfinite(eps) && eps > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (N == 0) return ATTN_OK;
+  st = check_rows(q, q_stride, Hq, d, true);
+  if (st == ATTN_OK) st = check_rows(k, k_stride, Hkv, d, Hkv > 0);
+  if (st != ATTN_OK) return st;
+  if (!q_out || (Hkv > 0 && !k_out)) return ATTN_ERR_INVALID_ARG;
+  // in place only where the rows lie as the output's
+  if ((q_out == q && q_stride != static_cast<long long>(Hq) * d) ||
+      (Hkv > 0 && k_out == k && k_stride != static_cast<long long>(Hkv) * d))
+    return ATTN_ERR_INVALID_ARG;
+  if (off16(q_out) || (Hkv > 0 && off16(k_out)) || off16(q_weight) || off16(k_weight) || off4(positions))
+    return ATTN_ERR_MISALIGNED;
+  attn::QkNormRopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q;
+  p.k = k;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.rope = rope_params(rope_cos, rope_sin, max_pos, rot_dim, interleaved);
+  p.positions = positions;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  return attn::launch_qk_norm_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int Hkv, int d) {
+  if (check_qk_sizes(B, N, Hq, Hkv, d) != ATTN_OK) return 0;
+  int nbq, nbk;
+  attn::qk_norm_rope_bwd_blocks(B, N, Hq, Hkv, d, &nbq, &nbk);
+  return static_cast<size_t>(nbq + nbk) * d * sizeof(float);
+}
+
+attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, long long q_stride,
+                                  const void* k, long long k_stride, const float* q_weight, const float* k_weight,
+                                  float eps, const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim,
+                                  int interleaved, const int* positions, void* dq, void* dk, float* dq_weight,
+                                  float* dk_weight, int B, int N, int Hq, int Hkv, int d, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  attn_status st = check_qk_sizes(B, N, Hq, Hkv, d);
+  if (st == ATTN_OK) st = check_rope(rope_cos, rope_sin, max_pos, rot_dim, interleaved, d);
+  if (st != ATTN_OK) return st;
+  const bool norm = q_weight || k_weight;
+  if (norm && !(std::isfinite(eps) && eps > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (Hkv == 0 && k_weight) return ATTN_ERR_INVALID_ARG;
+  if (N == 0 && !norm) return ATTN_OK;
+  if (N > 0) {
+    st = check_rows(q, q_stride, Hq, d, q_weight != nullptr);
+    if (st == ATTN_OK) st = check_rows(k, k_stride, Hkv, d, k_weight != nullptr);
+    if (st != ATTN_OK) return st;
+    if (!dq_out || !dq || (Hkv > 0 && (!dk_out || !dk))) return ATTN_ERR_INVALID_ARG;
+    if (off16(dq_out) || off16(dq) || (Hkv > 0 && (off16(dk_out) || off16(dk)))) return ATTN_ERR_MISALIGNED;
+  }
+  if (off16(q_weight) || off16(k_weight) || off4(dq_weight) || off4(dk_weight) || off4(positions))
+    return ATTN_ERR_MISALIGNED;
+  if (norm && (!workspace || off16(workspace) ||
+               workspace_bytes < attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)))
+    return ATTN_ERR_WORKSPACE;
+  attn::QkNormRopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q;
+  p.k = k;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.rope = rope_params(rope_cos, rope_sin, max_pos, rot_dim, interleaved);
+  p.positions = positions;
+  p.dq_out = dq_out;
+  p.dk_out = dk_out;
+  p.dq = dq;
+  p.dk = dk;
+  p.dq_weight = dq_weight;
+  p.dk_weight = dk_weight;
+  p.dw_part = static_cast<float*>(workspace);
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  return attn::launch_qk_norm_rope_bwd(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                             : ATTN_ERR_LAUNCH;
+}
+
+attn_status attn_kvcache_append_paged(const void* k, long long k_stride, const void* v, long long v_stride,
+                                      void* k_pages, void* v_pages, const int* block_table, int max_blocks,
+                                      int page_size, int num_pages, const int* seqlens, const int* new_lens,
+                                      int* seqlens_out, const float* rope_cos, const float* rope_sin, int max_pos,
+                                      int rot_dim, int interleaved, int B, int Nn, int Hkv, int d, void* stream) {
+  return append(k, k_stride, v, v_stride, k_pages, v_pages, nullptr, nullptr, block_table, max_blocks, page_size,
+                num_pages, seqlens, new_lens, seqlens_out, rope_cos, rope_sin, max_pos, rot_dim, interleaved, B, Nn,
+                Hkv, d, stream);
+}
+
+attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_stride, const void* v, long long v_stride,
+                                          void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                                          const int* block_table, int max_blocks, int page_size, int num_pages,
+                                          const int* seqlens, const int* new_lens, int* seqlens_out,
+                                          const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim,
+                                          int interleaved, int B, int Nn, int Hkv, int d, void* stream) {
+  if (!k_scales || !v_scales) return ATTN_ERR_INVALID_ARG;
+  if (off4(k_scales) || off4(v_scales)) return ATTN_ERR_MISALIGNED;
+  return append(k, k_stride, v, v_stride, k_pages, v_pages, k_scales, v_scales, block_table, max_blocks, page_size,
+                num_pages, seqlens, new_lens, seqlens_out, rope_cos, rope_sin, max_pos, rot_dim, interleaved, B, Nn,
+                Hkv, d, stream);
+}
+
+int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen) {
+  if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_seqlen < 1) return 0;
+  return 1024;
+}
+
+attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                       const float* v_scales, const int* block_table, int max_blocks, int page_size,
+                                       int num_pages, const int* seqlens, void* o, float* lse, int B, int Nq, int Hq,
+                                       int Hkv, int d, float scale, int chunk, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (max_blocks < 1 || num_pages < 1 || page_size < 64 || page_size % 64 != 0) return ATTN_ERR_INVALID_ARG;
+  if (chunk < 64 || chunk % 64 != 0 || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const long long cap = static_cast<long long>(max_blocks) * page_size;
+  if (cap + Nq + 256 > kIntMax || Nq > 64 || B > 65535 || (cap + chunk - 1) / chunk > 65535 ||
+      static_cast<long long>(Nq) * Hq > 65535)
+    return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Nq * Hq > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !block_table || !seqlens || !o || !lse)
+    return ATTN_ERR_INVALID_ARG;
+  if (off16(q) || off16(k_pages) || off16(v_pages) || off16(o) || off4(k_scales) || off4(v_scales) ||
+      off4(block_table) || off4(seqlens) || off4(lse))
+    return ATTN_ERR_MISALIGNED;
+  const int max_seqlen = static_cast<int>(cap);
+  if (!workspace || off16(workspace) ||
+      workspace_bytes < attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk))
+    return ATTN_ERR_WORKSPACE;
+  attn::DecodeFp8Params p;
+  std::memset(&p, 0, sizeof p);
+  if (!attn::make_map_e4m3(&p.tm_k, k_pages, num_pages, page_size, Hkv, d, 64) ||
+      !attn::make_map_e4m3(&p.tm_v, v_pages, num_pages, page_size, Hkv, d, 64))
+    return ATTN_ERR_LAUNCH;
+  p.q = q;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.o = o;
+  p.lse = lse;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.max_seqlen = max_seqlen;
+  p.chunk = chunk;
+  p.n_split = static_cast<int>((cap + chunk - 1) / chunk);
+  const size_t parts = static_cast<size_t>(B) * Nq * Hq * p.n_split;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts * d * sizeof(float));
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  return attn::launch_decode_fp8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // extern "C"

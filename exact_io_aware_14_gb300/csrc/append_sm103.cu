@@ -1,0 +1,300 @@
+// Appending keys and values of new tokens to a paged cache, keys rotated to
+// their position on the way, for sm_103a: a bf16 cache, or e4m3 codes with
+// one scale for each page and KV head.
+//
+// New row i of sequence b goes to position pos = seqlens[b] + i, that is row
+// pos % page_size of page block_table[b][pos / page_size].
+//
+// 8-bit form.  value = code * scale, the scale a power of two: the smallest
+// s with amax <= 448.5 s (448 is e4m3's largest value and 448.5 rounds to
+// it), amax the largest magnitude that the page's rows of this head hold, at
+// least 2^-100.  A power of two makes the division by it exact, so a new
+// value is rounded once, and an older code whose page's scale is raised is
+// divided by a power of two: exact but for codes that fall below e4m3's
+// smallest normal value.  A page that starts with this call (its row 0 is
+// new) takes its scale from the new rows alone; otherwise
+// max(its scale, the new rows' scale).
+//
+// Both are bound by memory: one read of the new rows, one write of the cache
+// rows; single tokens by latency.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace attn {
+namespace {
+
+__device__ uint32_t g_append_status;
+
+__device__ __forceinline__ void record(uint32_t site, uint32_t code) {
+  atomicCAS(&g_append_status, 0u, (site << 8) | code);
+}
+
+// Cache length before the call and new rows of sequence b, clamped to what
+// the cache holds.
+struct Span {
+  int len, n;
+};
+__device__ __forceinline__ Span span_of(const AppendParams& p, int b, bool report) {
+  const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
+  int len = p.seqlens[b], n = p.new_lens ? p.new_lens[b] : p.Nn;
+  const bool bad = len < 0 || len > cap || n < 0 || n > p.Nn;
+  len = len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
+  n = n < 0 ? 0 : (n > p.Nn ? p.Nn : n);
+  const bool full = len + static_cast<long long>(n) > cap;
+  if (full) n = static_cast<int>(cap - len);
+  if (report && (bad || full)) record(1, kDevBadSeqlen);
+  return {len, n};
+}
+
+// Page of block blk of sequence b, or -1 (recorded; nothing is written there).
+__device__ __forceinline__ int page_of(const AppendParams& p, int b, int blk) {
+  const int pg = p.block_table[static_cast<long long>(b) * p.max_blocks + blk];
+  if (pg < 0 || pg >= p.num_pages) {
+    record(2, kDevBadPage);
+    return -1;
+  }
+  return pg;
+}
+
+__device__ __forceinline__ int checked_pos(int pos, int max_pos) {
+  if (pos >= max_pos) {
+    record(3, kDevBadPosition);
+    return max_pos - 1;
+  }
+  return pos;
+}
+
+// ---------------------------------------------------------------------------
+// bf16 cache: D/16 threads hold one head's K and V row; kHeads heads of a
+// token share its cosines and sines.
+constexpr int kThreads = 256;
+
+template <int D, int kHeads, bool kInter>
+__global__ void __launch_bounds__(kThreads) append_bf16_kernel(const AppendParams p, int per) {
+  constexpr int kTPR = D / 16;
+  const int l = threadIdx.x % kTPR;
+  const int b = blockIdx.y;
+  const long long i = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTPR;
+  const Span s = span_of(p, b, blockIdx.x == 0 && threadIdx.x == 0);
+  if (p.seqlens_out && blockIdx.x == 0 && threadIdx.x == 0) p.seqlens_out[b] = s.len + s.n;
+  const int row = static_cast<int>(i / per);
+  const int h0 = static_cast<int>(i % per) * kHeads;
+  if (row >= s.n) return;
+  const int nh = min(kHeads, p.Hkv - h0);
+  const long long token = static_cast<long long>(b) * p.Nn + row;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + token * p.k_stride + static_cast<long long>(h0) * D;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + token * p.v_stride + static_cast<long long>(h0) * D;
+  const int2 ch = row_chunks(l, p.rope.rot);
+  uint4 rk[kHeads][2], rv[kHeads][2];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    if (h < nh) {
+      rk[h][0] = *reinterpret_cast<const uint4*>(k + h * D + 8 * ch.x);
+      rk[h][1] = *reinterpret_cast<const uint4*>(k + h * D + 8 * ch.y);
+      rv[h][0] = *reinterpret_cast<const uint4*>(v + h * D + 8 * ch.x);
+      rv[h][1] = *reinterpret_cast<const uint4*>(v + h * D + 8 * ch.y);
+    }
+  }
+  const int pos = s.len + row;
+  const int pg = page_of(p, b, pos / p.page_size);
+  Angles ang;
+  if (p.rope.rot > 0) load_angles(p.rope, checked_pos(pos, p.rope.max_pos), l, ang);
+  if (pg < 0) return;
+  const long long dst = ((static_cast<long long>(pg) * p.page_size + pos % p.page_size) * p.Hkv + h0) * D;
+  __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(p.k_pages) + dst;
+  __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(p.v_pages) + dst;
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    if (h >= nh) break;
+    if (p.rope.rot > 0 && l < (p.rope.rot >> 4)) {
+      float x[16];
+      unpack8(rk[h][0], x);
+      unpack8(rk[h][1], x + 8);
+      rotate16<kInter, false>(x, ang);
+      rk[h][0] = pack8(x);
+      rk[h][1] = pack8(x + 8);
+    }
+    *reinterpret_cast<uint4*>(ko + h * D + 8 * ch.x) = rk[h][0];
+    *reinterpret_cast<uint4*>(ko + h * D + 8 * ch.y) = rk[h][1];
+    *reinterpret_cast<uint4*>(vo + h * D + 8 * ch.x) = rv[h][0];
+    *reinterpret_cast<uint4*>(vo + h * D + 8 * ch.y) = rv[h][1];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// e4m3 cache.  One block per (touched page, KV head, K or V, sequence): it
+// alone writes that page's codes and scale of the head, so no two blocks meet.
+
+// Bits of |x|, 0 where x is not finite (such a value takes no part in the
+// scale and is stored as NaN).
+__device__ __forceinline__ uint32_t abs_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+// Exponent of the scale for largest magnitude amax (given by its bits):
+// amax <= 448.5 * 2^e, 448.5 = 0x1.c08p8.
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x604000u ? 1 : 0);
+  return max(e, -100);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Two floats -> two e4m3 codes (nearest, ties to even), `lo` in the low byte.
+// Infinities become NaN: e4m3 has none, and saturating would hide them.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  uint32_t u = r;
+  if (!(fabsf(lo) < INFINITY)) u = (u & 0xff00u) | 0x7fu;
+  if (!(fabsf(hi) < INFINITY)) u = (u & 0x00ffu) | 0x7f00u;
+  return u;
+}
+__device__ __forceinline__ uint2 e4m3x8(const float* x, float inv) {
+  return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
+                    e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
+}
+// One e4m3 pair -> two floats (through f16, which holds every e4m3 value).
+__device__ __forceinline__ float2 from_e4m3x2(uint16_t u) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(u));
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  return make_float2(lo, hi);
+}
+// Four codes times f (a power of two), rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  const float2 a = from_e4m3x2(static_cast<uint16_t>(w & 0xffffu)), b = from_e4m3x2(static_cast<uint16_t>(w >> 16));
+  return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
+}
+
+template <int D, int kBlock, bool kInter>
+__global__ void __launch_bounds__(kBlock) append_e4m3_kernel(const AppendParams p) {
+  constexpr int kTPR = D / 16;
+  constexpr int kRows = kBlock / kTPR;  // rows a round of the block covers
+  const int b = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int h = blockIdx.x % p.Hkv, j = blockIdx.x / p.Hkv;
+  const bool first = blockIdx.x == 0 && !is_v && threadIdx.x == 0;
+  const Span s = span_of(p, b, first);
+  if (p.seqlens_out && first) p.seqlens_out[b] = s.len + s.n;
+  if (s.n == 0) return;
+  const int blk = s.len / p.page_size + j;
+  if (blk >= p.max_blocks) return;
+  const int start = blk * p.page_size;  // position of the page's row 0
+  const int lo = max(s.len, start) - start;
+  const int hi = static_cast<int>(min(static_cast<long long>(s.len) + s.n - start, static_cast<long long>(p.page_size)));
+  if (hi <= lo) return;  // past the last touched page
+  const int pg = page_of(p, b, blk);
+  if (pg < 0) return;
+  const RopeParams& rope = p.rope;
+  const int l = threadIdx.x % kTPR, r0 = threadIdx.x / kTPR;
+  const int2 ch = row_chunks(l, rope.rot);
+  const bool turn = !is_v && rope.rot > 0 && l < (rope.rot >> 4);
+  const long long stride = is_v ? p.v_stride : p.k_stride;
+  // row r of the page is new row start + r - len of the sequence
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
+                             (static_cast<long long>(b) * p.Nn + start - s.len) * stride + static_cast<long long>(h) * D;
+  const long long pitch = static_cast<long long>(p.Hkv) * D;
+  uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + static_cast<long long>(pg) * p.page_size * pitch +
+                 static_cast<long long>(h) * D;
+  float* scale = (is_v ? p.v_scales : p.k_scales) + static_cast<long long>(pg) * p.Hkv + h;
+  const float was = lo > 0 ? *scale : 0.f;
+
+  auto load_row = [&](int r, float* x) {
+    const __nv_bfloat16* row = src + r * stride;
+    unpack8(*reinterpret_cast<const uint4*>(row + 8 * ch.x), x);
+    unpack8(*reinterpret_cast<const uint4*>(row + 8 * ch.y), x + 8);
+    if (turn) {
+      Angles ang;
+      load_angles(rope, checked_pos(start + r, rope.max_pos), l, ang);
+      rotate16<kInter, false>(x, ang);
+    }
+  };
+
+  uint32_t amax = 0u;
+  for (int r = lo + r0; r < hi; r += kRows) {
+    float x[16];
+    load_row(r, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max(amax, abs_bits(x[i]));
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  __shared__ uint32_t s_max[kBlock / 32];
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
+  __syncthreads();  // also: every thread has read the old scale before it is written
+#pragma unroll
+  for (int w = 0; w < kBlock / 32; ++w) amax = max(amax, s_max[w]);
+  const int e = scale_exp(amax);
+  const float now = fmaxf(was, pow2(e));
+  const float inv = 1.f / now;  // exact: a power of two
+  if (threadIdx.x == 0) *scale = now;
+  if (lo > 0 && now != was) {
+    const float f = was * inv;
+    for (int i = threadIdx.x; i < lo * (D / 16); i += kBlock) {
+      uint4* q = reinterpret_cast<uint4*>(dst + static_cast<long long>(i / (D / 16)) * pitch + (i % (D / 16)) * 16);
+      uint4 u = *q;
+      u.x = rescale4(u.x, f);
+      u.y = rescale4(u.y, f);
+      u.z = rescale4(u.z, f);
+      u.w = rescale4(u.w, f);
+      *q = u;
+    }
+  }
+  for (int r = lo + r0; r < hi; r += kRows) {
+    float x[16];
+    load_row(r, x);
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.x) = e4m3x8(x, inv);
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.y) = e4m3x8(x + 8, inv);
+  }
+}
+
+constexpr int kHeads = 4;
+
+template <int D>
+cudaError_t launch_bf16(const AppendParams& p, cudaStream_t stream) {
+  const int per = (p.Hkv + kHeads - 1) / kHeads;
+  const long long threads = static_cast<long long>(p.Nn) * per * (D / 16);
+  // one block at least: it writes seqlens_out
+  const long long blocks = threads > 0 ? (threads + kThreads - 1) / kThreads : 1;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B));
+  if (p.rope.inter)
+    append_bf16_kernel<D, kHeads, true><<<grid, kThreads, 0, stream>>>(p, per);
+  else
+    append_bf16_kernel<D, kHeads, false><<<grid, kThreads, 0, stream>>>(p, per);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_e4m3(const AppendParams& p, cudaStream_t stream) {
+  const int pages = static_cast<int>((static_cast<long long>(p.Nn) + p.page_size - 2) / p.page_size) + 1;
+  const dim3 grid(static_cast<unsigned>(pages) * p.Hkv, static_cast<unsigned>(p.B), 2u);
+  if (p.rope.inter)
+    append_e4m3_kernel<D, 256, true><<<grid, 256, 0, stream>>>(p);
+  else
+    append_e4m3_kernel<D, 256, false><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+  if (p.k_scales) return p.d == 64 ? launch_e4m3<64>(p, stream) : launch_e4m3<128>(p, stream);
+  return p.d == 64 ? launch_bf16<64>(p, stream) : launch_bf16<128>(p, stream);
+}
+
+cudaError_t fetch_status_append(cudaStream_t stream, uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_append_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(g_append_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e;
+}
+
+}  // namespace attn

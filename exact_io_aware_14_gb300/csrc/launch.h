@@ -7,12 +7,14 @@
 #include <cuda_runtime.h>
 
 #include "../../include/attn.h"
+#include "rope.cuh"
 
 namespace attn {
 
 // Device status codes.  Kernels never trap: a wait that runs out of time
 // records (site << 8) | code in the unit's status word and the kernel unwinds.
-enum DeviceCode : uint32_t { kDevOk = 0, kDevTimeout = 5, kDevBadSeqlen = 6, kDevBadPage = 7 };
+enum DeviceCode : uint32_t { kDevOk = 0, kDevTimeout = 5, kDevBadSeqlen = 6, kDevBadPage = 7,
+                             kDevBadPosition = 8 };
 
 struct PrefillParams {
   CUtensorMap tm_q, tm_k, tm_v;  // 4-D maps {d, H, N, B}, box {64, 1, 128, 1}, 128-B swizzle
@@ -49,6 +51,76 @@ attn_status check_splitkv_args(const void* q, const void* k, const void* v, cons
                                const int* block_table, int page_size, const void* o, const float* lse, int B, int Hq,
                                int Hkv, int d, float scale, int chunk);
 
+// Map of an e4m3 page pool {d, Hkv, page_size, num_pages}: box {d, 1, rows, 1}
+// of bytes, swizzle as wide as a head row (64 or 128 bytes).  False on failure.
+bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d, int box_rows);
+
+// Norms and rotation of queries and keys.  Token rows of q and k are q_stride
+// and k_stride elements apart; outputs and gradients are dense.
+struct QkNormRopeParams {
+  const void* q;
+  const void* k;
+  long long q_stride, k_stride;
+  const float* q_weight;  // null: no norm
+  const float* k_weight;
+  float eps;
+  RopeParams rope;
+  const int* positions;  // [B, N], or null: 0 .. N-1
+  void* q_out;           // forward
+  void* k_out;
+  const void* dq_out;    // backward
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dq_weight;
+  float* dk_weight;
+  float* dw_part;  // [blocks, d] partial sums
+  int B, N, Hq, Hkv, d;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(const QkNormRopeParams& p, cudaStream_t stream);
+// Blocks of the backward kernel that walk q's rows and k's rows.
+void qk_norm_rope_bwd_blocks(int B, int N, int Hq, int Hkv, int d, int* nbq, int* nbk);
+
+// Appending to a paged cache; bf16 pages, or e4m3 pages with scales.
+struct AppendParams {
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;  // null: bf16 pages
+  float* v_scales;
+  const int* block_table;
+  const int* seqlens;
+  const int* new_lens;  // null: Nn each
+  int* seqlens_out;     // null: not wanted
+  RopeParams rope;
+  int max_blocks, page_size, num_pages;
+  int B, Nn, Hkv, d;
+};
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
+
+// Split-KV decode over a paged e4m3 cache.
+struct DecodeFp8Params {
+  CUtensorMap tm_k, tm_v;
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const float* k_scales;
+  const float* v_scales;
+  const int* block_table;
+  const int* seqlens;
+  void* o;
+  float* lse;
+  float* o_part;    // [B, Nq, Hq, n_split, d]
+  float* lse_part;  // [B, Nq, Hq, n_split]
+  int max_blocks, page_size, num_pages;
+  int B, Nq, Hq, Hkv, d, max_seqlen, chunk, n_split;
+  float scale_log2;
+};
+cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream);
+
 // Reads and clears the device status word of each kernel unit (stream-ordered,
 // then synchronises the stream).  Returns the first non-zero word, or 0.
 cudaError_t fetch_status_prefill(cudaStream_t stream, uint32_t* out);
@@ -57,5 +129,8 @@ cudaError_t launch_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream)
 cudaError_t launch_selftest_exp2_poly(const float* x, float* y, long long n, cudaStream_t stream);
 cudaError_t launch_read_probe(const void* buf, long long n16, unsigned long long* sink, cudaStream_t stream);
 cudaError_t fetch_status_selftest(cudaStream_t stream, uint32_t* out);
+cudaError_t fetch_status_rope(cudaStream_t stream, uint32_t* out);
+cudaError_t fetch_status_append(cudaStream_t stream, uint32_t* out);
+cudaError_t fetch_status_decode_fp8(cudaStream_t stream, uint32_t* out);
 
 }  // namespace attn

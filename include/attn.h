@@ -62,7 +62,7 @@ typedef enum {
   ATTN_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned */
   ATTN_ERR_LAUNCH = 4,       /* the CUDA runtime refused a launch or a query */
   ATTN_ERR_TIMEOUT = 5,      /* device: a pipeline wait gave up (reported later) */
-  ATTN_ERR_DEVICE_ARG = 6,   /* device: a cache length or page index was out of range */
+  ATTN_ERR_DEVICE_ARG = 6,   /* device: a cache length, page index or position was out of range */
   ATTN_ERR_WORKSPACE = 7     /* workspace missing or smaller than required */
 } attn_status;
 
@@ -234,6 +234,152 @@ ATTN_API attn_status attn_fwd_splitkv_noalloc(const void* q, const void* k_cache
                                               void* o, float* lse,
                                               int B, int Hq, int Hkv, int d, float scale, int chunk,
                                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the attention kernels.  The pages have no counterpart to
+ * these; they are what a program runs before attn_fwd (norms and rotation of
+ * q and k) and around a decode step (the new tokens go into the paged cache,
+ * which may be held in 8 bits).
+ *
+ * Position rotation (rope_cos, rope_sin, max_pos, rot_dim, interleaved): the
+ * first rot_dim of a head's d values are rotated in pairs, pair i of a token
+ * at position t by the angle whose cosine and sine are rope_cos[t][i] and
+ * rope_sin[t][i] (device fp32 [max_pos, rot_dim / 2], 16-byte aligned):
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * interleaved 0 pairs x[i] with x[i + rot_dim/2], 1 pairs x[2i] with
+ * x[2i + 1].  rot_dim: a multiple of 16 in [0, d]; 0 is no rotation (the
+ * tables may then be NULL).  Products and sums are fp32, each rounded by
+ * itself.  A position outside [0, max_pos) is clamped into it and reported
+ * as ATTN_ERR_DEVICE_ARG by attn_get_device_status.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass:  y = R(x * w / sqrt(mean(x^2) + eps)) for every head row x.
+ *   q [B,N,Hq,d], k [B,N,Hkv,d] bf16 in, with token rows q_stride and
+ *            k_stride elements apart (token t = b*N + n starts at t * stride;
+ *            Hq*d and Hkv*d for dense tensors, more for a part of a fused
+ *            projection's rows); strides are multiples of 8;
+ *   q_weight, k_weight: fp32 [d], 16-byte aligned; NULL leaves that tensor
+ *            without a norm (rotation only);
+ *   eps: finite and > 0 (not looked at when both weights are NULL);
+ *   positions: device int32 [B,N], or NULL for 0 .. N-1 in every sequence;
+ *   q_out [B,N,Hq,d], k_out [B,N,Hkv,d] bf16 out, dense.  q_out may be q, and
+ *            k_out k, where that input is dense; otherwise they must not
+ *            overlap the inputs.
+ * Hkv = 0: q alone (k, k_out NULL).  The statistics are fp32, the result is
+ * rounded once.  Constraints: B, Hq >= 1; N, Hkv >= 0 (Hkv need not divide
+ * Hq); d in {64, 128}; tensors 16-byte aligned.
+ */
+ATTN_API attn_status attn_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                                       const float* q_weight, const float* k_weight, float eps,
+                                       const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim,
+                                       int interleaved, const int* positions, void* q_out, void* k_out,
+                                       int B, int N, int Hq, int Hkv, int d, void* stream);
+
+/* Bytes of workspace attn_qk_norm_rope_bwd needs; 0 for invalid arguments. */
+ATTN_API size_t attn_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int Hkv, int d);
+
+/*
+ * Gradients of attn_qk_norm_rope.  dq_out, dk_out (bf16, dense) are the
+ * gradients of q_out, k_out; q, k and the other arguments are the forward
+ * call's (its outputs are not needed: the norms are computed again).
+ *   dq [B,N,Hq,d], dk [B,N,Hkv,d] bf16 out, dense; dq may be dq_out, dk dk_out;
+ *   dq_weight, dk_weight: fp32 [d] out (written, not added to), NULL exactly
+ *            where the weight is NULL; q (k) may be NULL where its weight is;
+ *   workspace: attn_qk_norm_rope_bwd_workspace_size bytes, 16-byte aligned,
+ *            contents ignored; may be NULL when both weights are NULL.
+ * Sums over tokens and heads are fp32 in a fixed order: the same call gives
+ * the same bits.  N = 0 writes zero weight gradients.
+ */
+ATTN_API attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, long long q_stride,
+                                           const void* k, long long k_stride, const float* q_weight,
+                                           const float* k_weight, float eps, const float* rope_cos,
+                                           const float* rope_sin, int max_pos, int rot_dim, int interleaved,
+                                           const int* positions, void* dq, void* dk, float* dq_weight,
+                                           float* dk_weight, int B, int N, int Hq, int Hkv, int d,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Appends the keys and values of new tokens to a paged cache (the layout of
+ * attn_fwd_splitkv_paged), the keys rotated to their position on the way.
+ * New row i of sequence b goes to position seqlens[b] + i.
+ *   k, v [B,Nn,Hkv,d] bf16, token rows k_stride and v_stride elements apart
+ *            (as for attn_qk_norm_rope);
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, updated in place:
+ *            rows other than the new tokens' are left as they are;
+ *   block_table: device int32 [B, max_blocks]; page_size: a multiple of 64;
+ *   seqlens: device int32 [B], the lengths before the call;
+ *   new_lens: device int32 [B], how many of the Nn rows of each sequence are
+ *            real (the rows behind them are not read); NULL: all Nn;
+ *   seqlens_out: device int32 [B], receives the lengths after the call (the
+ *            seqlens of a decode that follows); NULL where not wanted; must
+ *            not be seqlens.
+ * A length outside [0, max_blocks * page_size], a new_lens entry outside
+ * [0, Nn], rows that do not fit the table (they are dropped) and page indices
+ * outside [0, num_pages) (nothing is written there) are reported as
+ * ATTN_ERR_DEVICE_ARG by attn_get_device_status.  A page that a call writes
+ * to belongs to one sequence: where two of them list it, its new rows are
+ * undefined.
+ */
+ATTN_API attn_status attn_kvcache_append_paged(const void* k, long long k_stride, const void* v, long long v_stride,
+                                               void* k_pages, void* v_pages, const int* block_table, int max_blocks,
+                                               int page_size, int num_pages, const int* seqlens, const int* new_lens,
+                                               int* seqlens_out, const float* rope_cos, const float* rope_sin,
+                                               int max_pos, int rot_dim, int interleaved, int B, int Nn, int Hkv,
+                                               int d, void* stream);
+
+/*
+ * The same for a cache held in 8 bits: k_pages, v_pages hold e4m3 codes and
+ * k_scales, v_scales [num_pages, Hkv] fp32 one scale for each page and KV
+ * head; a value is code * scale.  A scale is a power of two: the smallest s
+ * with amax <= 448.5 s, at least 2^-100, where amax is the largest finite
+ * magnitude among the page's rows of that head.  A page whose row 0 is new
+ * takes its scale from the new rows (whatever page and scale held before); a
+ * page that the call continues keeps its scale, or has it raised and its
+ * older codes divided by the same power of two and rounded again.  New values
+ * are rounded once, to nearest (ties to even), from the fp32 rotated value;
+ * infinities and NaN are stored as NaN.
+ */
+ATTN_API attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_stride, const void* v,
+                                                   long long v_stride, void* k_pages, void* v_pages, float* k_scales,
+                                                   float* v_scales, const int* block_table, int max_blocks,
+                                                   int page_size, int num_pages, const int* seqlens,
+                                                   const int* new_lens, int* seqlens_out, const float* rope_cos,
+                                                   const float* rope_sin, int max_pos, int rot_dim, int interleaved,
+                                                   int B, int Nn, int Hkv, int d, void* stream);
+
+/*
+ * A split length (keys per split) that suits attn_fwd_splitkv_paged_fp8 for
+ * these sizes; 0 for invalid arguments.  It depends on the arguments alone.
+ */
+ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen);
+
+/*
+ * Split-KV decode over a paged cache held in 8 bits (as written by
+ * attn_kvcache_append_paged_fp8): key j of sequence b is code * scale with
+ * the scale of its page and head, likewise its value.  The last Nq tokens of
+ * each sequence are the queries, masked causally among themselves: row i sees
+ * keys 0 .. seqlens[b] - Nq + i (Nq = 1: the whole cache).
+ *   q [B,Nq,Hq,d] bf16, Nq in [1, 64]; o [B,Nq,Hq,d] bf16 and lse [B,Hq,Nq]
+ *            fp32 out; a row that sees no key gets O = 0 and LSE = -inf;
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] e4m3, 16-byte aligned;
+ *   k_scales, v_scales fp32 [num_pages, Hkv], finite and >= 0 (any such value,
+ *            not powers of two alone);
+ *   seqlens: device int32 [B], each in [0, max_blocks * page_size], the new
+ *            tokens counted; codes behind a sequence's end reach no result,
+ *            whatever they hold;
+ *   chunk: keys per split, a positive multiple of 64 (attn_splitkv_fp8_chunk);
+ *   workspace: attn_splitkv_workspace_size(B, Nq * Hq, max_blocks * page_size,
+ *            d, chunk) bytes, 16-byte aligned, contents ignored.
+ * Bad lengths and pages are handled as in attn_fwd_splitkv_paged.
+ */
+ATTN_API attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                                const float* k_scales, const float* v_scales, const int* block_table,
+                                                int max_blocks, int page_size, int num_pages, const int* seqlens,
+                                                void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d,
+                                                float scale, int chunk, void* workspace, size_t workspace_bytes,
+                                                void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the library's device status

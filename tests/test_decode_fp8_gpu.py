@@ -1,0 +1,259 @@
+"""GPU: split-KV decode over a paged e4m3 cache against attention in 64 bits
+over the values that the codes and scales stand for."""
+import pytest
+import torch
+
+from exact_io_aware_14_gb300 import _native, build as native_build
+from tests import _serving as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    native_build.build()
+    _native.lib()
+    torch.cuda.init()
+
+
+def _cache(B, Hkv, d, page, lens, seed, amp=1.0, pow2=True, spread=3, extra=2, cap=None):
+    """Pools, scales, table on the CPU; codes behind a sequence's end and of free pages are NaN."""
+    g = torch.Generator().manual_seed(seed)
+    mb = max(1, -(-(cap or max(lens)) // page))
+    num_pages = B * mb + extra
+    table = torch.randperm(num_pages, generator=g)[:B * mb].view(B, mb).to(torch.int32)
+    pools, scales = [], []
+    for _ in range(2):
+        x = torch.randn((num_pages, page, Hkv, d), generator=g)
+        s = amp * torch.exp2(torch.randint(-spread, spread + 1, (num_pages, Hkv), generator=g).float() - 6)
+        if not pow2:
+            s = s * (1 + torch.rand((num_pages, Hkv), generator=g))
+        codes = (x * amp / s[:, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        live = torch.zeros((num_pages, page), dtype=torch.bool)
+        for b in range(B):
+            for blk in range(mb):
+                live[table[b, blk], :max(0, min(page, lens[b] - blk * page))] = True
+        codes[~live] = 0x7F
+        pools.append(codes)
+        scales.append(s)
+    return g, pools, scales, table
+
+
+def _run(q, pools, scales, table, lens, scale, chunk=None, **kw):
+    return _native.decode_paged_fp8(q.cuda(), *(p.cuda().view(torch.float8_e4m3fn) for p in pools),
+                                    *(s.cuda() for s in scales), table.cuda(),
+                                    torch.tensor(lens, dtype=torch.int32).cuda(), scale, chunk, **kw)
+
+
+def _check(q, pools, scales, table, lens, scale, got, what):
+    n = max(max(lens), 1)
+    k, v = (S.paged_rows(p.view(torch.float8_e4m3fn).double() * s.double()[:, None, :, None], table, n)
+            for p, s in zip(pools, scales))
+    o, lse, eo, el = S.decode(q, k, v, lens, scale)
+    S.assert_within(got[0], o, eo + 2.0 ** -8 * (o.abs() + eo), what + " o")
+    empty = lse.isinf()
+    L = got[1].double().cpu()
+    assert torch.equal(L == -float("inf"), empty), what
+    S.assert_within(torch.where(empty, torch.zeros_like(L), L), torch.where(empty, torch.zeros_like(lse), lse), el,
+                    what + " lse")
+
+
+CASES = [
+    # B, Nq, Hq, Hkv, d, page, lens, chunk
+    (1, 1, 1, 1, 64, 64, [1], 64),
+    (3, 1, 4, 1, 128, 64, [1, 64, 65], 128),
+    (2, 1, 32, 8, 128, 256, [700, 1025], None),
+    (4, 1, 8, 8, 128, 64, [127, 128, 129, 300], 256),
+    (3, 1, 6, 2, 64, 192, [191, 192, 500], 128),
+    (2, 1, 16, 1, 128, 128, [333, 1], 192),
+    (2, 1, 40, 1, 64, 64, [210, 64], 64),
+    (2, 1, 5, 1, 128, 320, [640, 77], 448),
+    (3, 2, 8, 2, 128, 64, [1, 2, 200], 64),
+    (2, 3, 24, 4, 64, 192, [3, 700], 256),
+    (3, 4, 7, 7, 128, 64, [4, 131, 66], 64),
+    (2, 7, 16, 2, 64, 128, [513, 7], 128),
+    (1, 64, 2, 1, 64, 64, [130], 64),
+    (4, 5, 4, 2, 128, 64, [0, 1, 3, 68], 64),       # rows that see no key, a sequence without any
+]
+
+
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,lens,chunk", CASES)
+def test_decode(B, Nq, Hq, Hkv, d, page, lens, chunk):
+    g, pools, scales, table = _cache(B, Hkv, d, page, lens, 500 + Hq + d + page)
+    q = torch.randn((B, Nq, Hq, d), generator=g).to(torch.bfloat16)
+    got = _run(q, pools, scales, table, lens, d ** -0.5, chunk)
+    assert _native.attn_get_device_status() == 0
+    _check(q, pools, scales, table, lens, d ** -0.5, got, "decode")
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1.0])
+def test_scales_of_any_size(scale):
+    """Scales that are no powers of two and differ by 2^12 between pages; a negative, zero and large softmax scale."""
+    lens = [900, 257]
+    g, pools, scales, table = _cache(2, 2, 128, 64, lens, 71, pow2=False, spread=6)
+    q = torch.randn((2, 1, 8, 128), generator=g).to(torch.bfloat16)
+    got = _run(q, pools, scales, table, lens, scale, 256)
+    _check(q, pools, scales, table, lens, scale, got, "scales")
+
+
+def test_zero_scales():
+    """Pages whose scale is zero hold zeros: their keys score 0 and add nothing to o."""
+    lens = [300]
+    g, pools, scales, table = _cache(1, 2, 64, 64, lens, 72)
+    scales[0][table[0, 1]] = 0.0
+    scales[1][table[0, 2]] = 0.0
+    q = torch.randn((1, 1, 4, 64), generator=g).to(torch.bfloat16)
+    _check(q, pools, scales, table, lens, 0.125, _run(q, pools, scales, table, lens, 0.125, 128), "zero scales")
+    for s in scales:
+        s.zero_()
+    _check(q, pools, scales, table, lens, 0.125, _run(q, pools, scales, table, lens, 0.125, 128), "all zero")
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_rising_scores(sign):
+    """Scores that climb by about 60 along the sequence: the softmax's reference moves many times in a split."""
+    B, Hq, Hkv, d, page, lens = 2, 8, 2, 128, 64, [1500, 700]
+    g, pools, scales, table = _cache(B, Hkv, d, page, lens, 73)
+    q = torch.ones((B, 1, Hq, d), dtype=torch.bfloat16)
+    scales[0].fill_(2.0 ** -6)
+    for b in range(B):
+        ramp = torch.linspace(-4, 4, lens[b]) * 64
+        for blk in range(-(-lens[b] // page)):
+            r = ramp[blk * page:(blk + 1) * page]
+            pools[0][table[b, blk], :len(r)] = r[:, None, None].expand(-1, Hkv, d).to(torch.float8_e4m3fn).view(
+                torch.uint8)
+    got = _run(q, pools, scales, table, lens, sign * d ** -0.5, 1024)
+    _check(q, pools, scales, table, lens, sign * d ** -0.5, got, "rising")
+
+
+def test_peaked_and_wide_queries():
+    """Queries whose values differ by 2^20 within a row, and rows where one key outweighs all others."""
+    lens = [400, 130]
+    g, pools, scales, table = _cache(2, 1, 64, 64, lens, 74)
+    q = torch.randn((2, 1, 4, 64), generator=g)
+    q = q * torch.exp2(-torch.randint(0, 21, q.shape, generator=g).float())
+    q[1] *= 100
+    q[0, 0, 3] = 0
+    q = q.to(torch.bfloat16)
+    _check(q, pools, scales, table, lens, 0.125, _run(q, pools, scales, table, lens, 0.125, 128), "wide")
+
+
+def test_splits_and_repeats():
+    """Results do not depend on a sequence's neighbours, and the same call gives the same bits; every split length
+    stays inside the bounds."""
+    lens = [1000, 1, 321]
+    g, pools, scales, table = _cache(3, 2, 128, 64, lens, 75)
+    q = torch.randn((3, 2, 8, 128), generator=g).to(torch.bfloat16)
+    for chunk in (64, 192, 512, 4096):
+        a = _run(q, pools, scales, table, lens, 0.09, chunk)
+        b = _run(q, pools, scales, table, lens, 0.09, chunk)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        _check(q, pools, scales, table, lens, 0.09, a, "chunk %d" % chunk)
+        c = _run(q[2:], pools, scales, table[2:], lens[2:], 0.09, chunk)
+        assert torch.equal(a[0][2:], c[0]) and torch.equal(a[1][2:], c[1])
+    assert _native.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("B", [33, 70, 300])
+def test_many_sequences(B):
+    g0 = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 200, (B,), generator=g0).tolist()
+    lens[0], lens[-1] = 193, 0
+    g, pools, scales, table = _cache(B, 1, 64, 64, lens, 76, cap=256)
+    q = torch.randn((B, 1, 3, 64), generator=g).to(torch.bfloat16)
+    _check(q, pools, scales, table, lens, 0.125, _run(q, pools, scales, table, lens, 0.125, 64), "B%d" % B)
+
+
+def test_nan_in_the_cache_spoils_its_sequence_only():
+    lens = [300, 200]
+    g, pools, scales, table = _cache(2, 1, 128, 64, lens, 77)
+    q = torch.randn((2, 1, 4, 128), generator=g).to(torch.bfloat16)
+    pools[1][table[0, 1], 5, 0, 17] = 0x7F     # a value of sequence 0
+    o, lse = _run(q, pools, scales, table, lens, 0.09, 128)
+    assert o[0, :, :, 17].isnan().all() and o[0, :, :, :17].isfinite().all() and o[1].isfinite().all()
+    assert lse.isfinite().all()
+    pools[0][table[1, 0], 3, 0, 0] = 0x7F      # a key of sequence 1
+    o, lse = _run(q, pools, scales, table, lens, 0.09, 128)
+    assert o[1].isnan().all() and lse[1].isnan().all() and lse[0].isfinite().all()
+
+
+def test_bad_lengths_and_pages_are_reported():
+    lens = [300, 200]
+    g, pools, scales, table = _cache(2, 1, 128, 64, lens, 78)
+    q = torch.randn((2, 1, 4, 128), generator=g).to(torch.bfloat16)
+    for bad in (-1, table.max().item() + 1000, 2 ** 31 - 1):
+        t = table.clone()
+        t[0, 1] = bad
+        o, _ = _run(q, pools, scales, t, lens, 0.09, 128)
+        assert _native.attn_get_device_status() == _native.ATTN_ERR_DEVICE_ARG
+        assert o[1].isfinite().all()
+    o, lse = _run(q, pools, scales, table, [-3, 200], 0.09, 128)
+    assert _native.attn_get_device_status() == _native.ATTN_ERR_DEVICE_ARG
+    assert o[0].abs().max() == 0 and (lse[0] == -float("inf")).all()
+    _run(q, pools, scales, table, [100000, 200], 0.09, 128)
+    assert _native.attn_get_device_status() == _native.ATTN_ERR_DEVICE_ARG
+    assert _native.attn_get_device_status() == 0
+
+
+def test_far_pages():
+    """Pages past 2^31 codes into the pool."""
+    page, Hkv, d = 256, 8, 128
+    num_pages = 2 ** 31 // (page * Hkv * d) + 3
+    table = torch.tensor([[num_pages - 1, 2, num_pages - 2]], dtype=torch.int32)
+    lens = [600]
+    g, small, scales, t3 = _cache(1, Hkv, d, page, lens, 79, extra=0)
+    big = [torch.full((num_pages, page, Hkv, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    bs = [torch.ones((num_pages, Hkv), device="cuda") for _ in range(2)]
+    for i in range(2):
+        for blk in range(3):
+            big[i][table[0, blk]] = small[i][t3[0, blk]].cuda()
+            bs[i][table[0, blk]] = scales[i][t3[0, blk]].cuda()
+    q = torch.randn((1, 1, 16, d), generator=g).to(torch.bfloat16)
+    got = _run(q, big, bs, table, lens, 0.09, 256)
+    _check(q, small, scales, t3, lens, 0.09, got, "far pages")
+
+
+def test_captured_and_two_streams():
+    """A captured call replayed, and two calls at once on two streams with workspaces of their own."""
+    lens = [900, 400]
+    g, pools, scales, table = _cache(2, 2, 128, 64, lens, 80)
+    q = torch.randn((2, 1, 8, 128), generator=g).to(torch.bfloat16)
+    dev = [q.cuda()] + [p.cuda().view(torch.float8_e4m3fn) for p in pools] + [s.cuda() for s in scales] + [
+        table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()]
+    want = _native.decode_paged_fp8(*dev, 0.09, 256)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _native.decode_paged_fp8(*dev, 0.09, 256)
+    for _ in range(3):
+        graph.replay()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    res = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            res.append([_native.decode_paged_fp8(*dev, 0.09, 256) for _ in range(5)])
+    torch.cuda.synchronize()
+    for o, lse in [got] + res[0] + res[1]:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert _native.attn_get_device_status() == 0
+
+
+def test_refusals():
+    lens = [100]
+    g, pools, scales, table = _cache(1, 2, 64, 64, lens, 81)
+    q = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    kp, vp = (p.cuda().view(torch.float8_e4m3fn) for p in pools)
+    ks, vs = (s.cuda() for s in scales)
+    t, n = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    f = _native.decode_paged_fp8
+    for bad in (lambda: f(q.float(), kp, vp, ks, vs, t, n, 0.1), lambda: f(q, kp.view(torch.uint8), vp, ks, vs, t, n, 0.1),
+                lambda: f(q, kp, vp, ks[:1], vs, t, n, 0.1), lambda: f(q, kp, vp, ks, vs, t.long(), n, 0.1),
+                lambda: f(q, kp, vp, ks, vs, t, n[:0], 0.1), lambda: f(q[:, :, ::2], kp, vp, ks, vs, t, n, 0.1)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: f(q[:, :, :3].contiguous(), kp, vp, ks, vs, t, n, 0.1),
+                lambda: f(q, kp, vp, ks, vs, t, n, float("nan")), lambda: f(q, kp, vp, ks, vs, t, n, 0.1, chunk=100),
+                lambda: f(q, kp, vp, ks, vs, t, n, 0.1, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                lambda: f(q.expand(1, 65, 4, 64).contiguous(), kp, vp, ks, vs, t, n, 0.1)):
+        with pytest.raises(_native.AttnError):
+            bad()

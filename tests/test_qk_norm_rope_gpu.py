@@ -1,0 +1,215 @@
+"""GPU: norms and rotation of queries and keys, forward and backward, against
+the formulas in 64 bits."""
+import pytest
+import torch
+
+from exact_io_aware_14_gb300 import _native, build as native_build
+from tests import _serving as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    native_build.build()
+    _native.lib()
+    torch.cuda.init()
+
+
+def _inputs(B, N, Hq, Hkv, d, rot, seed, positions=True, extra=0, max_pos=600):
+    """q, k as parts of a projection with `extra` more heads a token (0: dense tensors), weights, tables, positions."""
+    g = torch.Generator().manual_seed(seed)
+    if extra:
+        x = torch.randn((B, N, Hq + Hkv + extra, d), generator=g).to(torch.bfloat16)
+        q, k = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv]
+        xc = x.cuda()
+        qc, kc = xc[:, :, :Hq], xc[:, :, Hq:Hq + Hkv]
+    else:
+        q, k = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+        qc, kc = q.cuda(), k.cuda()
+    wq, wk = (1 + 0.3 * torch.randn(d, generator=g) for _ in range(2))
+    rope = _native.rope_table(max_pos, rot, device="cpu") if rot else None
+    pos = torch.randint(0, max_pos, (B, N), generator=g, dtype=torch.int32) if positions else None
+    at = pos if positions else torch.arange(N).expand(B, N)
+    return g, q, k, qc, kc, wq, wk, rope, pos, S.angles(rope, at)
+
+
+def _gpu(rope):
+    return None if rope is None else (rope[0].cuda(), rope[1].cuda())
+
+
+SHAPES = [
+    # B, N, Hq, Hkv, d, rot, inter, positions, extra
+    (1, 1, 1, 1, 64, 64, False, True, 0),
+    (1, 1, 32, 8, 128, 128, False, True, 8),
+    (64, 1, 32, 8, 128, 128, False, True, 8),
+    (3, 37, 9, 3, 64, 32, True, True, 3),
+    (2, 65, 5, 1, 128, 48, False, True, 1),
+    (2, 33, 7, 2, 128, 16, True, False, 2),
+    (2, 130, 4, 4, 64, 0, False, False, 0),
+    (1, 515, 6, 2, 128, 128, True, False, 0),
+    (2, 19, 3, 5, 64, 64, False, True, 4),     # more k heads than q heads
+]
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot,inter,positions,extra", SHAPES)
+@pytest.mark.parametrize("norm", [True, False])
+def test_forward(B, N, Hq, Hkv, d, rot, inter, positions, extra, norm):
+    _, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, rot, 100 + N + d, positions, extra)
+    w = (wq.cuda(), wk.cuda()) if norm else (None, None)
+    qo, ko = _native.qk_norm_rope(qc, kc, *w, 1e-6, _gpu(rope), None if pos is None else pos.cuda(), inter)
+    assert _native.attn_get_device_status() == 0
+    for x, wx, got, what in ((q, wq, qo, "q"), (k, wk, ko, "k")):
+        y, size = S.norm_rope(x, wx if norm else None, 1e-6, cs, inter)
+        # one rounding to bf16, under 16 fp32 roundings of values up to the row's largest
+        S.assert_within(got, y, 2.0 ** -8 * y.abs() + 2.0 ** -20 * size, what)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot,inter,positions,extra", SHAPES)
+@pytest.mark.parametrize("norm", [True, False])
+def test_backward(B, N, Hq, Hkv, d, rot, inter, positions, extra, norm):
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, rot, 200 + N + d, positions, extra)
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+    w = (wq.cuda(), wk.cuda()) if norm else (None, None)
+    xs = (qc, kc) if norm else (None, None)
+    got = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda(), *xs, *w, 1e-6, _gpu(rope),
+                                   None if pos is None else pos.cuda(), inter)
+    assert _native.attn_get_device_status() == 0
+    for x, wx, dy, dx_got, dw_got, what in ((q, wq, gq, got[0], got[2], "q"), (k, wk, gk, got[1], got[3], "k")):
+        dx, err, dw, size = S.norm_rope_bwd(dy, x, wx if norm else None, 1e-6, cs, inter)
+        S.assert_within(dx_got, dx, 2.0 ** -8 * dx.abs() + err, "d" + what)
+        if norm:
+            # at these sizes under 256 fp32 additions lie between a term and the sum
+            S.assert_within(dw_got, dw, 2.0 ** -16 * size, "dw" + what)
+        else:
+            assert dw_got is None
+
+
+def test_backward_against_differences():
+    """dx and dw of the kernel against central differences of the forward formula in 64 bits, along one direction."""
+    B, N, H, d, rot = 2, 3, 2, 64, 32
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, H, H, d, rot, 5)
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    dq, _, dwq, _ = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda(), qc, kc, wq.cuda(), wk.cuda(), 1e-6, _gpu(rope),
+                                             pos.cuda())
+    v = torch.randn((B, N, H, d), generator=g, dtype=torch.float64)
+    vw = torch.randn(d, generator=g, dtype=torch.float64)
+    f = lambda x, w: float((S.norm_rope(x, w, 1e-6, cs, False)[0] * gq.double()).sum())
+    h = 1e-5
+    x, w = q.double(), wq.double()
+    num = (f(x + h * v, w) - f(x - h * v, w)) / (2 * h)
+    dq = dq.double().cpu()
+    assert abs(num - float((dq * v).sum())) <= float((2.0 ** -8 * dq.abs() * v.abs()).sum()) + 1e-4
+    num = (f(x, w + h * vw) - f(x, w - h * vw)) / (2 * h)
+    dwq = dwq.double().cpu()
+    terms = (gq.double().abs().sum() * 8)  # |xr| <= 8 = sqrt(d)
+    assert abs(num - float((dwq * vw).sum())) <= 2.0 ** -20 * float(terms) * float(vw.abs().max()) + 1e-4
+
+
+def test_large_and_repeatable():
+    """More rows than the backward pass has threads (every thread walks several): bounds, and the same bits twice."""
+    B, N, Hq, Hkv, d = 2, 2500, 16, 4, 128
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, 128, 9, True, 4, 4000)
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+    args = (gq.cuda(), gk.cuda(), qc, kc, wq.cuda(), wk.cuda(), 1e-6, _gpu(rope), pos.cuda())
+    a, b = _native.qk_norm_rope_bwd(*args), _native.qk_norm_rope_bwd(*args)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    dx, err, dw, size = S.norm_rope_bwd(gq, q, wq, 1e-6, cs, False)
+    S.assert_within(a[0], dx, 2.0 ** -8 * dx.abs() + err, "dq")
+    S.assert_within(a[2], dw, 2.0 ** -16 * size, "dwq")
+    dx, err, dw, size = S.norm_rope_bwd(gk, k, wk, 1e-6, cs, False)
+    S.assert_within(a[1], dx, 2.0 ** -8 * dx.abs() + err, "dk")
+    S.assert_within(a[3], dw, 2.0 ** -16 * size, "dwk")
+
+
+def test_in_place_q_alone_and_empty():
+    _, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(2, 9, 4, 2, 128, 128, 11)
+    r = _gpu(rope)
+    want = _native.qk_norm_rope(qc, kc, wq.cuda(), wk.cuda(), 1e-6, r, pos.cuda())
+    a, b = qc.clone(), kc.clone()
+    _native.qk_norm_rope(a, b, wq.cuda(), wk.cuda(), 1e-6, r, pos.cuda(), out=(a, b))
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    alone, none = _native.qk_norm_rope(qc, None, wq.cuda(), None, 1e-6, r, pos.cuda())
+    assert none is None and torch.equal(alone, want[0])
+    only_k = _native.qk_norm_rope(qc, kc, None, wk.cuda(), 1e-6, r, pos.cuda())
+    assert torch.equal(only_k[1], want[1])
+    e = torch.empty((2, 0, 4, 128), dtype=torch.bfloat16, device="cuda")
+    assert _native.qk_norm_rope(e, e, None, None)[0].shape == e.shape
+    w = torch.ones(128, device="cuda")
+    g = _native.qk_norm_rope_bwd(e, e, e, e, w, w)
+    assert g[2].abs().max() == 0 and g[3].abs().max() == 0
+    assert _native.attn_get_device_status() == 0
+
+
+def test_extreme_rows():
+    """Rows of zeros, of the type's smallest and of large values; a row with NaN or an infinity spoils itself only."""
+    d = 128
+    x = torch.randn((1, 6, 1, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    x[0, 0] = 0
+    x[0, 1] = 1e-38
+    x[0, 2] = 1e18
+    x[0, 3, 0, 5] = float("nan")
+    x[0, 4, 0, 77] = float("inf")
+    w = torch.ones(d)
+    got, _ = _native.qk_norm_rope(x.cuda(), None, w.cuda(), None, 1e-6)
+    got = got.cpu()
+    y, size = S.norm_rope(x, w, 1e-6, None, False)
+    fine = [0, 1, 2, 5]
+    S.assert_within(got[:, fine], y[:, fine], 2.0 ** -8 * y[:, fine].abs() + 2.0 ** -20 * size[:, fine], "rows")
+    assert got[0, 0].abs().max() == 0
+    assert got[0, 3].isnan().all()
+    assert got[0, 4, 0, 77].isnan() and (got[0, 4, 0, :77] == 0).all()   # inf * 0; the others are 0
+
+
+def test_positions_out_of_range_are_reported():
+    rope = _native.rope_table(10, 64)
+    q = torch.randn((1, 3, 2, 64), device="cuda").to(torch.bfloat16)
+    pos = torch.tensor([[-1, 4, 10]], dtype=torch.int32, device="cuda")
+    got, _ = _native.qk_norm_rope(q, None, None, None, rope=rope, positions=pos)
+    assert _native.attn_get_device_status() == _native.ATTN_ERR_DEVICE_ARG
+    assert _native.attn_get_device_status() == 0
+    ok, _ = _native.qk_norm_rope(q, None, None, None, rope=rope, positions=pos.clamp(0, 9))
+    assert torch.equal(got, ok)
+    assert _native.attn_get_device_status() == 0
+
+
+def test_captured_and_on_another_stream():
+    _, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(2, 40, 4, 2, 128, 128, 21, True, 2)
+    r, p = _gpu(rope), pos.cuda()
+    g = [torch.randn((2, 40, H, 128), device="cuda").to(torch.bfloat16) for H in (4, 2)]
+    w = (wq.cuda(), wk.cuda())
+    want = _native.qk_norm_rope(qc, kc, *w, 1e-6, r, p), _native.qk_norm_rope_bwd(*g, qc, kc, *w, 1e-6, r, p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        two = _native.qk_norm_rope(qc, kc, *w, 1e-6, r, p), _native.qk_norm_rope_bwd(*g, qc, kc, *w, 1e-6, r, p)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        three = _native.qk_norm_rope(qc, kc, *w, 1e-6, r, p), _native.qk_norm_rope_bwd(*g, qc, kc, *w, 1e-6, r, p)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in (two, three):
+        for a, b in zip(want[0] + want[1], got[0] + got[1]):
+            assert torch.equal(a, b)
+
+
+def test_refusals():
+    q = torch.zeros((1, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    rope = _native.rope_table(8, 64)
+    for bad in (lambda: _native.qk_norm_rope(q.float(), None, w, None),
+                lambda: _native.qk_norm_rope(q, q, w.bfloat16(), w),
+                lambda: _native.qk_norm_rope(q, q, w[:32], w),
+                lambda: _native.qk_norm_rope(q, q.cpu(), w, w),
+                lambda: _native.qk_norm_rope(q, q, w, w, rope=(rope[0], rope[1][:4])),
+                lambda: _native.qk_norm_rope(q, q, w, w, rope=rope, positions=torch.zeros((1, 2), device="cuda")),
+                lambda: _native.qk_norm_rope(q, q, w, w, out=(q[:, :1], q)),
+                lambda: _native.qk_norm_rope_bwd(q, q, q[:, :1], q, w, w)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(_native.AttnError):
+        _native.qk_norm_rope(q, q, w, w, eps=0.0)
+    with pytest.raises(_native.AttnError):
+        _native.qk_norm_rope(q[..., :48].contiguous(), None, None, None)

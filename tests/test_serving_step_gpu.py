@@ -1,0 +1,137 @@
+"""GPU: the operators together, as a serving loop and a training step use them."""
+import pytest
+import torch
+
+from exact_io_aware_14_gb300 import _native, build as native_build
+from tests import _serving as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    native_build.build()
+    _native.lib()
+    torch.cuda.init()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompt_then_tokens(fp8):
+    """A padded batch of prompts, then tokens one at a time: norms and rotation, append, decode; the step captured
+    once and replayed.  Every step's attention is compared with 64-bit attention over what the cache then holds, and
+    the cache with the keys and values that went in."""
+    B, Hq, Hkv, d, page, Nn, steps = 3, 8, 2, 128, 64, 150, 5
+    g = torch.Generator().manual_seed(90)
+    lens = torch.tensor([150, 63, 97], dtype=torch.int32)
+    mb = 4
+    num_pages = B * mb + 1
+    table = torch.randperm(num_pages, generator=g)[:B * mb].view(B, mb).to(torch.int32).cuda()
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    pools = [torch.full((num_pages, page, Hkv, d), 0xFF, dtype=torch.uint8 if fp8 else torch.int16,
+                        device="cuda").view(dtype) for _ in range(2)] if fp8 else [
+        torch.full((num_pages, page, Hkv, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((num_pages, Hkv), device="cuda") for _ in range(2)] if fp8 else []
+    rope = _native.rope_table(mb * page, d)
+    wq, wk = (1 + 0.1 * torch.randn(d, generator=g).cuda() for _ in range(2))
+    append = _native.kvcache_append_paged_fp8 if fp8 else _native.kvcache_append_paged
+
+    def step(qkv, seqlens, after, new_lens, pos):
+        q, k, v = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:]
+        q, k = _native.qk_norm_rope(q, k, wq, wk, 1e-6, rope, pos)
+        append(k, v, *pools, *scales, table, seqlens, new_lens=new_lens, seqlens_out=after)
+        return q, k, v
+
+    def attend(q, seqlens):
+        if fp8:
+            return _native.decode_paged_fp8(q, *pools, *scales, table, seqlens, d ** -0.5)
+        return _native.decode_paged(q, *pools, table, seqlens, d ** -0.5, chunk=128)
+
+    prompt = torch.randn((B, Nn, Hq + 2 * Hkv, d), generator=g).to(torch.bfloat16).cuda()
+    seqlens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    after = torch.empty_like(seqlens)
+    _, k, v = step(prompt, seqlens, after, lens.cuda(), None)
+    assert after.tolist() == lens.tolist()
+    ks, vs = ([x[b, :int(lens[b])].cpu() for b in range(B)] for x in (k, v))
+    # one decode step, captured: its inputs and lengths are updated in place between replays
+    token = torch.zeros((B, 1, Hq + 2 * Hkv, d), dtype=torch.bfloat16, device="cuda")
+    seqlens.copy_(after)
+    pos = seqlens.view(B, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, k, v = step(token, seqlens, after, None, pos)
+        o, lse = attend(q, after)
+        seqlens.copy_(after)
+    for t in range(steps):
+        token.copy_(torch.randn(token.shape, generator=g).to(torch.bfloat16))
+        graph.replay()
+        now = [int(x) for x in after.tolist()]
+        assert now == [int(lens[b]) + t + 1 for b in range(B)]
+        kc, vc = ([], [])
+        n = max(now)
+        full = []
+        for i, (pool, new, old) in enumerate(zip(pools, (k, v), (ks, vs))):
+            val = pool.float().cpu().double()
+            if fp8:
+                val = val * scales[i].cpu().double()[:, None, :, None]
+            rows = S.paged_rows(val, table.cpu(), n)
+            for b in range(B):
+                old[b] = torch.cat((old[b], new[b].cpu()))
+                got, want = rows[b, :now[b]], old[b].double()
+                if fp8:   # two roundings at most at the smallest codes: a scale raised after a value was stored
+                    sc = S.paged_rows(scales[i].cpu().double()[:, None, :, None].expand(-1, page, -1, 1), table.cpu(),
+                                      n)[b, :now[b]]
+                    assert ((got - want).abs() <= torch.maximum(2.0 ** -4 * want.abs(), 2.0 ** -9 * sc)).all()
+                else:
+                    assert torch.equal(got, want)
+            full.append(rows)
+        o64, lse64, eo, el = S.decode(q.cpu(), *full, now, d ** -0.5)
+        S.assert_within(o, o64, eo + 2.0 ** -8 * (o64.abs() + eo), "o at step %d" % t)
+        S.assert_within(lse, lse64, el, "lse at step %d" % t)
+    assert _native.attn_get_device_status() == 0
+
+
+def test_training_step():
+    """Norms and rotation before the training forward, and their backward pass with the gradients that attention
+    gives: compared with 64-bit autograd through the whole step."""
+    B, N, Hq, Hkv, d = 2, 70, 4, 2, 64
+    g = torch.Generator().manual_seed(91)
+    qkv = torch.randn((B, N, Hq + 2 * Hkv, d), generator=g).to(torch.bfloat16)
+    wq, wk = (1 + 0.1 * torch.randn(d, generator=g) for _ in range(2))
+    rope = _native.rope_table(N, d, device="cpu")
+    do = torch.randn((B, N, Hq, d), generator=g).double()
+    qc = qkv.cuda()
+    q, k, v = qc[:, :, :Hq], qc[:, :, Hq:Hq + Hkv], qc[:, :, Hq + Hkv:]
+    r = (rope[0].cuda(), rope[1].cuda())
+    qo, ko = _native.qk_norm_rope(q, k, wq.cuda(), wk.cuda(), 1e-6, r)
+    o, lse = _native.forward(qo, ko, v.contiguous(), 1, d ** -0.5)
+    # 64-bit step
+    x = qkv.double().requires_grad_()
+    w = [t.double().requires_grad_() for t in (wq, wk)]
+    cs = S.angles(rope, torch.arange(N).expand(B, N))
+    turned = []
+    for part, wt in ((x[:, :, :Hq], w[0]), (x[:, :, Hq:Hq + Hkv], w[1])):
+        y = part * (part.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * wt
+        a, b = y[..., :d // 2], y[..., d // 2:]
+        turned.append(torch.cat((a * cs[0] - b * cs[1], b * cs[0] + a * cs[1]), -1))
+    turned[0].retain_grad(), turned[1].retain_grad()
+    kk, vv = (t.repeat_interleave(Hq // Hkv, 2) for t in (turned[1], x[:, :, Hq + Hkv:]))
+    s = torch.einsum("bihd,bjhd->bhij", turned[0], kk) * d ** -0.5
+    s = s.masked_fill(torch.ones(N, N).triu(1).bool(), -float("inf"))
+    o64 = torch.einsum("bhij,bjhd->bihd", s.softmax(-1), vv)
+    # the workloads' bar for bf16 attention, here with q and k rounded to bf16 before it as well
+    assert (o.double().cpu() - o64.detach()).abs().max() <= 4e-2
+    (o64 * do).sum().backward()
+    gq, gk = (t.grad.to(torch.bfloat16) for t in turned)
+    dq, dk, dwq, dwk = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda(), q, k, wq.cuda(), wk.cuda(), 1e-6, r)
+    # the incoming gradients were rounded to bf16: 2^-8 of each, through R^T, w and the norm (a projection)
+    for got, part, gy, wt, dw, lo, hi in ((dq, qkv[:, :, :Hq], gq, wq, dwq, 0, Hq),
+                                          (dk, qkv[:, :, Hq:Hq + Hkv], gk, wk, dwk, Hq, Hq + Hkv)):
+        want = x.grad[:, :, lo:hi]
+        rr = (part.double().square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+        size = 2.0 ** -8 * rr * float(wt.abs().max()) * gy.double().norm(dim=-1, keepdim=True) * 2
+        S.assert_within(got, want, 2.0 ** -8 * (want.abs() + size) + size, "gradient")
+        w64 = w[0].grad if lo == 0 else w[1].grad
+        xr = part.double() * rr
+        terms = (xr.abs() * gy.double().norm(dim=-1, keepdim=True)).reshape(-1, d).sum(0)
+        S.assert_within(dw, w64, (2.0 ** -8 + 2.0 ** -16) * terms, "weight gradient")
+    assert _native.attn_get_device_status() == 0
