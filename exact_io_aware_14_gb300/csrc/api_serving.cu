@@ -252,7 +252,7 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   if (chunk < 64 || chunk % 64 != 0 || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   const long long cap = static_cast<long long>(max_blocks) * page_size;
-  if (cap + Nq + 256 > kIntMax || Nq > 64 || B > 65535 || chunk > 16384 || (cap + chunk - 1) / chunk > 65535 ||
+  if (cap + Nq + 256 > kIntMax || Nq > 64 || B > 65535 || chunk > attn::kMaxChunkFp8 || (cap + chunk - 1) / chunk > 65535 ||
       static_cast<long long>(Nq) * Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Nq * Hq > kIntMax) return ATTN_ERR_UNSUPPORTED;

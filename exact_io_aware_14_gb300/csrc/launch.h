@@ -102,6 +102,15 @@ struct AppendParams {
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 
 // Split-KV decode over a paged e4m3 cache.
+constexpr int kMaxChunkFp8 = 4096;  // keys per split at most
+struct DecodeFp8CombineParams {
+  const float* o_part;
+  const float* lse_part;
+  const int* seqlens;
+  void* o;
+  float* lse;
+  int Nq, Hq, max_seqlen, chunk, n_split;
+};
 struct DecodeFp8Params {
   CUtensorMap tm_k, tm_v;
   const void* q;

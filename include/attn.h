@@ -369,7 +369,7 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  *   seqlens: device int32 [B], each in [0, max_blocks * page_size], the new
  *            tokens counted; codes behind a sequence's end reach no result,
  *            whatever they hold;
- *   chunk: keys per split, a multiple of 64 in [64, 16384]
+ *   chunk: keys per split, a multiple of 64 in [64, 4096]
  *            (attn_splitkv_fp8_chunk);
  *   workspace: attn_splitkv_workspace_size(B, Nq * Hq, max_blocks * page_size,
  *            d, chunk) bytes, 16-byte aligned, contents ignored.
