@@ -260,35 +260,47 @@ def attn_fwd_splitkv_noalloc(q, k_cache, v_cache, seqlens, o, lse, scale, chunk,
 
 
 # --------------------------------------------------------------------------- operators around the attention kernels
+# These calls are launched once or more a layer and token, where the host's time for a call counts: each argument is
+# looked at once, with the cheapest query that settles it, and the stream is asked for as a handle.
 _BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+_fns = {}
 
 
-def _call(name, device, stream, *args):
-    """The C call `name` on `device`, whichever is current, on `stream` (None: that device's current stream).
-    Returns the status."""
-    fn = getattr(lib(), name)
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, handle)
-    with torch.cuda.device(device):
-        return fn(*args, handle)
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    return f
 
 
-def _need(name, t, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on the device; returns its address."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+def _call(name, dev, stream, *args):
+    """The C call `name` on device number dev, whichever is current, on `stream` (None: that device's current stream).
+    Raises unless it returns ATTN_OK."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = _fn(name)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = _fn(name)(*args, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+
+
+def _need(name, t, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on device number dev (-1: the CPU); returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s %s)"
-                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+                         % (name, dtype, tuple(shape), "cuda:%d" % dev, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
 
 
-def _rows(name, t, shape, device):
+def _rows(name, t, shape, dev):
     """t [B, N, H, d] bf16 with dense heads and one distance between its token rows (a part of a fused projection's
     rows); returns (address, that distance)."""
-    B, N, H, d = shape
-    if t.dtype != _BF16 or t.shape != shape or t.device != device:
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
         raise ValueError("%s must be a bf16 tensor of shape %s on %s (got %s %s %s)"
-                         % (name, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+                         % (name, tuple(shape), "cuda:%d" % dev, t.dtype, tuple(t.shape), t.device))
+    B, N, H, d = shape
     if t.is_contiguous():
         return t.data_ptr(), H * d
     sb, sn, sh, sd = t.stride()
@@ -298,7 +310,7 @@ def _rows(name, t, shape, device):
     return t.data_ptr(), row
 
 
-def _rope_args(rope, interleaved, device):
+def _rope_args(rope, interleaved, dev):
     """(cos, sin, max_pos, rot_dim, interleaved) of the C calls; rope: None or (cos, sin) fp32 [max_pos, rot_dim/2]."""
     if rope is None:
         return None, None, 0, 0, 0
@@ -306,14 +318,15 @@ def _rope_args(rope, interleaved, device):
     shape = cos.shape
     if len(shape) != 2:
         raise ValueError("rope tables must be [max_pos, rot_dim / 2]")
-    return (_need("rope cos", cos, _F32, shape, device), _need("rope sin", sin, _F32, shape, device), shape[0],
-            2 * shape[1], int(bool(interleaved)))
+    return (_need("rope cos", cos, _F32, shape, dev), _need("rope sin", sin, _F32, shape, dev), shape[0],
+            2 * shape[1], 1 if interleaved else 0)
 
 
 def _cuda_device(t):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("a CUDA tensor is wanted (got %s)" % t.device)
-    return t.device
+    return dev
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
@@ -324,8 +337,8 @@ def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
     return a.cos().float(), a.sin().float()
 
 
-def _weight(name, w, d, device):
-    return None if w is None else _need(name, w, _F32, (d,), device)
+def _weight(name, w, d, dev):
+    return None if w is None else _need(name, w, _F32, (d,), dev)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, interleaved=False, out=None,
@@ -335,24 +348,24 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, 
     rope: (cos, sin) from rope_table, or None; positions int32 [B,N], or None for 0 .. N-1; out: (q_out, k_out) to
     write to (q and k themselves where dense), or None.  Returns (q_out, k_out)."""
     dev = _cuda_device(q)
-    B, N, Hq, d = q.shape
+    q_shape = q.shape
+    B, N, Hq, d = q_shape
     Hkv = 0 if k is None else k.shape[2]
-    qp, qs = _rows("q", q, (B, N, Hq, d), dev)
-    kp, ks = (None, 0) if k is None else _rows("k", k, (B, N, Hkv, d), dev)
+    k_shape = (B, N, Hkv, d)
+    qp, qs = _rows("q", q, q_shape, dev)
+    kp, ks = (None, 0) if k is None else _rows("k", k, k_shape, dev)
     if out is None:
-        qo = torch.empty((B, N, Hq, d), dtype=_BF16, device=dev)
-        ko = None if k is None else torch.empty((B, N, Hkv, d), dtype=_BF16, device=dev)
+        qo = torch.empty(q_shape, dtype=_BF16, device=dev)
+        ko = None if k is None else torch.empty(k_shape, dtype=_BF16, device=dev)
     else:
         qo, ko = out
-        _need("q_out", qo, _BF16, (B, N, Hq, d), dev)
+        _need("q_out", qo, _BF16, q_shape, dev)
         if k is not None:
-            _need("k_out", ko, _BF16, (B, N, Hkv, d), dev)
+            _need("k_out", ko, _BF16, k_shape, dev)
     pos = None if positions is None else _need("positions", positions, _I32, (B, N), dev)
-    rc = _call("attn_qk_norm_rope", dev, stream, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
-               _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, qo.data_ptr(),
-               None if ko is None else ko.data_ptr(), B, N, Hq, Hkv, d)
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_qk_norm_rope")
+    _call("attn_qk_norm_rope", dev, stream, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
+          _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, qo.data_ptr(),
+          None if ko is None else ko.data_ptr(), B, N, Hq, Hkv, d)
     return qo, ko
 
 
@@ -379,41 +392,40 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps=1e-6, rope=No
     ws, nbytes = None, 0
     if dwq is not None or dwk is not None:
         if workspace is None:
-            nbytes = attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)
+            nbytes = _fn("attn_qk_norm_rope_bwd_workspace_size")(B, N, Hq, Hkv, d)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
         else:
             nbytes = workspace.numel() * workspace.element_size()
         ws = workspace.data_ptr()
     pos = None if positions is None else _need("positions", positions, _I32, (B, N), dev)
-    rc = _call("attn_qk_norm_rope_bwd", dev, stream, gq, gk, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
-               _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, dq.data_ptr(),
-               None if dk is None else dk.data_ptr(), None if dwq is None else dwq.data_ptr(),
-               None if dwk is None else dwk.data_ptr(), B, N, Hq, Hkv, d, ws, nbytes)
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_qk_norm_rope_bwd")
+    _call("attn_qk_norm_rope_bwd", dev, stream, gq, gk, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
+          _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, dq.data_ptr(),
+          None if dk is None else dk.data_ptr(), None if dwq is None else dwq.data_ptr(),
+          None if dwk is None else dwk.data_ptr(), B, N, Hq, Hkv, d, ws, nbytes)
     return dq, dk, dwq, dwk
 
 
 def _append(name, k, v, k_pages, v_pages, scales, block_table, seqlens, rope, interleaved, new_lens, seqlens_out,
             stream):
     dev = _cuda_device(k_pages)
-    B, Nn, Hkv, d = k.shape
-    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
-    kp, ks = _rows("k", k, (B, Nn, Hkv, d), dev)
-    vp, vs = _rows("v", v, (B, Nn, Hkv, d), dev)
-    pools = (num_pages, page_size, Hkv, d)
+    shape = k.shape
+    B, Nn, Hkv, d = shape
+    pools = k_pages.shape
+    num_pages, page_size = pools[:2]
+    if pools[2:] != (Hkv, d):
+        raise ValueError("k_pages must be [num_pages, page_size, %d, %d] (got %s)" % (Hkv, d, tuple(pools)))
+    kp, ks = _rows("k", k, shape, dev)
+    vp, vs = _rows("v", v, shape, dev)
     dtype = _E4M3 if scales else _BF16
     args = [kp, ks, vp, vs, _need("k_pages", k_pages, dtype, pools, dev), _need("v_pages", v_pages, dtype, pools, dev)]
     for what, s in zip(("k_scales", "v_scales"), scales):
         args.append(_need(what, s, _F32, (num_pages, Hkv), dev))
     max_blocks = block_table.shape[-1]
-    rc = _call(name, dev, stream, *args, _need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks,
-               page_size, num_pages, _need("seqlens", seqlens, _I32, (B,), dev),
-               None if new_lens is None else _need("new_lens", new_lens, _I32, (B,), dev),
-               None if seqlens_out is None else _need("seqlens_out", seqlens_out, _I32, (B,), dev),
-               *_rope_args(rope, interleaved, dev), B, Nn, Hkv, d)
-    if rc != ATTN_OK:
-        raise AttnError(rc, name)
+    _call(name, dev, stream, *args, _need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks,
+          page_size, num_pages, _need("seqlens", seqlens, _I32, (B,), dev),
+          None if new_lens is None else _need("new_lens", new_lens, _I32, (B,), dev),
+          None if seqlens_out is None else _need("seqlens_out", seqlens_out, _I32, (B,), dev),
+          *_rope_args(rope, interleaved, dev), B, Nn, Hkv, d)
 
 
 def kvcache_append_paged(k, v, k_pages, v_pages, block_table, seqlens, rope=None, interleaved=False, new_lens=None,
@@ -443,28 +455,29 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqle
     fp32 scales [num_pages, Hkv] (attn_fwd_splitkv_paged_fp8); chunk None: attn_splitkv_fp8_chunk's.
     Returns (o, lse [B,Hq,Nq])."""
     dev = _cuda_device(q)
-    B, Nq, Hq, d = q.shape
-    num_pages, page_size, Hkv = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
+    q_shape, pools = q.shape, k_pages.shape
+    B, Nq, Hq, d = q_shape
+    num_pages, page_size, Hkv = pools[:3]
+    if pools[3:] != (d,):
+        raise ValueError("k_pages must be [num_pages, page_size, Hkv, %d] (got %s)" % (d, tuple(pools)))
     max_blocks = block_table.shape[-1]
-    pools = (num_pages, page_size, Hkv, d)
-    args = (_need("q", q, _BF16, (B, Nq, Hq, d), dev), _need("k_pages", k_pages, _E4M3, pools, dev),
+    args = (_need("q", q, _BF16, q_shape, dev), _need("k_pages", k_pages, _E4M3, pools, dev),
             _need("v_pages", v_pages, _E4M3, pools, dev), _need("k_scales", k_scales, _F32, (num_pages, Hkv), dev),
             _need("v_scales", v_scales, _F32, (num_pages, Hkv), dev),
             _need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks, page_size, num_pages,
             _need("seqlens", seqlens, _I32, (B,), dev))
-    L = lib()
-    cap = max_blocks * page_size
+    cap = min(max_blocks * page_size, 0x7fffffff)  # the C call refuses more
     if chunk is None:
-        chunk = L.attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, min(cap, 0x7fffffff))
-    o = torch.empty((B, Nq, Hq, d), dtype=_BF16, device=dev)
+        chunk = _fn("attn_splitkv_fp8_chunk")(B, Nq, Hq, Hkv, cap)
+    o = torch.empty(q_shape, dtype=_BF16, device=dev)
     lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
     if workspace is None:
-        n = L.attn_splitkv_workspace_size(B, Nq * Hq, min(cap, 0x7fffffff), d, chunk)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    rc = _call("attn_fwd_splitkv_paged_fp8", dev, stream, *args, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
-               scale, chunk, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_fwd_splitkv_paged_fp8")
+        n = _fn("attn_splitkv_workspace_size")(B, Nq * Hq, cap, d, chunk)
+        workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+    else:
+        n = workspace.numel() * workspace.element_size()
+    _call("attn_fwd_splitkv_paged_fp8", dev, stream, *args, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
+          scale, chunk, workspace.data_ptr(), n)
     return o, lse
 
 

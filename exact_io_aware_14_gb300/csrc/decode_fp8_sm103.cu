@@ -56,7 +56,6 @@ __device__ __forceinline__ void record(uint32_t site, uint32_t code) {
 }
 
 constexpr int kTile = 128;     // keys per tile (MMA M of S, K of O^T)
-constexpr int kThreads = 352;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kMoveLog2 = 4.f;      // the reference moves when a score passes it by this
 constexpr float kWeightScale = 1024.f;  // 2^10: weights up to 2^14, e5m2 ends at 57344
@@ -65,9 +64,16 @@ template <int D, int R>
 struct Cfg {
   static constexpr int kN = (3 * R + 15) / 16 * 16;  // MMA columns
   static constexpr int kTmem = kN <= 16 ? 64 : (kN <= 32 ? 128 : 256);  // 4 kN, a power of two
-  static constexpr int kCtas = R == 4 || (R == 8 && D == 64) ? 2 : 1;   // per SM
+  static constexpr int kCtas = R == 4 ? 2 : 1;                          // per SM
+  // softmax groups of four warps, each with its own kRows of the rows: one
+  // group takes about 0.06 us a row and tile, 0.72 us is a tile's time at HBM rate
+  static constexpr int kGroups = R == 4 ? 1 : 2;
+  static constexpr int kRows = R / kGroups;
+  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int kWarps = kSoftWarps + 7;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStages = (kCtas == 2 ? 3 : (R == 16 ? 5 : 6)) * 128 / D - (D == 64 && R == 8 ? 1 : 0);
+  static constexpr int kStages = (kCtas == 2 ? 3 : (R == 16 ? 5 : 6)) * 128 / D;
   static constexpr int kItems = 3;  // items prepared or in work
   static constexpr int kMaxBlocks = kMaxChunkFp8 / 64;
   static constexpr int kOffV = 0;  // V first: the M-major reads of a 64-dim V tile run into K's (see below)
@@ -77,11 +83,12 @@ struct Cfg {
   static constexpr int kOffQ = kStages * kStage;            // [kItems]
   static constexpr int kOffP = kOffQ + kItems * kQBytes;    // [2][kN][128] bytes
   static constexpr int kOffItem = kOffP + 2 * kN * kTile;   // [kItems]
-  static constexpr int kOffAlpha = kOffItem + kItems * ((12 + 3 * kMaxBlocks + R) * 4);  // float [2][R]
-  static constexpr int kOffRed = kOffAlpha + 2 * R * 4;     // float [4][R], then 4 flags
-  static constexpr int kOffMl = kOffRed + 4 * R * 4 + 16;   // [2] float m[R], l[4][R]
+  static constexpr int kOffAlpha = kOffItem + kItems * ((8 + 3 * kMaxBlocks + 4 * R) * 4);  // float [2][R]
+  static constexpr int kOffRed = kOffAlpha + 2 * R * 4;     // [kGroups] float [4][kRows], then [kGroups] 4 flags
+  static constexpr int kOffSpoil = kOffRed + 4 * R * 4 + kGroups * 16;  // byte [2][kTile]
+  static constexpr int kOffMl = kOffSpoil + 2 * kTile;      // [2] float m[R], l[4][R]
   static constexpr int kOffBar = (kOffMl + 2 * 5 * R * 4 + 15) / 16 * 16;
-  static constexpr int kNumBars = 2 * kStages + 3 * kItems + 4 * 2 + 2 * 2 + 1;
+  static constexpr int kNumBars = 2 * kStages + 3 * kItems + 4 * 2 + 2 * 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -92,14 +99,16 @@ template <int R>
 struct Item {
   int n_t;       // key tiles; -1: no more items
   int kn;        // keys of the split
-  int b, split, hkv, row0;
-  int lim0;      // keys of the split that token 0 sees (may be negative or past kn)
+  int split, hkv;
+  int lim_min;   // keys of the split that every row sees, at least
   int direct;    // the sequence's only split: the result goes straight to o and lse
   float vref;    // largest value scale of the split
-  int pad[3];
+  int pad[1];
   int page[kMaxChunkFp8 / 64];  // of the split's 64-key blocks
   float ks[kMaxChunkFp8 / 64], vs[kMaxChunkFp8 / 64];
   float qm[R];   // softmax scale (base 2) over the row's power of two
+  int lim[R];    // keys of the split that row r sees: those below lim[r] (0 or less: none)
+  int o_row[R], lse_row[R];  // where its results go, in rows of o and entries of lse; -1: no such row
 };
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
@@ -114,20 +123,22 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatil
   return ok;
 }
 
-// named barrier 1 over the softmax warps, with an OR of a flag
-__device__ __forceinline__ bool softmax_bar_or(bool v) {
+// named barrier over the four warps of a softmax group, with an OR of a flag
+__device__ __forceinline__ bool softmax_bar_or(int group, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\t"
       "setp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.or.pred po, 1, 128, pi;\n\t"
+      "bar.red.or.pred po, %2, 128, pi;\n\t"
       "selp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(v))
+      : "r"(static_cast<uint32_t>(v)), "r"(1 + group)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_bar(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
 
 // two floats -> two e5m2 codes, `lo` in the low byte
 __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
@@ -142,6 +153,13 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Largest value of the warp, NaN left out: one integer reduction, the floats
+// mapped to integers of the same order.
+__device__ __forceinline__ float warp_max_ordered(float v) {
+  const uint32_t u = __float_as_uint(v == v ? v : -INFINITY);
+  const uint32_t m = __reduce_max_sync(0xffffffffu, u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u));
+  return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -153,6 +171,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// MMA column of term k of row r: the rows of a softmax group lie together.
+template <int R, int kRows>
+__device__ __forceinline__ constexpr int column(int k, int r) {
+  return r / kRows * 3 * kRows + k * kRows + r % kRows;
+}
+
 // Byte offset of row n, byte c of an operand with rows of D bytes, swizzled
 // as TMA and the MMA descriptors have it.
 template <int kRow>
@@ -161,18 +185,21 @@ __device__ __forceinline__ int swizzled(int n, int c) {
   return n * kRow + (chunk << 4) + (c & 15);
 }
 
+// The first kN (at least) columns of this thread's TMEM lane from addr on.
 template <int kN>
 __device__ __forceinline__ void tmem_ld_row(uint32_t addr, uint32_t (&u)[kN]) {
 #pragma unroll
-  for (int c = 0; c < kN; c += 16) tmem_ld16(addr + c, u + c);
+  for (int c = 0; c + 16 <= kN; c += 16) tmem_ld16(addr + c, u + c);
+  if (kN % 16 == 8) tmem_ld8(addr + kN / 16 * 16, u + kN / 16 * 16);
   tmem_wait_ld();
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
+__global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     decode_fp8_split_kernel(const __grid_constant__ DecodeFp8Params p) {
   using C = Cfg<D, R>;
-  constexpr int kN = C::kN;
+  constexpr int kN = C::kN, kRows = C::kRows, kOut0 = C::kSoftWarps;  // kOut0: the first output warp
+  constexpr int kItemWarp = kOut0 + 4, kMmaWarp = kOut0 + 5, kLoadWarp = kOut0 + 6;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -180,10 +207,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
   const int rows = p.Nq * G;  // query rows of a KV head: row r is token r / G, head r % G of the group
 
   Item<R>* items = reinterpret_cast<Item<R>*>(smem + C::kOffItem);
-  static_assert(sizeof(Item<R>) == (12 + 3 * C::kMaxBlocks + R) * 4, "item size");
+  static_assert(sizeof(Item<R>) == (8 + 3 * C::kMaxBlocks + 4 * R) * 4, "item size");
   float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
   float* s_red = reinterpret_cast<float*>(smem + C::kOffRed);
   int* s_fail = reinterpret_cast<int*>(smem + C::kOffRed + 4 * R * 4);
+  volatile uint8_t* s_spoil = smem + C::kOffSpoil;
   float* s_ml = reinterpret_cast<float*>(smem + C::kOffMl);
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* bar_empty = bar_full + C::kStages;
@@ -196,14 +224,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
   uint64_t* bar_of = bar_o + 2;                  // [2] O^T and alpha read (D / 32 output warps)
   uint64_t* bar_ml = bar_of + 2;                 // [2] an item's m and l are there (4 softmax warps)
   uint64_t* bar_mf = bar_ml + 2;                 // [2] they were read (D / 32 output warps)
-  uint64_t* bar_drain = bar_mf + 2;
+  uint64_t* bar_sp = bar_mf + 2;                 // [2] group 0's look at the V rows that some rows do not see
+  uint64_t* bar_drain = bar_sp + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const uint32_t sQ = smem_u32(smem + C::kOffQ), sP = smem_u32(smem + C::kOffP);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 8) {
+  if (warp == kLoadWarp) {
     if (lane == 0) {
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
       for (int s = 0; s < C::kStages; ++s) {
         mbar_init(bar_full + s, 1);
         mbar_init(bar_empty + s, 1);
@@ -211,114 +242,120 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
       for (int i = 0; i < C::kItems; ++i) {
         mbar_init(bar_pages + i, 1);
         mbar_init(bar_ready + i, 1);
-        mbar_init(bar_free + i, 4 + D / 32 + 2);
+        mbar_init(bar_free + i, C::kSoftWarps + D / 32 + 2);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar_s + i, 1);
-        mbar_init(bar_p + i, 4);
+        mbar_init(bar_p + i, C::kSoftWarps);
         mbar_init(bar_o + i, 1);
         mbar_init(bar_of + i, D / 32);
-        mbar_init(bar_ml + i, 4);
+        mbar_init(bar_ml + i, C::kSoftWarps);
         mbar_init(bar_mf + i, D / 32);
+        mbar_init(bar_sp + i, 4);
       }
       mbar_init(bar_drain, 1);
       *abort_flag = 0;
       mbar_fence_init();
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= kOut0 && warp < kOut0 + 4) {
     // the MMA columns past 3R stay 0 in every Q and P
     constexpr int kPad = kN - 3 * R;
-    for (int i = tid - 128; i < C::kItems * kPad * (D / 4); i += 128) {
+    for (int i = tid - 32 * kOut0; i < C::kItems * kPad * (D / 4); i += 128) {
       const int n = 3 * R + i / (D / 4) % (kPad + (kPad == 0)), slot = i / (D / 4) / (kPad + (kPad == 0));
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sQ + slot * C::kQBytes + swizzled<D>(n, 4 * (i % (D / 4)))), "r"(0u)
                    : "memory");
     }
-    for (int i = tid - 128; i < 2 * kPad * (kTile / 4); i += 128) {
+    for (int i = tid - 32 * kOut0; i < 2 * kPad * (kTile / 4); i += 128) {
       const int n = 3 * R + i / (kTile / 4) % (kPad + (kPad == 0)), buf = i / (kTile / 4) / (kPad + (kPad == 0));
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sP + buf * kN * kTile + swizzled<128>(n, 4 * (i % (kTile / 4)))),
                    "r"(0u)
                    : "memory");
     }
     fence_proxy_async_smem();
-  } else if (warp == 10 && lane == 0) {
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S at columns 0, kN; O^T at 2 kN, 3 kN
+  uint32_t tmem = 0u;  // S at columns 0, kN; O^T at 2 kN, 3 kN
+  if (warp != kItemWarp) {  // it looks for its first item before it meets the others there
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *s_tmem;
+  }
   int n_issued = 0;               // the loader's tiles
 
-  if (warp < 4) {
+  if (warp < C::kSoftWarps) {
     // ================================================================ softmax
+    const int grp = warp >> 2, w4 = warp & 3, row = tid & 127;  // rows grp * kRows ..; TMEM lane (key of a tile)
+    float* red = s_red + grp * 4 * kRows;
+    int* fail = s_fail + grp * 4;
+    int looks = 0;  // times that group 0 looked at V rows
     bool failed = false, stop = false;
     int g = 0;  // tiles so far, over all items
     for (int n = 0; !stop; ++n) {
       const Item<R>& it = items[n % C::kItems];
       if (!wait_all(bar_ready + n % C::kItems, (n / C::kItems) & 1, abort_flag, 3)) failed = true;
-      if (softmax_bar_or(failed || *abort_flag)) {
+      if (softmax_bar_or(grp, failed || *abort_flag)) {
         *abort_flag = 1;
         break;
       }
       const int n_t = it.n_t, kn = it.kn;
       if (n_t < 0) break;
-      const int nr = min(R, rows - it.row0);
-      // keys of the split that row r sees: those below lim(r)
-      auto lim = [&](int r) { return min(kn, it.lim0 + (it.row0 + r) / G); };
-      const int lim_min = lim(0);
+      const int lim_min = it.lim_min;
       const float vmul = it.vref > 0.f ? kWeightScale / it.vref : 0.f;
-      float m[R], l[R], qm[R];
+      float m[kRows], l[kRows], qm[kRows];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < kRows; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
-        qm[r] = r < nr ? it.qm[r] : 0.f;
+        qm[r] = it.qm[grp * kRows + r];  // 0 for a row past the last: its scores are 0
       }
       for (int t = 0; t < n_t; ++t, ++g) {
         const int buf = g & 1, s = g % C::kStages;
-        const int key = t * kTile + tid;
+        const int key = t * kTile + row;
         const bool live = key < kn;
         const float ks = live ? it.ks[key >> 6] : 0.f, wv = live ? it.vs[key >> 6] * vmul : 0.f;
         if (!wait_all(bar_s + buf, (g >> 1) & 1, abort_flag, 4)) failed = true;
         tc_fence_after();
-        uint32_t u[kN];
-        tmem_ld_row<kN>(tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * kN, u);
+        constexpr int kLd = (3 * kRows + 7) / 8 * 8;
+        uint32_t u[kLd];
+        tmem_ld_row<kLd>(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + buf * kN + grp * 3 * kRows, u);
         tc_fence_before();
         const bool edge = (t + 1) * kTile > lim_min;  // uniform: some row does not see the whole tile
-        float x[R];
+        float x[kRows];
         bool big = false;
+        uint32_t hidden = 0u;  // rows that do not see this thread's key
+        if (edge) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float sum = __uint_as_float(u[r]) + __uint_as_float(u[R + r]) + __uint_as_float(u[2 * R + r]);
-          x[r] = sum * (qm[r] * ks);
-          if (edge && key >= lim(r)) x[r] = -INFINITY;
-          if (r >= nr) x[r] = -INFINITY;
+          for (int r = 0; r < kRows; ++r) hidden |= (key >= it.lim[grp * kRows + r] ? 1u : 0u) << r;
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float sum = __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]);
+          x[r] = (hidden >> r) & 1u ? -INFINITY : sum * (qm[r] * ks);
           big = big || x[r] > m[r] + kMoveLog2;  // -inf > -inf: no
         }
-        float al[R];
+        float al[kRows];
 #pragma unroll
-        for (int r = 0; r < R; ++r) al[r] = 1.f;
-        if (softmax_bar_or(big || failed || *abort_flag)) {
+        for (int r = 0; r < kRows; ++r) al[r] = 1.f;
+        if (softmax_bar_or(grp, big || failed || *abort_flag)) {
           // some row's reference moves (or a wait gave up)
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float mx = warp_max(x[r]);  // NaN scores are left out: they show in p
-            if (lane == 0) s_red[warp * R + r] = mx;
+          for (int r = 0; r < kRows; ++r) {
+            const float mx = warp_max_ordered(x[r]);  // NaN scores show in p
+            if (lane == 0) red[w4 * kRows + r] = mx;
           }
-          if (lane == 0) s_fail[warp] = failed || *abort_flag;
-          softmax_bar();
-          if (s_fail[0] | s_fail[1] | s_fail[2] | s_fail[3]) {
+          if (lane == 0) fail[w4] = failed || *abort_flag;
+          softmax_bar(grp);
+          if (fail[0] | fail[1] | fail[2] | fail[3]) {
             *abort_flag = 1;
             stop = true;
             break;
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float mx = fmaxf(fmaxf(s_red[r], s_red[R + r]), fmaxf(s_red[2 * R + r], s_red[3 * R + r]));
+          for (int r = 0; r < kRows; ++r) {
+            const float mx = fmaxf(fmaxf(red[r], red[kRows + r]), fmaxf(red[2 * kRows + r], red[3 * kRows + r]));
             if (mx > m[r] + kMoveLog2) {
               al[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mx);
               l[r] *= al[r];
@@ -326,66 +363,79 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
             }
           }
         }
+        // P and alpha of this buffer are free once tile g-2 is added up
+        if (g >= 2 && !wait_all(bar_of + buf, ((g - 2) >> 1) & 1, abort_flag, 6)) failed = true;
         // rows of V past the sequence may hold anything: they are cleared, so
         // that a weight of 0 adds exactly nothing.  A row that only some of the
         // new tokens see is cleared too if it holds a NaN, which its weight
-        // then carries to the rows that do see it.
+        // then carries to the rows that do see it.  Group 0 does so and tells
+        // the other (whose next tile but one waits for this one's O^T).
         float spoil = 0.f;
         if (edge) {
-          // long done: S needed it
-          if (!wait_all(bar_full + s, (g / C::kStages) & 1, abort_flag, 5)) failed = true;
-          const uint32_t vrow = smem_u32(smem + s * C::kStage + C::kOffV);
-          bool clear = !live;
-          if (live && key >= lim_min) {
-            uint32_t nan = 0u;
+          if (grp == 0) {
+            // long done: S needed it
+            if (!wait_all(bar_full + s, (g / C::kStages) & 1, abort_flag, 5)) failed = true;
+            const uint32_t vrow = smem_u32(smem + s * C::kStage + C::kOffV);
+            bool clear = !live;
+            if (live && key >= lim_min) {
+              uint32_t nan = 0u;
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
-              const uint4 w = ld_shared_v4(vrow + swizzled<D>(tid, c));
-              nan |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
-                     ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+              for (int c = 0; c < D; c += 16) {
+                const uint4 v = ld_shared_v4(vrow + swizzled<D>(row, c));
+                nan |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                       ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+              }
+              if (nan & 0x80808080u) {
+                clear = true;
+                spoil = NAN;
+              }
             }
-            if (nan & 0x80808080u) {
-              clear = true;
-              spoil = NAN;
+            if (clear) {
+#pragma unroll
+              for (int c = 0; c < D; c += 16) st_shared_v4(vrow + swizzled<D>(row, c), 0u, 0u, 0u, 0u);
             }
           }
-          if (clear) {
-#pragma unroll
-            for (int c = 0; c < D; c += 16) st_shared_v4(vrow + swizzled<D>(tid, c), 0u, 0u, 0u, 0u);
+          if (C::kGroups > 1 && lim_min < kn) {
+            if (grp == 0) {
+              s_spoil[(looks & 1) * kTile + row] = spoil != spoil;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_sp + (looks & 1));
+            } else {
+              if (!wait_all(bar_sp + (looks & 1), (looks >> 1) & 1, abort_flag, 19)) failed = true;
+              if (s_spoil[(looks & 1) * kTile + row]) spoil = NAN;
+            }
+            ++looks;
           }
         }
-        // P and alpha of this buffer are free once tile g-2 is added up
-        if (g >= 2 && !wait_all(bar_of + buf, ((g - 2) >> 1) & 1, abort_flag, 6)) failed = true;
-        float w[R];
+        float w[kRows];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < kRows; ++r) {
           float pr = ex2_approx(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-          if (edge && key >= lim(r)) pr = 0.f;
-          if (r >= nr) pr = 0.f;
+          if ((hidden >> r) & 1u) pr = 0.f;
           l[r] += pr;
           w[r] = pr * wv;
-          if (edge && key < lim(r)) w[r] += spoil;
+          if (edge && !((hidden >> r) & 1u)) w[r] += spoil;
         }
         const uint32_t pcol = sP + buf * kN * kTile;
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
+        for (int r = 0; r < kRows; r += 2) {
           float a = w[r], c = w[r + 1];
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const float ta = k < 2 ? lead3(a) : a, tc = k < 2 ? lead3(c) : c;
             const uint32_t two = e5m2x2(ta, tc);
-            st_shared_u8(pcol + swizzled<128>(k * R + r, tid), two);
-            st_shared_u8(pcol + swizzled<128>(k * R + r + 1, tid), two >> 8);
+            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + r, row), two);
+            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + r + 1, row), two >> 8);
             a -= ta;
             c -= tc;
           }
         }
-        if (tid < R) {
+        if (row < kRows) {
           float v = 1.f;
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (tid == r) v = al[r];
-          s_alpha[buf * R + tid] = v;
+          for (int r = 0; r < kRows; ++r)
+            if (row == r) v = al[r];
+          s_alpha[buf * R + grp * kRows + row] = v;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -396,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
       if (n >= 2 && !wait_all(bar_mf + (n & 1), ((n >> 1) - 1) & 1, abort_flag, 7)) failed = true;
       float* ml = s_ml + (n & 1) * 5 * R;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < kRows; ++r) {
         l[r] = warp_sum(l[r]);
-        if (lane == 0) ml[(1 + warp) * R + r] = l[r];
-        if (tid == 0) ml[r] = m[r];
+        if (lane == 0) ml[(1 + w4) * R + grp * kRows + r] = l[r];
+        if (row == 0) ml[grp * kRows + r] = m[r];
       }
       __syncwarp();
       if (lane == 0) {
@@ -407,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
         mbar_arrive(bar_free + n % C::kItems);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < kOut0 + 4) {
     // ================================================================ output
-    const int dd = tid - 128;
+    const int dd = tid - 32 * kOut0;
     if (dd < D) {
       int g = 0;
       bool ok = true;
@@ -428,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
           if (!ok) break;
           tc_fence_after();
           uint32_t u[kN];
-          tmem_ld_row<kN>(tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + (2 + buf) * kN, u);
+          tmem_ld_row<kN>(tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN, u);
           float al[R];
 #pragma unroll
           for (int r = 0; r < R; ++r) al[r] = s_alpha[buf * R + r];
@@ -438,20 +488,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
           for (int r = 0; r < R; ++r)
             acc[r] = fmaf(acc[r], al[r],
-                          __uint_as_float(u[r]) + __uint_as_float(u[R + r]) + __uint_as_float(u[2 * R + r]));
+                          __uint_as_float(u[column<R, kRows>(0, r)]) + __uint_as_float(u[column<R, kRows>(1, r)]) +
+                              __uint_as_float(u[column<R, kRows>(2, r)]));
         }
         if (!ok || !wait_all(bar_ml + (n & 1), (n >> 1) & 1, abort_flag, 11)) break;
         const float* ml = s_ml + (n & 1) * 5 * R;
-        const int nr = min(R, rows - it.row0), b = it.b, split = it.split, hkv = it.hkv, row0 = it.row0;
+        const int split = it.split;
         const bool direct = it.direct != 0;
         const float osc = it.vref * (1.f / kWeightScale);
         float o[R], lse[R];
+        int o_row[R], lse_row[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float lr = (ml[R + r] + ml[2 * R + r]) + (ml[3 * R + r] + ml[4 * R + r]);
           // l is 0 exactly where the row sees no key of the split (NaN, not 0, where a score is NaN)
           o[r] = lr == 0.f ? 0.f : acc[r] * osc / lr;
           lse[r] = lr == 0.f ? -INFINITY : (ml[r] + __log2f(lr)) * 0.6931471805599453f;
+          o_row[r] = it.o_row[r];
+          lse_row[r] = it.lse_row[r];
         }
         __syncwarp();
         if (lane == 0) {
@@ -460,20 +514,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          if (r >= nr) break;
-          const int tok = (row0 + r) / G, hq = hkv * G + (row0 + r) % G;
-          const long long qrow = (static_cast<long long>(b) * p.Nq + tok) * p.Hq + hq;
+          if (o_row[r] < 0) break;
           if (direct) {
-            static_cast<__nv_bfloat16*>(p.o)[qrow * D + dd] = __float2bfloat16_rn(o[r]);
-            if (dd == 0) p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + tok] = lse[r];
+            static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(o_row[r]) * D + dd] = __float2bfloat16_rn(o[r]);
+            if (dd == 0) p.lse[lse_row[r]] = lse[r];
           } else {
-            p.o_part[(qrow * p.n_split + split) * D + dd] = o[r];
-            if (dd == 0) p.lse_part[qrow * p.n_split + split] = lse[r];
+            const long long part = static_cast<long long>(o_row[r]) * p.n_split + split;
+            p.o_part[part * D + dd] = o[r];
+            if (dd == 0) p.lse_part[part] = lse[r];
           }
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kItemWarp) {
     // ================================================================ items
     // Item i of the whole call: j = i / H counts (sequence, split) pairs, the
     // full splits of all sequences first and the shorter last ones after them,
@@ -481,10 +534,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
     // the same cache rows).  The lanes hold 32 sequences at a time; j only
     // grows, so they walk the batch once for the full splits and once for the
     // rest.
+    // launched as a programmatic dependent of whatever ran before: nothing of
+    // that is read before this wait
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n_rblk = (rows + R - 1) / R, H = p.Hkv * n_rblk;
+    const int step_j = gridDim.x / H, step_h = gridDim.x - step_j * H;
     bool full_phase = true;
     int b0 = -32;
-    long long before = 0;  // pairs before the lanes' sequences
+    long long before = 0, j = blockIdx.x / H;  // pairs before the lanes' sequences; the next item's pair
+    int h = blockIdx.x - static_cast<int>(j) * H;
     int Lb = 0, cnt = 0, excl = 0, total = 0;
     // next 32 sequences; false past the last
     auto next_block = [&]() {
@@ -510,12 +568,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
       total = __shfl_sync(0xffffffffu, incl, 31);
       return true;
     };
+    // An item in hand: found, its page numbers and q on their way.
+    // 32 / R lanes share a row of q, each a run of kDims of it.
+    constexpr int kPg = C::kMaxBlocks / 32, kLanes = 32 / R, kDims = D / kLanes;
+    const int qr = lane / kLanes, qd = lane % kLanes * kDims;
+    struct Found {
+      bool more;
+      int b, split, len, h;
+      int pg[kPg];
+      int lim;  // cache positions that the lane's row sees: those below it
+      int o_row, lse_row;
+      uint4 q[kDims / 8];
+    };
     bool more = next_block();
-    for (int n = 0;; ++n) {
-      const int slot = n % C::kItems;
-      Item<R>& it = items[slot];
-      const long long i = blockIdx.x + static_cast<long long>(n) * gridDim.x, j = i / H;
-      const int h = static_cast<int>(i - j * H);
+    auto find = [&]() {
+      Found f;
+      f.h = h;
       while (more && j >= before + total) {
         more = next_block();
         if (!more && full_phase) {
@@ -525,122 +593,151 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
           more = next_block();
         }
       }
-      int b = 0, split = 0, len = 0;
+      f.more = more;
+      f.b = f.split = f.len = 0;
       if (more) {
         const int rel = static_cast<int>(j - before);
         const unsigned who = __ballot_sync(0xffffffffu, cnt > 0 && rel >= excl && rel < excl + cnt);
         const int src = __ffs(who) - 1;
-        b = b0 + src;
-        len = __shfl_sync(0xffffffffu, Lb, src);
-        split = full_phase ? rel - __shfl_sync(0xffffffffu, excl, src) : len / p.chunk;
-      }
-      if (n >= C::kItems && !wait_all(bar_free + slot, (n / C::kItems - 1) & 1, abort_flag, 12)) break;
-      const int k0 = split * p.chunk, kn = min(p.chunk, len - k0), n_blk = (kn + 63) / 64;
-      const int hkv = h / n_rblk, row0 = (h - hkv * n_rblk) * R;
-      if (lane == 0) {
-        it.n_t = more ? (kn + kTile - 1) / kTile : -1;
-        it.kn = kn;
-        it.b = b;
-        it.split = split;
-        it.hkv = hkv;
-        it.row0 = row0;
-        it.lim0 = len - p.Nq + 1 - k0;
-        it.direct = len <= p.chunk;
-      }
-      int pg[C::kMaxBlocks / 32];
-      if (more) {
+        f.b = b0 + src;
+        f.len = __shfl_sync(0xffffffffu, Lb, src);
+        f.split = full_phase ? rel - __shfl_sync(0xffffffffu, excl, src) : f.len / p.chunk;
+        const int k0 = f.split * p.chunk, n_blk = (min(p.chunk, f.len - k0) + 63) / 64;
 #pragma unroll
-        for (int k = 0; k < C::kMaxBlocks / 32; ++k) {
+        for (int k = 0; k < kPg; ++k) {
           const int blk = 32 * k + lane;
-          pg[k] = 0;
-          if (blk < n_blk) {
-            pg[k] = p.block_table[static_cast<long long>(b) * p.max_blocks + (k0 + 64 * blk) / p.page_size];
-            if (pg[k] < 0 || pg[k] >= p.num_pages) {
-              record(2, kDevBadPage);
-              pg[k] = 0;  // keep every load inside the page pool; the result is flagged
-            }
-            it.page[blk] = pg[k];
+          f.pg[k] = blk < n_blk ? p.block_table[static_cast<long long>(f.b) * p.max_blocks + (k0 + 64 * blk) / p.page_size]
+                                : 0;
+        }
+        const int hkv = f.h / n_rblk, row = (f.h - hkv * n_rblk) * R + qr;
+        const int tok = row / G;
+        f.lim = f.len - p.Nq + 1 + tok;
+        const int hq = hkv * G + row - tok * G;
+        f.o_row = row < rows ? (f.b * p.Nq + tok) * p.Hq + hq : -1;
+        f.lse_row = (f.b * p.Hq + hq) * p.Nq + tok;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                                 ((static_cast<long long>(f.b) * p.Nq + tok) * p.Hq + hq) * D + qd;
+#pragma unroll
+        for (int c = 0; c < kDims / 8; ++c)
+          f.q[c] = row < rows ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      j += step_j;
+      h += step_h;
+      if (h >= H) {
+        h -= H;
+        ++j;
+      }
+      return f;
+    };
+    Found cur = find();
+    __syncthreads();
+    for (int n = 0;; ++n) {
+      const int slot = n % C::kItems;
+      Item<R>& it = items[slot];
+      // the next item's loads go out before this one's are waited for
+      Found nxt;
+      nxt.more = false;
+      const int k0 = cur.split * p.chunk, kn = min(p.chunk, cur.len - k0), n_blk = (kn + 63) / 64;
+      const int hkv = cur.h / n_rblk, row0 = (cur.h - hkv * n_rblk) * R;
+      float ks[kPg], vs[kPg];
+      if (cur.more) {
+        // scales before the loader is told of the pages: their latency is not
+        // spent behind its loads
+#pragma unroll
+        for (int k = 0; k < kPg; ++k) {
+          if (cur.pg[k] < 0 || cur.pg[k] >= p.num_pages) {
+            record(2, kDevBadPage);
+            cur.pg[k] = 0;  // keep every load inside the page pool; the result is flagged
+          }
+          ks[k] = vs[k] = 0.f;
+          if (32 * k + lane < n_blk) {
+            ks[k] = p.k_scales[static_cast<long long>(cur.pg[k]) * p.Hkv + hkv];
+            vs[k] = p.v_scales[static_cast<long long>(cur.pg[k]) * p.Hkv + hkv];
           }
         }
       }
+      if (n >= C::kItems && !wait_all(bar_free + slot, (n / C::kItems - 1) & 1, abort_flag, 12)) break;
+      if (lane == 0) {
+        it.n_t = cur.more ? (kn + kTile - 1) / kTile : -1;
+        it.kn = kn;
+        it.split = cur.split;
+        it.hkv = hkv;
+        it.lim_min = min(kn, cur.len - p.Nq + 1 + row0 / G - k0);
+        it.direct = cur.len <= p.chunk;
+      }
+      if (cur.more) {
+#pragma unroll
+        for (int k = 0; k < kPg; ++k)
+          if (32 * k + lane < n_blk) it.page[32 * k + lane] = cur.pg[k];
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_pages + slot);
-      if (more) {
+      if (cur.more) {
+        nxt = find();
+        // q as three e5m2 terms a row
+        uint32_t amax = 0u;
+#pragma unroll
+        for (int c = 0; c < kDims / 8; ++c) {
+          const uint32_t w[4] = {cur.q[c].x, cur.q[c].y, cur.q[c].z, cur.q[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const bool fin = amax < 0x7f800000u;  // bits of the row's largest magnitude
+        const int e = fin ? max(static_cast<int>(amax >> 23) - 127, -100) : 0;
+        const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+        const uint32_t q_at = sQ + slot * C::kQBytes;
+#pragma unroll
+        for (int c = 0; c < kDims / 8; ++c) {  // 8 values: 8 bytes a term, at a multiple of 8
+          const uint32_t w[4] = {cur.q[c].x, cur.q[c].y, cur.q[c].z, cur.q[c].w};
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16lo(w[i]) * f;
+            x[2 * i + 1] = bf16hi(w[i]) * f;
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            float t3[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              t3[i] = lead3(x[i]);
+              x[i] -= t3[i];
+            }
+            const uint32_t at = q_at + swizzled<D>(column<R, kRows>(j, qr), qd + 8 * c);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
+                         "r"(e5m2x2(t3[0], t3[1]) | (e5m2x2(t3[2], t3[3]) << 16)),
+                         "r"(e5m2x2(t3[4], t3[5]) | (e5m2x2(t3[6], t3[7]) << 16))
+                         : "memory");
+          }
+        }
+        if (lane % kLanes == 0) {
+          it.lim[qr] = min(kn, cur.lim - k0);
+          it.o_row[qr] = cur.o_row;
+          it.lse_row[qr] = cur.lse_row;
+          // a row with an infinity or NaN: every score NaN
+          it.qm[qr] = fin ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2 : NAN;
+        }
         float vref = 0.f;
 #pragma unroll
-        for (int k = 0; k < C::kMaxBlocks / 32; ++k) {
-          const int blk = 32 * k + lane;
-          if (blk < n_blk) {
-            it.ks[blk] = p.k_scales[static_cast<long long>(pg[k]) * p.Hkv + hkv];
-            const float vs = p.v_scales[static_cast<long long>(pg[k]) * p.Hkv + hkv];
-            it.vs[blk] = vs;
-            vref = fmaxf(vref, vs);
+        for (int k = 0; k < kPg; ++k) {
+          if (32 * k + lane < n_blk) {
+            it.ks[32 * k + lane] = ks[k];
+            it.vs[32 * k + lane] = vs[k];
+            vref = fmaxf(vref, vs[k]);
           }
         }
         vref = warp_max(vref);
         if (lane == 0) it.vref = vref;
-        // q as three e5m2 terms a row: column term * R + r
-        const int nr = min(R, rows - row0);
-        const uint32_t q_at = sQ + slot * C::kQBytes;
-        float x[R][D / 32];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int tok = (row0 + r) / G, hq = hkv * G + (row0 + r) % G;
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; i2 += 2) {
-            uint32_t two = 0u;
-            if (r < nr)
-              two = *reinterpret_cast<const uint32_t*>(
-                  static_cast<const __nv_bfloat16*>(p.q) +
-                  ((static_cast<long long>(b) * p.Nq + tok) * p.Hq + hq) * D + (D / 32) * lane + i2);
-            x[r][i2] = bf16lo(two);
-            x[r][i2 + 1] = bf16hi(two);
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float amax = 0.f;
-          bool fin = true;
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; ++i2) {
-            fin = fin && fabsf(x[r][i2]) < INFINITY;
-            amax = fmaxf(amax, fabsf(x[r][i2]));
-          }
-          amax = warp_max(amax);
-          fin = __all_sync(0xffffffffu, fin);
-          const int e = fin ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100) : 0;
-          const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-          uint32_t term[3] = {0u, 0u, 0u};
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; i2 += 2) {
-            float a = fin ? x[r][i2] * f : 0.f, c = fin ? x[r][i2 + 1] * f : 0.f;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const float ta = lead3(a), tc = lead3(c);
-              term[k] |= e5m2x2(ta, tc) << (8 * i2);
-              a -= ta;
-              c -= tc;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t at = q_at + swizzled<D>(k * R + r, (D / 32) * lane);
-            if (D == 128)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(term[k]) : "memory");
-            else
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(term[k])) : "memory");
-          }
-          // a row with an infinity or NaN: every score NaN
-          if (lane == 0)
-            it.qm[r] = fin ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2 : NAN;
-        }
         fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ready + slot);
-      if (!more) break;
+      if (!cur.more) break;
+      cur = nxt;
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ================================================================ MMA
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_e4m3_e5m2_f32(128, kN, 0), idesc_o = idesc_e4m3_e5m2_f32(128, kN, 1);
@@ -735,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
   } else {
     // ================================================================ loads
     if (lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const Item<R>& it = items[n % C::kItems];
@@ -768,27 +866,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
     __syncwarp();
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
 }
 
-// One block of 8 warps per row of q: LSE = ln sum_s exp(LSE_s), O = sum_s
-// exp(LSE_s - LSE) O_s.  A warp takes every eighth split, D/32 values a lane,
-// four splits' loads in flight; the warps' sums are added in a fixed order.
-constexpr int kCombineWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(32 * kCombineWarps) decode_fp8_combine_kernel(const DecodeFp8CombineParams p) {
-  constexpr int kV = D / 32;
-  __shared__ float s_max[kCombineWarps], s_tot[kCombineWarps];
-  __shared__ float s_acc[kCombineWarps][D];
-  const long long qrow = blockIdx.x;
-  const int hq = static_cast<int>(qrow % p.Hq);
-  const int i = static_cast<int>(qrow / p.Hq % p.Nq);
-  const int b = static_cast<int>(qrow / p.Hq / p.Nq);
+// LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s for each row of q.
+// A block of kWarps warps takes kCols columns of a row, a warp every
+// kWarps-th split, four splits' loads in flight; the warps' sums are added in
+// a fixed order.  Few splits: eight warps and the whole row.  Many (a few
+// long sequences, so few rows too): sixteen warps for each 32 columns, as one
+// block's loads are then what the step waits for (64 rows of 512 splits: 39 us
+// in whole rows).
+template <int D, int kCols, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const DecodeFp8CombineParams p) {
+  constexpr int kV = kCols / 32, kBlocks = D / kCols;
+  __shared__ float s_max[kWarps], s_tot[kWarps];
+  __shared__ float s_acc[kWarps][kCols];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qrow = blockIdx.x / kBlocks, col0 = blockIdx.x % kBlocks * kCols;
+  const int bi = qrow / p.Hq, hq = qrow - bi * p.Hq, b = bi / p.Nq, i = bi - b * p.Nq;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // launched as a programmatic dependent of the split kernel: wait until all
   // of its partials are written and visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -796,34 +895,37 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode_fp8_combine_kernel(
   Lb = Lb < 0 ? 0 : (Lb > p.max_seqlen ? p.max_seqlen : Lb);
   const int ns = (Lb + p.chunk - 1) / p.chunk;
   if (ns == 1) return;  // written by the split kernel
-  const float* lp = p.lse_part + qrow * p.n_split;
-  const float* op = p.o_part + qrow * p.n_split * D + kV * lane;
+  const float* lp = p.lse_part + static_cast<long long>(qrow) * p.n_split;
+  const float* op = p.o_part + static_cast<long long>(qrow) * p.n_split * D + col0 + kV * lane;
   float mx = -INFINITY;
-  for (int s = threadIdx.x; s < ns; s += 32 * kCombineWarps) mx = fmaxf(mx, lp[s]);
+  for (int s = threadIdx.x; s < ns; s += 32 * kWarps) mx = fmaxf(mx, lp[s]);
   mx = warp_max(mx);
   if (lane == 0) s_max[warp] = mx;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) mx = fmaxf(mx, s_max[w]);
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_max[w]);
   if (mx == -INFINITY) mx = 0.f;  // no key seen (or every LSE NaN): the weights are then 0 (NaN)
   float tot = 0.f, acc[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) acc[k] = 0.f;
-  for (int s = warp; s < ns; s += 4 * kCombineWarps) {
+  for (int s = warp; s < ns; s += 4 * kWarps) {
     float lv[4], ov[4][kV];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int su = s + u * kCombineWarps;
+      const int su = s + u * kWarps;
       lv[u] = su < ns ? lp[su] : -INFINITY;
 #pragma unroll
       for (int k = 0; k < kV; ++k) ov[u][k] = 0.f;
       if (su < ns) {
+        const float* o = op + static_cast<long long>(su) * D;
         if (kV == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(op + static_cast<long long>(su) * D);
-          ov[u][0] = v.x; ov[u][1] = v.y; ov[u][kV - 2] = v.z; ov[u][kV - 1] = v.w;
+          const float4 v = *reinterpret_cast<const float4*>(o);
+          ov[u][0] = v.x; ov[u][1 % kV] = v.y; ov[u][2 % kV] = v.z; ov[u][3 % kV] = v.w;
+        } else if (kV == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(o);
+          ov[u][0] = v.x; ov[u][1 % kV] = v.y;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(op + static_cast<long long>(su) * D);
-          ov[u][0] = v.x; ov[u][1] = v.y;
+          ov[u][0] = *o;
         }
       }
     }
@@ -839,16 +941,36 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode_fp8_combine_kernel(
 #pragma unroll
   for (int k = 0; k < kV; ++k) s_acc[warp][kV * lane + k] = acc[k];
   __syncthreads();
-  if (threadIdx.x >= D) return;
+  if (threadIdx.x >= kCols) return;
   float a = 0.f, sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     a += s_acc[w][threadIdx.x];
     sum += s_tot[w];
   }
   const bool none = sum == 0.f;
-  static_cast<__nv_bfloat16*>(p.o)[qrow * D + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : a / sum);
-  if (threadIdx.x == 0) p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + i] = none ? -INFINITY : mx + logf(sum);
+  static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(qrow) * D + col0 + threadIdx.x] =
+      __float2bfloat16_rn(none ? 0.f : a / sum);
+  if (threadIdx.x == 0 && col0 == 0)
+    p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + i] = none ? -INFINITY : mx + logf(sum);
+}
+
+// A launch that may start while the kernel before it ends (that kernel's
+// results are waited for on the device).
+template <typename P>
+cudaError_t launch_dependent(void (*kern)(const P), unsigned grid, unsigned block, int smem, const P& p,
+                             cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int D, int R>
@@ -860,21 +982,16 @@ cudaError_t launch_rows(const DecodeFp8Params& p, int sms, cudaStream_t stream) 
   const int rows = p.Nq * (p.Hq / p.Hkv);
   const long long items = static_cast<long long>(p.Hkv) * ((rows + R - 1) / R) * p.B * p.n_split;
   const long long ctas = static_cast<long long>(sms) * C::kCtas;
-  kern<<<static_cast<unsigned>(items < ctas ? items : ctas), kThreads, C::kAlloc, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_dependent<DecodeFp8Params>(kern, static_cast<unsigned>(items < ctas ? items : ctas), C::kThreads, C::kAlloc,
+                                        p, stream);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const DecodeFp8CombineParams c = {p.o_part, p.lse_part, p.seqlens, p.o, p.lse, p.Nq, p.Hq, p.max_seqlen, p.chunk,
                                     p.n_split};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Nq * p.Hq);
-  cfg.blockDim = dim3(32 * kCombineWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D>, c);
+  const unsigned q_rows = static_cast<unsigned>(p.B) * p.Nq * p.Hq;
+  if (p.n_split <= 32 || q_rows > 0x7fffffffu / (D / 32))
+    return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, D, 8>, q_rows, 256, 0, c, stream);
+  return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, 32, 16>, q_rows * (D / 32), 512, 0, c,
+                                                  stream);
 }
 
 template <int D>

@@ -149,7 +149,7 @@ def test_binding_refuses_tensors_off_the_gpu():
 
 def test_row_strides_of_parts_of_a_projection():
     """The binding reads parts of fused projections in place: their row distance, or a refusal."""
-    dev = torch.device("cpu")
+    dev = -1   # the CPU
     qkv = torch.zeros((3, 5, 12, 64), dtype=torch.bfloat16)
     rows = lambda t: _native._rows("t", t, tuple(t.shape), dev)[1]
     assert rows(qkv[:, :, :8]) == 12 * 64
