@@ -242,6 +242,12 @@ int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen) {
   return 1024;
 }
 
+size_t attn_splitkv_fp8_workspace_size(int B, int Nq, int Hq, int max_seqlen, int d, int chunk) {
+  if (Nq < 1 || Hq < 1 || static_cast<long long>(Nq) * Hq > kIntMax) return 0;
+  const size_t parts = attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk);
+  return parts ? parts + 16 : 0;
+}
+
 attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
                                        const float* v_scales, const int* block_table, int max_blocks, int page_size,
                                        int num_pages, const int* seqlens, void* o, float* lse, int B, int Nq, int Hq,
@@ -255,7 +261,8 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   if (cap + Nq + 256 > kIntMax || Nq > 64 || B > 65535 || chunk > attn::kMaxChunkFp8 || (cap + chunk - 1) / chunk > 65535 ||
       static_cast<long long>(Nq) * Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Nq * Hq > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  // rows, and items (at most one a row and split) with a margin for claims past the last, in 32 bits
+  if (static_cast<long long>(B) * Nq * Hq * ((cap + chunk - 1) / chunk) > kIntMax) return ATTN_ERR_UNSUPPORTED;
   if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !block_table || !seqlens || !o || !lse)
     return ATTN_ERR_INVALID_ARG;
   if (off16(q) || off16(k_pages) || off16(v_pages) || off16(o) || off4(k_scales) || off4(v_scales) ||
@@ -263,7 +270,7 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
     return ATTN_ERR_MISALIGNED;
   const int max_seqlen = static_cast<int>(cap);
   if (!workspace || off16(workspace) ||
-      workspace_bytes < attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk))
+      workspace_bytes < attn_splitkv_fp8_workspace_size(B, Nq, Hq, max_seqlen, d, chunk))
     return ATTN_ERR_WORKSPACE;
   attn::DecodeFp8Params p;
   std::memset(&p, 0, sizeof p);
@@ -292,7 +299,9 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   p.n_split = static_cast<int>((cap + chunk - 1) / chunk);
   const size_t parts = static_cast<size_t>(B) * Nq * Hq * p.n_split;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts * d * sizeof(float));
+  p.lse_part = p.o_part + parts * d;
+  p.counter = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) +
+                                          attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
   return attn::launch_decode_fp8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }

@@ -538,11 +538,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     // that is read before this wait
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n_rblk = (rows + R - 1) / R, H = p.Hkv * n_rblk;
-    const int step_j = gridDim.x / H, step_h = gridDim.x - step_j * H;
     bool full_phase = true;
     int b0 = -32;
-    long long before = 0, j = blockIdx.x / H;  // pairs before the lanes' sequences; the next item's pair
-    int h = blockIdx.x - static_cast<int>(j) * H;
+    long long before = 0;  // pairs before the lanes' sequences
     int Lb = 0, cnt = 0, excl = 0, total = 0;
     // next 32 sequences; false past the last
     auto next_block = [&]() {
@@ -568,22 +566,40 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       total = __shfl_sync(0xffffffffu, incl, 31);
       return true;
     };
-    // An item in hand: found, its page numbers and q on their way.
+    // The first item is the CTA's own number; further ones are claimed from a
+    // counter where there is one (SMs do not get equal shares of the memory's
+    // rate: with equal shares of the work the slowest ended 15 to 20% after
+    // the mean), else every gridDim-th follows.  A claim is asked for an item
+    // before it is used.
+    unsigned claimed = blockIdx.x;
+    auto claim = [&]() {
+      if (p.counter == nullptr)
+        claimed += gridDim.x;  // fits: the host sees to it
+      else if (lane == 0)
+        claimed = gridDim.x + atomicAdd(p.counter, 1u);
+    };
     // 32 / R lanes share a row of q, each a run of kDims of it.
     constexpr int kPg = C::kMaxBlocks / 32, kLanes = 32 / R, kDims = D / kLanes;
     const int qr = lane / kLanes, qd = lane % kLanes * kDims;
-    struct Found {
+    struct Found {  // an item found, its page numbers on their way
       bool more;
-      int b, split, len, h;
+      int b, split, len, hkv, row0;
       int pg[kPg];
+    };
+    struct Loading {  // its scales and q on their way
+      bool more;
+      int k0, kn, n_blk;
       int lim;  // cache positions that the lane's row sees: those below it
       int o_row, lse_row;
+      float ks[kPg], vs[kPg];
       uint4 q[kDims / 8];
     };
     bool more = next_block();
     auto find = [&]() {
       Found f;
-      f.h = h;
+      const unsigned i = __shfl_sync(0xffffffffu, claimed, 0);
+      claim();
+      const unsigned j = i / static_cast<unsigned>(H), h = i - j * H;
       while (more && j >= before + total) {
         more = next_block();
         if (!more && full_phase) {
@@ -595,6 +611,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       f.more = more;
       f.b = f.split = f.len = 0;
+      f.hkv = h / n_rblk;
+      f.row0 = (h - f.hkv * n_rblk) * R;
+#pragma unroll
+      for (int k = 0; k < kPg; ++k) f.pg[k] = 0;
       if (more) {
         const int rel = static_cast<int>(j - before);
         const unsigned who = __ballot_sync(0xffffffffu, cnt > 0 && rel >= excl && rel < excl + cnt);
@@ -606,74 +626,73 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
           const int blk = 32 * k + lane;
-          f.pg[k] = blk < n_blk ? p.block_table[static_cast<long long>(f.b) * p.max_blocks + (k0 + 64 * blk) / p.page_size]
-                                : 0;
+          if (blk < n_blk)
+            f.pg[k] = p.block_table[static_cast<long long>(f.b) * p.max_blocks + (k0 + 64 * blk) / p.page_size];
         }
-        const int hkv = f.h / n_rblk, row = (f.h - hkv * n_rblk) * R + qr;
-        const int tok = row / G;
-        f.lim = f.len - p.Nq + 1 + tok;
-        const int hq = hkv * G + row - tok * G;
-        f.o_row = row < rows ? (f.b * p.Nq + tok) * p.Hq + hq : -1;
-        f.lse_row = (f.b * p.Hq + hq) * p.Nq + tok;
+      }
+      return f;
+    };
+    // Item n, found: tells the loader, starts its other loads (before the
+    // loader's, behind which they would wait).  False: a wait gave up.
+    bool ok = true;
+    auto open = [&](Found& f, int n) {
+      Loading a;
+      const int slot = n % C::kItems;
+      Item<R>& it = items[slot];
+      a.more = f.more;
+      a.k0 = f.split * p.chunk;
+      a.kn = min(p.chunk, f.len - a.k0);
+      a.n_blk = (a.kn + 63) / 64;
+      a.lim = a.o_row = a.lse_row = 0;
+      if (f.more) {
+#pragma unroll
+        for (int k = 0; k < kPg; ++k) {
+          if (f.pg[k] < 0 || f.pg[k] >= p.num_pages) {
+            record(2, kDevBadPage);
+            f.pg[k] = 0;  // keep every load inside the page pool; the result is flagged
+          }
+          a.ks[k] = a.vs[k] = 0.f;
+          if (32 * k + lane < a.n_blk) {
+            a.ks[k] = p.k_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
+            a.vs[k] = p.v_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
+          }
+        }
+        const int row = f.row0 + qr, tok = row / G, hq = f.hkv * G + row - tok * G;
+        a.lim = f.len - p.Nq + 1 + tok;
+        a.o_row = row < rows ? (f.b * p.Nq + tok) * p.Hq + hq : -1;
+        a.lse_row = (f.b * p.Hq + hq) * p.Nq + tok;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
                                  ((static_cast<long long>(f.b) * p.Nq + tok) * p.Hq + hq) * D + qd;
 #pragma unroll
         for (int c = 0; c < kDims / 8; ++c)
-          f.q[c] = row < rows ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+          a.q[c] = row < rows ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
       }
-      j += step_j;
-      h += step_h;
-      if (h >= H) {
-        h -= H;
-        ++j;
+      if (n >= C::kItems && !wait_all(bar_free + slot, (n / C::kItems - 1) & 1, abort_flag, 12)) {
+        ok = false;
+        return a;
       }
-      return f;
-    };
-    Found cur = find();
-    __syncthreads();
-    for (int n = 0;; ++n) {
-      const int slot = n % C::kItems;
-      Item<R>& it = items[slot];
-      // the next item's loads go out before this one's are waited for
-      Found nxt;
-      nxt.more = false;
-      const int k0 = cur.split * p.chunk, kn = min(p.chunk, cur.len - k0), n_blk = (kn + 63) / 64;
-      const int hkv = cur.h / n_rblk, row0 = (cur.h - hkv * n_rblk) * R;
-      float ks[kPg], vs[kPg];
-      if (cur.more) {
-        // scales before the loader is told of the pages: their latency is not
-        // spent behind its loads
-#pragma unroll
-        for (int k = 0; k < kPg; ++k) {
-          if (cur.pg[k] < 0 || cur.pg[k] >= p.num_pages) {
-            record(2, kDevBadPage);
-            cur.pg[k] = 0;  // keep every load inside the page pool; the result is flagged
-          }
-          ks[k] = vs[k] = 0.f;
-          if (32 * k + lane < n_blk) {
-            ks[k] = p.k_scales[static_cast<long long>(cur.pg[k]) * p.Hkv + hkv];
-            vs[k] = p.v_scales[static_cast<long long>(cur.pg[k]) * p.Hkv + hkv];
-          }
-        }
-      }
-      if (n >= C::kItems && !wait_all(bar_free + slot, (n / C::kItems - 1) & 1, abort_flag, 12)) break;
       if (lane == 0) {
-        it.n_t = cur.more ? (kn + kTile - 1) / kTile : -1;
-        it.kn = kn;
-        it.split = cur.split;
-        it.hkv = hkv;
-        it.lim_min = min(kn, cur.len - p.Nq + 1 + row0 / G - k0);
-        it.direct = cur.len <= p.chunk;
+        it.n_t = f.more ? (a.kn + kTile - 1) / kTile : -1;
+        it.kn = a.kn;
+        it.split = f.split;
+        it.hkv = f.hkv;
+        it.lim_min = min(a.kn, f.len - p.Nq + 1 + f.row0 / G - a.k0);
+        it.direct = f.len <= p.chunk;
       }
-      if (cur.more) {
+      if (f.more) {
 #pragma unroll
         for (int k = 0; k < kPg; ++k)
-          if (32 * k + lane < n_blk) it.page[32 * k + lane] = cur.pg[k];
+          if (32 * k + lane < a.n_blk) it.page[32 * k + lane] = f.pg[k];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_pages + slot);
+      return a;
+    };
+    // Item n, its loads landed: the rest of its description, and its Q operand.
+    auto finish = [&](const Loading& cur, int n) {
+      const int slot = n % C::kItems;
+      Item<R>& it = items[slot];
       if (cur.more) {
-        nxt = find();
         // q as three e5m2 terms a row
         uint32_t amax = 0u;
 #pragma unroll
@@ -698,14 +717,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             x[2 * i + 1] = bf16hi(w[i]) * f;
           }
 #pragma unroll
-          for (int j = 0; j < 3; ++j) {
+          for (int k = 0; k < 3; ++k) {
             float t3[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               t3[i] = lead3(x[i]);
               x[i] -= t3[i];
             }
-            const uint32_t at = q_at + swizzled<D>(column<R, kRows>(j, qr), qd + 8 * c);
+            const uint32_t at = q_at + swizzled<D>(column<R, kRows>(k, qr), qd + 8 * c);
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
                          "r"(e5m2x2(t3[0], t3[1]) | (e5m2x2(t3[2], t3[3]) << 16)),
                          "r"(e5m2x2(t3[4], t3[5]) | (e5m2x2(t3[6], t3[7]) << 16))
@@ -713,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           }
         }
         if (lane % kLanes == 0) {
-          it.lim[qr] = min(kn, cur.lim - k0);
+          it.lim[qr] = min(cur.kn, cur.lim - cur.k0);
           it.o_row[qr] = cur.o_row;
           it.lse_row[qr] = cur.lse_row;
           // a row with an infinity or NaN: every score NaN
@@ -722,10 +741,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         float vref = 0.f;
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
-          if (32 * k + lane < n_blk) {
-            it.ks[32 * k + lane] = ks[k];
-            it.vs[32 * k + lane] = vs[k];
-            vref = fmaxf(vref, vs[k]);
+          if (32 * k + lane < cur.n_blk) {
+            it.ks[32 * k + lane] = cur.ks[k];
+            it.vs[32 * k + lane] = cur.vs[k];
+            vref = fmaxf(vref, cur.vs[k]);
           }
         }
         vref = warp_max(vref);
@@ -734,8 +753,29 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ready + slot);
-      if (!cur.more) break;
-      cur = nxt;
+    };
+    Found nxt = find();
+    __syncthreads();
+    // the first item by itself, then with item n+1's loads and item n+2's page
+    // numbers on their way while item n is finished
+    Loading cur = open(nxt, 0);
+    if (cur.more) nxt = find();
+    finish(cur, 0);
+    if (cur.more) {
+      cur = open(nxt, 1);
+      if (cur.more) nxt = find();
+      for (int n = 1; ok; ++n) {
+        Loading then;
+        then.more = false;
+        if (cur.more) {
+          then = open(nxt, n + 1);
+          if (!ok) break;
+          if (then.more) nxt = find();
+        }
+        finish(cur, n);
+        if (!cur.more) break;
+        cur = then;
+      }
     }
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA
@@ -874,12 +914,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 
 // LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s for each row of q.
 // A block of kWarps warps takes kCols columns of a row, a warp every
-// kWarps-th split, four splits' loads in flight; the warps' sums are added in
-// a fixed order.  Few splits: eight warps and the whole row.  Many (a few
-// long sequences, so few rows too): sixteen warps for each 32 columns, as one
+// kWarps-th split, kBatch splits' loads in flight; the warps' sums are added
+// in a fixed order.  Few splits: eight warps and the whole row.  Many (a few
+// long sequences, so few rows too): 32 warps for each 32 columns, as one
 // block's loads are then what the step waits for (64 rows of 512 splits: 39 us
-// in whole rows).
-template <int D, int kCols, int kWarps>
+// in whole rows by eight warps).
+template <int D, int kCols, int kWarps, int kBatch>
 __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const DecodeFp8CombineParams p) {
   constexpr int kV = kCols / 32, kBlocks = D / kCols;
   __shared__ float s_max[kWarps], s_tot[kWarps];
@@ -897,21 +937,12 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const D
   if (ns == 1) return;  // written by the split kernel
   const float* lp = p.lse_part + static_cast<long long>(qrow) * p.n_split;
   const float* op = p.o_part + static_cast<long long>(qrow) * p.n_split * D + col0 + kV * lane;
-  float mx = -INFINITY;
-  for (int s = threadIdx.x; s < ns; s += 32 * kWarps) mx = fmaxf(mx, lp[s]);
-  mx = warp_max(mx);
-  if (lane == 0) s_max[warp] = mx;
-  __syncthreads();
+  // kBatch splits of the warp: their LSEs and this lane's columns.  The first
+  // batch is loaded before the largest LSE is known.
+  float lv[kBatch], ov[kBatch][kV];
+  auto load = [&](int s) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_max[w]);
-  if (mx == -INFINITY) mx = 0.f;  // no key seen (or every LSE NaN): the weights are then 0 (NaN)
-  float tot = 0.f, acc[kV];
-#pragma unroll
-  for (int k = 0; k < kV; ++k) acc[k] = 0.f;
-  for (int s = warp; s < ns; s += 4 * kWarps) {
-    float lv[4], ov[4][kV];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       const int su = s + u * kWarps;
       lv[u] = su < ns ? lp[su] : -INFINITY;
 #pragma unroll
@@ -929,8 +960,23 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const D
         }
       }
     }
+  };
+  load(warp);
+  float mx = -INFINITY;
+  for (int s = threadIdx.x; s < ns; s += 32 * kWarps) mx = fmaxf(mx, lp[s]);
+  mx = warp_max(mx);
+  if (lane == 0) s_max[warp] = mx;
+  __syncthreads();
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_max[w]);
+  if (mx == -INFINITY) mx = 0.f;  // no key seen (or every LSE NaN): the weights are then 0 (NaN)
+  float tot = 0.f, acc[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+  for (int s = warp; s < ns; s += kBatch * kWarps) {
+    if (s != warp) load(s);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
       const float w = expf(lv[u] - mx);
       tot += w;
 #pragma unroll
@@ -973,15 +1019,32 @@ cudaError_t launch_dependent(void (*kern)(const P), unsigned grid, unsigned bloc
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Clears the counter that items are claimed from: the workspace comes with any contents.
+struct CounterParams {
+  unsigned* counter;
+};
+__global__ void __launch_bounds__(32) decode_fp8_counter_kernel(const CounterParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // a call before this one may use the same workspace
+  if (threadIdx.x == 0) *p.counter = 0u;
+}
+
 template <int D, int R>
-cudaError_t launch_rows(const DecodeFp8Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch_rows(DecodeFp8Params p, int sms, cudaStream_t stream) {
   using C = Cfg<D, R>;
   auto kern = decode_fp8_split_kernel<D, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
   const int rows = p.Nq * (p.Hq / p.Hkv);
+  // the most items there can be: the lengths are known on the device alone
   const long long items = static_cast<long long>(p.Hkv) * ((rows + R - 1) / R) * p.B * p.n_split;
   const long long ctas = static_cast<long long>(sms) * C::kCtas;
+  if (items <= ctas) {
+    p.counter = nullptr;
+  } else {
+    e = launch_dependent<CounterParams>(decode_fp8_counter_kernel, 1, 32, 0, {p.counter}, stream);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_dependent<DecodeFp8Params>(kern, static_cast<unsigned>(items < ctas ? items : ctas), C::kThreads, C::kAlloc,
                                         p, stream);
   if (e != cudaSuccess || p.n_split == 1) return e;
@@ -989,8 +1052,8 @@ cudaError_t launch_rows(const DecodeFp8Params& p, int sms, cudaStream_t stream) 
                                     p.n_split};
   const unsigned q_rows = static_cast<unsigned>(p.B) * p.Nq * p.Hq;
   if (p.n_split <= 32 || q_rows > 0x7fffffffu / (D / 32))
-    return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, D, 8>, q_rows, 256, 0, c, stream);
-  return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, 32, 16>, q_rows * (D / 32), 512, 0, c,
+    return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, D, 8, 4>, q_rows, 256, 0, c, stream);
+  return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, 32, 32, 8>, q_rows * (D / 32), 1024, 0, c,
                                                   stream);
 }
 

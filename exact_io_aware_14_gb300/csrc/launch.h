@@ -124,6 +124,7 @@ struct DecodeFp8Params {
   float* lse;
   float* o_part;    // [B, Nq, Hq, n_split, d]
   float* lse_part;  // [B, Nq, Hq, n_split]
+  unsigned* counter;  // items claimed
   int max_blocks, page_size, num_pages;
   int B, Nq, Hq, Hkv, d, max_seqlen, chunk, n_split;
   float scale_log2;

@@ -125,7 +125,10 @@ def test_decode_fp8_argument_checks(L, want, kw):
 
 
 def test_decode_fp8_workspace_and_chunk(L):
-    need = L.attn_splitkv_workspace_size(2, 3 * 8, 8 * 256, 128, 512)
+    need = L.attn_splitkv_fp8_workspace_size(2, 3, 8, 8 * 256, 128, 512)
+    assert need == L.attn_splitkv_workspace_size(2, 3 * 8, 8 * 256, 128, 512) + 16
+    assert L.attn_splitkv_fp8_workspace_size(2, 0, 8, 2048, 128, 512) == 0
+    assert L.attn_splitkv_fp8_workspace_size(2, 1, 8, 2048, 128, 100) == 0
     assert _dec(L, Nq=3, chunk=512, wsb=need - 1) == 7
     for B, Nq, Hq, Hkv, n in ((1, 1, 32, 8, 64), (1, 1, 32, 8, 1 << 20), (64, 7, 8, 1, 4096), (16, 1, 32, 8, 16384)):
         c = L.attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, n)
