@@ -92,8 +92,6 @@ def _open(path):
     L.attn_kvcache_append_paged_fp8.argtypes = append[:6] + [vp, vp] + append[6:]
     L.attn_splitkv_fp8_chunk.restype = i
     L.attn_splitkv_fp8_chunk.argtypes = [i, i, i, i, i]
-    L.attn_splitkv_fp8_workspace_size.restype = sz
-    L.attn_splitkv_fp8_workspace_size.argtypes = [i, i, i, i, i, i]
     L.attn_fwd_splitkv_paged_fp8.restype = i
     L.attn_fwd_splitkv_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, i, f, i, vp, sz,
                                              vp]
@@ -451,10 +449,6 @@ def attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, max_seqlen):
     return int(lib().attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, max_seqlen))
 
 
-def attn_splitkv_fp8_workspace_size(B, Nq, Hq, max_seqlen, d, chunk):
-    return int(lib().attn_splitkv_fp8_workspace_size(B, Nq, Hq, max_seqlen, d, chunk))
-
-
 def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens, scale, chunk=None,
                      workspace=None, stream=None):
     """Attention of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over a paged float8_e4m3fn cache with
@@ -478,7 +472,7 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqle
     o = torch.empty(q_shape, dtype=_BF16, device=dev)
     lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
     if workspace is None:
-        n = _fn("attn_splitkv_fp8_workspace_size")(B, Nq, Hq, cap, d, chunk)
+        n = _fn("attn_splitkv_workspace_size")(B, Nq * Hq, cap, d, chunk)
         workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
     else:
         n = workspace.numel() * workspace.element_size()

@@ -237,15 +237,21 @@ attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_stride, con
                 Hkv, d, stream);
 }
 
+// Keys per CTA of the kernel's grid, in rounds of equal splits of about 1024
+// keys (2048 where there are many rounds anyway).  Measured on GB300: a
+// serving batch (16 sequences of 1 to 16 K keys, 8 KV heads) 56.7 us with
+// splits of 384, 55.1 with 768 and 1024; two sequences of 256 K keys 195, 182
+// and 173 us with 512, 1024 and 2048; one of 701 keys 8.4 us with 128 and 9.9
+// with 1024 (one split).
 int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen) {
   if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_seqlen < 1) return 0;
-  return 1024;
-}
-
-size_t attn_splitkv_fp8_workspace_size(int B, int Nq, int Hq, int max_seqlen, int d, int chunk) {
-  if (Nq < 1 || Hq < 1 || static_cast<long long>(Nq) * Hq > kIntMax) return 0;
-  const size_t parts = attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk);
-  return parts ? parts + 16 : 0;
+  const long long rows = static_cast<long long>(Nq) * (Hq / Hkv);
+  const long long ctas = rows <= 4 ? 304 : 152;
+  const double keys = static_cast<double>(B) * Hkv * static_cast<double>((rows + 15) / 16) * max_seqlen / ctas;
+  const double most = keys > 8192 ? 2048 : 1024;
+  const double rounds = std::ceil(keys / most);
+  const double chunk = std::ceil(keys / (rounds < 1 ? 1 : rounds) / 128) * 128;
+  return static_cast<int>(chunk < 128 ? 128 : (chunk > most ? most : chunk));
 }
 
 attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -261,8 +267,8 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   if (cap + Nq + 256 > kIntMax || Nq > 64 || B > 65535 || chunk > attn::kMaxChunkFp8 || (cap + chunk - 1) / chunk > 65535 ||
       static_cast<long long>(Nq) * Hq > 65535)
     return ATTN_ERR_UNSUPPORTED;
-  // rows, and items (at most one a row and split) with a margin for claims past the last, in 32 bits
-  if (static_cast<long long>(B) * Nq * Hq * ((cap + chunk - 1) / chunk) > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  // rows, and items (at most one a row and split) with a margin for the numbers past the last, in 31 bits
+  if (static_cast<long long>(B) * Nq * Hq * ((cap + chunk - 1) / chunk) > kIntMax - 4096) return ATTN_ERR_UNSUPPORTED;
   if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !block_table || !seqlens || !o || !lse)
     return ATTN_ERR_INVALID_ARG;
   if (off16(q) || off16(k_pages) || off16(v_pages) || off16(o) || off4(k_scales) || off4(v_scales) ||
@@ -270,7 +276,7 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
     return ATTN_ERR_MISALIGNED;
   const int max_seqlen = static_cast<int>(cap);
   if (!workspace || off16(workspace) ||
-      workspace_bytes < attn_splitkv_fp8_workspace_size(B, Nq, Hq, max_seqlen, d, chunk))
+      workspace_bytes < attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk))
     return ATTN_ERR_WORKSPACE;
   attn::DecodeFp8Params p;
   std::memset(&p, 0, sizeof p);
@@ -300,8 +306,6 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   const size_t parts = static_cast<size_t>(B) * Nq * Hq * p.n_split;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = p.o_part + parts * d;
-  p.counter = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) +
-                                          attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
   return attn::launch_decode_fp8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }

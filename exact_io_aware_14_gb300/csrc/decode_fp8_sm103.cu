@@ -24,7 +24,11 @@
 // one KV head's group times new tokens).  A fixed grid of CTAs takes them in
 // turn, full splits first, and keeps its pipeline running from one item to
 // the next: with a CTA for each item, its start (lengths, pages, first loads)
-// and end cost about 8 us each time, the time of 24 tiles of one SM.
+// and end cost about 8 us each time, the time of 24 tiles of one SM.  Which
+// items a CTA takes is fixed (SMs end up to 15% apart; claiming items from a
+// counter evened that out, but clearing the counter took a launch, and the
+// two cancelled: 55.1 and 56.9 us on a serving batch, 182 and 181 us on two
+// sequences of 256 K keys).
 // Eleven warps a CTA:
 //   warps 0-3  softmax, a thread a key (TMEM lane): scales, running
 //              reference, weights, their three terms as bytes into shared
@@ -40,6 +44,8 @@
 // Two tiles of S, P and O are in flight.
 //
 // Combine kernel: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -74,7 +80,7 @@ struct Cfg {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = kTile * D;
   static constexpr int kStages = (kCtas == 2 ? 3 : (R == 16 ? 5 : 6)) * 128 / D;
-  static constexpr int kItems = 3;  // items prepared or in work
+  static constexpr int kItems = 4;  // items prepared or in work
   static constexpr int kMaxBlocks = kMaxChunkFp8 / 64;
   static constexpr int kOffV = 0;  // V first: the M-major reads of a 64-dim V tile run into K's (see below)
   static constexpr int kOffK = kTileBytes;
@@ -203,8 +209,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.Hq / p.Hkv;
-  const int rows = p.Nq * G;  // query rows of a KV head: row r is token r / G, head r % G of the group
+  const int rows = p.rows;  // query rows of a KV head: row r is token r / G, head r % G of the group of G heads
 
   Item<R>* items = reinterpret_cast<Item<R>*>(smem + C::kOffItem);
   static_assert(sizeof(Item<R>) == (8 + 3 * C::kMaxBlocks + 4 * R) * 4, "item size");
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     // launched as a programmatic dependent of whatever ran before: nothing of
     // that is read before this wait
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n_rblk = (rows + R - 1) / R, H = p.Hkv * n_rblk;
+    const int n_rblk = static_cast<int>(p.n_rblk.d), H = static_cast<int>(p.H.d), G = static_cast<int>(p.G.d);
     bool full_phase = true;
     int b0 = -32;
     long long before = 0;  // pairs before the lanes' sequences
@@ -566,18 +571,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       total = __shfl_sync(0xffffffffu, incl, 31);
       return true;
     };
-    // The first item is the CTA's own number; further ones are claimed from a
-    // counter where there is one (SMs do not get equal shares of the memory's
-    // rate: with equal shares of the work the slowest ended 15 to 20% after
-    // the mean), else every gridDim-th follows.  A claim is asked for an item
-    // before it is used.
-    unsigned claimed = blockIdx.x;
-    auto claim = [&]() {
-      if (p.counter == nullptr)
-        claimed += gridDim.x;  // fits: the host sees to it
-      else if (lane == 0)
-        claimed = gridDim.x + atomicAdd(p.counter, 1u);
-    };
     // 32 / R lanes share a row of q, each a run of kDims of it.
     constexpr int kPg = C::kMaxBlocks / 32, kLanes = 32 / R, kDims = D / kLanes;
     const int qr = lane / kLanes, qd = lane % kLanes * kDims;
@@ -595,11 +588,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       uint4 q[kDims / 8];
     };
     bool more = next_block();
+    unsigned item = blockIdx.x;
     auto find = [&]() {
       Found f;
-      const unsigned i = __shfl_sync(0xffffffffu, claimed, 0);
-      claim();
-      const unsigned j = i / static_cast<unsigned>(H), h = i - j * H;
+      const unsigned j = p.H.div(item), h = item - j * H;
+      item += gridDim.x;  // fits: the host sees to it
       while (more && j >= before + total) {
         more = next_block();
         if (!more && full_phase) {
@@ -611,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       f.more = more;
       f.b = f.split = f.len = 0;
-      f.hkv = h / n_rblk;
+      f.hkv = p.n_rblk.div(h);
       f.row0 = (h - f.hkv * n_rblk) * R;
 #pragma unroll
       for (int k = 0; k < kPg; ++k) f.pg[k] = 0;
@@ -621,13 +614,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const int src = __ffs(who) - 1;
         f.b = b0 + src;
         f.len = __shfl_sync(0xffffffffu, Lb, src);
-        f.split = full_phase ? rel - __shfl_sync(0xffffffffu, excl, src) : f.len / p.chunk;
+        f.split = full_phase ? rel - __shfl_sync(0xffffffffu, excl, src) : p.split.div(f.len);
         const int k0 = f.split * p.chunk, n_blk = (min(p.chunk, f.len - k0) + 63) / 64;
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
           const int blk = 32 * k + lane;
           if (blk < n_blk)
-            f.pg[k] = p.block_table[static_cast<long long>(f.b) * p.max_blocks + (k0 + 64 * blk) / p.page_size];
+            f.pg[k] = p.block_table[static_cast<long long>(f.b) * p.max_blocks + p.page.div(k0 + 64 * blk)];
         }
       }
       return f;
@@ -657,7 +650,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             a.vs[k] = p.v_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
           }
         }
-        const int row = f.row0 + qr, tok = row / G, hq = f.hkv * G + row - tok * G;
+        const int row = f.row0 + qr, tok = p.G.div(row), hq = f.hkv * G + row - tok * G;
         a.lim = f.len - p.Nq + 1 + tok;
         a.o_row = row < rows ? (f.b * p.Nq + tok) * p.Hq + hq : -1;
         a.lse_row = (f.b * p.Hq + hq) * p.Nq + tok;
@@ -676,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         it.kn = a.kn;
         it.split = f.split;
         it.hkv = f.hkv;
-        it.lim_min = min(a.kn, f.len - p.Nq + 1 + f.row0 / G - a.k0);
+        it.lim_min = min(a.kn, f.len - p.Nq + 1 + static_cast<int>(p.G.div(f.row0)) - a.k0);
         it.direct = f.len <= p.chunk;
       }
       if (f.more) {
@@ -888,7 +881,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           const int nb = min(2, n_blk - 2 * t);
           mbar_arrive_expect_tx(bar_full + s, 2 * nb * 64 * D);
           for (int i = 0; i < nb; ++i) {
-            const int blk = 2 * t + i, row = (k0 + 64 * blk) % p.page_size, page = it.page[blk];
+            const int blk = 2 * t + i, key = k0 + 64 * blk, page = it.page[blk];
+            const int row = key - static_cast<int>(p.page.div(key)) * p.page_size;
             tma_load_4d(smem + s * C::kStage + C::kOffK + i * 64 * D, &p.tm_k, bar_full + s, 0, hkv, row, page);
             tma_load_4d(smem + s * C::kStage + C::kOffV + i * 64 * D, &p.tm_v, bar_full + s, 0, hkv, row, page);
           }
@@ -915,10 +909,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 // LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s for each row of q.
 // A block of kWarps warps takes kCols columns of a row, a warp every
 // kWarps-th split, kBatch splits' loads in flight; the warps' sums are added
-// in a fixed order.  Few splits: eight warps and the whole row.  Many (a few
-// long sequences, so few rows too): 32 warps for each 32 columns, as one
-// block's loads are then what the step waits for (64 rows of 512 splits: 39 us
-// in whole rows by eight warps).
+// in a fixed order.  Many rows, or few splits: eight warps and the whole row.
+// Few rows of many splits (a few long sequences): 32 warps for each 32
+// columns, as one block's loads are then what the step waits for (64 rows of
+// 512 splits: 39 us in whole rows by eight warps, 5 us so; 512 rows of 32
+// splits: 3 us and 30 us).
 template <int D, int kCols, int kWarps, int kBatch>
 __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const DecodeFp8CombineParams p) {
   constexpr int kV = kCols / 32, kBlocks = D / kCols;
@@ -1019,39 +1014,36 @@ cudaError_t launch_dependent(void (*kern)(const P), unsigned grid, unsigned bloc
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Clears the counter that items are claimed from: the workspace comes with any contents.
-struct CounterParams {
-  unsigned* counter;
-};
-__global__ void __launch_bounds__(32) decode_fp8_counter_kernel(const CounterParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // a call before this one may use the same workspace
-  if (threadIdx.x == 0) *p.counter = 0u;
-}
-
 template <int D, int R>
-cudaError_t launch_rows(DecodeFp8Params p, int sms, cudaStream_t stream) {
+cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream) {
   using C = Cfg<D, R>;
   auto kern = decode_fp8_split_kernel<D, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
-  if (e != cudaSuccess) return e;
+  // asked for once a device (bit dev of `set`; past 63 every time)
+  static std::atomic<unsigned long long> set{0};
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  cudaError_t e = cudaSuccess;
+  if (!(set.load(std::memory_order_acquire) & bit) || bit == 0ull) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_release);
+  }
   const int rows = p.Nq * (p.Hq / p.Hkv);
   // the most items there can be: the lengths are known on the device alone
   const long long items = static_cast<long long>(p.Hkv) * ((rows + R - 1) / R) * p.B * p.n_split;
   const long long ctas = static_cast<long long>(sms) * C::kCtas;
-  if (items <= ctas) {
-    p.counter = nullptr;
-  } else {
-    e = launch_dependent<CounterParams>(decode_fp8_counter_kernel, 1, 32, 0, {p.counter}, stream);
-    if (e != cudaSuccess) return e;
-  }
+  p.rows = rows;
+  p.n_rblk = FastDiv((rows + R - 1) / R);
+  p.H = FastDiv(p.Hkv * ((rows + R - 1) / R));
+  p.G = FastDiv(p.Hq / p.Hkv);
+  p.page = FastDiv(p.page_size);
+  p.split = FastDiv(p.chunk);
   e = launch_dependent<DecodeFp8Params>(kern, static_cast<unsigned>(items < ctas ? items : ctas), C::kThreads, C::kAlloc,
                                         p, stream);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const DecodeFp8CombineParams c = {p.o_part, p.lse_part, p.seqlens, p.o, p.lse, p.Nq, p.Hq, p.max_seqlen, p.chunk,
                                     p.n_split};
   const unsigned q_rows = static_cast<unsigned>(p.B) * p.Nq * p.Hq;
-  if (p.n_split <= 32 || q_rows > 0x7fffffffu / (D / 32))
+  if (q_rows >= 2u * sms || p.n_split <= 32)
     return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, D, 8, 4>, q_rows, 256, 0, c, stream);
   return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, 32, 32, 8>, q_rows * (D / 32), 1024, 0, c,
                                                   stream);
@@ -1064,9 +1056,9 @@ cudaError_t launch_d(const DecodeFp8Params& p, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int rows = p.Nq * (p.Hq / p.Hkv);
-  if (rows <= 4) return launch_rows<D, 4>(p, sms, stream);
-  if (rows <= 8) return launch_rows<D, 8>(p, sms, stream);
-  return launch_rows<D, 16>(p, sms, stream);
+  if (rows <= 4) return launch_rows<D, 4>(p, dev, sms, stream);
+  if (rows <= 8) return launch_rows<D, 8>(p, dev, sms, stream);
+  return launch_rows<D, 16>(p, dev, sms, stream);
 }
 
 }  // namespace

@@ -101,8 +101,24 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 
+// Division of n < 2^31 by a fixed d in [1, 2^31): with 2^s >= d, m = floor(2^32
+// (2^s - d) / d) + 1, n / d = (hi(n m) + n) >> s
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __host__ __device__ uint32_t div(uint32_t n) const {
+    return (static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> 32) + n) >> s;
+  }
+};
+
 // Split-KV decode over a paged e4m3 cache.
-constexpr int kMaxChunkFp8 = 4096;  // keys per split at most
+constexpr int kMaxChunkFp8 = 2048;  // keys per split at most
 struct DecodeFp8CombineParams {
   const float* o_part;
   const float* lse_part;
@@ -124,10 +140,13 @@ struct DecodeFp8Params {
   float* lse;
   float* o_part;    // [B, Nq, Hq, n_split, d]
   float* lse_part;  // [B, Nq, Hq, n_split]
-  unsigned* counter;  // items claimed
   int max_blocks, page_size, num_pages;
   int B, Nq, Hq, Hkv, d, max_seqlen, chunk, n_split;
   float scale_log2;
+  // set at launch: query rows of a KV head, its blocks of rows, those of all
+  // KV heads, heads of a group, page size, split length
+  int rows;
+  FastDiv n_rblk, H, G, page, split;
 };
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream);
 

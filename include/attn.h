@@ -356,13 +356,6 @@ ATTN_API attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_st
 ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen);
 
 /*
- * Bytes of workspace attn_fwd_splitkv_paged_fp8 needs: the partial results of
- * attn_splitkv_workspace_size for Nq * Hq rows, and a counter.  Returns 0 for
- * invalid arguments.
- */
-ATTN_API size_t attn_splitkv_fp8_workspace_size(int B, int Nq, int Hq, int max_seqlen, int d, int chunk);
-
-/*
  * Split-KV decode over a paged cache held in 8 bits (as written by
  * attn_kvcache_append_paged_fp8): key j of sequence b is code * scale with
  * the scale of its page and head, likewise its value.  The last Nq tokens of
@@ -376,11 +369,11 @@ ATTN_API size_t attn_splitkv_fp8_workspace_size(int B, int Nq, int Hq, int max_s
  *   seqlens: device int32 [B], each in [0, max_blocks * page_size], the new
  *            tokens counted; codes behind a sequence's end reach no result,
  *            whatever they hold;
- *   chunk: keys per split, a multiple of 64 in [64, 4096]
+ *   chunk: keys per split, a multiple of 64 in [64, 2048]
  *            (attn_splitkv_fp8_chunk);
- *   workspace: attn_splitkv_fp8_workspace_size(B, Nq, Hq, max_blocks *
- *            page_size, d, chunk) bytes, 16-byte aligned, contents ignored.
- * B * Nq * Hq times the splits of a sequence must stay below 2^31.
+ *   workspace: attn_splitkv_workspace_size(B, Nq * Hq, max_blocks * page_size,
+ *            d, chunk) bytes, 16-byte aligned, contents ignored.
+ * B * Nq * Hq times the splits of a sequence must stay below 2^31 - 4096.
  * Bad lengths and pages are handled as in attn_fwd_splitkv_paged.
  */
 ATTN_API attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages,

@@ -115,7 +115,7 @@ def _dec(L, **kw):
 
 @pytest.mark.parametrize("want,kw", [
     (1, dict(B=0)), (1, dict(Nq=0)), (2, dict(Nq=65)), (1, dict(Hq=7)), (1, dict(mb=0)), (1, dict(npg=0)),
-    (1, dict(ps=32)), (1, dict(ps=100)), (1, dict(chunk=0)), (1, dict(chunk=100)), (1, dict(scale=math.inf)),
+    (1, dict(ps=32)), (1, dict(ps=100)), (1, dict(chunk=0)), (1, dict(chunk=100)), (2, dict(chunk=2112)), (1, dict(scale=math.inf)),
     (2, dict(d=256)), (2, dict(mb=1 << 23)), (2, dict(B=65536)), (1, dict(q=0)), (1, dict(sk=0)), (1, dict(sv=0)),
     (1, dict(bt=0)), (1, dict(sl=0)), (1, dict(o=0)), (1, dict(lse=0)), (3, dict(q=24)), (3, dict(kp=24)),
     (3, dict(sk=18)), (3, dict(bt=18)), (3, dict(lse=18)), (7, dict(ws=0)), (7, dict(ws=24)), (7, dict(wsb=1024)),
@@ -125,15 +125,12 @@ def test_decode_fp8_argument_checks(L, want, kw):
 
 
 def test_decode_fp8_workspace_and_chunk(L):
-    need = L.attn_splitkv_fp8_workspace_size(2, 3, 8, 8 * 256, 128, 512)
-    assert need == L.attn_splitkv_workspace_size(2, 3 * 8, 8 * 256, 128, 512) + 16
-    assert L.attn_splitkv_fp8_workspace_size(2, 0, 8, 2048, 128, 512) == 0
-    assert L.attn_splitkv_fp8_workspace_size(2, 1, 8, 2048, 128, 100) == 0
+    need = L.attn_splitkv_workspace_size(2, 3 * 8, 8 * 256, 128, 512)
     assert _dec(L, Nq=3, chunk=512, wsb=need - 1) == 7
-    for B, Nq, Hq, Hkv, n in ((1, 1, 32, 8, 64), (1, 1, 32, 8, 1 << 20), (64, 7, 8, 1, 4096), (16, 1, 32, 8, 16384)):
+    for B, Nq, Hq, Hkv, n in ((1, 1, 32, 8, 64), (1, 1, 32, 8, 1 << 20), (64, 7, 8, 1, 4096), (16, 1, 32, 8, 16384),
+                             (65535, 64, 128, 1, 2 ** 31 - 1), (1, 1, 1, 1, 1)):
         c = L.attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, n)
-        assert c >= 64 and c % 64 == 0
-        assert -(-n // c) <= 65535
+        assert 64 <= c <= 2048 and c % 64 == 0
     assert L.attn_splitkv_fp8_chunk(0, 1, 8, 8, 64) == 0
     assert L.attn_splitkv_fp8_chunk(1, 1, 8, 3, 64) == 0
 
