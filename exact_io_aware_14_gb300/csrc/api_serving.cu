@@ -45,8 +45,8 @@ attn_status check_qk_sizes(int B, int N, int Hq, int Hkv, int d) {
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   const long long tokens = static_cast<long long>(B) * N;
   if (tokens > kIntMax || static_cast<long long>(Hq) + Hkv > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
-  // grid: one block per 256 threads, d/16 threads a row at most
-  if (tokens * (static_cast<long long>(Hq) + Hkv) > kIntMax * 16) return ATTN_ERR_UNSUPPORTED;
+  // rows are counted in 31 bits, with room for the numbers past the last
+  if (tokens * (static_cast<long long>(Hq) + Hkv) > kIntMax - (1 << 20)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

@@ -55,6 +55,22 @@ attn_status check_splitkv_args(const void* q, const void* k, const void* v, cons
 // of bytes, swizzle as wide as a head row (64 or 128 bytes).  False on failure.
 bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d, int box_rows);
 
+// Division of n < 2^31 by a fixed d in [1, 2^31): with 2^s >= d, m = floor(2^32
+// (2^s - d) / d) + 1, n / d = (hi(n m) + n) >> s
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __host__ __device__ uint32_t div(uint32_t n) const {
+    return (static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> 32) + n) >> s;
+  }
+};
+
 // Norms and rotation of queries and keys.  Token rows of q and k are q_stride
 // and k_stride elements apart; outputs and gradients are dense.
 struct QkNormRopeParams {
@@ -100,22 +116,6 @@ struct AppendParams {
   int B, Nn, Hkv, d;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
-
-// Division of n < 2^31 by a fixed d in [1, 2^31): with 2^s >= d, m = floor(2^32
-// (2^s - d) / d) + 1, n / d = (hi(n m) + n) >> s
-// (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994).
-struct FastDiv {
-  uint32_t d, m, s;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t divisor) : d(divisor), s(0) {
-    while ((1ull << s) < d) ++s;
-    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-  __host__ __device__ uint32_t div(uint32_t n) const {
-    return (static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> 32) + n) >> s;
-  }
-};
 
 // Split-KV decode over a paged e4m3 cache.
 constexpr int kMaxChunkFp8 = 2048;  // keys per split at most

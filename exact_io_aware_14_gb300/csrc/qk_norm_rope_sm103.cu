@@ -7,11 +7,22 @@
 // Without a weight there is no norm: y = R(x), dx = R^T dy.
 //
 // Both are bound by memory (about 4 flops a byte), so each value is read and
-// written once, 16 bytes a thread and access: D/16 threads hold a row, two
-// chunks each (rope.cuh), the mean square is a shuffle reduction over them,
-// and the rotation needs no exchange.  A group of threads takes kHeads heads
-// of one token, whose loads are all issued before the first is used and
-// which share the token's cosines and sines.
+// written once: D/16 threads hold a row, two 16-byte chunks each (rope.cuh),
+// the mean square is a shuffle reduction over them, and the rotation needs no
+// exchange.
+//
+// Two forms, chosen by size (launch rules below):
+//   short   (forward) a group of threads takes one row of one token: the
+//           least latency
+//   long    a fixed grid of CTAs walks q's items and k's (kHeads heads of one
+//           token, which share its cosines and sines).  As soon as a head's
+//           values are unpacked, its registers take the same head of the
+//           group's next item, so loads stay in flight while the arithmetic
+//           runs
+// Tiles brought into shared memory by bulk copies were slower (105 us on the
+// training forward against 61.5 for plain loads into registers without the
+// overlap): a row's angles are then read again for each head, and the
+// instructions, twice as many, became the limit.
 //
 // The backward pass needs x again to recompute r, so the forward pass saves
 // nothing.  dw: every thread keeps its 16 columns' sums in 32 bits over the
@@ -122,185 +133,274 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRope
   }
 }
 
-// Backward.  Blocks [0, nbq) walk q's items, the rest k's, each a fixed set,
-// so a block's dw row belongs to one of the two weights.
-template <int D, int kHeads, bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const QkNormRopeParams p, int nbq, int nbk) {
+// ---------------------------------------------------------------------------
+// The long form.
+
+// How one of the two tensors is shared out.
+struct RowPlan {
+  int H, blocks;
+  FastDiv per;  // items of a token
+};
+struct LongPlan {
+  RowPlan q, k;
+  FastDiv by_N;
+};
+
+template <int D, int kHeads, int kMinBlocks, bool kInter, bool kBwd>
+__global__ void __launch_bounds__(kThreads, kMinBlocks)
+    qk_norm_rope_long_kernel(const QkNormRopeParams p, const LongPlan plan) {
   constexpr int kTPR = D / 16;
   constexpr int kGroups = kThreads / kTPR;
-  const bool is_k = static_cast<int>(blockIdx.x) >= nbq;
-  const int nb = is_k ? nbk : nbq, blk = is_k ? blockIdx.x - nbq : blockIdx.x;
-  const int H = is_k ? p.Hkv : p.Hq, per = (H + kHeads - 1) / kHeads;
-  const long long n_items = static_cast<long long>(p.B) * p.N * per;
-  const __nv_bfloat16* x0 = static_cast<const __nv_bfloat16*>(is_k ? p.k : p.q);
+  const bool is_k = static_cast<int>(blockIdx.x) >= plan.q.blocks;
+  const int H = is_k ? plan.k.H : plan.q.H;
+  FastDiv per;
+  per.d = is_k ? plan.k.per.d : plan.q.per.d;
+  per.m = is_k ? plan.k.per.m : plan.q.per.m;
+  per.s = is_k ? plan.k.per.s : plan.q.per.s;
+  const unsigned step = (is_k ? plan.k.blocks : plan.q.blocks) * kGroups;
+  const unsigned n_items = static_cast<unsigned>(p.B) * p.N * per.d;  // fits: checked on the host
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(is_k ? p.k : p.q);
   const long long stride = is_k ? p.k_stride : p.q_stride;
-  const __nv_bfloat16* dy0 = static_cast<const __nv_bfloat16*>(is_k ? p.dk_out : p.dq_out);
-  __nv_bfloat16* dx0 = static_cast<__nv_bfloat16*>(is_k ? p.dk : p.dq);
+  const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(is_k ? p.dk_out : p.dq_out);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(kBwd ? (is_k ? p.dk : p.dq) : (is_k ? p.k_out : p.q_out));
   const float* w = is_k ? p.k_weight : p.q_weight;
+  const bool need_x = !kBwd || w != nullptr;
   const int l = threadIdx.x % kTPR;
   const int2 ch = row_chunks(l, p.rope.rot);
-  float wv[16], dw[16];
+  const bool turn = l < (p.rope.rot >> 4);  // this thread's chunks are rotated
+  float wv[16], dw[kBwd ? 16 : 1];
+  if (kBwd) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) dw[j] = 0.f;
+    for (int j = 0; j < 16; ++j) dw[kBwd ? j : 0] = 0.f;
+  }
   if (w) {
     load4(w + 8 * ch.x, wv);
     load4(w + 8 * ch.x + 4, wv + 4);
     load4(w + 8 * ch.y, wv + 8);
     load4(w + 8 * ch.y + 4, wv + 12);
   }
+
+  // an item's place; nh 0 past the last
+  struct Place {
+    unsigned token;
+    int h0, nh;
+  };
+  auto place = [&](unsigned i) {
+    Place a;
+    a.token = per.div(i);
+    a.h0 = static_cast<int>(i - a.token * per.d) * kHeads;
+    a.nh = i < n_items ? min(kHeads, H - a.h0) : 0;
+    return a;
+  };
+  uint4 rx[kHeads][2], rd[kBwd ? kHeads : 1][2];
+  auto load_head = [&](const Place& a, int h) {
+    rx[h][0] = rx[h][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (kBwd) rd[kBwd ? h : 0][0] = rd[kBwd ? h : 0][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < a.nh) {
+      if (need_x) {
+        const __nv_bfloat16* r = x + a.token * stride + static_cast<long long>(a.h0 + h) * D;
+        rx[h][0] = *reinterpret_cast<const uint4*>(r + 8 * ch.x);
+        rx[h][1] = *reinterpret_cast<const uint4*>(r + 8 * ch.y);
+      }
+      if (kBwd) {
+        const __nv_bfloat16* r = dy + (static_cast<long long>(a.token) * H + a.h0 + h) * D;
+        rd[kBwd ? h : 0][0] = *reinterpret_cast<const uint4*>(r + 8 * ch.x);
+        rd[kBwd ? h : 0][1] = *reinterpret_cast<const uint4*>(r + 8 * ch.y);
+      }
+    }
+  };
+  auto position = [&](const Place& a) {
+    if (p.rope.rot == 0 || a.nh == 0) return 0;
+    return p.positions ? __ldg(p.positions + a.token)
+                       : static_cast<int>(a.token - plan.by_N.div(a.token) * plan.by_N.d);
+  };
+  auto angles = [&](const Place& a, int pos, Angles& ang) {
+    if (turn && a.nh > 0) load_angles(p.rope, checked_pos(pos, p.rope.max_pos), l, ang);
+  };
+
   // every group of a warp makes the same number of rounds: the row sums are warp-wide shuffles
-  const long long step = static_cast<long long>(nb) * kGroups;
-  for (long long base = static_cast<long long>(blk) * kGroups; base < n_items; base += step) {
-    const long long i = base + threadIdx.x / kTPR;
-    const long long token = i / per;
-    const int h0 = static_cast<int>(i - token * per) * kHeads;
-    const int nh = i < n_items ? min(kHeads, H - h0) : 0;
-    const __nv_bfloat16* x = x0 + token * stride + static_cast<long long>(h0) * D;
-    const long long dense = (token * H + h0) * D;
-    uint4 rx[kHeads][2], rd[kHeads][2];
+  const unsigned first = (is_k ? blockIdx.x - plan.q.blocks : blockIdx.x) * kGroups;
+  const unsigned grp = threadIdx.x / kTPR;
+  Place cur = place(first + grp);
+  Angles ang;
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) load_head(cur, h);
+  angles(cur, position(cur), ang);
+  Place nxt = place(first + step + grp);
+  int pos_nxt = position(nxt);
+  for (unsigned base = first; base < n_items; base += step) {
+    const Place after = place(base + 2 * step + grp);
+    const int pos_after = position(after);
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) {
-      rx[h][0] = rx[h][1] = rd[h][0] = rd[h][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < nh) {
-        rd[h][0] = *reinterpret_cast<const uint4*>(dy0 + dense + h * D + 8 * ch.x);
-        rd[h][1] = *reinterpret_cast<const uint4*>(dy0 + dense + h * D + 8 * ch.y);
-        if (w) {
-          rx[h][0] = *reinterpret_cast<const uint4*>(x + h * D + 8 * ch.x);
-          rx[h][1] = *reinterpret_cast<const uint4*>(x + h * D + 8 * ch.y);
-        }
-      }
-    }
-    Angles ang;
-    const bool turn = p.rope.rot > 0 && nh > 0;
-    if (turn) {
-      const int pos = p.positions ? p.positions[token] : static_cast<int>(token % p.N);
-      load_angles(p.rope, checked_pos(pos, p.rope.max_pos), l, ang);
-    }
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      float u[16], v[16];
-      unpack8(rd[h][0], u);
-      unpack8(rd[h][1], u + 8);
-      if (turn && l < (p.rope.rot >> 4)) rotate16<kInter, true>(u, ang);
-      if (w) {  // uniform over the block
+      float y[16], v[kBwd ? 16 : 1];
+      if (!kBwd) {
+        unpack8(rx[h][0], y);
+        unpack8(rx[h][1], y + 8);
+      } else {
+        unpack8(rd[kBwd ? h : 0][0], y);
+        unpack8(rd[kBwd ? h : 0][1], y + 8);
         unpack8(rx[h][0], v);
-        unpack8(rx[h][1], v + 8);
-        float ss = 0.f, gx = 0.f;
+        unpack8(rx[h][1], v + (kBwd ? 8 : 0));
+      }
+      load_head(nxt, h);
+      if (!kBwd) {
+        if (w) {
+          float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          ss = fmaf(v[j], v[j], ss);
-          gx = fmaf(u[j] * wv[j], v[j], gx);
+          for (int j = 0; j < 16; ++j) ss = fmaf(y[j], y[j], ss);
+          ss = row_sum<kTPR>(ss);
+          const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = y[j] * rs * wv[j];
         }
-        ss = row_sum<kTPR>(ss);
-        gx = row_sum<kTPR>(gx);
-        const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-        const float m = gx * r * (1.f / D);  // mean(g * xr)
+        if (turn) rotate16<kInter, false>(y, ang);
+        if (h == kHeads - 1) angles(nxt, pos_nxt, ang);
+      } else {
+        if (turn) rotate16<kInter, true>(y, ang);
+        if (h == kHeads - 1) angles(nxt, pos_nxt, ang);
+        if (w) {
+          float ss = 0.f, gx = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float xr = v[j] * r;
-          dw[j] = fmaf(u[j], xr, dw[j]);
-          u[j] = r * fmaf(-xr, m, u[j] * wv[j]);
+          for (int j = 0; j < 16; ++j) {
+            const float vj = v[kBwd ? j : 0];
+            ss = fmaf(vj, vj, ss);
+            gx = fmaf(y[j] * wv[j], vj, gx);
+          }
+          ss = row_sum<kTPR>(ss);
+          gx = row_sum<kTPR>(gx);
+          const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+          const float m = gx * rs * (1.f / D);  // mean(g * xr)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float xr = v[kBwd ? j : 0] * rs;
+            if (h < cur.nh) dw[kBwd ? j : 0] = fmaf(y[j], xr, dw[kBwd ? j : 0]);
+            y[j] = rs * fmaf(-xr, m, y[j] * wv[j]);
+          }
         }
       }
-      if (h < nh) {
-        *reinterpret_cast<uint4*>(dx0 + dense + h * D + 8 * ch.x) = pack8(u);
-        *reinterpret_cast<uint4*>(dx0 + dense + h * D + 8 * ch.y) = pack8(u + 8);
+      if (h < cur.nh) {
+        __nv_bfloat16* o = out + (static_cast<long long>(cur.token) * H + cur.h0 + h) * D;
+        *reinterpret_cast<uint4*>(o + 8 * ch.x) = pack8(y);
+        *reinterpret_cast<uint4*>(o + 8 * ch.y) = pack8(y + 8);
       }
     }
+    cur = nxt;
+    nxt = after;
+    pos_nxt = pos_after;
   }
-  if (!w) return;
-  __shared__ float s_dw[kThreads / 32][D];
+  if (!kBwd || !w) return;
+  __shared__ float s_dw[kBwd ? kThreads / 32 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
+    float v = dw[kBwd ? j : 0];
 #pragma unroll
-    for (int o = kTPR; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
-    if (lane < kTPR) s_dw[warp][8 * (j < 8 ? ch.x : ch.y) + (j & 7)] = dw[j];
+    for (int o = kTPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane < kTPR) s_dw[kBwd ? warp : 0][8 * (j < 8 ? ch.x : ch.y) + (j & 7)] = v;
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < D; c += kThreads) {
-    float s = 0.f;
+  if (threadIdx.x < D) {
+    float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) s += s_dw[k][c];
-    p.dw_part[static_cast<size_t>(blockIdx.x) * D + c] = s;
+    for (int k = 0; k < kThreads / 32; ++k) v += s_dw[kBwd ? k : 0][threadIdx.x];
+    p.dw_part[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = v;
   }
 }
 
-// Adds the blocks' dw rows: block 0 q's, block 1 k's; 1024/D threads a
-// column, then a fixed-order sum over them.
+// Adds the blocks' dw rows, 32 columns of one tensor a block: 32 warps take
+// every 32nd row (loads independent of one another), then their sums are
+// added in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const float* part, int nbq, int nbk, float* dwq,
                                                                float* dwk) {
-  constexpr int kPer = 1024 / D;
-  float* out = blockIdx.x == 0 ? dwq : dwk;
+  const bool is_k = blockIdx.x >= D / 32;
+  float* out = is_k ? dwk : dwq;
   if (!out) return;
-  __shared__ float s_sum[kPer][D];
-  const int c = threadIdx.x % D, g = threadIdx.x / D;
-  const int lo = blockIdx.x == 0 ? 0 : nbq, n = blockIdx.x == 0 ? nbq : nbk;
+  __shared__ float s_sum[32][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x % (D / 32) * 32 + lane;
+  const int lo = is_k ? nbq : 0, n = is_k ? nbk : nbq;
   float s = 0.f;
-  for (int i = g; i < n; i += kPer) s += part[static_cast<size_t>(lo + i) * D + c];
-  s_sum[g][c] = s;
+#pragma unroll 8
+  for (int i = warp; i < n; i += 32) s += part[static_cast<size_t>(lo + i) * D + c];
+  s_sum[warp][lane] = s;
   __syncthreads();
-  if (g == 0) {
+  if (warp == 0) {
 #pragma unroll
-    for (int k = 1; k < kPer; ++k) s += s_sum[k][c];
+    for (int k = 1; k < 32; ++k) s += s_sum[k][lane];
     out[c] = s;
   }
 }
 
-template <int D, int kHeads>
-cudaError_t launch_fwd(const QkNormRopeParams& p, cudaStream_t stream) {
-  const int gq = (p.Hq + kHeads - 1) / kHeads, gk = (p.Hkv + kHeads - 1) / kHeads;
-  const long long items = static_cast<long long>(p.B) * p.N * (gq + gk);
+// Short forward: one row a group of threads.
+template <int D>
+cudaError_t launch_short(const QkNormRopeParams& p, cudaStream_t stream) {
+  const long long items = static_cast<long long>(p.B) * p.N * (p.Hq + p.Hkv);
   const unsigned blocks = static_cast<unsigned>((items * (D / 16) + kThreads - 1) / kThreads);
   if (p.rope.inter)
-    qk_norm_rope_kernel<D, kHeads, true><<<blocks, kThreads, 0, stream>>>(p, items, gq, gk);
+    qk_norm_rope_kernel<D, 1, true><<<blocks, kThreads, 0, stream>>>(p, items, p.Hq, p.Hkv);
   else
-    qk_norm_rope_kernel<D, kHeads, false><<<blocks, kThreads, 0, stream>>>(p, items, gq, gk);
+    qk_norm_rope_kernel<D, 1, false><<<blocks, kThreads, 0, stream>>>(p, items, p.Hq, p.Hkv);
   return cudaGetLastError();
 }
 
-constexpr int kBwdHeads = 2;
+constexpr long long kLongElements = 1 << 21;  // rows times d from which the long forward is taken
+constexpr int kFwdHeads = 4, kFwdBlocks = 2;  // heads of an item, CTAs of an SM
+constexpr int kBwdHeads = 2, kBwdBlocks = 2;
 
-template <int D>
-cudaError_t launch_bwd(const QkNormRopeParams& p, int nbq, int nbk, cudaStream_t stream) {
-  if (p.rope.inter)
-    qk_norm_rope_bwd_kernel<D, kBwdHeads, true><<<nbq + nbk, kThreads, 0, stream>>>(p, nbq, nbk);
-  else
-    qk_norm_rope_bwd_kernel<D, kBwdHeads, false><<<nbq + nbk, kThreads, 0, stream>>>(p, nbq, nbk);
+// CTAs for q and for k by their share of the rows, no more than there is work for.
+LongPlan plan_long(int B, int N, int Hq, int Hkv, int d, bool bwd) {
+  LongPlan plan;
+  const int ctas = 152 * (bwd ? kBwdBlocks : kFwdBlocks), heads = bwd ? kBwdHeads : kFwdHeads;
+  const int groups = kThreads / (d / 16);
+  auto share = [&](int H, int cap) {
+    RowPlan r;
+    r.H = H;
+    const int per = H == 0 ? 1 : (H + heads - 1) / heads;
+    r.per = FastDiv(per);
+    const long long want = (static_cast<long long>(B) * N * per + groups - 1) / groups;
+    r.blocks = H == 0 ? 0 : static_cast<int>(want < 1 ? 1 : (want > cap ? cap : want));
+    return r;
+  };
+  int nq = static_cast<int>(static_cast<long long>(ctas) * Hq / (Hq + Hkv));
+  nq = nq < 1 ? 1 : (Hkv > 0 && nq > ctas - 1 ? ctas - 1 : nq);
+  plan.q = share(Hq, nq);
+  plan.k = share(Hkv, Hkv > 0 ? ctas - nq : 0);
+  plan.by_N = FastDiv(N < 1 ? 1 : N);
+  return plan;
+}
+
+template <int D, bool kInter, bool kBwd>
+cudaError_t launch_long(const QkNormRopeParams& p, cudaStream_t stream) {
+  const LongPlan plan = plan_long(p.B, p.N, p.Hq, p.Hkv, p.d, kBwd);
+  qk_norm_rope_long_kernel<D, kBwd ? kBwdHeads : kFwdHeads, kBwd ? kBwdBlocks : kFwdBlocks, kInter, kBwd>
+      <<<plan.q.blocks + plan.k.blocks, kThreads, 0, stream>>>(p, plan);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (!p.dq_weight && !p.dk_weight)) return e;
-  qk_norm_rope_dw_kernel<D><<<2, 1024, 0, stream>>>(p.dw_part, nbq, nbk, p.dq_weight, p.dk_weight);
+  if (!kBwd || e != cudaSuccess || (!p.dq_weight && !p.dk_weight)) return e;
+  qk_norm_rope_dw_kernel<D>
+      <<<2 * (D / 32), 1024, 0, stream>>>(p.dw_part, plan.q.blocks, plan.k.blocks, p.dq_weight, p.dk_weight);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 void qk_norm_rope_bwd_blocks(int B, int N, int Hq, int Hkv, int d, int* nbq, int* nbk) {
-  // blocks for about the rows there are, at most kMax in all, shared out by heads
-  constexpr int kMax = 152 * 6;
-  const long long groups = kThreads / (d / 16);
-  const long long tokens = static_cast<long long>(B) * N;
-  auto want = [&](int H, int cap) {
-    const long long n = (tokens * ((H + kBwdHeads - 1) / kBwdHeads) + groups - 1) / groups;
-    return static_cast<int>(n < 1 ? 1 : (n > cap ? cap : n));
-  };
-  int cap_q = static_cast<int>(static_cast<long long>(kMax) * Hq / (Hq + Hkv));
-  cap_q = cap_q < 1 ? 1 : (cap_q > kMax - 1 ? kMax - 1 : cap_q);
-  *nbq = want(Hq, cap_q);
-  *nbk = Hkv > 0 ? want(Hkv, kMax - cap_q) : 0;
+  const LongPlan plan = plan_long(B, N, Hq, Hkv, d, true);
+  *nbq = plan.q.blocks;
+  *nbk = plan.k.blocks;
 }
 
 cudaError_t launch_qk_norm_rope(const QkNormRopeParams& p, cudaStream_t stream) {
-  if (p.d == 64) return launch_fwd<64, 4>(p, stream);
-  return launch_fwd<128, 4>(p, stream);
+  const bool is_long = static_cast<long long>(p.B) * p.N * (p.Hq + p.Hkv) * p.d >= kLongElements;
+  if (!is_long) return p.d == 64 ? launch_short<64>(p, stream) : launch_short<128>(p, stream);
+  if (p.d == 64) return p.rope.inter ? launch_long<64, true, false>(p, stream) : launch_long<64, false, false>(p, stream);
+  return p.rope.inter ? launch_long<128, true, false>(p, stream) : launch_long<128, false, false>(p, stream);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkNormRopeParams& p, cudaStream_t stream) {
-  int nbq, nbk;
-  qk_norm_rope_bwd_blocks(p.B, p.N, p.Hq, p.Hkv, p.d, &nbq, &nbk);
-  if (p.d == 64) return launch_bwd<64>(p, nbq, nbk, stream);
-  return launch_bwd<128>(p, nbq, nbk, stream);
+  if (p.d == 64) return p.rope.inter ? launch_long<64, true, true>(p, stream) : launch_long<64, false, true>(p, stream);
+  return p.rope.inter ? launch_long<128, true, true>(p, stream) : launch_long<128, false, true>(p, stream);
 }
 
 cudaError_t fetch_status_rope(cudaStream_t stream, uint32_t* out) {
