@@ -14,6 +14,12 @@
 // smallest normal value.  A page that starts with this call (its row 0 is
 // new) takes its scale from the new rows alone; otherwise
 // max(its scale, the new rows' scale).
+// The scale has to be known before a code is written, so a block keeps its
+// rotated values in registers between the two: as bf16 rounded to odd (cut
+// off, the last bit set where anything was cut), from which rounding to
+// e4m3's four significant bits or fewer gives what rounding the fp32 value
+// gives (Boldo and Melquiond, "Emulation of a FMA and correctly rounded sums:
+// proved algorithms using rounding to odd", 2008: two spare bits are enough).
 //
 // Both are bound by memory: one read of the new rows, one write of the cache
 // rows; single tokens by latency.
@@ -129,33 +135,44 @@ __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const AppendParam
 // e4m3 cache.  One block per (touched page, KV head, K or V, sequence): it
 // alone writes that page's codes and scale of the head, so no two blocks meet.
 
-// Bits of |x|, 0 where x is not finite (such a value takes no part in the
-// scale and is stored as NaN).
-__device__ __forceinline__ uint32_t abs_bits(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
-// Exponent of the scale for largest magnitude amax (given by its bits):
-// amax <= 448.5 * 2^e, 448.5 = 0x1.c08p8.
-__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
-  const int e = static_cast<int>(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x604000u ? 1 : 0);
+// Exponent of the scale for largest magnitude amax (finite): amax <= 448.5 *
+// 2^e, 448.5 = 0x1.c08p8.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x604000u ? 1 : 0);
   return max(e, -100);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Two floats -> two e4m3 codes (nearest, ties to even), `lo` in the low byte.
-// Infinities become NaN: e4m3 has none, and saturating would hide them.
+// Two floats -> two e4m3 codes (nearest, ties to even), `lo` in the low byte;
+// NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  uint32_t u = r;
-  if (!(fabsf(lo) < INFINITY)) u = (u & 0xff00u) | 0x7fu;
-  if (!(fabsf(hi) < INFINITY)) u = (u & 0x00ffu) | 0x7f00u;
-  return u;
+  return r;
 }
-__device__ __forceinline__ uint2 e4m3x8(const float* x, float inv) {
-  return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
-                    e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
+// Two bf16 of a word rounded to odd from two floats.
+__device__ __forceinline__ uint32_t pack_odd(float lo, float hi) {
+  const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+  const uint32_t ao = a | (((a & 0xffffu) + 0xffffu) & 0x10000u), bo = b | (((b & 0xffffu) + 0xffffu) & 0x10000u);
+  return __byte_perm(ao, bo, 0x7632);
+}
+// Eight values (four words of bf16) times inv -> eight codes.
+__device__ __forceinline__ uint2 e4m3x8(const uint4& u, float inv) {
+  return make_uint2(e4m3x2(bf16lo(u.x) * inv, bf16hi(u.x) * inv) | (e4m3x2(bf16lo(u.y) * inv, bf16hi(u.y) * inv) << 16),
+                    e4m3x2(bf16lo(u.z) * inv, bf16hi(u.z) * inv) | (e4m3x2(bf16lo(u.w) * inv, bf16hi(u.w) * inv) << 16));
+}
+// The word with every infinity made NaN (e4m3 has none, and saturating would hide them).
+__device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
+  if ((w & 0x7fffu) == 0x7f80u) w |= 0x40u;
+  if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x400000u;
+  return w;
+}
+__device__ __forceinline__ float max_abs8(const uint4& u, float m) {
+  m = fmax3(m, fabsf(bf16lo(u.x)), fabsf(bf16hi(u.x)));
+  m = fmax3(m, fabsf(bf16lo(u.y)), fabsf(bf16hi(u.y)));
+  m = fmax3(m, fabsf(bf16lo(u.z)), fabsf(bf16hi(u.z)));
+  return fmax3(m, fabsf(bf16lo(u.w)), fabsf(bf16hi(u.w)));
 }
 // One e4m3 pair -> two floats (through f16, which holds every e4m3 value).
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t u) {
@@ -173,8 +190,10 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
 }
 
-template <int D, int kBlock, bool kInter>
-__global__ void __launch_bounds__(kBlock) append_e4m3_kernel(const AppendParams p) {
+// kKeep: rows a thread keeps at most (the page has no more than kBlock * 16 /
+// D * kKeep); 0: any number, read and rotated a second time for the codes.
+template <int D, int kBlock, int kKeep, bool kInter>
+__global__ void __launch_bounds__(kBlock, kKeep > 1 ? 2 : 1) append_e4m3_kernel(const AppendParams p) {
   constexpr int kTPR = D / 16;
   constexpr int kRows = kBlock / kTPR;  // rows a round of the block covers
   const int b = blockIdx.y;
@@ -195,7 +214,7 @@ __global__ void __launch_bounds__(kBlock) append_e4m3_kernel(const AppendParams 
   const RopeParams& rope = p.rope;
   const int l = threadIdx.x % kTPR, r0 = threadIdx.x / kTPR;
   const int2 ch = row_chunks(l, rope.rot);
-  const bool turn = !is_v && rope.rot > 0 && l < (rope.rot >> 4);
+  const bool turn = !is_v && l < (rope.rot >> 4);
   const long long stride = is_v ? p.v_stride : p.k_stride;
   // row r of the page is new row start + r - len of the sequence
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
@@ -206,32 +225,74 @@ __global__ void __launch_bounds__(kBlock) append_e4m3_kernel(const AppendParams 
   float* scale = (is_v ? p.v_scales : p.k_scales) + static_cast<long long>(pg) * p.Hkv + h;
   const float was = lo > 0 ? *scale : 0.f;
 
-  auto load_row = [&](int r, float* x) {
+  auto load_row = [&](int r, uint4 (&u)[2]) {
     const __nv_bfloat16* row = src + r * stride;
-    unpack8(*reinterpret_cast<const uint4*>(row + 8 * ch.x), x);
-    unpack8(*reinterpret_cast<const uint4*>(row + 8 * ch.y), x + 8);
+    u[0] = *reinterpret_cast<const uint4*>(row + 8 * ch.x);
+    u[1] = *reinterpret_cast<const uint4*>(row + 8 * ch.y);
+  };
+  // Row r as the codes are taken from it (rotated, rounded to odd), its largest
+  // magnitude into m: of the fp32 values, as rounding to odd can pass the
+  // scale's border.  NaN is left out, with finite_only infinities too (they
+  // become NaN).
+  auto take_row = [&](int r, uint4 (&u)[2], float& m, bool finite_only) {
     if (turn) {
       Angles ang;
       load_angles(rope, checked_pos(start + r, rope.max_pos), l, ang);
+      float x[16];
+      unpack8(u[0], x);
+      unpack8(u[1], x + 8);
       rotate16<kInter, false>(x, ang);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (finite_only && fabsf(x[i]) == INFINITY) x[i] = NAN;
+        if (i & 1) m = fmax3(m, fabsf(x[i - 1]), fabsf(x[i]));
+      }
+      u[0] = make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
+      u[1] = make_uint4(pack_odd(x[8], x[9]), pack_odd(x[10], x[11]), pack_odd(x[12], x[13]), pack_odd(x[14], x[15]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (finite_only)
+          u[c] = make_uint4(inf_to_nan(u[c].x), inf_to_nan(u[c].y), inf_to_nan(u[c].z), inf_to_nan(u[c].w));
+        m = max_abs8(u[c], m);
+      }
     }
   };
-
-  uint32_t amax = 0u;
-  for (int r = lo + r0; r < hi; r += kRows) {
-    float x[16];
-    load_row(r, x);
+  constexpr int kHeld = kKeep > 0 ? kKeep : 1;
+  uint4 held[kHeld][2];
+  auto largest = [&](bool finite_only) {
+    float m = 0.f;
+    if (kKeep > 0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, abs_bits(x[i]));
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  __shared__ uint32_t s_max[kBlock / 32];
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-  __syncthreads();  // also: every thread has read the old scale before it is written
+      for (int i = 0; i < kHeld; ++i) {
+        held[i][0] = held[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (lo + i * kRows + r0 < hi) load_row(lo + i * kRows + r0, held[i]);
+      }
 #pragma unroll
-  for (int w = 0; w < kBlock / 32; ++w) amax = max(amax, s_max[w]);
-  const int e = scale_exp(amax);
-  const float now = fmaxf(was, pow2(e));
+      for (int i = 0; i < kHeld; ++i)
+        if (lo + i * kRows + r0 < hi) take_row(lo + i * kRows + r0, held[i], m, finite_only);
+    } else {
+      for (int r = lo + r0; r < hi; r += kRows) {
+        uint4 u[2];
+        load_row(r, u);
+        take_row(r, u, m, finite_only);
+      }
+    }
+    return m;
+  };
+  __shared__ float s_max[2][kBlock / 32];
+  auto block_max = [&](float m, int k) {
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // m >= 0: ordered as integers
+    if ((threadIdx.x & 31) == 0) s_max[k][threadIdx.x >> 5] = m;
+    __syncthreads();  // also: every thread has read the old scale before it is written
+#pragma unroll
+    for (int w = 0; w < kBlock / 32; ++w) m = fmaxf(m, s_max[k][w]);
+    return m;
+  };
+  float amax = block_max(largest(false), 0);
+  const bool inf = amax == INFINITY;  // rare: take the infinities out
+  if (inf) amax = block_max(largest(true), 1);
+  const float now = fmaxf(was, pow2(scale_exp(amax)));
   const float inv = 1.f / now;  // exact: a power of two
   if (threadIdx.x == 0) *scale = now;
   if (lo > 0 && now != was) {
@@ -246,11 +307,24 @@ __global__ void __launch_bounds__(kBlock) append_e4m3_kernel(const AppendParams 
       *q = u;
     }
   }
-  for (int r = lo + r0; r < hi; r += kRows) {
-    float x[16];
-    load_row(r, x);
-    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.x) = e4m3x8(x, inv);
-    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.y) = e4m3x8(x + 8, inv);
+  auto put = [&](int r, const uint4 (&u)[2]) {
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.x) = e4m3x8(u[0], inv);
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.y) = e4m3x8(u[1], inv);
+  };
+  if (kKeep > 0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int r = lo + i * kRows + r0;
+      if (r < hi) put(r, held[i]);
+    }
+  } else {
+    for (int r = lo + r0; r < hi; r += kRows) {
+      uint4 u[2];
+      load_row(r, u);
+      float m = 0.f;
+      take_row(r, u, m, inf);
+      put(r, u);
+    }
   }
 }
 
@@ -270,15 +344,23 @@ cudaError_t launch_bf16(const AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, int kBlock, int kKeep>
+cudaError_t launch_e4m3_as(const AppendParams& p, dim3 grid, cudaStream_t stream) {
+  if (p.rope.inter)
+    append_e4m3_kernel<D, kBlock, kKeep, true><<<grid, kBlock, 0, stream>>>(p);
+  else
+    append_e4m3_kernel<D, kBlock, kKeep, false><<<grid, kBlock, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_e4m3(const AppendParams& p, cudaStream_t stream) {
   const int pages = static_cast<int>((static_cast<long long>(p.Nn) + p.page_size - 2) / p.page_size) + 1;
   const dim3 grid(static_cast<unsigned>(pages) * p.Hkv, static_cast<unsigned>(p.B), 2u);
-  if (p.rope.inter)
-    append_e4m3_kernel<D, 256, true><<<grid, 256, 0, stream>>>(p);
-  else
-    append_e4m3_kernel<D, 256, false><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int rows = p.Nn < p.page_size ? p.Nn : p.page_size;  // new rows of a page at most
+  if (rows <= 64 / (D / 16)) return launch_e4m3_as<D, 64, 1>(p, grid, stream);
+  if (rows <= 256 / (D / 16) * 8) return launch_e4m3_as<D, 256, 8>(p, grid, stream);
+  return launch_e4m3_as<D, 256, 0>(p, grid, stream);
 }
 
 }  // namespace

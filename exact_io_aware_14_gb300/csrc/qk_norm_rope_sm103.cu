@@ -58,50 +58,36 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// One work item: up to kHeads heads of one token, q's or k's.
-struct Item {
-  bool is_k;
-  int h0, nh;        // first head, heads (0: no item)
-  long long token;   // b * N + n
-};
-template <int kHeads>
-__device__ __forceinline__ Item item_of(long long i, long long n_items, int gq, int gk, int Hq, int Hkv) {
-  Item it;
-  const int per = gq + gk;
-  it.token = i / per;
-  const int g = static_cast<int>(i - it.token * per);
-  it.is_k = g >= gq;
-  it.h0 = (it.is_k ? g - gq : g) * kHeads;
-  it.nh = i < n_items ? min(kHeads, (it.is_k ? Hkv : Hq) - it.h0) : 0;
-  return it;
-}
-
-template <int D, int kHeads, bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRopeParams p, long long n_items, int gq,
-                                                               int gk) {
+// The short form: row i of the q and k rows of all tokens (a token's q heads,
+// then its k heads).
+template <int D, bool kInter>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRopeParams p, long long rows) {
   constexpr int kTPR = D / 16;
   const int l = threadIdx.x % kTPR;
   const long long i = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTPR;
-  const Item it = item_of<kHeads>(i, n_items, gq, gk, p.Hq, p.Hkv);  // nh 0 past the end: no load or store
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(it.is_k ? p.k : p.q) +
-                           it.token * (it.is_k ? p.k_stride : p.q_stride) + static_cast<long long>(it.h0) * D;
+  const bool has = i < rows;  // the others take part in the shuffles
+  const int per = p.Hq + p.Hkv;
+  const long long token = i / per;
+  int h = static_cast<int>(i - token * per);
+  const bool is_k = h >= p.Hq;
+  if (is_k) h -= p.Hq;
   const int2 ch = row_chunks(l, p.rope.rot);
-  uint4 raw[kHeads][2];
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    raw[h][0] = raw[h][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < it.nh) {
-      raw[h][0] = *reinterpret_cast<const uint4*>(x + h * D + 8 * ch.x);
-      raw[h][1] = *reinterpret_cast<const uint4*>(x + h * D + 8 * ch.y);
-    }
+  float v[16];
+  uint4 raw[2];
+  raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+  if (has) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(is_k ? p.k : p.q) +
+                             token * (is_k ? p.k_stride : p.q_stride) + static_cast<long long>(h) * D;
+    raw[0] = *reinterpret_cast<const uint4*>(x + 8 * ch.x);
+    raw[1] = *reinterpret_cast<const uint4*>(x + 8 * ch.y);
   }
   Angles ang;
-  const bool turn = p.rope.rot > 0 && it.nh > 0;
+  const bool turn = has && l < (p.rope.rot >> 4);
   if (turn) {
-    const int pos = p.positions ? p.positions[it.token] : static_cast<int>(it.token % p.N);
+    const int pos = p.positions ? p.positions[token] : static_cast<int>(token % p.N);
     load_angles(p.rope, checked_pos(pos, p.rope.max_pos), l, ang);
   }
-  const float* w = it.is_k ? p.k_weight : p.q_weight;
+  const float* w = is_k ? p.k_weight : p.q_weight;
   float wv[16];
   if (w) {
     load4(w + 8 * ch.x, wv);
@@ -109,27 +95,23 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRope
     load4(w + 8 * ch.y, wv + 8);
     load4(w + 8 * ch.y + 4, wv + 12);
   }
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(it.is_k ? p.k_out : p.q_out) +
-                     (it.token * (it.is_k ? p.Hkv : p.Hq) + it.h0) * D;
+  unpack8(raw[0], v);
+  unpack8(raw[1], v + 8);
+  float ss = 0.f;
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    float v[16];
-    unpack8(raw[h][0], v);
-    unpack8(raw[h][1], v + 8);
-    float ss = 0.f;
+  for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
+  ss = row_sum<kTPR>(ss);
+  if (w) {
+    const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
 #pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
-    ss = row_sum<kTPR>(ss);
-    if (w) {
-      const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = v[j] * r * wv[j];
-    }
-    if (turn && l < (p.rope.rot >> 4)) rotate16<kInter, false>(v, ang);
-    if (h < it.nh) {
-      *reinterpret_cast<uint4*>(y + h * D + 8 * ch.x) = pack8(v);
-      *reinterpret_cast<uint4*>(y + h * D + 8 * ch.y) = pack8(v + 8);
-    }
+    for (int j = 0; j < 16; ++j) v[j] = v[j] * r * wv[j];
+  }
+  if (turn) rotate16<kInter, false>(v, ang);
+  if (has) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(is_k ? p.k_out : p.q_out) +
+                       (token * (is_k ? p.Hkv : p.Hq) + h) * D;
+    *reinterpret_cast<uint4*>(y + 8 * ch.x) = pack8(v);
+    *reinterpret_cast<uint4*>(y + 8 * ch.y) = pack8(v + 8);
   }
 }
 
@@ -333,26 +315,25 @@ __global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const float* part
   }
 }
 
-// Short forward: one row a group of threads.
-template <int D>
-cudaError_t launch_short(const QkNormRopeParams& p, cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.B) * p.N * (p.Hq + p.Hkv);
-  const unsigned blocks = static_cast<unsigned>((items * (D / 16) + kThreads - 1) / kThreads);
-  if (p.rope.inter)
-    qk_norm_rope_kernel<D, 1, true><<<blocks, kThreads, 0, stream>>>(p, items, p.Hq, p.Hkv);
-  else
-    qk_norm_rope_kernel<D, 1, false><<<blocks, kThreads, 0, stream>>>(p, items, p.Hq, p.Hkv);
-  return cudaGetLastError();
+// Launch rules, each with both sides measured (GB300, d = 128 where not said).
+// Long forward from 2 M values on: 1.0 M (32 + 8 heads) short 3.0 us, long
+// 3.2; 4.1 M 5.8 and 4.3; 33 M 35 and 25.
+constexpr long long kLongElements = 1 << 21;
+// Heads of an item: four where that leaves few places empty (33 M values, 32
+// + 8 heads: four 25.1 us, two 25.5, one 29.5), else one (12 M, 5 + 1 heads, d
+// = 64: 18.6, 13.5 and 11.8).  Two CTAs of 128 registers a thread: with three
+// the loads in flight spill (119 us for 58).  Backward: two heads (88 us; one
+// 135, four with one CTA 100).
+constexpr int kBwdHeads = 2, kCtasPerSm = 2;
+int fwd_heads(int Hq, int Hkv) {
+  const int places = (Hq + 3) / 4 * 4 + (Hkv + 3) / 4 * 4;
+  return places * 10 <= (Hq + Hkv) * 11 ? 4 : 1;
 }
 
-constexpr long long kLongElements = 1 << 21;  // rows times d from which the long forward is taken
-constexpr int kFwdHeads = 4, kFwdBlocks = 2;  // heads of an item, CTAs of an SM
-constexpr int kBwdHeads = 2, kBwdBlocks = 2;
-
 // CTAs for q and for k by their share of the rows, no more than there is work for.
-LongPlan plan_long(int B, int N, int Hq, int Hkv, int d, bool bwd) {
+LongPlan plan_long(int B, int N, int Hq, int Hkv, int d, int heads) {
   LongPlan plan;
-  const int ctas = 152 * (bwd ? kBwdBlocks : kFwdBlocks), heads = bwd ? kBwdHeads : kFwdHeads;
+  const int ctas = 152 * kCtasPerSm;
   const int groups = kThreads / (d / 16);
   auto share = [&](int H, int cap) {
     RowPlan r;
@@ -371,10 +352,10 @@ LongPlan plan_long(int B, int N, int Hq, int Hkv, int d, bool bwd) {
   return plan;
 }
 
-template <int D, bool kInter, bool kBwd>
+template <int D, int kHeads, bool kInter, bool kBwd>
 cudaError_t launch_long(const QkNormRopeParams& p, cudaStream_t stream) {
-  const LongPlan plan = plan_long(p.B, p.N, p.Hq, p.Hkv, p.d, kBwd);
-  qk_norm_rope_long_kernel<D, kBwd ? kBwdHeads : kFwdHeads, kBwd ? kBwdBlocks : kFwdBlocks, kInter, kBwd>
+  const LongPlan plan = plan_long(p.B, p.N, p.Hq, p.Hkv, p.d, kHeads);
+  qk_norm_rope_long_kernel<D, kHeads, kCtasPerSm, kInter, kBwd>
       <<<plan.q.blocks + plan.k.blocks, kThreads, 0, stream>>>(p, plan);
   cudaError_t e = cudaGetLastError();
   if (!kBwd || e != cudaSuccess || (!p.dq_weight && !p.dk_weight)) return e;
@@ -383,24 +364,35 @@ cudaError_t launch_long(const QkNormRopeParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, bool kInter>
+cudaError_t launch_fwd(const QkNormRopeParams& p, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.B) * p.N * (p.Hq + p.Hkv);
+  if (rows * D >= kLongElements)
+    return fwd_heads(p.Hq, p.Hkv) == 4 ? launch_long<D, 4, kInter, false>(p, stream)
+                                       : launch_long<D, 1, kInter, false>(p, stream);
+  const unsigned blocks = static_cast<unsigned>((rows * (D / 16) + kThreads - 1) / kThreads);
+  qk_norm_rope_kernel<D, kInter><<<blocks, kThreads, 0, stream>>>(p, rows);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 void qk_norm_rope_bwd_blocks(int B, int N, int Hq, int Hkv, int d, int* nbq, int* nbk) {
-  const LongPlan plan = plan_long(B, N, Hq, Hkv, d, true);
+  const LongPlan plan = plan_long(B, N, Hq, Hkv, d, kBwdHeads);
   *nbq = plan.q.blocks;
   *nbk = plan.k.blocks;
 }
 
 cudaError_t launch_qk_norm_rope(const QkNormRopeParams& p, cudaStream_t stream) {
-  const bool is_long = static_cast<long long>(p.B) * p.N * (p.Hq + p.Hkv) * p.d >= kLongElements;
-  if (!is_long) return p.d == 64 ? launch_short<64>(p, stream) : launch_short<128>(p, stream);
-  if (p.d == 64) return p.rope.inter ? launch_long<64, true, false>(p, stream) : launch_long<64, false, false>(p, stream);
-  return p.rope.inter ? launch_long<128, true, false>(p, stream) : launch_long<128, false, false>(p, stream);
+  if (p.d == 64) return p.rope.inter ? launch_fwd<64, true>(p, stream) : launch_fwd<64, false>(p, stream);
+  return p.rope.inter ? launch_fwd<128, true>(p, stream) : launch_fwd<128, false>(p, stream);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkNormRopeParams& p, cudaStream_t stream) {
-  if (p.d == 64) return p.rope.inter ? launch_long<64, true, true>(p, stream) : launch_long<64, false, true>(p, stream);
-  return p.rope.inter ? launch_long<128, true, true>(p, stream) : launch_long<128, false, true>(p, stream);
+  constexpr int h = kBwdHeads;
+  if (p.d == 64)
+    return p.rope.inter ? launch_long<64, h, true, true>(p, stream) : launch_long<64, h, false, true>(p, stream);
+  return p.rope.inter ? launch_long<128, h, true, true>(p, stream) : launch_long<128, h, false, true>(p, stream);
 }
 
 cudaError_t fetch_status_rope(cudaStream_t stream, uint32_t* out) {
