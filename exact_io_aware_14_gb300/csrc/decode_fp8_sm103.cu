@@ -69,18 +69,18 @@ constexpr float kWeightScale = 1024.f;  // 2^10: weights up to 2^14, e5m2 ends a
 template <int D, int R>
 struct Cfg {
   static constexpr int kN = (3 * R + 15) / 16 * 16;  // MMA columns
-  static constexpr int kTmem = kN <= 16 ? 64 : (kN <= 32 ? 128 : 256);  // 4 kN, a power of two
+  static constexpr int kTmem = kN <= 16 ? 64 : (kN <= 32 ? 128 : (kN <= 64 ? 256 : 512));  // 4 kN, a power of two
   static constexpr int kCtas = R == 4 ? 2 : 1;                          // per SM
   // softmax groups of four warps, each with its own kRows of the rows: one
   // group takes about 0.06 us a row and tile, 0.72 us is a tile's time at HBM rate
-  static constexpr int kGroups = R == 4 ? 1 : 2;
+  static constexpr int kGroups = R == 4 ? 1 : (R == 24 ? 3 : 2);
   static constexpr int kRows = R / kGroups;
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kWarps = kSoftWarps + 7;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = kTile * D;
-  static constexpr int kStages = (kCtas == 2 ? 3 : (R == 16 ? 5 : 6)) * 128 / D;
-  static constexpr int kItems = 4;  // items prepared or in work
+  static constexpr int kStages = (kCtas == 2 ? 3 : (R == 8 ? 6 : 5)) * 128 / D;
+  static constexpr int kItems = R == 24 ? 3 : 4;  // items prepared or in work
   static constexpr int kMaxBlocks = kMaxChunkFp8 / 64;
   static constexpr int kOffV = 0;  // V first: the M-major reads of a 64-dim V tile run into K's (see below)
   static constexpr int kOffK = kTileBytes;
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       if (n_t < 0) break;
       const int lim_min = it.lim_min;
       const float vmul = it.vref > 0.f ? kWeightScale / it.vref : 0.f;
+      const bool idle = grp > 0 && it.o_row[grp * kRows] < 0;  // no row of the group is real: it only keeps step
       float m[kRows], l[kRows], qm[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
@@ -322,6 +323,13 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const bool live = key < kn;
         const float ks = live ? it.ks[key >> 6] : 0.f, wv = live ? it.vs[key >> 6] * vmul : 0.f;
         if (!wait_all(bar_s + buf, (g >> 1) & 1, abort_flag, 4)) failed = true;
+        if (idle) {
+          // (its columns of P and O^T are not looked at); looks at V are counted as the others count them
+          if (g >= 2 && !wait_all(bar_of + buf, ((g - 2) >> 1) & 1, abort_flag, 6)) failed = true;
+          if ((t + 1) * kTile > lim_min && lim_min < kn) ++looks;
+          if (lane == 0) mbar_arrive(bar_p + buf);
+          continue;  // also where a wait gave up: the group's warps leave together, at the next item
+        }
         tc_fence_after();
         constexpr int kLd = (3 * kRows + 7) / 8 * 8;
         uint32_t u[kLd];
@@ -482,36 +490,41 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           ok = wait_all(bar_p + buf, (g >> 1) & 1, abort_flag, 9) && wait_all(bar_o + buf, (g >> 1) & 1, abort_flag, 10);
           if (!ok) break;
           tc_fence_after();
-          uint32_t u[kN];
-          tmem_ld_row<kN>(tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN, u);
-          float al[R];
+            constexpr int kLd = (3 * kRows + 7) / 8 * 8;
+          const uint32_t o_at = tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN;
 #pragma unroll
-          for (int r = 0; r < R; ++r) al[r] = s_alpha[buf * R + r];
+          for (int q = 0; q < C::kGroups; ++q) {
+            uint32_t u[kLd];
+            tmem_ld_row<kLd>(o_at + q * 3 * kRows, u);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              acc[q * kRows + r] =
+                  fmaf(acc[q * kRows + r], s_alpha[buf * R + q * kRows + r],
+                       __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]));
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_of + buf);
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            acc[r] = fmaf(acc[r], al[r],
-                          __uint_as_float(u[column<R, kRows>(0, r)]) + __uint_as_float(u[column<R, kRows>(1, r)]) +
-                              __uint_as_float(u[column<R, kRows>(2, r)]));
         }
         if (!ok || !wait_all(bar_ml + (n & 1), (n >> 1) & 1, abort_flag, 11)) break;
         const float* ml = s_ml + (n & 1) * 5 * R;
         const int split = it.split;
         const bool direct = it.direct != 0;
         const float osc = it.vref * (1.f / kWeightScale);
-        float o[R], lse[R];
-        int o_row[R], lse_row[R];
+        // what the slot holds is read before it is given back; rows are in order,
+        // those past the last (-1) behind
+        int o_row[R];
+        float lse[R];
+        int lse_row = -1;  // lane r keeps row r's
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float lr = (ml[R + r] + ml[2 * R + r]) + (ml[3 * R + r] + ml[4 * R + r]);
           // l is 0 exactly where the row sees no key of the split (NaN, not 0, where a score is NaN)
-          o[r] = lr == 0.f ? 0.f : acc[r] * osc / lr;
+          acc[r] = lr == 0.f ? 0.f : acc[r] * osc / lr;
           lse[r] = lr == 0.f ? -INFINITY : (ml[r] + __log2f(lr)) * 0.6931471805599453f;
           o_row[r] = it.o_row[r];
-          lse_row[r] = it.lse_row[r];
         }
+        if (lane < R) lse_row = it.lse_row[lane];
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar_mf + (n & 1));
@@ -521,11 +534,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         for (int r = 0; r < R; ++r) {
           if (o_row[r] < 0) break;
           if (direct) {
-            static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(o_row[r]) * D + dd] = __float2bfloat16_rn(o[r]);
-            if (dd == 0) p.lse[lse_row[r]] = lse[r];
+            static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(o_row[r]) * D + dd] = __float2bfloat16_rn(acc[r]);
+            if (dd == r) p.lse[lse_row] = lse[r];
           } else {
             const long long part = static_cast<long long>(o_row[r]) * p.n_split + split;
-            p.o_part[part * D + dd] = o[r];
+            p.o_part[part * D + dd] = acc[r];
             if (dd == 0) p.lse_part[part] = lse[r];
           }
         }
@@ -571,9 +584,27 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       total = __shfl_sync(0xffffffffu, incl, 31);
       return true;
     };
-    // 32 / R lanes share a row of q, each a run of kDims of it.
-    constexpr int kPg = C::kMaxBlocks / 32, kLanes = 32 / R, kDims = D / kLanes;
+    // kLanes lanes share a row of q, each a run of kDims of it; kPasses times
+    // 32 / kLanes rows.  One pass of q is loaded an item ahead; several would
+    // not fit the registers, and their items are longer.
+    constexpr int kPg = C::kMaxBlocks / 32, kLanes = R == 4 ? 8 : 4, kDims = D / kLanes, kPassRows = 32 / kLanes;
+    constexpr int kPasses = R / kPassRows;
+    constexpr bool kAhead = kPasses == 1;
     const int qr = lane / kLanes, qd = lane % kLanes * kDims;
+    // row r of an item: its place, and this lane's part of its q
+    auto row_of = [&](int b, int hkv, int row0, int r, int& tok, int& hq) {
+      const int row = row0 + r;
+      tok = p.G.div(row);
+      hq = hkv * G + row - tok * G;
+      return row < rows;
+    };
+    auto load_q = [&](int b, int tok, int hq, bool real, uint4 (&q)[kDims / 8]) {
+      const __nv_bfloat16* at =
+          static_cast<const __nv_bfloat16*>(p.q) + ((static_cast<long long>(b) * p.Nq + tok) * p.Hq + hq) * D + qd;
+#pragma unroll
+      for (int c = 0; c < kDims / 8; ++c)
+        q[c] = real ? *reinterpret_cast<const uint4*>(at + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    };
     struct Found {  // an item found, its page numbers on their way
       bool more;
       int b, split, len, hkv, row0;
@@ -581,11 +612,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     };
     struct Loading {  // its scales and q on their way
       bool more;
-      int k0, kn, n_blk;
-      int lim;  // cache positions that the lane's row sees: those below it
-      int o_row, lse_row;
+      int k0, kn, n_blk, len, b, hkv, row0;
       float ks[kPg], vs[kPg];
-      uint4 q[kDims / 8];
+      uint4 q[kAhead ? kDims / 8 : 1];
     };
     bool more = next_block();
     unsigned item = blockIdx.x;
@@ -636,7 +665,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       a.k0 = f.split * p.chunk;
       a.kn = min(p.chunk, f.len - a.k0);
       a.n_blk = (a.kn + 63) / 64;
-      a.lim = a.o_row = a.lse_row = 0;
+      a.len = f.len;
+      a.b = f.b;
+      a.hkv = f.hkv;
+      a.row0 = f.row0;
       if (f.more) {
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
@@ -650,15 +682,11 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             a.vs[k] = p.v_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
           }
         }
-        const int row = f.row0 + qr, tok = p.G.div(row), hq = f.hkv * G + row - tok * G;
-        a.lim = f.len - p.Nq + 1 + tok;
-        a.o_row = row < rows ? (f.b * p.Nq + tok) * p.Hq + hq : -1;
-        a.lse_row = (f.b * p.Hq + hq) * p.Nq + tok;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                                 ((static_cast<long long>(f.b) * p.Nq + tok) * p.Hq + hq) * D + qd;
-#pragma unroll
-        for (int c = 0; c < kDims / 8; ++c)
-          a.q[c] = row < rows ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kAhead) {
+          int tok, hq;
+          const bool real = row_of(f.b, f.hkv, f.row0, qr, tok, hq);
+          load_q(f.b, tok, hq, real, a.q);
+        }
       }
       if (n >= C::kItems && !wait_all(bar_free + slot, (n / C::kItems - 1) & 1, abort_flag, 12)) {
         ok = false;
@@ -687,49 +715,67 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       Item<R>& it = items[slot];
       if (cur.more) {
         // q as three e5m2 terms a row
-        uint32_t amax = 0u;
+        uint4 q[kPasses][kDims / 8];
 #pragma unroll
-        for (int c = 0; c < kDims / 8; ++c) {
-          const uint32_t w[4] = {cur.q[c].x, cur.q[c].y, cur.q[c].z, cur.q[c].w};
+        for (int ps = 0; ps < kPasses; ++ps) {
+          int tok, hq;
+          const int r = ps * kPassRows + qr;
+          const bool real = row_of(cur.b, cur.hkv, cur.row0, r, tok, hq);
+          if constexpr (kAhead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
+            for (int c = 0; c < kDims / 8; ++c) q[0][c] = cur.q[c];
+          } else {
+            load_q(cur.b, tok, hq, real, q[ps]);
+          }
+          if (lane % kLanes == 0) {
+            it.lim[r] = min(cur.kn, cur.len - p.Nq + 1 + tok - cur.k0);
+            it.o_row[r] = real ? (cur.b * p.Nq + tok) * p.Hq + hq : -1;
+            it.lse_row[r] = (cur.b * p.Hq + hq) * p.Nq + tok;
+          }
         }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const bool fin = amax < 0x7f800000u;  // bits of the row's largest magnitude
-        const int e = fin ? max(static_cast<int>(amax >> 23) - 127, -100) : 0;
-        const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
         const uint32_t q_at = sQ + slot * C::kQBytes;
 #pragma unroll
-        for (int c = 0; c < kDims / 8; ++c) {  // 8 values: 8 bytes a term, at a multiple of 8
-          const uint32_t w[4] = {cur.q[c].x, cur.q[c].y, cur.q[c].z, cur.q[c].w};
-          float x[8];
+        for (int ps = 0; ps < kPasses; ++ps) {
+          const int r = ps * kPassRows + qr;
+          uint32_t amax = 0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16lo(w[i]) * f;
-            x[2 * i + 1] = bf16hi(w[i]) * f;
+          for (int c = 0; c < kDims / 8; ++c) {
+            const uint32_t w[4] = {q[ps][c].x, q[ps][c].y, q[ps][c].z, q[ps][c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
           }
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            float t3[8];
+          for (int o = kLanes / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const bool fin = amax < 0x7f800000u;  // bits of the row's largest magnitude
+          const int e = fin ? max(static_cast<int>(amax >> 23) - 127, -100) : 0;
+          const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              t3[i] = lead3(x[i]);
-              x[i] -= t3[i];
+          for (int c = 0; c < kDims / 8; ++c) {  // 8 values: 8 bytes a term, at a multiple of 8
+            const uint32_t w[4] = {q[ps][c].x, q[ps][c].y, q[ps][c].z, q[ps][c].w};
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[2 * i] = bf16lo(w[i]) * f;
+              x[2 * i + 1] = bf16hi(w[i]) * f;
             }
-            const uint32_t at = q_at + swizzled<D>(column<R, kRows>(k, qr), qd + 8 * c);
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
-                         "r"(e5m2x2(t3[0], t3[1]) | (e5m2x2(t3[2], t3[3]) << 16)),
-                         "r"(e5m2x2(t3[4], t3[5]) | (e5m2x2(t3[6], t3[7]) << 16))
-                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              float t3[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                t3[i] = lead3(x[i]);
+                x[i] -= t3[i];
+              }
+              const uint32_t at = q_at + swizzled<D>(column<R, kRows>(k, r), qd + 8 * c);
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
+                           "r"(e5m2x2(t3[0], t3[1]) | (e5m2x2(t3[2], t3[3]) << 16)),
+                           "r"(e5m2x2(t3[4], t3[5]) | (e5m2x2(t3[6], t3[7]) << 16))
+                           : "memory");
+            }
           }
-        }
-        if (lane % kLanes == 0) {
-          it.lim[qr] = min(cur.kn, cur.lim - cur.k0);
-          it.o_row[qr] = cur.o_row;
-          it.lse_row[qr] = cur.lse_row;
           // a row with an infinity or NaN: every score NaN
-          it.qm[qr] = fin ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2 : NAN;
+          if (lane % kLanes == 0)
+            it.qm[r] = fin ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2 : NAN;
         }
         float vref = 0.f;
 #pragma unroll
@@ -1058,6 +1104,8 @@ cudaError_t launch_d(const DecodeFp8Params& p, cudaStream_t stream) {
   const int rows = p.Nq * (p.Hq / p.Hkv);
   if (rows <= 4) return launch_rows<D, 4>(p, dev, sms, stream);
   if (rows <= 8) return launch_rows<D, 8>(p, dev, sms, stream);
+  // blocks of 16 or 24 rows: whichever reads the cache fewer times, 16 where equal
+  if ((rows + 23) / 24 < (rows + 15) / 16) return launch_rows<D, 24>(p, dev, sms, stream);
   return launch_rows<D, 16>(p, dev, sms, stream);
 }
 

@@ -73,6 +73,10 @@ CASES = [
     (3, 4, 7, 7, 128, 64, [4, 131, 66], 64),
     (2, 7, 16, 2, 64, 128, [513, 7], 128),
     (1, 64, 2, 1, 64, 64, [130], 64),
+    (2, 1, 18, 1, 128, 64, [300, 65], 128),          # 18 rows: three groups, the last with two
+    (2, 3, 18, 3, 64, 192, [3, 500], 256),
+    (2, 7, 24, 3, 128, 64, [7, 400], 192),           # 56 rows: blocks of 24, the last with one real group
+    (1, 7, 16, 1, 64, 64, [200], 64),
     (4, 5, 4, 2, 128, 64, [0, 1, 3, 68], 64),       # rows that see no key, a sequence without any
 ]
 
@@ -175,6 +179,25 @@ def test_nan_in_the_cache_spoils_its_sequence_only():
     pools[0][table[1, 0], 3, 0, 0] = 0x7F      # a key of sequence 1
     o, lse = _run(q, pools, scales, table, lens, 0.09, 128)
     assert o[1].isnan().all() and lse[1].isnan().all() and lse[0].isfinite().all()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 1), (24, 1)])
+def test_nan_among_the_new_tokens(Hq, Hkv):
+    """A NaN in a value that only the last of the new tokens sees leaves the others as they are."""
+    lens, Nq, d = [131], 3, 128
+    g, pools, scales, table = _cache(1, Hkv, d, 64, lens, 79)
+    q = torch.randn((1, Nq, Hq, d), generator=g).to(torch.bfloat16)
+    want = _run(q, pools, scales, table, lens, 0.09, 128)
+    spoilt = [p.clone() for p in pools]
+    spoilt[1][table[0, 2], 2, 0, 17] = 0xFF    # the value of key 130
+    o, lse = _run(q, spoilt, scales, table, lens, 0.09, 128)
+    assert torch.equal(o[:, :2], want[0][:, :2]) and torch.equal(lse, want[1])
+    assert o[:, 2].isnan().any(-1).all()
+    spoilt = [p.clone() for p in pools]
+    spoilt[0][table[0, 2], 2, 0, 5] = 0x7F     # its key
+    o, lse = _run(q, spoilt, scales, table, lens, 0.09, 128)
+    assert torch.equal(o[:, :2], want[0][:, :2]) and torch.equal(lse[..., :2], want[1][..., :2])
+    assert o[:, 2].isnan().all() and lse[..., 2].isnan().all()
 
 
 def test_bad_lengths_and_pages_are_reported():
