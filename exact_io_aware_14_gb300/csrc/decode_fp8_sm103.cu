@@ -310,12 +310,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       const int lim_min = it.lim_min;
       const float vmul = it.vref > 0.f ? kWeightScale / it.vref : 0.f;
       const bool idle = grp > 0 && it.o_row[grp * kRows] < 0;  // no row of the group is real: it only keeps step
-      float m[kRows], l[kRows], qm[kRows];
+      // Rows in pairs (packed fp32 arithmetic).  nm: the reference (base 2),
+      // negated, 0 until the item's first tile sets it (every row that sees a
+      // key sees the split's first one); seen: bit r once row r's is set.
+      constexpr int kPairs = kRows / 2;
+      float2 nm[kPairs], l[kPairs], qm[kPairs];
+      uint32_t seen = 0u;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-        qm[r] = it.qm[grp * kRows + r];  // 0 for a row past the last: its scores are 0
+      for (int r = 0; r < kPairs; ++r) {
+        nm[r] = l[r] = make_float2(0.f, 0.f);
+        qm[r] = make_float2(it.qm[grp * kRows + 2 * r], it.qm[grp * kRows + 2 * r + 1]);
       }
       for (int t = 0; t < n_t; ++t, ++g) {
         const int buf = g & 1, s = g % C::kStages;
@@ -336,27 +340,31 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         tmem_ld_row<kLd>(tmem + (static_cast<uint32_t>(w4 * 32) << 16) + buf * kN + grp * 3 * kRows, u);
         tc_fence_before();
         const bool edge = (t + 1) * kTile > lim_min;  // uniform: some row does not see the whole tile
-        float x[kRows];
-        bool big = false;
         uint32_t hidden = 0u;  // rows that do not see this thread's key
         if (edge) {
 #pragma unroll
           for (int r = 0; r < kRows; ++r) hidden |= (key >= it.lim[grp * kRows + r] ? 1u : 0u) << r;
         }
+        float2 x[kPairs];  // scores in base 2, less the reference
+        bool big = t == 0;
+        const float2 ks2 = make_float2(ks, ks);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float sum = __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]);
-          x[r] = (hidden >> r) & 1u ? -INFINITY : sum * (qm[r] * ks);
-          big = big || x[r] > m[r] + kMoveLog2;  // -inf > -inf: no
+        for (int r = 0; r < kPairs; ++r) {
+          auto at = [&](int k) {
+            return make_float2(__uint_as_float(u[k * kRows + 2 * r]), __uint_as_float(u[k * kRows + 2 * r + 1]));
+          };
+          x[r] = ffma2(fadd2(fadd2(at(0), at(1)), at(2)), fmul2(qm[r], ks2), nm[r]);
+          big = big || fmaxf(x[r].x, x[r].y) > kMoveLog2;  // (masked keys can only ask for the look below)
         }
         float al[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) al[r] = 1.f;
         if (softmax_bar_or(grp, big || failed || *abort_flag)) {
-          // some row's reference moves (or a wait gave up)
+          // some row's reference may have to move (or a wait gave up)
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            const float mx = warp_max_ordered(x[r]);  // NaN scores show in p
+            const float xr = r & 1 ? x[r / 2].y : x[r / 2].x;
+            const float mx = warp_max_ordered((hidden >> r) & 1u ? -INFINITY : xr);  // NaN scores show in p
             if (lane == 0) red[w4 * kRows + r] = mx;
           }
           if (lane == 0) fail[w4] = failed || *abort_flag;
@@ -369,10 +377,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
             const float mx = fmaxf(fmaxf(red[r], red[kRows + r]), fmaxf(red[2 * kRows + r], red[3 * kRows + r]));
-            if (mx > m[r] + kMoveLog2) {
-              al[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mx);
-              l[r] *= al[r];
-              m[r] = mx;
+            const bool first = !((seen >> r) & 1u);
+            if (mx > (first ? -INFINITY : kMoveLog2)) {
+              float& mr = r & 1 ? nm[r / 2].y : nm[r / 2].x;
+              float& lr = r & 1 ? l[r / 2].y : l[r / 2].x;
+              float& xr = r & 1 ? x[r / 2].y : x[r / 2].x;
+              al[r] = first ? 0.f : ex2_approx(-mx);
+              lr *= al[r];
+              mr -= mx;
+              xr -= mx;
+              seen |= 1u << r;
             }
           }
         }
@@ -420,27 +434,28 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             ++looks;
           }
         }
-        float w[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          float pr = ex2_approx(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-          if ((hidden >> r) & 1u) pr = 0.f;
-          l[r] += pr;
-          w[r] = pr * wv;
-          if (edge && !((hidden >> r) & 1u)) w[r] += spoil;
-        }
         const uint32_t pcol = sP + buf * kN * kTile;
+        const float2 wv2 = make_float2(wv, wv);
 #pragma unroll
-        for (int r = 0; r < kRows; r += 2) {
-          float a = w[r], c = w[r + 1];
+        for (int r = 0; r < kPairs; ++r) {
+          float2 pr = make_float2(ex2_approx(x[r].x), ex2_approx(x[r].y));
+          if (edge) {
+            if ((hidden >> (2 * r)) & 1u) pr.x = 0.f;
+            if ((hidden >> (2 * r + 1)) & 1u) pr.y = 0.f;
+          }
+          l[r] = fadd2(l[r], pr);
+          float2 w = fmul2(pr, wv2);
+          if (edge) {
+            if (!((hidden >> (2 * r)) & 1u)) w.x += spoil;
+            if (!((hidden >> (2 * r + 1)) & 1u)) w.y += spoil;
+          }
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            const float ta = k < 2 ? lead3(a) : a, tc = k < 2 ? lead3(c) : c;
-            const uint32_t two = e5m2x2(ta, tc);
-            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + r, row), two);
-            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + r + 1, row), two >> 8);
-            a -= ta;
-            c -= tc;
+            const float2 tm = k < 2 ? make_float2(lead3(w.x), lead3(w.y)) : w;
+            const uint32_t two = e5m2x2(tm.x, tm.y);
+            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + 2 * r, row), two);
+            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + 2 * r + 1, row), two >> 8);
+            if (k < 2) w = fadd2(w, make_float2(-tm.x, -tm.y));
           }
         }
         if (row < kRows) {
@@ -460,9 +475,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       float* ml = s_ml + (n & 1) * 5 * R;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        l[r] = warp_sum(l[r]);
-        if (lane == 0) ml[(1 + w4) * R + grp * kRows + r] = l[r];
-        if (row == 0) ml[grp * kRows + r] = m[r];
+        const float lr = warp_sum(r & 1 ? l[r / 2].y : l[r / 2].x);
+        if (lane == 0) ml[(1 + w4) * R + grp * kRows + r] = lr;
+        if (row == 0) ml[grp * kRows + r] = r & 1 ? -nm[r / 2].y : -nm[r / 2].x;
       }
       __syncwarp();
       if (lane == 0) {
