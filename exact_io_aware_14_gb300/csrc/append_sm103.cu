@@ -154,8 +154,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Two bf16 of a word rounded to odd from two floats.
 __device__ __forceinline__ uint32_t pack_odd(float lo, float hi) {
   const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
-  const uint32_t ao = a | (((a & 0xffffu) + 0xffffu) & 0x10000u), bo = b | (((b & 0xffffu) + 0xffffu) & 0x10000u);
-  return __byte_perm(ao, bo, 0x7632);
+  // upper halves; 1 for each lower half that is not 0
+  return __byte_perm(a, b, 0x7632) | __vminu2(__byte_perm(a, b, 0x5410), 0x00010001u);
 }
 // Eight values (four words of bf16) times inv -> eight codes.
 __device__ __forceinline__ uint2 e4m3x8(const uint4& u, float inv) {
@@ -191,9 +191,16 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 }
 
 // kKeep: rows a thread keeps at most (the page has no more than kBlock * 16 /
-// D * kKeep); 0: any number, read and rotated a second time for the codes.
+// D * kKeep new ones); 0: any number, read and rotated a second time for the
+// codes.  Four rows a thread and 64 registers, so that an SM holds 1024
+// threads, in the smallest blocks that hold a page's rows.  Measured on 49 K
+// new tokens, 8 heads, d = 128, pages of 64 / 128 / 256 rows: blocks of 128
+// threads 61 us / - / -, 256 threads 84 / 68 / -, 512 threads 144 / 97 / 74;
+// 256 threads with eight rows and 128 registers 124 / 91 / 75; rows read twice
+// 109 at 256; clusters of 128-thread blocks that exchange their largest values
+// - / 79 / 83.
 template <int D, int kBlock, int kKeep, bool kInter>
-__global__ void __launch_bounds__(kBlock, kKeep > 1 ? 2 : 1) append_e4m3_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(const AppendParams p) {
   constexpr int kTPR = D / 16;
   constexpr int kRows = kBlock / kTPR;  // rows a round of the block covers
   const int b = blockIdx.y;
@@ -209,8 +216,8 @@ __global__ void __launch_bounds__(kBlock, kKeep > 1 ? 2 : 1) append_e4m3_kernel(
   const int lo = max(s.len, start) - start;
   const int hi = static_cast<int>(min(static_cast<long long>(s.len) + s.n - start, static_cast<long long>(p.page_size)));
   if (hi <= lo) return;  // past the last touched page
-  const int pg = page_of(p, b, blk);
-  if (pg < 0) return;
+  // the page's number is asked for here and looked at behind the rows' loads
+  const int pg = p.block_table[static_cast<long long>(b) * p.max_blocks + blk];
   const RopeParams& rope = p.rope;
   const int l = threadIdx.x % kTPR, r0 = threadIdx.x / kTPR;
   const int2 ch = row_chunks(l, rope.rot);
@@ -219,12 +226,6 @@ __global__ void __launch_bounds__(kBlock, kKeep > 1 ? 2 : 1) append_e4m3_kernel(
   // row r of the page is new row start + r - len of the sequence
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
                              (static_cast<long long>(b) * p.Nn + start - s.len) * stride + static_cast<long long>(h) * D;
-  const long long pitch = static_cast<long long>(p.Hkv) * D;
-  uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + static_cast<long long>(pg) * p.page_size * pitch +
-                 static_cast<long long>(h) * D;
-  float* scale = (is_v ? p.v_scales : p.k_scales) + static_cast<long long>(pg) * p.Hkv + h;
-  const float was = lo > 0 ? *scale : 0.f;
-
   auto load_row = [&](int r, uint4 (&u)[2]) {
     const __nv_bfloat16* row = src + r * stride;
     u[0] = *reinterpret_cast<const uint4*>(row + 8 * ch.x);
@@ -289,7 +290,18 @@ __global__ void __launch_bounds__(kBlock, kKeep > 1 ? 2 : 1) append_e4m3_kernel(
     for (int w = 0; w < kBlock / 32; ++w) m = fmaxf(m, s_max[k][w]);
     return m;
   };
-  float amax = block_max(largest(false), 0);
+  const float mine = largest(false);
+  if (pg < 0 || pg >= p.num_pages) {  // uniform: the rows are dropped
+    if (threadIdx.x == 0) record(2, kDevBadPage);
+    return;
+  }
+  const long long pitch = static_cast<long long>(p.Hkv) * D;
+  uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + static_cast<long long>(pg) * p.page_size * pitch +
+                 static_cast<long long>(h) * D;
+  float* scale = (is_v ? p.v_scales : p.k_scales) + static_cast<long long>(pg) * p.Hkv + h;
+  const float was = lo > 0 ? *scale : 0.f;
+
+  float amax = block_max(mine, 0);
   const bool inf = amax == INFINITY;  // rare: take the infinities out
   if (inf) amax = block_max(largest(true), 1);
   const float now = fmaxf(was, pow2(scale_exp(amax)));
@@ -358,8 +370,12 @@ cudaError_t launch_e4m3(const AppendParams& p, cudaStream_t stream) {
   const int pages = static_cast<int>((static_cast<long long>(p.Nn) + p.page_size - 2) / p.page_size) + 1;
   const dim3 grid(static_cast<unsigned>(pages) * p.Hkv, static_cast<unsigned>(p.B), 2u);
   const int rows = p.Nn < p.page_size ? p.Nn : p.page_size;  // new rows of a page at most
-  if (rows <= 64 / (D / 16)) return launch_e4m3_as<D, 64, 1>(p, grid, stream);
-  if (rows <= 256 / (D / 16) * 8) return launch_e4m3_as<D, 256, 8>(p, grid, stream);
+  // few new rows: the smallest block, for latency (64 sequences' single tokens
+  // 2.9 us, with blocks of 256 threads 5.4)
+  if (rows <= 64 * 16 / D) return launch_e4m3_as<D, 64, 1>(p, grid, stream);
+  if (rows <= 128 * 16 / D * 4) return launch_e4m3_as<D, 128, 4>(p, grid, stream);
+  if (rows <= 256 * 16 / D * 4) return launch_e4m3_as<D, 256, 4>(p, grid, stream);
+  if (rows <= 512 * 16 / D * 4) return launch_e4m3_as<D, 512, 4>(p, grid, stream);
   return launch_e4m3_as<D, 256, 0>(p, grid, stream);
 }
 

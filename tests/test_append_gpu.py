@@ -141,6 +141,11 @@ CASES = [
     (2, 1, 64, 512, [511, 3], 700, [600, 700], 0, False),
     (2, 9, 128, 128, [17, 0], 33, [2, 33], 16, True),
     (1, 2, 128, 1024, [700], 500, None, 128, True),
+    (2, 1, 128, 1024, [3, 1000], 1500, [1500, 30], 64, False),   # more new rows of a page than a block keeps
+    (2, 3, 128, 256, [250, 130], 260, [260, 9], 128, True),      # pages full and nearly empty
+    (2, 2, 64, 1024, [1, 1023], 1100, None, 64, False),
+    (3, 2, 128, 512, [500, 0, 40], 17, [17, 1, 9], 32, False),
+    (2, 1, 128, 320, [319, 100], 333, [320, 333], 128, False),
 ]
 
 
@@ -193,6 +198,46 @@ def test_values_at_the_ends_of_the_range():
         pools, _ = _run(c, k, k2, None, False)
         _check(c, k, k2, None, False, None, pools)
     assert _native.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("page,Nn,d", [(256, 256, 128), (512, 300, 64), (64, 40, 128), (1024, 1024, 128)])
+def test_one_large_value_and_infinities_anywhere_in_a_page(page, Nn, d):
+    """The largest value sits in any thread's share of the page; infinities are left out of the scale, wherever."""
+    for at in (0, Nn // 3, Nn - 1):
+        c = Cache(1, 2, d, page, [0], 2 * page, True, 50 + at)
+        k, v = (torch.randn((1, Nn, 2, d), generator=c.g) for _ in range(2))
+        k[0, at, 0, 7] = 1000.0
+        v[0, at, 1, d - 1] = -3000.0
+        k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+        rope = _native.rope_table(Nn, 32, device="cpu")
+        pools, _ = _run(c, k, v, rope, False)
+        _check(c, k, v, rope, False, None, pools)
+        v[0, (at + 5) % Nn, 0, 3] = float("inf")
+        k[0, (at + 9) % Nn, 1, 40] = float("-inf")     # not among the rotated ones
+        pools, _ = _run(c, k, v, rope, False)
+        _check(c, k, v, rope, False, None, pools)
+    assert _native.attn_get_device_status() == 0
+
+
+def test_rounding_to_nearest_after_rotation():
+    """Rotated values at and next to the codes' ties and the scale's border: angles of 0 (the values as they are) and
+    of 45 degrees, every code equal to the one that the fp32 rotation rounds to."""
+    d, Nn = 64, 64
+    base = torch.tensor([1.0, 1.0625, 1.1875, 1.3125, 1.75, 1.7578125, 1.765625, 1.9375])
+    x = (base[:, None] * torch.exp2(torch.arange(-7, 9).float())[None]).reshape(-1)     # 128 values to 496
+    k = x[torch.randint(0, 128, (1, Nn, 1, d), generator=torch.Generator().manual_seed(6))].to(torch.bfloat16)
+    c = Cache(1, 1, d, 64, [0], 64, True, 55)
+    ang = torch.zeros((64, 32))
+    ang[::2] = torch.pi / 4
+    ang[1::4] = 1e-7
+    rope = (ang.cos(), ang.sin())
+    pools, _ = _run(c, k, k, rope, False)
+    a, b = k[0, :, 0, :32].float(), k[0, :, 0, 32:].float()
+    y = torch.cat((a * rope[0] - b * rope[1], b * rope[0] + a * rope[1]), -1)
+    s = S.scale_for(y.abs().max().double()).float()
+    pg = int(c.table[0, 0])
+    assert pools[2][pg, 0].item() == s
+    assert torch.equal(pools[0][pg, :, 0].cpu().view(torch.uint8), (y / s).to(torch.float8_e4m3fn).view(torch.uint8))
 
 
 def test_bad_lengths_pages_and_positions_are_reported():
