@@ -169,10 +169,10 @@ __device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
   return w;
 }
 __device__ __forceinline__ float max_abs8(const uint4& u, float m) {
-  m = fmax3(m, fabsf(bf16lo(u.x)), fabsf(bf16hi(u.x)));
-  m = fmax3(m, fabsf(bf16lo(u.y)), fabsf(bf16hi(u.y)));
-  m = fmax3(m, fabsf(bf16lo(u.z)), fabsf(bf16hi(u.z)));
-  return fmax3(m, fabsf(bf16lo(u.w)), fabsf(bf16hi(u.w)));
+  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.x))), fabsf(bf16hi(u.x)));
+  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.y))), fabsf(bf16hi(u.y)));
+  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.z))), fabsf(bf16hi(u.z)));
+  return fmaxf(fmaxf(m, fabsf(bf16lo(u.w))), fabsf(bf16hi(u.w)));
 }
 // One e4m3 pair -> two floats (through f16, which holds every e4m3 value).
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t u) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (finite_only && fabsf(x[i]) == INFINITY) x[i] = NAN;
-        if (i & 1) m = fmax3(m, fabsf(x[i - 1]), fabsf(x[i]));
+        m = fmaxf(m, fabsf(x[i]));
       }
       u[0] = make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
       u[1] = make_uint4(pack_odd(x[8], x[9]), pack_odd(x[10], x[11]), pack_odd(x[12], x[13]), pack_odd(x[14], x[15]));

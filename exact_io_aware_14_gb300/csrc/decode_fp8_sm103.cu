@@ -111,7 +111,8 @@ struct Item {
   float vref;    // largest value scale of the split
   int pad[1];
   int page[kMaxChunkFp8 / 64];  // of the split's 64-key blocks
-  float ks[kMaxChunkFp8 / 64], vs[kMaxChunkFp8 / 64];
+  float ks[kMaxChunkFp8 / 64];
+  float vs[kMaxChunkFp8 / 64];  // over vref, times kWeightScale
   float qm[R];   // softmax scale (base 2) over the row's power of two
   int lim[R];    // keys of the split that row r sees: those below lim[r] (0 or less: none)
   int o_row[R], lse_row[R];  // where its results go, in rows of o and entries of lse; -1: no such row
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       const int n_t = it.n_t, kn = it.kn;
       if (n_t < 0) break;
       const int lim_min = it.lim_min;
-      const float vmul = it.vref > 0.f ? kWeightScale / it.vref : 0.f;
       const bool idle = grp > 0 && it.o_row[grp * kRows] < 0;  // no row of the group is real: it only keeps step
       // Rows in pairs (packed fp32 arithmetic).  nm: the reference (base 2),
       // negated, 0 until the item's first tile sets it (every row that sees a
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const int buf = g & 1, s = g % C::kStages;
         const int key = t * kTile + row;
         const bool live = key < kn;
-        const float ks = live ? it.ks[key >> 6] : 0.f, wv = live ? it.vs[key >> 6] * vmul : 0.f;
+        const float ks = live ? it.ks[key >> 6] : 0.f, wv = live ? it.vs[key >> 6] : 0.f;
         if (!wait_all(bar_s + buf, (g >> 1) & 1, abort_flag, 4)) failed = true;
         if (idle) {
           // (its columns of P and O^T are not looked at); looks at V are counted as the others count them
@@ -794,14 +794,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         }
         float vref = 0.f;
 #pragma unroll
+        for (int k = 0; k < kPg; ++k) vref = fmaxf(vref, cur.vs[k]);
+        vref = warp_max(vref);
+#pragma unroll
         for (int k = 0; k < kPg; ++k) {
           if (32 * k + lane < cur.n_blk) {
             it.ks[32 * k + lane] = cur.ks[k];
-            it.vs[32 * k + lane] = cur.vs[k];
-            vref = fmaxf(vref, cur.vs[k]);
+            // at most kWeightScale, however small the scales are
+            it.vs[32 * k + lane] = vref > 0.f ? cur.vs[k] / vref * kWeightScale : 0.f;
           }
         }
-        vref = warp_max(vref);
         if (lane == 0) it.vref = vref;
         fence_proxy_async_smem();
       }

@@ -269,7 +269,8 @@ ATTN_API attn_status attn_fwd_splitkv_noalloc(const void* q, const void* k_cache
  *            overlap the inputs.
  * Hkv = 0: q alone (k, k_out NULL).  The statistics are fp32, the result is
  * rounded once.  Constraints: B, Hq >= 1; N, Hkv >= 0 (Hkv need not divide
- * Hq); d in {64, 128}; tensors 16-byte aligned.
+ * Hq); d in {64, 128}; tensors 16-byte aligned; Hq + Hkv at most 2^20 and
+ * B * N * (Hq + Hkv) below 2^31 - 2^20.
  */
 ATTN_API attn_status attn_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
                                        const float* q_weight, const float* k_weight, float eps,

@@ -100,6 +100,24 @@ def test_scales_of_any_size(scale):
     _check(q, pools, scales, table, lens, scale, got, "scales")
 
 
+@pytest.mark.parametrize("size", [2.0 ** -120, 1e-41, 2.0 ** 60])
+def test_value_scales_at_the_ends_of_the_range(size):
+    """Value scales near the smallest normal number, below it, and large: o follows them."""
+    lens = [200]
+    g, pools, scales, table = _cache(1, 1, 128, 64, lens, 82)
+    q = torch.randn((1, 1, 4, 128), generator=g).to(torch.bfloat16)
+    scales[1] = torch.full_like(scales[1], size)
+    scales[1][table[0, 1]] *= 0.5
+    n = max(lens)
+    k, v = (S.paged_rows(p.view(torch.float8_e4m3fn).double() * s.double()[:, None, :, None], table, n)
+            for p, s in zip(pools, scales))
+    o, lse, eo, el = S.decode(q, k, v, lens, 0.09)
+    got = _run(q, pools, scales, table, lens, 0.09, 128)
+    # fp32 on the way: multiples of 2^-149 at the least, and bf16 below 2^-126 has steps of 2^-133
+    S.assert_within(got[0], o, eo + 2.0 ** -8 * (o.abs() + eo) + (2.0 ** -133 if size < 1 else 0), "o")
+    S.assert_within(got[1], lse, el, "lse")
+
+
 def test_zero_scales():
     """Pages whose scale is zero hold zeros: their keys score 0 and add nothing to o."""
     lens = [300]

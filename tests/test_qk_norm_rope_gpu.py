@@ -141,6 +141,48 @@ def test_in_place_q_alone_and_empty():
     assert _native.attn_get_device_status() == 0
 
 
+def test_in_place_long_and_odd_heads():
+    """Sizes that take the long form, in place, with head counts that four do not divide and that they do."""
+    for Hq, Hkv in ((9, 3), (16, 4)):
+        _, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(2, 1500, Hq, Hkv, 128, 128, 12, True, 0, 4000)
+        r = _gpu(rope)
+        want = _native.qk_norm_rope(qc, kc, wq.cuda(), wk.cuda(), 1e-6, r, pos.cuda())
+        _native.qk_norm_rope(qc, kc, wq.cuda(), wk.cuda(), 1e-6, r, pos.cuda(), out=(qc, kc))
+        assert torch.equal(qc, want[0]) and torch.equal(kc, want[1])
+        for x, wx, got in ((q, wq, want[0]), (k, wk, want[1])):
+            y, size = S.norm_rope(x, wx, 1e-6, cs, False)
+            S.assert_within(got, y, 2.0 ** -8 * y.abs() + 2.0 ** -20 * size, "rows")
+
+
+def test_one_norm_only_and_gradients_in_place():
+    """A norm on k alone (q rotated only), and the C call's gradients written over the incoming ones."""
+    B, N, Hq, Hkv, d = 2, 50, 6, 2, 128
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, 64, 13)
+    r, p = _gpu(rope), pos.cuda()
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+    dq, dk, dwq, dwk = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda(), None, kc, None, wk.cuda(), 1e-6, r, p)
+    assert dwq is None
+    dx, err, _, _ = S.norm_rope_bwd(gq, q, None, 1e-6, cs, False)
+    S.assert_within(dq, dx, 2.0 ** -8 * dx.abs() + err, "dq")
+    dx, err, dw, size = S.norm_rope_bwd(gk, k, wk, 1e-6, cs, False)
+    S.assert_within(dk, dx, 2.0 ** -8 * dx.abs() + err, "dk")
+    S.assert_within(dwk, dw, 2.0 ** -16 * size, "dwk")
+    full = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda(), qc, kc, wq.cuda(), wk.cuda(), 1e-6, r, p)
+    a, b = gq.cuda(), gk.cuda()
+    dw = [torch.empty(d, device="cuda") for _ in range(2)]
+    n = _native.attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    w = [t.cuda() for t in (wq, wk)]
+    st = torch.cuda.current_stream().cuda_stream
+    rc = _native.lib().attn_qk_norm_rope_bwd(
+        a.data_ptr(), b.data_ptr(), qc.data_ptr(), Hq * d, kc.data_ptr(), Hkv * d, w[0].data_ptr(), w[1].data_ptr(),
+        1e-6, r[0].data_ptr(), r[1].data_ptr(), r[0].shape[0], 64, 0, p.data_ptr(), a.data_ptr(), b.data_ptr(),
+        dw[0].data_ptr(), dw[1].data_ptr(), B, N, Hq, Hkv, d, ws.data_ptr(), n, st)
+    assert rc == 0
+    for got, want in zip((a, b, *dw), full):
+        assert torch.equal(got, want)
+
+
 def test_extreme_rows():
     """Rows of zeros, of the type's smallest and of large values; a row with NaN or an infinity spoils itself only."""
     d = 128
