@@ -81,6 +81,7 @@ constexpr int kThreads = 256;
 
 template <int D, int kHeads, bool kInter>
 __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const AppendParams p, int per) {
+  grid_depends();
   constexpr int kTPR = D / 16;
   const int l = threadIdx.x % kTPR;
   const int b = blockIdx.y;
@@ -201,6 +202,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 // - / 79 / 83.
 template <int D, int kBlock, int kKeep, bool kInter>
 __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(const AppendParams p) {
+  grid_depends();
   constexpr int kTPR = D / 16;
   constexpr int kRows = kBlock / kTPR;  // rows a round of the block covers
   const int b = blockIdx.y;
@@ -349,20 +351,14 @@ cudaError_t launch_bf16(const AppendParams& p, cudaStream_t stream) {
   // one block at least: it writes seqlens_out
   const long long blocks = threads > 0 ? (threads + kThreads - 1) / kThreads : 1;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B));
-  if (p.rope.inter)
-    append_bf16_kernel<D, kHeads, true><<<grid, kThreads, 0, stream>>>(p, per);
-  else
-    append_bf16_kernel<D, kHeads, false><<<grid, kThreads, 0, stream>>>(p, per);
-  return cudaGetLastError();
+  return p.rope.inter ? launch_dependent(append_bf16_kernel<D, kHeads, true>, grid, kThreads, 0, stream, p, per)
+                      : launch_dependent(append_bf16_kernel<D, kHeads, false>, grid, kThreads, 0, stream, p, per);
 }
 
 template <int D, int kBlock, int kKeep>
 cudaError_t launch_e4m3_as(const AppendParams& p, dim3 grid, cudaStream_t stream) {
-  if (p.rope.inter)
-    append_e4m3_kernel<D, kBlock, kKeep, true><<<grid, kBlock, 0, stream>>>(p);
-  else
-    append_e4m3_kernel<D, kBlock, kKeep, false><<<grid, kBlock, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.rope.inter ? launch_dependent(append_e4m3_kernel<D, kBlock, kKeep, true>, grid, kBlock, 0, stream, p)
+                      : launch_dependent(append_e4m3_kernel<D, kBlock, kKeep, false>, grid, kBlock, 0, stream, p);
 }
 
 template <int D>

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const uint32_t sQ = smem_u32(smem + C::kOffQ), sP = smem_u32(smem + C::kOffP);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_k);
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     // rest.
     // launched as a programmatic dependent of whatever ran before: nothing of
     // that is read before this wait
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const int n_rblk = static_cast<int>(p.n_rblk.d), H = static_cast<int>(p.H.d), G = static_cast<int>(p.G.d);
     bool full_phase = true;
     int b0 = -32;
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   } else {
     // ================================================================ loads
     if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      grid_wait();
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const Item<R>& it = items[n % C::kItems];
@@ -985,10 +985,10 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qrow = blockIdx.x / kBlocks, col0 = blockIdx.x % kBlocks * kCols;
   const int bi = qrow / p.Hq, hq = qrow - bi * p.Hq, b = bi / p.Nq, i = bi - b * p.Nq;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   // launched as a programmatic dependent of the split kernel: wait until all
   // of its partials are written and visible
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   int Lb = p.seqlens[b];
   Lb = Lb < 0 ? 0 : (Lb > p.max_seqlen ? p.max_seqlen : Lb);
   const int ns = (Lb + p.chunk - 1) / p.chunk;
@@ -1059,24 +1059,6 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const D
     p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + i] = none ? -INFINITY : mx + logf(sum);
 }
 
-// A launch that may start while the kernel before it ends (that kernel's
-// results are waited for on the device).
-template <typename P>
-cudaError_t launch_dependent(void (*kern)(const P), unsigned grid, unsigned block, int smem, const P& p,
-                             cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <int D, int R>
 cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream) {
   using C = Cfg<D, R>;
@@ -1100,16 +1082,14 @@ cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream
   p.G = FastDiv(p.Hq / p.Hkv);
   p.page = FastDiv(p.page_size);
   p.split = FastDiv(p.chunk);
-  e = launch_dependent<DecodeFp8Params>(kern, static_cast<unsigned>(items < ctas ? items : ctas), C::kThreads, C::kAlloc,
-                                        p, stream);
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(items < ctas ? items : ctas)), C::kThreads, C::kAlloc, stream, p);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const DecodeFp8CombineParams c = {p.o_part, p.lse_part, p.seqlens, p.o, p.lse, p.Nq, p.Hq, p.max_seqlen, p.chunk,
                                     p.n_split};
   const unsigned q_rows = static_cast<unsigned>(p.B) * p.Nq * p.Hq;
   if (q_rows >= 2u * sms || p.n_split <= 32)
-    return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, D, 8, 4>, q_rows, 256, 0, c, stream);
-  return launch_dependent<DecodeFp8CombineParams>(decode_fp8_combine_kernel<D, 32, 32, 8>, q_rows * (D / 32), 1024, 0, c,
-                                                  stream);
+    return launch_dependent(decode_fp8_combine_kernel<D, D, 8, 4>, dim3(q_rows), 256, 0, stream, c);
+  return launch_dependent(decode_fp8_combine_kernel<D, 32, 32, 8>, dim3(q_rows * (D / 32)), 1024, 0, stream, c);
 }
 
 template <int D>

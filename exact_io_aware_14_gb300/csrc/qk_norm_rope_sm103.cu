@@ -62,6 +62,7 @@ __device__ __forceinline__ float row_sum(float v) {
 // then its k heads).
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormRopeParams p, long long rows) {
+  grid_depends();
   constexpr int kTPR = D / 16;
   const int l = threadIdx.x % kTPR;
   const long long i = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTPR;
@@ -132,6 +133,7 @@ struct LongPlan {
 template <int D, int kHeads, int kMinBlocks, bool kInter, bool kBwd, bool kStream>
 __global__ void __launch_bounds__(kThreads, kMinBlocks)
     qk_norm_rope_long_kernel(const QkNormRopeParams p, const LongPlan plan) {
+  grid_depends();
   constexpr int kTPR = D / 16;
   constexpr int kGroups = kThreads / kTPR;
   const bool is_k = static_cast<int>(blockIdx.x) >= plan.q.blocks;
@@ -306,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
 template <int D>
 __global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const float* part, int nbq, int nbk, float* dwq,
                                                                float* dwk) {
+  grid_depends();
   const bool is_k = blockIdx.x >= D / 32;
   float* out = is_k ? dwk : dwq;
   if (!out) return;
@@ -367,17 +370,15 @@ cudaError_t launch_long(const QkNormRopeParams& p, cudaStream_t stream) {
   const LongPlan plan = plan_long(p.B, p.N, p.Hq, p.Hkv, p.d, kHeads);
   // tensors past L2's 129 MB together (172 MB in, 172 MB out: 56.2 us streamed, 58.1 not)
   const bool past_l2 = static_cast<double>(p.B) * p.N * (p.Hq + p.Hkv) * D * 2 * (kBwd ? 3 : 2) > 129e6;
-  if (past_l2)
-    qk_norm_rope_long_kernel<D, kHeads, kCtasPerSm, kInter, kBwd, true>
-        <<<plan.q.blocks + plan.k.blocks, kThreads, 0, stream>>>(p, plan);
-  else
-    qk_norm_rope_long_kernel<D, kHeads, kCtasPerSm, kInter, kBwd, false>
-        <<<plan.q.blocks + plan.k.blocks, kThreads, 0, stream>>>(p, plan);
-  cudaError_t e = cudaGetLastError();
+  const dim3 grid(plan.q.blocks + plan.k.blocks);
+  cudaError_t e =
+      past_l2 ? launch_dependent(qk_norm_rope_long_kernel<D, kHeads, kCtasPerSm, kInter, kBwd, true>, grid, kThreads, 0,
+                                 stream, p, plan)
+              : launch_dependent(qk_norm_rope_long_kernel<D, kHeads, kCtasPerSm, kInter, kBwd, false>, grid, kThreads, 0,
+                                 stream, p, plan);
   if (!kBwd || e != cudaSuccess || (!p.dq_weight && !p.dk_weight)) return e;
-  qk_norm_rope_dw_kernel<D>
-      <<<2 * (D / 32), 1024, 0, stream>>>(p.dw_part, plan.q.blocks, plan.k.blocks, p.dq_weight, p.dk_weight);
-  return cudaGetLastError();
+  return launch_dependent(qk_norm_rope_dw_kernel<D>, dim3(2 * (D / 32)), 1024, 0, stream, p.dw_part, plan.q.blocks,
+                          plan.k.blocks, p.dq_weight, p.dk_weight);
 }
 
 template <int D, bool kInter>
@@ -387,8 +388,7 @@ cudaError_t launch_fwd(const QkNormRopeParams& p, cudaStream_t stream) {
     return fwd_heads(p.Hq, p.Hkv) == 4 ? launch_long<D, 4, kInter, false>(p, stream)
                                        : launch_long<D, 1, kInter, false>(p, stream);
   const unsigned blocks = static_cast<unsigned>((rows * (D / 16) + kThreads - 1) / kThreads);
-  qk_norm_rope_kernel<D, kInter><<<blocks, kThreads, 0, stream>>>(p, rows);
-  return cudaGetLastError();
+  return launch_dependent(qk_norm_rope_kernel<D, kInter>, dim3(blocks), kThreads, 0, stream, p, rows);
 }
 
 }  // namespace
