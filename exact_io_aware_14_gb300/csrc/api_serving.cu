@@ -237,19 +237,24 @@ attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_stride, con
                 Hkv, d, stream);
 }
 
-// Keys per CTA of the kernel's grid, in one or two rounds of equal splits of
-// at most 1024 keys; beyond that splits of 1024 (2048 where there are many
-// rounds anyway).  Measured on GB300: a
-// serving batch (16 sequences of 1 to 16 K keys, 8 KV heads) 56.7 us with
-// splits of 384, 55.1 with 768 and 1024; two sequences of 256 K keys 195, 182
-// and 173 us with 512, 1024 and 2048; one of 701 keys 8.4 us with 128 and 9.9
-// with 1024 (one split).
+// Few sequences: as many splits as a cluster holds, where those are short (one
+// of 701 keys, 8 KV heads: 8.0 us by two kernels, 7.1 in a cluster).  Else the
+// keys per CTA of the grid, in one or two rounds of equal splits of at most
+// 1024 keys; beyond that splits of 1024 (2048 where there are many rounds
+// anyway).  Measured on GB300: a serving batch (16 sequences of 1 to 16 K keys,
+// 8 KV heads) 56.0 us with splits of 384, 53.7 with 1024; two sequences of 256
+// K keys 192, 177 and 172 us with 512, 1024 and 2048.
 int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen) {
   if (B < 1 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_seqlen < 1) return 0;
   const long long rows = static_cast<long long>(Nq) * (Hq / Hkv);
   const long long ctas = rows <= 4 ? 304 : 152;
-  const double keys = static_cast<double>(B) * Hkv * static_cast<double>((rows + 15) / 16 < (rows + 23) / 24 ? (rows + 15) / 16 : (rows + 23) / 24) *
-                      max_seqlen / ctas;
+  const long long blocks = (rows + 15) / 16 < (rows + 23) / 24 ? (rows + 15) / 16 : (rows + 23) / 24;
+  const double groups = static_cast<double>(B) * Hkv * blocks;
+  for (int splits = 8; splits > 1; splits /= 2) {
+    const int chunk = static_cast<int>((static_cast<long long>(max_seqlen) + 64 * splits - 1) / (64 * splits)) * 64;
+    if (groups * splits <= ctas && chunk <= 512) return chunk < 128 ? 128 : chunk;
+  }
+  const double keys = groups * max_seqlen / ctas;
   const double most = keys > 8192 ? 2048 : 1024;
   const double rounds = keys > 2048 ? keys / most : std::ceil(keys / most);
   const double chunk = std::ceil(keys / (rounds < 1 ? 1 : rounds) / 128) * 128;

@@ -43,6 +43,10 @@
 //              (pages are multiples of 64 rows)
 // Two tiles of S, P and O are in flight.
 //
+// Where the splits of a group of rows are two to eight and all CTAs fit the GPU
+// at once, they form a cluster instead, a CTA a split, and combine their
+// results through distributed shared memory: no second kernel.
+//
 // Combine kernel: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.
 #include <atomic>
 
@@ -282,6 +286,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     }
     fence_proxy_async_smem();
   }
+  // clustered: this split's result, in the place of the first stages
+  float* s_part = reinterpret_cast<float*>(smem);
+  float* s_part_lse = s_part + R * D;
+  int* s_part_row = reinterpret_cast<int*>(s_part_lse + R);  // rows of o, then entries of lse
+  static_assert((R * D + 3 * R) * 4 <= C::kStages * C::kStage, "a split's result fits the stages");
+
   uint32_t tmem = 0u;  // S at columns 0, kN; O^T at 2 kN, 3 kN
   if (warp != kItemWarp) {  // it looks for its first item before it meets the others there
     tc_fence_before();
@@ -524,6 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         if (!ok || !wait_all(bar_ml + (n & 1), (n >> 1) & 1, abort_flag, 11)) break;
         const float* ml = s_ml + (n & 1) * 5 * R;
         const int split = it.split;
+        const bool clustered = p.cluster != 0;
         const bool direct = it.direct != 0;
         const float osc = it.vref * (1.f / kWeightScale);
         // what the slot holds is read before it is given back; rows are in order,
@@ -547,6 +558,16 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+          if (clustered) {
+            // over the stages, whose last tile has been multiplied
+            s_part[r * D + dd] = acc[r];
+            if (dd == r) {
+              s_part_lse[r] = lse[r];
+              s_part_row[r] = o_row[r];
+              s_part_row[R + r] = lse_row;
+            }
+            continue;
+          }
           if (o_row[r] < 0) break;
           if (direct) {
             static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(o_row[r]) * D + dd] = __float2bfloat16_rn(acc[r]);
@@ -631,10 +652,35 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       float ks[kPg], vs[kPg];
       uint4 q[kAhead ? kDims / 8 : 1];
     };
-    bool more = next_block();
+    // Clustered: one item a CTA, split by rank, nothing to look for (empty
+    // splits are items too: the cluster's combine wants them all).
+    bool more = p.cluster ? true : next_block();
     unsigned item = blockIdx.x;
     auto find = [&]() {
       Found f;
+      if (p.cluster) {
+        const unsigned g = blockIdx.x / p.cluster, h = p.H.div(g) * p.H.d;
+        f.more = item == blockIdx.x;
+        item += gridDim.x;
+        f.b = p.H.div(g);
+        f.hkv = p.n_rblk.div(g - h);
+        f.row0 = (static_cast<int>(g - h) - f.hkv * n_rblk) * R;
+        f.split = blockIdx.x % p.cluster;
+        f.len = p.seqlens[f.b];
+        if (f.len < 0 || f.len > p.max_seqlen) {
+          record(1, kDevBadSeqlen);
+          f.len = f.len < 0 ? 0 : p.max_seqlen;
+        }
+        const int k0 = f.split * p.chunk, n_blk = f.more ? (min(p.chunk, f.len - k0) + 63) / 64 : 0;
+#pragma unroll
+        for (int k = 0; k < kPg; ++k) {
+          const int blk = 32 * k + lane;
+          f.pg[k] = blk < n_blk
+                        ? p.block_table[static_cast<long long>(f.b) * p.max_blocks + p.page.div(k0 + 64 * blk)]
+                        : 0;
+        }
+        return f;
+      }
       const unsigned j = p.H.div(item), h = item - j * H;
       item += gridDim.x;  // fits: the host sees to it
       while (more && j >= before + total) {
@@ -678,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       Item<R>& it = items[slot];
       a.more = f.more;
       a.k0 = f.split * p.chunk;
-      a.kn = min(p.chunk, f.len - a.k0);
+      a.kn = max(0, min(p.chunk, f.len - a.k0));
       a.n_blk = (a.kn + 63) / 64;
       a.len = f.len;
       a.b = f.b;
@@ -967,6 +1013,47 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
+  if (p.cluster == 0) return;
+  if (*abort_flag) {  // there may be no result: this CTA writes none (the others' are as undefined, and reported)
+    for (int r = tid; r < R; r += C::kThreads) s_part_row[r] = -1;
+    __syncthreads();
+  }
+  // Combine within the cluster, through the CTAs' shared memory: rank k takes
+  // rows k, k + cluster, ...  The arithmetic, in its order, is the combine
+  // kernel's (which has at most one split a warp for so few), so the same
+  // splits give the same bits either way.
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  auto peer = [](const void* at, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+  };
+  for (int i = tid; i < R * D; i += C::kThreads) {
+    const int r = i / D, dd = i % D;
+    if (r % p.cluster != static_cast<int>(blockIdx.x % p.cluster) || s_part_row[r] < 0) continue;
+    float lv[8], mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      lv[k] = k < p.n_split ? peer(s_part_lse + r, k) : -INFINITY;
+      mx = fmaxf(mx, lv[k]);
+    }
+    if (mx == -INFINITY) mx = 0.f;
+    float a = 0.f, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = expf(lv[k] - mx);
+      sum = __fadd_rn(sum, w);
+      a = __fadd_rn(a, __fmul_rn(w, k < p.n_split ? peer(s_part + i, k) : 0.f));
+    }
+    const bool none = sum == 0.f;
+    static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(s_part_row[r]) * D + dd] =
+        __float2bfloat16_rn(none ? 0.f : a / sum);
+    if (dd == 0) p.lse[s_part_row[R + r]] = none ? -INFINITY : mx + logf(sum);
+  }
+  // the others may still read this CTA's shared memory
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s for each row of q.
@@ -1082,6 +1169,17 @@ cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream
   p.G = FastDiv(p.Hq / p.Hkv);
   p.page = FastDiv(p.page_size);
   p.split = FastDiv(p.chunk);
+  // Few splits and few of them in all: the splits of a group of rows form a
+  // cluster, which combines them itself; all CTAs are resident at once.
+  int cluster = 1;
+  while (cluster < p.n_split) cluster *= 2;
+  const long long clustered = items / p.n_split * cluster;
+  if (p.n_split > 1 && cluster <= 8 && clustered <= ctas) {
+    p.cluster = cluster;
+    return launch_dependent_clusters(kern, dim3(static_cast<unsigned>(clustered)), cluster, C::kThreads, C::kAlloc,
+                                     stream, p);
+  }
+  p.cluster = 0;
   e = launch_dependent(kern, dim3(static_cast<unsigned>(items < ctas ? items : ctas)), C::kThreads, C::kAlloc, stream, p);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const DecodeFp8CombineParams c = {p.o_part, p.lse_part, p.seqlens, p.o, p.lse, p.Nq, p.Hq, p.max_seqlen, p.chunk,

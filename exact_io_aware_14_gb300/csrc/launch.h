@@ -17,22 +17,32 @@ enum DeviceCode : uint32_t { kDevOk = 0, kDevTimeout = 5, kDevBadSeqlen = 6, kDe
                              kDevBadPosition = 8 };
 
 // A launch that may start while the kernel before it on the stream ends.  Such
-// kernels (grid_depends below) wait on the device until that kernel is done
-// and its writes are visible, before they read or write global memory.
+// kernels (grid_depends in ptx.cuh) wait on the device until that kernel is
+// done and its writes are visible, before they read or write global memory.
+// cluster: blocks of a cluster along x.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, int smem, cudaStream_t stream,
-                             const A&... args) {
+cudaError_t launch_dependent_clusters(void (*kern)(P...), dim3 grid, int cluster, unsigned block, int smem,
+                                      cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, int smem, cudaStream_t stream,
+                             const A&... args) {
+  return launch_dependent_clusters(kern, grid, 1, block, smem, stream, args...);
 }
 
 struct PrefillParams {
@@ -166,6 +176,7 @@ struct DecodeFp8Params {
   // KV heads, heads of a group, page size, split length
   int rows;
   FastDiv n_rblk, H, G, page, split;
+  int cluster;  // CTAs of a cluster, one a split (0: no clusters)
 };
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream);
 

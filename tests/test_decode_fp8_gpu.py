@@ -176,6 +176,25 @@ def test_splits_and_repeats():
     assert _native.attn_get_device_status() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,Nq,d", [(4, 1, 1, 128), (8, 1, 1, 64), (16, 1, 1, 128), (18, 1, 1, 64), (6, 2, 2, 64)])
+@pytest.mark.parametrize("cap,chunk", [(128, 64), (192, 64), (320, 64), (512, 64), (640, 128)])
+def test_clusters_of_splits(Hq, Hkv, Nq, d, cap, chunk):
+    """Two to eight splits that one cluster takes (ranks beyond the splits, splits behind a sequence's end, sequences
+    without a key), against 64 bits and, bit for bit, the same splits among so many sequences that the combine
+    kernel merges them."""
+    lens = [cap, 1, 0, cap - 65, 64]
+    g, pools, scales, table = _cache(5, Hkv, d, 64, lens, 83 + cap, cap=cap)
+    q = torch.randn((5, Nq, Hq, d), generator=g).to(torch.bfloat16)
+    got = _run(q, pools, scales, table, lens, 0.1, chunk)
+    assert _native.attn_get_device_status() == 0
+    _check(q, pools, scales, table, lens, 0.1, got, "clusters")
+    many = 64
+    big = _run(q.repeat(many, 1, 1, 1), pools, scales, table.repeat(many, 1), lens * many, 0.1, chunk)
+    for a, b in zip(big, got):
+        assert torch.equal(a.view(many, 5, *a.shape[1:]), b.expand(many, *b.shape))
+    assert _native.attn_get_device_status() == 0
+
+
 @pytest.mark.parametrize("B", [33, 70, 300])
 def test_many_sequences(B):
     g0 = torch.Generator().manual_seed(B)
