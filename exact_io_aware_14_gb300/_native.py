@@ -261,7 +261,8 @@ def attn_fwd_splitkv_noalloc(q, k_cache, v_cache, seqlens, o, lse, scale, chunk,
 
 # --------------------------------------------------------------------------- operators around the attention kernels
 # These calls are launched once or more a layer and token, where the host's time for a call counts: each argument is
-# looked at once, with the cheapest query that settles it, and the stream is asked for as a handle.
+# looked at once, with the cheapest query that settles it, and the stream is asked for as a handle.  With `stream`, what
+# a call allocates belongs to that stream; the caller keeps the tensors it passes until the stream has passed the call.
 _BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 _fns = {}
 
@@ -284,6 +285,21 @@ def _call(name, dev, stream, *args):
             rc = _fn(name)(*args, handle)
     if rc != ATTN_OK:
         raise AttnError(rc, name)
+
+
+def _on(stream, dev):
+    """Makes `stream` current for a call that allocates: what it allocates is then that stream's, not reused before
+    the stream has passed the call."""
+    if stream.device_index != dev:
+        raise ValueError("the stream is one of cuda:%d, the tensors are on cuda:%d" % (stream.device_index, dev))
+    return torch.cuda.stream(stream)
+
+
+def _space(workspace, dev):
+    """(address, bytes) of a workspace that the caller brought."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on cuda:%d (got one on %s)" % (dev, workspace.device))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _need(name, t, dtype, shape, dev):
@@ -348,6 +364,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, 
     rope: (cos, sin) from rope_table, or None; positions int32 [B,N], or None for 0 .. N-1; out: (q_out, k_out) to
     write to (q and k themselves where dense), or None.  Returns (q_out, k_out)."""
     dev = _cuda_device(q)
+    if stream is not None:
+        with _on(stream, dev):
+            return qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, interleaved, out)
     q_shape = q.shape
     B, N, Hq, d = q_shape
     Hkv = 0 if k is None else k.shape[2]
@@ -379,6 +398,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps=1e-6, rope=No
     arguments its own (q, k may be None without a norm).  Returns (dq, dk, dq_weight, dk_weight), None where there
     is nothing to differentiate."""
     dev = _cuda_device(dq_out)
+    if stream is not None:
+        with _on(stream, dev):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps, rope, positions, interleaved,
+                                    workspace)
     B, N, Hq, d = dq_out.shape
     Hkv = 0 if dk_out is None else dk_out.shape[2]
     gq = _need("dq_out", dq_out, _BF16, (B, N, Hq, d), dev)
@@ -394,9 +417,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps=1e-6, rope=No
         if workspace is None:
             nbytes = _fn("attn_qk_norm_rope_bwd_workspace_size")(B, N, Hq, Hkv, d)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        else:
-            nbytes = workspace.numel() * workspace.element_size()
-        ws = workspace.data_ptr()
+        ws, nbytes = _space(workspace, dev)
     pos = None if positions is None else _need("positions", positions, _I32, (B, N), dev)
     _call("attn_qk_norm_rope_bwd", dev, stream, gq, gk, qp, qs, kp, ks, _weight("q_weight", q_weight, d, dev),
           _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, dq.data_ptr(),
@@ -455,6 +476,10 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqle
     fp32 scales [num_pages, Hkv] (attn_fwd_splitkv_paged_fp8); chunk None: attn_splitkv_fp8_chunk's.
     Returns (o, lse [B,Hq,Nq])."""
     dev = _cuda_device(q)
+    if stream is not None:
+        with _on(stream, dev):
+            return decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens, scale, chunk,
+                                    workspace)
     q_shape, pools = q.shape, k_pages.shape
     B, Nq, Hq, d = q_shape
     num_pages, page_size, Hkv = pools[:3]
@@ -474,10 +499,9 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqle
     if workspace is None:
         n = _fn("attn_splitkv_workspace_size")(B, Nq * Hq, cap, d, chunk)
         workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
-    else:
-        n = workspace.numel() * workspace.element_size()
+    ws, n = _space(workspace, dev)
     _call("attn_fwd_splitkv_paged_fp8", dev, stream, *args, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
-          scale, chunk, workspace.data_ptr(), n)
+          scale, chunk, ws, n)
     return o, lse
 
 

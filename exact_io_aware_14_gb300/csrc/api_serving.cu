@@ -17,6 +17,20 @@ constexpr double kLog2e = 1.4426950408889634;
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
+// Memory from the first to the last element of a tensor; empty where p is NULL.
+struct Extent {
+  uintptr_t at, end;
+};
+Extent bytes_at(const void* p, long long n) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, p && n > 0 ? at + static_cast<uintptr_t>(n) : at};
+}
+// bf16 rows of `width` elements, `stride` (below 2^31) elements apart
+Extent rows_at(const void* p, long long rows, long long stride, long long width) {
+  return bytes_at(p, rows > 0 ? 2 * ((rows - 1) * stride + width) : 0);
+}
+bool overlap(const Extent& a, const Extent& b) { return a.at < b.end && b.at < a.end; }
+
 attn_status check_rope(const float* cosv, const float* sinv, int max_pos, int rot_dim, int interleaved, int d) {
   if (rot_dim < 0 || rot_dim > d || interleaved < 0 || interleaved > 1) return ATTN_ERR_INVALID_ARG;
   if (rot_dim == 0) return ATTN_OK;
@@ -36,6 +50,7 @@ attn_status check_rows(const void* x, long long stride, int H, int d, bool read)
   if (!read) return ATTN_OK;
   if (!x || stride < static_cast<long long>(H) * d) return ATTN_ERR_INVALID_ARG;
   if (stride % 8 != 0 || off16(x)) return ATTN_ERR_MISALIGNED;
+  if (stride > kIntMax) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -63,7 +78,6 @@ attn_status check_append(const void* k, long long k_stride, const void* v, long 
   if ((static_cast<long long>(Nn) / page_size + 2) * Hkv > kIntMax) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(Nn) * Hkv * (d / 16) > kIntMax * 256) return ATTN_ERR_UNSUPPORTED;
   if (!seqlens || !block_table || !k_pages || !v_pages) return ATTN_ERR_INVALID_ARG;
-  if (seqlens_out && seqlens_out == seqlens) return ATTN_ERR_INVALID_ARG;
   if (Nn > 0) {
     attn_status st = check_rows(k, k_stride, Hkv, d, true);
     if (st == ATTN_OK) st = check_rows(v, v_stride, Hkv, d, true);
@@ -72,6 +86,9 @@ attn_status check_append(const void* k, long long k_stride, const void* v, long 
   if (off16(k_pages) || off16(v_pages) || off4(block_table) || off4(seqlens) || (new_lens && off4(new_lens)) ||
       (seqlens_out && off4(seqlens_out)))
     return ATTN_ERR_MISALIGNED;
+  const Extent lens_out = bytes_at(seqlens_out, 4LL * B);
+  if (overlap(lens_out, bytes_at(seqlens, 4LL * B)) || overlap(lens_out, bytes_at(new_lens, 4LL * B)))
+    return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -126,12 +143,18 @@ attn_status attn_qk_norm_rope(const void* q, long long q_stride, const void* k, 
   if (st == ATTN_OK) st = check_rows(k, k_stride, Hkv, d, Hkv > 0);
   if (st != ATTN_OK) return st;
   if (!q_out || (Hkv > 0 && !k_out)) return ATTN_ERR_INVALID_ARG;
-  // in place only where the rows lie as the output's
-  if ((q_out == q && q_stride != static_cast<long long>(Hq) * d) ||
-      (Hkv > 0 && k_out == k && k_stride != static_cast<long long>(Hkv) * d))
-    return ATTN_ERR_INVALID_ARG;
   if (off16(q_out) || (Hkv > 0 && off16(k_out)) || off16(q_weight) || off16(k_weight) || off4(positions))
     return ATTN_ERR_MISALIGNED;
+  // over an input only in place, where its rows lie as the output's
+  const long long tokens = static_cast<long long>(B) * N, q_width = static_cast<long long>(Hq) * d,
+                  k_width = static_cast<long long>(Hkv) * d;
+  const bool q_same = q_out == q && q_stride == q_width, k_same = k_out == k && k_stride == k_width;
+  const Extent qi = rows_at(q, tokens, q_stride, q_width), ki = rows_at(Hkv ? k : nullptr, tokens, k_stride, k_width),
+               qo = rows_at(q_out, tokens, q_width, q_width),
+               ko = rows_at(Hkv ? k_out : nullptr, tokens, k_width, k_width);
+  if ((!q_same && overlap(qo, qi)) || (!k_same && overlap(ko, ki)) || overlap(qo, ki) || overlap(ko, qi) ||
+      overlap(qo, ko))
+    return ATTN_ERR_INVALID_ARG;
   attn::QkNormRopeParams p;
   std::memset(&p, 0, sizeof p);
   p.q = q;
@@ -187,6 +210,21 @@ attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const 
   if (norm && (!workspace || off16(workspace) ||
                workspace_bytes < attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d)))
     return ATTN_ERR_WORKSPACE;
+  if (N > 0) {
+    // over the outputs' gradients only in place, over q and k not at all
+    const long long tokens = static_cast<long long>(B) * N, q_width = static_cast<long long>(Hq) * d,
+                    k_width = static_cast<long long>(Hkv) * d;
+    const Extent qi = rows_at(q_weight ? q : nullptr, tokens, q_stride, q_width),
+                 ki = rows_at(k_weight ? k : nullptr, tokens, k_stride, k_width),
+                 gq = rows_at(dq_out, tokens, q_width, q_width),
+                 gk = rows_at(Hkv ? dk_out : nullptr, tokens, k_width, k_width),
+                 dqo = rows_at(dq, tokens, q_width, q_width),
+                 dko = rows_at(Hkv ? dk : nullptr, tokens, k_width, k_width);
+    if ((dq != dq_out && overlap(dqo, gq)) || (dk != dk_out && overlap(dko, gk)) || overlap(dqo, gk) ||
+        overlap(dko, gq) || overlap(dqo, dko) || overlap(dqo, qi) || overlap(dqo, ki) || overlap(dko, qi) ||
+        overlap(dko, ki))
+      return ATTN_ERR_INVALID_ARG;
+  }
   attn::QkNormRopeParams p;
   std::memset(&p, 0, sizeof p);
   p.q = q;
@@ -285,14 +323,14 @@ attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const
   if (!workspace || off16(workspace) ||
       workspace_bytes < attn_splitkv_workspace_size(B, Nq * Hq, max_seqlen, d, chunk))
     return ATTN_ERR_WORKSPACE;
+  const long long rows = static_cast<long long>(B) * Nq * Hq;
+  if (overlap(bytes_at(q, 2 * rows * d), bytes_at(o, 2 * rows * d))) return ATTN_ERR_INVALID_ARG;
   attn::DecodeFp8Params p;
   std::memset(&p, 0, sizeof p);
   if (!attn::make_map_e4m3(&p.tm_k, k_pages, num_pages, page_size, Hkv, d, 64) ||
       !attn::make_map_e4m3(&p.tm_v, v_pages, num_pages, page_size, Hkv, d, 64))
     return ATTN_ERR_LAUNCH;
   p.q = q;
-  p.k_pages = k_pages;
-  p.v_pages = v_pages;
   p.k_scales = k_scales;
   p.v_scales = v_scales;
   p.block_table = block_table;

@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
   if (threadIdx.x == 0) *scale = now;
   if (lo > 0 && now != was) {
     const float f = was * inv;
-    for (int i = threadIdx.x; i < lo * (D / 16); i += kBlock) {
-      uint4* q = reinterpret_cast<uint4*>(dst + static_cast<long long>(i / (D / 16)) * pitch + (i % (D / 16)) * 16);
+    for (long long i = threadIdx.x; i < static_cast<long long>(lo) * (D / 16); i += kBlock) {
+      uint4* q = reinterpret_cast<uint4*>(dst + i / (D / 16) * pitch + i % (D / 16) * 16);
       uint4 u = *q;
       u.x = rescale4(u.x, f);
       u.y = rescale4(u.y, f);

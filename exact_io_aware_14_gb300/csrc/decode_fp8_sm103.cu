@@ -29,17 +29,17 @@
 // counter evened that out, but clearing the counter took a launch, and the
 // two cancelled: 55.1 and 56.9 us on a serving batch, 182 and 181 us on two
 // sequences of 256 K keys).
-// Eleven warps a CTA:
-//   warps 0-3  softmax, a thread a key (TMEM lane): scales, running
-//              reference, weights, their three terms as bytes into shared
-//              memory
-//   warps 4-7  output, a thread a dim: adds each tile's O^T columns to its
+// The warps of a CTA, in this order:
+//   softmax    one to three groups of four warps, a thread a key (TMEM lane):
+//              scales, running reference, weights, their three terms as bytes
+//              into shared memory
+//   output     four warps, a thread a dim: adds each tile's O^T columns to its
 //              fp32 registers (so no rescaling in TMEM)
-//   warp 8     items: finds them from the lengths, fetches their pages and
+//   items      one warp: finds them from the lengths, fetches their pages and
 //              scales, turns q into e5m2 terms, up to kItems ahead
-//   warp 9     TMEM, MMA issue: S of the next tile goes out before O of this
-//              one where its K is there
-//   warp 10    TMA loads, 128 keys of K and V a stage, in boxes of 64 rows
+//   MMA        one warp: TMEM, MMA issue; S of the next tile goes out before O
+//              of this one where its K is there
+//   loads      one warp: TMA, 128 keys of K and V a stage, in boxes of 64 rows
 //              (pages are multiples of 64 rows)
 // Two tiles of S, P and O are in flight.
 //
@@ -75,8 +75,9 @@ struct Cfg {
   static constexpr int kN = (3 * R + 15) / 16 * 16;  // MMA columns
   static constexpr int kTmem = kN <= 16 ? 64 : (kN <= 32 ? 128 : (kN <= 64 ? 256 : 512));  // 4 kN, a power of two
   static constexpr int kCtas = R == 4 ? 2 : 1;                          // per SM
-  // softmax groups of four warps, each with its own kRows of the rows: one
-  // group takes about 0.06 us a row and tile, 0.72 us is a tile's time at HBM rate
+  // softmax groups of four warps, each with its own kRows of the rows: a group
+  // takes about 0.5 us for a tile of four rows and 1 us for eight; at HBM rate
+  // a tile of d = 128 arrives every 0.72 us on an SM
   static constexpr int kGroups = R == 4 ? 1 : (R == 24 ? 3 : 2);
   static constexpr int kRows = R / kGroups;
   static constexpr int kSoftWarps = 4 * kGroups;
@@ -229,10 +230,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   uint64_t* bar_ready = bar_pages + C::kItems;   // [kItems] its scales and q too
   uint64_t* bar_free = bar_ready + C::kItems;    // [kItems] its readers are done (softmax, output, MMA, loads)
   uint64_t* bar_s = bar_free + C::kItems;        // [2] S of a tile in TMEM
-  uint64_t* bar_p = bar_s + 2;                   // [2] P of a tile in shared memory (4 softmax warps)
+  uint64_t* bar_p = bar_s + 2;                   // [2] P of a tile in shared memory (the softmax warps)
   uint64_t* bar_o = bar_p + 2;                   // [2] O^T of a tile in TMEM
   uint64_t* bar_of = bar_o + 2;                  // [2] O^T and alpha read (D / 32 output warps)
-  uint64_t* bar_ml = bar_of + 2;                 // [2] an item's m and l are there (4 softmax warps)
+  uint64_t* bar_ml = bar_of + 2;                 // [2] an item's m and l are there (the softmax warps)
   uint64_t* bar_mf = bar_ml + 2;                 // [2] they were read (D / 32 output warps)
   uint64_t* bar_sp = bar_mf + 2;                 // [2] group 0's look at the V rows that some rows do not see
   uint64_t* bar_drain = bar_sp + 2;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           ok = wait_all(bar_p + buf, (g >> 1) & 1, abort_flag, 9) && wait_all(bar_o + buf, (g >> 1) & 1, abort_flag, 10);
           if (!ok) break;
           tc_fence_after();
-            constexpr int kLd = (3 * kRows + 7) / 8 * 8;
+          constexpr int kLd = (3 * kRows + 7) / 8 * 8;
           const uint32_t o_at = tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN;
 #pragma unroll
           for (int q = 0; q < C::kGroups; ++q) {

@@ -159,8 +159,6 @@ struct DecodeFp8CombineParams {
 struct DecodeFp8Params {
   CUtensorMap tm_k, tm_v;
   const void* q;
-  const void* k_pages;
-  const void* v_pages;
   const float* k_scales;
   const float* v_scales;
   const int* block_table;

@@ -259,14 +259,14 @@ ATTN_API attn_status attn_fwd_splitkv_noalloc(const void* q, const void* k_cache
  *   q [B,N,Hq,d], k [B,N,Hkv,d] bf16 in, with token rows q_stride and
  *            k_stride elements apart (token t = b*N + n starts at t * stride;
  *            Hq*d and Hkv*d for dense tensors, more for a part of a fused
- *            projection's rows); strides are multiples of 8;
+ *            projection's rows); strides are multiples of 8 below 2^31;
  *   q_weight, k_weight: fp32 [d], 16-byte aligned; NULL leaves that tensor
  *            without a norm (rotation only);
  *   eps: finite and > 0 (not looked at when both weights are NULL);
  *   positions: device int32 [B,N], or NULL for 0 .. N-1 in every sequence;
  *   q_out [B,N,Hq,d], k_out [B,N,Hkv,d] bf16 out, dense.  q_out may be q, and
  *            k_out k, where that input is dense; otherwise they must not
- *            overlap the inputs.
+ *            overlap the inputs (from first to last element) or each other.
  * Hkv = 0: q alone (k, k_out NULL).  The statistics are fp32, the result is
  * rounded once.  Constraints: B, Hq >= 1; N, Hkv >= 0 (Hkv need not divide
  * Hq); d in {64, 128}; tensors 16-byte aligned; Hq + Hkv at most 2^20 and
@@ -286,10 +286,13 @@ ATTN_API size_t attn_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int H
  * gradients of q_out, k_out; q, k and the other arguments are the forward
  * call's (its outputs are not needed: the norms are computed again).
  *   dq [B,N,Hq,d], dk [B,N,Hkv,d] bf16 out, dense; dq may be dq_out, dk dk_out;
+ *            otherwise they must not overlap the inputs or each other;
  *   dq_weight, dk_weight: fp32 [d] out (written, not added to), NULL exactly
  *            where the weight is NULL; q (k) may be NULL where its weight is;
  *   workspace: attn_qk_norm_rope_bwd_workspace_size bytes, 16-byte aligned,
- *            contents ignored; may be NULL when both weights are NULL.
+ *            contents ignored; may be NULL when both weights are NULL.  Calls
+ *            that may run at once (on other streams, in graphs replayed side
+ *            by side) need workspaces of their own.
  * Sums over tokens and heads are fp32 in a fixed order: the same call gives
  * the same bits.  N = 0 writes zero weight gradients.
  */
@@ -315,7 +318,7 @@ ATTN_API attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_ou
  *            real (the rows behind them are not read); NULL: all Nn;
  *   seqlens_out: device int32 [B], receives the lengths after the call (the
  *            seqlens of a decode that follows); NULL where not wanted; must
- *            not be seqlens.
+ *            not overlap seqlens or new_lens.
  * A length outside [0, max_blocks * page_size], a new_lens entry outside
  * [0, Nn], rows that do not fit the table (they are dropped) and page indices
  * outside [0, num_pages) (nothing is written there) are reported as
@@ -364,6 +367,7 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  * keys 0 .. seqlens[b] - Nq + i (Nq = 1: the whole cache).
  *   q [B,Nq,Hq,d] bf16, Nq in [1, 64]; o [B,Nq,Hq,d] bf16 and lse [B,Hq,Nq]
  *            fp32 out; a row that sees no key gets O = 0 and LSE = -inf;
+ *            o must not overlap q;
  *   k_pages, v_pages [num_pages, page_size, Hkv, d] e4m3, 16-byte aligned;
  *   k_scales, v_scales fp32 [num_pages, Hkv], finite and >= 0 (any such value,
  *            not powers of two alone);
@@ -373,7 +377,8 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  *   chunk: keys per split, a multiple of 64 in [64, 2048]
  *            (attn_splitkv_fp8_chunk);
  *   workspace: attn_splitkv_workspace_size(B, Nq * Hq, max_blocks * page_size,
- *            d, chunk) bytes, 16-byte aligned, contents ignored.
+ *            d, chunk) bytes, 16-byte aligned, contents ignored; one for each
+ *            call that may run at once, as for attn_qk_norm_rope_bwd.
  * B * Nq * Hq times the splits of a sequence must stay below 2^31 - 4096.
  * Bad lengths and pages are handled as in attn_fwd_splitkv_paged.
  */

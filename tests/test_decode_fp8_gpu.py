@@ -218,6 +218,22 @@ def test_nan_in_the_cache_spoils_its_sequence_only():
     assert o[1].isnan().all() and lse[1].isnan().all() and lse[0].isfinite().all()
 
 
+def test_queries_that_are_not_finite():
+    """A NaN or an infinity in a query row spoils that row only."""
+    lens = [300]
+    g, pools, scales, table = _cache(1, 2, 64, 64, lens, 84)
+    q = torch.randn((1, 2, 8, 64), generator=g).to(torch.bfloat16)
+    want = _run(q, pools, scales, table, lens, 0.125, 128)
+    bad = q.clone()
+    bad[0, 0, 1, 7] = float("nan")
+    bad[0, 1, 6, 60] = float("-inf")
+    o, lse = _run(bad, pools, scales, table, lens, 0.125, 128)
+    spoilt = torch.zeros((2, 8), dtype=torch.bool)
+    spoilt[0, 1] = spoilt[1, 6] = True
+    assert o[0][spoilt].isnan().all() and lse[0].t()[spoilt].isnan().all()
+    assert torch.equal(o[0][~spoilt], want[0][0][~spoilt]) and torch.equal(lse[0].t()[~spoilt], want[1][0].t()[~spoilt])
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 1), (24, 1)])
 def test_nan_among_the_new_tokens(Hq, Hkv):
     """A NaN in a value that only the last of the new tokens sees leaves the others as they are."""
@@ -298,6 +314,28 @@ def test_captured_and_two_streams():
     assert _native.attn_get_device_status() == 0
 
 
+def test_a_late_stream_keeps_what_the_call_allocated():
+    """stream=: what the call allocates is that stream's, so allocations of the current stream made while the other
+    is still behind do not get its workspace or outputs."""
+    lens = [900, 400]
+    g, pools, scales, table = _cache(2, 2, 128, 64, lens, 82)
+    q = torch.randn((2, 1, 8, 128), generator=g).to(torch.bfloat16)
+    dev = [q.cuda()] + [p.cuda().view(torch.float8_e4m3fn) for p in pools] + [s.cuda() for s in scales] + [
+        table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()]
+    want = _native.decode_paged_fp8(*dev, 0.09, 64)      # 15 splits: partial results in the workspace
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = _native.decode_paged_fp8(*dev, 0.09, 64, stream=side)
+    sizes = [want[0].numel() * 2, want[1].numel() * 4, _native.attn_splitkv_workspace_size(2, 8, 960, 128, 64)]
+    held = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(bool((h == 255).all()) for h in held)
+    assert _native.attn_get_device_status() == 0
+
+
 def test_refusals():
     lens = [100]
     g, pools, scales, table = _cache(1, 2, 64, 64, lens, 81)
@@ -308,6 +346,8 @@ def test_refusals():
     f = _native.decode_paged_fp8
     for bad in (lambda: f(q.float(), kp, vp, ks, vs, t, n, 0.1), lambda: f(q, kp.view(torch.uint8), vp, ks, vs, t, n, 0.1),
                 lambda: f(q, kp, vp, ks[:1], vs, t, n, 0.1), lambda: f(q, kp, vp, ks, vs, t.long(), n, 0.1),
+                lambda: f(q, kp, vp, ks, vs, t, n, 0.1, workspace=torch.empty(1 << 20, dtype=torch.uint8)),
+                lambda: f(q, kp, vp, ks, vs, t, n, 0.1, workspace=torch.empty(1 << 20, device="cuda")[::2]),
                 lambda: f(q, kp, vp, ks, vs, t, n[:0], 0.1), lambda: f(q[:, :, ::2], kp, vp, ks, vs, t, n, 0.1)):
         with pytest.raises(ValueError):
             bad()

@@ -237,6 +237,27 @@ def test_captured_and_on_another_stream():
             assert torch.equal(a, b)
 
 
+def test_a_late_stream_keeps_what_the_call_allocated():
+    """stream=: what the calls allocate is that stream's, so allocations of the current stream made while the other
+    is still behind do not get the workspace or outputs."""
+    _, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(2, 40, 4, 2, 128, 128, 22, True, 2)
+    r, p, w = _gpu(rope), pos.cuda(), (wq.cuda(), wk.cuda())
+    g = [torch.randn((2, 40, H, 128), device="cuda").to(torch.bfloat16) for H in (4, 2)]
+    want = _native.qk_norm_rope(qc, kc, *w, 1e-6, r, p) + _native.qk_norm_rope_bwd(*g, qc, kc, *w, 1e-6, r, p)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = _native.qk_norm_rope(qc, kc, *w, 1e-6, r, p, stream=side) + _native.qk_norm_rope_bwd(
+        *g, qc, kc, *w, 1e-6, r, p, stream=side)
+    sizes = [t.numel() * t.element_size() for t in want] + [
+        _native.attn_qk_norm_rope_bwd_workspace_size(2, 40, 4, 2, 128)]
+    held = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert all(bool((h == 255).all()) for h in held)
+
+
 def test_refusals():
     q = torch.zeros((1, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, device="cuda")
@@ -248,10 +269,15 @@ def test_refusals():
                 lambda: _native.qk_norm_rope(q, q, w, w, rope=(rope[0], rope[1][:4])),
                 lambda: _native.qk_norm_rope(q, q, w, w, rope=rope, positions=torch.zeros((1, 2), device="cuda")),
                 lambda: _native.qk_norm_rope(q, q, w, w, out=(q[:, :1], q)),
+                lambda: _native.qk_norm_rope_bwd(q, q, q, q, w, w, workspace=torch.empty(1 << 20, dtype=torch.uint8)),
                 lambda: _native.qk_norm_rope_bwd(q, q, q[:, :1], q, w, w)):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(_native.AttnError):
         _native.qk_norm_rope(q, q, w, w, eps=0.0)
+    other = torch.zeros_like(q)
+    for out in ((other, other), (other, q)):     # outputs over each other, an output over the other input
+        with pytest.raises(_native.AttnError):
+            _native.qk_norm_rope(q, other.clone(), w, w, out=out)
     with pytest.raises(_native.AttnError):
         _native.qk_norm_rope(q[..., :48].contiguous(), None, None, None)

@@ -37,7 +37,11 @@ def _qk(L, **kw):
     (1, dict(q=0)), (1, dict(k=0)), (1, dict(qo=0)), (1, dict(ko=0)), (1, dict(qs=1016)), (3, dict(qs=1028)),
     (3, dict(q=24)), (3, dict(qo=40)), (3, dict(wq=20)), (3, dict(pos=18)),
     (1, dict(qo=16, qs=2048)),                # in place needs dense rows
-    (2, dict(B=1 << 20, N=1 << 20)), (2, dict(Hq=1 << 21, qs=1 << 28)),
+    (2, dict(B=1 << 20, N=1 << 20)), (2, dict(Hq=1 << 21, qs=1 << 28)), (2, dict(qs=1 << 31)),
+    # outputs over another tensor's rows: the other input, the other output, an input moved by one row
+    (1, dict(q=1 << 20, k=2 << 20, qo=2 << 20, ko=4 << 20)), (1, dict(q=1 << 20, k=2 << 20, qo=3 << 20, ko=1 << 20)),
+    (1, dict(q=1 << 20, k=2 << 20, qo=3 << 20, ko=(3 << 20) + 10 * 2048 - 16)),
+    (1, dict(q=1 << 20, k=2 << 20, qo=(1 << 20) + 256, ko=3 << 20)),
 ])
 def test_qk_norm_rope_argument_checks(L, want, kw):
     assert _qk(L, **kw) == want
@@ -58,7 +62,10 @@ def _qkb(L, **kw):
     (0, dict(N=0, wq=0, wk=0, dwq=0, dwk=0)), (1, dict(B=0)), (2, dict(d=80)), (1, dict(rot=130)),
     (1, dict(eps=0.0)), (1, dict(dwq=0)), (1, dict(wk=0)), (1, dict(gq=0)), (1, dict(dk=0)), (1, dict(q=0)),
     (1, dict(ks=128)), (3, dict(ks=260)), (3, dict(gq=24)), (3, dict(dwq=18)), (7, dict(ws=0)), (7, dict(wsb=64)),
-    (7, dict(ws=24)), (1, dict(Hkv=0)),
+    (7, dict(ws=24)), (1, dict(Hkv=0)), (2, dict(ks=1 << 31)),
+    (1, dict(gq=1 << 20, gk=2 << 20, q=3 << 20, k=4 << 20, dq=3 << 20, dk=2 << 20)),
+    (1, dict(gq=1 << 20, gk=2 << 20, q=3 << 20, k=4 << 20, dq=2 << 20, dk=5 << 20)),
+    (1, dict(gq=1 << 20, gk=2 << 20, q=3 << 20, k=4 << 20, dq=(1 << 20) + 256, dk=2 << 20)),
 ])
 def test_qk_norm_rope_bwd_argument_checks(L, want, kw):
     assert _qkb(L, **kw) == want
@@ -89,9 +96,10 @@ def _app(L, fp8=False, **kw):
 @pytest.mark.parametrize("want,kw", [
     (1, dict(B=0)), (1, dict(Nn=-1)), (1, dict(Hkv=0)), (1, dict(mb=0)), (1, dict(npg=0)), (1, dict(ps=0)),
     (1, dict(ps=100)), (2, dict(d=96)), (2, dict(B=65536)), (2, dict(mb=1 << 23)), (1, dict(sl=0)), (1, dict(bt=0)),
-    (1, dict(kp=0)), (1, dict(vp=0)), (1, dict(so=16)), (1, dict(k=0)), (1, dict(v=0)), (1, dict(ks=1016)),
+    (1, dict(kp=0)), (1, dict(vp=0)), (1, dict(so=16)), (1, dict(nl=32, so=32)),
+    (1, dict(k=0)), (1, dict(v=0)), (1, dict(ks=1016)), (2, dict(ks=1 << 31)),
     (3, dict(vs=1028)), (3, dict(k=24)), (3, dict(kp=24)), (3, dict(bt=18)), (3, dict(sl=18)), (3, dict(nl=18)),
-    (3, dict(so=18)), (1, dict(rot=130)), (2, dict(rot=8)), (1, dict(c=0)), (3, dict(s=24)), (1, dict(inter=-1)),
+    (3, dict(so=18)), (1, dict(so=20)), (1, dict(sl=64, nl=32, so=28)), (1, dict(rot=130)), (2, dict(rot=8)), (1, dict(c=0)), (3, dict(s=24)), (1, dict(inter=-1)),
 ])
 def test_append_argument_checks(L, fp8, want, kw):
     assert _app(L, fp8, **kw) == want
@@ -119,6 +127,7 @@ def _dec(L, **kw):
     (2, dict(d=256)), (2, dict(mb=1 << 23)), (2, dict(B=65536)), (1, dict(q=0)), (1, dict(sk=0)), (1, dict(sv=0)),
     (1, dict(bt=0)), (1, dict(sl=0)), (1, dict(o=0)), (1, dict(lse=0)), (3, dict(q=24)), (3, dict(kp=24)),
     (3, dict(sk=18)), (3, dict(bt=18)), (3, dict(lse=18)), (7, dict(ws=0)), (7, dict(ws=24)), (7, dict(wsb=1024)),
+    (1, dict(q=1 << 20, o=1 << 20)), (1, dict(q=1 << 20, o=(1 << 20) + 2 * 8 * 256 - 16)),
 ])
 def test_decode_fp8_argument_checks(L, want, kw):
     assert _dec(L, **kw) == want
@@ -145,6 +154,19 @@ def test_binding_refuses_tensors_off_the_gpu():
         _native.kvcache_append_paged(x, x, x, x, x, x)
     with pytest.raises(ValueError):
         _native.decode_paged_fp8(x, x, x, x, x, x, x, 1.0)
+
+
+def test_binding_refuses_workspaces_and_streams_of_other_devices():
+    w = torch.zeros(64)
+    assert _native._space(w, -1) == (w.data_ptr(), 256)
+    for bad, dev in ((w, 0), (w[::2], -1)):
+        with pytest.raises(ValueError):
+            _native._space(bad, dev)
+
+    class Stream:
+        device_index = 1
+    with pytest.raises(ValueError):
+        _native._on(Stream(), 0)
 
 
 def test_row_strides_of_parts_of_a_projection():
