@@ -33,10 +33,10 @@
 //   softmax    one to three groups of four warps, a thread a key (TMEM lane):
 //              scales, running reference, weights, their three terms as bytes
 //              into shared memory
-//   output     four warps, a thread a dim: adds each tile's O^T columns to its
+//   output     two or four warps, a thread a dim: adds each tile's O^T columns to its
 //              fp32 registers (so no rescaling in TMEM)
-//   items      one warp: finds them from the lengths, fetches their pages and
-//              scales, turns q into e5m2 terms, up to kItems ahead
+//   items      one to three warps: find them from the lengths, fetch their pages
+//              and scales, turn q into e5m2 terms, up to kItems ahead
 //   MMA        one warp: TMEM, MMA issue; S of the next tile goes out before O
 //              of this one where its K is there
 //   loads      one warp: TMA, 128 keys of K and V a stage, in boxes of 64 rows
@@ -81,7 +81,11 @@ struct Cfg {
   static constexpr int kGroups = R == 4 ? 1 : (R == 24 ? 3 : 2);
   static constexpr int kRows = R / kGroups;
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kWarps = kSoftWarps + 7;
+  static constexpr int kOutWarps = D / 32;
+  // warps that prepare items, each 8 rows of q (4 of R = 4): one warp took 5 us
+  // for 24 rows, the time of five tiles.  20 warps at most, for 96 registers.
+  static constexpr int kItemWarps = R <= 8 ? 1 : (R == 24 && D == 128 ? 2 : R / 8);
+  static constexpr int kWarps = kSoftWarps + kOutWarps + kItemWarps + 2;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = kTile * D;
   static constexpr int kStages = (kCtas == 2 ? 3 : (R == 8 ? 6 : 5)) * 128 / D;
@@ -96,6 +100,7 @@ struct Cfg {
   static constexpr int kOffItem = kOffP + 2 * kN * kTile;   // [kItems]
   static constexpr int kOffAlpha = kOffItem + kItems * ((8 + 3 * kMaxBlocks + 4 * R) * 4);  // float [2][R]
   static constexpr int kOffRed = kOffAlpha + 2 * R * 4;     // [kGroups] float [4][kRows], then [kGroups] 4 flags
+  static_assert(kOffRed % 16 == 0 && kRows % 4 == 0, "read four rows at a time");
   static constexpr int kOffSpoil = kOffRed + 4 * R * 4 + kGroups * 16;  // byte [2][kTile]
   static constexpr int kOffMl = kOffSpoil + 2 * kTile;      // [2] float m[R], l[4][R]
   static constexpr int kOffBar = (kOffMl + 2 * 5 * R * 4 + 15) / 16 * 16;
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     decode_fp8_split_kernel(const __grid_constant__ DecodeFp8Params p) {
   using C = Cfg<D, R>;
   constexpr int kN = C::kN, kRows = C::kRows, kOut0 = C::kSoftWarps;  // kOut0: the first output warp
-  constexpr int kItemWarp = kOut0 + 4, kMmaWarp = kOut0 + 5, kLoadWarp = kOut0 + 6;
+  constexpr int kItemWarp = kOut0 + C::kOutWarps, kMmaWarp = kItemWarp + C::kItemWarps, kLoadWarp = kMmaWarp + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       }
       for (int i = 0; i < C::kItems; ++i) {
         mbar_init(bar_pages + i, 1);
-        mbar_init(bar_ready + i, 1);
+        mbar_init(bar_ready + i, C::kItemWarps);
         mbar_init(bar_free + i, C::kSoftWarps + D / 32 + 2);
       }
       for (int i = 0; i < 2; ++i) {
@@ -271,15 +276,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   } else if (warp == kMmaWarp) {
     tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
-  } else if (warp >= kOut0 && warp < kOut0 + 4) {
+  } else if (warp >= kOut0 && warp < kItemWarp) {
     // the MMA columns past 3R stay 0 in every Q and P
     constexpr int kPad = kN - 3 * R;
-    for (int i = tid - 32 * kOut0; i < C::kItems * kPad * (D / 4); i += 128) {
+    for (int i = tid - 32 * kOut0; i < C::kItems * kPad * (D / 4); i += D) {
       const int n = 3 * R + i / (D / 4) % (kPad + (kPad == 0)), slot = i / (D / 4) / (kPad + (kPad == 0));
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sQ + slot * C::kQBytes + swizzled<D>(n, 4 * (i % (D / 4)))), "r"(0u)
                    : "memory");
     }
-    for (int i = tid - 32 * kOut0; i < 2 * kPad * (kTile / 4); i += 128) {
+    for (int i = tid - 32 * kOut0; i < 2 * kPad * (kTile / 4); i += D) {
       const int n = 3 * R + i / (kTile / 4) % (kPad + (kPad == 0)), buf = i / (kTile / 4) / (kPad + (kPad == 0));
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sP + buf * kN * kTile + swizzled<128>(n, 4 * (i % (kTile / 4)))),
                    "r"(0u)
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   static_assert((R * D + 3 * R) * 4 <= C::kStages * C::kStage, "a split's result fits the stages");
 
   uint32_t tmem = 0u;  // S at columns 0, kN; O^T at 2 kN, 3 kN
-  if (warp != kItemWarp) {  // it looks for its first item before it meets the others there
+  if (warp < kItemWarp || warp >= kMmaWarp) {  // the item warps look for their first item before they join
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           for (int r = 0; r < kRows; ++r) hidden |= (key >= it.lim[grp * kRows + r] ? 1u : 0u) << r;
         }
         float2 x[kPairs];  // scores in base 2, less the reference
-        bool big = t == 0;
+        bool big = false;
         const float2 ks2 = make_float2(ks, ks);
 #pragma unroll
         for (int r = 0; r < kPairs; ++r) {
@@ -370,8 +375,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         float al[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) al[r] = 1.f;
-        if (softmax_bar_or(grp, big || failed || *abort_flag)) {
-          // some row's reference may have to move (or a wait gave up)
+        if (t == 0 || softmax_bar_or(grp, big || failed || *abort_flag)) {
+          // the first tile sets the references; some row's may have to move (or a wait gave up)
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
             const float xr = r & 1 ? x[r / 2].y : x[r / 2].x;
@@ -385,9 +390,21 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             stop = true;
             break;
           }
+          float top[kRows];
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) top[r] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {  // four rows of a warp a load
+            const float4 v = reinterpret_cast<const float4*>(red)[i];
+            const int r = 4 * i % kRows;
+            top[r] = fmaxf(top[r], v.x);
+            top[r + 1] = fmaxf(top[r + 1], v.y);
+            top[r + 2] = fmaxf(top[r + 2], v.z);
+            top[r + 3] = fmaxf(top[r + 3], v.w);
+          }
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            const float mx = fmaxf(fmaxf(red[r], red[kRows + r]), fmaxf(red[2 * kRows + r], red[3 * kRows + r]));
+            const float mx = top[r];
             const bool first = !((seen >> r) & 1u);
             if (mx > (first ? -INFINITY : kMoveLog2)) {
               float& mr = r & 1 ? nm[r / 2].y : nm[r / 2].x;
@@ -496,93 +513,100 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         mbar_arrive(bar_free + n % C::kItems);
       }
     }
-  } else if (warp < kOut0 + 4) {
+  } else if (warp < kItemWarp) {
     // ================================================================ output
     const int dd = tid - 32 * kOut0;
-    if (dd < D) {
-      int g = 0;
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        const Item<R>& it = items[n % C::kItems];
-        if (!wait_all(bar_ready + n % C::kItems, (n / C::kItems) & 1, abort_flag, 8)) break;
-        const int n_t = it.n_t;
-        if (n_t < 0) break;
-        float acc[R];
+    int g = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const Item<R>& it = items[n % C::kItems];
+      if (!wait_all(bar_ready + n % C::kItems, (n / C::kItems) & 1, abort_flag, 8)) break;
+      const int n_t = it.n_t;
+      if (n_t < 0) break;
+      float acc[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = 0.f;
-        for (int t = 0; t < n_t; ++t, ++g) {
-          const int buf = g & 1;
-          // bar_p for alpha (the softmax warps' own arrivals), bar_o for O^T
-          ok = wait_all(bar_p + buf, (g >> 1) & 1, abort_flag, 9) && wait_all(bar_o + buf, (g >> 1) & 1, abort_flag, 10);
-          if (!ok) break;
-          tc_fence_after();
-          constexpr int kLd = (3 * kRows + 7) / 8 * 8;
-          const uint32_t o_at = tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN;
+      for (int r = 0; r < R; ++r) acc[r] = 0.f;
+      for (int t = 0; t < n_t; ++t, ++g) {
+        const int buf = g & 1;
+        // bar_p for alpha (the softmax warps' own arrivals), bar_o for O^T
+        ok = wait_all(bar_p + buf, (g >> 1) & 1, abort_flag, 9) && wait_all(bar_o + buf, (g >> 1) & 1, abort_flag, 10);
+        if (!ok) break;
+        tc_fence_after();
+        constexpr int kLd = (3 * kRows + 7) / 8 * 8;
+        const uint32_t o_at = tmem + (static_cast<uint32_t>((warp - kOut0) * 32) << 16) + (2 + buf) * kN;
 #pragma unroll
-          for (int q = 0; q < C::kGroups; ++q) {
-            uint32_t u[kLd];
-            tmem_ld_row<kLd>(o_at + q * 3 * kRows, u);
+        for (int q = 0; q < C::kGroups; ++q) {
+          uint32_t u[kLd];
+          tmem_ld_row<kLd>(o_at + q * 3 * kRows, u);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
-              acc[q * kRows + r] =
-                  fmaf(acc[q * kRows + r], s_alpha[buf * R + q * kRows + r],
-                       __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]));
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_of + buf);
+          for (int r = 0; r < kRows; ++r)
+            acc[q * kRows + r] =
+                fmaf(acc[q * kRows + r], s_alpha[buf * R + q * kRows + r],
+                     __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]));
         }
-        if (!ok || !wait_all(bar_ml + (n & 1), (n >> 1) & 1, abort_flag, 11)) break;
-        const float* ml = s_ml + (n & 1) * 5 * R;
-        const int split = it.split;
-        const bool clustered = p.cluster != 0;
-        const bool direct = it.direct != 0;
-        const float osc = it.vref * (1.f / kWeightScale);
-        // what the slot holds is read before it is given back; rows are in order,
-        // those past the last (-1) behind
-        int o_row[R];
-        float lse[R];
-        int lse_row = -1;  // lane r keeps row r's
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float lr = (ml[R + r] + ml[2 * R + r]) + (ml[3 * R + r] + ml[4 * R + r]);
-          // l is 0 exactly where the row sees no key of the split (NaN, not 0, where a score is NaN)
-          acc[r] = lr == 0.f ? 0.f : acc[r] * osc / lr;
-          lse[r] = lr == 0.f ? -INFINITY : (ml[r] + __log2f(lr)) * 0.6931471805599453f;
-          o_row[r] = it.o_row[r];
-        }
-        if (lane < R) lse_row = it.lse_row[lane];
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar_mf + (n & 1));
-          mbar_arrive(bar_free + n % C::kItems);
-        }
+        if (lane == 0) mbar_arrive(bar_of + buf);
+      }
+      if (!ok || !wait_all(bar_ml + (n & 1), (n >> 1) & 1, abort_flag, 11)) break;
+      const float* ml = s_ml + (n & 1) * 5 * R;
+      const int split = it.split;
+      const bool direct = it.direct != 0;
+      const float vref = it.vref;
+      // Lane r forms row r's factor and LSE (every lane all of them took 3.5 us
+      // for 24 rows); what the slot holds is read before it is given back.
+      // l is 0 exactly where the row sees no key of the split (NaN, not 0, where a score is NaN).
+      int o_row = -1, lse_row = -1;
+      float lr = 0.f, lse = -INFINITY;
+      if (lane < R) {
+        lr = (ml[R + lane] + ml[2 * R + lane]) + (ml[3 * R + lane] + ml[4 * R + lane]);
+        if (lr != 0.f) lse = (ml[lane] + __log2f(lr)) * 0.6931471805599453f;
+        o_row = it.o_row[lane];
+        lse_row = it.lse_row[lane];
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_mf + (n & 1));
+        mbar_arrive(bar_free + n % C::kItems);
+      }
+      const float inv = lr == 0.f ? 0.f : (1.f / kWeightScale) / lr;
+      const unsigned none = __ballot_sync(0xffffffffu, lr == 0.f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (clustered) {
-            // over the stages, whose last tile has been multiplied
-            s_part[r * D + dd] = acc[r];
-            if (dd == r) {
-              s_part_lse[r] = lse[r];
-              s_part_row[r] = o_row[r];
-              s_part_row[R + r] = lse_row;
-            }
-            continue;
-          }
-          if (o_row[r] < 0) break;
-          if (direct) {
-            static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(o_row[r]) * D + dd] = __float2bfloat16_rn(acc[r]);
-            if (dd == r) p.lse[lse_row] = lse[r];
-          } else {
-            const long long part = static_cast<long long>(o_row[r]) * p.n_split + split;
-            p.o_part[part * D + dd] = acc[r];
-            if (dd == 0) p.lse_part[part] = lse[r];
-          }
+      for (int r = 0; r < R; ++r) {
+        acc[r] = acc[r] * __shfl_sync(0xffffffffu, inv, r) * vref;
+        if ((none >> r) & 1u) acc[r] = 0.f;
+      }
+      if (p.cluster != 0) {
+        // over the stages, whose last tile has been multiplied
+#pragma unroll
+        for (int r = 0; r < R; ++r) s_part[r * D + dd] = acc[r];
+        if (dd < R) {
+          s_part_lse[dd] = lse;
+          s_part_row[dd] = o_row;
+          s_part_row[R + dd] = lse_row;
         }
+        continue;
+      }
+      if (dd < R && o_row >= 0) {
+        if (direct)
+          p.lse[lse_row] = lse;
+        else
+          p.lse_part[static_cast<long long>(o_row) * p.n_split + split] = lse;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int to = __shfl_sync(0xffffffffu, o_row, r);
+        if (to < 0) break;  // rows are in order, those past the last behind
+        if (direct)
+          static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(to) * D + dd] = __float2bfloat16_rn(acc[r]);
+        else
+          p.o_part[(static_cast<long long>(to) * p.n_split + split) * D + dd] = acc[r];
       }
     }
-  } else if (warp == kItemWarp) {
+  } else if (warp < kMmaWarp) {
     // ================================================================ items
+    // Every item warp finds every item; the first one writes its description
+    // and tells the loader, each one turns its own rows of q into e5m2 terms.
     // Item i of the whole call: j = i / H counts (sequence, split) pairs, the
     // full splits of all sequences first and the shorter last ones after them,
     // i % H is the KV head and block of its rows (so neighbouring CTAs read
@@ -622,14 +646,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       return true;
     };
     // kLanes lanes share a row of q, each a run of kDims of it; kPasses times
-    // 32 / kLanes rows.  One pass of q is loaded an item ahead; several would
-    // not fit the registers, and their items are longer.
-    constexpr int kPg = C::kMaxBlocks / 32, kLanes = R == 4 ? 8 : 4, kDims = D / kLanes, kPassRows = 32 / kLanes;
-    constexpr int kPasses = R / kPassRows;
+    // kPassRows rows.  One pass of q is loaded an item ahead; two would not fit
+    // the registers.
+    constexpr int kPg = C::kMaxBlocks / 32, kLanes = R == 4 ? 8 : 4, kDims = D / kLanes;
+    constexpr int kPassRows = C::kItemWarps * 32 / kLanes, kPasses = (R + kPassRows - 1) / kPassRows;
     constexpr bool kAhead = kPasses == 1;
-    const int qr = lane / kLanes, qd = lane % kLanes * kDims;
+    const bool leads = warp == kItemWarp;
+    const int qr = ((warp - kItemWarp) * 32 + lane) / kLanes, qd = lane % kLanes * kDims;
     // row r of an item: its place, and this lane's part of its q
-    auto row_of = [&](int b, int hkv, int row0, int r, int& tok, int& hq) {
+    auto row_of = [&](int hkv, int row0, int r, int& tok, int& hq) {
       const int row = row0 + r;
       tok = p.G.div(row);
       hq = hkv * G + row - tok * G;
@@ -676,7 +701,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
           const int blk = 32 * k + lane;
-          f.pg[k] = blk < n_blk
+          f.pg[k] = leads && blk < n_blk
                         ? p.block_table[static_cast<long long>(f.b) * p.max_blocks + p.page.div(k0 + 64 * blk)]
                         : 0;
         }
@@ -710,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
         for (int k = 0; k < kPg; ++k) {
           const int blk = 32 * k + lane;
-          if (blk < n_blk)
+          if (leads && blk < n_blk)
             f.pg[k] = p.block_table[static_cast<long long>(f.b) * p.max_blocks + p.page.div(k0 + 64 * blk)];
         }
       }
@@ -739,14 +764,14 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             f.pg[k] = 0;  // keep every load inside the page pool; the result is flagged
           }
           a.ks[k] = a.vs[k] = 0.f;
-          if (32 * k + lane < a.n_blk) {
+          if (leads && 32 * k + lane < a.n_blk) {
             a.ks[k] = p.k_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
             a.vs[k] = p.v_scales[static_cast<long long>(f.pg[k]) * p.Hkv + f.hkv];
           }
         }
         if constexpr (kAhead) {
           int tok, hq;
-          const bool real = row_of(f.b, f.hkv, f.row0, qr, tok, hq);
+          const bool real = row_of(f.hkv, f.row0, qr, tok, hq);
           load_q(f.b, tok, hq, real, a.q);
         }
       }
@@ -754,6 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         ok = false;
         return a;
       }
+      if (!leads) return a;
       if (lane == 0) {
         it.n_t = f.more ? (a.kn + kTile - 1) / kTile : -1;
         it.kn = a.kn;
@@ -777,32 +803,24 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       Item<R>& it = items[slot];
       if (cur.more) {
         // q as three e5m2 terms a row
-        uint4 q[kPasses][kDims / 8];
-#pragma unroll
-        for (int ps = 0; ps < kPasses; ++ps) {
-          int tok, hq;
-          const int r = ps * kPassRows + qr;
-          const bool real = row_of(cur.b, cur.hkv, cur.row0, r, tok, hq);
-          if constexpr (kAhead) {
-#pragma unroll
-            for (int c = 0; c < kDims / 8; ++c) q[0][c] = cur.q[c];
-          } else {
-            load_q(cur.b, tok, hq, real, q[ps]);
-          }
-          if (lane % kLanes == 0) {
-            it.lim[r] = min(cur.kn, cur.len - p.Nq + 1 + tok - cur.k0);
-            it.o_row[r] = real ? (cur.b * p.Nq + tok) * p.Hq + hq : -1;
-            it.lse_row[r] = (cur.b * p.Hq + hq) * p.Nq + tok;
-          }
-        }
         const uint32_t q_at = sQ + slot * C::kQBytes;
 #pragma unroll
         for (int ps = 0; ps < kPasses; ++ps) {
           const int r = ps * kPassRows + qr;
+          if (R % kPassRows != 0 && r >= R) break;  // uniform: whole warps
+          int tok, hq;
+          const bool real = row_of(cur.hkv, cur.row0, r, tok, hq);
+          uint4 q[kDims / 8];
+          if constexpr (kAhead) {
+#pragma unroll
+            for (int c = 0; c < kDims / 8; ++c) q[c] = cur.q[c];
+          } else {
+            load_q(cur.b, tok, hq, real, q);
+          }
           uint32_t amax = 0u;
 #pragma unroll
           for (int c = 0; c < kDims / 8; ++c) {
-            const uint32_t w[4] = {q[ps][c].x, q[ps][c].y, q[ps][c].z, q[ps][c].w};
+            const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
           }
@@ -813,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           const float f = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
 #pragma unroll
           for (int c = 0; c < kDims / 8; ++c) {  // 8 values: 8 bytes a term, at a multiple of 8
-            const uint32_t w[4] = {q[ps][c].x, q[ps][c].y, q[ps][c].z, q[ps][c].w};
+            const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
             float x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -835,23 +853,29 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
                            : "memory");
             }
           }
-          // a row with an infinity or NaN: every score NaN
-          if (lane % kLanes == 0)
+          if (lane % kLanes == 0) {
+            it.lim[r] = min(cur.kn, cur.len - p.Nq + 1 + tok - cur.k0);
+            it.o_row[r] = real ? (cur.b * p.Nq + tok) * p.Hq + hq : -1;
+            it.lse_row[r] = (cur.b * p.Hq + hq) * p.Nq + tok;
+            // a row with an infinity or NaN: every score NaN
             it.qm[r] = fin ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2 : NAN;
-        }
-        float vref = 0.f;
-#pragma unroll
-        for (int k = 0; k < kPg; ++k) vref = fmaxf(vref, cur.vs[k]);
-        vref = warp_max(vref);
-#pragma unroll
-        for (int k = 0; k < kPg; ++k) {
-          if (32 * k + lane < cur.n_blk) {
-            it.ks[32 * k + lane] = cur.ks[k];
-            // at most kWeightScale, however small the scales are
-            it.vs[32 * k + lane] = vref > 0.f ? cur.vs[k] / vref * kWeightScale : 0.f;
           }
         }
-        if (lane == 0) it.vref = vref;
+        if (leads) {
+          float vref = 0.f;
+#pragma unroll
+          for (int k = 0; k < kPg; ++k) vref = fmaxf(vref, cur.vs[k]);
+          vref = warp_max(vref);
+#pragma unroll
+          for (int k = 0; k < kPg; ++k) {
+            if (32 * k + lane < cur.n_blk) {
+              it.ks[32 * k + lane] = cur.ks[k];
+              // at most kWeightScale, however small the scales are
+              it.vs[32 * k + lane] = vref > 0.f ? cur.vs[k] / vref * kWeightScale : 0.f;
+            }
+          }
+          if (lane == 0) it.vref = vref;
+        }
         fence_proxy_async_smem();
       }
       __syncwarp();
