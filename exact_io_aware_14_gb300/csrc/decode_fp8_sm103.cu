@@ -170,12 +170,25 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Largest value of the warp, NaN left out: one integer reduction, the floats
-// mapped to integers of the same order.
-__device__ __forceinline__ float warp_max_ordered(float v) {
-  const uint32_t u = __float_as_uint(v == v ? v : -INFINITY);
-  const uint32_t m = __reduce_max_sync(0xffffffffu, u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u));
-  return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+// Largest values of kN rows (4 or 8) over the warp, NaN left out: each step
+// halves the rows a lane holds, then the lanes of a row are reduced.  Returns
+// row lane / (32 / kN)'s.
+template <int kN>
+__device__ __forceinline__ float warp_max_rows(float (&v)[kN]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int half = kN / 2; half > 0; half /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[half + i], keep = up ? v[half + i] : v[i];
+      v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o > 0; o /= 2) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -377,12 +390,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         for (int r = 0; r < kRows; ++r) al[r] = 1.f;
         if (t == 0 || softmax_bar_or(grp, big || failed || *abort_flag)) {
           // the first tile sets the references; some row's may have to move (or a wait gave up)
+          float top[kRows];
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const float xr = r & 1 ? x[r / 2].y : x[r / 2].x;
-            const float mx = warp_max_ordered((hidden >> r) & 1u ? -INFINITY : xr);  // NaN scores show in p
-            if (lane == 0) red[w4 * kRows + r] = mx;
-          }
+          for (int r = 0; r < kRows; ++r)
+            top[r] = (hidden >> r) & 1u ? -INFINITY : (r & 1 ? x[r / 2].y : x[r / 2].x);  // NaN scores show in p
+          const float mine = warp_max_rows(top);
+          if (lane % (32 / kRows) == 0) red[w4 * kRows + lane / (32 / kRows)] = mine;
           if (lane == 0) fail[w4] = failed || *abort_flag;
           softmax_bar(grp);
           if (fail[0] | fail[1] | fail[2] | fail[3]) {
@@ -390,7 +403,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             stop = true;
             break;
           }
-          float top[kRows];
 #pragma unroll
           for (int r = 0; r < kRows; ++r) top[r] = -INFINITY;
 #pragma unroll
