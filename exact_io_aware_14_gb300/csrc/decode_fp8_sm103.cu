@@ -96,11 +96,12 @@ struct Cfg {
   static constexpr int kStage = 2 * kTileBytes;
   static constexpr int kQBytes = (kN * D + 1023) / 1024 * 1024;
   static constexpr int kOffQ = kStages * kStage;            // [kItems]
-  static constexpr int kOffP = kOffQ + kItems * kQBytes;    // [2][kN][128] bytes
+  static constexpr int kOffP = kOffQ + kItems * kQBytes;    // [2] kN x 128 bytes (p_at)
   static constexpr int kOffItem = kOffP + 2 * kN * kTile;   // [kItems]
   static constexpr int kOffAlpha = kOffItem + kItems * ((8 + 3 * kMaxBlocks + 4 * R) * 4);  // float [2][R]
   static constexpr int kOffRed = kOffAlpha + 2 * R * 4;     // [kGroups] float [4][kRows], then [kGroups] 4 flags
-  static_assert(kOffRed % 16 == 0 && kRows % 4 == 0, "read four rows at a time");
+  static_assert(kRows == 4 || kRows == 8, "stored as words");
+  static_assert(kOffRed % 16 == 0, "read four rows at a time");
   static constexpr int kOffSpoil = kOffRed + 4 * R * 4 + kGroups * 16;  // byte [2][kTile]
   static constexpr int kOffMl = kOffSpoil + 2 * kTile;      // [2] float m[R], l[4][R]
   static constexpr int kOffBar = (kOffMl + 2 * 5 * R * 4 + 15) / 16 * 16;
@@ -166,10 +167,6 @@ __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
 // x cut to its 3 leading significant bits (what one e5m2 term holds)
 __device__ __forceinline__ float lead3(float x) { return __uint_as_float(__float_as_uint(x) & 0xffe00000u); }
 
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Largest values of kN rows (4 or 8) over the warp, NaN left out: each step
 // halves the rows a lane holds, then the lanes of a row are reduced.  Returns
 // row lane / (32 / kN)'s.
@@ -214,6 +211,12 @@ __device__ __forceinline__ int swizzled(int n, int c) {
   const int chunk = (c >> 4) ^ (kRow == 128 ? (n & 7) : ((n >> 1) & 3));
   return n * kRow + (chunk << 4) + (c & 15);
 }
+
+// Byte offset of column n of key k in P (N-major without swizzle: a key's
+// columns lie together in 16-byte pieces, so a thread writes a term of all its
+// rows at once; with K-major rows it wrote each byte by itself, 24 stores a
+// tile for eight rows).
+__device__ __forceinline__ int p_at(int n, int k) { return (n >> 4) * (16 * kTile) + k * 16 + (n & 15); }
 
 // The first kN (at least) columns of this thread's TMEM lane from addr on.
 template <int kN>
@@ -297,11 +300,9 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sQ + slot * C::kQBytes + swizzled<D>(n, 4 * (i % (D / 4)))), "r"(0u)
                    : "memory");
     }
-    for (int i = tid - 32 * kOut0; i < 2 * kPad * (kTile / 4); i += D) {
-      const int n = 3 * R + i / (kTile / 4) % (kPad + (kPad == 0)), buf = i / (kTile / 4) / (kPad + (kPad == 0));
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sP + buf * kN * kTile + swizzled<128>(n, 4 * (i % (kTile / 4)))),
-                   "r"(0u)
-                   : "memory");
+    for (int i = tid - 32 * kOut0; i < 2 * kPad / 4 * kTile; i += D) {
+      const int n = 3 * R + i / kTile % (kPad / 4 + (kPad == 0)) * 4, buf = i / kTile / (kPad / 4 + (kPad == 0));
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sP + buf * kN * kTile + p_at(n, i % kTile)), "r"(0u) : "memory");
     }
     fence_proxy_async_smem();
   }
@@ -474,8 +475,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             ++looks;
           }
         }
-        const uint32_t pcol = sP + buf * kN * kTile;
         const float2 wv2 = make_float2(wv, wv);
+        uint32_t code[3][kPairs];  // two rows each
 #pragma unroll
         for (int r = 0; r < kPairs; ++r) {
           float2 pr = make_float2(ex2_approx(x[r].x), ex2_approx(x[r].y));
@@ -492,11 +493,20 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const float2 tm = k < 2 ? make_float2(lead3(w.x), lead3(w.y)) : w;
-            const uint32_t two = e5m2x2(tm.x, tm.y);
-            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + 2 * r, row), two);
-            st_shared_u8(pcol + swizzled<128>(grp * 3 * kRows + k * kRows + 2 * r + 1, row), two >> 8);
+            code[k][r] = e5m2x2(tm.x, tm.y);
             if (k < 2) w = fadd2(w, make_float2(-tm.x, -tm.y));
           }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {  // a term's rows lie together
+          const uint32_t at = sP + buf * kN * kTile + p_at((grp * 3 + k) * kRows, row);
+          const uint32_t lo = code[k][0] | (code[k][1] << 16);
+          if constexpr (kRows == 8)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo),
+                         "r"(code[k][2] | (code[k][3] << 16))
+                         : "memory");
+          else
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(lo) : "memory");
         }
         if (row < kRows) {
           float v = 1.f;
@@ -985,8 +995,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const uint32_t v = smem_u32(smem + s * C::kStage + C::kOffV), pb = sP + (g & 1) * kN * kTile;
 #pragma unroll
         for (int c = 0; c < kTile; c += 32)
-          mma_f8_ss(tmem + (2 + (g & 1)) * kN, desc(v + c * D, C::kTileBytes), sdesc_sw128(pb + c, 16, 1024), idesc_o,
-                    c > 0);
+          mma_f8_ss(tmem + (2 + (g & 1)) * kN, desc(v + c * D, C::kTileBytes),
+                    sdesc_sw0(pb + p_at(0, c), 128, 16 * kTile), idesc_o, c > 0);
         mma_commit(bar_o + (g & 1));
         mma_commit(bar_empty + s);
         if (!issued) {

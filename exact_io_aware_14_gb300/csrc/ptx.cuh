@@ -251,6 +251,12 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo_byte
   return (sdesc_sw128(saddr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
 }
 
+// The same without swizzle.  MN-major 8-bit operand: cores of 16 B (MN) x 8 (K),
+// 128 B each; LBO between cores along K, SBO between cores along MN.
+__device__ __forceinline__ uint64_t sdesc_sw0(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return sdesc_sw128(saddr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61);
+}
+
 // Instruction descriptor, kind::f16: f32 accumulator, bf16 A and B.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format
 //   (1 = bf16), 15 A major (0 = K), 16 B major (1 = MN), 17-22 N >> 3,
@@ -260,9 +266,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, ui
 }
 
 // Instruction descriptor, kind::f8f6f4: f32 accumulator, A e4m3 (format 0), B
-// e5m2 (format 1), B K-major; a_mn_major: A is M-contiguous.
-__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(uint32_t M, uint32_t N, uint32_t a_mn_major) {
-  return (1u << 4) | (0u << 7) | (1u << 10) | (a_mn_major << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// e5m2 (format 1); mn_major: A is M-contiguous and B N-contiguous, else both K-contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(uint32_t M, uint32_t N, uint32_t mn_major) {
+  return (1u << 4) | (0u << 7) | (1u << 10) | (mn_major << 15) | (mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // ---------------------------------------------------------------------------
