@@ -158,10 +158,16 @@ __device__ __forceinline__ uint32_t pack_odd(float lo, float hi) {
   // upper halves; 1 for each lower half that is not 0
   return __byte_perm(a, b, 0x7632) | __vminu2(__byte_perm(a, b, 0x5410), 0x00010001u);
 }
-// Eight values (four words of bf16) times inv -> eight codes.
-__device__ __forceinline__ uint2 e4m3x8(const uint4& u, float inv) {
-  return make_uint2(e4m3x2(bf16lo(u.x) * inv, bf16hi(u.x) * inv) | (e4m3x2(bf16lo(u.y) * inv, bf16hi(u.y) * inv) << 16),
-                    e4m3x2(bf16lo(u.z) * inv, bf16hi(u.z) * inv) | (e4m3x2(bf16lo(u.w) * inv, bf16hi(u.w) * inv) << 16));
+// Eight values (four words of bf16) times inv (twice, as bf16: exact, a power
+// of two, but where the result is far below e4m3's smallest) -> eight codes.
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t w, uint32_t inv2) {
+  uint32_t t;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(w), "r"(inv2));
+  return e4m3x2(bf16lo(t), bf16hi(t));
+}
+__device__ __forceinline__ uint2 e4m3x8(const uint4& u, uint32_t inv2) {
+  return make_uint2(e4m3x2_of(u.x, inv2) | (e4m3x2_of(u.y, inv2) << 16),
+                    e4m3x2_of(u.z, inv2) | (e4m3x2_of(u.w, inv2) << 16));
 }
 // The word with every infinity made NaN (e4m3 has none, and saturating would hide them).
 __device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
@@ -169,11 +175,14 @@ __device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
   if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x400000u;
   return w;
 }
+// Largest magnitudes of the words' low and high halves (NaN left out), as bf16 pairs.
+__device__ __forceinline__ uint32_t max_abs_pair(uint32_t w, uint32_t m) {
+  asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.bf16x2 %0, %0, t;\n\t}" : "+r"(m) : "r"(w));
+  return m;
+}
 __device__ __forceinline__ float max_abs8(const uint4& u, float m) {
-  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.x))), fabsf(bf16hi(u.x)));
-  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.y))), fabsf(bf16hi(u.y)));
-  m = fmaxf(fmaxf(m, fabsf(bf16lo(u.z))), fabsf(bf16hi(u.z)));
-  return fmaxf(fmaxf(m, fabsf(bf16lo(u.w))), fabsf(bf16hi(u.w)));
+  const uint32_t p = max_abs_pair(u.w, max_abs_pair(u.z, max_abs_pair(u.y, max_abs_pair(u.x, 0u))));
+  return fmax3(m, bf16lo(p), bf16hi(p));
 }
 // One e4m3 pair -> two floats (through f16, which holds every e4m3 value).
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t u) {
@@ -246,9 +255,12 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
       unpack8(u[1], x + 8);
       rotate16<kInter, false>(x, ang);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (finite_only && fabsf(x[i]) == INFINITY) x[i] = NAN;
-        m = fmaxf(m, fabsf(x[i]));
+      for (int i = 0; i < 16; i += 2) {
+        if (finite_only) {
+          if (fabsf(x[i]) == INFINITY) x[i] = NAN;
+          if (fabsf(x[i + 1]) == INFINITY) x[i + 1] = NAN;
+        }
+        m = fmax3(m, fabsf(x[i]), fabsf(x[i + 1]));
       }
       u[0] = make_uint4(pack_odd(x[0], x[1]), pack_odd(x[2], x[3]), pack_odd(x[4], x[5]), pack_odd(x[6], x[7]));
       u[1] = make_uint4(pack_odd(x[8], x[9]), pack_odd(x[10], x[11]), pack_odd(x[12], x[13]), pack_odd(x[14], x[15]));
@@ -308,6 +320,7 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
   if (inf) amax = block_max(largest(true), 1);
   const float now = fmaxf(was, pow2(scale_exp(amax)));
   const float inv = 1.f / now;  // exact: a power of two
+  const uint32_t inv2 = pack_bf16x2(inv, inv);
   if (threadIdx.x == 0) *scale = now;
   if (lo > 0 && now != was) {
     const float f = was * inv;
@@ -322,8 +335,8 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
     }
   }
   auto put = [&](int r, const uint4 (&u)[2]) {
-    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.x) = e4m3x8(u[0], inv);
-    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.y) = e4m3x8(u[1], inv);
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.x) = e4m3x8(u[0], inv2);
+    *reinterpret_cast<uint2*>(dst + r * pitch + 8 * ch.y) = e4m3x8(u[1], inv2);
   };
   if (kKeep > 0) {
 #pragma unroll
