@@ -68,10 +68,11 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// One pair, or two at once (packed fp32 arithmetic): each product and sum
-// rounded by itself (no fused multiply-add), so the value that a cache's 8-bit
-// code is taken from does not depend on the compiler's contraction.  kBack: by
-// the negative angle (the transpose).
+// One pair, or two at once (packed products): each product and sum rounded by
+// itself (no fused multiply-add), so the value that a cache's 8-bit code is
+// taken from does not depend on the compiler's contraction.  kBack: by the
+// negative angle (the transpose).  The sums of two pairs are not packed: packed
+// products and sums were contracted in spite of their rounding modifiers.
 template <bool kBack>
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
   const float ac = __fmul_rn(a, c), bs = __fmul_rn(b, s), bc = __fmul_rn(b, c), as = __fmul_rn(a, s);
@@ -83,11 +84,10 @@ __device__ __forceinline__ void rotate_two(float* a, float* b, const float* c, c
   const float2 a2 = make_float2(a[0], a[1]), b2 = make_float2(b[0], b[1]), c2 = make_float2(c[0], c[1]),
                s2 = make_float2(s[0], s[1]);
   const float2 ac = fmul2(a2, c2), bs = fmul2(b2, s2), bc = fmul2(b2, c2), as = fmul2(a2, s2);
-  const float2 x = kBack ? fadd2(ac, bs) : sub2(ac, bs), y = kBack ? sub2(bc, as) : fadd2(bc, as);
-  a[0] = x.x;
-  a[1] = x.y;
-  b[0] = y.x;
-  b[1] = y.y;
+  a[0] = kBack ? __fadd_rn(ac.x, bs.x) : __fsub_rn(ac.x, bs.x);
+  a[1] = kBack ? __fadd_rn(ac.y, bs.y) : __fsub_rn(ac.y, bs.y);
+  b[0] = kBack ? __fsub_rn(bc.x, as.x) : __fadd_rn(bc.x, as.x);
+  b[1] = kBack ? __fsub_rn(bc.y, as.y) : __fadd_rn(bc.y, as.y);
 }
 
 // Rotates a thread's 16 values x (chunk 0 in x[0..7], chunk 1 in x[8..15]).
