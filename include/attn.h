@@ -289,6 +289,7 @@ ATTN_API size_t attn_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int H
  *            otherwise they must not overlap the inputs or each other;
  *   dq_weight, dk_weight: fp32 [d] out (written, not added to), NULL exactly
  *            where the weight is NULL; q (k) may be NULL where its weight is;
+ *            Hkv = 0 wants k_weight NULL;
  *   workspace: attn_qk_norm_rope_bwd_workspace_size bytes, 16-byte aligned,
  *            contents ignored; may be NULL when both weights are NULL.  Calls
  *            that may run at once (on other streams, in graphs replayed side
