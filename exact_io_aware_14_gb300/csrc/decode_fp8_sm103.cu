@@ -15,10 +15,13 @@
 // range of 2^31 below the row's largest value): with R rows the MMA has N =
 // 3R columns, the three terms of a row are added up in fp32 afterwards.
 // q is scaled by a power of two a row (largest value in [2^14, 2^15)).  The
-// weights p are formed with a running reference (moved only when a score
-// passes it by 2^4) and multiplied by the page's value scale over the split's
-// largest, times 2^10: at most 2^14, and what is lost is under 2^-27 of the
-// largest value for each key.
+// weights p = 2^(s - m) enter the second product as p v 2^10, v the page's
+// value scale over the split's largest.  The running reference m follows the
+// largest s + ceil(log2 v), not the largest score, and moves when a key passes
+// it by 4: so the largest p v 2^10 of a row is in (2^9, 2^14], however far the
+// pages' scales lie apart, and what e5m2 drops below 2^-17 is under 2^-26 of
+// it.  p itself, which only the sum of weights sees, may be as large as 2^104
+// (log2 v counts down to -100).
 //
 // Work items are (split of the keys, sequence, up to R query rows: heads of
 // one KV head's group times new tokens).  A fixed grid of CTAs takes them in
@@ -67,7 +70,7 @@ __device__ __forceinline__ void record(uint32_t site, uint32_t code) {
 
 constexpr int kTile = 128;     // keys per tile (MMA M of S, K of O^T)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr float kMoveLog2 = 4.f;      // the reference moves when a score passes it by this
+constexpr float kMoveLog2 = 4.f;      // the reference moves when a key passes it by this
 constexpr float kWeightScale = 1024.f;  // 2^10: weights up to 2^14, e5m2 ends at 57344
 
 template <int D, int R>
@@ -202,6 +205,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <int R, int kRows>
 __device__ __forceinline__ constexpr int column(int k, int r) {
   return r / kRows * 3 * kRows + k * kRows + r % kRows;
+}
+
+// ceil(log2 v) of wv = v * kWeightScale, v in [0, 1]; -100 at the least.
+__device__ __forceinline__ float log2_up(float wv) {
+  const uint32_t u = __float_as_uint(wv);
+  return static_cast<float>(max(static_cast<int>(u >> 23) - (127 + 10) + ((u & 0x7fffffu) != 0u ? 1 : 0), -100));
 }
 
 // Byte offset of row n, byte c of an operand with rows of D bytes, swizzled
@@ -356,6 +365,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const int key = t * kTile + row;
         const bool live = key < kn;
         const float ks = live ? it.ks[key >> 6] : 0.f, wv = live ? it.vs[key >> 6] : 0.f;
+        const float lift = log2_up(wv);  // what the key's scale adds to its score, as the reference sees it
         if (!wait_all(bar_s + buf, (g >> 1) & 1, abort_flag, 4)) failed = true;
         if (idle) {
           // (its columns of P and O^T are not looked at); looks at V are counted as the others count them
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
             return make_float2(__uint_as_float(u[k * kRows + 2 * r]), __uint_as_float(u[k * kRows + 2 * r + 1]));
           };
           x[r] = ffma2(fadd2(fadd2(at(0), at(1)), at(2)), fmul2(qm[r], ks2), nm[r]);
-          big = big || fmaxf(x[r].x, x[r].y) > kMoveLog2;  // (masked keys can only ask for the look below)
+          big = big || fmaxf(x[r].x, x[r].y) + lift > kMoveLog2;  // (masked keys can only ask for the look below)
         }
         float al[kRows];
 #pragma unroll
@@ -394,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           float top[kRows];
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
-            top[r] = (hidden >> r) & 1u ? -INFINITY : (r & 1 ? x[r / 2].y : x[r / 2].x);  // NaN scores show in p
+            top[r] = (hidden >> r) & 1u ? -INFINITY : (r & 1 ? x[r / 2].y : x[r / 2].x) + lift;  // NaN scores show in p
           const float mine = warp_max_rows(top);
           if (lane % (32 / kRows) == 0) red[w4 * kRows + lane / (32 / kRows)] = mine;
           if (lane == 0) fail[w4] = failed || *abort_flag;

@@ -371,7 +371,8 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  *            o must not overlap q;
  *   k_pages, v_pages [num_pages, page_size, Hkv, d] e4m3, 16-byte aligned;
  *   k_scales, v_scales fp32 [num_pages, Hkv], finite and >= 0 (any such value,
- *            not powers of two alone);
+ *            not powers of two alone; a page whose value scale is below 2^-100
+ *            of the largest in its split adds to o with fewer bits, or nothing);
  *   seqlens: device int32 [B], each in [0, max_blocks * page_size], the new
  *            tokens counted; codes behind a sequence's end reach no result,
  *            whatever they hold;

@@ -118,6 +118,44 @@ def test_value_scales_at_the_ends_of_the_range(size):
     S.assert_within(got[1], lse, el, "lse")
 
 
+@pytest.mark.parametrize("Hq,Hkv,Nq,d", [(4, 1, 1, 128), (8, 1, 1, 64), (12, 1, 1, 128), (8, 1, 3, 64)])
+@pytest.mark.parametrize("apart", [20, 27, 40, 60, 95])
+def test_value_scales_far_apart(Hq, Hkv, Nq, d, apart):
+    """Value scales 2^20 to 2^95 apart within a split, the softmax on the page with the smallest: its values are the
+    result as long as the others' weights leave them so, wherever the page lies."""
+    page, n, scale = 64, 400, d ** -0.5
+    for at in (0, 1, 2, 6):
+        g, pools, scales, table = _cache(1, Hkv, d, page, [n], 600 + at)
+        q = torch.randn((1, Nq, Hq, d), generator=g).abs().to(torch.bfloat16)
+        scales[0].fill_(2.0 ** -6)
+        pools[0][table[0, at], :min(page, n - at * page)] = 0x7E   # 448: scores higher by 40 or more
+        scales[1].fill_(1.0)
+        scales[1][table[0, at]] = 2.0 ** -apart
+        for chunk in (64, 128, 512):
+            o, lse = _run(q, pools, scales, table, [n], scale, chunk)
+            k, v = (S.paged_rows(p.view(torch.float8_e4m3fn).double() * s.double()[:, None, :, None], table, n)
+                    for p, s in zip(pools, scales))
+            vs = scales[1].double()[table[0].long()].repeat_interleave(page, 0)[:n, 0]
+            for i in range(Nq):
+                m = n - Nq + 1 + i
+                kk, vv = k[0, :m, 0], v[0, :m, 0]
+                for h in range(Hq):
+                    qq = q[0, i, h].double()
+                    s = scale * (kk @ qq)
+                    p = torch.softmax(s, 0)
+                    ds = 2.0 ** -23 * d * scale * float((kk.abs() @ qq.abs()).max())
+                    top = float((p * vs[:m]).max())   # the largest weight with its scale
+                    want = p @ vv
+                    # weights: 9 bits, moved by the scores' error; what e5m2 drops: 2^-26 of the largest weight for
+                    # each code; 2^-20 of the largest product for fp32 sums
+                    err = (2.0 ** -9 + 2 * ds) * (p @ vv.abs()) + 2.0 ** -26 * top * (vv.abs() / vs[:m, None]).sum(0) \
+                        + 2.0 ** -20 * top * 448
+                    S.assert_within(o[0, i, h], want, err + 2.0 ** -8 * (want.abs() + err),
+                                    "o, page %d, chunk %d, row %d, head %d" % (at, chunk, i, h))
+                    L = float(torch.logsumexp(s, 0))
+                    assert abs(float(lse[0, h, i]) - L) <= ds + 2.0 ** -20 * (1 + abs(L) + apart)
+
+
 def test_zero_scales():
     """Pages whose scale is zero hold zeros: their keys score 0 and add nothing to o."""
     lens = [300]
