@@ -71,6 +71,7 @@ __device__ __forceinline__ void record(uint32_t site, uint32_t code) {
 constexpr int kTile = 128;     // keys per tile (MMA M of S, K of O^T)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kMoveLog2 = 4.f;      // the reference moves when a key passes it by this
+constexpr int kNoKey = 0x7fffffff;
 constexpr float kWeightScale = 1024.f;  // 2^10: weights up to 2^14, e5m2 ends at 57344
 
 template <int D, int R>
@@ -105,13 +106,14 @@ struct Cfg {
   static constexpr int kOffRed = kOffAlpha + 2 * R * 4;     // [kGroups] float [4][kRows], then [kGroups] 4 flags
   static_assert(kRows == 4 || kRows == 8, "stored as words");
   static_assert(kOffRed % 16 == 0, "read four rows at a time");
-  static constexpr int kOffSpoil = kOffRed + 4 * R * 4 + kGroups * 16;  // byte [2][kTile]
-  static constexpr int kOffMl = kOffSpoil + 2 * kTile;      // [2] float m[R], l[4][R]
+  static constexpr int kOffNan = kOffRed + 4 * R * 4 + kGroups * 16;  // int [2][D]
+  static constexpr int kOffMl = kOffNan + 2 * D * 4;        // [2] float m[R], l[4][R]
   static constexpr int kOffBar = (kOffMl + 2 * 5 * R * 4 + 15) / 16 * 16;
-  static constexpr int kNumBars = 2 * kStages + 3 * kItems + 4 * 2 + 2 * 2 + 2 + 1;
+  static constexpr int kNumBars = 2 * kStages + 3 * kItems + 4 * 2 + 2 * 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "an SM's shared memory, 1 KB of it reserved for each CTA");
 };
 
 // One work item as the item warp hands it to the others.
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
   float* s_red = reinterpret_cast<float*>(smem + C::kOffRed);
   int* s_fail = reinterpret_cast<int*>(smem + C::kOffRed + 4 * R * 4);
-  volatile uint8_t* s_spoil = smem + C::kOffSpoil;
+  int* s_nan = reinterpret_cast<int*>(smem + C::kOffNan);  // first key of a tile whose value has a NaN in a dim
   float* s_ml = reinterpret_cast<float*>(smem + C::kOffMl);
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* bar_empty = bar_full + C::kStages;
@@ -265,8 +267,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   uint64_t* bar_of = bar_o + 2;                  // [2] O^T and alpha read (D / 32 output warps)
   uint64_t* bar_ml = bar_of + 2;                 // [2] an item's m and l are there (the softmax warps)
   uint64_t* bar_mf = bar_ml + 2;                 // [2] they were read (D / 32 output warps)
-  uint64_t* bar_sp = bar_mf + 2;                 // [2] group 0's look at the V rows that some rows do not see
-  uint64_t* bar_drain = bar_sp + 2;
+  uint64_t* bar_drain = bar_mf + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const uint32_t sQ = smem_u32(smem + C::kOffQ), sP = smem_u32(smem + C::kOffP);
@@ -292,7 +293,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         mbar_init(bar_of + i, D / 32);
         mbar_init(bar_ml + i, C::kSoftWarps);
         mbar_init(bar_mf + i, D / 32);
-        mbar_init(bar_sp + i, 4);
       }
       mbar_init(bar_drain, 1);
       *abort_flag = 0;
@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       const int n = 3 * R + i / kTile % (kPad / 4 + (kPad == 0)) * 4, buf = i / kTile / (kPad / 4 + (kPad == 0));
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(sP + buf * kN * kTile + p_at(n, i % kTile)), "r"(0u) : "memory");
     }
+    s_nan[tid - 32 * kOut0] = s_nan[D + tid - 32 * kOut0] = kNoKey;
     fence_proxy_async_smem();
   }
   // clustered: this split's result, in the place of the first stages
@@ -335,7 +336,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     const int grp = warp >> 2, w4 = warp & 3, row = tid & 127;  // rows grp * kRows ..; TMEM lane (key of a tile)
     float* red = s_red + grp * 4 * kRows;
     int* fail = s_fail + grp * 4;
-    int looks = 0;  // times that group 0 looked at V rows
     bool failed = false, stop = false;
     int g = 0;  // tiles so far, over all items
     for (int n = 0; !stop; ++n) {
@@ -368,9 +368,8 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         const float lift = log2_up(wv);  // what the key's scale adds to its score, as the reference sees it
         if (!wait_all(bar_s + buf, (g >> 1) & 1, abort_flag, 4)) failed = true;
         if (idle) {
-          // (its columns of P and O^T are not looked at); looks at V are counted as the others count them
+          // (its columns of P and O^T are not looked at)
           if (g >= 2 && !wait_all(bar_of + buf, ((g - 2) >> 1) & 1, abort_flag, 6)) failed = true;
-          if ((t + 1) * kTile > lim_min && lim_min < kn) ++looks;
           if (lane == 0) mbar_arrive(bar_p + buf);
           continue;  // also where a wait gave up: the group's warps leave together, at the next item
         }
@@ -443,46 +442,37 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
         }
         // P and alpha of this buffer are free once tile g-2 is added up
         if (g >= 2 && !wait_all(bar_of + buf, ((g - 2) >> 1) & 1, abort_flag, 6)) failed = true;
-        // rows of V past the sequence may hold anything: they are cleared, so
-        // that a weight of 0 adds exactly nothing.  A row that only some of the
-        // new tokens see is cleared too if it holds a NaN, which its weight
-        // then carries to the rows that do see it.  Group 0 does so and tells
-        // the other (whose next tile but one waits for this one's O^T).
-        float spoil = 0.f;
-        if (edge) {
-          if (grp == 0) {
-            // long done: S needed it
-            if (!wait_all(bar_full + s, (g / C::kStages) & 1, abort_flag, 5)) failed = true;
-            const uint32_t vrow = smem_u32(smem + s * C::kStage + C::kOffV);
-            bool clear = !live;
-            if (live && key >= lim_min) {
-              uint32_t nan = 0u;
+        // Rows of V past the sequence may hold anything: they are cleared, so
+        // that a weight of 0 adds exactly nothing.  In a row that only some of
+        // the new tokens see each NaN is cleared, and its dim noted with the
+        // first key for the output warps, who give it to the rows that see it.
+        // Group 0 does so (the MMA waits for every group).
+        if (edge && grp == 0) {
+          // long done: S needed it
+          if (!wait_all(bar_full + s, (g / C::kStages) & 1, abort_flag, 5)) failed = true;
+          const uint32_t vrow = smem_u32(smem + s * C::kStage + C::kOffV);
+          if (!live) {
 #pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                const uint4 v = ld_shared_v4(vrow + swizzled<D>(row, c));
-                nan |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                       ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-              }
+            for (int c = 0; c < D; c += 16) st_shared_v4(vrow + swizzled<D>(row, c), 0u, 0u, 0u, 0u);
+          } else if (key >= lim_min) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              const uint4 v = ld_shared_v4(vrow + swizzled<D>(row, c));
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, nan = 0u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
               if (nan & 0x80808080u) {
-                clear = true;
-                spoil = NAN;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  for (int k = 0; k < 4; ++k) {
+                    if (((w[i] >> (8 * k)) & 0x7fu) != 0x7fu) continue;
+                    atomicMin(s_nan + buf * D + c + 4 * i + k, key);
+                    w[i] &= ~(0xffu << (8 * k));
+                  }
+                }
+                st_shared_v4(vrow + swizzled<D>(row, c), w[0], w[1], w[2], w[3]);
               }
             }
-            if (clear) {
-#pragma unroll
-              for (int c = 0; c < D; c += 16) st_shared_v4(vrow + swizzled<D>(row, c), 0u, 0u, 0u, 0u);
-            }
-          }
-          if (C::kGroups > 1 && lim_min < kn) {
-            if (grp == 0) {
-              s_spoil[(looks & 1) * kTile + row] = spoil != spoil;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar_sp + (looks & 1));
-            } else {
-              if (!wait_all(bar_sp + (looks & 1), (looks >> 1) & 1, abort_flag, 19)) failed = true;
-              if (s_spoil[(looks & 1) * kTile + row]) spoil = NAN;
-            }
-            ++looks;
           }
         }
         const float2 wv2 = make_float2(wv, wv);
@@ -496,10 +486,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
           }
           l[r] = fadd2(l[r], pr);
           float2 w = fmul2(pr, wv2);
-          if (edge) {
-            if (!((hidden >> (2 * r)) & 1u)) w.x += spoil;
-            if (!((hidden >> (2 * r + 1)) & 1u)) w.y += spoil;
-          }
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const float2 tm = k < 2 ? make_float2(lead3(w.x), lead3(w.y)) : w;
@@ -577,6 +563,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
                      __uint_as_float(u[r]) + __uint_as_float(u[kRows + r]) + __uint_as_float(u[2 * kRows + r]));
         }
         tc_fence_before();
+        if ((t + 1) * kTile > it.lim_min && it.lim_min < it.kn) {  // NaN values that some rows see
+          const int first = s_nan[buf * D + dd];
+          if (first != kNoKey) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (first < it.lim[r]) acc[r] = NAN;
+            s_nan[buf * D + dd] = kNoKey;
+          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_of + buf);
       }

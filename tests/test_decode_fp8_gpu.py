@@ -291,6 +291,30 @@ def test_nan_among_the_new_tokens(Hq, Hkv):
     assert o[:, 2].isnan().all() and lse[..., 2].isnan().all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 128), (8, 1, 64), (24, 1, 128), (6, 3, 64)])
+@pytest.mark.parametrize("n,chunk", [(131, 128), (129, 128), (129, 64), (300, 512), (258, 128), (66, 64)])
+def test_nan_values_among_the_new_tokens_stay_in_their_dimension(Hq, Hkv, d, n, chunk):
+    """A NaN in a value that only some of the new tokens see: NaN in that dimension for those that see it, every other
+    value as if it were a number."""
+    Nq = 3
+    g, pools, scales, table = _cache(2, Hkv, d, 64, [n, 40], 85)
+    q = torch.randn((2, Nq, Hq, d), generator=g).to(torch.bfloat16)
+    G = Hq // Hkv
+    spots = [(n - 1, 17, 0), (n - 1, 63, Hkv - 1), (n - 2, 5, 0), (n - 2, 17, 0), (n - 4, 44, Hkv - 1)]
+    clean, bad = [p.clone() for p in pools], [p.clone() for p in pools]
+    hit = torch.zeros((2, Nq, Hq, d), dtype=torch.bool)
+    for j, c, h in spots:
+        clean[1][table[0, j // 64], j % 64, h, c] = 0
+        bad[1][table[0, j // 64], j % 64, h, c] = 0xFF if c == 17 else 0x7F
+        hit[0, max(0, j - (n - Nq)):, h * G:(h + 1) * G, c] = True
+    want = _run(q, clean, scales, table, [n, 40], 0.09, chunk)
+    o, lse = _run(q, bad, scales, table, [n, 40], 0.09, chunk)
+    o, w = o.cpu(), want[0].cpu()
+    assert o[hit].isnan().all()
+    assert torch.equal(o[~hit], w[~hit]) and torch.equal(lse, want[1])
+    assert _native.attn_get_device_status() == 0
+
+
 def test_bad_lengths_and_pages_are_reported():
     lens = [300, 200]
     g, pools, scales, table = _cache(2, 1, 128, 64, lens, 78)
