@@ -12,8 +12,9 @@
 // value is rounded once, and an older code whose page's scale is raised is
 // divided by a power of two: exact but for codes that fall below e4m3's
 // smallest normal value.  A page that starts with this call (its row 0 is
-// new) takes its scale from the new rows alone; otherwise
-// max(its scale, the new rows' scale).
+// new) takes its scale from the new rows alone; otherwise it is the larger of
+// its scale, taken up to the next power of two where it came from elsewhere
+// and is none, and the new rows' scale.
 // The scale has to be known before a code is written, so a block keeps its
 // rotated values in registers between the two: as bf16 rounded to odd (cut
 // off, the last bit set where anything was cut), from which rounding to
@@ -145,6 +146,11 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// The smallest power of two that is no less than x (0 stays 0; below 2^127).
+__device__ __forceinline__ float pow2_up(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x7fffffu) & 0x7f800000u);
+}
+
 // Two floats -> two e4m3 codes (nearest, ties to even), `lo` in the low byte;
 // NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -194,7 +200,7 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t u) {
       : "r"(h));
   return make_float2(lo, hi);
 }
-// Four codes times f (a power of two), rounded again.
+// Four codes times f (at most 1, a power of two but for a scale that was none), rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   const float2 a = from_e4m3x2(static_cast<uint16_t>(w & 0xffffu)), b = from_e4m3x2(static_cast<uint16_t>(w >> 16));
   return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(cons
   float amax = block_max(mine, 0);
   const bool inf = amax == INFINITY;  // rare: take the infinities out
   if (inf) amax = block_max(largest(true), 1);
-  const float now = fmaxf(was, pow2(scale_exp(amax)));
+  const float now = fmaxf(pow2_up(was), pow2(scale_exp(amax)));
   const float inv = 1.f / now;  // exact: a power of two
   const uint32_t inv2 = pack_bf16x2(inv, inv);
   if (threadIdx.x == 0) *scale = now;

@@ -324,8 +324,8 @@ ATTN_API attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_ou
  * [0, Nn], rows that do not fit the table (they are dropped) and page indices
  * outside [0, num_pages) (nothing is written there) are reported as
  * ATTN_ERR_DEVICE_ARG by attn_get_device_status.  A page that a call writes
- * to belongs to one sequence: where two of them list it, its new rows are
- * undefined.
+ * to belongs to one sequence: where two of them list it, what it holds after
+ * the call (in an 8-bit cache its older rows and its scale, too) is undefined.
  */
 ATTN_API attn_status attn_kvcache_append_paged(const void* k, long long k_stride, const void* v, long long v_stride,
                                                void* k_pages, void* v_pages, const int* block_table, int max_blocks,
@@ -342,7 +342,10 @@ ATTN_API attn_status attn_kvcache_append_paged(const void* k, long long k_stride
  * magnitude among the page's rows of that head.  A page whose row 0 is new
  * takes its scale from the new rows (whatever page and scale held before); a
  * page that the call continues keeps its scale, or has it raised and its
- * older codes divided by the same power of two and rounded again.  New values
+ * older codes divided by the same power of two and rounded again.  A scale
+ * written elsewhere (finite, in [0, 2^127]) is first taken up to the next power
+ * of two, at least 2^-100, the older codes multiplied by the quotient and
+ * rounded again.  New values
  * are rounded once, to nearest (ties to even), from the fp32 rotated value;
  * infinities and NaN are stored as NaN.
  */

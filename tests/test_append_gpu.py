@@ -1,5 +1,7 @@
 """GPU: appending keys and values to a paged cache, bf16 and e4m3, against the
 definition in 64 bits; rows that a call does not own stay as they were."""
+import math
+
 import pytest
 import torch
 
@@ -160,6 +162,42 @@ def test_append(fp8, B, Hkv, d, page, lens, Nn, new, rot, inter):
     _check(c, k, v, rope, inter, new, pools)
     n = new if new is not None else [Nn] * B
     assert after.tolist() == [a + b for a, b in zip(lens, n)]
+
+
+@pytest.mark.parametrize("was", [0.3, 1.0 / 448, 0.75 * 2.0 ** -9, 1.9e-31, 3e-38, 1e-41, 0.0])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_pages_with_scales_that_are_no_powers_of_two(was, rot):
+    """A page written elsewhere, its scale any number: the append takes the next power of two (2^-100 at least) for it,
+    multiplies the older codes by the quotient and rounds them once, and rounds the new values once."""
+    page, Hkv, d, Nn, lens = 64, 2, 64, 20, [10, 63]
+    c = Cache(2, Hkv, d, page, lens, 128, True, 19)
+    for s in c.scales:
+        s.fill_(was)
+    before = float(c.scales[0][0, 0])                      # as fp32 holds it
+    size = max(before, 2.0 ** -99)
+    k, v = ((torch.randn((2, Nn, Hkv, d), generator=c.g) * 60 * size).to(torch.bfloat16) for _ in range(2))
+    rope = _native.rope_table(200, rot, device="cpu") if rot else None
+    pools, _ = _run(c, k, v, rope, False)
+    assert _native.attn_get_device_status() == 0
+    up = 2.0 ** max(-100, math.ceil(math.log2(before)) if before else -100)
+    for t, x in enumerate((k, v)):
+        got, sc = pools[t].float().double().cpu(), pools[2 + t].double().cpu()
+        for b, L in enumerate(lens):
+            pg, m = int(c.table[b, 0]), min(Nn, page - L)
+            y = x[b, :m].double()
+            slack = torch.zeros((m, Hkv, 1), dtype=torch.float64)
+            if t == 0 and rot:
+                slack = 2.0 ** -22 * y.abs().amax(-1, keepdim=True)    # three fp32 roundings
+                y = S.rotate(y, *S.angles(rope, torch.arange(L, L + m)), False)
+            now = S.scale_for(y.abs().amax(dim=(0, 2))).clamp(min=up)
+            assert torch.equal(sc[pg], now)
+            # one rounding to e4m3 of a product that fp32 holds to 2^-24 of it
+            old = c.pools[t].view(torch.float8_e4m3fn).double()[pg, :L] * (before / now)[:, None]
+            err = torch.clamp(2.0 ** -4 * old.abs(), min=2.0 ** -10) * (1 + 2.0 ** -19)
+            assert ((got[pg, :L] - old).abs() <= err).all(), "older rows"
+            y, slack = y / now[:, None], slack / now[:, None]
+            err = torch.clamp(2.0 ** -4 * y.abs(), min=2.0 ** -10) + slack
+            assert ((got[pg, L:L + m] - y).abs() <= err).all(), "new rows"
 
 
 @pytest.mark.parametrize("grow", [1.0, 3.0, 1000.0, 1e30])
