@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   }
   // Combine within the cluster, through the CTAs' shared memory: rank k takes
   // rows k, k + cluster, ...  The arithmetic, in its order, is the combine
-  // kernel's (which has at most one split a warp for so few), so the same
+  // kernel's (which has at most one split a sum for so few), so the same
   // splits give the same bits either way.
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   auto peer = [](const void* at, int rank) {
@@ -1110,8 +1110,12 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 
 // LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s for each row of q.
 // A block of kWarps warps takes kCols columns of a row, a warp every
-// kWarps-th split, kBatch splits' loads in flight; the warps' sums are added
-// in a fixed order.  Many rows, or few splits: eight warps and the whole row.
+// kWarps-th split, kBatch splits' loads in flight.  Whatever the form, 32 sums
+// are kept, of the splits s, s + 32, ... each, and then added in order: a row's
+// bits depend on its own splits alone, not on the form that other rows or the
+// table's width ask for.  Many rows, or few splits: eight warps and the whole
+// row; with at most eight splits these have a sum each and the other 24 are left
+// out (1728 rows of up to 5 splits: the step takes 31.4 us so, 32.0 with all).
 // Few rows of many splits (a few long sequences): 32 warps for each 32
 // columns, as one block's loads are then what the step waits for (64 rows of
 // 512 splits: 39 us in whole rows by eight warps, 5 us so; 512 rows of 32
@@ -1119,8 +1123,10 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
 template <int D, int kCols, int kWarps, int kBatch>
 __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const DecodeFp8CombineParams p) {
   constexpr int kV = kCols / 32, kBlocks = D / kCols;
-  __shared__ float s_max[kWarps], s_tot[kWarps];
-  __shared__ float s_acc[kWarps][kCols];
+  constexpr int kSums = kBatch == 1 ? 1 : 32 / kWarps, kAll = kSums * kWarps;  // of a warp, of the block
+  static_assert(kBatch % kSums == 0, "split s of a batch belongs to sum s % 32");
+  __shared__ float s_max[kWarps], s_tot[kAll];
+  __shared__ float s_acc[kAll][kCols];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qrow = blockIdx.x / kBlocks, col0 = blockIdx.x % kBlocks * kCols;
   const int bi = qrow / p.Hq, hq = qrow - bi * p.Hq, b = bi / p.Nq, i = bi - b * p.Nq;
@@ -1167,29 +1173,45 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp8_combine_kernel(const D
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_max[w]);
   if (mx == -INFINITY) mx = 0.f;  // no key seen (or every LSE NaN): the weights are then 0 (NaN)
-  float tot = 0.f, acc[kV];
+  float tot[kSums], acc[kSums][kV];
 #pragma unroll
-  for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+  for (int i = 0; i < kSums; ++i) {
+    tot[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[i][k] = 0.f;
+  }
   for (int s = warp; s < ns; s += kBatch * kWarps) {
     if (s != warp) load(s);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const float w = expf(lv[u] - mx);
-      tot += w;
+      tot[u % kSums] += w;
 #pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] = fmaf(w, ov[u][k], acc[k]);
+      for (int k = 0; k < kV; ++k) acc[u % kSums][k] = fmaf(w, ov[u][k], acc[u % kSums][k]);
     }
   }
-  if (lane == 0) s_tot[warp] = tot;
 #pragma unroll
-  for (int k = 0; k < kV; ++k) s_acc[warp][kV * lane + k] = acc[k];
+  for (int i = 0; i < kSums; ++i) {
+    if (warp + i * kWarps >= ns) break;  // (0, not read)
+    if (lane == 0) s_tot[warp + i * kWarps] = tot[i];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) s_acc[warp + i * kWarps][kV * lane + k] = acc[i][k];
+  }
   __syncthreads();
   if (threadIdx.x >= kCols) return;
   float a = 0.f, sum = 0.f;
+  for (int i0 = 0; i0 < min(ns, kAll); i0 += 8) {  // the sums past the last split are 0
+    float av[8], tv[8];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    a += s_acc[w][threadIdx.x];
-    sum += s_tot[w];
+    for (int i = 0; i < 8; ++i) {
+      av[i] = i0 + i < ns ? s_acc[i0 + i][threadIdx.x] : 0.f;
+      tv[i] = i0 + i < ns ? s_tot[i0 + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a += av[i];
+      sum += tv[i];
+    }
   }
   const bool none = sum == 0.f;
   static_cast<__nv_bfloat16*>(p.o)[static_cast<long long>(qrow) * D + col0 + threadIdx.x] =
@@ -1237,6 +1259,7 @@ cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream
   const DecodeFp8CombineParams c = {p.o_part, p.lse_part, p.seqlens, p.o, p.lse, p.Nq, p.Hq, p.max_seqlen, p.chunk,
                                     p.n_split};
   const unsigned q_rows = static_cast<unsigned>(p.B) * p.Nq * p.Hq;
+  if (p.n_split <= 8) return launch_dependent(decode_fp8_combine_kernel<D, D, 8, 1>, dim3(q_rows), 256, 0, stream, c);
   if (q_rows >= 2u * sms || p.n_split <= 32)
     return launch_dependent(decode_fp8_combine_kernel<D, D, 8, 4>, dim3(q_rows), 256, 0, stream, c);
   return launch_dependent(decode_fp8_combine_kernel<D, 32, 32, 8>, dim3(q_rows * (D / 32)), 1024, 0, stream, c);

@@ -214,6 +214,51 @@ def test_splits_and_repeats():
     assert _native.attn_get_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [449, 600, 1500, 2048, 2113, 4200])
+def test_long_rows_do_not_depend_on_batch_or_table(d, n):
+    """A row of 8 to 66 splits: the same bits alone, among many rows and behind a wider table, and within its bounds."""
+    Hq, Hkv, chunk = 4, 2, 64
+    g, pools, scales, table = _cache(1, Hkv, d, 64, [n], 610 + n)
+    q = torch.randn((1, 1, Hq, d), generator=g).to(torch.bfloat16)
+    alone = _run(q, pools, scales, table, [n], 0.1, chunk)
+    _check(q, pools, scales, table, [n], 0.1, alone, "alone")
+    for cap in (n, 2112, 5000):
+        t = torch.zeros((1, max(table.shape[1], -(-cap // 64))), dtype=torch.int32)
+        t[:, :table.shape[1]] = table
+        wide = _run(q, pools, scales, t, [n], 0.1, chunk)
+        many = _run(q.repeat(160, 1, 1, 1), pools, scales, t.repeat(160, 1), [n] * 160, 0.1, chunk)
+        for a, b, c in zip(alone, wide, many):
+            assert torch.equal(a, b) and torch.equal(a.expand(160, *a.shape[1:]), c), "table of %d keys" % cap
+    assert _native.attn_get_device_status() == 0
+
+
+LONG = [
+    # B, Nq, Hq, Hkv, d, page, lens, chunk
+    (4, 1, 8, 2, 128, 64, [2200, 0, 40, 100], 64),      # 35 splits, few rows; neighbours of no, one and two splits
+    (4, 1, 8, 2, 64, 64, [4200, 0, 64, 65], 64),        # 66
+    (80, 1, 4, 2, 128, 64, [2200, 0, 40, 100] + [70] * 76, 64),   # more rows than twice the SMs: whole rows
+    (80, 1, 4, 2, 64, 128, [4200, 0, 64, 65] + [130] * 76, 64),
+    (2, 1, 2, 1, 128, 256, [17001, 16384], 64),         # 266 and 256 splits
+    (2, 3, 2, 2, 64, 64, [16500, 2], 64),               # 258; new tokens that see nothing beside it
+    (2, 1, 8, 2, 128, 64, [2100, 2048], 2048),          # a split of 32 pages
+    (1, 1, 24, 1, 64, 64, [4097], 2048),
+    (1, 1, 4, 1, 128, 256, [70001], None),              # far into a sequence
+    (1, 2, 3, 1, 64, 64, [66000], 1024),
+]
+
+
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,lens,chunk", LONG)
+def test_long_sequences(B, Nq, Hq, Hkv, d, page, lens, chunk):
+    """Many splits (each form of the combine, its second round of splits), splits of 2048 keys, long sequences."""
+    g, pools, scales, table = _cache(B, Hkv, d, page, lens, 620 + d + page)
+    q = torch.randn((B, Nq, Hq, d), generator=g).to(torch.bfloat16)
+    got = _run(q, pools, scales, table, lens, d ** -0.5, chunk)
+    assert _native.attn_get_device_status() == 0
+    few = B if B <= 4 else 4      # the neighbours behind the fourth are there for their number
+    _check(q[:few], pools, scales, table[:few], lens[:few], d ** -0.5, [x[:few] for x in got], "long")
+
+
 @pytest.mark.parametrize("Hq,Hkv,Nq,d", [(4, 1, 1, 128), (8, 1, 1, 64), (16, 1, 1, 128), (18, 1, 1, 64), (6, 2, 2, 64)])
 @pytest.mark.parametrize("cap,chunk", [(128, 64), (192, 64), (320, 64), (512, 64), (640, 128)])
 def test_clusters_of_splits(Hq, Hkv, Nq, d, cap, chunk):
