@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
   };
   auto position = [&](const Place& a) {
     if (p.rope.rot == 0 || a.nh == 0) return 0;
-    return p.positions ? __ldg(p.positions + a.token)
+    return p.positions ? p.positions[a.token]
                        : static_cast<int>(a.token - plan.by_N.div(a.token) * plan.by_N.d);
   };
   auto angles = [&](const Place& a, int pos, Angles& ang) {

@@ -33,8 +33,11 @@ struct Angles {
   float c[8], s[8];
 };
 
+// Ordinary loads: these kernels start while earlier ones, which may write what
+// is read here, still run, so nothing is constant over a kernel's time and no
+// load may be moved before grid_depends.
 __device__ __forceinline__ void load4(const float* p, float* r) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 v = *reinterpret_cast<const float4*>(p);
   r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
 }
 

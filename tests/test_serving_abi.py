@@ -3,6 +3,8 @@ the binding's own checks, and the plain forms that the GPU tests compare with
 (no GPU: every C call here returns before any CUDA call)."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -142,6 +144,15 @@ def test_decode_fp8_workspace_and_chunk(L):
         assert 64 <= c <= 2048 and c % 64 == 0
     assert L.attn_splitkv_fp8_chunk(0, 1, 8, 8, 64) == 0
     assert L.attn_splitkv_fp8_chunk(1, 1, 8, 3, 64) == 0
+
+
+def test_dependent_kernels_use_no_read_only_loads():
+    """Kernels that start while earlier ones run must not read through the read-only path, whose loads the compiler may
+    move before the wait and which wants memory that nothing writes while the kernel lives."""
+    csrc = os.path.dirname(native_build.LIB.replace("_build", "csrc"))
+    for name in ("qk_norm_rope_sm103.cu", "append_sm103.cu", "decode_fp8_sm103.cu", "rope.cuh", "ptx.cuh"):
+        text = open(os.path.join(csrc, name)).read()
+        assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", text), name
 
 
 def test_binding_refuses_tensors_off_the_gpu():

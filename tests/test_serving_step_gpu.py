@@ -135,3 +135,46 @@ def test_training_step():
         terms = (xr.abs() * gy.double().norm(dim=-1, keepdim=True)).reshape(-1, d).sum(0)
         S.assert_within(dw, w64, (2.0 ** -8 + 2.0 ** -16) * terms, "weight gradient")
     assert _native.attn_get_device_status() == 0
+
+
+def test_positions_written_by_earlier_kernels_of_the_chain():
+    """Steps in a row without any other kernel between them, so that each starts while the one before ends: the norms
+    take as positions the lengths that the append two launches earlier wrote."""
+    B, Hq, Hkv, d, page, steps = 40, 8, 2, 128, 64, 24
+    g = torch.Generator().manual_seed(92)
+    pools = [torch.zeros((B, page, Hkv, d), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    scales = [torch.zeros((B, Hkv), device="cuda") for _ in range(2)]
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    rope = _native.rope_table(page, d)
+    w = torch.ones(d, device="cuda")
+    qkv = torch.randn((B, 1, Hq + 2 * Hkv, d), generator=g).to(torch.bfloat16).cuda()
+    parts = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:]
+    lens = [torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+    def chain():
+        got = []
+        for t in range(steps):
+            before, after = lens[t % 2], lens[1 - t % 2]
+            q, k = _native.qk_norm_rope(parts[0], parts[1], w, w, 1e-6, rope, before.view(B, 1))
+            _native.kvcache_append_paged_fp8(k, parts[2], *pools, *scales, table, before, seqlens_out=after)
+            _native.decode_paged_fp8(q, *pools, *scales, table, after, 0.09)
+            got.append((q, k))
+        return got
+
+    want = [_native.qk_norm_rope(parts[0], parts[1], w, w, 1e-6, rope,
+                                 torch.full((B, 1), t, dtype=torch.int32, device="cuda")) for t in range(steps)]
+    first = chain()
+    lens[0].zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = chain()
+    for _ in range(3):
+        lens[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lens[0].tolist() == [steps] * B
+        for got in (first, again):
+            for a, b in zip(got, want):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert _native.attn_get_device_status() == 0
