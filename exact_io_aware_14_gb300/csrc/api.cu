@@ -311,16 +311,14 @@ attn_status attn_probe_read_bandwidth(const void* buf, size_t bytes, unsigned lo
 attn_status attn_get_device_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  uint32_t w_prefill = 0, w_decode = 0, w_selftest = 0, w_rope = 0, w_append = 0, w_fp8 = 0;
-  if (attn::fetch_status_prefill(s, &w_prefill) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (attn::fetch_status_decode(s, &w_decode) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (attn::fetch_status_selftest(s, &w_selftest) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (attn::fetch_status_rope(s, &w_rope) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (attn::fetch_status_append(s, &w_append) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  if (attn::fetch_status_decode_fp8(s, &w_fp8) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  attn::StatusWords words;
   uint32_t w = 0;
-  for (uint32_t x : {w_prefill, w_decode, w_selftest, w_fp8, w_append, w_rope})
-    if (!w) w = x;
+  if (attn::status_word_prefill(&words.at[0]) != cudaSuccess || attn::status_word_decode(&words.at[1]) != cudaSuccess ||
+      attn::status_word_selftest(&words.at[2]) != cudaSuccess ||
+      attn::status_word_decode_fp8(&words.at[3]) != cudaSuccess ||
+      attn::status_word_append(&words.at[4]) != cudaSuccess || attn::status_word_rope(&words.at[5]) != cudaSuccess ||
+      attn::fetch_status(words, s, &w) != cudaSuccess)
+    return ATTN_ERR_LAUNCH;
   switch (w & 0xffu) {
     case 0: return ATTN_OK;
     case attn::kDevTimeout: return ATTN_ERR_TIMEOUT;

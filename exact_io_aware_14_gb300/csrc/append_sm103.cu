@@ -404,13 +404,6 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   return p.d == 64 ? launch_bf16<64>(p, stream) : launch_bf16<128>(p, stream);
 }
 
-cudaError_t fetch_status_append(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_append_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyToSymbolAsync(g_append_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t status_word_append(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_append_status); }
 
 }  // namespace attn

@@ -1285,14 +1285,6 @@ cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream) {
   return p.d == 64 ? launch_d<64>(p, stream) : launch_d<128>(p, stream);
 }
 
-cudaError_t fetch_status_decode_fp8(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e =
-      cudaMemcpyFromSymbolAsync(out, g_decode_fp8_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyToSymbolAsync(g_decode_fp8_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t status_word_decode_fp8(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_decode_fp8_status); }
 
 }  // namespace attn

@@ -579,12 +579,6 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-cudaError_t fetch_status_decode(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_decode_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_decode_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t status_word_decode(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_decode_status); }
 
 }  // namespace attn

@@ -178,16 +178,22 @@ struct DecodeFp8Params {
 };
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream);
 
-// Reads and clears the device status word of each kernel unit (stream-ordered,
-// then synchronises the stream).  Returns the first non-zero word, or 0.
-cudaError_t fetch_status_prefill(cudaStream_t stream, uint32_t* out);
-cudaError_t fetch_status_decode(cudaStream_t stream, uint32_t* out);
+// Device status words, one a kernel unit, of the current device.
+cudaError_t status_word_prefill(uint32_t** at);
+cudaError_t status_word_decode(uint32_t** at);
+cudaError_t status_word_selftest(uint32_t** at);
+cudaError_t status_word_rope(uint32_t** at);
+cudaError_t status_word_append(uint32_t** at);
+cudaError_t status_word_decode_fp8(uint32_t** at);
+constexpr int kStatusUnits = 6;
+struct StatusWords {
+  uint32_t* at[kStatusUnits];
+};
+// Takes and clears them all on the stream, one round trip, and synchronises it:
+// the first that is not 0, in the order given, or 0.
+cudaError_t fetch_status(const StatusWords& words, cudaStream_t stream, uint32_t* out);
 cudaError_t launch_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_selftest_exp2_poly(const float* x, float* y, long long n, cudaStream_t stream);
 cudaError_t launch_read_probe(const void* buf, long long n16, unsigned long long* sink, cudaStream_t stream);
-cudaError_t fetch_status_selftest(cudaStream_t stream, uint32_t* out);
-cudaError_t fetch_status_rope(cudaStream_t stream, uint32_t* out);
-cudaError_t fetch_status_append(cudaStream_t stream, uint32_t* out);
-cudaError_t fetch_status_decode_fp8(cudaStream_t stream, uint32_t* out);
 
 }  // namespace attn

@@ -975,12 +975,6 @@ cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-cudaError_t fetch_status_prefill(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_prefill_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_prefill_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t status_word_prefill(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_prefill_status); }
 
 }  // namespace attn

@@ -411,13 +411,6 @@ cudaError_t launch_qk_norm_rope_bwd(const QkNormRopeParams& p, cudaStream_t stre
   return p.rope.inter ? launch_long<128, h, true, true>(p, stream) : launch_long<128, h, false, true>(p, stream);
 }
 
-cudaError_t fetch_status_rope(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_rope_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyToSymbolAsync(g_rope_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t status_word_rope(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_rope_status); }
 
 }  // namespace attn

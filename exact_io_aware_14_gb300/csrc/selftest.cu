@@ -9,6 +9,9 @@
 // attention kernels do; warp 1, waiting with the library's full 2 s limit,
 // must see that flag and give up at once.  Nothing faults, traps or spins
 // without a limit; the kernel returns and the context stays usable.
+// And the reading of the units' status words.
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "exp2_poly.cuh"
@@ -82,6 +85,20 @@ __global__ void __launch_bounds__(256) read_probe_kernel(const uint4* __restrict
   }
 }
 
+// Status words of the units, taken and cleared in one launch.  Calls at the
+// same time on several streams use a slot each.
+constexpr unsigned kStatusSlots = 64;
+__device__ uint32_t g_status_slots[kStatusSlots];
+
+__global__ void take_status_kernel(const StatusWords words, uint32_t* out) {
+  uint32_t first = 0;
+  for (int i = 0; i < kStatusUnits; ++i) {
+    const uint32_t w = atomicExch(words.at[i], 0u);
+    if (first == 0u) first = w;
+  }
+  *out = first;
+}
+
 }  // namespace
 
 cudaError_t launch_read_probe(const void* buf, long long n16, unsigned long long* sink, cudaStream_t stream) {
@@ -105,12 +122,19 @@ cudaError_t launch_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream)
   return cudaGetLastError();
 }
 
-cudaError_t fetch_status_selftest(cudaStream_t stream, uint32_t* out) {
-  uint32_t zero = 0;
-  cudaError_t e =
-      cudaMemcpyFromSymbolAsync(out, g_selftest_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyToSymbolAsync(g_selftest_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+cudaError_t status_word_selftest(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_selftest_status); }
+
+cudaError_t fetch_status(const StatusWords& words, cudaStream_t stream, uint32_t* out) {
+  static std::atomic<unsigned> turn{0};
+  const unsigned slot = turn.fetch_add(1, std::memory_order_relaxed) % kStatusSlots;
+  uint32_t* slots;
+  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&slots), g_status_slots);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = cfg.blockDim = dim3(1);
+  cfg.stream = stream;
+  e = cudaLaunchKernelEx(&cfg, take_status_kernel, words, slots + slot);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(out, slots + slot, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   return e;
 }

@@ -178,3 +178,29 @@ def test_positions_written_by_earlier_kernels_of_the_chain():
             for a, b in zip(got, want):
                 assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert _native.attn_get_device_status() == 0
+
+
+def test_status_is_read_in_one_round_trip():
+    """Problems of several kernel units are reported once and cleared together; a call costs a launch and one copy (under
+    two copies of a word as measured; six words read one after the other took nine), not a round trip a unit."""
+    import time
+    x = torch.randn((1, 1, 2, 64), device="cuda").to(torch.bfloat16)
+    _native.qk_norm_rope(x, None, None, None, rope=_native.rope_table(4, 64),
+                         positions=torch.tensor([[9]], dtype=torch.int32, device="cuda"))
+    pools = [torch.zeros((1, 64, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    _native.kvcache_append_paged(x, x, *pools, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                                 torch.tensor([64], dtype=torch.int32, device="cuda"))
+    assert _native.attn_get_device_status() == _native.ATTN_ERR_DEVICE_ARG
+    assert _native.attn_get_device_status() == 0
+    word = torch.zeros(1, device="cuda")
+
+    def least(f):
+        times = []
+        for _ in range(300):
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            f()
+            times.append(time.perf_counter() - t)
+        return min(times)
+
+    assert least(_native.attn_get_device_status) < 4 * least(word.item)
