@@ -362,11 +362,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, 
     """Norms of q and k for each head (weights fp32 [d]; None: no norm) and the position rotation, in one pass
     (attn_qk_norm_rope).  q [B,N,Hq,d], k [B,N,Hkv,d] (or None) bf16, possibly parts of a fused projection's rows;
     rope: (cos, sin) from rope_table, or None; positions int32 [B,N], or None for 0 .. N-1; out: (q_out, k_out) to
-    write to (q and k themselves where dense), or None.  Returns (q_out, k_out)."""
+    write to (q and k themselves where dense), or None.  Returns (q_out, k_out).  Differentiable in q, k and the weights
+    (qk_norm_rope_bwd runs in the backward pass); with out, no graph is recorded."""
     dev = _cuda_device(q)
     if stream is not None:
         with _on(stream, dev):
             return qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, interleaved, out)
+    if (q.requires_grad or (k is not None and k.requires_grad) or (q_weight is not None and q_weight.requires_grad)
+            or (k_weight is not None and k_weight.requires_grad)) and out is None and torch.is_grad_enabled():
+        return _QkNormRope.apply(q, k, q_weight, k_weight, eps, rope, positions, interleaved)
     q_shape = q.shape
     B, N, Hq, d = q_shape
     Hkv = 0 if k is None else k.shape[2]
@@ -386,6 +390,36 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, 
           _weight("k_weight", k_weight, d, dev), eps, *_rope_args(rope, interleaved, dev), pos, qo.data_ptr(),
           None if ko is None else ko.data_ptr(), B, N, Hq, Hkv, d)
     return qo, ko
+
+
+class _QkNormRope(torch.autograd.Function):
+    """qk_norm_rope as a node of the autograd graph."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, eps, rope, positions, interleaved):
+        outs = qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, interleaved)
+        if k is None or k.shape[2] == 0:
+            k_weight = None   # there is nothing to differentiate
+        cos, sin = (None, None) if rope is None else rope
+        # without a norm x does not enter its gradient
+        ctx.save_for_backward(None if q_weight is None else q, None if k_weight is None else k, q_weight, k_weight,
+                              cos, sin, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return outs
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        grads = qk_norm_rope_bwd(_dense(dq_out), None if dk_out is None else _dense(dk_out), q, k, q_weight, k_weight,
+                                 ctx.eps, None if cos is None else (cos, sin), positions, ctx.interleaved)
+        return (*grads, None, None, None, None)
+
+
+def _dense(t):
+    """t as the C calls want a tensor: contiguous, from a 16-byte boundary on."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def attn_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hkv, d):

@@ -183,6 +183,85 @@ def test_one_norm_only_and_gradients_in_place():
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot,inter,positions,extra", SHAPES)
+@pytest.mark.parametrize("which", ["q", "w", "all", "plain"])
+def test_gradients_through_autograd(B, N, Hq, Hkv, d, rot, inter, positions, extra, which):
+    """Outputs of inputs that require gradients carry a graph; its gradients are qk_norm_rope_bwd's, against the formula
+    in 64 bits: of the inputs alone, the weights alone, both, and of a rotation without norms."""
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, rot, 300 + N + d, positions, extra)
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+    x = [qc.detach(), kc.detach()]
+    w = [None, None] if which == "plain" else [wq.cuda(), wk.cuda()]
+    leaves = (x[:1] if which == "q" else x if which == "plain" else w if which == "w" else x + w)
+    for t in leaves:
+        t.requires_grad_()
+    p = None if pos is None else pos.cuda()
+    outs = _native.qk_norm_rope(*x, *w, 1e-6, _gpu(rope), p, inter)
+    assert all(o.requires_grad for o in outs)
+    with torch.no_grad():
+        plain = _native.qk_norm_rope(*x, *w, 1e-6, _gpu(rope), p, inter)
+    assert not any(o.requires_grad for o in plain) and all(torch.equal(a, b) for a, b in zip(outs, plain))
+    (outs[0].float() * gq.cuda().float()).sum().backward(retain_graph=True)    # one output's part alone
+    outs[1].backward(gk.cuda())                                               # and the other's added to it
+    for i, (t, wt, xc, wx, dy) in enumerate(((x[0], w[0], q, wq, gq), (x[1], w[1], k, wk, gk))):
+        dx, err, dw, size = S.norm_rope_bwd(dy, xc, None if which == "plain" else wx, 1e-6, cs, inter)
+        if t.requires_grad:
+            S.assert_within(t.grad, dx, 2.0 ** -8 * dx.abs() + err, "dx %d" % i)
+        else:
+            assert t.grad is None
+        if wt is not None and wt.requires_grad:
+            S.assert_within(wt.grad, dw, 2.0 ** -16 * size, "dw %d" % i)
+    assert _native.attn_get_device_status() == 0
+
+
+def test_autograd_edges():
+    """Gradients that are expanded, strided or off a 16-byte boundary, k left out or without heads, out=, a captured
+    step, and an input changed between the passes."""
+    d = 64
+    g = torch.Generator().manual_seed(31)
+    base = torch.randn((2, 5, 3, d), generator=g).to(torch.bfloat16).cuda()
+    w0 = (1 + 0.3 * torch.randn(d, generator=g)).cuda()
+    dy = torch.randn((2, 5, 3, d), generator=g).to(torch.bfloat16).cuda()
+
+    def grads(dy, k=None, kw=None):
+        q, w = base.clone().requires_grad_(), w0.clone().requires_grad_()
+        o, _ = _native.qk_norm_rope(q, k, w, kw)
+        return torch.autograd.grad(o, (q, w), dy)
+
+    want = _native.qk_norm_rope_bwd(dy, None, base, None, w0, None)
+    odd = torch.empty(dy.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view_as(dy).copy_(dy)
+    wide = torch.empty((2, 5, 3, 2 * d), dtype=torch.bfloat16, device="cuda")[..., :d].copy_(dy)
+    none = torch.empty((2, 5, 0, d), dtype=torch.bfloat16, device="cuda")
+    for got in (grads(dy), grads(odd), grads(wide), grads(dy, none, w0.clone().requires_grad_())):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[2])
+    one = torch.ones((1, 1, 1, 1), dtype=torch.bfloat16, device="cuda").expand_as(dy)
+    want1 = _native.qk_norm_rope_bwd(one.contiguous(), None, base, None, w0, None)
+    assert torch.equal(grads(one)[0], want1[0])
+    q = base.clone().requires_grad_()
+    o, _ = _native.qk_norm_rope(q, None, w0, None, out=(torch.empty_like(base), None))
+    assert not o.requires_grad
+    x = base.clone().requires_grad_()
+    y = x * 1
+    o, _ = _native.qk_norm_rope(y, None, w0, None)
+    with torch.no_grad():
+        y.zero_()
+    with pytest.raises(RuntimeError):
+        o.backward(dy)
+    q, w = base.clone().requires_grad_(), w0.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(_native.qk_norm_rope(q, None, w, None)[0], (q, w), dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(_native.qk_norm_rope(q, None, w, None)[0], (q, w), dy)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[2])
+
+
 def test_extreme_rows():
     """Rows of zeros, of the type's smallest and of large values; a row with NaN or an infinity spoils itself only."""
     d = 128
