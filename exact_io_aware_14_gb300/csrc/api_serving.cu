@@ -101,6 +101,8 @@ attn_status append(const void* k, long long k_stride, const void* v, long long v
                                 num_pages, seqlens, new_lens, seqlens_out, B, Nn, Hkv, d);
   if (st == ATTN_OK) st = check_rope(rope_cos, rope_sin, max_pos, rot_dim, interleaved, d);
   if (st != ATTN_OK) return st;
+  // a page's keys and values would be written over each other
+  if (Nn > 0 && (k_pages == v_pages || (k_scales && k_scales == v_scales))) return ATTN_ERR_INVALID_ARG;
   attn::AppendParams p;
   std::memset(&p, 0, sizeof p);
   p.k = k;

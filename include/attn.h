@@ -312,7 +312,8 @@ ATTN_API attn_status attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_ou
  *   k, v [B,Nn,Hkv,d] bf16, token rows k_stride and v_stride elements apart
  *            (as for attn_qk_norm_rope);
  *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, updated in place:
- *            rows other than the new tokens' are left as they are;
+ *            rows other than the new tokens' are left as they are; not the same
+ *            memory (nor k_scales and v_scales below);
  *   block_table: device int32 [B, max_blocks]; page_size: a multiple of 64;
  *   seqlens: device int32 [B], the lengths before the call;
  *   new_lens: device int32 [B], how many of the Nn rows of each sequence are

@@ -113,6 +113,13 @@ def test_append_fp8_wants_scales(L):
     assert _app(L, True, sv=18) == 3
 
 
+def test_append_refuses_one_memory_for_keys_and_values(L):
+    apart = dict(kp=1 << 30, vp=1 << 31, sk=1 << 20, sv=1 << 21)
+    assert _app(L, False, **dict(apart, vp=1 << 30)) == 1
+    assert _app(L, True, **dict(apart, vp=1 << 30)) == 1
+    assert _app(L, True, **dict(apart, sv=1 << 20)) == 1
+
+
 def _dec(L, **kw):
     a = dict(q=16, kp=16, vp=16, sk=16, sv=16, bt=16, mb=8, ps=256, npg=64, sl=16, o=16, lse=16, B=2, Nq=1, Hq=8,
              Hkv=2, d=128, scale=0.1, chunk=1024, ws=16, wsb=1 << 30)
