@@ -183,6 +183,81 @@ def test_one_norm_only_and_gradients_in_place():
         assert torch.equal(got, want)
 
 
+# past 2^21 values, where the forward pass takes the long form: four heads an item and one, each rotation
+LONG = [
+    # B, N, Hq, Hkv, d, rot, inter, positions, extra
+    (2, 900, 16, 4, 64, 64, False, True, 3),
+    (3, 1100, 9, 3, 64, 32, True, False, 2),
+    (2, 850, 16, 8, 64, 64, True, False, 0),
+    (2, 1400, 9, 3, 64, 48, False, False, 1),
+    (2, 450, 16, 4, 128, 128, True, False, 0),
+    (2, 850, 9, 1, 128, 48, True, True, 1),
+    (2, 900, 5, 5, 128, 32, False, False, 2),
+    (1, 1100, 20, 4, 128, 0, False, False, 0),
+    (1, 1701, 12, 0, 128, 96, False, True, 4),        # q alone
+]
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot,inter,positions,extra", LONG)
+@pytest.mark.parametrize("norms", ["both", "none", "q", "k"])
+def test_long_form(B, N, Hq, Hkv, d, rot, inter, positions, extra, norms):
+    """Forward and backward at sizes of the long form, with and without each norm."""
+    g, q, k, qc, kc, wq, wk, rope, pos, cs = _inputs(B, N, Hq, Hkv, d, rot, 400 + N + d, positions, extra, 2000)
+    gq, gk = (torch.randn((B, N, H, d), generator=g).to(torch.bfloat16) for H in (Hq, Hkv))
+    w = [wq if norms in ("both", "q") else None, wk if norms in ("both", "k") and Hkv else None]
+    wc = [None if t is None else t.cuda() for t in w]
+    r, p = _gpu(rope), None if pos is None else pos.cuda()
+    out = _native.qk_norm_rope(qc, kc if Hkv else None, *wc, 1e-6, r, p, inter)
+    back = _native.qk_norm_rope_bwd(gq.cuda(), gk.cuda() if Hkv else None, qc, kc if Hkv else None, *wc, 1e-6, r, p,
+                                    inter)
+    assert _native.attn_get_device_status() == 0
+    for i, (x, dy) in enumerate(((q, gq), (k, gk))[:2 if Hkv else 1]):
+        y, size = S.norm_rope(x, w[i], 1e-6, cs, inter)
+        S.assert_within(out[i], y, 2.0 ** -8 * y.abs() + 2.0 ** -20 * size, "y %d" % i)
+        dx, err, dw, size = S.norm_rope_bwd(dy, x, w[i], 1e-6, cs, inter)
+        S.assert_within(back[i], dx, 2.0 ** -8 * dx.abs() + err, "dx %d" % i)
+        if w[i] is not None:
+            S.assert_within(back[2 + i], dw, 2.0 ** -16 * size, "dw %d" % i)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,inter", [(24, 8, 128, False), (24, 8, 128, True), (27, 5, 128, False),
+                                            (27, 5, 128, True), (24, 8, 64, False), (24, 8, 64, True),
+                                            (27, 5, 64, False), (27, 5, 64, True), (53, 11, 64, False)])
+def test_past_the_second_level_cache(Hq, Hkv, d, inter):
+    """Tensors of more than 129 MB together, whose loads and stores are streamed: every row against 64 bits (formed on the
+    GPU, some tokens at a time), dw over all of them."""
+    B, N, rot = 4, 2101 * 128 // d, d if Hq % 2 == 0 else d // 2
+    positions = Hq % 4 == 0
+    gen = torch.Generator(device="cuda").manual_seed(40 + Hq + d)
+    x = torch.randn((B, N, Hq + Hkv + 1, d), generator=gen, device="cuda").to(torch.bfloat16)
+    xs = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv]
+    gs = [torch.randn((B, N, H, d), generator=gen, device="cuda").to(torch.bfloat16) for H in (Hq, Hkv)]
+    ws = [1 + 0.3 * torch.randn(d, generator=gen, device="cuda") for _ in range(2)]
+    rope = _native.rope_table(N, rot)
+    pos = torch.randint(0, N, (B, N), generator=gen, device="cuda", dtype=torch.int32) if positions else None
+    at = pos if positions else torch.arange(N, device="cuda").expand(B, N)
+    out = _native.qk_norm_rope(*xs, *ws, 1e-6, rope, pos, inter)
+    back = _native.qk_norm_rope_bwd(*gs, *xs, *ws, 1e-6, rope, pos, inter)
+    assert _native.attn_get_device_status() == 0
+
+    def close(got, want, bound, what):
+        bad = (got.double() - want).abs() > bound
+        assert not bad.any(), "%s: %d values outside their bound" % (what, int(bad.sum()))
+
+    for i in range(2):
+        sums = [0.0, 0.0]
+        for n in range(0, N, 300):
+            part = slice(n, n + 300)
+            cs = S.angles(rope, at[:, part])
+            y, size = S.norm_rope(xs[i][:, part], ws[i], 1e-6, cs, inter)
+            close(out[i][:, part], y, 2.0 ** -8 * y.abs() + 2.0 ** -20 * size, "y %d" % i)
+            dx, err, dw, size = S.norm_rope_bwd(gs[i][:, part], xs[i][:, part], ws[i], 1e-6, cs, inter)
+            close(back[i][:, part], dx, 2.0 ** -8 * dx.abs() + err, "dx %d" % i)
+            sums = [sums[0] + dw, sums[1] + size]
+        # under 256 fp32 additions between a term and the sum here too (under 60 rows a thread, 304 blocks)
+        close(back[2 + i], sums[0], 2.0 ** -16 * sums[1], "dw %d" % i)
+
+
 @pytest.mark.parametrize("B,N,Hq,Hkv,d,rot,inter,positions,extra", SHAPES)
 @pytest.mark.parametrize("which", ["q", "w", "all", "plain"])
 def test_gradients_through_autograd(B, N, Hq, Hkv, d, rot, inter, positions, extra, which):
