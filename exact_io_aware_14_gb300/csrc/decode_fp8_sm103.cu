@@ -298,9 +298,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
       *abort_flag = 0;
       mbar_fence_init();
     }
-  } else if (warp == kMmaWarp) {
-    tmem_alloc(s_tmem, C::kTmem);
-    tmem_relinquish();
   } else if (warp >= kOut0 && warp < kItemWarp) {
     // the MMA columns past 3R stay 0 in every Q and P
     constexpr int kPad = kN - 3 * R;
@@ -322,6 +319,15 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   int* s_part_row = reinterpret_cast<int*>(s_part_lse + R);  // rows of o, then entries of lse
   static_assert((R * D + 3 * R) * 4 <= C::kStages * C::kStage, "a split's result fits the stages");
 
+  // Launched as a programmatic dependent of whatever ran before: nothing of that
+  // is read before this wait, and no Tensor Memory is held during it (the kernel
+  // before may have CTAs that are still to ask for theirs), nor does the limit of
+  // any wait below run.
+  grid_wait();
+  if (warp == kMmaWarp) {
+    tmem_alloc(s_tmem, C::kTmem);
+    tmem_relinquish();
+  }
   uint32_t tmem = 0u;  // S at columns 0, kN; O^T at 2 kN, 3 kN
   if (warp < kItemWarp || warp >= kMmaWarp) {  // the item warps look for their first item before they join
     tc_fence_before();
@@ -640,9 +646,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
     // the same cache rows).  The lanes hold 32 sequences at a time; j only
     // grows, so they walk the batch once for the full splits and once for the
     // rest.
-    // launched as a programmatic dependent of whatever ran before: nothing of
-    // that is read before this wait
-    grid_wait();
     const int n_rblk = static_cast<int>(p.n_rblk.d), H = static_cast<int>(p.H.d), G = static_cast<int>(p.G.d);
     bool full_phase = true;
     int b0 = -32;
@@ -1026,7 +1029,6 @@ __global__ void __launch_bounds__(Cfg<D, R>::kThreads, Cfg<D, R>::kCtas)
   } else {
     // ================================================================ loads
     if (lane == 0) {
-      grid_wait();
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const Item<R>& it = items[n % C::kItems];

@@ -162,6 +162,14 @@ def test_dependent_kernels_use_no_read_only_loads():
         assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", text), name
 
 
+def test_tensor_memory_is_asked_for_after_the_wait():
+    """A kernel that starts while the one before it runs holds no Tensor Memory while it waits: that kernel may have CTAs
+    that still need some, and neither would go on."""
+    csrc = os.path.dirname(native_build.LIB.replace("_build", "csrc"))
+    text = open(os.path.join(csrc, "decode_fp8_sm103.cu")).read()
+    assert 0 < text.index("  grid_wait();") < text.index("  tmem_alloc(")
+
+
 def test_binding_refuses_tensors_off_the_gpu():
     x = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
