@@ -70,6 +70,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr double kLog2e = 1.4426950408889634;
 
+// Splits of max_seqlen keys (the sum may pass 31 bits).
+int split_count(int max_seqlen, int chunk) {
+  return static_cast<int>((max_seqlen + static_cast<long long>(chunk) - 1) / chunk);
+}
 size_t splitkv_part_elems(int B, int Hq, int n_split) {
   return static_cast<size_t>(B) * Hq * n_split;
 }
@@ -176,7 +180,7 @@ attn_status attn_fwd_kvcache(const void* q, const void* k_cache, const void* v_c
 
 size_t attn_splitkv_workspace_size(int B, int Hq, int max_seqlen, int d, int chunk) {
   if (B < 1 || Hq < 1 || max_seqlen < 1 || d < 1 || chunk < 64 || (chunk % 64) != 0) return 0;
-  const int n_split = (max_seqlen + chunk - 1) / chunk;
+  const int n_split = split_count(max_seqlen, chunk);
   const size_t parts = splitkv_part_elems(B, Hq, n_split);
   return round16(parts * d * sizeof(float)) + round16(parts * sizeof(float));
 }
@@ -234,7 +238,7 @@ attn_status splitkv(const void* q, const void* k, const void* v, const int* seql
                                    : (make_map(&p.tm_k, k, B, max_seqlen, Hkv, d, 64) &&
                                       make_map(&p.tm_v, v, B, max_seqlen, Hkv, d, 64));
   if (!ok_maps) return ATTN_ERR_LAUNCH;
-  p.n_split = (max_seqlen + chunk - 1) / chunk;
+  p.n_split = split_count(max_seqlen, chunk);
   const size_t parts = splitkv_part_elems(B, Hq, p.n_split);
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + round16(parts * d * sizeof(float)));

@@ -153,6 +153,14 @@ def test_decode_fp8_workspace_and_chunk(L):
     assert L.attn_splitkv_fp8_chunk(1, 1, 8, 3, 64) == 0
 
 
+def test_workspace_of_the_longest_tables(L):
+    """Capacities whose sum with the split length passes 31 bits."""
+    n = 2 ** 31 - 1
+    for chunk in (2048, 1 << 20):
+        splits = -(-n // chunk)
+        assert L.attn_splitkv_workspace_size(3, 2, n, 64, chunk) == 3 * 2 * splits * (64 + 1) * 4
+
+
 def test_dependent_kernels_use_no_read_only_loads():
     """Kernels that start while earlier ones run must not read through the read-only path, whose loads the compiler may
     move before the wait and which wants memory that nothing writes while the kernel lives."""
