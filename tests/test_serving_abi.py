@@ -239,6 +239,24 @@ def test_plain_scale_and_rounding():
     assert torch.equal(S.round_e4m3(x.double()).float(), x.to(torch.float8_e4m3fn).float())
 
 
+def test_rounding_to_odd_first_gives_the_nearest_code():
+    """What the append keeps between finding a page's scale and writing its codes: the fp32 value cut to bf16, the last bit
+    set where anything was cut.  Rounded to e4m3 it gives the code that the value itself gives, next to every border
+    between two codes and at random."""
+    codes = torch.arange(0, 0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    ties = torch.cat((codes, (codes[1:] + codes[:-1]) / 2, torch.tensor([448.5, 464.0]).double())).float()
+    bits = ties.view(torch.int32)[:, None] + torch.arange(-70000, 70001, 7, dtype=torch.int32)
+    bits = torch.cat((bits, ties.view(torch.int32)[:, None] + torch.arange(-9, 10, dtype=torch.int32)), 1).flatten()
+    x = bits[bits >= 0].view(torch.float32)
+    g = torch.Generator().manual_seed(6)
+    x = torch.cat((x[x <= 448.5], torch.rand(200000, generator=g) * 448, torch.randn(200000, generator=g) * 0.01))
+    for v in (x, -x):
+        u = v.view(torch.int32)
+        odd = (u & -65536) | ((u & 0xFFFF) != 0).int() * (1 << 16)
+        want = S.round_e4m3(v.double()).clamp(-448.0, 448.0)
+        assert torch.equal(S.round_e4m3(odd.view(torch.float32).double()).clamp(-448.0, 448.0), want)
+
+
 def test_plain_gradients_against_differences():
     """The formulas of the backward pass against central differences of the forward formula, in 64 bits."""
     g = torch.Generator().manual_seed(7)
