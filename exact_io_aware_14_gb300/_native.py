@@ -363,7 +363,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, rope=None, positions=None, 
     (attn_qk_norm_rope).  q [B,N,Hq,d], k [B,N,Hkv,d] (or None) bf16, possibly parts of a fused projection's rows;
     rope: (cos, sin) from rope_table, or None; positions int32 [B,N], or None for 0 .. N-1; out: (q_out, k_out) to
     write to (q and k themselves where dense), or None.  Returns (q_out, k_out).  Differentiable in q, k and the weights
-    (qk_norm_rope_bwd runs in the backward pass); with out, no graph is recorded."""
+    (qk_norm_rope_bwd runs in the backward pass); with out, no graph is recorded.  To capture a backward pass, capture its
+    forward pass with it, and keep no other graph of the same leaves, as for any torch operator."""
     dev = _cuda_device(q)
     if stream is not None:
         with _on(stream, dev):
@@ -507,7 +508,8 @@ def attn_splitkv_fp8_chunk(B, Nq, Hq, Hkv, max_seqlen):
 def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens, scale, chunk=None,
                      workspace=None, stream=None):
     """Attention of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over a paged float8_e4m3fn cache with
-    fp32 scales [num_pages, Hkv] (attn_fwd_splitkv_paged_fp8); chunk None: attn_splitkv_fp8_chunk's.
+    fp32 scales [num_pages, Hkv] (attn_fwd_splitkv_paged_fp8); chunk None: attn_splitkv_fp8_chunk's for the table's
+    capacity (one for the longest sequence suits short sequences in a wide table better).
     Returns (o, lse [B,Hq,Nq])."""
     dev = _cuda_device(q)
     if stream is not None:

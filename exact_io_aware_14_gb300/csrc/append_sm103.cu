@@ -208,13 +208,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 
 // kKeep: rows a thread keeps at most (the page has no more than kBlock * 16 /
 // D * kKeep new ones); 0: any number, read and rotated a second time for the
-// codes.  Four rows a thread and 64 registers, so that an SM holds 1024
-// threads, in the smallest blocks that hold a page's rows.  Measured on 49 K
+// codes.  Four rows a thread and 64 registers (60 to 64 bytes of them spilled),
+// so that an SM holds 1024 threads, in the smallest blocks that hold a page's
+// rows.  Measured on 49 K
 // new tokens, 8 heads, d = 128, pages of 64 / 128 / 256 rows: blocks of 128
 // threads 61 us / - / -, 256 threads 84 / 68 / -, 512 threads 144 / 97 / 74;
 // 256 threads with eight rows and 128 registers 124 / 91 / 75; rows read twice
 // 109 at 256; clusters of 128-thread blocks that exchange their largest values
-// - / 79 / 83.
+// - / 79 / 83.  Pages that the largest block does not hold are read twice: 512 and
+// 1024 rows of d = 128 105 and 120 us, 1024 rows of d = 64 53 (512 rows, kept: 38).
 template <int D, int kBlock, int kKeep, bool kInter>
 __global__ void __launch_bounds__(kBlock, 1024 / kBlock) append_e4m3_kernel(const AppendParams p) {
   grid_depends();

@@ -13,7 +13,10 @@
 // kind::f8f6f4 multiplies e4m3 by e5m2, so q and p are split into three e5m2
 // terms each (3 significant bits a term: 9 bits, more than bf16's 8, and a
 // range of 2^31 below the row's largest value): with R rows the MMA has N =
-// 3R columns, the three terms of a row are added up in fp32 afterwards.
+// 3R columns, the three terms of a row are added up in fp32 afterwards.  Four
+// terms a weight brought outputs from 0.0012 to 0.0004 of those with 32-bit
+// weights, under the 0.0017 of their own rounding to bf16, and took 58.2 us for
+// 57.2 on a serving batch, 107 for 100 where there are 24 rows (d = 128).
 // q is scaled by a power of two a row (largest value in [2^14, 2^15)).  The
 // weights p = 2^(s - m) enter the second product as p v 2^10, v the page's
 // value scale over the split's largest.  The running reference m follows the
@@ -46,9 +49,10 @@
 //              (pages are multiples of 64 rows)
 // Two tiles of S, P and O are in flight.
 //
-// Where the splits of a group of rows are two to eight and all CTAs fit the GPU
-// at once, they form a cluster instead, a CTA a split, and combine their
-// results through distributed shared memory: no second kernel.
+// Where the splits of a group of rows are two to eight and there is a place on an
+// SM for every CTA, they form a cluster instead, a CTA a split, and combine their
+// results through distributed shared memory: no second kernel.  (Clusters do not
+// wait for one another, so those that find no group of SMs free take their turn.)
 //
 // Combine kernel: LSE = ln sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.
 #include <atomic>
@@ -1246,7 +1250,7 @@ cudaError_t launch_rows(DecodeFp8Params p, int dev, int sms, cudaStream_t stream
   p.page = FastDiv(p.page_size);
   p.split = FastDiv(p.chunk);
   // Few splits and few of them in all: the splits of a group of rows form a
-  // cluster, which combines them itself; all CTAs are resident at once.
+  // cluster, which combines them itself; no more CTAs than places for them.
   int cluster = 1;
   while (cluster < p.n_split) cluster *= 2;
   const long long clustered = items / p.n_split * cluster;

@@ -267,8 +267,8 @@ ATTN_API attn_status attn_fwd_splitkv_noalloc(const void* q, const void* k_cache
  *   q_out [B,N,Hq,d], k_out [B,N,Hkv,d] bf16 out, dense.  q_out may be q, and
  *            k_out k, where that input is dense; otherwise they must not
  *            overlap the inputs (from first to last element) or each other.
- * Hkv = 0: q alone (k, k_out NULL).  The statistics are fp32, the result is
- * rounded once.  Constraints: B, Hq >= 1; N, Hkv >= 0 (Hkv need not divide
+ * Hkv = 0: q alone (k, k_out NULL).  The statistics are fp32 (squares too: values
+ * of a normed row below 2^60), the result is rounded once.  Constraints: B, Hq >= 1; N, Hkv >= 0 (Hkv need not divide
  * Hq); d in {64, 128}; tensors 16-byte aligned; Hq + Hkv at most 2^20 and
  * B * N * (Hq + Hkv) below 2^31 - 2^20.
  */
@@ -360,7 +360,11 @@ ATTN_API attn_status attn_kvcache_append_paged_fp8(const void* k, long long k_st
 
 /*
  * A split length (keys per split) that suits attn_fwd_splitkv_paged_fp8 for
- * these sizes; 0 for invalid arguments.  It depends on the arguments alone.
+ * these sizes, with max_seqlen the longest sequence; 0 for invalid arguments.  It
+ * depends on the arguments alone.  Given a table's capacity instead (a program
+ * that does not know its lengths, the Python binding by default), splits are as
+ * long as sequences that fill the table want them, and shorter sequences spread
+ * over fewer SMs.
  */
 ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seqlen);
 
@@ -372,7 +376,8 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  * keys 0 .. seqlens[b] - Nq + i (Nq = 1: the whole cache).
  *   q [B,Nq,Hq,d] bf16, Nq in [1, 64]; o [B,Nq,Hq,d] bf16 and lse [B,Hq,Nq]
  *            fp32 out; a row that sees no key gets O = 0 and LSE = -inf;
- *            o must not overlap q;
+ *            o must not overlap q; scores and sums of weights are fp32, the
+ *            weights enter the product with V with nine significant bits;
  *   k_pages, v_pages [num_pages, page_size, Hkv, d] e4m3, 16-byte aligned;
  *   k_scales, v_scales fp32 [num_pages, Hkv], finite and >= 0 (any such value,
  *            not powers of two alone; a page whose value scale is below 2^-100
@@ -385,7 +390,8 @@ ATTN_API int attn_splitkv_fp8_chunk(int B, int Nq, int Hq, int Hkv, int max_seql
  *   workspace: attn_splitkv_workspace_size(B, Nq * Hq, max_blocks * page_size,
  *            d, chunk) bytes, 16-byte aligned, contents ignored; one for each
  *            call that may run at once, as for attn_qk_norm_rope_bwd.
- * B * Nq * Hq times the splits of a sequence must stay below 2^31 - 4096.
+ * B and Nq * Hq are at most 65535, and B * Nq * Hq times the splits of a sequence
+ * stays below 2^31 - 4096.
  * Bad lengths and pages are handled as in attn_fwd_splitkv_paged.
  */
 ATTN_API attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
