@@ -337,6 +337,28 @@ def test_autograd_edges():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[2])
 
 
+def test_autograd_on_another_stream_and_without_tokens():
+    """stream=: the graph's gradients are formed on that stream; empty calls give zero gradients of the weights."""
+    d = 64
+    g = torch.Generator().manual_seed(32)
+    q0, dy = (torch.randn((2, 7, 4, d), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w0 = (1 + 0.3 * torch.randn(d, generator=g)).cuda()
+    want = _native.qk_norm_rope_bwd(dy, None, q0, None, w0, None)
+    q, w = q0.clone().requires_grad_(), w0.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, _ = _native.qk_norm_rope(q, None, w, None, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    o.backward(dy)
+    assert torch.equal(q.grad, want[0]) and torch.equal(w.grad, want[2])
+    e = torch.empty((2, 0, 4, d), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w.grad = None
+    o, _ = _native.qk_norm_rope(e, None, w, None)
+    o.sum().backward()
+    assert e.grad.shape == e.shape and w.grad.abs().max() == 0
+    assert _native.attn_get_device_status() == 0
+
+
 def test_extreme_rows():
     """Rows of zeros, of the type's smallest and of large values; a row with NaN or an infinity spoils itself only."""
     d = 128

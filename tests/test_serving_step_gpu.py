@@ -204,3 +204,31 @@ def test_status_is_read_in_one_round_trip():
         return min(times)
 
     assert least(_native.attn_get_device_status) < 4 * least(word.item)
+
+
+def test_prompt_behind_a_prefix_attended_in_blocks():
+    """A prompt appended in one call behind keys that are there already, then attended 64 new rows at a time."""
+    B, Hq, Hkv, d, page, L, n = 2, 6, 2, 64, 128, 40, 150
+    g = torch.Generator().manual_seed(93)
+    pools = [torch.full((4, page, Hkv, d), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    scales = [torch.zeros((4, Hkv), device="cuda") for _ in range(2)]
+    table = torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    after = torch.empty_like(lens)
+    for m in (L, n):
+        k, v = (torch.randn((B, m, Hkv, d), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+        _native.kvcache_append_paged_fp8(k, v, *pools, *scales, table, lens, seqlens_out=after)
+        lens, after = after, lens
+    q = torch.randn((B, n, Hq, d), generator=g).to(torch.bfloat16)
+    parts = []
+    for i in range(0, n, 64):
+        m = min(64, n - i)
+        parts.append(_native.decode_paged_fp8(q[:, i:i + m].contiguous().cuda(), *pools, *scales, table,
+                                              torch.full((B,), L + i + m, dtype=torch.int32, device="cuda"), 0.125))
+    assert _native.attn_get_device_status() == 0
+    k, v = (S.paged_rows(p.float().cpu().double() * s.cpu().double()[:, None, :, None], table.cpu(), L + n)
+            for p, s in zip(pools, scales))
+    o, lse, eo, el = S.decode(q, k, v, [L + n] * B, 0.125)
+    S.assert_within(torch.cat([p[0] for p in parts], 1), o, eo + 2.0 ** -8 * (o.abs() + eo), "o")
+    S.assert_within(torch.cat([p[1] for p in parts], 2), lse, el, "lse")
