@@ -211,7 +211,7 @@ def _plain_tables(s):
     # pages for the new tokens, sequence by sequence while they last
     need = -(-(keep + new) // page) - have
     ends = need.cumsum(0)
-    served = ends <= count
+    served = (need == 0) | (ends <= count)  # who wants no page gets its tokens in any case
     granted = torch.where(served, new, 0)
     j = (ends - need)[:, None] + (col - have[:, None])
     ok = served[:, None] & (col >= have[:, None]) & (col < (have + need)[:, None])
@@ -376,7 +376,7 @@ def _exact_tables(c):
     for b in range(c["B"]):
         first, end = -(-keep[b] // page), -(-(keep[b] + new[b]) // page)
         wanted += end - first
-        if wanted > have:
+        if wanted > have and end > first:
             granted.append(0)
             continue
         for blk in range(first, end):
