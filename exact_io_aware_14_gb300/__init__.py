@@ -10,13 +10,19 @@ from ._native import (  # noqa: F401
     attn_fwd_splitkv,
     attn_get_device_status,
     attn_splitkv_workspace_size,
+    attend_blocks_paged,
     decode,
     decode_paged_fp8,
+    decode_paged_shared,
     forward,
     kvcache_append_paged,
     kvcache_append_paged_fp8,
+    kvcache_bounds_paged,
+    kvcache_release_paged,
+    kvcache_reserve_paged,
     qk_norm_rope,
     qk_norm_rope_bwd,
     rope_table,
+    select_blocks_paged,
     status_string,
 )

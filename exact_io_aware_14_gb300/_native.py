@@ -95,6 +95,24 @@ def _open(path):
     L.attn_fwd_splitkv_paged_fp8.restype = i
     L.attn_fwd_splitkv_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, i, f, i, vp, sz,
                                              vp]
+    L.attn_kvcache_reserve_paged.restype = i
+    L.attn_kvcache_reserve_paged.argtypes = [vp, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, vp]
+    L.attn_kvcache_release_paged.restype = i
+    L.attn_kvcache_release_paged.argtypes = [vp, i, i, i, vp, vp, vp, vp, vp, i, vp]
+    L.attn_splitkv_paged_shared_workspace_size.restype = sz
+    L.attn_splitkv_paged_shared_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_fwd_splitkv_paged_shared.restype = i
+    L.attn_fwd_splitkv_paged_shared.argtypes = [vp, vp, vp, vp, i, i, i, vp, i, vp, vp, i, i, i, i, i, f, vp, sz, vp]
+    L.attn_kvcache_bounds_paged.restype = i
+    L.attn_kvcache_bounds_paged.argtypes = [vp, vp, vp, i, i, i, vp, vp, i, i, i, i, vp]
+    L.attn_select_blocks_workspace_size.restype = sz
+    L.attn_select_blocks_workspace_size.argtypes = [i, i, i, i]
+    L.attn_select_blocks_paged.restype = i
+    L.attn_select_blocks_paged.argtypes = [vp, vp, vp, i, i, i, vp, vp, i, i, i, i, i, i, i, i, vp, sz, vp]
+    L.attn_fwd_blocks_paged_workspace_size.restype = sz
+    L.attn_fwd_blocks_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_fwd_blocks_paged.restype = i
+    L.attn_fwd_blocks_paged.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, i, vp, vp, i, i, i, i, i, f, vp, sz, vp]
     L.attn_get_device_status.restype = i
     L.attn_get_device_status.argtypes = [vp]
     L.attn_selftest_wait_timeout.restype = i
@@ -539,6 +557,145 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqle
     _call("attn_fwd_splitkv_paged_fp8", dev, stream, *args, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
           scale, chunk, ws, n)
     return o, lse
+
+
+# --------------------------------------------------------------------------- operators on a paged cache
+def _table(block_table, seqlens, B, dev):
+    """(block_table, max_blocks, seqlens) as the C calls take them."""
+    max_blocks = block_table.shape[-1]
+    return (_need("block_table", block_table, _I32, (B, max_blocks), dev), max_blocks,
+            _need("seqlens", seqlens, _I32, (B,), dev))
+
+
+def kvcache_reserve_paged(block_table, seqlens, new_lens, free_pages, free_count, page_size, max_new, slots=True,
+                          seqlens_out=None, stream=None):
+    """Gives the sequences pages for their new tokens, on the GPU (attn_kvcache_reserve_paged): block_table int32
+    [B, max_blocks] is extended in place from the stack free_pages int32 [num_pages] with free_count int32 [1] valid
+    entries; seqlens int32 [B]: the tokens held; new_lens int32 [B]: how many more, at most max_new each (None: max_new
+    each); seqlens_out int32 [B]: receives the lengths with the new tokens.  Returns (granted int32 [B]: new_lens, 0
+    where the pages ran out, new slots int64 [B, max_new] of the tokens or None with slots=False, and the count of free
+    pages that remain, int32 [1])."""
+    dev = _cuda_device(block_table)
+    if stream is not None:
+        with _on(stream, dev):
+            return kvcache_reserve_paged(block_table, seqlens, new_lens, free_pages, free_count, page_size, max_new,
+                                         slots, seqlens_out)
+    B, num_pages = block_table.shape[0], free_pages.shape[0]
+    bt, max_blocks, sl = _table(block_table, seqlens, B, dev)
+    args = (None if new_lens is None else _need("new_lens", new_lens, _I32, (B,), dev),
+            _need("free_pages", free_pages, _I32, (num_pages,), dev),
+            _need("free_count", free_count, _I32, (1,), dev))
+    so = None if seqlens_out is None else _need("seqlens_out", seqlens_out, _I32, (B,), dev)
+    granted = torch.empty((B,), dtype=_I32, device=dev)
+    slot = torch.empty((B, max_new), dtype=torch.int64, device=dev) if slots else None
+    count = torch.empty((1,), dtype=_I32, device=dev)
+    _call("attn_kvcache_reserve_paged", dev, stream, bt, max_blocks, page_size, num_pages, sl, *args,
+          granted.data_ptr(), so, None if slot is None else slot.data_ptr(), count.data_ptr(), B, max_new)
+    return granted, slot, count
+
+
+def kvcache_release_paged(block_table, seqlens, keep_lens, free_pages, free_count, page_size, stream=None):
+    """Puts the pages behind the first keep_lens[b] of each sequence's seqlens[b] tokens back on the stack free_pages,
+    in place (attn_kvcache_release_paged).  Returns the new count of free pages, int32 [1]."""
+    dev = _cuda_device(block_table)
+    if stream is not None:
+        with _on(stream, dev):
+            return kvcache_release_paged(block_table, seqlens, keep_lens, free_pages, free_count, page_size)
+    B, num_pages = block_table.shape[0], free_pages.shape[0]
+    bt, max_blocks, sl = _table(block_table, seqlens, B, dev)
+    args = (_need("keep_lens", keep_lens, _I32, (B,), dev), _need("free_pages", free_pages, _I32, (num_pages,), dev),
+            _need("free_count", free_count, _I32, (1,), dev))
+    count = torch.empty((1,), dtype=_I32, device=dev)
+    _call("attn_kvcache_release_paged", dev, stream, bt, max_blocks, page_size, num_pages, sl, *args,
+          count.data_ptr(), B)
+    return count
+
+
+def _pools(q, k_pages, v_pages, block_table, seqlens, dev):
+    """The arguments that the attention calls over a paged bf16 cache share, and (page_size, Hkv)."""
+    B, Nq, Hq, d = q.shape
+    pools = k_pages.shape
+    if len(pools) != 4 or pools[3] != d:
+        raise ValueError("k_pages must be [num_pages, page_size, Hkv, %d] (got %s)" % (d, tuple(pools)))
+    bt, max_blocks, sl = _table(block_table, seqlens, B, dev)
+    return (_need("q", q, _BF16, q.shape, dev), _need("k_pages", k_pages, _BF16, pools, dev),
+            _need("v_pages", v_pages, _BF16, pools, dev), bt, max_blocks, pools[1], pools[0], sl), pools[2]
+
+
+def _attend(name, size, q, pools, Hkv, extra, scale, workspace, dev):
+    B, Nq, Hq, d = q.shape
+    o = torch.empty(q.shape, dtype=_BF16, device=dev)
+    lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
+    if workspace is None:
+        n = _fn(size)(B, Nq, Hq, Hkv, d)
+        workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+    ws, n = _space(workspace, dev)
+    _call(name, dev, None, *pools, *extra, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d, scale, ws, n)
+    return o, lse
+
+
+def decode_paged_shared(q, k_pages, v_pages, block_table, seqlens, shared_len, scale, workspace=None, stream=None):
+    """Attention of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over a paged bf16 cache whose first
+    shared_len keys (whole pages) all sequences have in common, the pages of row 0 of the block table
+    (attn_fwd_splitkv_paged_shared).  Returns (o, lse [B,Hq,Nq])."""
+    dev = _cuda_device(q)
+    if stream is not None:
+        with _on(stream, dev):
+            return decode_paged_shared(q, k_pages, v_pages, block_table, seqlens, shared_len, scale, workspace)
+    pools, Hkv = _pools(q, k_pages, v_pages, block_table, seqlens, dev)
+    return _attend("attn_fwd_splitkv_paged_shared", "attn_splitkv_paged_shared_workspace_size", q, pools, Hkv,
+                   (shared_len,), scale, workspace, dev)
+
+
+def kvcache_bounds_paged(k_pages, k_bounds, block_table, seqlens, max_new, new_lens=None, stream=None):
+    """Smallest and largest keys of the 64-key blocks that the last new_lens[b] (int32 [B]; None: max_new) of each
+    sequence's seqlens[b] tokens reach, into k_bounds [num_pages, page_size / 64, Hkv, 2, d] bf16 in place
+    (attn_kvcache_bounds_paged)."""
+    dev = _cuda_device(k_pages)
+    num_pages, page_size, Hkv, d = pools = k_pages.shape
+    B = block_table.shape[0]
+    bt, max_blocks, sl = _table(block_table, seqlens, B, dev)
+    _call("attn_kvcache_bounds_paged", dev, stream, _need("k_pages", k_pages, _BF16, pools, dev),
+          _need("k_bounds", k_bounds, _BF16, (num_pages, page_size // 64, Hkv, 2, d), dev), bt, max_blocks, page_size,
+          num_pages, sl, None if new_lens is None else _need("new_lens", new_lens, _I32, (B,), dev), B, max_new, Hkv, d)
+
+
+def select_blocks_paged(q, k_bounds, block_table, seqlens, topk, sink=1, local=1, workspace=None, stream=None):
+    """The topk blocks of 64 keys whose bounds allow the largest scores, for each of the last Nq tokens q [B,Nq,Hq,d]
+    of each sequence and each KV head: int32 [B, Nq, Hkv, topk], ascending, -1 behind the last; the first `sink` and
+    the last `local` blocks that a token sees are among them (attn_select_blocks_paged)."""
+    dev = _cuda_device(q)
+    if stream is not None:
+        with _on(stream, dev):
+            return select_blocks_paged(q, k_bounds, block_table, seqlens, topk, sink, local, workspace)
+    B, Nq, Hq, d = q.shape
+    shape = k_bounds.shape
+    if len(shape) != 5 or shape[3:] != (2, d):
+        raise ValueError("k_bounds must be [num_pages, page_size / 64, Hkv, 2, %d] (got %s)" % (d, tuple(shape)))
+    num_pages, page_size, Hkv = shape[0], 64 * shape[1], shape[2]
+    bt, max_blocks, sl = _table(block_table, seqlens, B, dev)
+    args = (_need("q", q, _BF16, q.shape, dev), _need("k_bounds", k_bounds, _BF16, shape, dev), bt, max_blocks,
+            page_size, num_pages, sl)
+    blocks = torch.empty((B, Nq, Hkv, topk), dtype=_I32, device=dev)
+    if workspace is None:
+        n = _fn("attn_select_blocks_workspace_size")(B, Nq, Hkv, min(max_blocks * page_size, 0x7fffffff))
+        workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+    ws, n = _space(workspace, dev)
+    _call("attn_select_blocks_paged", dev, None, *args, blocks.data_ptr(), B, Nq, Hq, Hkv, d, topk, sink, local, ws, n)
+    return blocks
+
+
+def attend_blocks_paged(q, k_pages, v_pages, block_table, seqlens, blocks, scale, workspace=None, stream=None):
+    """Attention of each of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over the 64-key blocks listed for
+    it and its KV head, blocks int32 [B, Nq, Hkv, n] (attn_fwd_blocks_paged).  Returns (o, lse [B,Hq,Nq])."""
+    dev = _cuda_device(q)
+    if stream is not None:
+        with _on(stream, dev):
+            return attend_blocks_paged(q, k_pages, v_pages, block_table, seqlens, blocks, scale, workspace)
+    pools, Hkv = _pools(q, k_pages, v_pages, block_table, seqlens, dev)
+    n_sel = blocks.shape[-1]
+    return _attend("attn_fwd_blocks_paged", "attn_fwd_blocks_paged_workspace_size", q, pools, Hkv,
+                   (_need("blocks", blocks, _I32, q.shape[:2] + (Hkv, n_sel), dev), n_sel), scale, workspace, dev)
 
 
 def attn_get_device_status(stream=None):

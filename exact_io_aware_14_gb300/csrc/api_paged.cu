@@ -1,0 +1,311 @@
+// extern "C" boundary of the operators on a paged cache beyond one decode
+// step: block tables from request lengths, decode behind a shared prefix, key
+// bounds, block selection and attention over selected blocks.  Argument checks
+// and dispatch; declared in include/attn.h.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "launch.h"
+
+namespace {
+
+constexpr long long kIntMax = 0x7fffffffLL;
+constexpr double kLog2e = 1.4426950408889634;
+
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+// Memory of n bytes at p; empty where p is NULL.
+struct Extent {
+  uintptr_t at, end;
+};
+Extent bytes_at(const void* p, long long n) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, p && n > 0 ? at + static_cast<uintptr_t>(n) : at};
+}
+bool overlap(const Extent& a, const Extent& b) { return a.at < b.end && b.at < a.end; }
+// Whether one of the first `outs` overlaps another of the n.
+bool outputs_overlap(const Extent* e, int outs, int n) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(e[i], e[j])) return true;
+  return false;
+}
+
+// A block table [B, max_blocks] of pages of page_size rows.
+attn_status check_table(const int* block_table, int max_blocks, int page_size, int num_pages, const int* seqlens,
+                        int B, long long extra) {
+  if (B < 1 || max_blocks < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (page_size < 64 || page_size % 64 != 0) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks) * page_size + extra + 256 > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (!block_table || !seqlens) return ATTN_ERR_INVALID_ARG;
+  if (off(block_table, 4) || off(seqlens, 4)) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+attn_status check_paging(const int* block_table, int max_blocks, int page_size, int num_pages, const int* seqlens,
+                         const int* lens, const int* free_pages, const int* free_count, const int* free_count_out,
+                         int B, int Nn) {
+  if (Nn < 0) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_table(block_table, max_blocks, page_size, num_pages, seqlens, B, Nn);
+  if (st != ATTN_OK) return st;
+  if (!free_pages || !free_count || !free_count_out) return ATTN_ERR_INVALID_ARG;
+  if (off(lens, 4) || off(free_pages, 4) || off(free_count, 4) || off(free_count_out, 4)) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+attn_status check_heads(int Nq, int Hq, int Hkv, int d) {
+  if (Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Tokens of a launch of the selection: at most 2^26 scores, 65535 tokens (the
+// grid's z).
+long long select_tokens(int B, int Nq, int Hkv, long long n_blocks) {
+  const long long tokens = static_cast<long long>(B) * Nq;
+  long long t = (1LL << 26) / (Hkv * n_blocks);
+  t = t < 1 ? 1 : (t > 65535 ? 65535 : t);
+  return t < tokens ? t : tokens;
+}
+long long select_chunks(long long n_blocks) { return (n_blocks + attn::kSelectChunk - 1) / attn::kSelectChunk; }
+
+// The arguments that both attention calls share.
+attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                            int max_blocks, int page_size, int num_pages, const int* seqlens, const void* o,
+                            const float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale) {
+  attn_status st = check_heads(Nq, Hq, Hkv, d);
+  if (st == ATTN_OK) st = check_table(block_table, max_blocks, page_size, num_pages, seqlens, B, Nq);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;  // a token's heads of a group fit one tile of rows
+  if (static_cast<long long>(B) * Nq * Hq > kIntMax - 4096) return ATTN_ERR_UNSUPPORTED;
+  if (!q || !k_pages || !v_pages || !o || !lse) return ATTN_ERR_INVALID_ARG;
+  if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(o, 16) || off(lse, 4)) return ATTN_ERR_MISALIGNED;
+  const long long rows = static_cast<long long>(B) * Nq * Hq;
+  if (overlap(bytes_at(q, 2 * rows * d), bytes_at(o, 2 * rows * d))) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn::RowsParams rows_params(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                             int max_blocks, int page_size, int num_pages, const int* seqlens, void* o, float* lse,
+                             int B, int Nq, int Hq, int Hkv, int d, float scale) {
+  attn::RowsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.o = o;
+  p.lse = lse;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_kvcache_reserve_paged(int* block_table, int max_blocks, int page_size, int num_pages,
+                                       const int* seqlens, const int* new_lens, const int* free_pages,
+                                       const int* free_count, int* new_lens_out, int* seqlens_out, long long* slots,
+                                       int* free_count_out, int B, int Nn, void* stream) {
+  const attn_status st = check_paging(block_table, max_blocks, page_size, num_pages, seqlens, new_lens, free_pages,
+                                      free_count, free_count_out, B, Nn);
+  if (st != ATTN_OK) return st;
+  if (!new_lens_out) return ATTN_ERR_INVALID_ARG;
+  if (off(new_lens_out, 4) || off(seqlens_out, 4) || off(slots, 8)) return ATTN_ERR_MISALIGNED;
+  const Extent e[] = {bytes_at(block_table, 4LL * B * max_blocks), bytes_at(new_lens_out, 4LL * B),
+                      bytes_at(seqlens_out, 4LL * B), bytes_at(slots, 8LL * B * Nn), bytes_at(free_count_out, 4),
+                      bytes_at(seqlens, 4LL * B), bytes_at(new_lens, 4LL * B), bytes_at(free_pages, 4LL * num_pages),
+                      bytes_at(free_count, 4)};
+  if (outputs_overlap(e, 5, 9)) return ATTN_ERR_INVALID_ARG;
+  attn::PagingParams p;
+  std::memset(&p, 0, sizeof p);
+  p.seqlens = seqlens;
+  p.new_lens = new_lens;
+  p.free_count = free_count;
+  p.free_pages = free_pages;
+  p.block_table = block_table;
+  p.seqlens_out = seqlens_out;
+  p.new_lens_out = new_lens_out;
+  p.free_count_out = free_count_out;
+  p.slots = Nn > 0 ? slots : nullptr;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nn = Nn;
+  return attn::launch_reserve(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+attn_status attn_kvcache_release_paged(const int* block_table, int max_blocks, int page_size, int num_pages,
+                                       const int* seqlens, const int* keep_lens, int* free_pages,
+                                       const int* free_count, int* free_count_out, int B, void* stream) {
+  const attn_status st = check_paging(block_table, max_blocks, page_size, num_pages, seqlens, keep_lens, free_pages,
+                                      free_count, free_count_out, B, 0);
+  if (st != ATTN_OK) return st;
+  if (!keep_lens) return ATTN_ERR_INVALID_ARG;
+  const Extent e[] = {bytes_at(free_pages, 4LL * num_pages), bytes_at(free_count_out, 4),
+                      bytes_at(block_table, 4LL * B * max_blocks), bytes_at(seqlens, 4LL * B),
+                      bytes_at(keep_lens, 4LL * B), bytes_at(free_count, 4)};
+  if (outputs_overlap(e, 2, 6)) return ATTN_ERR_INVALID_ARG;
+  attn::PagingParams p;
+  std::memset(&p, 0, sizeof p);
+  p.seqlens = seqlens;
+  p.new_lens = keep_lens;
+  p.free_count = free_count;
+  p.free_list = free_pages;
+  p.block_table = const_cast<int*>(block_table);
+  p.free_count_out = free_count_out;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  return attn::launch_release(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_bounds, const int* block_table, int max_blocks,
+                                      int page_size, int num_pages, const int* seqlens, const int* new_lens, int B,
+                                      int Nn, int Hkv, int d, void* stream) {
+  if (Nn < 0 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const attn_status st = check_table(block_table, max_blocks, page_size, num_pages, seqlens, B, Nn);
+  if (st != ATTN_OK) return st;
+  if (Hkv > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  const long long slabs = (static_cast<long long>(Hkv) * d + 511) / 512;
+  if ((static_cast<long long>(Nn) / 64 + 2) * slabs > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (!k_pages || !k_bounds) return ATTN_ERR_INVALID_ARG;
+  if (off(k_pages, 16) || off(k_bounds, 16) || off(new_lens, 4)) return ATTN_ERR_MISALIGNED;
+  const long long row = 2LL * Hkv * d, rows = static_cast<long long>(num_pages) * page_size;
+  if (overlap(bytes_at(k_pages, rows * row), bytes_at(k_bounds, rows / 64 * 2 * row))) return ATTN_ERR_INVALID_ARG;
+  if (Nn == 0) return ATTN_OK;
+  attn::KeyBoundsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.k_pages = k_pages;
+  p.k_bounds = k_bounds;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.new_lens = new_lens;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nn = Nn;
+  p.Hkv = Hkv;
+  p.d = d;
+  return attn::launch_key_bounds(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+size_t attn_select_blocks_workspace_size(int B, int Nq, int Hkv, int max_seqlen) {
+  if (B < 1 || Nq < 1 || Hkv < 1 || max_seqlen < 64) return 0;
+  const long long n = max_seqlen / 64;
+  return static_cast<size_t>(select_tokens(B, Nq, Hkv, n)) * Hkv * (n + select_chunks(n)) * sizeof(float);
+}
+
+attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const int* block_table, int max_blocks,
+                                     int page_size, int num_pages, const int* seqlens, int* blocks, int B, int Nq,
+                                     int Hq, int Hkv, int d, int topk, int sink, int local, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  attn_status st = check_heads(Nq, Hq, Hkv, d);
+  if (st == ATTN_OK) st = check_table(block_table, max_blocks, page_size, num_pages, seqlens, B, Nq);
+  if (st != ATTN_OK) return st;
+  if (topk < 1 || sink < 0 || local < 0 || static_cast<long long>(sink) + local > topk) return ATTN_ERR_INVALID_ARG;
+  const long long tokens = static_cast<long long>(B) * Nq;
+  if (Hkv > 65535 || tokens > kIntMax || tokens * Hkv > kIntMax) return ATTN_ERR_UNSUPPORTED;
+  if (!q || !k_bounds || !blocks) return ATTN_ERR_INVALID_ARG;
+  if (off(q, 16) || off(k_bounds, 16) || off(blocks, 4)) return ATTN_ERR_MISALIGNED;
+  const long long cap = static_cast<long long>(max_blocks) * page_size;
+  const long long n = cap / 64;
+  if (!workspace || off(workspace, 16) ||
+      workspace_bytes < attn_select_blocks_workspace_size(B, Nq, Hkv, static_cast<int>(cap)))
+    return ATTN_ERR_WORKSPACE;
+  attn::SelectParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q;
+  p.k_bounds = k_bounds;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.blocks = blocks;
+  p.max_blocks = max_blocks;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.topk = topk;
+  p.sink = sink;
+  p.local = local;
+  p.n_blocks = static_cast<int>(n);
+  p.n_chunks = static_cast<int>(select_chunks(n));
+  const long long step = select_tokens(B, Nq, Hkv, n);
+  p.scores = static_cast<float*>(workspace);
+  p.err = p.scores + step * Hkv * n;
+  for (long long t = 0; t < tokens; t += step) {
+    const int m = static_cast<int>(tokens - t < step ? tokens - t : step);
+    if (attn::launch_select(p, static_cast<int>(t), m, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return ATTN_ERR_LAUNCH;
+  }
+  return ATTN_OK;
+}
+
+size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
+  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK) return 0;
+  return 16;
+}
+
+attn_status attn_fwd_blocks_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                  int max_blocks, int page_size, int num_pages, const int* seqlens, const int* blocks,
+                                  int n_sel, void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  const attn_status st = check_rows_args(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens,
+                                         o, lse, B, Nq, Hq, Hkv, d, scale);
+  if (st != ATTN_OK) return st;
+  if (n_sel < 1 || !blocks) return ATTN_ERR_INVALID_ARG;
+  if (off(blocks, 4)) return ATTN_ERR_MISALIGNED;
+  if (!workspace || off(workspace, 16) || workspace_bytes < attn_fwd_blocks_paged_workspace_size(B, Nq, Hq, Hkv, d))
+    return ATTN_ERR_WORKSPACE;
+  attn::RowsParams p = rows_params(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, o, lse,
+                                   B, Nq, Hq, Hkv, d, scale);
+  p.blocks = blocks;
+  p.n_sel = n_sel;
+  return attn::launch_rows(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
+  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK) return 0;
+  return 16;
+}
+
+attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_pages, const void* v_pages,
+                                          const int* block_table, int max_blocks, int page_size, int num_pages,
+                                          const int* seqlens, int shared_len, void* o, float* lse, int B, int Nq,
+                                          int Hq, int Hkv, int d, float scale, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  const attn_status st = check_rows_args(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens,
+                                         o, lse, B, Nq, Hq, Hkv, d, scale);
+  if (st != ATTN_OK) return st;
+  if (shared_len < 0 || shared_len % page_size != 0 || shared_len / page_size > max_blocks) return ATTN_ERR_INVALID_ARG;
+  if (!workspace || off(workspace, 16) || workspace_bytes < attn_splitkv_paged_shared_workspace_size(B, Nq, Hq, Hkv, d))
+    return ATTN_ERR_WORKSPACE;
+  attn::RowsParams p = rows_params(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, o, lse,
+                                   B, Nq, Hq, Hkv, d, scale);
+  p.shared_len = shared_len;
+  return attn::launch_rows(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,504 @@
+// Which blocks of a paged cache a query attends to, for sm_103a: bounds of
+// the keys of each 64-key block, the scores that they allow, and the choice of
+// the largest ones.
+//
+// Bounds: lo_i = min, hi_i = max over the block's keys of channel i; exact in
+// bf16, whatever the order of the keys.
+//
+// Score of block j for a query row of one KV head, with q+ = max(q, 0) and
+// q- = min(q, 0) for each of the group's heads:
+//     score(j) = max over heads of sum_i (q+_i hi_ij + q-_i lo_ij),
+// no key of the block has a larger <q, k>.
+//
+// Choice: the row's first `sink` and last `local` blocks, then the largest
+// scores, the lower index first among equals; the order is that of the scores
+// in 64 bits.  The scores are formed in fp32 first.  With A = max_j sum |terms|
+// an fp32 score is off by at most E = 2^-19 A (each sum rounds no partial sum
+// more than 32 times, 2^-24 of it each), so a block is in where its score is
+// above the k-th largest T by more than 2 E, out where it is that far below,
+// and only the few in between are scored again in 64 bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace attn {
+namespace {
+
+__device__ uint32_t g_select_status;
+
+__device__ __forceinline__ void record(uint32_t site, uint32_t code) {
+  atomicCAS(&g_select_status, 0u, (site << 8) | code);
+}
+
+constexpr int kThreads = 256;
+constexpr int kBlock = kSelectBlock;  // keys of a block
+
+__device__ __forceinline__ int clamped_len(const int* seqlens, int b, int cap, bool report) {
+  const int len = seqlens[b];
+  if (report && (len < 0 || len > cap)) record(1, kDevBadSeqlen);
+  return min(max(len, 0), cap);
+}
+
+// ---------------------------------------------------------------------------
+// Bounds.  One CTA for each touched block and 64 chunks of 8 channels: four
+// groups of 64 threads take 16 rows each, a thread's loads all in flight at
+// once, and meet in shared memory.  Bound by memory: each key read once.
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 min4(const uint4& a, const uint4& b) {
+  return make_uint4(min_nan2(a.x, b.x), min_nan2(a.y, b.y), min_nan2(a.z, b.z), min_nan2(a.w, b.w));
+}
+__device__ __forceinline__ uint4 max4(const uint4& a, const uint4& b) {
+  return make_uint4(max_nan2(a.x, b.x), max_nan2(a.y, b.y), max_nan2(a.z, b.z), max_nan2(a.w, b.w));
+}
+
+__global__ void __launch_bounds__(kThreads) bounds_kernel(const KeyBoundsParams p, int slabs) {
+  grid_depends();
+  __shared__ uint4 s_lo[3][64], s_hi[3][64];
+  const int b = blockIdx.y;
+  const int cap = p.max_blocks * p.page_size;
+  const int len = clamped_len(p.seqlens, b, cap, blockIdx.x == 0 && threadIdx.x == 0);
+  int n = p.new_lens ? p.new_lens[b] : min(p.Nn, len);
+  if (n < 0 || n > p.Nn || n > len) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record(2, kDevBadSeqlen);
+    n = min(max(n, 0), min(p.Nn, len));
+  }
+  if (n == 0) return;
+  const int blk = (len - n) / kBlock + static_cast<int>(blockIdx.x) / slabs;
+  if (blk * kBlock >= len) return;
+  const int pg = p.block_table[static_cast<long long>(b) * p.max_blocks + blk * kBlock / p.page_size];
+  if (pg < 0 || pg >= p.num_pages) {
+    if (threadIdx.x == 0) record(3, kDevBadPage);
+    return;
+  }
+  const int row0 = blk * kBlock % p.page_size;
+  const int rows = min(kBlock, len - blk * kBlock);
+  const int per = p.Hkv * p.d / 8;  // chunks of a key row
+  const int chunk = static_cast<int>(blockIdx.x) % slabs * 64 + (threadIdx.x & 63);
+  const int g = threadIdx.x >> 6;
+  const uint32_t inf2 = 0x7f807f80u, ninf2 = 0xff80ff80u;
+  uint4 lo = make_uint4(inf2, inf2, inf2, inf2), hi = make_uint4(ninf2, ninf2, ninf2, ninf2);
+  if (chunk < per) {
+    const uint4* src = static_cast<const uint4*>(p.k_pages) +
+                       (static_cast<long long>(pg) * p.page_size + row0 + 16 * g) * per + chunk;
+    uint4 u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (16 * g + i < rows) u[i] = src[static_cast<long long>(i) * per];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (16 * g + i < rows) {
+        lo = min4(lo, u[i]);
+        hi = max4(hi, u[i]);
+      }
+  }
+  if (g > 0) {
+    s_lo[g - 1][threadIdx.x & 63] = lo;
+    s_hi[g - 1][threadIdx.x & 63] = hi;
+  }
+  __syncthreads();
+  if (g == 0 && chunk < per) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      lo = min4(lo, s_lo[i][threadIdx.x]);
+      hi = max4(hi, s_hi[i][threadIdx.x]);
+    }
+    const int dc = p.d / 8;
+    uint4* dst = static_cast<uint4*>(p.k_bounds) +
+                 ((static_cast<long long>(pg) * (p.page_size / kBlock) + row0 / kBlock) * p.Hkv + chunk / dc) * 2 * dc +
+                 chunk % dc;
+    dst[0] = lo;
+    dst[dc] = hi;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Blocks of a query row.  A row is (token, KV head); token t = b * Nq + n.
+struct RowSpan {
+  int b, n, nb;  // sequence, new token, blocks that it sees (the last one its own)
+};
+__device__ __forceinline__ RowSpan row_span(const SelectParams& p, int token, bool report) {
+  RowSpan r;
+  r.b = token / p.Nq;
+  r.n = token - r.b * p.Nq;
+  const int len = clamped_len(p.seqlens, r.b, p.max_blocks * p.page_size, report);
+  const int pos = len - p.Nq + r.n;
+  r.nb = pos < 0 ? 0 : pos / kBlock + 1;
+  return r;
+}
+
+// Bounds of block j of a sequence and KV head: lo [D], hi [D].
+__device__ __forceinline__ const __nv_bfloat16* bounds_at(const SelectParams& p, int b, int j, int h) {
+  const int per = p.page_size / kBlock;
+  int pg = p.block_table[static_cast<long long>(b) * p.max_blocks + j / per];
+  if (pg < 0 || pg >= p.num_pages) {
+    record(4, kDevBadPage);
+    pg = 0;
+  }
+  return static_cast<const __nv_bfloat16*>(p.k_bounds) +
+         ((static_cast<long long>(pg) * per + j % per) * p.Hkv + h) * 2 * p.d;
+}
+
+// fp32 scores.  One CTA for a row and kChunk blocks; 8 threads a block, each
+// with D / 8 channels, and the group's heads four at a time.
+constexpr int kChunk = kSelectChunk;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p, int token0) {
+  grid_depends();
+  constexpr int kPer = D / 8;  // channels of a thread
+  const int G = p.Hq / p.Hkv;
+  const int h = blockIdx.y;
+  const int lrow = blockIdx.z * p.Hkv + h;
+  const int token = token0 + blockIdx.z;
+  const RowSpan r = row_span(p, token, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  const int j0 = blockIdx.x * kChunk, j1 = min(r.nb, j0 + kChunk);
+  __shared__ float s_a[kThreads / 32];
+  if (j0 >= r.nb) return;
+  const int l = threadIdx.x & 7;
+  float* out = p.scores + static_cast<long long>(lrow) * p.n_blocks;
+  float a_max = 0.f;
+  for (int j = j0 + (threadIdx.x >> 3); j < j0 + kChunk; j += kThreads / 8) {  // same steps for a warp's lanes
+    const bool on = j < j1;
+    float lo[kPer], hi[kPer];
+    {
+      const __nv_bfloat16* src = bounds_at(p, r.b, on ? j : j0, h) + l * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 8) {
+        unpack8(*reinterpret_cast<const uint4*>(src + i), lo + i);
+        unpack8(*reinterpret_cast<const uint4*>(src + D + i), hi + i);
+      }
+    }
+    float best = -INFINITY;
+    for (int g = 0; g < G; ++g) {
+      const __nv_bfloat16* qs = static_cast<const __nv_bfloat16*>(p.q) +
+                                (static_cast<long long>(token) * p.Hq + h * G + g) * D + l * kPer;
+      float q[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; i += 8) unpack8(*reinterpret_cast<const uint4*>(qs + i), q + i);
+      float2 s = make_float2(0.f, 0.f);
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        s = ffma2(make_float2(fmaxf(q[i], 0.f), fminf(q[i], 0.f)), make_float2(hi[i], lo[i]), s);
+        a = fmaf(fabsf(q[i]), fmaxf(fabsf(hi[i]), fabsf(lo[i])), a);
+        if (q[i] != q[i]) s.x = a = NAN;  // fmaxf, fminf drop it
+      }
+      float v = s.x + s.y;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+      }
+      if (!(v == v)) a = INFINITY;  // looked at in 64 bits
+      best = fmaxf(best, v);
+      if (on) a_max = a > a_max || a != a ? a : a_max;
+    }
+    if (on && l == 0) out[j] = best;
+  }
+  if (a_max != a_max) a_max = INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a_max = fmaxf(a_max, __shfl_xor_sync(0xffffffffu, a_max, o));
+  if ((threadIdx.x & 31) == 0) s_a[threadIdx.x >> 5] = a_max;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) a_max = fmaxf(a_max, s_a[w]);
+    p.err[static_cast<long long>(lrow) * p.n_chunks + blockIdx.x] = a_max;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Choice.
+__device__ __forceinline__ uint32_t ordered(float x) {  // larger float, larger integer
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+// The 64-bit score of block j, formed by a warp; NaN ranks as +inf.
+__device__ double exact_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
+  const int lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  const __nv_bfloat16* kb = bounds_at(p, r.b, j, h);
+  double best = -INFINITY;
+  for (int g = 0; g < G; ++g) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(token) * p.Hq + h * G + g) * p.d;
+    double s = 0.;
+    for (int i = lane; i < p.d; i += 32) {
+      const float x = __bfloat162float(q[i]);
+      const double lo = __bfloat162float(kb[i]), hi = __bfloat162float(kb[p.d + i]);
+      s += x != x ? static_cast<double>(x) : fmax(static_cast<double>(x), 0.) * hi + fmin(static_cast<double>(x), 0.) * lo;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (s != s) s = INFINITY;
+    best = fmax(best, s);
+  }
+  return best;
+}
+
+constexpr int kHeld = 8192;   // scores kept in shared memory
+constexpr int kBand = 1024;   // blocks scored again at most, else all by passes over 64-bit keys
+
+__device__ __forceinline__ unsigned long long ordered64(double x) {
+  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x + 0.));  // -0 as 0
+  return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+// One CTA for a row.
+__global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, int token0) {
+  grid_depends();
+  extern __shared__ float s_score[];  // [min(n_blocks, kHeld)]
+  __shared__ unsigned s_hist[256];
+  __shared__ int s_pick, s_left, s_count[2];
+  __shared__ unsigned s_warp[kThreads / 32];
+  __shared__ int s_id[kBand];
+  __shared__ double s_exact[kBand];
+  __shared__ uint32_t s_take[kBand / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.Hkv;
+  const int token = token0 + static_cast<int>(blockIdx.x / p.Hkv);
+  const int lrow = blockIdx.x;
+  const RowSpan r = row_span(p, token, false);
+  int* out = p.blocks + (static_cast<long long>(token) * p.Hkv + h) * p.topk;
+  if (r.nb <= p.topk) {
+    for (int i = tid; i < p.topk; i += kThreads) out[i] = i < r.nb ? i : -1;
+    return;
+  }
+  // candidates [c0, c1), k of them wanted; sink + local <= topk < nb
+  const int c0 = p.sink, c1 = r.nb - p.local, k = p.topk - p.sink - p.local;
+  const int n = c1 - c0;
+  const float* scores = p.scores + static_cast<long long>(lrow) * p.n_blocks + c0;
+  const bool held = n <= kHeld;
+  if (held)
+    for (int i = tid; i < n; i += kThreads) s_score[i] = scores[i];
+  __syncthreads();
+  auto score = [&](int i) { return held ? s_score[i] : scores[i]; };
+  float t_lo = INFINITY, t_hi = INFINITY;  // chosen above t_hi, perhaps from t_lo on
+  int mode = 0;                            // 0: nothing but scores > t_hi; 1: band scored again; 2: by passes
+  unsigned long long cut = 0;              // mode 2: keys above it are in, of those equal the first `left`
+  int left = 0;
+  if (k > 0) {
+    // error bound of the row
+    float e = 0.f;
+    for (int c = lane; c <= (r.nb - 1) / kChunk; c += 32) e = fmaxf(e, p.err[static_cast<long long>(lrow) * p.n_chunks + c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
+    const float band = e * 3.814697265625e-6f + 1e-36f;  // 2 E, and what products below fp32's range lose
+    bool all = !(band < 1e38f);
+    if (!all) {
+      // the k-th largest, a byte of its key at a time
+      uint32_t prefix = 0;
+      int want = k;
+      for (int shift = 24; shift >= 0; shift -= 8) {
+        s_hist[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+          const uint32_t u = ordered(score(i));
+          if (shift == 24 || (u >> (shift + 8)) == prefix) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
+        }
+        __syncthreads();
+        if (warp == 0) {
+          // bins from the top, 8 a lane
+          unsigned c[8], sum = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[255 - (lane * 8 + i)];
+          unsigned incl = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+          }
+          unsigned before = incl - sum;
+          if (before < static_cast<unsigned>(want) && static_cast<unsigned>(want) <= incl) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (before < static_cast<unsigned>(want) && static_cast<unsigned>(want) <= before + c[i]) {
+                s_pick = 255 - (lane * 8 + i);
+                s_left = want - static_cast<int>(before);
+              }
+              before += c[i];
+            }
+          }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | static_cast<uint32_t>(s_pick);
+        want = s_left;
+      }
+      const float t = unordered(prefix);
+      t_hi = t + band;
+      t_lo = t - band;
+    } else {
+      t_hi = INFINITY;
+      t_lo = -INFINITY;
+    }
+    // how many are in for sure, and the blocks between
+    if (tid < 2) s_count[tid] = 0;
+    if (tid < kBand / 32) s_take[tid] = 0;
+    __syncthreads();
+    int sure = 0;
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = score(i);
+      if (!all && x > t_hi) {
+        ++sure;
+      } else if (all || x >= t_lo) {
+        const int at = atomicAdd(&s_count[1], 1);
+        if (at < kBand) s_id[at] = i;
+      }
+    }
+    if (sure) atomicAdd(&s_count[0], sure);
+    __syncthreads();
+    const int between = s_count[1];
+    left = k - s_count[0];
+    if (between > left) {
+      if (between <= kBand) {
+        mode = 1;
+        for (int m = warp; m < between; m += kThreads / 32) {
+          const double x = exact_score(p, r, token, h, c0 + s_id[m]);
+          if (lane == 0) s_exact[m] = x;
+        }
+        __syncthreads();
+        for (int m = tid; m < between; m += kThreads) {
+          const double x = s_exact[m];
+          const int id = s_id[m];
+          int rank = 0;
+          for (int o = 0; o < between; ++o) rank += s_exact[o] > x || (s_exact[o] == x && s_id[o] < id);
+          if (rank < left) atomicOr(&s_take[m >> 5], 1u << (m & 31));
+        }
+        __syncthreads();
+        // the taken ones get a score above all: marked in place of their number
+        for (int m = tid; m < between; m += kThreads)
+          if (!(s_take[m >> 5] >> (m & 31) & 1u)) s_id[m] = -1;
+      } else {
+        mode = 2;
+        int want = left;
+        for (int shift = 56; shift >= 0; shift -= 8) {
+          s_hist[tid] = 0;
+          __syncthreads();
+          for (int i = warp; i < n; i += kThreads / 32) {
+            const float x = score(i);
+            if (!all && !(x >= t_lo && x <= t_hi)) continue;
+            const unsigned long long u = ordered64(exact_score(p, r, token, h, c0 + i));
+            if (lane == 0 && (shift == 56 || (u >> (shift + 8)) == cut)) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
+          }
+          __syncthreads();
+          if (tid == 0) {
+            int c = want;
+            int v = 255;
+            while (static_cast<int>(s_hist[v]) < c) c -= static_cast<int>(s_hist[v--]);
+            s_pick = v;
+            s_left = c;
+          }
+          __syncthreads();
+          cut = (cut << 8) | static_cast<unsigned>(s_pick);
+          want = s_left;
+          __syncthreads();
+        }
+        left = want;
+      }
+    } else {
+      t_hi = -INFINITY;  // everything from t_lo on
+    }
+  }
+  // the chosen blocks in ascending order
+  __shared__ int s_done, s_equal;
+  if (tid == 0) s_done = s_equal = 0;
+  __syncthreads();
+  for (int base = 0; base < r.nb; base += kThreads) {
+    const int j = base + tid, i = j - c0;
+    bool in = j < r.nb && (j < c0 || j >= c1);
+    if (k > 0 && i >= 0 && i < n) {
+      const float x = score(i);
+      if (mode == 0)
+        in = x >= t_lo;
+      else
+        in = x > t_hi;
+    }
+    if (mode == 1) {
+      // numbers of this stretch among the taken ones
+      __shared__ uint32_t s_bits[kThreads / 32];
+      if (tid < kThreads / 32) s_bits[tid] = 0;
+      __syncthreads();
+      for (int m = tid; m < s_count[1]; m += kThreads) {
+        const int at = s_id[m] < 0 ? -1 : s_id[m] + c0 - base;
+        if (at >= 0 && at < kThreads) atomicOr(&s_bits[at >> 5], 1u << (at & 31));
+      }
+      __syncthreads();
+      in = in || (s_bits[warp] >> lane & 1u);
+      __syncthreads();
+    } else if (mode == 2) {
+      // each warp scores its 32 blocks again; equal ones are counted in order
+      uint32_t above = 0, equal = 0;
+      for (int o = 0; o < 32; ++o) {
+        const int io = base + warp * 32 + o - c0;
+        if (io < 0 || io >= n) continue;
+        const float x = score(io);
+        const bool certain = t_hi < INFINITY && x > t_hi;
+        if (certain || (t_lo > -INFINITY && x < t_lo)) continue;
+        const unsigned long long u = ordered64(exact_score(p, r, token, h, c0 + io));
+        if (u > cut) above |= 1u << o;
+        if (u == cut) equal |= 1u << o;
+      }
+      if (lane == 0) s_warp[warp] = equal;
+      __syncthreads();
+      int before = s_equal;
+      for (int w = 0; w < warp; ++w) before += __popc(s_warp[w]);
+      before += __popc(equal & ((1u << lane) - 1u));
+      in = in || (above >> lane & 1u) || ((equal >> lane & 1u) && before < left);
+      __syncthreads();
+      if (tid == 0)
+        for (int w = 0; w < kThreads / 32; ++w) s_equal += __popc(s_warp[w]);
+      __syncthreads();
+    }
+    const unsigned vote = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s_warp[warp] = vote;
+    __syncthreads();
+    int at = s_done;
+    for (int w = 0; w < warp; ++w) at += __popc(s_warp[w]);
+    at += __popc(vote & ((1u << lane) - 1u));
+    if (in && at < p.topk) out[at] = j;
+    __syncthreads();
+    if (tid == 0)
+      for (int w = 0; w < kThreads / 32; ++w) s_done += __popc(s_warp[w]);
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_key_bounds(const KeyBoundsParams& p, cudaStream_t stream) {
+  const int slabs = (p.Hkv * p.d / 8 + 63) / 64;
+  const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
+  const long long most = p.Nn < cap ? p.Nn : cap;
+  const long long blocks = (most + kBlock - 2) / kBlock + 1;
+  return launch_dependent(bounds_kernel, dim3(static_cast<unsigned>(blocks * slabs), static_cast<unsigned>(p.B)), kThreads,
+                          0, stream, p, slabs);
+}
+
+cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.n_chunks), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(tokens));
+  cudaError_t e = p.d == 64 ? launch_dependent(score_kernel<64>, grid, kThreads, 0, stream, p, token0)
+                            : launch_dependent(score_kernel<128>, grid, kThreads, 0, stream, p, token0);
+  if (e != cudaSuccess) return e;
+  const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
+  return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(tokens * p.Hkv)), kThreads,
+                          held * static_cast<int>(sizeof(float)), stream, p, token0);
+}
+
+cudaError_t status_word_select(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_select_status); }
+
+}  // namespace attn

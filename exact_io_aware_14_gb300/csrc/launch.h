@@ -178,6 +178,67 @@ struct DecodeFp8Params {
 };
 cudaError_t launch_decode_fp8(const DecodeFp8Params& p, cudaStream_t stream);
 
+// Block tables from request lengths.  new_lens: what a reserve wants (null: Nn
+// each), or what a release keeps.
+struct PagingParams {
+  const int* seqlens;
+  const int* new_lens;
+  const int* free_count;
+  const int* free_pages;  // reserve: the free list, read
+  int* free_list;         // release: the free list, written
+  int* block_table;
+  int* seqlens_out;   // null: not wanted
+  int* new_lens_out;
+  int* free_count_out;
+  long long* slots;   // [B, Nn], or null
+  int max_blocks, page_size, num_pages, B, Nn;
+};
+cudaError_t launch_reserve(const PagingParams& p, cudaStream_t stream);
+cudaError_t launch_release(const PagingParams& p, cudaStream_t stream);
+
+// Bounds of the keys of 64-key blocks, and the choice of blocks by them.
+constexpr int kSelectBlock = 64;   // keys of a block
+constexpr int kSelectChunk = 64;   // blocks of a scoring CTA
+struct KeyBoundsParams {
+  const void* k_pages;
+  void* k_bounds;  // [num_pages, page_size / 64, Hkv, 2, d]
+  const int* block_table;
+  const int* seqlens;
+  const int* new_lens;  // null: Nn each, or the whole sequence where it is shorter
+  int max_blocks, page_size, num_pages, B, Nn, Hkv, d;
+};
+cudaError_t launch_key_bounds(const KeyBoundsParams& p, cudaStream_t stream);
+
+struct SelectParams {
+  const void* q;
+  const void* k_bounds;
+  const int* block_table;
+  const int* seqlens;
+  int* blocks;    // [B, Nq, Hkv, topk]
+  float* scores;  // [tokens of a launch, Hkv, n_blocks]
+  float* err;     // [tokens of a launch, Hkv, n_chunks]: largest sums of magnitudes
+  int max_blocks, page_size, num_pages, B, Nq, Hq, Hkv, d, topk, sink, local;
+  int n_blocks, n_chunks;  // blocks of a full table, chunks of them
+};
+cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStream_t stream);
+
+// Attention of query rows over a paged bf16 cache: over a whole sequence whose
+// first shared_len keys all sequences have in common, or over listed blocks.
+struct RowsParams {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int* block_table;
+  const int* seqlens;
+  const int* blocks;  // [B, Nq, Hkv, n_sel], or null
+  void* o;
+  float* lse;
+  int max_blocks, page_size, num_pages, shared_len, n_sel;
+  int B, Nq, Hq, Hkv, d;
+  float scale_log2;
+};
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream);
+
 // Device status words, one a kernel unit, of the current device.
 cudaError_t status_word_prefill(uint32_t** at);
 cudaError_t status_word_decode(uint32_t** at);
@@ -185,7 +246,10 @@ cudaError_t status_word_selftest(uint32_t** at);
 cudaError_t status_word_rope(uint32_t** at);
 cudaError_t status_word_append(uint32_t** at);
 cudaError_t status_word_decode_fp8(uint32_t** at);
-constexpr int kStatusUnits = 6;
+cudaError_t status_word_paging(uint32_t** at);
+cudaError_t status_word_select(uint32_t** at);
+cudaError_t status_word_rows(uint32_t** at);
+constexpr int kStatusUnits = 9;
 struct StatusWords {
   uint32_t* at[kStatusUnits];
 };

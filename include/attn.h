@@ -401,6 +401,147 @@ ATTN_API attn_status attn_fwd_splitkv_paged_fp8(const void* q, const void* k_pag
                                                 float scale, int chunk, void* workspace, size_t workspace_bytes,
                                                 void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators on a paged cache beyond one decode step.  The pages have no
+ * counterpart to these either.  Where a call takes a block table, lengths and
+ * pages, their layouts, limits and the reports of bad ones are those of
+ * attn_kvcache_append_paged and attn_fwd_splitkv_paged; B is at most 65535.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Block tables and slot maps from request lengths: gives each sequence the
+ * pages that its new tokens need, on the GPU, so that a captured step needs no
+ * host.  Sequence b holds seqlens[b] tokens in the first
+ * ceil(seqlens[b] / page_size) entries of its row and asks for new_lens[b] more.
+ *   free_pages: device int32 [num_pages], a stack of free pages, of which
+ *            entries 0 .. *free_count - 1 are valid; pages are taken from its
+ *            end, sequence by sequence, each one's blocks in order.  A sequence
+ *            that needs more pages than are left behind those before it gets
+ *            none of its tokens, nor does any later one that needs a page;
+ *   block_table: the entries of the new pages are written, no others;
+ *   new_lens: device int32 [B], each in [0, Nn], or NULL for Nn each;
+ *   new_lens_out: device int32 [B], new_lens[b] where the sequence was served,
+ *            else 0 (new_lens of the append that follows);
+ *   seqlens_out: device int32 [B], seqlens[b] + new_lens_out[b], or NULL;
+ *   slots: device int64 [B, Nn], row number in the pools (page * page_size +
+ *            row) of each new token, -1 behind the served ones; or NULL;
+ *   free_count_out: device int32 [1], entries that remain valid.
+ * No output may overlap another or an input (free_count_out is memory of its
+ * own: the next call's free_count).  A length out of range, tokens that do not
+ * fit the table (such a sequence gets 0), a free count outside [0, num_pages] and
+ * a page outside [0, num_pages) are reported as ATTN_ERR_DEVICE_ARG by
+ * attn_get_device_status.
+ */
+ATTN_API attn_status attn_kvcache_reserve_paged(int* block_table, int max_blocks, int page_size, int num_pages,
+                                                const int* seqlens, const int* new_lens, const int* free_pages,
+                                                const int* free_count, int* new_lens_out, int* seqlens_out,
+                                                long long* slots, int* free_count_out, int B, int Nn, void* stream);
+
+/*
+ * Gives pages back to the free list: sequence b keeps the first keep_lens[b]
+ * of its seqlens[b] tokens (0 where it is finished, less than seqlens where
+ * drafted tokens were rejected, the prefix' length where its first pages are
+ * shared), and its pages from block ceil(keep_lens[b] / page_size) on become
+ * entries *free_count, ... of free_pages, the last sequence's last page first,
+ * so that releasing what a reserve took restores the list.  block_table is left
+ * as it is.  A keep_lens outside [0, seqlens[b]] (nothing is released) and pages
+ * past num_pages of them (dropped) are reported as ATTN_ERR_DEVICE_ARG.
+ */
+ATTN_API attn_status attn_kvcache_release_paged(const int* block_table, int max_blocks, int page_size, int num_pages,
+                                                const int* seqlens, const int* keep_lens, int* free_pages,
+                                                const int* free_count, int* free_count_out, int B, void* stream);
+
+/* Bytes of workspace attn_fwd_splitkv_paged_shared needs; 0 for invalid arguments. */
+ATTN_API size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+
+/*
+ * Decode over a paged bf16 cache where the batch shares a prefix: the first
+ * shared_len keys of every sequence lie in the same pages, which are read once
+ * for all sequences instead of once for each.  The last Nq tokens of each
+ * sequence are the queries, masked causally among themselves: row i sees keys
+ * 0 .. seqlens[b] - Nq + i, prefix and own ones alike.
+ *   q [B,Nq,Hq,d] bf16, Nq >= 1; o [B,Nq,Hq,d] bf16 and lse [B,Hq,Nq] fp32
+ *            out; a row that sees no key gets O = 0 and LSE = -inf; o must not
+ *            overlap q;
+ *   block_table, seqlens: as for attn_fwd_splitkv_paged, the prefix' pages first
+ *            in every row and counted in seqlens (a sequence may be shorter than
+ *            the prefix); the prefix is read through row 0 of the table;
+ *   shared_len: a multiple of page_size in [0, max_blocks * page_size]; with 0
+ *            each sequence is read by itself;
+ *   workspace: attn_splitkv_paged_shared_workspace_size bytes, 16-byte aligned,
+ *            contents ignored; one for each call that may run at once.
+ * The weights enter the product with V rounded to bf16, as in attn_fwd.  Keys
+ * and values that some row sees must be finite; behind a sequence's end there
+ * may be anything.  Hq / Hkv is at most 128, B * Nq * Hq below 2^31 - 4096.
+ */
+ATTN_API attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_pages, const void* v_pages,
+                                                   const int* block_table, int max_blocks, int page_size,
+                                                   int num_pages, const int* seqlens, int shared_len, void* o,
+                                                   float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale,
+                                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Sparse attention over blocks of 64 keys, in three calls.  Block j of a
+ * sequence is its keys 64 j .. 64 j + 63; new token n of Nq sits at position
+ * seqlens[b] - Nq + n and sees the keys up to its own.
+ *
+ * (1) Bounds of the keys, kept beside the key pages: k_bounds [num_pages,
+ * page_size / 64, Hkv, 2, d] bf16 holds for each block, KV head and channel the
+ * smallest (0) and the largest (1) value of the block's keys.  The call forms
+ * them anew, from the pages, for the blocks that hold any of the last
+ * new_lens[b] of sequence b's seqlens[b] tokens (NULL: the last Nn, or all of a
+ * shorter sequence), each over all its keys before the sequence's end.  A NaN
+ * key makes its channel's bounds NaN.  k_bounds must not overlap k_pages.
+ */
+ATTN_API attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_bounds, const int* block_table,
+                                               int max_blocks, int page_size, int num_pages, const int* seqlens,
+                                               const int* new_lens, int B, int Nn, int Hkv, int d, void* stream);
+
+/*
+ * (2) Selection: for each new token and KV head the blocks whose bounds allow
+ * the largest scores.
+ *     score(j) = max over the group's heads h of
+ *                sum_i max(q_hi, 0) * hi_ji + min(q_hi, 0) * lo_ji
+ * (no key of block j has a larger <q_h, k>).  Of the blocks that the token sees
+ * the first `sink` and the last `local` are taken, then those of the largest
+ * score, the lower index first among equals, topk in all (all of them where
+ * there are no more).
+ *   blocks: device int32 [B, Nq, Hkv, topk] out, ascending, -1 behind the last;
+ *   sink, local >= 0, sink + local <= topk;
+ *   workspace: attn_select_blocks_workspace_size(B, Nq, Hkv, max_blocks *
+ *            page_size) bytes, 16-byte aligned, contents ignored; one for each
+ *            call that may run at once.
+ * The order is that of the scores in 64 bits (the products exact, the sums in
+ * double precision); a score that is not a number ranks as +inf.
+ */
+ATTN_API size_t attn_select_blocks_workspace_size(int B, int Nq, int Hkv, int max_seqlen);
+ATTN_API attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const int* block_table,
+                                              int max_blocks, int page_size, int num_pages, const int* seqlens,
+                                              int* blocks, int B, int Nq, int Hq, int Hkv, int d, int topk, int sink,
+                                              int local, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_blocks_paged needs; 0 for invalid arguments. */
+ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+
+/*
+ * (3) Attention of each new token over the keys of its listed blocks that it
+ * sees.
+ *   blocks: device int32 [B, Nq, Hkv, n_sel], in any order; negative entries
+ *            are passed over, as are blocks behind the token's position; a block
+ *            listed twice counts twice; an entry past the table is passed over
+ *            and reported as ATTN_ERR_DEVICE_ARG by attn_get_device_status;
+ *   workspace: attn_fwd_blocks_paged_workspace_size bytes.
+ * The other arguments, limits and results are those of
+ * attn_fwd_splitkv_paged_shared.  Nq may be in the thousands (a prompt, or a
+ * chunk of one).  Only keys and values that the row sees enter its result; what
+ * lies elsewhere may be anything.
+ */
+ATTN_API attn_status attn_fwd_blocks_paged(const void* q, const void* k_pages, const void* v_pages,
+                                           const int* block_table, int max_blocks, int page_size, int num_pages,
+                                           const int* seqlens, const int* blocks, int n_sel, void* o, float* lse,
+                                           int B, int Nq, int Hq, int Hkv, int d, float scale, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the library's device status
  * word.  Returns ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_DEVICE_ARG, or
