@@ -62,6 +62,23 @@ bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_siz
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d) {
+  return make_map(m, base, num_pages, page_size, Hkv, d, 64);
+}
+
+// 4-D view {d, G, Hkv, tokens} of q [tokens, Hkv * G, d]; box {64, G, 1, tokens}.
+bool make_map_group(CUtensorMap* m, const void* base, long long total_tokens, int Hkv, int G, int d, int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)total_tokens};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)G * d * 2, (cuuint64_t)Hkv * G * d * 2};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)G, 1u, (cuuint32_t)tokens};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace attn
 
 namespace {

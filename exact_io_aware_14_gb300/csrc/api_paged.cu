@@ -90,28 +90,63 @@ attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pa
   return ATTN_OK;
 }
 
-attn::RowsParams rows_params(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
-                             int max_blocks, int page_size, int num_pages, const int* seqlens, void* o, float* lse,
-                             int B, int Nq, int Hq, int Hkv, int d, float scale) {
+size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
+size_t rows_workspace(const attn::RowsSizes& z, int B, int d, bool lists) {
+  const size_t rows = static_cast<size_t>(z.pair_rows + z.lane_pieces * z.unit_rows);
+  return round16(lists ? 0 : (static_cast<size_t>(B) + 3) * sizeof(long long)) + rows * (d + 1) * sizeof(float);
+}
+
+// Both attention calls, behind their checks.  blocks: listed ones, or null.
+attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages, const int* block_table, int max_blocks,
+                        int page_size, int num_pages, const int* seqlens, const int* blocks, int n_sel, int shared_len,
+                        void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const attn::RowsSizes z = attn::rows_sizes(B, Nq, Hq, Hkv, blocks != nullptr);
+  if (!workspace || off(workspace, 16) || workspace_bytes < rows_workspace(z, B, d, blocks != nullptr))
+    return ATTN_ERR_WORKSPACE;
   attn::RowsParams p;
   std::memset(&p, 0, sizeof p);
-  p.q = q;
-  p.k_pages = k_pages;
-  p.v_pages = v_pages;
   p.block_table = block_table;
   p.seqlens = seqlens;
+  p.blocks = blocks;
   p.o = o;
   p.lse = lse;
   p.max_blocks = max_blocks;
   p.page_size = page_size;
   p.num_pages = num_pages;
+  p.shared_len = shared_len;
+  p.n_sel = n_sel;
   p.B = B;
   p.Nq = Nq;
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.d = d;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
-  return p;
+  p.tile_tokens = z.tile_tokens;
+  p.pairs = z.pairs;
+  p.own_tokens = z.own_tokens;
+  p.own_rt = z.own_rt;
+  p.unit_tokens = z.unit_tokens;
+  p.unit_rows = z.unit_rows;
+  p.q_buffers = z.unit_rows <= 64 ? 2 : 1;
+  p.pair_rows = z.pair_rows;
+  char* ws = static_cast<char*>(workspace);
+  if (!blocks) {
+    p.sums = reinterpret_cast<long long*>(ws);
+    ws += round16((static_cast<size_t>(B) + 3) * sizeof(long long));
+  }
+  p.o_part = reinterpret_cast<float*>(ws);
+  p.lse_part = p.o_part + static_cast<size_t>(z.pair_rows + z.lane_pieces * z.unit_rows) * d;
+  CUtensorMap tm_q, tm_qs, tm_k, tm_v;
+  const long long tokens = static_cast<long long>(B) * Nq;
+  if (!attn::make_map_group(&tm_q, q, tokens, Hkv, Hq / Hkv, d, z.tile_tokens) ||
+      !attn::make_map_group(&tm_qs, q, tokens, Hkv, Hq / Hkv, d, z.unit_tokens) ||
+      !attn::make_map_pages(&tm_k, k_pages, num_pages, page_size, Hkv, d) ||
+      !attn::make_map_pages(&tm_v, v_pages, num_pages, page_size, Hkv, d))
+    return ATTN_ERR_LAUNCH;
+  return attn::launch_rows(p, tm_q, tm_qs, tm_k, tm_v, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -264,8 +299,8 @@ attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const 
 }
 
 size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
-  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK) return 0;
-  return 16;
+  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK || Hq / Hkv > 128) return 0;
+  return rows_workspace(attn::rows_sizes(B, Nq, Hq, Hkv, true), B, d, true);
 }
 
 attn_status attn_fwd_blocks_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
@@ -276,19 +311,15 @@ attn_status attn_fwd_blocks_paged(const void* q, const void* k_pages, const void
                                          o, lse, B, Nq, Hq, Hkv, d, scale);
   if (st != ATTN_OK) return st;
   if (n_sel < 1 || !blocks) return ATTN_ERR_INVALID_ARG;
+  if (n_sel > attn::kMaxListed) return ATTN_ERR_UNSUPPORTED;
   if (off(blocks, 4)) return ATTN_ERR_MISALIGNED;
-  if (!workspace || off(workspace, 16) || workspace_bytes < attn_fwd_blocks_paged_workspace_size(B, Nq, Hq, Hkv, d))
-    return ATTN_ERR_WORKSPACE;
-  attn::RowsParams p = rows_params(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, o, lse,
-                                   B, Nq, Hq, Hkv, d, scale);
-  p.blocks = blocks;
-  p.n_sel = n_sel;
-  return attn::launch_rows(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  return attend_rows(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, blocks, n_sel, 0, o,
+                     lse, B, Nq, Hq, Hkv, d, scale, workspace, workspace_bytes, stream);
 }
 
 size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
-  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK) return 0;
-  return 16;
+  if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK || Hq / Hkv > 128) return 0;
+  return rows_workspace(attn::rows_sizes(B, Nq, Hq, Hkv, false), B, d, false);
 }
 
 attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_pages, const void* v_pages,
@@ -300,12 +331,8 @@ attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_pages, co
                                          o, lse, B, Nq, Hq, Hkv, d, scale);
   if (st != ATTN_OK) return st;
   if (shared_len < 0 || shared_len % page_size != 0 || shared_len / page_size > max_blocks) return ATTN_ERR_INVALID_ARG;
-  if (!workspace || off(workspace, 16) || workspace_bytes < attn_splitkv_paged_shared_workspace_size(B, Nq, Hq, Hkv, d))
-    return ATTN_ERR_WORKSPACE;
-  attn::RowsParams p = rows_params(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, o, lse,
-                                   B, Nq, Hq, Hkv, d, scale);
-  p.shared_len = shared_len;
-  return attn::launch_rows(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  return attend_rows(q, k_pages, v_pages, block_table, max_blocks, page_size, num_pages, seqlens, nullptr, 0,
+                     shared_len, o, lse, B, Nq, Hq, Hkv, d, scale, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

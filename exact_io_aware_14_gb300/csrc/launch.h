@@ -224,20 +224,41 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
 
 // Attention of query rows over a paged bf16 cache: over a whole sequence whose
 // first shared_len keys all sequences have in common, or over listed blocks.
+constexpr int kRowsCtas = 152;    // CTAs at most, one an SM
+constexpr int kMaxListed = 512;   // blocks listed for a token
+struct RowsSizes {
+  int tile_tokens;     // tokens of a tile of rows
+  int pairs;           // pairs of such tiles in the batch; 0: a single tile
+  int own_tokens;      // tokens of a sequence in a tile, tiles of its tokens
+  int own_rt;
+  int unit_tokens;     // tokens loaded for a lane's unit, rows of its pieces
+  int unit_rows;
+  long long pair_rows;    // rows of the pair pieces, number of the lanes' pieces at most
+  long long lane_pieces;
+};
+RowsSizes rows_sizes(int B, int Nq, int Hq, int Hkv, bool lists);
 struct RowsParams {
-  const void* q;
-  const void* k_pages;
-  const void* v_pages;
   const int* block_table;
   const int* seqlens;
   const int* blocks;  // [B, Nq, Hkv, n_sel], or null
   void* o;
   float* lse;
+  float* o_part;      // [pair_rows + lane_pieces * unit_rows, d]
+  float* lse_part;    // the same rows, base 2
+  long long* sums;    // [B + 3]: tiles before each sequence, of all; of pairs; keys of the prefix
   int max_blocks, page_size, num_pages, shared_len, n_sel;
   int B, Nq, Hq, Hkv, d;
   float scale_log2;
+  int tile_tokens, pairs, own_tokens, own_rt, unit_tokens, unit_rows;
+  int q_buffers;      // buffers of rows of a slot (lane work)
+  long long pair_rows;
 };
-cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream);
+// q as {d, heads of a group, Hkv, tokens}: tiles of tile_tokens and of unit_tokens tokens; the page pools in 64 rows.
+cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
+                        const CUtensorMap& tm_v, cudaStream_t stream);
+// Maps of bf16 tensors: a page pool's boxes of 64 rows of a head; q's of `tokens` tokens of a group of heads.
+bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d);
+bool make_map_group(CUtensorMap* m, const void* base, long long total_tokens, int Hkv, int G, int d, int tokens);
 
 // Device status words, one a kernel unit, of the current device.
 cudaError_t status_word_prefill(uint32_t** at);

@@ -528,7 +528,7 @@ ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int 
  * sees.
  *   blocks: device int32 [B, Nq, Hkv, n_sel], in any order; negative entries
  *            are passed over, as are blocks behind the token's position; a block
- *            listed twice counts twice; an entry past the table is passed over
+ *            listed twice counts twice; n_sel is at most 512; an entry past the table is passed over
  *            and reported as ATTN_ERR_DEVICE_ARG by attn_get_device_status;
  *   workspace: attn_fwd_blocks_paged_workspace_size bytes.
  * The other arguments, limits and results are those of
