@@ -63,7 +63,7 @@ bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_siz
 }
 
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d) {
-  return make_map(m, base, num_pages, page_size, Hkv, d, 64);
+  return make_map(m, base, num_pages * (page_size / 64), 64, Hkv, d, 64);
 }
 
 // 4-D view {d, G, Hkv, tokens} of q [tokens, Hkv * G, d]; box {64, G, 1, tokens}.

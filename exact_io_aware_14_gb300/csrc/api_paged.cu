@@ -83,6 +83,7 @@ attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pa
   if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;  // a token's heads of a group fit one tile of rows
   if (static_cast<long long>(B) * Nq * Hq > kIntMax - 4096) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * (page_size / 64) > kIntMax) return ATTN_ERR_UNSUPPORTED;  // blocks of the pool
   if (!q || !k_pages || !v_pages || !o || !lse) return ATTN_ERR_INVALID_ARG;
   if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(o, 16) || off(lse, 4)) return ATTN_ERR_MISALIGNED;
   const long long rows = static_cast<long long>(B) * Nq * Hq;

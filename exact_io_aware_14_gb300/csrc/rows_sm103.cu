@@ -90,16 +90,18 @@ struct Layout {
 };
 static_assert(Layout<128>::kAlloc <= 232448 && Layout<64>::kAlloc <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
-  bool ok = mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
-  ok = __all_sync(0xffffffffu, ok);
-  if (!ok && (threadIdx.x & 31) == 0) record(site, kDevTimeout);
-  return ok;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
+// Bounded waits: one probe in line, the rest out of line, as the warps' code
+// together has to fit the instruction cache (57% of the fetches hit it before).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
   const bool ok = mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
   if (!ok) record(site, kDevTimeout);
   return ok;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
+  return mbar_test_wait(bar, parity) || wait_long(bar, parity, abort_flag, site);
+}
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, site));
 }
 
 __device__ __forceinline__ int clamped_len(const RowsParams& p, int b) {
@@ -112,11 +114,11 @@ __device__ __forceinline__ int own_tiles(const RowsParams& p, int b) {
 }
 // `total` tiles dealt to `lanes` in runs of equal length, none of them empty but
 // the last ones: where run i starts, and which run holds tile x.
-__device__ __forceinline__ long long run_start(long long total, int lanes, int i) {
+__device__ __noinline__ long long run_start(long long total, int lanes, int i) {
   const long long runs = min(total, static_cast<long long>(lanes));
   return i < runs ? total * i / runs : total;
 }
-__device__ __forceinline__ int run_of(long long total, int lanes, long long x) {
+__device__ __noinline__ int run_of(long long total, int lanes, long long x) {
   const long long runs = min(total, static_cast<long long>(lanes));
   return static_cast<int>(((x + 1) * runs - 1) / total);
 }
@@ -202,18 +204,658 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
   }
 }
 
-// Where a lane stands in its run (all lanes of the producer warp alike).
-struct Lane {
-  long long left;       // ranges: tiles left
-  long long unit, end;  // lists: next whole unit and their end; then the cut ones
-  int b, h, rt, t;      // ranges
+// Shared memory of a CTA.
+template <int D>
+struct Smem {
+  uint8_t *q, *ring;
+  Piece* pieces;         // [slot][2]
+  uint64_t* full;        // [kSlots] ring slot holds its tile
+  uint64_t* empty;       // [kSlots] ring slot read
+  uint64_t* sfull;       // [2] scores complete
+  uint64_t* pfull;       // [2] P written (4 warps)
+  uint64_t* odone;       // [2] a piece's last P V complete
+  uint64_t* ofree;       // [2] a piece's O read (4 warps)
+  uint64_t* qfull;       // [slot][2] rows loaded
+  uint64_t* qfree;       // [slot][2] a piece's last Q K^T complete
+  uint64_t* pieced;      // [slot][2] piece told
+  uint64_t* unpieced;    // [slot][2] piece done with (MMA thread, 4 warps)
+  uint64_t* fixset;      // [4] clearing asked for
+  uint64_t* fixdone;     // [4] done
+  uint64_t* raw;         // [4] value tile to be cleared landed
+  uint64_t* drain;       // after an abort: the MMAs issued so far completed
+  Fix* fixes;
+  Plan* plan;
+  volatile int* abort_flag;
+  uint32_t* tmem_slot;
+  __device__ __forceinline__ explicit Smem(uint8_t* base) {
+    using L = Layout<D>;
+    q = base;
+    ring = base + L::kOffRing;
+    pieces = reinterpret_cast<Piece*>(base + L::kOffPiece);
+    full = reinterpret_cast<uint64_t*>(base + L::kOffBar);
+    empty = full + L::kSlots;
+    sfull = empty + L::kSlots;
+    pfull = sfull + 2;
+    odone = pfull + 2;
+    ofree = odone + 2;
+    qfull = ofree + 2;
+    qfree = qfull + 4;
+    pieced = qfree + 4;
+    unpieced = pieced + 4;
+    fixset = unpieced + 4;
+    fixdone = fixset + 4;
+    raw = fixdone + 4;
+    drain = raw + 4;
+    fixes = reinterpret_cast<Fix*>(base + L::kOffFix);
+    plan = reinterpret_cast<Plan*>(base + L::kOffPlan);
+    tmem_slot = reinterpret_cast<uint32_t*>(base + L::kOffMisc);
+    abort_flag = reinterpret_cast<volatile int*>(base + L::kOffMisc + 4);
+  }
 };
 
-// The producer's view of a piece: its keys.
-struct Keys {
-  int key0, end, row;     // ranges: first key, end of the keys; table row
-  const int* list;        // lists: entries of the piece, `count` of them
-  int count, seen;        // seen: keys before the token's own end
+// A place in the ring: slot and phase of the turn through it.
+template <int NS>
+struct RingAt {
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == NS) {
+      slot = 0;
+      ++turn;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Producer: one warp, whose lanes look up 32 blocks of a piece at a time; lane 0
+// waits and issues.  What belongs to a slot is in a struct; the two take turns in
+// the same registers and the same code (exchanged after each step), so that no
+// state lies in local memory and the code is there once.
+struct Tile {
+  int g0, g1;      // blocks of the pool
+  uint32_t flags;  // bits 0, 1: seen; 2, 3: seen whole
+  int part;
+};
+struct ProducerSlot {
+  // the lane's run
+  long long left;        // tiles left (lists: of the cut units)
+  long long unit;        // lists: next whole unit
+  int b, h, rt, t;       // ranges: where it stands
+  // the piece being loaded
+  int n, j, head;
+  int key0, end, row;    // ranges: first key, end of the keys; table row
+  const int* list;       // lists: entries of the piece, `count` of them
+  int count, seen;       // seen: keys before the token's own end
+  int blk;               // this lane's block of the 32 looked up
+  uint32_t seen_bits, full_bits;
+  int part;
+  Tile last;             // the tile whose V comes next
+  uint32_t told, rows_n[2];
+  int slot;
+  bool fin, pend;
+};
+template <typename T>
+__device__ __forceinline__ void exchange(T& a, T& b) {
+  const T t = a;
+  a = b;
+  b = t;
+}
+
+template <int D, bool kList>
+struct Producer {
+  using L = Layout<D>;
+  const RowsParams& p;
+  const CUtensorMap *tm_q, *tm_qs, *tm_k, *tm_v;
+  const Smem<D>& sm;
+  const int lane;
+  RingAt<L::kSlots> at;
+  uint32_t fix_n = 0;
+  bool ok = true;  // lane 0's view until `agree`
+  // the last loads: whether on a ring slot's `full` (its phase), on a `raw` (its phase)
+  uint32_t on_full = 0, full_ph = 0, on_raw = 0, raw_ph = 0;
+
+  __device__ __forceinline__ Producer(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* qs, const CUtensorMap* k,
+                                      const CUtensorMap* v, const Smem<D>& sm_, int lane_)
+      : p(p_), tm_q(q), tm_qs(qs), tm_k(k), tm_v(v), sm(sm_), lane(lane_) {}
+
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  __device__ __forceinline__ bool agree() {
+    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+    return ok;
+  }
+
+  // block `blk` of table row `row`, as a block of the pool
+  __device__ __forceinline__ int pool_block(int row, int blk) {
+    const int at_page = blk * 64 / p.page_size;
+    int g = p.block_table[static_cast<long long>(row) * p.max_blocks + at_page];
+    if (g < 0 || g >= p.num_pages) {
+      record(2, kDevBadPage);
+      g = 0;
+    }
+    return g * (p.page_size / 64) + blk - at_page * (p.page_size / 64);
+  }
+  // blocks 32 i .. 32 i + 31 of the piece
+  __device__ __forceinline__ void look_up(ProducerSlot& s, int i) {
+    int v = 0, blk;
+    if (kList) {
+      const int e = 32 * i + lane;
+      blk = e < s.count ? s.list[e] : -1;
+      if (blk >= 0) {
+        if (blk >= p.max_blocks * (p.page_size / 64))
+          record(3, kDevBadPage);
+        else
+          v = min(64, s.seen - blk * 64);
+      }
+    } else {
+      const int key = s.key0 + 64 * (32 * i + lane);
+      v = min(64, s.end - key);
+      blk = key >> 6;
+    }
+    s.blk = 0;
+    if (v > 0) s.blk = pool_block(s.row, blk);
+    s.seen_bits = __ballot_sync(0xffffffffu, v > 0);
+    s.full_bits = __ballot_sync(0xffffffffu, v == 64);
+    const uint32_t some = s.seen_bits & ~s.full_bits;
+    s.part = some ? __shfl_sync(0xffffffffu, v, __ffs(some) - 1) : 0;  // the same for all of them
+  }
+  __device__ __forceinline__ Tile tile(const ProducerSlot& s, int j) {
+    const int e = 2 * (j & 15);
+    Tile t;
+    t.g0 = __shfl_sync(0xffffffffu, s.blk, e);
+    t.g1 = __shfl_sync(0xffffffffu, s.blk, e + 1);
+    t.flags = (s.seen_bits >> e & 3u) | (s.full_bits >> e & 3u) << 2;
+    t.part = s.part;
+    return t;
+  }
+  // a K or V tile into the next ring slot
+  __device__ __forceinline__ void load(const Tile& t, int h, bool is_v) {
+    if (lane == 0) {
+      if (at.turn > 0) wait(sm.empty + at.slot, at.turn - 1, 11);
+      const bool fix = is_v && (t.flags >> 2) != 3u;
+      const uint32_t fi = fix_n & 3;
+      if (fix && fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+      if (ok) {
+        const bool s0 = t.flags & 1u, s1 = t.flags & 2u;
+        uint64_t* done = fix ? sm.raw + fi : sm.full + at.slot;
+        if (fix) {
+          sm.fixes[fi].slot = static_cast<int>(at.slot);
+          sm.fixes[fi].v0 = t.flags & 4u ? 64 : (s0 ? t.part : 0);
+          sm.fixes[fi].v1 = t.flags & 8u ? 64 : (s1 ? t.part : 0);
+        }
+        if (s0 || s1)
+          mbar_arrive_expect_tx(done, s0 && s1 ? L::kTile : L::kTile / 2);
+        else
+          mbar_arrive(done);
+        uint8_t* dst = sm.ring + at.slot * L::kTile;
+        const CUtensorMap* tm = is_v ? tm_v : tm_k;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          if (s0) tma_load_4d(dst + c * L::kHalf, tm, done, c * 64, h, 0, t.g0);
+          if (s1) tma_load_4d(dst + c * L::kHalf + 64 * 128, tm, done, c * 64, h, 0, t.g1);
+        }
+        if (fix) {
+          mbar_arrive(sm.fixset + fi);
+          on_full &= ~(1u << at.slot);
+          on_raw |= 1u << fi;
+          raw_ph = (raw_ph & ~(1u << fi)) | ((fix_n / 4 & 1u) << fi);
+          ++fix_n;
+        } else {
+          on_full |= 1u << at.slot;
+          full_ph = (full_ph & ~(1u << at.slot)) | ((at.turn & 1u) << at.slot);
+        }
+      }
+    }
+    at.next();
+  }
+  // the place of the slot's next piece, once it is free
+  __device__ __forceinline__ Piece& place(const ProducerSlot& s) {
+    if (lane == 0 && s.told >= 2) wait(sm.unpieced + s.slot * 2 + (s.told & 1), s.told / 2 - 1, 13);
+    return sm.pieces[s.slot * 2 + (s.told & 1)];
+  }
+  __device__ __forceinline__ void tell(ProducerSlot& s, Piece& d, int n, int share, int h, int tok0, int ntok, int key0, int keys,
+                                       int dst) {
+    if (lane == 0 && ok) {
+      d.n = n;
+      d.share = share;
+      d.h = h;
+      d.tok0 = tok0;
+      d.ntok = ntok;
+      d.key0 = key0;
+      d.keys = keys;
+      d.dst = dst;
+      mbar_arrive(sm.pieced + s.slot * 2 + (s.told & 1));
+    }
+    ++s.told;
+  }
+  // the rows of a piece; buffers in turn where there are two
+  __device__ __forceinline__ void load_rows(ProducerSlot& s, bool second, bool pair, int h, int tok0) {
+    uint32_t uses = second ? s.rows_n[1] : s.rows_n[0];
+    const int buf = s.slot * 2 + (second ? 1 : 0);
+    if (lane == 0) {
+      if (uses > 0) wait(sm.qfree + buf, uses - 1, 14);
+      if (ok) {
+        const int tokens = pair ? p.tile_tokens : p.unit_tokens;
+        mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(tokens * (p.Hq / p.Hkv) * D * 2));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sm.q + s.slot * L::kTile + c * L::kHalf + (second ? 64 * 128 : 0), pair ? tm_q : tm_qs, sm.qfull + buf, c * 64, 0,
+                      h, tok0);
+        if (second)
+          ++s.rows_n[1];
+        else
+          ++s.rows_n[0];
+      }
+    }
+  }
+
+  // Pair work: pieces of the CTA's run, each to its end.
+  __device__ __forceinline__ void pair_work(ProducerSlot& a, ProducerSlot& b) {
+    const int end = sm.plan->prefix_end, nt = tiles_of(end), grid = gridDim.x, tokens = p.B * p.Nq;
+    long long x = run_start(sm.plan->pair_total, grid, blockIdx.x);
+    const long long x1 = run_start(sm.plan->pair_total, grid, blockIdx.x + 1);
+    while (x < x1 && agree()) {
+      const int unit = static_cast<int>(x / nt), t = static_cast<int>(x - static_cast<long long>(unit) * nt);
+      const int n = static_cast<int>(min(static_cast<long long>(nt - t), x1 - x));
+      const int h = unit / p.pairs, pair = unit - h * p.pairs;
+      const int tok0 = 2 * pair * p.tile_tokens, tok1 = tok0 + p.tile_tokens;
+      const int share = tok1 < tokens ? 1 : 2, dst = static_cast<int>(blockIdx.x) + unit;
+      a.key0 = 128 * t;
+      a.end = end;
+      a.row = 0;
+      Piece& d0 = place(a);
+      tell(a, d0, n, share, h, tok0, min(p.tile_tokens, tokens - tok0), a.key0, end - a.key0, dst);
+      Piece& d1 = place(b);
+      tell(b, d1, n, share, h, tok1, max(0, min(p.tile_tokens, tokens - tok1)), a.key0, end - a.key0, dst);
+      load_rows(a, false, true, h, tok0);
+      if (share == 1) load_rows(b, false, true, h, tok1);
+      for (int j = 0; j <= n; ++j) {
+        if (j > 0) load(a.last, h, true);
+        if (j == n) break;
+        if ((j & 15) == 0) look_up(a, j >> 4);
+        a.last = tile(a, j);
+        load(a.last, h, false);
+      }
+      x += n;
+    }
+  }
+
+  // Next piece of a slot: told, its rows on their way; n = 0 where there is none or nothing to compute.
+  __device__ __forceinline__ void next_piece(ProducerSlot& s) {
+    const int l = lane_of(s.slot), lanes = 2 * gridDim.x;
+    Piece& d = place(s);
+    int tok0, ntok, dst;
+    s.j = 0;
+    if (kList) {
+      const int units = p.B * p.Nq * p.Hkv, unit_tiles = (p.n_sel + 1) >> 1;
+      const int whole = units / lanes * lanes;
+      const long long cut = static_cast<long long>(units - whole) * unit_tiles;
+      long long u;
+      int t0 = 0, nt = unit_tiles;
+      dst = -1;
+      if (s.unit < whole) {
+        u = s.unit;
+        s.unit += lanes;
+      } else if (s.left > 0) {
+        const long long first = run_start(cut, lanes, l), x = run_start(cut, lanes, l + 1) - s.left;
+        const int cu = static_cast<int>(x / unit_tiles);
+        u = whole + cu;
+        t0 = static_cast<int>(x - static_cast<long long>(cu) * unit_tiles);
+        nt = static_cast<int>(min(static_cast<long long>(unit_tiles - t0), s.left));
+        if (nt < unit_tiles) dst = 2 * l + (x > first ? 1 : 0);
+        s.left -= nt;
+      } else {
+        s.fin = true;
+        s.n = 0;
+        tell(s, d, -1, 0, 0, 0, 0, 0, 0, 0);
+        return;
+      }
+      // units by sequence, head, token: neighbours read the same head's keys
+      const int per = p.Hkv * p.Nq;
+      const int b = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<long long>(b) * per);
+      s.head = r / p.Nq;
+      const int i = r - s.head * p.Nq;
+      tok0 = b * p.Nq + i;
+      ntok = 1;
+      const int len = clamped_len(p, b);
+      if (lane == 0 && s.head == 0 && i == 0 && t0 == 0 && len != p.seqlens[b]) record(1, kDevBadSeqlen);
+      s.row = b;
+      s.seen = max(0, len - p.Nq + i + 1);
+      s.list = p.blocks + (static_cast<long long>(tok0) * p.Hkv + s.head) * p.n_sel + 2 * t0;
+      s.count = min(p.n_sel - 2 * t0, 2 * nt);
+      s.key0 = s.end = 0;
+      // which of them are seen; the last one that is ends the piece
+      int last = -1;
+      for (int w = (s.count - 1) >> 5; w >= 0; --w) {  // ends with the first 32 looked up
+        look_up(s, w);
+        if (lane == 0 && ok) {
+          d.full[w] = s.full_bits;
+          d.some[w] = s.seen_bits & ~s.full_bits;
+          if (d.some[w]) d.part = s.part;
+        }
+        if (last < 0 && s.seen_bits) last = 32 * w + 31 - __clz(s.seen_bits);
+      }
+      s.n = (last + 2) >> 1;
+    } else {
+      if (s.left == 0) {
+        s.fin = true;
+        s.n = 0;
+        tell(s, d, -1, 0, 0, 0, 0, 0, 0, 0);
+        return;
+      }
+      int len = s.b < 0 ? 0 : clamped_len(p, s.b);
+      while (s.b >= 0 && len <= p.shared_len) len = clamped_len(p, ++s.b);  // a sequence with keys of its own is ahead
+      int nt, rts, unit;
+      s.head = s.h;
+      if (s.b < 0) {
+        s.end = sm.plan->prefix_end;
+        s.key0 = 128 * s.t;
+        s.row = 0;
+        nt = tiles_of(s.end);
+        rts = 1;
+        unit = s.h;
+        tok0 = 0;
+        ntok = p.B * p.Nq;
+      } else {
+        s.end = len;
+        s.key0 = p.shared_len + 128 * s.t;
+        s.row = s.b;
+        nt = tiles_of(len - p.shared_len);
+        rts = p.own_rt;
+        unit = (s.b * p.Hkv + s.h) * rts + s.rt + (p.pairs ? 0 : p.Hkv);
+        tok0 = s.b * p.Nq + s.rt * p.own_tokens;
+        ntok = min(p.own_tokens, p.Nq - s.rt * p.own_tokens);
+      }
+      dst = l + unit;
+      s.n = static_cast<int>(min(static_cast<long long>(nt - s.t), s.left));
+      s.left -= s.n;
+      s.t += s.n;
+      if (s.t == nt) {
+        s.t = 0;
+        if (++s.rt == rts) {
+          s.rt = 0;
+          if (++s.h == p.Hkv) {
+            s.h = 0;
+            ++s.b;
+          }
+        }
+      }
+    }
+    tell(s, d, s.n, 0, s.head, tok0, ntok, s.key0, s.end - s.key0, dst);
+    if (s.n == 0) return;
+    load_rows(s, p.q_buffers == 2 && (s.rows_n[0] + s.rows_n[1] & 1u), false, s.head, tok0);
+    if (!kList) look_up(s, 0);
+  }
+
+  __device__ __forceinline__ void start_lane(ProducerSlot& s) {
+    const int l = lane_of(s.slot), lanes = 2 * gridDim.x;
+    s.n = s.j = 0;
+    if (kList) {
+      const int units = p.B * p.Nq * p.Hkv;
+      const long long cut = static_cast<long long>(units - units / lanes * lanes) * ((p.n_sel + 1) >> 1);
+      s.unit = l;
+      s.left = run_start(cut, lanes, l + 1) - run_start(cut, lanes, l);
+    } else {
+      const long long total = sm.plan->total;
+      s.left = run_start(total, lanes, l + 1) - run_start(total, lanes, l);
+      if (s.left > 0) {
+        s.b = sm.plan->lane_b[s.slot];
+        const int nt = s.b < 0 ? tiles_of(sm.plan->prefix_end) : own_tiles(p, s.b), rts = s.b < 0 ? 1 : p.own_rt;
+        const long long x = sm.plan->lane_at[s.slot];
+        const int u = static_cast<int>(x / nt);
+        s.h = u / rts;
+        s.rt = u - s.h * rts;
+        s.t = static_cast<int>(x - static_cast<long long>(u) * nt);
+      }
+      // rows of pairs lie over both buffers: read to their end
+      if (lane == 0 && s.rows_n[0] > 0) wait(sm.qfree + s.slot * 2, s.rows_n[0] - 1, 14);
+    }
+  }
+
+  __device__ __forceinline__ void lane_step(ProducerSlot& s) {
+    if (s.pend) load(s.last, s.head, true);
+    s.pend = false;
+    while (!s.fin && s.j == s.n && agree()) next_piece(s);
+    if (s.fin) return;  // the lanes part nowhere else: what lane 0 alone knows of a failure only keeps it from issuing
+    if (s.j > 0 && (s.j & 15) == 0) look_up(s, s.j >> 4);
+    s.last = tile(s, s.j);
+    load(s.last, s.head, false);
+    ++s.j;
+    s.pend = true;
+  }
+
+  __device__ __forceinline__ void run() {
+    ProducerSlot a, b;
+    a.told = b.told = a.rows_n[0] = a.rows_n[1] = b.rows_n[0] = b.rows_n[1] = 0;
+    a.fin = b.fin = a.pend = b.pend = false;
+    a.slot = 0;
+    b.slot = 1;
+    if (!kList && sm.plan->pair_total > 0) pair_work(a, b);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      start_lane(a);
+      exchange(a, b);
+    }
+#pragma unroll 1
+    while (agree() && !(a.fin && b.fin && !a.pend && !b.pend)) {
+      lane_step(a);
+      exchange(a, b);
+    }
+    if (a.slot) exchange(a, b);
+    if (lane != 0) return;
+    if (ok) {
+      // no more to clear
+      const uint32_t fi = fix_n & 3;
+      if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+      if (ok) {
+        sm.fixes[fi].slot = -1;
+        mbar_arrive(sm.fixset + fi);
+      }
+    }
+    // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
+    volatile int no_abort = 0;
+    auto drain = [&](uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity & 1, &no_abort, kWaitLimitNs); };
+    if (a.rows_n[0]) drain(sm.qfull + 0, a.rows_n[0] - 1);
+    if (a.rows_n[1]) drain(sm.qfull + 1, a.rows_n[1] - 1);
+    if (b.rows_n[0]) drain(sm.qfull + 2, b.rows_n[0] - 1);
+    if (b.rows_n[1]) drain(sm.qfull + 3, b.rows_n[1] - 1);
+    for (int i = 0; i < 4; ++i)
+      if (on_raw >> i & 1u) drain(sm.raw + i, raw_ph >> i);
+    for (int i = 0; i < L::kSlots; ++i)
+      if (on_full >> i & 1u) drain(sm.full + i, full_ph >> i);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// MMA issuer: one thread.
+struct MmaSlot {
+  int n, j;
+  uint32_t seen, done, tiles;  // pieces looked at, with products; P tiles consumed
+  uint32_t rows_n[2];
+  uint32_t buf;
+  uint32_t slot;
+  bool fin, pend;
+};
+
+template <int D>
+struct Issuer {
+  using L = Layout<D>;
+  static constexpr uint32_t kIdescQk = idesc_bf16_f32(128, 128, 0), kIdescPv = idesc_bf16_f32(128, D, 1);
+  const Smem<D>& sm;
+  const uint32_t tmem;
+  const bool two_buffers;
+  uint64_t dQ, dK, dV;
+  RingAt<L::kSlots> at;
+  bool ok = true;
+
+  __device__ __forceinline__ Issuer(const Smem<D>& sm_, uint32_t tmem_, bool two) : sm(sm_), tmem(tmem_), two_buffers(two) {
+    dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);
+    dK = sdesc_sw128(smem_u32(sm.ring), 16, 1024);
+    dV = sdesc_sw128(smem_u32(sm.ring), L::kHalf, 1024);
+  }
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  // O_S (+)= P_S V, S_S = Q_S K^T with the tile in ring slot `slot`
+  __device__ __forceinline__ void pv(uint32_t S, uint32_t slot, bool first) {
+    const uint64_t dv = dV + static_cast<uint64_t>((slot * L::kTile) >> 4);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_bf16_ts(tmem + 256 + S * 128, tmem + S * 128 + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescPv,
+                  (!first || kk > 0) ? 1u : 0u);
+  }
+  __device__ __forceinline__ void qk(uint32_t S, uint32_t slot, uint32_t buf) {
+    const uint64_t da = dQ + static_cast<uint64_t>((S * L::kTile + buf * (64 * 128)) >> 4);
+    const uint64_t db = dK + static_cast<uint64_t>((slot * L::kTile) >> 4);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
+      mma_bf16_ss(tmem + S * 128, da + off, db + off, kIdescQk, kk > 0 ? 1u : 0u);
+    }
+    mma_commit(sm.sfull + S);
+  }
+  // Next piece of a slot; false where there is none to come.
+  __device__ __forceinline__ void take(MmaSlot& s, int* share) {
+    const uint32_t i = s.slot * 2 + (s.seen & 1);
+    wait(sm.pieced + i, s.seen / 2, 24);
+    if (!ok) return;
+    const volatile Piece& d = sm.pieces[i];
+    s.n = d.n;
+    *share = d.share;
+    mbar_arrive(sm.unpieced + i);
+    ++s.seen;
+    s.j = 0;
+    s.fin = s.n < 0;
+    if (s.fin) s.n = 0;
+  }
+
+  // One piece of pair work, both slots (told already); slot 1 has rows only if `both`.
+  __device__ __forceinline__ void pair_piece(MmaSlot& a, MmaSlot& b, bool both) {
+    const int n = a.n;
+    wait(sm.qfull + 0, a.rows_n[0]++, 26);
+    if (both) wait(sm.qfull + 2, b.rows_n[0]++, 26);
+    uint32_t vs = 0, vturn = 0;  // where V of the tile before lies
+    bool p0 = false;
+    for (int j = 0; ok && j <= n; ++j) {
+      // ring: (V of j - 1), K of j
+      if (j > 0) {
+        vs = at.slot;
+        vturn = at.turn;
+        at.next();
+        wait(sm.full + vs, vturn, 21);
+        if (!p0) wait(sm.pfull + 0, a.tiles, 22);
+        ++a.tiles;
+        if (j == 1 && a.done > 0) wait(sm.ofree + 0, a.done - 1, 23);
+        if (!ok) break;
+        tc_fence_after();
+        pv(0, vs, j == 1);
+      }
+      const uint32_t ks = at.slot, kturn = at.turn;
+      if (j < n) {
+        at.next();
+        wait(sm.full + ks, kturn, 25);
+        if (!ok) break;
+        tc_fence_after();
+        qk(0, ks, 0);
+        if (j == n - 1) mma_commit(sm.qfree + 0);
+      } else {
+        mma_commit(sm.odone + 0);
+      }
+      if (both) {
+        if (j > 0) {
+          wait(sm.pfull + 1, b.tiles++, 22);
+          if (j == 1 && b.done > 0) wait(sm.ofree + 1, b.done - 1, 23);
+          if (!ok) break;
+          tc_fence_after();
+          pv(1, vs, j == 1);
+        }
+        if (j < n) {
+          qk(1, ks, 0);
+          if (j == n - 1) mma_commit(sm.qfree + 2);
+        } else {
+          mma_commit(sm.odone + 1);
+        }
+      }
+      if (j > 0) mma_commit(sm.empty + vs);
+      if (j < n) mma_commit(sm.empty + ks);
+      // the next step's first wait, in the shadow of what was issued
+      p0 = mbar_test_wait(sm.pfull + 0, a.tiles & 1);
+    }
+    ++a.done;
+    if (both) ++b.done;
+  }
+
+  __device__ __forceinline__ void lane_step(MmaSlot& s) {
+    if (s.pend) {
+      const uint32_t vs = at.slot;
+      wait(sm.full + vs, at.turn, 21);
+      at.next();
+      wait(sm.pfull + s.slot, s.tiles++, 22);
+      const bool first = s.j == 1;
+      if (first && s.done > 0) wait(sm.ofree + s.slot, s.done - 1, 23);
+      if (!ok) return;
+      tc_fence_after();
+      pv(s.slot, vs, first);
+      mma_commit(sm.empty + vs);
+      if (s.j == s.n) {
+        mma_commit(sm.odone + s.slot);
+        ++s.done;
+      }
+      s.pend = false;
+    }
+    int share;
+    while (ok && !s.fin && s.j == s.n) take(s, &share);
+    if (!ok || s.fin) return;
+    const uint32_t ks = at.slot;
+    wait(sm.full + ks, at.turn, 25);
+    at.next();
+    if (s.j == 0) {
+      s.buf = two_buffers ? (s.rows_n[0] + s.rows_n[1]) & 1u : 0u;
+      wait(sm.qfull + s.slot * 2 + s.buf, s.buf ? s.rows_n[1] : s.rows_n[0], 26);
+      if (s.buf)
+        ++s.rows_n[1];
+      else
+        ++s.rows_n[0];
+    }
+    if (!ok) return;
+    tc_fence_after();
+    qk(s.slot, ks, s.buf);
+    ++s.j;
+    if (s.j == s.n) mma_commit(sm.qfree + s.slot * 2 + s.buf);
+    mma_commit(sm.empty + ks);
+    s.pend = true;
+  }
+
+  __device__ __forceinline__ void run() {
+    MmaSlot a, b;
+    a.n = a.j = b.n = b.j = 0;
+    a.seen = a.done = a.tiles = a.rows_n[0] = a.rows_n[1] = a.buf = 0;
+    b.seen = b.done = b.tiles = b.rows_n[0] = b.rows_n[1] = b.buf = 0;
+    a.fin = b.fin = a.pend = b.pend = false;
+    a.slot = 0;
+    b.slot = 1;
+    // pair pieces come first, both slots told of each
+    int share = 0;
+    for (;;) {
+      while (ok && !a.fin && a.n == 0) take(a, &share);
+      if (!ok || a.fin || share == 0) break;
+      int other;
+      take(b, &other);
+      if (ok) pair_piece(a, b, share == 1);
+      a.n = b.n = a.j = b.j = 0;
+    }
+#pragma unroll 1
+    while (ok && !(a.fin && b.fin && !a.pend && !b.pend)) {
+      lane_step(a);
+      exchange(a, b);
+    }
+    if (!ok) {
+      // the MMAs issued so far complete before TMEM is freed
+      volatile int no_abort = 0;
+      mma_commit(sm.drain);
+      mbar_wait(sm.drain, 0, &no_abort, kWaitLimitNs);
+    }
+  }
 };
 
 template <int D, bool kList>
@@ -225,532 +867,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NS = L::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sQ = smem;
-  uint8_t* sRing = smem + L::kOffRing;
-  Piece* pieces = reinterpret_cast<Piece*>(smem + L::kOffPiece);  // [slot][2]
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [NS] ring slot holds its tile
-  uint64_t* bar_empty = bar_full + NS;    // [NS] ring slot read
-  uint64_t* bar_sfull = bar_empty + NS;   // [2] scores complete
-  uint64_t* bar_pfull = bar_sfull + 2;    // [2] P written (4 warps)
-  uint64_t* bar_odone = bar_pfull + 2;    // [2] a piece's last P V complete
-  uint64_t* bar_ofree = bar_odone + 2;    // [2] a piece's O read (4 warps)
-  uint64_t* bar_qfull = bar_ofree + 2;    // [slot][2] rows loaded
-  uint64_t* bar_qfree = bar_qfull + 4;    // [slot][2] a piece's last Q K^T complete
-  uint64_t* bar_pieced = bar_qfree + 4;   // [slot][2] piece told
-  uint64_t* bar_unpieced = bar_pieced + 4;  // [slot][2] piece done with (MMA thread, 4 warps)
-  uint64_t* bar_fixset = bar_unpieced + 4;  // [4] clearing asked for
-  uint64_t* bar_fixdone = bar_fixset + 4;   // [4] done
-  uint64_t* bar_raw = bar_fixdone + 4;      // [4] value tile to be cleared landed
-  uint64_t* bar_drain = bar_raw + 4;        // after an abort: the MMAs issued so far completed
-  Fix* fixes = reinterpret_cast<Fix*>(smem + L::kOffFix);
-  Plan* plan = reinterpret_cast<Plan*>(smem + L::kOffPlan);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  const Smem<D> sm(smem);
+  volatile int* abort_flag = sm.abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bar_full + i, 1);
-      mbar_init(bar_empty + i, 1);
+      mbar_init(sm.full + i, 1);
+      mbar_init(sm.empty + i, 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar_sfull + s, 1);
-      mbar_init(bar_pfull + s, 4);
-      mbar_init(bar_odone + s, 1);
-      mbar_init(bar_ofree + s, 4);
+      mbar_init(sm.sfull + s, 1);
+      mbar_init(sm.pfull + s, 4);
+      mbar_init(sm.odone + s, 1);
+      mbar_init(sm.ofree + s, 4);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar_qfull + i, 1);
-      mbar_init(bar_qfree + i, 1);
-      mbar_init(bar_pieced + i, 1);
-      mbar_init(bar_unpieced + i, 5);
-      mbar_init(bar_fixset + i, 1);
-      mbar_init(bar_fixdone + i, 1);
-      mbar_init(bar_raw + i, 1);
+      mbar_init(sm.qfull + i, 1);
+      mbar_init(sm.qfree + i, 1);
+      mbar_init(sm.pieced + i, 1);
+      mbar_init(sm.unpieced + i, 5);
+      mbar_init(sm.fixset + i, 1);
+      mbar_init(sm.fixdone + i, 1);
+      mbar_init(sm.raw + i, 1);
     }
-    mbar_init(bar_drain, 1);
+    mbar_init(sm.drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
   grid_depends();
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_alloc(sm.tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   if (!kList)
-    make_plan(p, plan, reinterpret_cast<long long*>(smem + L::kOffScan),
+    make_plan(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
               reinterpret_cast<int*>(smem + L::kOffScan + 12 * 8));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *sm.tmem_slot;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    const int cap = p.max_blocks * p.page_size;
-    uint32_t ring = 0, fix_n = 0;
-    uint32_t told[2] = {0, 0};
-    uint32_t q_uses[2][2] = {{0, 0}, {0, 0}};
-    // the last loads: whether on a ring slot's bar_full (its phase), on a bar_raw (its phase)
-    uint32_t on_full = 0, full_ph = 0, on_raw = 0, raw_ph = 0;
-    bool ok = true;
-
-    // pages of 32 blocks of a piece, one a lane: number, row of the page; flags: bit 0 seen, bit 1 seen whole
-    int pg[2], prow[2];
-    uint32_t batch_seen[2] = {0, 0}, batch_full[2] = {0, 0};
-    int batch_part[2] = {0, 0};
-    Keys keys[2];
-
-    auto page_of = [&](int row, int blk, int* out_row) {
-      const int at = blk * 64 / p.page_size;
-      int g = p.block_table[static_cast<long long>(row) * p.max_blocks + at];
-      if (g < 0 || g >= p.num_pages) {
-        record(2, kDevBadPage);
-        g = 0;
-      }
-      *out_row = blk * 64 - at * p.page_size;
-      return g;
-    };
-    // looks up blocks 32 i .. 32 i + 31 of slot s's piece
-    auto look_up = [&](int s, int i) {
-      const Keys& k = keys[s];
-      bool seen = false;
-      pg[s] = prow[s] = 0;
-      int v = 0;
-      if (kList) {
-        const int e = 32 * i + lane;
-        const int blk = e < k.count ? k.list[e] : -1;
-        if (blk >= 0) {
-          if (blk >= cap / 64)
-            record(3, kDevBadPage);
-          else
-            v = min(64, k.seen - blk * 64);
-        }
-        seen = v > 0;
-        if (seen) pg[s] = page_of(k.row, blk, &prow[s]);
-      } else {
-        const int key = k.key0 + 64 * (32 * i + lane);
-        v = min(64, k.end - key);
-        seen = v > 0;
-        if (seen) pg[s] = page_of(k.row, key / 64, &prow[s]);
-      }
-      batch_seen[s] = __ballot_sync(0xffffffffu, seen);
-      batch_full[s] = __ballot_sync(0xffffffffu, v == 64);
-      const uint32_t some = batch_seen[s] & ~batch_full[s];
-      batch_part[s] = some ? __shfl_sync(0xffffffffu, v, __ffs(some) - 1) : 0;  // the same for all of them
-    };
-    // loads the K or V tile j of slot s's piece into the next ring slot
-    auto load = [&](int s, int j, bool is_v) {
-      const int e = 2 * (j & 15);
-      const int g0 = __shfl_sync(0xffffffffu, pg[s], e), g1 = __shfl_sync(0xffffffffu, pg[s], e + 1);
-      const int r0 = __shfl_sync(0xffffffffu, prow[s], e), r1 = __shfl_sync(0xffffffffu, prow[s], e + 1);
-      const bool s0 = batch_seen[s] >> e & 1u, s1 = batch_seen[s] >> (e + 1) & 1u;
-      const bool f0 = batch_full[s] >> e & 1u, f1 = batch_full[s] >> (e + 1) & 1u;
-      bool good = true;
-      if (lane == 0) {
-        const uint32_t slot = ring % NS;
-        good = ring < NS || wait_one(bar_empty + slot, (ring / NS - 1) & 1, abort_flag, 11);
-        const bool fix = is_v && !(f0 && f1);
-        const uint32_t fi = fix_n & 3;
-        if (good && fix && fix_n >= 4) good = wait_one(bar_fixdone + fi, (fix_n / 4 - 1) & 1, abort_flag, 12);
-        if (good) {
-          uint64_t* done = fix ? bar_raw + fi : bar_full + slot;
-          const uint32_t bytes = (s0 ? L::kTile / 2 : 0) + (s1 ? L::kTile / 2 : 0);
-          if (fix) {
-            fixes[fi].slot = static_cast<int>(slot);
-            fixes[fi].v0 = f0 ? 64 : (s0 ? batch_part[s] : 0);
-            fixes[fi].v1 = f1 ? 64 : (s1 ? batch_part[s] : 0);
-          }
-          if (bytes)
-            mbar_arrive_expect_tx(done, bytes);
-          else
-            mbar_arrive(done);
-          const int h = pieces[s * 2 + ((told[s] - 1) & 1)].h;
-          uint8_t* dst = sRing + slot * L::kTile;
-          const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-          for (int c = 0; c < D / 64; ++c) {
-            if (s0) tma_load_4d(dst + c * L::kHalf, tm, done, c * 64, h, r0, g0);
-            if (s1) tma_load_4d(dst + c * L::kHalf + 64 * 128, tm, done, c * 64, h, r1, g1);
-          }
-          if (fix) {
-            mbar_arrive(bar_fixset + fi);
-            on_full &= ~(1u << slot);
-            on_raw |= 1u << fi;
-            raw_ph = (raw_ph & ~(1u << fi)) | ((fix_n / 4 & 1u) << fi);
-          } else {
-            on_full |= 1u << slot;
-            full_ph = (full_ph & ~(1u << slot)) | ((ring / NS & 1u) << slot);
-          }
-        }
-        if (fix) ++fix_n;
-      }
-      ++ring;
-      return __shfl_sync(0xffffffffu, static_cast<int>(good), 0) != 0;
-    };
-    // tells slot s's warps of its next piece; its masks are in place but for n = -1
-    auto tell = [&](int s, int n, int share, int h, int tok0, int ntok, int dst) {
-      bool good = true;
-      if (lane == 0) {
-        Piece& d = pieces[s * 2 + (told[s] & 1)];
-        d.n = n;
-        d.share = share;
-        d.h = h;
-        d.tok0 = tok0;
-        d.ntok = ntok;
-        d.key0 = keys[share ? 0 : s].key0;
-        d.keys = keys[share ? 0 : s].end - d.key0;
-        d.dst = dst;
-        mbar_arrive(bar_pieced + s * 2 + (told[s] & 1));
-      }
-      ++told[s];
-      return good;
-    };
-    // the place of slot s's next piece is free
-    auto piece_free = [&](int s) {
-      bool good = true;
-      if (lane == 0 && told[s] >= 2)
-        good = wait_one(bar_unpieced + s * 2 + (told[s] & 1), (told[s] / 2 - 1) & 1, abort_flag, 13);
-      return __shfl_sync(0xffffffffu, static_cast<int>(good), 0) != 0;
-    };
-    // loads slot s's rows
-    auto load_rows = [&](int s, int buf, bool pair, int h, int tok0) {
-      bool good = true;
-      if (lane == 0) {
-        uint32_t& uses = q_uses[s][buf];
-        if (uses > 0) good = wait_one(bar_qfree + s * 2 + buf, (uses - 1) & 1, abort_flag, 14);
-        if (good) {
-          const int tokens = pair ? p.tile_tokens : p.unit_tokens;
-          mbar_arrive_expect_tx(bar_qfull + s * 2 + buf, static_cast<uint32_t>(tokens * G * D * 2));
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + s * L::kTile + c * L::kHalf + buf * (64 * 128), pair ? &tm_q : &tm_qs,
-                        bar_qfull + s * 2 + buf, c * 64, 0, h, tok0);
-          ++uses;
-        }
-      }
-      return __shfl_sync(0xffffffffu, static_cast<int>(good), 0) != 0;
-    };
-
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_qs);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    bool pend_pair = false;
-    int pend_j = 0;
-    if (!kList && plan->pair_total > 0) {
-      const int nt = tiles_of(plan->prefix_end);
-      const int grid = gridDim.x;
-      long long at = run_start(plan->pair_total, grid, blockIdx.x);
-      const long long end = run_start(plan->pair_total, grid, blockIdx.x + 1);
-      const int tokens = p.B * p.Nq;
-      while (ok && at < end) {
-        const int unit = static_cast<int>(at / nt), t = static_cast<int>(at - static_cast<long long>(unit) * nt);
-        const int n = static_cast<int>(min(static_cast<long long>(nt - t), end - at));
-        const int h = unit / p.pairs, pair = unit - h * p.pairs;
-        // the last tile of the piece before goes in front of this one's rows
-        if (pend_pair) ok = load(0, pend_j, true);
-        pend_pair = false;
-        keys[0].key0 = 128 * t;
-        keys[0].end = plan->prefix_end;
-        keys[0].row = 0;
-        const int tok0 = 2 * pair * p.tile_tokens, tok1 = tok0 + p.tile_tokens;
-        const int share = tok1 < tokens ? 1 : 2;
-        for (int s = 0; ok && s < 2; ++s) {
-          const int tok = s ? tok1 : tok0;
-          ok = piece_free(s);
-          if (ok) tell(s, n, share, h, tok, max(0, min(p.tile_tokens, tokens - tok)), static_cast<int>(blockIdx.x) + unit);
-          if (ok && (s == 0 || share == 1)) ok = load_rows(s, 0, true, h, tok);
-        }
-        for (int j = 0; ok && j < n; ++j) {
-          if (j > 0) ok = load(0, j - 1, true);
-          if (ok && (j & 15) == 0) look_up(0, j >> 4);
-          if (ok) ok = load(0, j, false);
-        }
-        pend_pair = true;
-        pend_j = n - 1;
-        at += n;
-      }
-    }
-    // lanes
-    Lane ln[2];
-    int j[2] = {0, 0}, n[2] = {0, 0};
-    bool fin[2] = {false, false}, pend[2] = {false, false};
-    const int lanes = 2 * gridDim.x;
-    const int units = p.B * p.Nq * p.Hkv, unit_tiles = (p.n_sel + 1) >> 1;  // lists
-    const int whole = kList ? units / lanes * lanes : 0;
-    const long long cut_total = static_cast<long long>(units - whole) * unit_tiles;
-    for (int s = 0; s < 2; ++s) {
-      const int l = lane_of(s);
-      if (kList) {
-        ln[s].unit = l;  // while below `whole`
-        ln[s].left = run_start(cut_total, lanes, l + 1) - run_start(cut_total, lanes, l);
-      } else {
-        ln[s].left = run_start(plan->total, lanes, l + 1) - run_start(plan->total, lanes, l);
-        if (ln[s].left > 0) {
-          const int b = plan->lane_b[s];
-          const int nt = b < 0 ? tiles_of(plan->prefix_end) : own_tiles(p, b);
-          const long long at = plan->lane_at[s];
-          const int u = static_cast<int>(at / nt), rt = b < 0 ? 1 : p.own_rt;
-          ln[s].b = b;
-          ln[s].h = u / rt;
-          ln[s].rt = u - ln[s].h * rt;
-          ln[s].t = static_cast<int>(at - static_cast<long long>(u) * nt);
-        }
-      }
-    }
-    if (ok && p.q_buffers == 2 && lane == 0) {
-      // the second buffer of rows lies over the lower half of a pair's rows
-      for (int s = 0; ok && s < 2; ++s)
-        if (q_uses[s][0] > 0) ok = wait_one(bar_qfree + s * 2, (q_uses[s][0] - 1) & 1, abort_flag, 14);
-    }
-    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
-    uint32_t q_next[2] = {0, 0};
-
-    // next piece of slot s: told, its rows on their way; n[s] = 0 where there is none or nothing to compute
-    auto next_piece = [&](int s) {
-      Lane& w = ln[s];
-      const int l = lane_of(s);
-      Keys& k = keys[s];
-      int h, tok0, ntok, dst;
-      if (!piece_free(s)) return false;
-      if (kList) {
-        long long u;
-        int t0 = 0, nt = unit_tiles;
-        dst = -1;
-        if (w.unit < whole) {
-          u = w.unit;
-          w.unit += lanes;
-        } else if (w.left > 0) {
-          const long long first = run_start(cut_total, lanes, l), at = run_start(cut_total, lanes, l + 1) - w.left;
-          const int cu = static_cast<int>(at / unit_tiles);
-          u = whole + cu;
-          t0 = static_cast<int>(at - static_cast<long long>(cu) * unit_tiles);
-          nt = static_cast<int>(min(static_cast<long long>(unit_tiles - t0), w.left));
-          if (nt < unit_tiles) dst = 2 * l + (at > first ? 1 : 0);
-          w.left -= nt;
-        } else {
-          fin[s] = true;
-          return tell(s, -1, 0, 0, 0, 0, 0);
-        }
-        // units by sequence, head, token: neighbours read the same head's keys
-        const int per = p.Hkv * p.Nq;
-        const int b = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<long long>(b) * per);
-        h = r / p.Nq;
-        const int i = r - h * p.Nq;
-        tok0 = b * p.Nq + i;
-        ntok = 1;
-        const int len = clamped_len(p, b);
-        if (lane == 0 && h == 0 && i == 0 && t0 == 0 && len != p.seqlens[b]) record(1, kDevBadSeqlen);
-        k.row = b;
-        k.seen = max(0, len - p.Nq + i + 1);
-        k.list = p.blocks + (static_cast<long long>(tok0) * p.Hkv + h) * p.n_sel + 2 * t0;
-        k.count = min(p.n_sel - 2 * t0, 2 * nt);
-        k.key0 = k.end = 0;
-        // which of them are seen; the last one that is ends the piece
-        Piece& d = pieces[s * 2 + (told[s] & 1)];
-        int last = -1;
-        for (int i32 = (k.count - 1) >> 5; i32 >= 0; --i32) {  // ends with the first 32 looked up
-          look_up(s, i32);
-          if (lane == 0) {
-            d.full[i32] = batch_full[s];
-            d.some[i32] = batch_seen[s] & ~batch_full[s];
-            if (d.some[i32]) d.part = batch_part[s];
-          }
-          if (last < 0 && batch_seen[s]) last = 32 * i32 + 31 - __clz(batch_seen[s]);
-        }
-        n[s] = (last + 2) >> 1;
-      } else {
-        if (w.left == 0) {
-          fin[s] = true;
-          return tell(s, -1, 0, 0, 0, 0, 0);
-        }
-        while (w.b >= 0 && w.t == 0 && w.rt == 0 && w.h == 0 && own_tiles(p, w.b) == 0) ++w.b;
-        int nt, rts, unit;
-        h = w.h;
-        if (w.b < 0) {
-          nt = tiles_of(plan->prefix_end);
-          rts = 1;
-          unit = h;
-          k.key0 = 128 * w.t;
-          k.end = plan->prefix_end;
-          k.row = 0;
-          tok0 = 0;
-          ntok = p.B * p.Nq;
-        } else {
-          nt = own_tiles(p, w.b);
-          rts = p.own_rt;
-          unit = (w.b * p.Hkv + h) * rts + w.rt + (p.pairs ? 0 : p.Hkv);
-          k.key0 = p.shared_len + 128 * w.t;
-          k.end = clamped_len(p, w.b);
-          k.row = w.b;
-          tok0 = w.b * p.Nq + w.rt * p.own_tokens;
-          ntok = min(p.own_tokens, p.Nq - w.rt * p.own_tokens);
-        }
-        dst = l + unit;
-        n[s] = static_cast<int>(min(static_cast<long long>(nt - w.t), w.left));
-        w.left -= n[s];
-        w.t += n[s];
-        if (w.t == nt) {
-          w.t = 0;
-          if (++w.rt == rts) {
-            w.rt = 0;
-            if (++w.h == p.Hkv) {
-              w.h = 0;
-              ++w.b;
-            }
-          }
-        }
-      }
-      j[s] = 0;
-      tell(s, n[s], 0, h, tok0, ntok, dst);
-      if (n[s] == 0) return true;
-      const int buf = p.q_buffers == 2 ? static_cast<int>(q_next[s]++ & 1) : 0;
-      if (!load_rows(s, buf, false, h, tok0)) return false;
-      if (!kList) look_up(s, 0);
-      return true;
-    };
-
-    if (ok && pend_pair) ok = load(0, pend_j, true);
-    while (ok && !(fin[0] && fin[1] && !pend[0] && !pend[1])) {
-      for (int s = 0; ok && s < 2; ++s) {
-        if (pend[s]) ok = load(s, j[s] - 1, true);
-        pend[s] = false;
-        while (ok && !fin[s] && j[s] == n[s]) ok = next_piece(s);
-        if (ok && !fin[s]) {
-          if (j[s] > 0 && (j[s] & 15) == 0) look_up(s, j[s] >> 4);
-          ok = load(s, j[s], false);
-          ++j[s];
-          pend[s] = true;
-        }
-      }
-    }
-    if (ok && lane == 0) {
-      // no more to clear
-      const uint32_t fi = fix_n & 3;
-      if (fix_n < 4 || wait_one(bar_fixdone + fi, (fix_n / 4 - 1) & 1, abort_flag, 12)) {
-        fixes[fi].slot = -1;
-        mbar_arrive(bar_fixset + fi);
-      }
-    }
-    if (lane == 0) {
-      // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
-      volatile int no_abort = 0;
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t uses = q_uses[i >> 1][i & 1];
-        if (uses > 0) mbar_wait(bar_qfull + i, (uses - 1) & 1, &no_abort, kWaitLimitNs);
-        if (on_raw >> i & 1u) mbar_wait(bar_raw + i, raw_ph >> i & 1u, &no_abort, kWaitLimitNs);
-      }
-      for (int i = 0; i < NS; ++i)
-        if (on_full >> i & 1u) mbar_wait(bar_full + i, full_ph >> i & 1u, &no_abort, kWaitLimitNs);
-    }
+    Producer<D, kList> producer(p, &tm_q, &tm_qs, &tm_k, &tm_v, sm, lane);
+    producer.run();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_u32(sRing), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(sRing), L::kHalf, 1024);
-      uint32_t ring = 0;
-      uint32_t seen[2] = {0, 0};          // pieces looked at
-      uint32_t done[2] = {0, 0};          // pieces with products
-      uint32_t tiles[2] = {0, 0};         // P tiles consumed
-      uint32_t q_uses[2][2] = {{0, 0}, {0, 0}};
-      uint32_t q_lane[2] = {0, 0};
-      int n[2] = {0, 0}, j[2] = {0, 0}, share[2] = {0, 0}, buf[2] = {0, 0};
-      bool fin[2] = {false, false};
-      bool pend[2] = {false, false}, pend_first[2] = {false, false}, pend_last[2] = {false, false};
-      int pend_share[2] = {0, 0};
-      uint32_t v_at = 0, k_at = 0;  // ring items that slot 1 shares
-      bool ok = true;
-      while (ok && !(fin[0] && fin[1] && !pend[0] && !pend[1])) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!ok) break;
-          const uint32_t tS = tmem + s * 128, tO = tmem + 256 + s * 128;
-          if (pend[s]) {
-            const bool shared = pend_share[s] != 0;
-            const bool mine = !(s == 1 && pend_share[s] == 2);  // rows at all
-            if (!(shared && s == 1)) v_at = ring++;
-            const uint32_t vs = v_at % NS;
-            if (mine) {
-              if (!wait_one(bar_full + vs, (v_at / NS) & 1, abort_flag, 21) ||
-                  !wait_one(bar_pfull + s, tiles[s] & 1, abort_flag, 22) ||
-                  (pend_first[s] && done[s] > 0 && !wait_one(bar_ofree + s, (done[s] - 1) & 1, abort_flag, 23))) {
-                ok = false;
-                break;
-              }
-              ++tiles[s];
-              tc_fence_after();
-              const uint64_t dv = dV + static_cast<uint64_t>((vs * L::kTile) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ts(tO, tS + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_pv, (!pend_first[s] || kk > 0) ? 1u : 0u);
-              if (pend_last[s]) {
-                mma_commit(bar_odone + s);
-                ++done[s];
-              }
-              if (!(s == 0 && pend_share[s] == 1)) mma_commit(bar_empty + vs);
-            }
-            pend[s] = false;
-          }
-          while (!fin[s] && j[s] == n[s]) {
-            uint64_t* told = bar_pieced + s * 2 + (seen[s] & 1);
-            if (!wait_one(told, (seen[s] / 2) & 1, abort_flag, 24)) {
-              ok = false;
-              break;
-            }
-            const volatile Piece& d = pieces[s * 2 + (seen[s] & 1)];
-            const int dn = d.n;
-            share[s] = d.share;
-            mbar_arrive(bar_unpieced + s * 2 + (seen[s] & 1));
-            ++seen[s];
-            fin[s] = dn < 0;
-            n[s] = max(dn, 0);
-            j[s] = 0;
-            if (n[s] > 0) buf[s] = share[s] == 0 && p.q_buffers == 2 ? static_cast<int>(q_lane[s]++ & 1) : 0;
-          }
-          if (!ok) break;
-          if (fin[s]) continue;
-          const bool shared = share[s] != 0, mine = !(s == 1 && share[s] == 2);
-          if (!(shared && s == 1)) k_at = ring++;
-          const uint32_t ks = k_at % NS;
-          if (mine) {
-            const int qb = s * 2 + buf[s];
-            if (!wait_one(bar_full + ks, (k_at / NS) & 1, abort_flag, 25) ||
-                (j[s] == 0 && !wait_one(bar_qfull + qb, q_uses[s][buf[s]] & 1, abort_flag, 26))) {
-              ok = false;
-              break;
-            }
-            if (j[s] == 0) ++q_uses[s][buf[s]];
-            tc_fence_after();
-            const uint64_t da = dQ + static_cast<uint64_t>((s * L::kTile + buf[s] * (64 * 128)) >> 4);
-            const uint64_t db = dK + static_cast<uint64_t>((ks * L::kTile) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
-              mma_bf16_ss(tS, da + off, db + off, idesc_qk, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(bar_sfull + s);
-            if (j[s] == n[s] - 1) mma_commit(bar_qfree + qb);
-            if (!(s == 0 && share[s] == 1)) mma_commit(bar_empty + ks);
-          }
-          pend[s] = mine;
-          pend_first[s] = j[s] == 0;
-          pend_share[s] = share[s];
-          ++j[s];
-          pend_last[s] = j[s] == n[s];
-        }
-      }
-      if (!ok) {
-        // the MMAs issued so far complete before TMEM is freed
-        volatile int no_abort = 0;
-        mma_commit(bar_drain);
-        mbar_wait(bar_drain, 0, &no_abort, kWaitLimitNs);
-      }
+      Issuer<D> issuer(sm, tmem, p.q_buffers == 2);
+      issuer.run();
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- clearing
@@ -758,11 +930,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P = 0 times NaN is not 0; halves that were not loaded hold older tiles.
     for (uint32_t i = 0;; ++i) {
       const uint32_t fi = i & 3;
-      if (!wait_all(bar_fixset + fi, (i / 4) & 1, abort_flag, 31)) break;
-      const int slot = fixes[fi].slot, v0 = fixes[fi].v0, v1 = fixes[fi].v1;
+      if (!wait_all(sm.fixset + fi, (i / 4) & 1, abort_flag, 31)) break;
+      const int slot = sm.fixes[fi].slot, v0 = sm.fixes[fi].v0, v1 = sm.fixes[fi].v1;
       if (slot < 0) break;
-      if (!wait_all(bar_raw + fi, (i / 4) & 1, abort_flag, 32)) break;
-      uint8_t* base = sRing + slot * L::kTile;
+      if (!wait_all(sm.raw + fi, (i / 4) & 1, abort_flag, 32)) break;
+      uint8_t* base = sm.ring + slot * L::kTile;
       for (int c = 0; c < D / 64; ++c)
         for (int half = 0; half < 2; ++half) {
           const int v = half ? v1 : v0;
@@ -772,8 +944,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();  // these stores before the tensor core's reads
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar_full + slot);
-        mbar_arrive(bar_fixdone + fi);
+        mbar_arrive(sm.full + slot);
+        mbar_arrive(sm.fixdone + fi);
       }
     }
   } else if (warp >= 4) {
@@ -786,8 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tiles = 0, done = 0;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
-      const Piece& d = pieces[s * 2 + (i & 1)];
-      if (!wait_all(bar_pieced + s * 2 + (i & 1), (i / 2) & 1, abort_flag, 41)) break;
+      const Piece& d = sm.pieces[s * 2 + (i & 1)];
+      if (!wait_all(sm.pieced + s * 2 + (i & 1), (i / 2) & 1, abort_flag, 41)) break;
       const int n = d.n, share = d.share, ntok = d.ntok, h = d.h, dst = d.dst;
       const int rows = share == 2 && s == 1 ? 0 : ntok * G;
       const bool live = r < rows;
@@ -811,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // keys seen of the piece's
           const int lim = kList || !live ? 0 : min(d.keys, clamped_len(p, b) - p.Nq + nth + 1 - d.key0);
           for (int j = 0; j < n; ++j) {
-            if (!wait_all(bar_sfull + s, tiles & 1, abort_flag, 42)) {
+            if (!wait_all(sm.sfull + s, tiles & 1, abort_flag, 42)) {
               ok = false;
               break;
             }
@@ -831,11 +1003,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vis.v[1] = min(max(lim - 128 * j - 64, 0), 64);
                 whole = __all_sync(0xffffffffu, !live || vis.v[1] == 64);
               }
-              RowTile t;
-              if (__any_sync(0xffffffffu, M == -INFINITY))
-                t = whole ? rows_first<false>(tS, vis, c, M) : rows_first<true>(tS, vis, c, M);
-              else
-                t = whole ? rows_tile<false>(tS, vis, c, M, live) : rows_tile<true>(tS, vis, c, M, live);
+              const RowTile t = !whole || __any_sync(0xffffffffu, M == -INFINITY) ? rows_first(tS, vis, c, M)
+                                                                                  : rows_tile(tS, c, M, live);
               const bool moved = live && t.M != M;
               const float a = !moved ? 1.f : (M == -INFINITY ? 0.f : ex2_approx(M - t.M));
               l = l * a + t.sum;
@@ -843,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // O holds the sum through the tile before: its P V completed before these scores were formed
                 const float f = moved && M != -INFINITY ? a : 1.f;
                 const float2 a2 = make_float2(f, f);
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                   uint32_t w[32];
                   tmem_ld32(tO + cc * 32, w);
@@ -862,10 +1031,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_pfull + s);
+            if (lane == 0) mbar_arrive(sm.pfull + s);
           }
           if (!ok) break;
-          if (!wait_all(bar_odone + s, done & 1, abort_flag, 43)) break;
+          if (!wait_all(sm.odone + s, done & 1, abort_flag, 43)) break;
           ++done;
           tc_fence_after();
         }
@@ -873,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
         if (quarter * 32 < rows) {
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t w[32];
             if (n > 0) {
@@ -910,11 +1079,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_ofree + s);
+          if (lane == 0) mbar_arrive(sm.ofree + s);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_unpieced + s * 2 + (i & 1));
+      if (lane == 0) mbar_arrive(sm.unpieced + s * 2 + (i & 1));
       if (n < 0) break;
     }
   }
