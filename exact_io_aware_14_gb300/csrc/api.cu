@@ -62,8 +62,21 @@ bool make_map_e4m3(CUtensorMap* m, const void* base, int num_pages, int page_siz
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 5-D view {64, 8, d / 64, groups, Hkv} of a bf16 page pool: keys in groups of 8,
+// a head's row in blocks of 64 columns; box {64, 8, d / 64, 8, 1}, a block of 64
+// keys.  One box an operand block: with boxes of 64 columns the loading thread
+// issued twice as many.
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d) {
-  return make_map(m, base, num_pages * (page_size / 64), 64, Hkv, d, 64);
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)Hkv * d * 2;
+  const cuuint64_t dims[5] = {64u, 8u, (cuuint64_t)(d / 64), (cuuint64_t)num_pages * (page_size / 8), (cuuint64_t)Hkv};
+  const cuuint64_t strides[4] = {row, 128u, 8 * row, (cuuint64_t)d * 2};
+  const cuuint32_t box[5] = {64u, 8u, (cuuint32_t)(d / 64), 8u, 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // 4-D view {d, G, Hkv, tokens} of q [tokens, Hkv * G, d]; box {64, G, 1, tokens}.

@@ -83,7 +83,7 @@ attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pa
   if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;  // a token's heads of a group fit one tile of rows
   if (static_cast<long long>(B) * Nq * Hq > kIntMax - 4096) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(num_pages) * (page_size / 64) > kIntMax) return ATTN_ERR_UNSUPPORTED;  // blocks of the pool
+  if (static_cast<long long>(num_pages) * (page_size / 8) > kIntMax) return ATTN_ERR_UNSUPPORTED;  // coordinates of the pool
   if (!q || !k_pages || !v_pages || !o || !lse) return ATTN_ERR_INVALID_ARG;
   if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(o, 16) || off(lse, 4)) return ATTN_ERR_MISALIGNED;
   const long long rows = static_cast<long long>(B) * Nq * Hq;
@@ -129,7 +129,7 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
   p.own_rt = z.own_rt;
   p.unit_tokens = z.unit_tokens;
   p.unit_rows = z.unit_rows;
-  p.q_buffers = z.unit_rows <= 64 ? 2 : 1;
+  p.lane_rows = z.unit_rows <= 32 ? 32 : (z.unit_rows <= 64 ? 64 : 128);
   p.pair_rows = z.pair_rows;
   char* ws = static_cast<char*>(workspace);
   if (!blocks) {

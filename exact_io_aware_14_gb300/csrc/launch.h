@@ -250,13 +250,13 @@ struct RowsParams {
   int B, Nq, Hq, Hkv, d;
   float scale_log2;
   int tile_tokens, pairs, own_tokens, own_rt, unit_tokens, unit_rows;
-  int q_buffers;      // buffers of rows of a slot (lane work)
+  int lane_rows;      // rows of a tile that lane work uses: 32, 64 or 128
   long long pair_rows;
 };
 // q as {d, heads of a group, Hkv, tokens}: tiles of tile_tokens and of unit_tokens tokens; the page pools in 64 rows.
 cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, cudaStream_t stream);
-// Maps of bf16 tensors: a page pool as blocks of 64 rows {d, Hkv, 64, blocks}, boxes of one block of a head; q's of
+// Maps of bf16 tensors: a page pool as {64, 8, d / 64, groups of 8 keys, Hkv}, boxes of a head's 64 keys; q's of
 // `tokens` tokens of a group of heads.
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d);
 bool make_map_group(CUtensorMap* m, const void* base, long long total_tokens, int Hkv, int G, int d, int tokens);

@@ -77,6 +77,9 @@ struct Layout {
   static constexpr int kSlots = D == 64 ? 10 : 5;
   static constexpr int kHalf = 128 * 128;  // one 64-column block of a 128-row tile
   static constexpr int kTile = 128 * D * 2;
+  // K and V tiles: groups of 8 keys, each with its D / 64 blocks of 8 rows of
+  // 128 B, so that one box holds a 64-key block and both halves follow on
+  static constexpr int kGroup = D / 64 * 1024;
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffPiece = kOffRing + kSlots * kTile;
   static constexpr int kOffBar = kOffPiece + 4 * static_cast<int>(sizeof(Piece));
@@ -253,6 +256,15 @@ struct Smem {
   }
 };
 
+// Lane work on few rows (lane_rows: 32 or 64 of a tile's 128).  The rows lie in
+// two buffers of the slot's Q tile; the product takes them as rows of another
+// part of the tile, whose warps of the softmax share no scheduler with the other
+// slot's, nor (32 rows) with the producer and the issuer.
+__device__ __forceinline__ int buffer_row(int lane_rows, int buf) { return lane_rows == 32 ? 64 + 32 * buf : 64 * buf; }
+__device__ __forceinline__ int first_row(int lane_rows, int slot) {
+  return lane_rows == 32 ? 64 + 32 * slot : (lane_rows == 64 ? 64 * slot : 0);
+}
+
 // A place in the ring: slot and phase of the turn through it.
 template <int NS>
 struct RingAt {
@@ -271,7 +283,7 @@ struct RingAt {
 // the same registers and the same code (exchanged after each step), so that no
 // state lies in local memory and the code is there once.
 struct Tile {
-  int g0, g1;      // blocks of the pool
+  int g0, g1;      // first groups of 8 keys in the pool
   uint32_t flags;  // bits 0, 1: seen; 2, 3: seen whole
   int part;
 };
@@ -285,7 +297,7 @@ struct ProducerSlot {
   int key0, end, row;    // ranges: first key, end of the keys; table row
   const int* list;       // lists: entries of the piece, `count` of them
   int count, seen;       // seen: keys before the token's own end
-  int blk;               // this lane's block of the 32 looked up
+  int blk;               // first group of 8 keys of this lane's block of the 32 looked up
   uint32_t seen_bits, full_bits;
   int part;
   Tile last;             // the tile whose V comes next
@@ -310,8 +322,6 @@ struct Producer {
   RingAt<L::kSlots> at;
   uint32_t fix_n = 0;
   bool ok = true;  // lane 0's view until `agree`
-  // the last loads: whether on a ring slot's `full` (its phase), on a `raw` (its phase)
-  uint32_t on_full = 0, full_ph = 0, on_raw = 0, raw_ph = 0;
 
   __device__ __forceinline__ Producer(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* qs, const CUtensorMap* k,
                                       const CUtensorMap* v, const Smem<D>& sm_, int lane_)
@@ -353,7 +363,7 @@ struct Producer {
       blk = key >> 6;
     }
     s.blk = 0;
-    if (v > 0) s.blk = pool_block(s.row, blk);
+    if (v > 0) s.blk = 8 * pool_block(s.row, blk);
     s.seen_bits = __ballot_sync(0xffffffffu, v > 0);
     s.full_bits = __ballot_sync(0xffffffffu, v == 64);
     const uint32_t some = s.seen_bits & ~s.full_bits;
@@ -370,40 +380,36 @@ struct Producer {
   }
   // a K or V tile into the next ring slot
   __device__ __forceinline__ void load(const Tile& t, int h, bool is_v) {
-    if (lane == 0) {
-      if (at.turn > 0) wait(sm.empty + at.slot, at.turn - 1, 11);
-      const bool fix = is_v && (t.flags >> 2) != 3u;
+    if (lane != 0) return;
+    if (at.turn > 0) wait(sm.empty + at.slot, at.turn - 1, 11);
+    if (!ok) return;
+    uint8_t* dst = sm.ring + at.slot * L::kTile;
+    const CUtensorMap* tm = is_v ? tm_v : tm_k;
+    if (t.flags == 15u) {
+      uint64_t* done = sm.full + at.slot;
+      mbar_arrive_expect_tx(done, L::kTile);
+      tma_load_5d(dst, tm, done, 0, 0, 0, t.g0, h);
+      tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, t.g1, h);
+    } else {
+      const bool s0 = t.flags & 1u, s1 = t.flags & 2u;
       const uint32_t fi = fix_n & 3;
-      if (fix && fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
-      if (ok) {
-        const bool s0 = t.flags & 1u, s1 = t.flags & 2u;
-        uint64_t* done = fix ? sm.raw + fi : sm.full + at.slot;
-        if (fix) {
-          sm.fixes[fi].slot = static_cast<int>(at.slot);
-          sm.fixes[fi].v0 = t.flags & 4u ? 64 : (s0 ? t.part : 0);
-          sm.fixes[fi].v1 = t.flags & 8u ? 64 : (s1 ? t.part : 0);
-        }
-        if (s0 || s1)
-          mbar_arrive_expect_tx(done, s0 && s1 ? L::kTile : L::kTile / 2);
-        else
-          mbar_arrive(done);
-        uint8_t* dst = sm.ring + at.slot * L::kTile;
-        const CUtensorMap* tm = is_v ? tm_v : tm_k;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          if (s0) tma_load_4d(dst + c * L::kHalf, tm, done, c * 64, h, 0, t.g0);
-          if (s1) tma_load_4d(dst + c * L::kHalf + 64 * 128, tm, done, c * 64, h, 0, t.g1);
-        }
-        if (fix) {
-          mbar_arrive(sm.fixset + fi);
-          on_full &= ~(1u << at.slot);
-          on_raw |= 1u << fi;
-          raw_ph = (raw_ph & ~(1u << fi)) | ((fix_n / 4 & 1u) << fi);
-          ++fix_n;
-        } else {
-          on_full |= 1u << at.slot;
-          full_ph = (full_ph & ~(1u << at.slot)) | ((at.turn & 1u) << at.slot);
-        }
+      uint64_t* done = is_v ? sm.raw + fi : sm.full + at.slot;
+      if (is_v) {
+        if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+        if (!ok) return;
+        sm.fixes[fi].slot = static_cast<int>(at.slot);
+        sm.fixes[fi].v0 = t.flags & 4u ? 64 : (s0 ? t.part : 0);
+        sm.fixes[fi].v1 = t.flags & 8u ? 64 : (s1 ? t.part : 0);
+      }
+      if (s0 || s1)
+        mbar_arrive_expect_tx(done, s0 && s1 ? L::kTile : L::kTile / 2);
+      else
+        mbar_arrive(done);
+      if (s0) tma_load_5d(dst, tm, done, 0, 0, 0, t.g0, h);
+      if (s1) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, t.g1, h);
+      if (is_v) {
+        mbar_arrive(sm.fixset + fi);
+        ++fix_n;
       }
     }
     at.next();
@@ -436,10 +442,11 @@ struct Producer {
       if (uses > 0) wait(sm.qfree + buf, uses - 1, 14);
       if (ok) {
         const int tokens = pair ? p.tile_tokens : p.unit_tokens;
+        const int row = pair ? 0 : buffer_row(p.lane_rows, second ? 1 : 0);
         mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(tokens * (p.Hq / p.Hkv) * D * 2));
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sm.q + s.slot * L::kTile + c * L::kHalf + (second ? 64 * 128 : 0), pair ? tm_q : tm_qs, sm.qfull + buf, c * 64, 0,
+          tma_load_4d(sm.q + s.slot * L::kTile + c * L::kHalf + row * 128, pair ? tm_q : tm_qs, sm.qfull + buf, c * 64, 0,
                       h, tok0);
         if (second)
           ++s.rows_n[1];
@@ -583,7 +590,7 @@ struct Producer {
     }
     tell(s, d, s.n, 0, s.head, tok0, ntok, s.key0, s.end - s.key0, dst);
     if (s.n == 0) return;
-    load_rows(s, p.q_buffers == 2 && (s.rows_n[0] + s.rows_n[1] & 1u), false, s.head, tok0);
+    load_rows(s, p.lane_rows < 128 && (s.rows_n[0] + s.rows_n[1] & 1u), false, s.head, tok0);
     if (!kList) look_up(s, 0);
   }
 
@@ -659,10 +666,11 @@ struct Producer {
     if (a.rows_n[1]) drain(sm.qfull + 1, a.rows_n[1] - 1);
     if (b.rows_n[0]) drain(sm.qfull + 2, b.rows_n[0] - 1);
     if (b.rows_n[1]) drain(sm.qfull + 3, b.rows_n[1] - 1);
-    for (int i = 0; i < 4; ++i)
-      if (on_raw >> i & 1u) drain(sm.raw + i, raw_ph >> i);
-    for (int i = 0; i < L::kSlots; ++i)
-      if (on_full >> i & 1u) drain(sm.full + i, full_ph >> i);
+    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) drain(sm.raw + i, (fix_n - 1 - i) / 4);
+    for (uint32_t i = 0; i < L::kSlots; ++i) {
+      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
+      if (turns > 0) drain(sm.full + i, turns - 1);
+    }
   }
 };
 
@@ -673,7 +681,7 @@ struct MmaSlot {
   uint32_t seen, done, tiles;  // pieces looked at, with products; P tiles consumed
   uint32_t rows_n[2];
   uint32_t buf;
-  uint32_t slot;
+  uint64_t da;  // descriptor of its rows
   bool fin, pend;
 };
 
@@ -683,40 +691,43 @@ struct Issuer {
   static constexpr uint32_t kIdescQk = idesc_bf16_f32(128, 128, 0), kIdescPv = idesc_bf16_f32(128, D, 1);
   const Smem<D>& sm;
   const uint32_t tmem;
-  const bool two_buffers;
+  const int lane_rows;
   uint64_t dQ, dK, dV;
   RingAt<L::kSlots> at;
   bool ok = true;
 
-  __device__ __forceinline__ Issuer(const Smem<D>& sm_, uint32_t tmem_, bool two) : sm(sm_), tmem(tmem_), two_buffers(two) {
+  __device__ __forceinline__ Issuer(const Smem<D>& sm_, uint32_t tmem_, int rows) : sm(sm_), tmem(tmem_), lane_rows(rows) {
     dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);
-    dK = sdesc_sw128(smem_u32(sm.ring), 16, 1024);
-    dV = sdesc_sw128(smem_u32(sm.ring), L::kHalf, 1024);
+    dK = sdesc_sw128(smem_u32(sm.ring), 16, L::kGroup);
+    dV = sdesc_sw128(smem_u32(sm.ring), 1024, L::kGroup);
   }
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
     if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
   }
   // O_S (+)= P_S V, S_S = Q_S K^T with the tile in ring slot `slot`
-  __device__ __forceinline__ void pv(uint32_t S, uint32_t slot, bool first) {
+  template <int S>
+  __device__ __forceinline__ void pv(uint32_t slot, bool first) {
     const uint64_t dv = dV + static_cast<uint64_t>((slot * L::kTile) >> 4);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-      mma_bf16_ts(tmem + 256 + S * 128, tmem + S * 128 + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdescPv,
+      mma_bf16_ts(tmem + 256 + S * 128, tmem + S * 128 + kk * 8, dv + ((kk * 2 * L::kGroup) >> 4), kIdescPv,
                   (!first || kk > 0) ? 1u : 0u);
   }
-  __device__ __forceinline__ void qk(uint32_t S, uint32_t slot, uint32_t buf) {
-    const uint64_t da = dQ + static_cast<uint64_t>((S * L::kTile + buf * (64 * 128)) >> 4);
+  template <int S>
+  __device__ __forceinline__ void qk(uint32_t slot, uint64_t da) {
     const uint64_t db = dK + static_cast<uint64_t>((slot * L::kTile) >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
-      mma_bf16_ss(tmem + S * 128, da + off, db + off, kIdescQk, kk > 0 ? 1u : 0u);
+      const uint32_t in = (kk & 3) * 32;
+      mma_bf16_ss(tmem + S * 128, da + (((kk >> 2) * L::kHalf + in) >> 4), db + (((kk >> 2) * 1024 + in) >> 4), kIdescQk,
+                  kk > 0 ? 1u : 0u);
     }
     mma_commit(sm.sfull + S);
   }
   // Next piece of a slot; false where there is none to come.
+  template <int S>
   __device__ __forceinline__ void take(MmaSlot& s, int* share) {
-    const uint32_t i = s.slot * 2 + (s.seen & 1);
+    const uint32_t i = S * 2 + (s.seen & 1);
     wait(sm.pieced + i, s.seen / 2, 24);
     if (!ok) return;
     const volatile Piece& d = sm.pieces[i];
@@ -748,7 +759,7 @@ struct Issuer {
         if (j == 1 && a.done > 0) wait(sm.ofree + 0, a.done - 1, 23);
         if (!ok) break;
         tc_fence_after();
-        pv(0, vs, j == 1);
+        pv<0>(vs, j == 1);
       }
       const uint32_t ks = at.slot, kturn = at.turn;
       if (j < n) {
@@ -756,7 +767,7 @@ struct Issuer {
         wait(sm.full + ks, kturn, 25);
         if (!ok) break;
         tc_fence_after();
-        qk(0, ks, 0);
+        qk<0>(ks, dQ);
         if (j == n - 1) mma_commit(sm.qfree + 0);
       } else {
         mma_commit(sm.odone + 0);
@@ -767,10 +778,10 @@ struct Issuer {
           if (j == 1 && b.done > 0) wait(sm.ofree + 1, b.done - 1, 23);
           if (!ok) break;
           tc_fence_after();
-          pv(1, vs, j == 1);
+          pv<1>(vs, j == 1);
         }
         if (j < n) {
-          qk(1, ks, 0);
+          qk<1>(ks, dQ + (L::kTile >> 4));
           if (j == n - 1) mma_commit(sm.qfree + 2);
         } else {
           mma_commit(sm.odone + 1);
@@ -785,33 +796,37 @@ struct Issuer {
     if (both) ++b.done;
   }
 
+  template <int S>
   __device__ __forceinline__ void lane_step(MmaSlot& s) {
     if (s.pend) {
       const uint32_t vs = at.slot;
       wait(sm.full + vs, at.turn, 21);
       at.next();
-      wait(sm.pfull + s.slot, s.tiles++, 22);
+      wait(sm.pfull + S, s.tiles++, 22);
       const bool first = s.j == 1;
-      if (first && s.done > 0) wait(sm.ofree + s.slot, s.done - 1, 23);
+      if (first && s.done > 0) wait(sm.ofree + S, s.done - 1, 23);
       if (!ok) return;
       tc_fence_after();
-      pv(s.slot, vs, first);
+      pv<S>(vs, first);
       mma_commit(sm.empty + vs);
       if (s.j == s.n) {
-        mma_commit(sm.odone + s.slot);
+        mma_commit(sm.odone + S);
         ++s.done;
       }
       s.pend = false;
     }
     int share;
-    while (ok && !s.fin && s.j == s.n) take(s, &share);
+    while (ok && !s.fin && s.j == s.n) take<S>(s, &share);
     if (!ok || s.fin) return;
     const uint32_t ks = at.slot;
     wait(sm.full + ks, at.turn, 25);
     at.next();
     if (s.j == 0) {
-      s.buf = two_buffers ? (s.rows_n[0] + s.rows_n[1]) & 1u : 0u;
-      wait(sm.qfull + s.slot * 2 + s.buf, s.buf ? s.rows_n[1] : s.rows_n[0], 26);
+      s.buf = lane_rows < 128 ? (s.rows_n[0] + s.rows_n[1]) & 1u : 0u;
+      // from where the tile's row 0 would lie
+      s.da = dQ + static_cast<uint64_t>(
+                      static_cast<int64_t>(S * L::kTile + (buffer_row(lane_rows, static_cast<int>(s.buf)) - first_row(lane_rows, S)) * 128) >> 4);
+      wait(sm.qfull + S * 2 + s.buf, s.buf ? s.rows_n[1] : s.rows_n[0], 26);
       if (s.buf)
         ++s.rows_n[1];
       else
@@ -819,9 +834,9 @@ struct Issuer {
     }
     if (!ok) return;
     tc_fence_after();
-    qk(s.slot, ks, s.buf);
+    qk<S>(ks, s.da);
     ++s.j;
-    if (s.j == s.n) mma_commit(sm.qfree + s.slot * 2 + s.buf);
+    if (s.j == s.n) mma_commit(sm.qfree + S * 2 + s.buf);
     mma_commit(sm.empty + ks);
     s.pend = true;
   }
@@ -832,22 +847,20 @@ struct Issuer {
     a.seen = a.done = a.tiles = a.rows_n[0] = a.rows_n[1] = a.buf = 0;
     b.seen = b.done = b.tiles = b.rows_n[0] = b.rows_n[1] = b.buf = 0;
     a.fin = b.fin = a.pend = b.pend = false;
-    a.slot = 0;
-    b.slot = 1;
     // pair pieces come first, both slots told of each
     int share = 0;
     for (;;) {
-      while (ok && !a.fin && a.n == 0) take(a, &share);
+      while (ok && !a.fin && a.n == 0) take<0>(a, &share);
       if (!ok || a.fin || share == 0) break;
       int other;
-      take(b, &other);
+      take<1>(b, &other);
       if (ok) pair_piece(a, b, share == 1);
       a.n = b.n = a.j = b.j = 0;
     }
 #pragma unroll 1
     while (ok && !(a.fin && b.fin && !a.pend && !b.pend)) {
-      lane_step(a);
-      exchange(a, b);
+      lane_step<0>(a);
+      lane_step<1>(b);
     }
     if (!ok) {
       // the MMAs issued so far complete before TMEM is freed
@@ -921,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     producer.run();
   } else if (warp == 1) {
     if (lane == 0) {
-      Issuer<D> issuer(sm, tmem, p.q_buffers == 2);
+      Issuer<D> issuer(sm, tmem, p.lane_rows);
       issuer.run();
     }
   } else if (warp == 2) {
@@ -935,12 +948,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (slot < 0) break;
       if (!wait_all(sm.raw + fi, (i / 4) & 1, abort_flag, 32)) break;
       uint8_t* base = sm.ring + slot * L::kTile;
-      for (int c = 0; c < D / 64; ++c)
-        for (int half = 0; half < 2; ++half) {
-          const int v = half ? v1 : v0;
-          for (int off = v * 128 + lane * 16; off < 64 * 128; off += 512)
-            *reinterpret_cast<uint4*>(base + c * L::kHalf + half * (64 * 128) + off) = make_uint4(0u, 0u, 0u, 0u);
+      for (int half = 0; half < 2; ++half) {
+        const int v = half ? v1 : v0;
+        for (int i = lane; i < (64 - v) * (D / 8); i += 32) {
+          const int r = v + i / (D / 8), ch = i % (D / 8);
+          *reinterpret_cast<uint4*>(base + half * (L::kTile / 2) + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
+                                    (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
+      }
       fence_proxy_async_smem();  // these stores before the tensor core's reads
       __syncwarp();
       if (lane == 0) {
@@ -951,10 +966,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax and results
     const int s = (warp - 4) >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + s * 128 + lane_off, tO = tmem + 256 + s * 128 + lane_off;
-    const int rtok = r / G, rg = r - rtok * G;
+    // this thread's row: of the tile (pair work), of the lane's rows
+    const int pair_r = quarter * 32 + lane, lane_r = pair_r - first_row(p.lane_rows, s);
+    const int pair_tok = pair_r / G, lane_tok = lane_r < 0 ? -1 : lane_r / G;
     uint32_t tiles = 0, done = 0;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
@@ -962,7 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_all(sm.pieced + s * 2 + (i & 1), (i / 2) & 1, abort_flag, 41)) break;
       const int n = d.n, share = d.share, ntok = d.ntok, h = d.h, dst = d.dst;
       const int rows = share == 2 && s == 1 ? 0 : ntok * G;
-      const bool live = r < rows;
+      const int r = share ? pair_r : lane_r, rtok = share ? pair_tok : lane_tok, rg = r - rtok * G;
+      const bool live = r >= 0 && r < rows;
+      const bool on = __any_sync(0xffffffffu, live);  // rows of this warp
       const int tok = d.tok0 + rtok;
       const int b = live ? tok / p.Nq : 0, nth = tok - b * p.Nq;
       if (n >= 0 && rows > 0) {
@@ -989,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++tiles;
             tc_fence_after();
-            if (quarter * 32 < rows) {
+            if (on) {
               Visible vis;
               bool whole;
               if (kList) {
@@ -1041,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // l is 0 where nothing was seen; NaN stays NaN
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
-        if (quarter * 32 < rows) {
+        if (on) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t w[32];
