@@ -352,7 +352,9 @@ attn_status attn_get_device_status(void* stream) {
       attn::status_word_decode_fp8(&words.at[3]) != cudaSuccess ||
       attn::status_word_append(&words.at[4]) != cudaSuccess || attn::status_word_rope(&words.at[5]) != cudaSuccess ||
       attn::status_word_paging(&words.at[6]) != cudaSuccess ||
-      attn::status_word_select(&words.at[7]) != cudaSuccess || attn::status_word_rows(&words.at[8]) != cudaSuccess ||
+      attn::status_word_select(&words.at[7]) != cudaSuccess ||
+      attn::status_word_wide_rows(&words.at[8]) != cudaSuccess ||
+      attn::status_word_few_rows(&words.at[9]) != cudaSuccess ||
       attn::fetch_status(words, s, &w) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
   switch (w & 0xffu) {

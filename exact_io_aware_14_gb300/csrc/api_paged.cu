@@ -129,7 +129,6 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
   p.own_rt = z.own_rt;
   p.unit_tokens = z.unit_tokens;
   p.unit_rows = z.unit_rows;
-  p.lane_rows = z.unit_rows <= 32 ? 32 : (z.unit_rows <= 64 ? 64 : 128);
   p.pair_rows = z.pair_rows;
   char* ws = static_cast<char*>(workspace);
   if (!blocks) {

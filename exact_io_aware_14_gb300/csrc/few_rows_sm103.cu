@@ -1,0 +1,905 @@
+// Attention of up to 32 query rows that read the same keys, over a paged bf16
+// cache, for sm_103a: the new tokens of one sequence with a group's heads, those
+// of a small batch on its shared prefix, or one token's heads on listed blocks.
+//
+// With few rows the keys take the MMA's M and the rows its N:
+//     S^T [128 keys x N]  = K Q^T            (A: the K tile, B: Q, K-major)
+//     O^T [d x N]        += V^T P^T          (A: the V tile, M-major, B: P^T)
+// Both products of a tile take as long as the tensor core needs to read the
+// tile from shared memory, whatever the rows (128 rows in M, mostly empty, took
+// 1100 cycles and a softmax of 1400 in one warp: 65 us for 16 tokens on 64 listed
+// blocks of 64 keys, 8 KV heads, where this form takes 54).
+//
+// The softmax has a thread for each key: its N scores from Tensor Memory, p to
+// shared memory as the next product's operand, a part of each row's sum of p in
+// its registers until the piece ends.  A row's exponent reference M is the
+// largest score of its first tile; p = 2^(x - M) keeps its relative precision in
+// bf16 and fp32 up to 2^127, so M moves (and O^T is rescaled in Tensor Memory)
+// only where x - M passes 96, on which the four warps vote once a tile.
+//
+// The work is that of the lanes of rows_sm103.cu: an equal run of (unit, key
+// tile) for each CTA, pieces joined by the joining kernels there.  S of the next
+// tile goes out before O of this one, also from piece to piece (scores, P, rows,
+// O^T are held twice).
+//
+// Warps: 0 producer, 1 MMA issuer, 2 clears value rows, 4-7 softmax and results.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "rows_plan.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;  // pieces told ahead
+
+struct Piece {
+  int n;           // key tiles; -1: no more work
+  int h;           // KV head
+  int tok0, ntok;  // first token, tokens
+  int key0, keys;  // ranges: position of the first key, keys from there on
+  int dst;         // piece number, -1: the result itself
+  int part;        // keys seen of the blocks marked in some[] (lists)
+  uint32_t full[kMaskWords], some[kMaskWords];  // lists: blocks seen whole, seen in part
+};
+
+template <int D, int R>
+struct Layout {
+  static constexpr int kN = R < 16 ? 16 : R;
+  static constexpr int kTile = 128 * D * 2;
+  // tiles: groups of 8 keys, each with its D / 64 blocks of 8 rows of 128 B
+  static constexpr int kGroup = D / 64 * 1024;
+  static constexpr int kSlots = (R == 32 ? 5 : 6) * (128 / D);
+  static constexpr int kQ = kN * D * 2;  // [D / 64][N][128 B]
+  static constexpr int kP = kN * 256;    // [2][N][128 B]
+  static constexpr int kOffQ = kSlots * kTile;  // behind the ring: with d = 64 the product's M reads on 1 KB past a tile
+  static constexpr int kOffP = kOffQ + 2 * kQ;
+  static constexpr int kOffPiece = kOffP + 2 * kP;
+  static constexpr int kOffBar = kOffPiece + kPieces * static_cast<int>(sizeof(Piece));
+  static constexpr int kNumBars = 2 * kSlots + 7 * 2 + 2 * kPieces + 3 * 4 + 1;
+  static constexpr int kOffFix = kOffBar + 8 * kNumBars;
+  static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
+  static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
+  static constexpr int kOffRed = kOffScan + 8 * 8 + 8 * 4;  // [4][R] floats
+  static constexpr int kOffLim = kOffRed + 4 * R * 4;       // [R] ints
+  static constexpr int kOffMisc = kOffLim + R * 4;
+  static constexpr int kBytes = kOffMisc + 32;
+  static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
+  static constexpr uint32_t kTmem = 4 * kN;     // S^T twice, O^T twice
+};
+static_assert(Layout<128, 4>::kAlloc <= 232448 && Layout<128, 16>::kAlloc <= 232448 && Layout<128, 32>::kAlloc <= 232448 &&
+                  Layout<64, 32>::kAlloc <= 232448 && Layout<64, 16>::kAlloc <= 232448,
+              "shared memory of a CTA");
+
+template <int D, int R>
+struct Smem {
+  uint8_t *ring, *q, *ps;
+  Piece* pieces;
+  uint64_t* full;      // [kSlots] ring slot holds its tile
+  uint64_t* empty;     // [kSlots] ring slot read
+  uint64_t* sfull;     // [2] scores complete
+  uint64_t* pfull;     // [2] P written (4 warps)
+  uint64_t* pvdone;    // [2] a tile's P V complete
+  uint64_t* odone;     // [2] a piece's last P V complete
+  uint64_t* ofree;     // [2] a piece's O read (4 warps)
+  uint64_t* qfull;     // [2] rows loaded
+  uint64_t* qfree;     // [2] a piece's last Q K^T complete
+  uint64_t* pieced;    // [kPieces] piece told
+  uint64_t* unpieced;  // [kPieces] piece done with (MMA thread, 4 warps)
+  uint64_t* fixset;    // [4] clearing asked for
+  uint64_t* fixdone;   // [4] done
+  uint64_t* raw;       // [4] value tile to be cleared landed
+  uint64_t* drain;     // after an abort: the MMAs issued so far completed
+  Fix* fixes;
+  Plan* plan;
+  float* red;
+  int* lim;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  volatile int* gone;  // [2] a softmax warp gave up (by the tile's parity)
+  __device__ __forceinline__ explicit Smem(uint8_t* base) {
+    using L = Layout<D, R>;
+    ring = base;
+    q = base + L::kOffQ;
+    ps = base + L::kOffP;
+    pieces = reinterpret_cast<Piece*>(base + L::kOffPiece);
+    full = reinterpret_cast<uint64_t*>(base + L::kOffBar);
+    empty = full + L::kSlots;
+    sfull = empty + L::kSlots;
+    pfull = sfull + 2;
+    pvdone = pfull + 2;
+    odone = pvdone + 2;
+    ofree = odone + 2;
+    qfull = ofree + 2;
+    qfree = qfull + 2;
+    pieced = qfree + 2;
+    unpieced = pieced + kPieces;
+    fixset = unpieced + kPieces;
+    fixdone = fixset + 4;
+    raw = fixdone + 4;
+    drain = raw + 4;
+    fixes = reinterpret_cast<Fix*>(base + L::kOffFix);
+    plan = reinterpret_cast<Plan*>(base + L::kOffPlan);
+    red = reinterpret_cast<float*>(base + L::kOffRed);
+    lim = reinterpret_cast<int*>(base + L::kOffLim);
+    tmem_slot = reinterpret_cast<uint32_t*>(base + L::kOffMisc);
+    abort_flag = reinterpret_cast<volatile int*>(base + L::kOffMisc + 4);
+    gone = reinterpret_cast<volatile int*>(base + L::kOffMisc + 8);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Producer: one warp, whose lanes look up 32 blocks of a piece at a time; lane 0
+// waits and issues.  Ring order of a piece of n tiles: K_0, then K_j, V_{j-1},
+// then V_{n-1}.
+template <int D, int R, bool kList>
+struct Producer {
+  using L = Layout<D, R>;
+  const RowsParams& p;
+  const CUtensorMap *tm_q, *tm_k, *tm_v;
+  const Smem<D, R>& sm;
+  const int lane;
+  RingAt<L::kSlots> at;
+  uint32_t fix_n = 0, told = 0, rows_n = 0;
+  bool ok = true;  // lane 0's view until `agree`
+  // the CTA's run
+  long long left, unit;      // tiles left (lists: of the cut units); lists: next whole unit
+  int b, hh, rt, t;          // ranges: where it stands
+  // the piece
+  int n, head, key0, end, row;
+  const int* list;
+  int count, seen;
+  int blk, part;
+  uint32_t seen_bits, full_bits;
+  bool fin = false;
+
+  __device__ __forceinline__ Producer(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* k, const CUtensorMap* v,
+                                      const Smem<D, R>& sm_, int lane_)
+      : p(p_), tm_q(q), tm_k(k), tm_v(v), sm(sm_), lane(lane_) {}
+
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  __device__ __forceinline__ bool agree() {
+    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+    return ok;
+  }
+  // blocks 32 i .. 32 i + 31 of the piece
+  __device__ __forceinline__ void look_up(int i) {
+    int v = 0, bl;
+    if (kList) {
+      const int e = 32 * i + lane;
+      bl = e < count ? list[e] : -1;
+      if (bl >= 0) {
+        if (bl >= p.max_blocks * (p.page_size / 64))
+          record(3, kDevBadPage);
+        else
+          v = min(64, seen - bl * 64);
+      }
+    } else {
+      const int key = key0 + 64 * (32 * i + lane);
+      v = min(64, end - key);
+      bl = key >> 6;
+    }
+    blk = 0;
+    if (v > 0) blk = pool_group(p, row, bl);
+    seen_bits = __ballot_sync(0xffffffffu, v > 0);
+    full_bits = __ballot_sync(0xffffffffu, v == 64);
+    const uint32_t some = seen_bits & ~full_bits;
+    part = some ? __shfl_sync(0xffffffffu, v, __ffs(some) - 1) : 0;  // the same for all of them
+  }
+  __device__ __forceinline__ Tile tile(int j) {
+    const int e = 2 * (j & 15);
+    Tile x;
+    x.g0 = __shfl_sync(0xffffffffu, blk, e);
+    x.g1 = __shfl_sync(0xffffffffu, blk, e + 1);
+    x.flags = (seen_bits >> e & 3u) | (full_bits >> e & 3u) << 2;
+    x.part = part;
+    return x;
+  }
+  // a K or V tile into the next ring slot
+  __device__ __forceinline__ void load(const Tile& x, bool is_v) {
+    if (lane != 0) return;
+    if (at.turn > 0) wait(sm.empty + at.slot, at.turn - 1, 11);
+    if (!ok) return;
+    uint8_t* dst = sm.ring + at.slot * L::kTile;
+    const CUtensorMap* tm = is_v ? tm_v : tm_k;
+    if (x.flags == 15u) {
+      uint64_t* done = sm.full + at.slot;
+      mbar_arrive_expect_tx(done, L::kTile);
+      tma_load_5d(dst, tm, done, 0, 0, 0, x.g0, head);
+      tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, x.g1, head);
+    } else {
+      const bool s0 = x.flags & 1u, s1 = x.flags & 2u;
+      const uint32_t fi = fix_n & 3;
+      uint64_t* done = is_v ? sm.raw + fi : sm.full + at.slot;
+      if (is_v) {
+        if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+        if (!ok) return;
+        sm.fixes[fi].slot = static_cast<int>(at.slot);
+        sm.fixes[fi].v0 = x.flags & 4u ? 64 : (s0 ? x.part : 0);
+        sm.fixes[fi].v1 = x.flags & 8u ? 64 : (s1 ? x.part : 0);
+      }
+      if (s0 || s1)
+        mbar_arrive_expect_tx(done, s0 && s1 ? L::kTile : L::kTile / 2);
+      else
+        mbar_arrive(done);
+      if (s0) tma_load_5d(dst, tm, done, 0, 0, 0, x.g0, head);
+      if (s1) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, x.g1, head);
+      if (is_v) {
+        mbar_arrive(sm.fixset + fi);
+        ++fix_n;
+      }
+    }
+    at.next();
+  }
+  __device__ __forceinline__ void tell(Piece& d, int n_, int tok0, int ntok, int dst) {
+    if (lane == 0 && ok) {
+      d.n = n_;
+      d.h = head;
+      d.tok0 = tok0;
+      d.ntok = ntok;
+      d.key0 = key0;
+      d.keys = end - key0;
+      d.dst = dst;
+      mbar_arrive(sm.pieced + told % kPieces);
+    }
+    ++told;
+  }
+
+  // Next piece: told, its rows on their way; n = 0 where there is nothing to compute.
+  __device__ __forceinline__ void next_piece() {
+    const int lanes = gridDim.x, l = blockIdx.x;
+    if (lane == 0 && told >= kPieces) wait(sm.unpieced + told % kPieces, told / kPieces - 1, 13);
+    Piece& d = sm.pieces[told % kPieces];
+    int tok0, ntok, dst;
+    n = 0;
+    if (kList) {
+      const int units = p.B * p.Nq * p.Hkv, unit_tiles = (p.n_sel + 1) >> 1;
+      const int whole = units / lanes * lanes;
+      long long u;
+      int t0 = 0, nt = unit_tiles;
+      dst = -1;
+      if (unit < whole) {
+        u = unit;
+        unit += lanes;
+      } else if (left > 0) {
+        const long long cut = static_cast<long long>(units - whole) * unit_tiles;
+        const long long first = run_start(cut, lanes, l), x = run_start(cut, lanes, l + 1) - left;
+        const int cu = static_cast<int>(x / unit_tiles);
+        u = whole + cu;
+        t0 = static_cast<int>(x - static_cast<long long>(cu) * unit_tiles);
+        nt = static_cast<int>(min(static_cast<long long>(unit_tiles - t0), left));
+        if (nt < unit_tiles) dst = 2 * l + (x > first ? 1 : 0);
+        left -= nt;
+      } else {
+        fin = true;
+        tell(d, -1, 0, 0, 0);
+        return;
+      }
+      // units by sequence, head, token: neighbours read the same head's keys
+      const int per = p.Hkv * p.Nq, ui = static_cast<int>(u);
+      const int bb = ui / per, r = ui - bb * per;
+      head = r / p.Nq;
+      const int i = r - head * p.Nq;
+      tok0 = bb * p.Nq + i;
+      ntok = 1;
+      list = p.blocks + (static_cast<long long>(tok0) * p.Hkv + head) * p.n_sel + 2 * t0;
+      count = min(p.n_sel - 2 * t0, 2 * nt);
+      const int len = clamped_len(p, bb);
+      if (lane == 0 && head == 0 && i == 0 && t0 == 0 && len != p.seqlens[bb]) record(1, kDevBadSeqlen);
+      row = bb;
+      seen = max(0, len - p.Nq + i + 1);
+      key0 = end = 0;
+      // which of them are seen; the last one that is ends the piece
+      int last = -1;
+      for (int w = (count - 1) >> 5; w >= 0; --w) {  // ends with the first 32 looked up
+        look_up(w);
+        if (lane == 0 && ok) {
+          d.full[w] = full_bits;
+          d.some[w] = seen_bits & ~full_bits;
+          if (d.some[w]) d.part = part;
+        }
+        if (last < 0 && seen_bits) last = 32 * w + 31 - __clz(seen_bits);
+      }
+      n = (last + 2) >> 1;
+    } else {
+      if (left == 0) {
+        fin = true;
+        tell(d, -1, 0, 0, 0);
+        return;
+      }
+      int len = b < 0 ? 0 : clamped_len(p, b);
+      while (b >= 0 && len <= p.shared_len) len = clamped_len(p, ++b);  // a sequence with keys of its own is ahead
+      int nt, rts, u;
+      head = hh;
+      if (b < 0) {
+        end = sm.plan->prefix_end;
+        key0 = 128 * t;
+        row = 0;
+        nt = tiles_of(end);
+        rts = 1;
+        u = hh;
+        tok0 = 0;
+        ntok = p.B * p.Nq;
+      } else {
+        end = len;
+        key0 = p.shared_len + 128 * t;
+        row = b;
+        nt = tiles_of(len - p.shared_len);
+        rts = p.own_rt;
+        u = (b * p.Hkv + hh) * rts + rt + (p.pairs ? 0 : p.Hkv);
+        tok0 = b * p.Nq + rt * p.own_tokens;
+        ntok = min(p.own_tokens, p.Nq - rt * p.own_tokens);
+      }
+      dst = l + u;
+      n = static_cast<int>(min(static_cast<long long>(nt - t), left));
+      left -= n;
+      t += n;
+      if (t == nt) {
+        t = 0;
+        if (++rt == rts) {
+          rt = 0;
+          if (++hh == p.Hkv) {
+            hh = 0;
+            ++b;
+          }
+        }
+      }
+    }
+    tell(d, n, tok0, ntok, dst);
+    if (n == 0) return;
+    if (lane == 0) {
+      const uint32_t buf = rows_n & 1;
+      if (rows_n >= 2) wait(sm.qfree + buf, rows_n / 2 - 1, 14);
+      if (ok) {
+        mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(p.unit_tokens * (p.Hq / p.Hkv) * D * 2));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sm.q + buf * L::kQ + c * (L::kN * 128), tm_q, sm.qfull + buf, c * 64, 0, head, tok0);
+        ++rows_n;
+      }
+    }
+    if (!kList) look_up(0);
+  }
+
+  __device__ __forceinline__ void run() {
+    const int lanes = gridDim.x, l = blockIdx.x;
+    if (kList) {
+      const int units = p.B * p.Nq * p.Hkv;
+      const long long cut = static_cast<long long>(units - units / lanes * lanes) * ((p.n_sel + 1) >> 1);
+      unit = l;
+      left = run_start(cut, lanes, l + 1) - run_start(cut, lanes, l);
+    } else {
+      const long long total = sm.plan->total;
+      left = run_start(total, lanes, l + 1) - run_start(total, lanes, l);
+      if (left > 0) {
+        b = sm.plan->lane_b[0];
+        const int nt = b < 0 ? tiles_of(sm.plan->prefix_end) : own_tiles(p, b), rts = b < 0 ? 1 : p.own_rt;
+        const long long x = sm.plan->lane_at[0];
+        const int u = static_cast<int>(x / nt);
+        hh = u / rts;
+        rt = u - hh * rts;
+        t = static_cast<int>(x - static_cast<long long>(u) * nt);
+      }
+    }
+    while (agree()) {
+      next_piece();
+      if (fin) break;
+      Tile last;
+      for (int j = 0; j <= n && n > 0; ++j) {
+        Tile x;
+        if (j < n) {
+          if (j > 0 && (j & 15) == 0) look_up(j >> 4);
+          x = tile(j);
+          load(x, false);
+        }
+        if (j > 0) load(last, true);
+        last = x;
+      }
+    }
+    if (lane != 0) return;
+    if (ok) {
+      // no more to clear
+      const uint32_t fi = fix_n & 3;
+      if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+      if (ok) {
+        sm.fixes[fi].slot = -1;
+        mbar_arrive(sm.fixset + fi);
+      }
+    }
+    // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
+    volatile int no_abort = 0;
+    for (uint32_t i = 0; i < 2 && i < rows_n; ++i) mbar_wait(sm.qfull + i, (rows_n - 1 - i) / 2 & 1, &no_abort, kWaitLimitNs);
+    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
+    for (uint32_t i = 0; i < L::kSlots; ++i) {
+      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
+      if (turns > 0) mbar_wait(sm.full + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// MMA issuer: one thread.
+template <int D, int R>
+struct Issuer {
+  using L = Layout<D, R>;
+  static constexpr uint32_t kN = L::kN;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kN, 0);
+  // A runs along M; d = 64: M = 128 takes two 64-dim blocks, of which the second
+  // (the keys behind, whatever lies there) only reaches lanes that nothing reads
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(128, kN, 0) | (1u << 15);
+  const Smem<D, R>& sm;
+  const uint32_t tmem;
+  uint64_t dK, dV, dQ, dP;
+  uint32_t base = 0, told = 0, piece = 0, ts = 0;  // first ring item of the piece, pieces looked at, with products, tiles
+  int n = 0, j = 0;
+  bool ok = true, fin = false;
+  struct Pv {
+    uint32_t item, tile, piece;
+    bool first, last, on;
+  };
+
+  __device__ __forceinline__ Issuer(const Smem<D, R>& sm_, uint32_t tmem_) : sm(sm_), tmem(tmem_) {
+    dK = sdesc_sw128(smem_u32(sm.ring), 16, L::kGroup);    // K-major
+    dV = sdesc_sw128(smem_u32(sm.ring), 1024, L::kGroup);  // MN-major
+    dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);            // K-major
+    dP = sdesc_sw128(smem_u32(sm.ps), 16, 1024);           // K-major
+  }
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  // Moves to the next tile; `block`: waits for its piece.  1: there is one, 0: no more, -1: not told yet.
+  __device__ __forceinline__ int next(bool block) {
+    while (ok && !fin && j == n) {
+      uint64_t* bar = sm.pieced + told % kPieces;
+      if (block)
+        wait(bar, told / kPieces, 24);
+      else if (!mbar_test_wait(bar, told / kPieces & 1))
+        return -1;
+      if (!ok) return 0;
+      const int dn = *const_cast<const volatile int*>(&sm.pieces[told % kPieces].n);
+      mbar_arrive(sm.unpieced + told % kPieces);
+      ++told;
+      if (dn < 0) {
+        fin = true;
+        return 0;
+      }
+      base += 2 * n;
+      n = dn;
+      j = 0;
+      if (n > 0) ++piece;
+    }
+    return ok && !fin ? 1 : 0;
+  }
+  __device__ __forceinline__ uint32_t k_item() const { return base + (j == 0 ? 0 : 2 * j - 1); }
+  // S of the tile moved to
+  __device__ __forceinline__ void scores(Pv& x) {
+    const uint32_t item = k_item(), slot = item % L::kSlots, buf = (piece - 1) & 1;
+    wait(sm.full + slot, item / L::kSlots, 25);
+    if (j == 0) wait(sm.qfull + buf, (piece - 1) / 2, 26);
+    if (!ok) return;
+    tc_fence_after();
+    const uint64_t a = dK + static_cast<uint64_t>((slot * L::kTile) >> 4), q = dQ + static_cast<uint64_t>((buf * L::kQ) >> 4);
+    const uint32_t to = tmem + (ts & 1) * kN;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_bf16_ss(to, a + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4),
+                  kIdescS, kk > 0 ? 1u : 0u);
+    mma_commit(sm.sfull + (ts & 1));
+    mma_commit(sm.empty + slot);
+    if (j == n - 1) mma_commit(sm.qfree + buf);
+    x.item = base + (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
+    x.tile = ts++;
+    x.piece = piece - 1;
+    x.first = j == 0;
+    x.last = j == n - 1;
+    x.on = true;
+    ++j;
+  }
+  __device__ __forceinline__ void run() {
+    Pv cur, nxt;
+    nxt.on = false;
+    int have = next(true);
+    if (have == 1) scores(nxt);
+    while (ok && nxt.on) {
+      cur = nxt;
+      nxt.on = false;
+      have = next(false);
+      if (have == 1) {
+        const uint32_t item = k_item();
+        if (mbar_test_wait(sm.full + item % L::kSlots, item / L::kSlots & 1)) scores(nxt);
+      }
+      const uint32_t slot = cur.item % L::kSlots, buf = cur.piece & 1;
+      wait(sm.pfull + (cur.tile & 1), cur.tile / 2, 22);
+      wait(sm.full + slot, cur.item / L::kSlots, 21);
+      if (cur.first && cur.piece >= 2) wait(sm.ofree + buf, cur.piece / 2 - 1, 23);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t a = dV + static_cast<uint64_t>((slot * L::kTile) >> 4),
+                     q = dP + static_cast<uint64_t>(((cur.tile & 1) * L::kP) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_bf16_ss(tmem + (2 + buf) * kN, a + ((kk * 2 * L::kGroup) >> 4),
+                    q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4), kIdescO, (!cur.first || kk > 0) ? 1u : 0u);
+      mma_commit(sm.empty + slot);
+      mma_commit(sm.pvdone + (cur.tile & 1));
+      if (cur.last) mma_commit(sm.odone + buf);
+      if (!nxt.on) {
+        if (have < 0) have = next(true);
+        if (ok && have == 1) scores(nxt);
+      }
+    }
+    if (!ok) {
+      // the MMAs issued so far complete before TMEM is freed
+      volatile int no_abort = 0;
+      mma_commit(sm.drain);
+      mbar_wait(sm.drain, 0, &no_abort, kWaitLimitNs);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The first R columns of this thread's TMEM lane.
+template <int R>
+__device__ __forceinline__ void tmem_row(uint32_t addr, float (&x)[R]) {
+  uint32_t u[R];
+  if constexpr (R == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"(addr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; i += 16) tmem_ld16(addr + i, u + i);
+  }
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < R; ++i) x[i] = __uint_as_float(u[i]);
+}
+template <int R>
+__device__ __forceinline__ void tmem_put_row(uint32_t addr, const float (&x)[R]) {
+  if constexpr (R == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(__float_as_uint(x[0])),
+                 "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3]))
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; i += 16) {
+      uint32_t u[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(x[i + k]);
+      tmem_st16(addr + i, u);
+    }
+  }
+  tmem_wait_st();
+}
+
+// The four softmax warps meet; true if any thread passes true.
+__device__ __forceinline__ bool group_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ int ordered_int(float x) {  // larger float, larger integer
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+
+constexpr float kMoveLog2 = 96.f;  // a row's reference moves where a score passes it by this much
+
+template <int D, int R, bool kList>
+struct Softmax {
+  using L = Layout<D, R>;
+  const RowsParams& p;
+  const Smem<D, R>& sm;
+  const uint32_t tmem;
+  const int lane, w4, key;  // key: of the tile (TMEM lane), and output dim
+  float M[R], l[R];
+  uint32_t ts = 0, piece = 0;
+  bool ok = true;  // this warp's view; all leave together
+
+  __device__ __forceinline__ Softmax(const RowsParams& p_, const Smem<D, R>& sm_, uint32_t tmem_)
+      : p(p_), sm(sm_), tmem(tmem_ + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21)), lane(threadIdx.x & 31),
+        w4((threadIdx.x >> 5) & 3), key(threadIdx.x & 127) {}
+
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_all(bar, parity & 1, sm.abort_flag, site);
+  }
+
+  // New references from this tile's largest scores; O^T and the sums so far are
+  // brought to them.  s: the scores, scaled; where not `vis` they do not count.
+  __device__ __forceinline__ void move(const float (&s)[R], uint32_t vis, bool first) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int m = __reduce_max_sync(0xffffffffu, ordered_int(vis >> r & 1u ? s[r] : -INFINITY));
+      if (lane == 0) sm.red[w4 * R + r] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+    }
+    group_sync();
+    float f[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mx = fmaxf(fmaxf(sm.red[r], sm.red[R + r]), fmaxf(sm.red[2 * R + r], sm.red[3 * R + r]));
+      const float m = M[r] == -INFINITY || mx - M[r] > 8.f ? fmaxf(M[r], mx) : M[r];
+      f[r] = M[r] == m ? 1.f : ex2_approx(M[r] - m);  // 0 where nothing was seen
+      M[r] = m;
+      l[r] *= f[r];
+    }
+    group_sync();  // red is read
+    if (first) return;
+    wait(sm.pvdone + ((ts - 1) & 1), (ts - 1) / 2, 44);
+    tc_fence_after();
+    float o[R];
+    const uint32_t at = tmem + (2 + (piece & 1)) * L::kN;
+    tmem_row<R>(at, o);
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[r] *= f[r];
+    tmem_put_row<R>(at, o);
+  }
+
+  __device__ __forceinline__ void run() {
+    const int G = p.Hq / p.Hkv;
+    for (uint32_t i = 0;; ++i) {
+      const Piece& d = sm.pieces[i % kPieces];
+      wait(sm.pieced + i % kPieces, i / kPieces, 41);
+      if (group_any(!ok)) return;
+      const int n = d.n, h = d.h, tok0 = d.tok0, ntok = d.ntok, dst = d.dst;
+      if (n < 0) return;
+      const int rows = ntok * G;
+      int whole = 0;  // ranges: keys that all rows see
+      if (!kList) {
+        int lim = 0x7fffffff;
+        if (key < rows) {
+          const int tok = tok0 + key / G, b = tok / p.Nq;
+          lim = min(d.keys, clamped_len(p, b) - p.Nq + tok - b * p.Nq + 1 - d.key0);
+          sm.lim[key] = lim;
+        }
+        const int m = __reduce_min_sync(0xffffffffu, lim);
+        if (lane == 0) sm.red[w4] = __int_as_float(m);
+        group_sync();
+        whole = min(min(__float_as_int(sm.red[0]), __float_as_int(sm.red[1])), min(__float_as_int(sm.red[2]), __float_as_int(sm.red[3])));
+        group_sync();
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        M[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+      for (int j = 0; j < n; ++j, ++ts) {
+        wait(sm.sfull + (ts & 1), ts / 2, 42);
+        tc_fence_after();
+        float s[R];
+        tmem_row<R>(tmem + (ts & 1) * L::kN, s);
+        uint32_t vis = ~0u;  // rows that see this key
+        if (kList) {
+          const int e = 2 * j + (key >> 6);
+          const int v = d.full[e >> 5] >> (e & 31) & 1u ? 64 : (d.some[e >> 5] >> (e & 31) & 1u ? d.part : 0);
+          if ((key & 63) >= v) vis = 0;
+        } else if (128 * (j + 1) > whole) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (r < rows && 128 * j + key >= sm.lim[r]) vis &= ~(1u << r);
+        }
+        bool over = j == 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          s[r] *= p.scale_log2;
+          over = over || (r < rows && (vis >> r & 1u) && s[r] - M[r] > kMoveLog2);
+        }
+        if (!ok) sm.gone[ts & 1] = 1;
+        if (group_any(over || !ok)) {
+          if (sm.gone[ts & 1]) return;
+          move(s, vis, j == 0);
+        }
+        // p, to its place in the operand: rows of 128 B (64 keys), chunks of 16 B
+        // exchanged by the row
+        uint8_t* to = sm.ps + (ts & 1) * L::kP + (key >> 6) * (L::kN * 128) + (key & 7) * 2;
+        const int ch = (key & 63) >> 3;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float x = ex2_approx(s[r] - (M[r] == -INFINITY ? 0.f : M[r]));
+          const float v = vis >> r & 1u ? x : 0.f;
+          l[r] += v;
+          *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((ch ^ (r & 7)) << 4)) = __float2bfloat16_rn(v);
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();  // P before the tensor core's reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.pfull + (ts & 1));
+      }
+      // sums of the rows: over a warp's keys, then the four warps
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane == 0) sm.red[w4 * R + r] = l[r];
+      }
+      group_sync();
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = (sm.red[r] + sm.red[R + r]) + (sm.red[2 * R + r] + sm.red[3 * R + r]);
+      group_sync();
+      float o[R];
+      if (n > 0) {
+        wait(sm.odone + (piece & 1), piece / 2, 43);
+        tc_fence_after();
+        tmem_row<R>(tmem + (2 + (piece & 1)) * L::kN, o);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.ofree + (piece & 1));
+        ++piece;
+      }
+      // l is 0 where nothing was seen; NaN stays NaN
+      int tok = tok0, g = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const float v = l[r] == 0.f ? 0.f : o[r] * (1.f / l[r]);
+        const float lse2 = l[r] == 0.f ? -INFINITY : M[r] + __log2f(l[r]);
+        if (dst >= 0) {
+          const long long at = p.pair_rows + static_cast<long long>(dst) * p.unit_rows + r;
+          if (key < D) p.o_part[at * D + key] = v;
+          if (key == 0) p.lse_part[at] = lse2;
+        } else {
+          const int hq = h * G + g;
+          if (key < D)
+            static_cast<__nv_bfloat16*>(p.o)[(static_cast<long long>(tok) * p.Hq + hq) * D + key] = __float2bfloat16_rn(v);
+          if (key == 0) {
+            const int b = tok / p.Nq;
+            p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
+          }
+        }
+        if (++g == G) {
+          g = 0;
+          ++tok;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.unpieced + i % kPieces);
+    }
+  }
+};
+
+// after_pairs: the kernel before on the stream is that of the pairs, whose CTAs
+// have all passed their own wait when this one starts: nothing it reads is
+// still being written, so it takes the SMs as they come free, and only ends
+// after that kernel (the joining kernel waits for this one).
+template <int D, int R, bool kList>
+__global__ void __launch_bounds__(kThreads, 1)
+    few_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RowsParams p, int after_pairs) {
+  using L = Layout<D, R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const Smem<D, R> sm(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(sm.full + i, 1);
+      mbar_init(sm.empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.sfull + i, 1);
+      mbar_init(sm.pfull + i, 4);
+      mbar_init(sm.pvdone + i, 1);
+      mbar_init(sm.odone + i, 1);
+      mbar_init(sm.ofree + i, 4);
+      mbar_init(sm.qfull + i, 1);
+      mbar_init(sm.qfree + i, 1);
+      sm.gone[i] = 0;
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(sm.pieced + i, 1);
+      mbar_init(sm.unpieced + i, 5);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(sm.fixset + i, 1);
+      mbar_init(sm.fixdone + i, 1);
+      mbar_init(sm.raw + i, 1);
+    }
+    mbar_init(sm.drain, 1);
+    *sm.abort_flag = 0;
+    mbar_fence_init();
+  }
+  grid_release();
+  if (!after_pairs) grid_wait();
+  if (warp == 1) {
+    tmem_alloc(sm.tmem_slot, L::kTmem);
+    tmem_relinquish();
+  }
+  if (!kList)
+    make_plan<kThreads / 32, 1>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
+                                reinterpret_cast<int*>(smem + L::kOffScan + 8 * 8));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    Producer<D, R, kList> producer(p, &tm_q, &tm_k, &tm_v, sm, lane);
+    producer.run();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      Issuer<D, R> issuer(sm, tmem);
+      issuer.run();
+    }
+  } else if (warp == 2) {
+    for (uint32_t i = 0;; ++i) {
+      const uint32_t fi = i & 3;
+      if (!wait_all(sm.fixset + fi, i / 4 & 1, sm.abort_flag, 31)) break;
+      const int slot = sm.fixes[fi].slot, v0 = sm.fixes[fi].v0, v1 = sm.fixes[fi].v1;
+      if (slot < 0) break;
+      if (!wait_all(sm.raw + fi, i / 4 & 1, sm.abort_flag, 32)) break;
+      uint8_t* base = sm.ring + slot * L::kTile;
+      for (int half = 0; half < 2; ++half) {
+        const int v = half ? v1 : v0;
+        for (int c = lane; c < (64 - v) * (D / 8); c += 32) {
+          const int r = v + c / (D / 8), ch = c % (D / 8);
+          *reinterpret_cast<uint4*>(base + half * (L::kTile / 2) + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
+                                    (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();  // these stores before the tensor core's reads
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(sm.full + slot);
+        mbar_arrive(sm.fixdone + fi);
+      }
+    }
+  } else if (warp >= 4) {
+    Softmax<D, R, kList> softmax(p, sm, tmem);
+    softmax.run();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmem);
+  }
+  if (after_pairs) grid_wait();
+}
+
+template <int D, int R>
+cudaError_t launch_r(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                     int grid, bool after_pairs, cudaStream_t stream) {
+  using L = Layout<D, R>;
+  auto kern = p.blocks ? few_rows_kernel<D, R, true> : few_rows_kernel<D, R, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(grid), kThreads, L::kAlloc, stream, tm_q, tm_k, tm_v, p, after_pairs ? 1 : 0);
+}
+template <int D>
+cudaError_t launch_d(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                     int grid, bool after_pairs, cudaStream_t stream) {
+  if (p.unit_rows <= 4) return launch_r<D, 4>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+  if (p.unit_rows <= 16) return launch_r<D, 16>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+  return launch_r<D, kFewRows>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                            int grid, bool after_pairs, cudaStream_t stream) {
+  return p.d == 64 ? launch_d<64>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream)
+                   : launch_d<128>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+}
+
+cudaError_t status_word_few_rows(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_rows_status); }
+
+}  // namespace attn

@@ -250,12 +250,16 @@ struct RowsParams {
   int B, Nq, Hq, Hkv, d;
   float scale_log2;
   int tile_tokens, pairs, own_tokens, own_rt, unit_tokens, unit_rows;
-  int lane_rows;      // rows of a tile that lane work uses: 32, 64 or 128
+  int only_pairs;     // set at launch: the lanes' work is another kernel's
   long long pair_rows;
 };
 // q as {d, heads of a group, Hkv, tokens}: tiles of tile_tokens and of unit_tokens tokens; the page pools in 64 rows.
 cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, cudaStream_t stream);
+// The lanes' work of units with up to kFewRows rows; after_pairs: the kernel before on the stream is that of the pairs.
+constexpr int kFewRows = 32;
+cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                            int grid, bool after_pairs, cudaStream_t stream);
 // Maps of bf16 tensors: a page pool as {64, 8, d / 64, groups of 8 keys, Hkv}, boxes of a head's 64 keys; q's of
 // `tokens` tokens of a group of heads.
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d);
@@ -270,8 +274,9 @@ cudaError_t status_word_append(uint32_t** at);
 cudaError_t status_word_decode_fp8(uint32_t** at);
 cudaError_t status_word_paging(uint32_t** at);
 cudaError_t status_word_select(uint32_t** at);
-cudaError_t status_word_rows(uint32_t** at);
-constexpr int kStatusUnits = 9;
+cudaError_t status_word_wide_rows(uint32_t** at);
+cudaError_t status_word_few_rows(uint32_t** at);
+constexpr int kStatusUnits = 10;
 struct StatusWords {
   uint32_t* at[kStatusUnits];
 };

@@ -34,21 +34,14 @@
 
 #include "launch.h"
 #include "ptx.cuh"
+#include "rows_plan.cuh"
 #include "rows_softmax.cuh"
 
 namespace attn {
 namespace {
 
-__device__ uint32_t g_rows_status;
-
-__device__ __forceinline__ void record(uint32_t site, uint32_t code) {
-  atomicCAS(&g_rows_status, 0u, (site << 8) | code);
-}
-
 constexpr int kThreads = 384;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: no legitimate wait comes close
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaskWords = kMaxListed / 32;
 
 // What a slot computes next, as the producer tells the other warps.
 struct Piece {
@@ -61,17 +54,6 @@ struct Piece {
   int part;   // keys seen of the blocks marked in part[] (lists)
   uint32_t full[kMaskWords], some[kMaskWords];  // lists: blocks seen whole, seen in part
 };
-struct Fix {
-  int slot, v0, v1;  // ring slot; value rows that count of its two halves
-};
-// Start of the slots' lanes, set up by all threads.
-struct Plan {
-  long long lane_at[2];  // tiles from the start of the sequence's keys
-  int lane_b[2];         // sequence at which the lanes start (-1: the prefix)
-  long long total, pair_total;
-  int prefix_end;        // keys of the prefix that any sequence has
-};
-
 template <int D>
 struct Layout {
   static constexpr int kSlots = D == 64 ? 10 : 5;
@@ -83,7 +65,7 @@ struct Layout {
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffPiece = kOffRing + kSlots * kTile;
   static constexpr int kOffBar = kOffPiece + 4 * static_cast<int>(sizeof(Piece));
-  static constexpr int kNumBars = 2 * kSlots + 4 * 2 + 4 * 4 + 3 * 4 + 1;
+  static constexpr int kNumBars = 2 * kSlots + 6 * 2 + 2 * 4 + 3 * 4 + 1;
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
@@ -93,119 +75,8 @@ struct Layout {
 };
 static_assert(Layout<128>::kAlloc <= 232448 && Layout<64>::kAlloc <= 232448, "shared memory of a CTA");
 
-// Bounded waits: one probe in line, the rest out of line, as the warps' code
-// together has to fit the instruction cache (57% of the fetches hit it before).
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
-  const bool ok = mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
-  if (!ok) record(site, kDevTimeout);
-  return ok;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
-  return mbar_test_wait(bar, parity) || wait_long(bar, parity, abort_flag, site);
-}
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t site) {
-  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, site));
-}
-
-__device__ __forceinline__ int clamped_len(const RowsParams& p, int b) {
-  return min(max(p.seqlens[b], 0), p.max_blocks * p.page_size);
-}
-__device__ __forceinline__ int tiles_of(int keys) { return (keys + 127) >> 7; }
-// Key tiles of a sequence behind the prefix.
-__device__ __forceinline__ int own_tiles(const RowsParams& p, int b) {
-  return tiles_of(max(0, clamped_len(p, b) - p.shared_len));
-}
-// `total` tiles dealt to `lanes` in runs of equal length, none of them empty but
-// the last ones: where run i starts, and which run holds tile x.
-__device__ __noinline__ long long run_start(long long total, int lanes, int i) {
-  const long long runs = min(total, static_cast<long long>(lanes));
-  return i < runs ? total * i / runs : total;
-}
-__device__ __noinline__ int run_of(long long total, int lanes, long long x) {
-  const long long runs = min(total, static_cast<long long>(lanes));
-  return static_cast<int>(((x + 1) * runs - 1) / total);
-}
 // The lane of a slot: with few runs the CTAs have one each.
 __device__ __forceinline__ int lane_of(int slot) { return slot * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); }
-
-// Lanes' starts for ranges: sums of the sequences' tiles, by all threads.  CTA 0
-// leaves the sums before each sequence, and the totals, for the second kernel.
-__device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int* s_max) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kThreads / 32;
-  const int per = p.Hkv * p.own_rt;  // units of a sequence
-  long long sum = 0;
-  int longest = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
-    sum += static_cast<long long>(own_tiles(p, b)) * per;
-    longest = max(longest, clamped_len(p, b));
-    if (blockIdx.x == 0 && (p.seqlens[b] < 0 || p.seqlens[b] > p.max_blocks * p.page_size)) record(1, kDevBadSeqlen);
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) {
-    s_sum[warp] = sum;
-    s_max[warp] = longest;
-  }
-  __syncthreads();
-  sum = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    sum += s_sum[w];
-    longest = max(longest, s_max[w]);
-  }
-  const int end = min(p.shared_len, longest);
-  const long long prefix = static_cast<long long>(tiles_of(end)) * p.Hkv;
-  const long long solo = p.pairs ? 0 : prefix;
-  const long long total = solo + sum;
-  const int lanes = 2 * gridDim.x;
-  if (tid == 0) {
-    plan->prefix_end = end;
-    plan->total = total;
-    plan->pair_total = p.pairs ? prefix * p.pairs : 0;
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.sums[p.B] = total;
-    p.sums[p.B + 1] = p.pairs ? prefix * p.pairs : 0;
-    p.sums[p.B + 2] = end;
-  }
-  long long x[2];
-  for (int s = 0; s < 2; ++s) {
-    x[s] = run_start(total, lanes, lane_of(s));
-    if (tid == 0 && x[s] < solo) {
-      plan->lane_b[s] = -1;
-      plan->lane_at[s] = x[s];
-    }
-  }
-  long long base = solo;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    // slot 1's lane starts last; CTA 0 needs all sums
-    if (blockIdx.x != 0 && base > x[1]) break;
-    const int b = b0 + tid;
-    const long long mine = b < p.B ? static_cast<long long>(own_tiles(p, b)) * per : 0;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    long long before = base + incl - mine, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
-    }
-    if (b < p.B && blockIdx.x == 0) p.sums[b] = before;
-    for (int s = 0; s < 2; ++s)
-      if (b < p.B && before <= x[s] && x[s] < before + mine) {
-        plan->lane_b[s] = b;
-        plan->lane_at[s] = x[s] - before;
-      }
-    base += all;
-  }
-}
 
 // Shared memory of a CTA.
 template <int D>
@@ -218,8 +89,8 @@ struct Smem {
   uint64_t* pfull;       // [2] P written (4 warps)
   uint64_t* odone;       // [2] a piece's last P V complete
   uint64_t* ofree;       // [2] a piece's O read (4 warps)
-  uint64_t* qfull;       // [slot][2] rows loaded
-  uint64_t* qfree;       // [slot][2] a piece's last Q K^T complete
+  uint64_t* qfull;       // [2] rows loaded
+  uint64_t* qfree;       // [2] a piece's last Q K^T complete
   uint64_t* pieced;      // [slot][2] piece told
   uint64_t* unpieced;    // [slot][2] piece done with (MMA thread, 4 warps)
   uint64_t* fixset;      // [4] clearing asked for
@@ -242,8 +113,8 @@ struct Smem {
     odone = pfull + 2;
     ofree = odone + 2;
     qfull = ofree + 2;
-    qfree = qfull + 4;
-    pieced = qfree + 4;
+    qfree = qfull + 2;
+    pieced = qfree + 2;
     unpieced = pieced + 4;
     fixset = unpieced + 4;
     fixdone = fixset + 4;
@@ -256,37 +127,11 @@ struct Smem {
   }
 };
 
-// Lane work on few rows (lane_rows: 32 or 64 of a tile's 128).  The rows lie in
-// two buffers of the slot's Q tile; the product takes them as rows of another
-// part of the tile, whose warps of the softmax share no scheduler with the other
-// slot's, nor (32 rows) with the producer and the issuer.
-__device__ __forceinline__ int buffer_row(int lane_rows, int buf) { return lane_rows == 32 ? 64 + 32 * buf : 64 * buf; }
-__device__ __forceinline__ int first_row(int lane_rows, int slot) {
-  return lane_rows == 32 ? 64 + 32 * slot : (lane_rows == 64 ? 64 * slot : 0);
-}
-
-// A place in the ring: slot and phase of the turn through it.
-template <int NS>
-struct RingAt {
-  uint32_t slot = 0, turn = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == NS) {
-      slot = 0;
-      ++turn;
-    }
-  }
-};
-
 // ---------------------------------------------------------------------------
 // Producer: one warp, whose lanes look up 32 blocks of a piece at a time; lane 0
 // waits and issues.  What belongs to a slot is in a struct; the two take turns in
 // the same registers and the same code (exchanged after each step), so that no
 // state lies in local memory and the code is there once.
-struct Tile {
-  int g0, g1;      // first groups of 8 keys in the pool
-  uint32_t flags;  // bits 0, 1: seen; 2, 3: seen whole
-  int part;
-};
 struct ProducerSlot {
   // the lane's run
   long long left;        // tiles left (lists: of the cut units)
@@ -301,7 +146,7 @@ struct ProducerSlot {
   uint32_t seen_bits, full_bits;
   int part;
   Tile last;             // the tile whose V comes next
-  uint32_t told, rows_n[2];
+  uint32_t told, rows_n;  // pieces told, rows loaded
   int slot;
   bool fin, pend;
 };
@@ -335,16 +180,6 @@ struct Producer {
     return ok;
   }
 
-  // block `blk` of table row `row`, as a block of the pool
-  __device__ __forceinline__ int pool_block(int row, int blk) {
-    const int at_page = blk * 64 / p.page_size;
-    int g = p.block_table[static_cast<long long>(row) * p.max_blocks + at_page];
-    if (g < 0 || g >= p.num_pages) {
-      record(2, kDevBadPage);
-      g = 0;
-    }
-    return g * (p.page_size / 64) + blk - at_page * (p.page_size / 64);
-  }
   // blocks 32 i .. 32 i + 31 of the piece
   __device__ __forceinline__ void look_up(ProducerSlot& s, int i) {
     int v = 0, blk;
@@ -363,7 +198,7 @@ struct Producer {
       blk = key >> 6;
     }
     s.blk = 0;
-    if (v > 0) s.blk = 8 * pool_block(s.row, blk);
+    if (v > 0) s.blk = pool_group(p, s.row, blk);
     s.seen_bits = __ballot_sync(0xffffffffu, v > 0);
     s.full_bits = __ballot_sync(0xffffffffu, v == 64);
     const uint32_t some = s.seen_bits & ~s.full_bits;
@@ -434,26 +269,17 @@ struct Producer {
     }
     ++s.told;
   }
-  // the rows of a piece; buffers in turn where there are two
-  __device__ __forceinline__ void load_rows(ProducerSlot& s, bool second, bool pair, int h, int tok0) {
-    uint32_t uses = second ? s.rows_n[1] : s.rows_n[0];
-    const int buf = s.slot * 2 + (second ? 1 : 0);
-    if (lane == 0) {
-      if (uses > 0) wait(sm.qfree + buf, uses - 1, 14);
-      if (ok) {
-        const int tokens = pair ? p.tile_tokens : p.unit_tokens;
-        const int row = pair ? 0 : buffer_row(p.lane_rows, second ? 1 : 0);
-        mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(tokens * (p.Hq / p.Hkv) * D * 2));
+  // the rows of a piece
+  __device__ __forceinline__ void load_rows(ProducerSlot& s, bool pair, int h, int tok0) {
+    if (lane != 0) return;
+    if (s.rows_n > 0) wait(sm.qfree + s.slot, s.rows_n - 1, 14);
+    if (!ok) return;
+    const int tokens = pair ? p.tile_tokens : p.unit_tokens;
+    mbar_arrive_expect_tx(sm.qfull + s.slot, static_cast<uint32_t>(tokens * (p.Hq / p.Hkv) * D * 2));
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sm.q + s.slot * L::kTile + c * L::kHalf + row * 128, pair ? tm_q : tm_qs, sm.qfull + buf, c * 64, 0,
-                      h, tok0);
-        if (second)
-          ++s.rows_n[1];
-        else
-          ++s.rows_n[0];
-      }
-    }
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_4d(sm.q + s.slot * L::kTile + c * L::kHalf, pair ? tm_q : tm_qs, sm.qfull + s.slot, c * 64, 0, h, tok0);
+    ++s.rows_n;
   }
 
   // Pair work: pieces of the CTA's run, each to its end.
@@ -474,8 +300,8 @@ struct Producer {
       tell(a, d0, n, share, h, tok0, min(p.tile_tokens, tokens - tok0), a.key0, end - a.key0, dst);
       Piece& d1 = place(b);
       tell(b, d1, n, share, h, tok1, max(0, min(p.tile_tokens, tokens - tok1)), a.key0, end - a.key0, dst);
-      load_rows(a, false, true, h, tok0);
-      if (share == 1) load_rows(b, false, true, h, tok1);
+      load_rows(a, true, h, tok0);
+      if (share == 1) load_rows(b, true, h, tok1);
       for (int j = 0; j <= n; ++j) {
         if (j > 0) load(a.last, h, true);
         if (j == n) break;
@@ -590,7 +416,7 @@ struct Producer {
     }
     tell(s, d, s.n, 0, s.head, tok0, ntok, s.key0, s.end - s.key0, dst);
     if (s.n == 0) return;
-    load_rows(s, p.lane_rows < 128 && (s.rows_n[0] + s.rows_n[1] & 1u), false, s.head, tok0);
+    load_rows(s, false, s.head, tok0);
     if (!kList) look_up(s, 0);
   }
 
@@ -604,7 +430,7 @@ struct Producer {
       s.left = run_start(cut, lanes, l + 1) - run_start(cut, lanes, l);
     } else {
       const long long total = sm.plan->total;
-      s.left = run_start(total, lanes, l + 1) - run_start(total, lanes, l);
+      s.left = p.only_pairs ? 0 : run_start(total, lanes, l + 1) - run_start(total, lanes, l);
       if (s.left > 0) {
         s.b = sm.plan->lane_b[s.slot];
         const int nt = s.b < 0 ? tiles_of(sm.plan->prefix_end) : own_tiles(p, s.b), rts = s.b < 0 ? 1 : p.own_rt;
@@ -614,8 +440,6 @@ struct Producer {
         s.rt = u - s.h * rts;
         s.t = static_cast<int>(x - static_cast<long long>(u) * nt);
       }
-      // rows of pairs lie over both buffers: read to their end
-      if (lane == 0 && s.rows_n[0] > 0) wait(sm.qfree + s.slot * 2, s.rows_n[0] - 1, 14);
     }
   }
 
@@ -633,7 +457,7 @@ struct Producer {
 
   __device__ __forceinline__ void run() {
     ProducerSlot a, b;
-    a.told = b.told = a.rows_n[0] = a.rows_n[1] = b.rows_n[0] = b.rows_n[1] = 0;
+    a.told = b.told = a.rows_n = b.rows_n = 0;
     a.fin = b.fin = a.pend = b.pend = false;
     a.slot = 0;
     b.slot = 1;
@@ -662,10 +486,8 @@ struct Producer {
     // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
     volatile int no_abort = 0;
     auto drain = [&](uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity & 1, &no_abort, kWaitLimitNs); };
-    if (a.rows_n[0]) drain(sm.qfull + 0, a.rows_n[0] - 1);
-    if (a.rows_n[1]) drain(sm.qfull + 1, a.rows_n[1] - 1);
-    if (b.rows_n[0]) drain(sm.qfull + 2, b.rows_n[0] - 1);
-    if (b.rows_n[1]) drain(sm.qfull + 3, b.rows_n[1] - 1);
+    if (a.rows_n) drain(sm.qfull + 0, a.rows_n - 1);
+    if (b.rows_n) drain(sm.qfull + 1, b.rows_n - 1);
     for (uint32_t i = 0; i < 4 && i < fix_n; ++i) drain(sm.raw + i, (fix_n - 1 - i) / 4);
     for (uint32_t i = 0; i < L::kSlots; ++i) {
       const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
@@ -679,9 +501,7 @@ struct Producer {
 struct MmaSlot {
   int n, j;
   uint32_t seen, done, tiles;  // pieces looked at, with products; P tiles consumed
-  uint32_t rows_n[2];
-  uint32_t buf;
-  uint64_t da;  // descriptor of its rows
+  uint32_t rows_n;             // rows used
   bool fin, pend;
 };
 
@@ -691,12 +511,11 @@ struct Issuer {
   static constexpr uint32_t kIdescQk = idesc_bf16_f32(128, 128, 0), kIdescPv = idesc_bf16_f32(128, D, 1);
   const Smem<D>& sm;
   const uint32_t tmem;
-  const int lane_rows;
   uint64_t dQ, dK, dV;
   RingAt<L::kSlots> at;
   bool ok = true;
 
-  __device__ __forceinline__ Issuer(const Smem<D>& sm_, uint32_t tmem_, int rows) : sm(sm_), tmem(tmem_), lane_rows(rows) {
+  __device__ __forceinline__ Issuer(const Smem<D>& sm_, uint32_t tmem_) : sm(sm_), tmem(tmem_) {
     dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);
     dK = sdesc_sw128(smem_u32(sm.ring), 16, L::kGroup);
     dV = sdesc_sw128(smem_u32(sm.ring), 1024, L::kGroup);
@@ -714,7 +533,8 @@ struct Issuer {
                   (!first || kk > 0) ? 1u : 0u);
   }
   template <int S>
-  __device__ __forceinline__ void qk(uint32_t slot, uint64_t da) {
+  __device__ __forceinline__ void qk(uint32_t slot) {
+    const uint64_t da = dQ + static_cast<uint64_t>((S * L::kTile) >> 4);
     const uint64_t db = dK + static_cast<uint64_t>((slot * L::kTile) >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -743,8 +563,8 @@ struct Issuer {
   // One piece of pair work, both slots (told already); slot 1 has rows only if `both`.
   __device__ __forceinline__ void pair_piece(MmaSlot& a, MmaSlot& b, bool both) {
     const int n = a.n;
-    wait(sm.qfull + 0, a.rows_n[0]++, 26);
-    if (both) wait(sm.qfull + 2, b.rows_n[0]++, 26);
+    wait(sm.qfull + 0, a.rows_n++, 26);
+    if (both) wait(sm.qfull + 1, b.rows_n++, 26);
     uint32_t vs = 0, vturn = 0;  // where V of the tile before lies
     bool p0 = false;
     for (int j = 0; ok && j <= n; ++j) {
@@ -767,7 +587,7 @@ struct Issuer {
         wait(sm.full + ks, kturn, 25);
         if (!ok) break;
         tc_fence_after();
-        qk<0>(ks, dQ);
+        qk<0>(ks);
         if (j == n - 1) mma_commit(sm.qfree + 0);
       } else {
         mma_commit(sm.odone + 0);
@@ -781,8 +601,8 @@ struct Issuer {
           pv<1>(vs, j == 1);
         }
         if (j < n) {
-          qk<1>(ks, dQ + (L::kTile >> 4));
-          if (j == n - 1) mma_commit(sm.qfree + 2);
+          qk<1>(ks);
+          if (j == n - 1) mma_commit(sm.qfree + 1);
         } else {
           mma_commit(sm.odone + 1);
         }
@@ -821,22 +641,12 @@ struct Issuer {
     const uint32_t ks = at.slot;
     wait(sm.full + ks, at.turn, 25);
     at.next();
-    if (s.j == 0) {
-      s.buf = lane_rows < 128 ? (s.rows_n[0] + s.rows_n[1]) & 1u : 0u;
-      // from where the tile's row 0 would lie
-      s.da = dQ + static_cast<uint64_t>(
-                      static_cast<int64_t>(S * L::kTile + (buffer_row(lane_rows, static_cast<int>(s.buf)) - first_row(lane_rows, S)) * 128) >> 4);
-      wait(sm.qfull + S * 2 + s.buf, s.buf ? s.rows_n[1] : s.rows_n[0], 26);
-      if (s.buf)
-        ++s.rows_n[1];
-      else
-        ++s.rows_n[0];
-    }
+    if (s.j == 0) wait(sm.qfull + S, s.rows_n++, 26);
     if (!ok) return;
     tc_fence_after();
-    qk<S>(ks, s.da);
+    qk<S>(ks);
     ++s.j;
-    if (s.j == s.n) mma_commit(sm.qfree + S * 2 + s.buf);
+    if (s.j == s.n) mma_commit(sm.qfree + S);
     mma_commit(sm.empty + ks);
     s.pend = true;
   }
@@ -844,8 +654,8 @@ struct Issuer {
   __device__ __forceinline__ void run() {
     MmaSlot a, b;
     a.n = a.j = b.n = b.j = 0;
-    a.seen = a.done = a.tiles = a.rows_n[0] = a.rows_n[1] = a.buf = 0;
-    b.seen = b.done = b.tiles = b.rows_n[0] = b.rows_n[1] = b.buf = 0;
+    a.seen = a.done = a.tiles = a.rows_n = 0;
+    b.seen = b.done = b.tiles = b.rows_n = 0;
     a.fin = b.fin = a.pend = b.pend = false;
     // pair pieces come first, both slots told of each
     int share = 0;
@@ -896,10 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(sm.pfull + s, 4);
       mbar_init(sm.odone + s, 1);
       mbar_init(sm.ofree + s, 4);
+      mbar_init(sm.qfull + s, 1);
+      mbar_init(sm.qfree + s, 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(sm.qfull + i, 1);
-      mbar_init(sm.qfree + i, 1);
       mbar_init(sm.pieced + i, 1);
       mbar_init(sm.unpieced + i, 5);
       mbar_init(sm.fixset + i, 1);
@@ -910,13 +720,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_fence_init();
   }
-  grid_depends();
+  // a kernel that starts behind this one may then count on what this one waited for
+  grid_wait();
+  grid_release();
   if (warp == 1) {
     tmem_alloc(sm.tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   if (!kList)
-    make_plan(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
+    make_plan<kThreads / 32, 2>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
               reinterpret_cast<int*>(smem + L::kOffScan + 12 * 8));
   tc_fence_before();
   __syncthreads();
@@ -934,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     producer.run();
   } else if (warp == 1) {
     if (lane == 0) {
-      Issuer<D> issuer(sm, tmem, p.lane_rows);
+      Issuer<D> issuer(sm, tmem);
       issuer.run();
     }
   } else if (warp == 2) {
@@ -968,9 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + s * 128 + lane_off, tO = tmem + 256 + s * 128 + lane_off;
-    // this thread's row: of the tile (pair work), of the lane's rows
-    const int pair_r = quarter * 32 + lane, lane_r = pair_r - first_row(p.lane_rows, s);
-    const int pair_tok = pair_r / G, lane_tok = lane_r < 0 ? -1 : lane_r / G;
+    const int r = quarter * 32 + lane, rtok = r / G, rg = r - rtok * G;
     uint32_t tiles = 0, done = 0;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
@@ -978,9 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_all(sm.pieced + s * 2 + (i & 1), (i / 2) & 1, abort_flag, 41)) break;
       const int n = d.n, share = d.share, ntok = d.ntok, h = d.h, dst = d.dst;
       const int rows = share == 2 && s == 1 ? 0 : ntok * G;
-      const int r = share ? pair_r : lane_r, rtok = share ? pair_tok : lane_tok, rg = r - rtok * G;
-      const bool live = r >= 0 && r < rows;
-      const bool on = __any_sync(0xffffffffu, live);  // rows of this warp
+      const bool live = r < rows, on = quarter * 32 < rows;  // this row, some row of the warp
       const int tok = d.tok0 + rtok;
       const int b = live ? tok / p.Nq : 0, nth = tok - b * p.Nq;
       if (n >= 0 && rows > 0) {
@@ -1180,7 +988,7 @@ __device__ __forceinline__ void write_row(const RowsParams& p, int tok, int hq, 
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __grid_constant__ RowsParams p, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __grid_constant__ RowsParams p, int grid, int lanes) {
   grid_depends();
   const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   if (row >= p.B * p.Nq * p.Hq) return;
@@ -1203,14 +1011,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __gr
     }
   } else if (nt > 0) {
     const long long a = static_cast<long long>(h) * nt;
-    const int first = run_of(total, 2 * grid, a), last = run_of(total, 2 * grid, a + nt - 1);
+    const int first = run_of(total, lanes, a), last = run_of(total, lanes, a + nt - 1);
     join<D>(p, p.pair_rows, static_cast<long long>(first) + h, last - first + 1, p.unit_rows, tok * G + g, s, acc);
   }
   const int own = own_tiles(p, b);
   if (own > 0) {
     const int rt = i / p.own_tokens, u = h * p.own_rt + rt;
     const long long a = p.sums[b] + static_cast<long long>(u) * own;
-    const int first = run_of(total, 2 * grid, a), last = run_of(total, 2 * grid, a + own - 1);
+    const int first = run_of(total, lanes, a), last = run_of(total, lanes, a + own - 1);
     const long long unit = static_cast<long long>(b) * p.Hkv * p.own_rt + u + (p.pairs ? 0 : p.Hkv);
     join<D>(p, p.pair_rows, first + unit, last - first + 1, p.unit_rows, (i - rt * p.own_tokens) * G + g, s, acc);
   }
@@ -1219,9 +1027,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __gr
 
 // Units of listed blocks that more than one lane computed.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_lists_kernel(const __grid_constant__ RowsParams p, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_lists_kernel(const __grid_constant__ RowsParams p, int lanes) {
   grid_depends();
-  const int G = p.Hq / p.Hkv, lanes = 2 * grid;
+  const int G = p.Hq / p.Hkv;
   const int units = p.B * p.Nq * p.Hkv, unit_tiles = (p.n_sel + 1) >> 1;
   const int whole = units / lanes * lanes;
   const long long total = static_cast<long long>(units - whole) * unit_tiles;
@@ -1245,35 +1053,46 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_lists_kernel(const __gri
   write_row<D>(p, b * p.Nq + x - h * p.Nq, h * G + g, s, acc);
 }
 
+template <int D, bool kList>
+cudaError_t launch_wide(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
+                        const CUtensorMap& tm_v, int grid, cudaStream_t stream) {
+  using L = Layout<D>;
+  auto kern = rows_kernel<D, kList>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(grid), kThreads, L::kAlloc, stream, tm_q, tm_qs, tm_k, tm_v, p);
+}
+
+// Lane work goes to few_rows_sm103.cu where its units have few rows.
 template <int D>
 cudaError_t launch_d(RowsParams p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
                      const CUtensorMap& tm_v, cudaStream_t stream) {
-  using L = Layout<D>;
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   int grid = n_sm < kRowsCtas ? n_sm : kRowsCtas;
   const int G = p.Hq / p.Hkv;
+  const bool few = p.unit_rows <= kFewRows;
   if (p.blocks) {
     const long long tiles = static_cast<long long>(p.B) * p.Nq * p.Hkv * ((p.n_sel + 1) / 2);
-    if ((tiles + 1) / 2 < grid) grid = static_cast<int>((tiles + 1) / 2);
-    auto kern = rows_kernel<D, true>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), kThreads, L::kAlloc, stream, tm_q, tm_qs, tm_k, tm_v, p);
+    if (tiles < grid) grid = static_cast<int>(tiles);
+    e = few ? launch_few_rows(p, tm_qs, tm_k, tm_v, grid, false, stream)
+            : launch_wide<D, true>(p, tm_q, tm_qs, tm_k, tm_v, grid, stream);
     if (e != cudaSuccess) return e;
-    const int units = p.B * p.Nq * p.Hkv, cut = units - units / (2 * grid) * (2 * grid);
+    const int lanes = few ? grid : 2 * grid;
+    const int units = p.B * p.Nq * p.Hkv, cut = units - units / lanes * lanes;
     if (cut == 0) return e;
     return launch_dependent(join_lists_kernel<D>, dim3((cut * G + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0,
-                            stream, p, grid);
+                            stream, p, lanes);
   }
-  auto kern = rows_kernel<D, false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), kThreads, L::kAlloc, stream, tm_q, tm_qs, tm_k, tm_v, p);
+  p.only_pairs = few ? 1 : 0;
+  if (p.pairs || !few) e = launch_wide<D, false>(p, tm_q, tm_qs, tm_k, tm_v, grid, stream);
+  if (e == cudaSuccess && few) e = launch_few_rows(p, tm_qs, tm_k, tm_v, grid, p.pairs > 0, stream);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.B) * p.Nq * p.Hq;
   return launch_dependent(join_ranges_kernel<D>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
-                          32 * kJoinWarps, 0, stream, p, grid);
+                          32 * kJoinWarps, 0, stream, p, grid, few ? grid : 2 * grid);
 }
 
 }  // namespace
@@ -1309,6 +1128,6 @@ cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUte
                    : launch_d<128>(p, tm_q, tm_qs, tm_k, tm_v, stream);
 }
 
-cudaError_t status_word_rows(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_rows_status); }
+cudaError_t status_word_wide_rows(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_rows_status); }
 
 }  // namespace attn
