@@ -1,4 +1,4 @@
-// Attention of up to 32 query rows that read the same keys, over a paged bf16
+// Attention of up to 16 query rows that read the same keys, over a paged bf16
 // cache, for sm_103a: the new tokens of one sequence with a group's heads, those
 // of a small batch on its shared prefix, or one token's heads on listed blocks.
 //
@@ -18,11 +18,12 @@
 // only where x - M passes 96, on which the four warps vote once a tile.
 //
 // The work is that of the lanes of rows_sm103.cu: an equal run of (unit, key
-// tile) for each CTA, pieces joined by the joining kernels there.  S of the next
-// tile goes out before O of this one, also from piece to piece (scores, P, rows,
-// O^T are held twice).
+// tile) for each CTA, pieces joined by the joining kernels there.  Scores, P,
+// rows and O^T are held twice, so that neither a tile nor a piece waits for the
+// one before to end.
 //
-// Warps: 0 producer, 1 MMA issuer, 2 clears value rows, 4-7 softmax and results.
+// Warps: 0 K loader (and the pieces), 8 V loader, 1 and 3 issuers of the two
+// products, 2 clears value rows, 4-7 softmax and results.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,7 +34,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 288;
 constexpr int kPieces = 4;  // pieces told ahead
 
 struct Piece {
@@ -42,44 +43,48 @@ struct Piece {
   int tok0, ntok;  // first token, tokens
   int key0, keys;  // ranges: position of the first key, keys from there on
   int dst;         // piece number, -1: the result itself
-  int part;        // keys seen of the blocks marked in some[] (lists)
+  int row;         // table row of the keys
+  const int* list;  // lists: the entries, `count` of them; the token sees `seen` keys
+  int count, seen;
+  int part;        // keys seen of the blocks marked in some[]
   uint32_t full[kMaskWords], some[kMaskWords];  // lists: blocks seen whole, seen in part
 };
 
 template <int D, int R>
 struct Layout {
-  static constexpr int kN = R < 16 ? 16 : R;
+  static constexpr int kN = 16;  // the least that M = 128 takes
   static constexpr int kTile = 128 * D * 2;
   // tiles: groups of 8 keys, each with its D / 64 blocks of 8 rows of 128 B
   static constexpr int kGroup = D / 64 * 1024;
-  static constexpr int kSlots = (R == 32 ? 5 : 6) * (128 / D);
+  static constexpr int kKs = 3 * (128 / D), kVs = kKs;  // K and V tiles held
   static constexpr int kQ = kN * D * 2;  // [D / 64][N][128 B]
   static constexpr int kP = kN * 256;    // [2][N][128 B]
-  static constexpr int kOffQ = kSlots * kTile;  // behind the ring: with d = 64 the product's M reads on 1 KB past a tile
+  static constexpr int kOffV = kKs * kTile;
+  static constexpr int kOffQ = kOffV + kVs * kTile;  // behind V: with d = 64 the product's M reads on 1 KB past a tile
   static constexpr int kOffP = kOffQ + 2 * kQ;
   static constexpr int kOffPiece = kOffP + 2 * kP;
   static constexpr int kOffBar = kOffPiece + kPieces * static_cast<int>(sizeof(Piece));
-  static constexpr int kNumBars = 2 * kSlots + 7 * 2 + 2 * kPieces + 3 * 4 + 1;
+  static constexpr int kNumBars = 2 * kKs + 2 * kVs + 7 * 2 + 2 * kPieces + 3 * 4 + 2;
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
-  static constexpr int kOffRed = kOffScan + 8 * 8 + 8 * 4;  // [4][R] floats
+  static constexpr int kOffRed = kOffScan + 9 * 8 + 9 * 4;  // [4][R] floats
   static constexpr int kOffLim = kOffRed + 4 * R * 4;       // [R] ints
   static constexpr int kOffMisc = kOffLim + R * 4;
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
   static constexpr uint32_t kTmem = 4 * kN;     // S^T twice, O^T twice
 };
-static_assert(Layout<128, 4>::kAlloc <= 232448 && Layout<128, 16>::kAlloc <= 232448 && Layout<128, 32>::kAlloc <= 232448 &&
-                  Layout<64, 32>::kAlloc <= 232448 && Layout<64, 16>::kAlloc <= 232448,
-              "shared memory of a CTA");
+static_assert(Layout<128, 16>::kAlloc <= 232448 && Layout<64, 16>::kAlloc <= 232448, "shared memory of a CTA");
 
 template <int D, int R>
 struct Smem {
-  uint8_t *ring, *q, *ps;
+  uint8_t *k, *v, *q, *ps;
   Piece* pieces;
-  uint64_t* full;      // [kSlots] ring slot holds its tile
-  uint64_t* empty;     // [kSlots] ring slot read
+  uint64_t* kfull;     // [kKs] K slot holds its tile
+  uint64_t* kempty;    // [kKs] K slot read
+  uint64_t* vfull;     // [kVs] V slot holds its tile
+  uint64_t* vempty;    // [kVs] V slot read
   uint64_t* sfull;     // [2] scores complete
   uint64_t* pfull;     // [2] P written (4 warps)
   uint64_t* pvdone;    // [2] a tile's P V complete
@@ -88,11 +93,11 @@ struct Smem {
   uint64_t* qfull;     // [2] rows loaded
   uint64_t* qfree;     // [2] a piece's last Q K^T complete
   uint64_t* pieced;    // [kPieces] piece told
-  uint64_t* unpieced;  // [kPieces] piece done with (MMA thread, 4 warps)
+  uint64_t* unpieced;  // [kPieces] piece done with (V loader, issuers, 4 warps)
   uint64_t* fixset;    // [4] clearing asked for
   uint64_t* fixdone;   // [4] done
   uint64_t* raw;       // [4] value tile to be cleared landed
-  uint64_t* drain;     // after an abort: the MMAs issued so far completed
+  uint64_t* drain;     // [2] after an abort: the MMAs that an issuer issued so far completed
   Fix* fixes;
   Plan* plan;
   float* red;
@@ -102,13 +107,16 @@ struct Smem {
   volatile int* gone;  // [2] a softmax warp gave up (by the tile's parity)
   __device__ __forceinline__ explicit Smem(uint8_t* base) {
     using L = Layout<D, R>;
-    ring = base;
+    k = base;
+    v = base + L::kOffV;
     q = base + L::kOffQ;
     ps = base + L::kOffP;
     pieces = reinterpret_cast<Piece*>(base + L::kOffPiece);
-    full = reinterpret_cast<uint64_t*>(base + L::kOffBar);
-    empty = full + L::kSlots;
-    sfull = empty + L::kSlots;
+    kfull = reinterpret_cast<uint64_t*>(base + L::kOffBar);
+    kempty = kfull + L::kKs;
+    vfull = kempty + L::kKs;
+    vempty = vfull + L::kVs;
+    sfull = vempty + L::kVs;
     pfull = sfull + 2;
     pvdone = pfull + 2;
     odone = pvdone + 2;
@@ -132,33 +140,28 @@ struct Smem {
 };
 
 // ---------------------------------------------------------------------------
-// Producer: one warp, whose lanes look up 32 blocks of a piece at a time; lane 0
-// waits and issues.  Ring order of a piece of n tiles: K_0, then K_j, V_{j-1},
-// then V_{n-1}.
-template <int D, int R, bool kList>
-struct Producer {
+// Loaders: a warp for K tiles, which also works out the pieces and loads their
+// rows, and one for V tiles; their lanes look up 32 blocks of a piece at a time,
+// lane 0 waits and issues.  (One warp for both took 770 cycles a tile and operand.)
+template <int D, int R, bool kList, bool kV>
+struct Loader {
   using L = Layout<D, R>;
   const RowsParams& p;
-  const CUtensorMap *tm_q, *tm_k, *tm_v;
+  const CUtensorMap* tm;
   const Smem<D, R>& sm;
   const int lane;
-  RingAt<L::kSlots> at;
-  uint32_t fix_n = 0, told = 0, rows_n = 0;
+  RingAt<kV ? L::kVs : L::kKs> at;
+  uint32_t fix_n = 0, told = 0;
   bool ok = true;  // lane 0's view until `agree`
-  // the CTA's run
-  long long left, unit;      // tiles left (lists: of the cut units); lists: next whole unit
-  int b, hh, rt, t;          // ranges: where it stands
-  // the piece
+  // the piece's keys
   int n, head, key0, end, row;
   const int* list;
   int count, seen;
   int blk, part;
   uint32_t seen_bits, full_bits;
-  bool fin = false;
 
-  __device__ __forceinline__ Producer(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* k, const CUtensorMap* v,
-                                      const Smem<D, R>& sm_, int lane_)
-      : p(p_), tm_q(q), tm_k(k), tm_v(v), sm(sm_), lane(lane_) {}
+  __device__ __forceinline__ Loader(const RowsParams& p_, const CUtensorMap* tm_, const Smem<D, R>& sm_)
+      : p(p_), tm(tm_), sm(sm_), lane(threadIdx.x & 31) {}
 
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
     if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
@@ -191,51 +194,88 @@ struct Producer {
     const uint32_t some = seen_bits & ~full_bits;
     part = some ? __shfl_sync(0xffffffffu, v, __ffs(some) - 1) : 0;  // the same for all of them
   }
-  __device__ __forceinline__ Tile tile(int j) {
+  // tile j of the piece into the next slot
+  __device__ __forceinline__ void load(int j) {
     const int e = 2 * (j & 15);
-    Tile x;
-    x.g0 = __shfl_sync(0xffffffffu, blk, e);
-    x.g1 = __shfl_sync(0xffffffffu, blk, e + 1);
-    x.flags = (seen_bits >> e & 3u) | (full_bits >> e & 3u) << 2;
-    x.part = part;
-    return x;
-  }
-  // a K or V tile into the next ring slot
-  __device__ __forceinline__ void load(const Tile& x, bool is_v) {
+    const int g0 = __shfl_sync(0xffffffffu, blk, e), g1 = __shfl_sync(0xffffffffu, blk, e + 1);
     if (lane != 0) return;
-    if (at.turn > 0) wait(sm.empty + at.slot, at.turn - 1, 11);
+    uint64_t* full = (kV ? sm.vfull : sm.kfull) + at.slot;
+    if (at.turn > 0) wait((kV ? sm.vempty : sm.kempty) + at.slot, at.turn - 1, 11);
     if (!ok) return;
-    uint8_t* dst = sm.ring + at.slot * L::kTile;
-    const CUtensorMap* tm = is_v ? tm_v : tm_k;
-    if (x.flags == 15u) {
-      uint64_t* done = sm.full + at.slot;
-      mbar_arrive_expect_tx(done, L::kTile);
-      tma_load_5d(dst, tm, done, 0, 0, 0, x.g0, head);
-      tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, x.g1, head);
+    uint8_t* dst = (kV ? sm.v : sm.k) + at.slot * L::kTile;
+    const uint32_t s = seen_bits >> e & 3u, f = full_bits >> e & 3u;
+    if (f == 3u) {
+      mbar_arrive_expect_tx(full, L::kTile);
+      tma_load_5d(dst, tm, full, 0, 0, 0, g0, head);
+      tma_load_5d(dst + L::kTile / 2, tm, full, 0, 0, 0, g1, head);
     } else {
-      const bool s0 = x.flags & 1u, s1 = x.flags & 2u;
       const uint32_t fi = fix_n & 3;
-      uint64_t* done = is_v ? sm.raw + fi : sm.full + at.slot;
-      if (is_v) {
+      uint64_t* done = kV ? sm.raw + fi : full;
+      if (kV) {
         if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
         if (!ok) return;
         sm.fixes[fi].slot = static_cast<int>(at.slot);
-        sm.fixes[fi].v0 = x.flags & 4u ? 64 : (s0 ? x.part : 0);
-        sm.fixes[fi].v1 = x.flags & 8u ? 64 : (s1 ? x.part : 0);
+        sm.fixes[fi].v0 = f & 1u ? 64 : (s & 1u ? part : 0);
+        sm.fixes[fi].v1 = f & 2u ? 64 : (s & 2u ? part : 0);
       }
-      if (s0 || s1)
-        mbar_arrive_expect_tx(done, s0 && s1 ? L::kTile : L::kTile / 2);
+      if (s)
+        mbar_arrive_expect_tx(done, s == 3u ? L::kTile : L::kTile / 2);
       else
         mbar_arrive(done);
-      if (s0) tma_load_5d(dst, tm, done, 0, 0, 0, x.g0, head);
-      if (s1) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, x.g1, head);
-      if (is_v) {
+      if (s & 1u) tma_load_5d(dst, tm, done, 0, 0, 0, g0, head);
+      if (s & 2u) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, g1, head);
+      if (kV) {
         mbar_arrive(sm.fixset + fi);
         ++fix_n;
       }
     }
     at.next();
   }
+  // the piece's tiles; its first 32 blocks are looked up
+  __device__ __forceinline__ void load_all() {
+    for (int j = 0; j < n; ++j) {
+      if (j > 0 && (j & 15) == 0) look_up(j >> 4);
+      load(j);
+    }
+  }
+  // Every load lands before the CTA may exit, whatever became of the others (bounded, not abortable).
+  __device__ __forceinline__ void drain() {
+    volatile int no_abort = 0;
+    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
+    for (uint32_t i = 0; i < (kV ? L::kVs : L::kKs); ++i) {
+      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
+      if (turns > 0) mbar_wait((kV ? sm.vfull : sm.kfull) + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
+    }
+  }
+};
+
+template <int D, int R, bool kList>
+struct KeyLoader : Loader<D, R, kList, false> {
+  using Base = Loader<D, R, kList, false>;
+  using L = Layout<D, R>;
+  using Base::p;
+  using Base::sm;
+  using Base::lane;
+  using Base::ok;
+  using Base::told;
+  using Base::n;
+  using Base::head;
+  using Base::key0;
+  using Base::end;
+  using Base::row;
+  using Base::list;
+  using Base::count;
+  using Base::seen;
+  const CUtensorMap* tm_q;
+  uint32_t rows_n = 0;
+  // the CTA's run
+  long long left, unit;  // tiles left (lists: of the cut units); lists: next whole unit
+  int b, hh, rt, t;      // ranges: where it stands
+  bool fin = false;
+
+  __device__ __forceinline__ KeyLoader(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* k, const Smem<D, R>& sm_)
+      : Base(p_, k, sm_), tm_q(q) {}
+
   __device__ __forceinline__ void tell(Piece& d, int n_, int tok0, int ntok, int dst) {
     if (lane == 0 && ok) {
       d.n = n_;
@@ -245,6 +285,10 @@ struct Producer {
       d.key0 = key0;
       d.keys = end - key0;
       d.dst = dst;
+      d.row = row;
+      d.list = list;
+      d.count = count;
+      d.seen = seen;
       mbar_arrive(sm.pieced + told % kPieces);
     }
     ++told;
@@ -253,7 +297,7 @@ struct Producer {
   // Next piece: told, its rows on their way; n = 0 where there is nothing to compute.
   __device__ __forceinline__ void next_piece() {
     const int lanes = gridDim.x, l = blockIdx.x;
-    if (lane == 0 && told >= kPieces) wait(sm.unpieced + told % kPieces, told / kPieces - 1, 13);
+    if (lane == 0 && told >= kPieces) this->wait(sm.unpieced + told % kPieces, told / kPieces - 1, 13);
     Piece& d = sm.pieces[told % kPieces];
     int tok0, ntok, dst;
     n = 0;
@@ -297,13 +341,13 @@ struct Producer {
       // which of them are seen; the last one that is ends the piece
       int last = -1;
       for (int w = (count - 1) >> 5; w >= 0; --w) {  // ends with the first 32 looked up
-        look_up(w);
+        this->look_up(w);
         if (lane == 0 && ok) {
-          d.full[w] = full_bits;
-          d.some[w] = seen_bits & ~full_bits;
-          if (d.some[w]) d.part = part;
+          d.full[w] = this->full_bits;
+          d.some[w] = this->seen_bits & ~this->full_bits;
+          if (d.some[w]) d.part = this->part;
         }
-        if (last < 0 && seen_bits) last = 32 * w + 31 - __clz(seen_bits);
+        if (last < 0 && this->seen_bits) last = 32 * w + 31 - __clz(this->seen_bits);
       }
       n = (last + 2) >> 1;
     } else {
@@ -354,7 +398,7 @@ struct Producer {
     if (n == 0) return;
     if (lane == 0) {
       const uint32_t buf = rows_n & 1;
-      if (rows_n >= 2) wait(sm.qfree + buf, rows_n / 2 - 1, 14);
+      if (rows_n >= 2) this->wait(sm.qfree + buf, rows_n / 2 - 1, 14);
       if (ok) {
         mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(p.unit_tokens * (p.Hq / p.Hkv) * D * 2));
 #pragma unroll
@@ -363,11 +407,13 @@ struct Producer {
         ++rows_n;
       }
     }
-    if (!kList) look_up(0);
+    if (!kList) this->look_up(0);
   }
 
   __device__ __forceinline__ void run() {
     const int lanes = gridDim.x, l = blockIdx.x;
+    list = nullptr;
+    count = seen = head = row = key0 = end = 0;
     if (kList) {
       const int units = p.B * p.Nq * p.Hkv;
       const long long cut = static_cast<long long>(units - units / lanes * lanes) * ((p.n_sel + 1) >> 1);
@@ -386,159 +432,149 @@ struct Producer {
         t = static_cast<int>(x - static_cast<long long>(u) * nt);
       }
     }
-    while (agree()) {
+    while (this->agree()) {
       next_piece();
       if (fin) break;
-      Tile last;
-      for (int j = 0; j <= n && n > 0; ++j) {
-        Tile x;
-        if (j < n) {
-          if (j > 0 && (j & 15) == 0) look_up(j >> 4);
-          x = tile(j);
-          load(x, false);
-        }
-        if (j > 0) load(last, true);
-        last = x;
-      }
+      this->load_all();
     }
     if (lane != 0) return;
-    if (ok) {
-      // no more to clear
-      const uint32_t fi = fix_n & 3;
-      if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
-      if (ok) {
-        sm.fixes[fi].slot = -1;
-        mbar_arrive(sm.fixset + fi);
-      }
-    }
-    // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
     volatile int no_abort = 0;
     for (uint32_t i = 0; i < 2 && i < rows_n; ++i) mbar_wait(sm.qfull + i, (rows_n - 1 - i) / 2 & 1, &no_abort, kWaitLimitNs);
-    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
-    for (uint32_t i = 0; i < L::kSlots; ++i) {
-      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
-      if (turns > 0) mbar_wait(sm.full + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
+    this->drain();
+  }
+};
+
+template <int D, int R, bool kList>
+struct ValueLoader : Loader<D, R, kList, true> {
+  using Base = Loader<D, R, kList, true>;
+  __device__ __forceinline__ ValueLoader(const RowsParams& p_, const CUtensorMap* v, const Smem<D, R>& sm_) : Base(p_, v, sm_) {}
+  __device__ __forceinline__ void run() {
+    for (;; ++this->told) {
+      const uint32_t at = this->told % kPieces;
+      if (this->lane == 0) this->wait(this->sm.pieced + at, this->told / kPieces, 15);
+      if (!this->agree()) break;
+      const volatile Piece& d = this->sm.pieces[at];
+      this->n = d.n;
+      this->head = d.h;
+      this->key0 = d.key0;
+      this->end = d.key0 + d.keys;
+      this->row = d.row;
+      this->list = d.list;
+      this->count = d.count;
+      this->seen = d.seen;
+      __syncwarp();
+      if (this->lane == 0) mbar_arrive(this->sm.unpieced + at);
+      if (this->n < 0) break;
+      if (this->n == 0) continue;
+      this->look_up(0);
+      this->load_all();
     }
+    if (this->lane != 0) return;
+    if (this->ok) {
+      // no more to clear
+      const uint32_t fi = this->fix_n & 3;
+      if (this->fix_n >= 4) this->wait(this->sm.fixdone + fi, this->fix_n / 4 - 1, 12);
+      if (this->ok) {
+        this->sm.fixes[fi].slot = -1;
+        mbar_arrive(this->sm.fixset + fi);
+      }
+    }
+    this->drain();
   }
 };
 
 // ---------------------------------------------------------------------------
-// MMA issuer: one thread.
+// Issuers of the two products, a thread each: their instructions between the
+// products overlap (one thread for both took 2100 cycles a tile, of which the
+// tensor core was busy half).
 template <int D, int R>
 struct Issuer {
   using L = Layout<D, R>;
   static constexpr uint32_t kN = L::kN;
-  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kN, 0);
-  // A runs along M; d = 64: M = 128 takes two 64-dim blocks, of which the second
-  // (the keys behind, whatever lies there) only reaches lanes that nothing reads
-  static constexpr uint32_t kIdescO = idesc_bf16_f32(128, kN, 0) | (1u << 15);
   const Smem<D, R>& sm;
   const uint32_t tmem;
-  uint64_t dK, dV, dQ, dP;
-  uint32_t base = 0, told = 0, piece = 0, ts = 0;  // first ring item of the piece, pieces looked at, with products, tiles
-  int n = 0, j = 0;
-  bool ok = true, fin = false;
-  struct Pv {
-    uint32_t item, tile, piece;
-    bool first, last, on;
-  };
+  uint32_t told = 0, piece = 0, tile = 0;  // pieces looked at, with products (before this one); tiles
+  int n = 0;
+  bool ok = true;
 
-  __device__ __forceinline__ Issuer(const Smem<D, R>& sm_, uint32_t tmem_) : sm(sm_), tmem(tmem_) {
-    dK = sdesc_sw128(smem_u32(sm.ring), 16, L::kGroup);    // K-major
-    dV = sdesc_sw128(smem_u32(sm.ring), 1024, L::kGroup);  // MN-major
-    dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);            // K-major
-    dP = sdesc_sw128(smem_u32(sm.ps), 16, 1024);           // K-major
-  }
+  __device__ __forceinline__ Issuer(const Smem<D, R>& sm_, uint32_t tmem_) : sm(sm_), tmem(tmem_) {}
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
     if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
   }
-  // Moves to the next tile; `block`: waits for its piece.  1: there is one, 0: no more, -1: not told yet.
-  __device__ __forceinline__ int next(bool block) {
-    while (ok && !fin && j == n) {
-      uint64_t* bar = sm.pieced + told % kPieces;
-      if (block)
-        wait(bar, told / kPieces, 24);
-      else if (!mbar_test_wait(bar, told / kPieces & 1))
-        return -1;
-      if (!ok) return 0;
-      const int dn = *const_cast<const volatile int*>(&sm.pieces[told % kPieces].n);
-      mbar_arrive(sm.unpieced + told % kPieces);
-      ++told;
-      if (dn < 0) {
-        fin = true;
-        return 0;
-      }
-      base += 2 * n;
-      n = dn;
-      j = 0;
-      if (n > 0) ++piece;
-    }
-    return ok && !fin ? 1 : 0;
+  // tiles of the next piece, -1: no more
+  __device__ __forceinline__ bool take() {
+    const uint32_t at = told % kPieces;
+    wait(sm.pieced + at, told / kPieces, 24);
+    if (!ok) return false;
+    n = *const_cast<const volatile int*>(&sm.pieces[at].n);
+    mbar_arrive(sm.unpieced + at);
+    ++told;
+    return n >= 0;
   }
-  __device__ __forceinline__ uint32_t k_item() const { return base + (j == 0 ? 0 : 2 * j - 1); }
-  // S of the tile moved to
-  __device__ __forceinline__ void scores(Pv& x) {
-    const uint32_t item = k_item(), slot = item % L::kSlots, buf = (piece - 1) & 1;
-    wait(sm.full + slot, item / L::kSlots, 25);
-    if (j == 0) wait(sm.qfull + buf, (piece - 1) / 2, 26);
-    if (!ok) return;
-    tc_fence_after();
-    const uint64_t a = dK + static_cast<uint64_t>((slot * L::kTile) >> 4), q = dQ + static_cast<uint64_t>((buf * L::kQ) >> 4);
-    const uint32_t to = tmem + (ts & 1) * kN;
+  __device__ __forceinline__ void finish(int which) {
+    if (ok) return;
+    // the MMAs issued so far complete before TMEM is freed
+    volatile int no_abort = 0;
+    mma_commit(sm.drain + which);
+    mbar_wait(sm.drain + which, 0, &no_abort, kWaitLimitNs);
+  }
+
+  __device__ __forceinline__ void scores() {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kN, 0);
+    const uint64_t dK = sdesc_sw128(smem_u32(sm.k), 16, L::kGroup), dQ = sdesc_sw128(smem_u32(sm.q), 16, 1024);
+    RingAt<L::kKs> at;
+    while (take()) {
+      const uint64_t q = dQ + static_cast<uint64_t>(((piece & 1) * L::kQ) >> 4);
+      for (int j = 0; j < n; ++j, ++tile) {
+        if (j == 0) wait(sm.qfull + (piece & 1), piece / 2, 26);
+        // the tile before the last left these scores: it wrote P
+        if (tile >= 2) wait(sm.pfull + (tile & 1), tile / 2 - 1, 27);
+        wait(sm.kfull + at.slot, at.turn, 25);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = dK + static_cast<uint64_t>((at.slot * L::kTile) >> 4);
+        const uint32_t to = tmem + (tile & 1) * kN;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      mma_bf16_ss(to, a + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4),
-                  kIdescS, kk > 0 ? 1u : 0u);
-    mma_commit(sm.sfull + (ts & 1));
-    mma_commit(sm.empty + slot);
-    if (j == n - 1) mma_commit(sm.qfree + buf);
-    x.item = base + (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
-    x.tile = ts++;
-    x.piece = piece - 1;
-    x.first = j == 0;
-    x.last = j == n - 1;
-    x.on = true;
-    ++j;
-  }
-  __device__ __forceinline__ void run() {
-    Pv cur, nxt;
-    nxt.on = false;
-    int have = next(true);
-    if (have == 1) scores(nxt);
-    while (ok && nxt.on) {
-      cur = nxt;
-      nxt.on = false;
-      have = next(false);
-      if (have == 1) {
-        const uint32_t item = k_item();
-        if (mbar_test_wait(sm.full + item % L::kSlots, item / L::kSlots & 1)) scores(nxt);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(to, a + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4),
+                      idesc, kk > 0 ? 1u : 0u);
+        mma_commit(sm.sfull + (tile & 1));
+        mma_commit(sm.kempty + at.slot);
+        at.next();
       }
-      const uint32_t slot = cur.item % L::kSlots, buf = cur.piece & 1;
-      wait(sm.pfull + (cur.tile & 1), cur.tile / 2, 22);
-      wait(sm.full + slot, cur.item / L::kSlots, 21);
-      if (cur.first && cur.piece >= 2) wait(sm.ofree + buf, cur.piece / 2 - 1, 23);
       if (!ok) break;
-      tc_fence_after();
-      const uint64_t a = dV + static_cast<uint64_t>((slot * L::kTile) >> 4),
-                     q = dP + static_cast<uint64_t>(((cur.tile & 1) * L::kP) >> 4);
+      if (n > 0) mma_commit(sm.qfree + (piece++ & 1));
+    }
+    finish(0);
+  }
+  __device__ __forceinline__ void outputs() {
+    // A runs along M; d = 64: M = 128 takes two 64-dim blocks, of which the second
+    // (the keys behind, whatever lies there) only reaches lanes that nothing reads
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kN, 0) | (1u << 15);
+    const uint64_t dV = sdesc_sw128(smem_u32(sm.v), 1024, L::kGroup), dP = sdesc_sw128(smem_u32(sm.ps), 16, 1024);
+    RingAt<L::kVs> at;
+    while (take()) {
+      const uint32_t to = tmem + (2 + (piece & 1)) * kN;
+      for (int j = 0; j < n; ++j, ++tile) {
+        if (j == 0 && piece >= 2) wait(sm.ofree + (piece & 1), piece / 2 - 1, 23);
+        wait(sm.vfull + at.slot, at.turn, 21);
+        wait(sm.pfull + (tile & 1), tile / 2, 22);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = dV + static_cast<uint64_t>((at.slot * L::kTile) >> 4),
+                       q = dP + static_cast<uint64_t>(((tile & 1) * L::kP) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_bf16_ss(tmem + (2 + buf) * kN, a + ((kk * 2 * L::kGroup) >> 4),
-                    q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4), kIdescO, (!cur.first || kk > 0) ? 1u : 0u);
-      mma_commit(sm.empty + slot);
-      mma_commit(sm.pvdone + (cur.tile & 1));
-      if (cur.last) mma_commit(sm.odone + buf);
-      if (!nxt.on) {
-        if (have < 0) have = next(true);
-        if (ok && have == 1) scores(nxt);
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ss(to, a + ((kk * 2 * L::kGroup) >> 4), q + (((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4), idesc,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(sm.pvdone + (tile & 1));
+        mma_commit(sm.vempty + at.slot);
+        at.next();
       }
+      if (!ok) break;
+      if (n > 0) mma_commit(sm.odone + (piece++ & 1));
     }
-    if (!ok) {
-      // the MMAs issued so far complete before TMEM is freed
-      volatile int no_abort = 0;
-      mma_commit(sm.drain);
-      mbar_wait(sm.drain, 0, &no_abort, kWaitLimitNs);
-    }
+    finish(1);
   }
 };
 
@@ -551,9 +587,10 @@ __device__ __forceinline__ void tmem_row(uint32_t addr, float (&x)[R]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
                  : "r"(addr));
+  } else if constexpr (R == 8) {
+    tmem_ld8(addr, u);
   } else {
-#pragma unroll
-    for (int i = 0; i < R; i += 16) tmem_ld16(addr + i, u + i);
+    tmem_ld16(addr, u);
   }
   tmem_wait_ld();
 #pragma unroll
@@ -561,20 +598,42 @@ __device__ __forceinline__ void tmem_row(uint32_t addr, float (&x)[R]) {
 }
 template <int R>
 __device__ __forceinline__ void tmem_put_row(uint32_t addr, const float (&x)[R]) {
-  if constexpr (R == 4) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(__float_as_uint(x[0])),
-                 "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3]))
+#pragma unroll
+  for (int i = 0; i < R; i += 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr + i), "r"(__float_as_uint(x[i])),
+                 "r"(__float_as_uint(x[i + 1])), "r"(__float_as_uint(x[i + 2])), "r"(__float_as_uint(x[i + 3]))
                  : "memory");
-  } else {
+  tmem_wait_st();
+}
+
+// Joins the warp's values of each of R rows (a power of two): by steps that halve
+// the rows a lane holds, then over the lanes of a row.  Lane i returns row
+// row_of(i)'s result.
+template <int R, typename Op>
+__device__ __forceinline__ float over_warp(const float (&x)[R], Op op) {
+  const int lane = threadIdx.x & 31;
+  float v[R];
 #pragma unroll
-    for (int i = 0; i < R; i += 16) {
-      uint32_t u[16];
+  for (int r = 0; r < R; ++r) v[r] = x[r];
+  int o = 16;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(x[i + k]);
-      tmem_st16(addr + i, u);
+  for (int n = R / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int r = 0; r < n; ++r) {
+      const float give = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
+      v[r] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
     }
   }
-  tmem_wait_st();
+#pragma unroll
+  for (; o > 0; o /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+// The row whose result over_warp leaves in this lane: the first step parts the
+// rows by lane bit 4, the next by bit 3, and so on.
+template <int R>
+__device__ __forceinline__ int row_of(int lane) {
+  return lane * R >> 5;
 }
 
 // The four softmax warps meet; true if any thread passes true.
@@ -589,11 +648,6 @@ __device__ __forceinline__ bool group_any(bool x) {
   return r != 0;
 }
 __device__ __forceinline__ void group_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
-__device__ __forceinline__ int ordered_int(float x) {  // larger float, larger integer
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
-}
 
 constexpr float kMoveLog2 = 96.f;  // a row's reference moves where a score passes it by this much
 
@@ -619,11 +673,10 @@ struct Softmax {
   // New references from this tile's largest scores; O^T and the sums so far are
   // brought to them.  s: the scores, scaled; where not `vis` they do not count.
   __device__ __forceinline__ void move(const float (&s)[R], uint32_t vis, bool first) {
+    float x[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int m = __reduce_max_sync(0xffffffffu, ordered_int(vis >> r & 1u ? s[r] : -INFINITY));
-      if (lane == 0) sm.red[w4 * R + r] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
-    }
+    for (int r = 0; r < R; ++r) x[r] = vis >> r & 1u ? s[r] : -INFINITY;
+    sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(x, [](float a, float b) { return fmaxf(a, b); });
     group_sync();
     float f[R];
 #pragma unroll
@@ -701,7 +754,8 @@ struct Softmax {
           move(s, vis, j == 0);
         }
         // p, to its place in the operand: rows of 128 B (64 keys), chunks of 16 B
-        // exchanged by the row
+        // exchanged by the row; the product that read this buffer is done
+        if (ts >= 2) wait(sm.pvdone + (ts & 1), ts / 2 - 1, 45);
         uint8_t* to = sm.ps + (ts & 1) * L::kP + (key >> 6) * (L::kN * 128) + (key & 7) * 2;
         const int ch = (key & 63) >> 3;
 #pragma unroll
@@ -717,12 +771,7 @@ struct Softmax {
         if (lane == 0) mbar_arrive(sm.pfull + (ts & 1));
       }
       // sums of the rows: over a warp's keys, then the four warps
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        if (lane == 0) sm.red[w4 * R + r] = l[r];
-      }
+      sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(l, [](float a, float b) { return a + b; });
       group_sync();
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = (sm.red[r] + sm.red[R + r]) + (sm.red[2 * R + r] + sm.red[3 * R + r]);
@@ -783,9 +832,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(sm.full + i, 1);
-      mbar_init(sm.empty + i, 1);
+    for (int i = 0; i < L::kKs; ++i) {
+      mbar_init(sm.kfull + i, 1);
+      mbar_init(sm.kempty + i, 1);
+    }
+    for (int i = 0; i < L::kVs; ++i) {
+      mbar_init(sm.vfull + i, 1);
+      mbar_init(sm.vempty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.sfull + i, 1);
@@ -799,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(sm.pieced + i, 1);
-      mbar_init(sm.unpieced + i, 5);
+      mbar_init(sm.unpieced + i, 7);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(sm.fixset + i, 1);
@@ -807,6 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(sm.raw + i, 1);
     }
     mbar_init(sm.drain, 1);
+    mbar_init(sm.drain + 1, 1);
     *sm.abort_flag = 0;
     mbar_fence_init();
   }
@@ -818,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!kList)
     make_plan<kThreads / 32, 1>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
-                                reinterpret_cast<int*>(smem + L::kOffScan + 8 * 8));
+                                reinterpret_cast<int*>(smem + L::kOffScan + 9 * 8));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -828,14 +882,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
     }
-    Producer<D, R, kList> producer(p, &tm_q, &tm_k, &tm_v, sm, lane);
-    producer.run();
+    KeyLoader<D, R, kList> loader(p, &tm_q, &tm_k, sm);
+    loader.run();
+  } else if (warp == 8) {
+    if (lane == 0) tma_prefetch_desc(&tm_v);
+    ValueLoader<D, R, kList> loader(p, &tm_v, sm);
+    loader.run();
   } else if (warp == 1) {
     if (lane == 0) {
       Issuer<D, R> issuer(sm, tmem);
-      issuer.run();
+      issuer.scores();
+    }
+  } else if (warp == 3) {
+    if (lane == 0) {
+      Issuer<D, R> issuer(sm, tmem);
+      issuer.outputs();
     }
   } else if (warp == 2) {
     for (uint32_t i = 0;; ++i) {
@@ -844,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = sm.fixes[fi].slot, v0 = sm.fixes[fi].v0, v1 = sm.fixes[fi].v1;
       if (slot < 0) break;
       if (!wait_all(sm.raw + fi, i / 4 & 1, sm.abort_flag, 32)) break;
-      uint8_t* base = sm.ring + slot * L::kTile;
+      uint8_t* base = sm.v + slot * L::kTile;
       for (int half = 0; half < 2; ++half) {
         const int v = half ? v1 : v0;
         for (int c = lane; c < (64 - v) * (D / 8); c += 32) {
@@ -856,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();  // these stores before the tensor core's reads
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(sm.full + slot);
+        mbar_arrive(sm.vfull + slot);
         mbar_arrive(sm.fixdone + fi);
       }
     }
@@ -888,7 +950,7 @@ template <int D>
 cudaError_t launch_d(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                      int grid, bool after_pairs, cudaStream_t stream) {
   if (p.unit_rows <= 4) return launch_r<D, 4>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
-  if (p.unit_rows <= 16) return launch_r<D, 16>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+  if (p.unit_rows <= 8) return launch_r<D, 8>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
   return launch_r<D, kFewRows>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
 }
 
