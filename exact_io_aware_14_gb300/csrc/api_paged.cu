@@ -91,10 +91,11 @@ attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pa
   return ATTN_OK;
 }
 
-size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
+size_t round32(size_t x) { return (x + 31) & ~size_t(31); }
 size_t rows_workspace(const attn::RowsSizes& z, int B, int d, bool lists) {
   const size_t rows = static_cast<size_t>(z.pair_rows + z.lane_pieces * z.unit_rows);
-  return round16(lists ? 0 : (static_cast<size_t>(B) + 3) * sizeof(long long)) + rows * (d + 1) * sizeof(float);
+  // rows of pieces start at a multiple of 32 bytes, wherever the workspace does
+  return 16 + round32(lists ? 0 : (static_cast<size_t>(B) + 3) * sizeof(long long)) + rows * (d + 1) * sizeof(float);
 }
 
 // Both attention calls, behind their checks.  blocks: listed ones, or null.
@@ -130,10 +131,10 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
   p.unit_tokens = z.unit_tokens;
   p.unit_rows = z.unit_rows;
   p.pair_rows = z.pair_rows;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = reinterpret_cast<char*>(round32(reinterpret_cast<uintptr_t>(workspace)));
   if (!blocks) {
     p.sums = reinterpret_cast<long long*>(ws);
-    ws += round16((static_cast<size_t>(B) + 3) * sizeof(long long));
+    ws += round32((static_cast<size_t>(B) + 3) * sizeof(long long));
   }
   p.o_part = reinterpret_cast<float*>(ws);
   p.lse_part = p.o_part + static_cast<size_t>(z.pair_rows + z.lane_pieces * z.unit_rows) * d;

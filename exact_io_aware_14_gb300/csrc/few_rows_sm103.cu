@@ -42,6 +42,7 @@ struct Piece {
   int h;           // KV head
   int tok0, ntok;  // first token, tokens
   int key0, keys;  // ranges: position of the first key, keys from there on
+  int all;         // ranges: every row sees all of them
   int dst;         // piece number, -1: the result itself
   int row;         // table row of the keys
   const int* list;  // lists: the entries, `count` of them; the token sees `seen` keys
@@ -68,8 +69,9 @@ struct Layout {
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
-  static constexpr int kOffRed = kOffScan + 9 * 8 + 9 * 4;  // [4][R] floats
-  static constexpr int kOffLim = kOffRed + 4 * R * 4;       // [R] ints
+  static constexpr int kOffRed = kOffScan + 9 * 8 + 2 * 9 * 4;  // [4][R] floats
+  static constexpr int kOffRow = kOffRed + 4 * R * 4;           // [2][R] floats
+  static constexpr int kOffLim = kOffRow + 2 * R * 4;           // [R] ints
   static constexpr int kOffMisc = kOffLim + R * 4;
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
@@ -100,8 +102,9 @@ struct Smem {
   uint64_t* drain;     // [2] after an abort: the MMAs that an issuer issued so far completed
   Fix* fixes;
   Plan* plan;
-  float* red;
-  int* lim;
+  float* red;  // [4][R] of the softmax warps
+  float* row;  // [2][R] of the rows
+  int* lim;    // [R] keys of the piece that a row sees
   uint32_t* tmem_slot;
   volatile int* abort_flag;
   volatile int* gone;  // [2] a softmax warp gave up (by the tile's parity)
@@ -132,6 +135,7 @@ struct Smem {
     fixes = reinterpret_cast<Fix*>(base + L::kOffFix);
     plan = reinterpret_cast<Plan*>(base + L::kOffPlan);
     red = reinterpret_cast<float*>(base + L::kOffRed);
+    row = reinterpret_cast<float*>(base + L::kOffRow);
     lim = reinterpret_cast<int*>(base + L::kOffLim);
     tmem_slot = reinterpret_cast<uint32_t*>(base + L::kOffMisc);
     abort_flag = reinterpret_cast<volatile int*>(base + L::kOffMisc + 4);
@@ -272,6 +276,7 @@ struct KeyLoader : Loader<D, R, kList, false> {
   long long left, unit;  // tiles left (lists: of the cut units); lists: next whole unit
   int b, hh, rt, t;      // ranges: where it stands
   bool fin = false;
+  int all = 0;
 
   __device__ __forceinline__ KeyLoader(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* k, const Smem<D, R>& sm_)
       : Base(p_, k, sm_), tm_q(q) {}
@@ -284,6 +289,7 @@ struct KeyLoader : Loader<D, R, kList, false> {
       d.ntok = ntok;
       d.key0 = key0;
       d.keys = end - key0;
+      d.all = all;
       d.dst = dst;
       d.row = row;
       d.list = list;
@@ -365,6 +371,7 @@ struct KeyLoader : Loader<D, R, kList, false> {
         key0 = 128 * t;
         row = 0;
         nt = tiles_of(end);
+        all = sm.plan->all_see >= end;
         rts = 1;
         u = hh;
         tok0 = 0;
@@ -374,6 +381,7 @@ struct KeyLoader : Loader<D, R, kList, false> {
         key0 = p.shared_len + 128 * t;
         row = b;
         nt = tiles_of(len - p.shared_len);
+        all = p.Nq == 1;
         rts = p.own_rt;
         u = (b * p.Hkv + hh) * rts + rt + (p.pairs ? 0 : p.Hkv);
         tok0 = b * p.Nq + rt * p.own_tokens;
@@ -678,16 +686,17 @@ struct Softmax {
     for (int r = 0; r < R; ++r) x[r] = vis >> r & 1u ? s[r] : -INFINITY;
     sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(x, [](float a, float b) { return fmaxf(a, b); });
     group_sync();
-    float f[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float mx = fmaxf(fmaxf(sm.red[r], sm.red[R + r]), fmaxf(sm.red[2 * R + r], sm.red[3 * R + r]));
-      const float m = M[r] == -INFINITY || mx - M[r] > 8.f ? fmaxf(M[r], mx) : M[r];
-      f[r] = M[r] == m ? 1.f : ex2_approx(M[r] - m);  // 0 where nothing was seen
-      M[r] = m;
-      l[r] *= f[r];
+    // a thread a row: its new reference and the factor of what there is (0 where nothing was seen)
+    if (key < R) {
+      const float mx = fmaxf(fmaxf(sm.red[key], sm.red[R + key]), fmaxf(sm.red[2 * R + key], sm.red[3 * R + key]));
+      const float was = first ? -INFINITY : sm.row[key];
+      const float m = was == -INFINITY || mx - was > 8.f ? fmaxf(was, mx) : was;
+      sm.row[key] = m;
+      sm.row[R + key] = was == m ? 1.f : ex2_approx(was - m);
     }
-    group_sync();  // red is read
+    group_sync();
+#pragma unroll
+    for (int r = 0; r < R; ++r) M[r] = sm.row[r];
     if (first) return;
     wait(sm.pvdone + ((ts - 1) & 1), (ts - 1) / 2, 44);
     tc_fence_after();
@@ -695,8 +704,13 @@ struct Softmax {
     const uint32_t at = tmem + (2 + (piece & 1)) * L::kN;
     tmem_row<R>(at, o);
 #pragma unroll
-    for (int r = 0; r < R; ++r) o[r] *= f[r];
+    for (int r = 0; r < R; ++r) {
+      const float f = sm.row[R + r];
+      o[r] *= f;
+      l[r] *= f;
+    }
     tmem_put_row<R>(at, o);
+    group_sync();  // the factors are read
   }
 
   __device__ __forceinline__ void run() {
@@ -709,18 +723,23 @@ struct Softmax {
       if (n < 0) return;
       const int rows = ntok * G;
       int whole = 0;  // ranges: keys that all rows see
+      const bool all = kList || d.all;
       if (!kList) {
-        int lim = 0x7fffffff;
-        if (key < rows) {
-          const int tok = tok0 + key / G, b = tok / p.Nq;
-          lim = min(d.keys, clamped_len(p, b) - p.Nq + tok - b * p.Nq + 1 - d.key0);
-          sm.lim[key] = lim;
+        whole = d.keys;
+        if (!all) {
+          int lim = 0x7fffffff;
+          if (key < rows) {
+            const int tok = tok0 + key / G, b = tok / p.Nq;
+            lim = min(whole, clamped_len(p, b) - p.Nq + tok - b * p.Nq + 1 - d.key0);
+            sm.lim[key] = lim;
+          }
+          const int m = __reduce_min_sync(0xffffffffu, lim);
+          if (lane == 0) sm.red[w4] = __int_as_float(m);
+          group_sync();
+          whole = min(min(__float_as_int(sm.red[0]), __float_as_int(sm.red[1])),
+                      min(__float_as_int(sm.red[2]), __float_as_int(sm.red[3])));
+          group_sync();
         }
-        const int m = __reduce_min_sync(0xffffffffu, lim);
-        if (lane == 0) sm.red[w4] = __int_as_float(m);
-        group_sync();
-        whole = min(min(__float_as_int(sm.red[0]), __float_as_int(sm.red[1])), min(__float_as_int(sm.red[2]), __float_as_int(sm.red[3])));
-        group_sync();
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -738,9 +757,13 @@ struct Softmax {
           const int v = d.full[e >> 5] >> (e & 31) & 1u ? 64 : (d.some[e >> 5] >> (e & 31) & 1u ? d.part : 0);
           if ((key & 63) >= v) vis = 0;
         } else if (128 * (j + 1) > whole) {
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (r < rows && 128 * j + key >= sm.lim[r]) vis &= ~(1u << r);
+          if (all) {
+            if (128 * j + key >= whole) vis = 0;
+          } else {
+#pragma unroll 1
+            for (int r = 0; r < rows; ++r)
+              if (128 * j + key >= sm.lim[r]) vis &= ~(1u << r);
+          }
         }
         bool over = j == 0;
 #pragma unroll
@@ -773,8 +796,18 @@ struct Softmax {
       // sums of the rows: over a warp's keys, then the four warps
       sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(l, [](float a, float b) { return a + b; });
       group_sync();
-#pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = (sm.red[r] + sm.red[R + r]) + (sm.red[2 * R + r] + sm.red[3 * R + r]);
+      // a thread a row: the factor of its outputs and its log-sum-exp; l is 0 where nothing was seen, NaN stays NaN
+      if (key < rows) {
+        const float sum = (sm.red[key] + sm.red[R + key]) + (sm.red[2 * R + key] + sm.red[3 * R + key]);
+        const float lse2 = sum == 0.f ? -INFINITY : sm.row[key] + __log2f(sum);
+        sm.row[R + key] = sum == 0.f ? 0.f : 1.f / sum;
+        if (dst >= 0) {
+          p.lse_part[p.pair_rows + static_cast<long long>(dst) * p.unit_rows + key] = lse2;
+        } else {
+          const int tok = tok0 + key / G, b = tok / p.Nq;
+          p.lse[(static_cast<long long>(b) * p.Hq + h * G + key % G) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
+        }
+      }
       group_sync();
       float o[R];
       if (n > 0) {
@@ -786,29 +819,30 @@ struct Softmax {
         if (lane == 0) mbar_arrive(sm.ofree + (piece & 1));
         ++piece;
       }
-      // l is 0 where nothing was seen; NaN stays NaN
-      int tok = tok0, g = 0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= rows) break;
-        const float v = l[r] == 0.f ? 0.f : o[r] * (1.f / l[r]);
-        const float lse2 = l[r] == 0.f ? -INFINITY : M[r] + __log2f(l[r]);
+        const float f = sm.row[R + r];
+        o[r] = n > 0 && f != 0.f ? o[r] * f : 0.f;
+      }
+      if (key < D) {
         if (dst >= 0) {
-          const long long at = p.pair_rows + static_cast<long long>(dst) * p.unit_rows + r;
-          if (key < D) p.o_part[at * D + key] = v;
-          if (key == 0) p.lse_part[at] = lse2;
+          float* to = p.o_part + (p.pair_rows + static_cast<long long>(dst) * p.unit_rows) * D + key;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (r < rows) to[r * D] = o[r];
         } else {
-          const int hq = h * G + g;
-          if (key < D)
-            static_cast<__nv_bfloat16*>(p.o)[(static_cast<long long>(tok) * p.Hq + hq) * D + key] = __float2bfloat16_rn(v);
-          if (key == 0) {
-            const int b = tok / p.Nq;
-            p.lse[(static_cast<long long>(b) * p.Hq + hq) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(tok0) * p.Hq + h * G) * D + key;
+          int g = 0;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (r >= rows) break;
+            *to = __float2bfloat16_rn(o[r]);
+            to += D;
+            if (++g == G) {  // the next token's heads of the group
+              g = 0;
+              to += static_cast<long long>(p.Hq - G) * D;
+            }
           }
-        }
-        if (++g == G) {
-          g = 0;
-          ++tok;
         }
       }
       __syncwarp();

@@ -31,6 +31,7 @@ struct Plan {
   int lane_b[2];         // sequence at which the lanes start (-1: the prefix)
   long long total, pair_total;
   int prefix_end;        // keys of the prefix that any sequence has
+  int all_see;           // keys that every row sees
 };
 
 // Bounded waits: one probe in line, the rest out of line, as the warps' code
@@ -58,13 +59,17 @@ __device__ __forceinline__ int own_tiles(const RowsParams& p, int b) {
 }
 // `total` tiles dealt to `lanes` in runs of equal length, none of them empty but
 // the last ones: where run i starts, and which run holds tile x.
-__device__ __noinline__ long long run_start(long long total, int lanes, int i) {
-  const long long runs = min(total, static_cast<long long>(lanes));
-  return i < runs ? total * i / runs : total;
+__device__ __noinline__ long long quotient(long long a, long long b) {  // a >= 0, b > 0; 64-bit divisions only where needed
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
-__device__ __noinline__ int run_of(long long total, int lanes, long long x) {
+__device__ __forceinline__ long long run_start(long long total, int lanes, int i) {
   const long long runs = min(total, static_cast<long long>(lanes));
-  return static_cast<int>(((x + 1) * runs - 1) / total);
+  return i < runs ? quotient(total * i, runs) : total;
+}
+__device__ __forceinline__ int run_of(long long total, int lanes, long long x) {
+  const long long runs = min(total, static_cast<long long>(lanes));
+  return static_cast<int>(quotient((x + 1) * runs - 1, total));
 }
 
 // Lanes' starts for ranges: sums of the sequences' tiles, by all threads of the
@@ -76,24 +81,29 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
   constexpr int kThreads = 32 * kWarps;
   const int per = p.Hkv * p.own_rt;  // units of a sequence
   long long sum = 0;
-  int longest = 0;
+  int longest = 0, shortest = 0x7fffffff;
   for (int b = tid; b < p.B; b += kThreads) {
     sum += static_cast<long long>(own_tiles(p, b)) * per;
-    longest = max(longest, clamped_len(p, b));
+    const int len = clamped_len(p, b);
+    longest = max(longest, len);
+    shortest = min(shortest, len);
     if (blockIdx.x == 0 && (p.seqlens[b] < 0 || p.seqlens[b] > p.max_blocks * p.page_size)) record(1, kDevBadSeqlen);
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
+  shortest = __reduce_min_sync(0xffffffffu, shortest);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) {
     s_sum[warp] = sum;
     s_max[warp] = longest;
+    s_max[kWarps + warp] = shortest;
   }
   __syncthreads();
   sum = 0;
   for (int w = 0; w < kWarps; ++w) {
     sum += s_sum[w];
     longest = max(longest, s_max[w]);
+    shortest = min(shortest, s_max[kWarps + w]);
   }
   const int end = min(p.shared_len, longest);
   const long long prefix = static_cast<long long>(tiles_of(end)) * p.Hkv;
@@ -101,6 +111,7 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
   const long long total = solo + sum;
   if (tid == 0) {
     plan->prefix_end = end;
+    plan->all_see = max(0, shortest - p.Nq + 1);
     plan->total = total;
     plan->pair_total = p.pairs ? prefix * p.pairs : 0;
   }

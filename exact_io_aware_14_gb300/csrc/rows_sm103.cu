@@ -69,7 +69,7 @@ struct Layout {
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
-  static constexpr int kOffMisc = kOffScan + 12 * 8 + 12 * 4;
+  static constexpr int kOffMisc = kOffScan + 12 * 8 + 2 * 12 * 4;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
 };
@@ -879,9 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x) w[x] = n > 0 && l != 0.f ? __float_as_uint(__uint_as_float(w[x]) * inv) : 0u;
             if (live) {
               if (dst >= 0) {
-                uint4* to = reinterpret_cast<uint4*>(part + cc * 32);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) to[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                for (int x = 0; x < 4; ++x) st_global_v8(part + cc * 32 + 8 * x, w + 8 * x);  // whole sectors
               } else {
                 uint4* to = reinterpret_cast<uint4*>(orow + cc * 32);
 #pragma unroll
@@ -931,16 +930,17 @@ constexpr int kJoinWarps = 4;
 struct Join {
   float m, l;
 };
-// Adds pieces first .. first + n - 1 (rows `row` of `rows` each, from `base` on) to a row's sums, which are kept
-// under the largest LSE so far.
-template <int D>
-__device__ __forceinline__ void join(const RowsParams& p, long long base, long long first, int n, int rows, int row,
-                                     Join& s, float (&acc)[D / 32]) {
+// A row's pieces, `count` of them: `place(i)` is the row of piece i in the
+// workspace.  32 at a time, a lane a piece for the weights; the outputs are on
+// their way meanwhile.
+template <int D, typename Place>
+__device__ __forceinline__ void join(const RowsParams& p, int count, Place place, Join& s, float (&acc)[D / 32]) {
+  constexpr int kV = D / 32;
   const int lane = threadIdx.x & 31;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int cnt = min(32, n - i0);
-    const long long at = base + (first + i0) * rows + row;
-    const float mine = lane < cnt ? p.lse_part[at + static_cast<long long>(lane) * rows] : -INFINITY;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int n = min(32, count - i0);
+    const long long at = lane < n ? place(i0 + lane) : 0;
+    const float mine = lane < n ? p.lse_part[at] : -INFINITY;
     float m = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -951,22 +951,27 @@ __device__ __forceinline__ void join(const RowsParams& p, long long base, long l
     s.m = m;
     s.l *= a;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) acc[x] *= a;
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* o = p.o_part + (at + static_cast<long long>(i) * rows) * D + lane * (D / 32);
-      s.l += wi;
-      if (D == 128) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(wi, v.x, acc[0]);
-        acc[1] = fmaf(wi, v.y, acc[1]);
-        acc[D / 32 - 2] = fmaf(wi, v.z, acc[D / 32 - 2]);
-        acc[D / 32 - 1] = fmaf(wi, v.w, acc[D / 32 - 1]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(wi, v.x, acc[0]);
-        acc[1] = fmaf(wi, v.y, acc[1]);
+    for (int x = 0; x < kV; ++x) acc[x] *= a;
+    for (int i = 0; i < n; i += 4) {
+      float v[4][kV];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* o = p.o_part + __shfl_sync(0xffffffffu, at, (i + k) & 31) * D + lane * kV;
+        if (i + k < n) {
+          if constexpr (kV == 4)
+            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(o);
+          else
+            *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(o);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float wi = __shfl_sync(0xffffffffu, w, (i + k) & 31);
+        if (i + k < n) {
+          s.l += wi;
+#pragma unroll
+          for (int x = 0; x < kV; ++x) acc[x] = fmaf(wi, v[k][x], acc[x]);
+        }
       }
     }
   }
@@ -1001,27 +1006,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __gr
   float acc[D / 32];
 #pragma unroll
   for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
-  if (p.pairs) {
-    if (nt > 0) {
-      const int rt = tok / p.tile_tokens, unit = h * p.pairs + (rt >> 1);
-      const long long a = static_cast<long long>(unit) * nt;
-      const int first = run_of(pair_total, grid, a), last = run_of(pair_total, grid, a + nt - 1);
-      join<D>(p, 0, static_cast<long long>(first) + unit, last - first + 1, 256,
-              (rt & 1) * 128 + (tok - rt * p.tile_tokens) * G + g, s, acc);
-    }
-  } else if (nt > 0) {
-    const long long a = static_cast<long long>(h) * nt;
-    const int first = run_of(total, lanes, a), last = run_of(total, lanes, a + nt - 1);
-    join<D>(p, p.pair_rows, static_cast<long long>(first) + h, last - first + 1, p.unit_rows, tok * G + g, s, acc);
+  // pieces of the prefix, then of the sequence's own keys: place = base + (number) * rows
+  long long base0 = 0, base1 = 0;
+  int n0 = 0, n1 = 0, rows0 = 256;
+  if (nt > 0) {
+    const int rt = tok / p.tile_tokens;
+    const int unit = p.pairs ? h * p.pairs + (rt >> 1) : h;
+    const long long a = static_cast<long long>(unit) * nt, all = p.pairs ? pair_total : total;
+    const int runs = p.pairs ? grid : lanes, first = run_of(all, runs, a);
+    n0 = run_of(all, runs, a + nt - 1) - first + 1;
+    if (!p.pairs) rows0 = p.unit_rows;
+    base0 = p.pairs ? (static_cast<long long>(first) + unit) * 256 + (rt & 1) * 128 + (tok - rt * p.tile_tokens) * G + g
+                    : p.pair_rows + (static_cast<long long>(first) + unit) * p.unit_rows + tok * G + g;
   }
   const int own = own_tiles(p, b);
   if (own > 0) {
     const int rt = i / p.own_tokens, u = h * p.own_rt + rt;
     const long long a = p.sums[b] + static_cast<long long>(u) * own;
-    const int first = run_of(total, lanes, a), last = run_of(total, lanes, a + own - 1);
+    const int first = run_of(total, lanes, a);
+    n1 = run_of(total, lanes, a + own - 1) - first + 1;
     const long long unit = static_cast<long long>(b) * p.Hkv * p.own_rt + u + (p.pairs ? 0 : p.Hkv);
-    join<D>(p, p.pair_rows, first + unit, last - first + 1, p.unit_rows, (i - rt * p.own_tokens) * G + g, s, acc);
+    base1 = p.pair_rows + (first + unit) * p.unit_rows + (i - rt * p.own_tokens) * G + g;
   }
+  join<D>(p, n0 + n1,
+          [&](int x) {
+            return x < n0 ? base0 + static_cast<long long>(x) * rows0 : base1 + static_cast<long long>(x - n0) * p.unit_rows;
+          },
+          s, acc);
   write_row<D>(p, tok, hq, s, acc);
 }
 
@@ -1043,11 +1054,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_lists_kernel(const __gri
   float acc[D / 32];
 #pragma unroll
   for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
-  // a lane's first piece, unless it started in the unit before
+  // place 2 lane, or 2 lane + 1 where the lane started in the unit before
   const int second = run_start(total, lanes, first) < a ? 1 : 0;
-  join<D>(p, 0, 2ll * first + second, 1, p.unit_rows, g, s, acc);
-  // its place is 2 lane: every second piece from the next lane on
-  for (int l = first + 1; l <= last; ++l) join<D>(p, 0, 2ll * l, 1, p.unit_rows, g, s, acc);
+  join<D>(p, last - first + 1,
+          [&](int x) { return static_cast<long long>(2 * (first + x) + (x == 0 ? second : 0)) * p.unit_rows + g; }, s, acc);
   const int per = p.Hkv * p.Nq, u = whole + cu;
   const int b = u / per, x = u - b * per, h = x / p.Nq;
   write_row<D>(p, b * p.Nq + x - h * p.Nq, h * G + g, s, acc);
