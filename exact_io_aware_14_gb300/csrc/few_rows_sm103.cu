@@ -22,8 +22,8 @@
 // rows and O^T are held twice, so that neither a tile nor a piece waits for the
 // one before to end.
 //
-// Warps: 0 K loader (and the pieces), 8 V loader, 1 and 3 issuers of the two
-// products, 2 clears value rows, 4-7 softmax and results.
+// Warps: 9 planner (pieces and their pages), 0 and 8 loaders of K and V, 1 and 3
+// issuers of the two products, 2 clears value rows, 4-7 softmax and results.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +34,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr int kPieces = 4;  // pieces told ahead
 
 struct Piece {
@@ -49,6 +49,7 @@ struct Piece {
   int count, seen;
   int part;        // keys seen of the blocks marked in some[]
   uint32_t full[kMaskWords], some[kMaskWords];  // lists: blocks seen whole, seen in part
+  int group[32];   // the first 32 blocks, as groups of 8 keys of the pool
 };
 
 template <int D, int R>
@@ -69,9 +70,9 @@ struct Layout {
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
-  static constexpr int kOffRed = kOffScan + 9 * 8 + 2 * 9 * 4;  // [4][R] floats
-  static constexpr int kOffRow = kOffRed + 4 * R * 4;           // [2][R] floats
-  static constexpr int kOffLim = kOffRow + 2 * R * 4;           // [R] ints
+  static constexpr int kOffRed = kOffScan + 10 * 8 + 2 * 10 * 4;  // [4][R] floats
+  static constexpr int kOffRow = kOffRed + 4 * R * 4;           // [3][R] floats
+  static constexpr int kOffLim = kOffRow + 3 * R * 4;           // [R] ints
   static constexpr int kOffMisc = kOffLim + R * 4;
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
@@ -95,7 +96,7 @@ struct Smem {
   uint64_t* qfull;     // [2] rows loaded
   uint64_t* qfree;     // [2] a piece's last Q K^T complete
   uint64_t* pieced;    // [kPieces] piece told
-  uint64_t* unpieced;  // [kPieces] piece done with (V loader, issuers, 4 warps)
+  uint64_t* unpieced;  // [kPieces] piece done with (loaders, issuers, 4 softmax warps)
   uint64_t* fixset;    // [4] clearing asked for
   uint64_t* fixdone;   // [4] done
   uint64_t* raw;       // [4] value tile to be cleared landed
@@ -103,7 +104,7 @@ struct Smem {
   Fix* fixes;
   Plan* plan;
   float* red;  // [4][R] of the softmax warps
-  float* row;  // [2][R] of the rows
+  float* row;  // [R] references, [2][R] factors of the rows
   int* lim;    // [R] keys of the piece that a row sees
   uint32_t* tmem_slot;
   volatile int* abort_flag;
@@ -144,237 +145,103 @@ struct Smem {
 };
 
 // ---------------------------------------------------------------------------
-// Loaders: a warp for K tiles, which also works out the pieces and loads their
-// rows, and one for V tiles; their lanes look up 32 blocks of a piece at a time,
-// lane 0 waits and issues.  (One warp for both took 770 cycles a tile and operand.)
-template <int D, int R, bool kList, bool kV>
-struct Loader {
-  using L = Layout<D, R>;
+// Planner: a warp that works out the pieces, up to kPieces ahead, with their first
+// 32 blocks looked up in the table (a lane each), so that the loaders have no
+// chain of loads of their own between two pieces.
+template <int D, int R, bool kList>
+struct Planner {
   const RowsParams& p;
-  const CUtensorMap* tm;
   const Smem<D, R>& sm;
   const int lane;
-  RingAt<kV ? L::kVs : L::kKs> at;
-  uint32_t fix_n = 0, told = 0;
-  bool ok = true;  // lane 0's view until `agree`
-  // the piece's keys
-  int n, head, key0, end, row;
-  const int* list;
-  int count, seen;
-  int blk, part;
-  uint32_t seen_bits, full_bits;
-
-  __device__ __forceinline__ Loader(const RowsParams& p_, const CUtensorMap* tm_, const Smem<D, R>& sm_)
-      : p(p_), tm(tm_), sm(sm_), lane(threadIdx.x & 31) {}
-
-  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
-    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
-  }
-  __device__ __forceinline__ bool agree() {
-    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
-    return ok;
-  }
-  // blocks 32 i .. 32 i + 31 of the piece
-  __device__ __forceinline__ void look_up(int i) {
-    int v = 0, bl;
-    if (kList) {
-      const int e = 32 * i + lane;
-      bl = e < count ? list[e] : -1;
-      if (bl >= 0) {
-        if (bl >= p.max_blocks * (p.page_size / 64))
-          record(3, kDevBadPage);
-        else
-          v = min(64, seen - bl * 64);
-      }
-    } else {
-      const int key = key0 + 64 * (32 * i + lane);
-      v = min(64, end - key);
-      bl = key >> 6;
-    }
-    blk = 0;
-    if (v > 0) blk = pool_group(p, row, bl);
-    seen_bits = __ballot_sync(0xffffffffu, v > 0);
-    full_bits = __ballot_sync(0xffffffffu, v == 64);
-    const uint32_t some = seen_bits & ~full_bits;
-    part = some ? __shfl_sync(0xffffffffu, v, __ffs(some) - 1) : 0;  // the same for all of them
-  }
-  // tile j of the piece into the next slot
-  __device__ __forceinline__ void load(int j) {
-    const int e = 2 * (j & 15);
-    const int g0 = __shfl_sync(0xffffffffu, blk, e), g1 = __shfl_sync(0xffffffffu, blk, e + 1);
-    if (lane != 0) return;
-    uint64_t* full = (kV ? sm.vfull : sm.kfull) + at.slot;
-    if (at.turn > 0) wait((kV ? sm.vempty : sm.kempty) + at.slot, at.turn - 1, 11);
-    if (!ok) return;
-    uint8_t* dst = (kV ? sm.v : sm.k) + at.slot * L::kTile;
-    const uint32_t s = seen_bits >> e & 3u, f = full_bits >> e & 3u;
-    if (f == 3u) {
-      mbar_arrive_expect_tx(full, L::kTile);
-      tma_load_5d(dst, tm, full, 0, 0, 0, g0, head);
-      tma_load_5d(dst + L::kTile / 2, tm, full, 0, 0, 0, g1, head);
-    } else {
-      const uint32_t fi = fix_n & 3;
-      uint64_t* done = kV ? sm.raw + fi : full;
-      if (kV) {
-        if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
-        if (!ok) return;
-        sm.fixes[fi].slot = static_cast<int>(at.slot);
-        sm.fixes[fi].v0 = f & 1u ? 64 : (s & 1u ? part : 0);
-        sm.fixes[fi].v1 = f & 2u ? 64 : (s & 2u ? part : 0);
-      }
-      if (s)
-        mbar_arrive_expect_tx(done, s == 3u ? L::kTile : L::kTile / 2);
-      else
-        mbar_arrive(done);
-      if (s & 1u) tma_load_5d(dst, tm, done, 0, 0, 0, g0, head);
-      if (s & 2u) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, g1, head);
-      if (kV) {
-        mbar_arrive(sm.fixset + fi);
-        ++fix_n;
-      }
-    }
-    at.next();
-  }
-  // the piece's tiles; its first 32 blocks are looked up
-  __device__ __forceinline__ void load_all() {
-    for (int j = 0; j < n; ++j) {
-      if (j > 0 && (j & 15) == 0) look_up(j >> 4);
-      load(j);
-    }
-  }
-  // Every load lands before the CTA may exit, whatever became of the others (bounded, not abortable).
-  __device__ __forceinline__ void drain() {
-    volatile int no_abort = 0;
-    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
-    for (uint32_t i = 0; i < (kV ? L::kVs : L::kKs); ++i) {
-      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
-      if (turns > 0) mbar_wait((kV ? sm.vfull : sm.kfull) + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
-    }
-  }
-};
-
-template <int D, int R, bool kList>
-struct KeyLoader : Loader<D, R, kList, false> {
-  using Base = Loader<D, R, kList, false>;
-  using L = Layout<D, R>;
-  using Base::p;
-  using Base::sm;
-  using Base::lane;
-  using Base::ok;
-  using Base::told;
-  using Base::n;
-  using Base::head;
-  using Base::key0;
-  using Base::end;
-  using Base::row;
-  using Base::list;
-  using Base::count;
-  using Base::seen;
-  const CUtensorMap* tm_q;
-  uint32_t rows_n = 0;
+  uint32_t told = 0;
+  bool ok = true;
   // the CTA's run
   long long left, unit;  // tiles left (lists: of the cut units); lists: next whole unit
   int b, hh, rt, t;      // ranges: where it stands
-  bool fin = false;
-  int all = 0;
 
-  __device__ __forceinline__ KeyLoader(const RowsParams& p_, const CUtensorMap* q, const CUtensorMap* k, const Smem<D, R>& sm_)
-      : Base(p_, k, sm_), tm_q(q) {}
+  __device__ __forceinline__ Planner(const RowsParams& p_, const Smem<D, R>& sm_) : p(p_), sm(sm_), lane(threadIdx.x & 31) {}
 
-  __device__ __forceinline__ void tell(Piece& d, int n_, int tok0, int ntok, int dst) {
-    if (lane == 0 && ok) {
-      d.n = n_;
-      d.h = head;
-      d.tok0 = tok0;
-      d.ntok = ntok;
-      d.key0 = key0;
-      d.keys = end - key0;
-      d.all = all;
-      d.dst = dst;
-      d.row = row;
-      d.list = list;
-      d.count = count;
-      d.seen = seen;
-      mbar_arrive(sm.pieced + told % kPieces);
-    }
-    ++told;
-  }
-
-  // Next piece: told, its rows on their way; n = 0 where there is nothing to compute.
-  __device__ __forceinline__ void next_piece() {
+  // Next piece; false: no more, or given up.
+  __device__ __forceinline__ bool next_piece() {
     const int lanes = gridDim.x, l = blockIdx.x;
-    if (lane == 0 && told >= kPieces) this->wait(sm.unpieced + told % kPieces, told / kPieces - 1, 13);
+    if (told >= kPieces) ok = wait_all(sm.unpieced + told % kPieces, (told / kPieces - 1) & 1, sm.abort_flag, 13);
+    if (!ok) return false;
     Piece& d = sm.pieces[told % kPieces];
-    int tok0, ntok, dst;
-    n = 0;
+    uint64_t* bar = sm.pieced + told % kPieces;
+    ++told;
+    int n = -1, h = 0, tok0 = 0, ntok = 0, key0 = 0, end = 0, all = 0, dst = -1, row = 0, count = 0, seen = 0;
+    const int* list = nullptr;
     if (kList) {
       const int units = p.B * p.Nq * p.Hkv, unit_tiles = (p.n_sel + 1) >> 1;
       const int whole = units / lanes * lanes;
-      long long u;
+      long long u = -1;
       int t0 = 0, nt = unit_tiles;
-      dst = -1;
       if (unit < whole) {
         u = unit;
         unit += lanes;
       } else if (left > 0) {
         const long long cut = static_cast<long long>(units - whole) * unit_tiles;
         const long long first = run_start(cut, lanes, l), x = run_start(cut, lanes, l + 1) - left;
-        const int cu = static_cast<int>(x / unit_tiles);
+        const int cu = static_cast<int>(quotient(x, unit_tiles));
         u = whole + cu;
         t0 = static_cast<int>(x - static_cast<long long>(cu) * unit_tiles);
         nt = static_cast<int>(min(static_cast<long long>(unit_tiles - t0), left));
         if (nt < unit_tiles) dst = 2 * l + (x > first ? 1 : 0);
         left -= nt;
-      } else {
-        fin = true;
-        tell(d, -1, 0, 0, 0);
-        return;
       }
-      // units by sequence, head, token: neighbours read the same head's keys
-      const int per = p.Hkv * p.Nq, ui = static_cast<int>(u);
-      const int bb = ui / per, r = ui - bb * per;
-      head = r / p.Nq;
-      const int i = r - head * p.Nq;
-      tok0 = bb * p.Nq + i;
-      ntok = 1;
-      list = p.blocks + (static_cast<long long>(tok0) * p.Hkv + head) * p.n_sel + 2 * t0;
-      count = min(p.n_sel - 2 * t0, 2 * nt);
-      const int len = clamped_len(p, bb);
-      if (lane == 0 && head == 0 && i == 0 && t0 == 0 && len != p.seqlens[bb]) record(1, kDevBadSeqlen);
-      row = bb;
-      seen = max(0, len - p.Nq + i + 1);
-      key0 = end = 0;
-      // which of them are seen; the last one that is ends the piece
-      int last = -1;
-      for (int w = (count - 1) >> 5; w >= 0; --w) {  // ends with the first 32 looked up
-        this->look_up(w);
-        if (lane == 0 && ok) {
-          d.full[w] = this->full_bits;
-          d.some[w] = this->seen_bits & ~this->full_bits;
-          if (d.some[w]) d.part = this->part;
+      if (u >= 0) {
+        // units by sequence, head, token: neighbours read the same head's keys
+        const int per = p.Hkv * p.Nq, ui = static_cast<int>(u);
+        row = ui / per;
+        const int r = ui - row * per;
+        h = r / p.Nq;
+        const int i = r - h * p.Nq;
+        tok0 = row * p.Nq + i;
+        ntok = 1;
+        list = p.blocks + (static_cast<long long>(tok0) * p.Hkv + h) * p.n_sel + 2 * t0;
+        count = min(p.n_sel - 2 * t0, 2 * nt);
+        const int len = clamped_len(p, row);
+        if (lane == 0 && h == 0 && i == 0 && t0 == 0 && len != p.seqlens[row]) record(1, kDevBadSeqlen);
+        seen = max(0, len - p.Nq + i + 1);
+        // which of them are seen; the last one that is ends the piece
+        int last = -1;
+        for (int w = 0; w < (count + 31) >> 5; ++w) {
+          const int e = 32 * w + lane;
+          const int blk = e < count ? list[e] : -1;
+          int v = 0;
+          if (blk >= 0) {
+            if (blk >= p.max_blocks * (p.page_size / 64))
+              record(3, kDevBadPage);
+            else
+              v = min(64, seen - blk * 64);
+          }
+          if (w == 0) d.group[lane] = v > 0 ? pool_group(p, row, blk) : 0;
+          const uint32_t any = __ballot_sync(0xffffffffu, v > 0), full = __ballot_sync(0xffffffffu, v == 64);
+          const uint32_t some = any & ~full;
+          if (lane == 0) {
+            d.full[w] = full;
+            d.some[w] = some;
+          }
+          if (some) {
+            const int part = __shfl_sync(0xffffffffu, v, __ffs(some) - 1);  // the same for all of them
+            if (lane == 0) d.part = part;
+          }
+          if (any) last = 32 * w + 31 - __clz(any);
         }
-        if (last < 0 && this->seen_bits) last = 32 * w + 31 - __clz(this->seen_bits);
+        n = (last + 2) >> 1;
       }
-      n = (last + 2) >> 1;
-    } else {
-      if (left == 0) {
-        fin = true;
-        tell(d, -1, 0, 0, 0);
-        return;
-      }
+    } else if (left > 0) {
       int len = b < 0 ? 0 : clamped_len(p, b);
       while (b >= 0 && len <= p.shared_len) len = clamped_len(p, ++b);  // a sequence with keys of its own is ahead
       int nt, rts, u;
-      head = hh;
+      h = hh;
       if (b < 0) {
         end = sm.plan->prefix_end;
         key0 = 128 * t;
-        row = 0;
         nt = tiles_of(end);
         all = sm.plan->all_see >= end;
         rts = 1;
         u = hh;
-        tok0 = 0;
         ntok = p.B * p.Nq;
       } else {
         end = len;
@@ -390,6 +257,8 @@ struct KeyLoader : Loader<D, R, kList, false> {
       dst = l + u;
       n = static_cast<int>(min(static_cast<long long>(nt - t), left));
       left -= n;
+      const int key = key0 + 64 * lane;
+      d.group[lane] = key < end && lane < 2 * n ? pool_group(p, row, key >> 6) : 0;
       t += n;
       if (t == nt) {
         t = 0;
@@ -402,26 +271,27 @@ struct KeyLoader : Loader<D, R, kList, false> {
         }
       }
     }
-    tell(d, n, tok0, ntok, dst);
-    if (n == 0) return;
     if (lane == 0) {
-      const uint32_t buf = rows_n & 1;
-      if (rows_n >= 2) this->wait(sm.qfree + buf, rows_n / 2 - 1, 14);
-      if (ok) {
-        mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(p.unit_tokens * (p.Hq / p.Hkv) * D * 2));
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sm.q + buf * L::kQ + c * (L::kN * 128), tm_q, sm.qfull + buf, c * 64, 0, head, tok0);
-        ++rows_n;
-      }
+      d.n = n;
+      d.h = h;
+      d.tok0 = tok0;
+      d.ntok = ntok;
+      d.key0 = key0;
+      d.keys = end - key0;
+      d.all = all;
+      d.dst = dst;
+      d.row = row;
+      d.list = list;
+      d.count = count;
+      d.seen = seen;
     }
-    if (!kList) this->look_up(0);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    return n >= 0;
   }
 
   __device__ __forceinline__ void run() {
     const int lanes = gridDim.x, l = blockIdx.x;
-    list = nullptr;
-    count = seen = head = row = key0 = end = 0;
     if (kList) {
       const int units = p.B * p.Nq * p.Hkv;
       const long long cut = static_cast<long long>(units - units / lanes * lanes) * ((p.n_sel + 1) >> 1);
@@ -434,60 +304,143 @@ struct KeyLoader : Loader<D, R, kList, false> {
         b = sm.plan->lane_b[0];
         const int nt = b < 0 ? tiles_of(sm.plan->prefix_end) : own_tiles(p, b), rts = b < 0 ? 1 : p.own_rt;
         const long long x = sm.plan->lane_at[0];
-        const int u = static_cast<int>(x / nt);
+        const int u = static_cast<int>(quotient(x, nt));
         hh = u / rts;
         rt = u - hh * rts;
         t = static_cast<int>(x - static_cast<long long>(u) * nt);
       }
     }
-    while (this->agree()) {
-      next_piece();
-      if (fin) break;
-      this->load_all();
+#pragma unroll 1
+    while (next_piece()) {
     }
-    if (lane != 0) return;
-    volatile int no_abort = 0;
-    for (uint32_t i = 0; i < 2 && i < rows_n; ++i) mbar_wait(sm.qfull + i, (rows_n - 1 - i) / 2 & 1, &no_abort, kWaitLimitNs);
-    this->drain();
   }
 };
 
-template <int D, int R, bool kList>
-struct ValueLoader : Loader<D, R, kList, true> {
-  using Base = Loader<D, R, kList, true>;
-  __device__ __forceinline__ ValueLoader(const RowsParams& p_, const CUtensorMap* v, const Smem<D, R>& sm_) : Base(p_, v, sm_) {}
-  __device__ __forceinline__ void run() {
-    for (;; ++this->told) {
-      const uint32_t at = this->told % kPieces;
-      if (this->lane == 0) this->wait(this->sm.pieced + at, this->told / kPieces, 15);
-      if (!this->agree()) break;
-      const volatile Piece& d = this->sm.pieces[at];
-      this->n = d.n;
-      this->head = d.h;
-      this->key0 = d.key0;
-      this->end = d.key0 + d.keys;
-      this->row = d.row;
-      this->list = d.list;
-      this->count = d.count;
-      this->seen = d.seen;
-      __syncwarp();
-      if (this->lane == 0) mbar_arrive(this->sm.unpieced + at);
-      if (this->n < 0) break;
-      if (this->n == 0) continue;
-      this->look_up(0);
-      this->load_all();
+// Loaders: a warp for K tiles (and a piece's rows) and one for V tiles; lane 0
+// waits and issues.  (One warp for both took 770 cycles a tile and operand.)
+template <int D, int R, bool kList, bool kV>
+struct Loader {
+  using L = Layout<D, R>;
+  const RowsParams& p;
+  const CUtensorMap *tm, *tm_q;
+  const Smem<D, R>& sm;
+  const int lane;
+  RingAt<kV ? L::kVs : L::kKs> at;
+  uint32_t fix_n = 0, rows_n = 0;
+  bool ok = true;  // lane 0's view until `agree`
+
+  __device__ __forceinline__ Loader(const RowsParams& p_, const CUtensorMap* tm_, const CUtensorMap* q, const Smem<D, R>& sm_)
+      : p(p_), tm(tm_), tm_q(q), sm(sm_), lane(threadIdx.x & 31) {}
+
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (ok) ok = wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  __device__ __forceinline__ bool agree() {
+    ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+    return ok;
+  }
+  // this lane's block of blocks 32 i .. 32 i + 31 of a piece
+  __device__ __forceinline__ int look_up(const Piece& d, int i) {
+    if (kList) {
+      const uint32_t seen = d.full[i] | d.some[i];
+      return seen >> lane & 1u ? pool_group(p, d.row, d.list[32 * i + lane]) : 0;
     }
-    if (this->lane != 0) return;
-    if (this->ok) {
-      // no more to clear
-      const uint32_t fi = this->fix_n & 3;
-      if (this->fix_n >= 4) this->wait(this->sm.fixdone + fi, this->fix_n / 4 - 1, 12);
-      if (this->ok) {
-        this->sm.fixes[fi].slot = -1;
-        mbar_arrive(this->sm.fixset + fi);
+    const int key = d.key0 + 64 * (32 * i + lane);
+    return key < d.key0 + d.keys && 32 * i + lane < 2 * d.n ? pool_group(p, d.row, key >> 6) : 0;
+  }
+  // a tile into the next slot: its blocks g0, g1, of which v0 and v1 keys count
+  __device__ __forceinline__ void load(int g0, int g1, int v0, int v1, int head) {
+    uint64_t* full = (kV ? sm.vfull : sm.kfull) + at.slot;
+    if (at.turn > 0) wait((kV ? sm.vempty : sm.kempty) + at.slot, at.turn - 1, 11);
+    if (!ok) return;
+    uint8_t* dst = (kV ? sm.v : sm.k) + at.slot * L::kTile;
+    if (v0 == 64 && v1 == 64) {
+      mbar_arrive_expect_tx(full, L::kTile);
+      tma_load_5d(dst, tm, full, 0, 0, 0, g0, head);
+      tma_load_5d(dst + L::kTile / 2, tm, full, 0, 0, 0, g1, head);
+    } else {
+      const uint32_t fi = fix_n & 3;
+      uint64_t* done = kV ? sm.raw + fi : full;
+      if (kV) {
+        if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+        if (!ok) return;
+        sm.fixes[fi].slot = static_cast<int>(at.slot);
+        sm.fixes[fi].v0 = v0;
+        sm.fixes[fi].v1 = v1;
+      }
+      if (v0 || v1)
+        mbar_arrive_expect_tx(done, v0 && v1 ? L::kTile : L::kTile / 2);
+      else
+        mbar_arrive(done);
+      if (v0) tma_load_5d(dst, tm, done, 0, 0, 0, g0, head);
+      if (v1) tma_load_5d(dst + L::kTile / 2, tm, done, 0, 0, 0, g1, head);
+      if (kV) {
+        mbar_arrive(sm.fixset + fi);
+        ++fix_n;
       }
     }
-    this->drain();
+    at.next();
+  }
+  __device__ __forceinline__ void run() {
+    for (uint32_t i = 0;; ++i) {
+      const Piece& d = sm.pieces[i % kPieces];
+      if (lane == 0) wait(sm.pieced + i % kPieces, i / kPieces, 15);
+      if (!agree()) break;
+      const int n = d.n, h = d.h;
+      if (n < 0) break;
+      if (!kV && n > 0 && lane == 0) {
+        const uint32_t buf = rows_n & 1;
+        if (rows_n >= 2) wait(sm.qfree + buf, rows_n / 2 - 1, 14);
+        if (ok) {
+          mbar_arrive_expect_tx(sm.qfull + buf, static_cast<uint32_t>(p.unit_tokens * (p.Hq / p.Hkv) * D * 2));
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sm.q + buf * L::kQ + c * (L::kN * 128), tm_q, sm.qfull + buf, c * 64, 0, h, d.tok0);
+          ++rows_n;
+        }
+      }
+      int blk = d.group[lane], next = 0;
+      const int keys = d.keys, part = d.part;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if ((j & 15) == 0 && j > 0) blk = next;
+        const int e = 2 * (j & 15);
+        const int g0 = __shfl_sync(0xffffffffu, blk, e), g1 = __shfl_sync(0xffffffffu, blk, e + 1);
+        if (lane == 0) {
+          int v0, v1;
+          if (kList) {
+            const uint32_t f = d.full[j >> 4] >> e, m = d.some[j >> 4] >> e;
+            v0 = f & 1u ? 64 : (m & 1u ? part : 0);
+            v1 = f & 2u ? 64 : (m & 2u ? part : 0);
+          } else {
+            v0 = min(64, keys - 128 * j);
+            v1 = max(0, min(64, keys - 128 * j - 64));
+          }
+          load(g0, g1, v0, v1, h);
+        }
+        if ((j & 15) == 4 && (j | 15) + 1 < n) next = look_up(d, (j >> 4) + 1);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.unpieced + i % kPieces);
+    }
+    if (lane != 0) return;
+    if (kV && ok) {
+      // no more to clear
+      const uint32_t fi = fix_n & 3;
+      if (fix_n >= 4) wait(sm.fixdone + fi, fix_n / 4 - 1, 12);
+      if (ok) {
+        sm.fixes[fi].slot = -1;
+        mbar_arrive(sm.fixset + fi);
+      }
+    }
+    // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
+    volatile int no_abort = 0;
+    for (uint32_t i = 0; i < 2 && i < rows_n; ++i) mbar_wait(sm.qfull + i, (rows_n - 1 - i) / 2 & 1, &no_abort, kWaitLimitNs);
+    for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
+    for (uint32_t i = 0; i < (kV ? L::kVs : L::kKs); ++i) {
+      const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
+      if (turns > 0) mbar_wait((kV ? sm.vfull : sm.kfull) + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
+    }
   }
 };
 
@@ -692,7 +645,7 @@ struct Softmax {
       const float was = first ? -INFINITY : sm.row[key];
       const float m = was == -INFINITY || mx - was > 8.f ? fmaxf(was, mx) : was;
       sm.row[key] = m;
-      sm.row[R + key] = was == m ? 1.f : ex2_approx(was - m);
+      sm.red[key] = was == m ? 1.f : ex2_approx(was - m);  // its place was read by this thread
     }
     group_sync();
 #pragma unroll
@@ -705,7 +658,7 @@ struct Softmax {
     tmem_row<R>(at, o);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float f = sm.row[R + r];
+      const float f = sm.red[r];
       o[r] *= f;
       l[r] *= f;
     }
@@ -713,14 +666,65 @@ struct Softmax {
     group_sync();  // the factors are read
   }
 
+  // Outputs of a piece, behind its last product: rows, their factors in row[R + which R ..].
+  static constexpr uint32_t kNone = 0xffffffffu;
+  struct Ended {
+    int rows, tok0, h, dst;
+    uint32_t which, piece;  // piece: number among those with products, kNone without
+  };
+  __device__ __forceinline__ void write_results(Ended& e) {
+    if (e.rows == 0) return;
+    group_sync();  // the factors are there
+    float o[R];
+    const bool any = e.piece != kNone;
+    if (any) {
+      wait(sm.odone + (e.piece & 1), e.piece / 2, 43);
+      tc_fence_after();
+      tmem_row<R>(tmem + (2 + (e.piece & 1)) * L::kN, o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.ofree + (e.piece & 1));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float f = sm.row[R + e.which * R + r];
+      o[r] = any && f != 0.f ? o[r] * f : 0.f;
+    }
+    if (key < D) {
+      if (e.dst >= 0) {
+        float* to = p.o_part + (p.pair_rows + static_cast<long long>(e.dst) * p.unit_rows) * D + key;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < e.rows) to[r * D] = o[r];
+      } else {
+        const int G = p.Hq / p.Hkv;
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(e.tok0) * p.Hq + e.h * G) * D + key;
+        int g = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (r >= e.rows) break;
+          *to = __float2bfloat16_rn(o[r]);
+          to += D;
+          if (++g == G) {  // the next token's heads of the group
+            g = 0;
+            to += static_cast<long long>(p.Hq - G) * D;
+          }
+        }
+      }
+    }
+    e.rows = 0;
+  }
+
   __device__ __forceinline__ void run() {
     const int G = p.Hq / p.Hkv;
+    Ended before;
+    before.rows = 0;
     for (uint32_t i = 0;; ++i) {
       const Piece& d = sm.pieces[i % kPieces];
       wait(sm.pieced + i % kPieces, i / kPieces, 41);
       if (group_any(!ok)) return;
       const int n = d.n, h = d.h, tok0 = d.tok0, ntok = d.ntok, dst = d.dst;
-      if (n < 0) return;
+      if (n < 0) break;
       const int rows = ntok * G;
       int whole = 0;  // ranges: keys that all rows see
       const bool all = kList || d.all;
@@ -792,7 +796,10 @@ struct Softmax {
         fence_proxy_async_smem();  // P before the tensor core's reads
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.pfull + (ts & 1));
+        // the piece before ended with a product that was still to come
+        if (j == 0) write_results(before);
       }
+      if (n == 0) write_results(before);
       // sums of the rows: over a warp's keys, then the four warps
       sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(l, [](float a, float b) { return a + b; });
       group_sync();
@@ -800,7 +807,7 @@ struct Softmax {
       if (key < rows) {
         const float sum = (sm.red[key] + sm.red[R + key]) + (sm.red[2 * R + key] + sm.red[3 * R + key]);
         const float lse2 = sum == 0.f ? -INFINITY : sm.row[key] + __log2f(sum);
-        sm.row[R + key] = sum == 0.f ? 0.f : 1.f / sum;
+        sm.row[R + (i & 1) * R + key] = sum == 0.f ? 0.f : 1.f / sum;
         if (dst >= 0) {
           p.lse_part[p.pair_rows + static_cast<long long>(dst) * p.unit_rows + key] = lse2;
         } else {
@@ -808,46 +815,12 @@ struct Softmax {
           p.lse[(static_cast<long long>(b) * p.Hq + h * G + key % G) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
         }
       }
-      group_sync();
-      float o[R];
-      if (n > 0) {
-        wait(sm.odone + (piece & 1), piece / 2, 43);
-        tc_fence_after();
-        tmem_row<R>(tmem + (2 + (piece & 1)) * L::kN, o);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm.ofree + (piece & 1));
-        ++piece;
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float f = sm.row[R + r];
-        o[r] = n > 0 && f != 0.f ? o[r] * f : 0.f;
-      }
-      if (key < D) {
-        if (dst >= 0) {
-          float* to = p.o_part + (p.pair_rows + static_cast<long long>(dst) * p.unit_rows) * D + key;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (r < rows) to[r * D] = o[r];
-        } else {
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(tok0) * p.Hq + h * G) * D + key;
-          int g = 0;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= rows) break;
-            *to = __float2bfloat16_rn(o[r]);
-            to += D;
-            if (++g == G) {  // the next token's heads of the group
-              g = 0;
-              to += static_cast<long long>(p.Hq - G) * D;
-            }
-          }
-        }
-      }
+      before = {rows, tok0, h, dst, i & 1u, n > 0 ? piece : kNone};
+      if (n > 0) ++piece;
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.unpieced + i % kPieces);
     }
+    write_results(before);
   }
 };
 
@@ -886,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(sm.pieced + i, 1);
-      mbar_init(sm.unpieced + i, 7);
+      mbar_init(sm.unpieced + i, 8);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(sm.fixset + i, 1);
@@ -906,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!kList)
     make_plan<kThreads / 32, 1>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
-                                reinterpret_cast<int*>(smem + L::kOffScan + 9 * 8));
+                                reinterpret_cast<int*>(smem + L::kOffScan + 10 * 8));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -917,12 +890,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
     }
-    KeyLoader<D, R, kList> loader(p, &tm_q, &tm_k, sm);
+    Loader<D, R, kList, false> loader(p, &tm_k, &tm_q, sm);
     loader.run();
   } else if (warp == 8) {
     if (lane == 0) tma_prefetch_desc(&tm_v);
-    ValueLoader<D, R, kList> loader(p, &tm_v, sm);
+    Loader<D, R, kList, true> loader(p, &tm_v, nullptr, sm);
     loader.run();
+  } else if (warp == 9) {
+    Planner<D, R, kList> planner(p, sm);
+    planner.run();
   } else if (warp == 1) {
     if (lane == 0) {
       Issuer<D, R> issuer(sm, tmem);
