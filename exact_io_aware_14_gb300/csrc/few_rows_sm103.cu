@@ -1,4 +1,4 @@
-// Attention of up to 16 query rows that read the same keys, over a paged bf16
+// Attention of up to 32 query rows that read the same keys, over a paged bf16
 // cache, for sm_103a: the new tokens of one sequence with a group's heads, those
 // of a small batch on its shared prefix, or one token's heads on listed blocks.
 //
@@ -22,8 +22,9 @@
 // rows and O^T are held twice, so that neither a tile nor a piece waits for the
 // one before to end.
 //
-// Warps: 9 planner (pieces and their pages), 0 and 8 loaders of K and V, 1 and 3
-// issuers of the two products, 2 clears value rows, 4-7 softmax and results.
+// Warps: 0 loader of K, 1 and 3 issuers of the two products, 2 clears value rows,
+// 4-7 (and 8-11 with more than 16 rows) softmax and results, then the loader of V
+// and the planner (pieces and their pages).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +35,6 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 320;
 constexpr int kPieces = 4;  // pieces told ahead
 
 struct Piece {
@@ -52,13 +52,19 @@ struct Piece {
   int group[32];   // the first 32 blocks, as groups of 8 keys of the pool
 };
 
+// R rows: 4, 8, 16 or 32.
 template <int D, int R>
 struct Layout {
-  static constexpr int kN = 16;  // the least that M = 128 takes
+  static constexpr int kN = R < 16 ? 16 : R;  // 16: the least that M = 128 takes
+  // Softmax groups of four warps, each with kRows of the rows: the code is that of
+  // 16 rows at most (one group with 32 rows a thread took 9000 cycles a tile: its
+  // code no longer stayed in the instruction cache).
+  static constexpr int kRows = R < 16 ? R : 16, kGroups = R / kRows;
+  static constexpr int kValueWarp = 4 + 4 * kGroups, kPlanWarp = kValueWarp + 1, kWarps = kPlanWarp + 1;
   static constexpr int kTile = 128 * D * 2;
   // tiles: groups of 8 keys, each with its D / 64 blocks of 8 rows of 128 B
   static constexpr int kGroup = D / 64 * 1024;
-  static constexpr int kKs = 3 * (128 / D), kVs = kKs;  // K and V tiles held
+  static constexpr int kKs = 3 * (128 / D), kVs = R == 32 && D == 128 ? 2 : kKs;  // K and V tiles held
   static constexpr int kQ = kN * D * 2;  // [D / 64][N][128 B]
   static constexpr int kP = kN * 256;    // [2][N][128 B]
   static constexpr int kOffV = kKs * kTile;
@@ -70,15 +76,16 @@ struct Layout {
   static constexpr int kOffFix = kOffBar + 8 * kNumBars;
   static constexpr int kOffPlan = (kOffFix + 4 * static_cast<int>(sizeof(Fix)) + 15) & ~15;
   static constexpr int kOffScan = kOffPlan + static_cast<int>(sizeof(Plan));
-  static constexpr int kOffRed = kOffScan + 10 * 8 + 2 * 10 * 4;  // [4][R] floats
-  static constexpr int kOffRow = kOffRed + 4 * R * 4;           // [3][R] floats
-  static constexpr int kOffLim = kOffRow + 3 * R * 4;           // [R] ints
+  static constexpr int kOffRed = kOffScan + kWarps * 8 + 2 * kWarps * 4;  // [4][R] floats
+  static constexpr int kOffRow = kOffRed + 4 * R * 4;                   // [3][R] floats
+  static constexpr int kOffLim = kOffRow + 3 * R * 4;                   // [R] ints
   static constexpr int kOffMisc = kOffLim + R * 4;
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
   static constexpr uint32_t kTmem = 4 * kN;     // S^T twice, O^T twice
 };
-static_assert(Layout<128, 16>::kAlloc <= 232448 && Layout<64, 16>::kAlloc <= 232448, "shared memory of a CTA");
+static_assert(Layout<128, 16>::kAlloc <= 232448 && Layout<64, 16>::kAlloc <= 232448 && Layout<128, 32>::kAlloc <= 232448 &&
+                  Layout<64, 32>::kAlloc <= 232448, "shared memory of a CTA");
 
 template <int D, int R>
 struct Smem {
@@ -103,12 +110,13 @@ struct Smem {
   uint64_t* drain;     // [2] after an abort: the MMAs that an issuer issued so far completed
   Fix* fixes;
   Plan* plan;
-  float* red;  // [4][R] of the softmax warps
-  float* row;  // [R] references, [2][R] factors of the rows
-  int* lim;    // [R] keys of the piece that a row sees
+  // of each softmax group, one after the other:
+  float* red;  // [4][kRows] of its warps
+  float* row;  // [kRows] references, [2][kRows] factors of its rows
+  int* lim;    // [kRows] keys of the piece that a row sees
   uint32_t* tmem_slot;
   volatile int* abort_flag;
-  volatile int* gone;  // [2] a softmax warp gave up (by the tile's parity)
+  volatile int* gone;  // [2][2] a warp of the softmax group gave up (by the tile's parity)
   __device__ __forceinline__ explicit Smem(uint8_t* base) {
     using L = Layout<D, R>;
     k = base;
@@ -435,8 +443,11 @@ struct Loader {
     }
     // every load lands before the CTA may exit, whatever became of the others (bounded, not abortable)
     volatile int no_abort = 0;
+#pragma unroll 1
     for (uint32_t i = 0; i < 2 && i < rows_n; ++i) mbar_wait(sm.qfull + i, (rows_n - 1 - i) / 2 & 1, &no_abort, kWaitLimitNs);
+#pragma unroll 1
     for (uint32_t i = 0; i < 4 && i < fix_n; ++i) mbar_wait(sm.raw + i, (fix_n - 1 - i) / 4 & 1, &no_abort, kWaitLimitNs);
+#pragma unroll 1
     for (uint32_t i = 0; i < (kV ? L::kVs : L::kKs); ++i) {
       const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
       if (turns > 0) mbar_wait((kV ? sm.vfull : sm.kfull) + i, (turns - 1) & 1, &no_abort, kWaitLimitNs);
@@ -551,7 +562,8 @@ __device__ __forceinline__ void tmem_row(uint32_t addr, float (&x)[R]) {
   } else if constexpr (R == 8) {
     tmem_ld8(addr, u);
   } else {
-    tmem_ld16(addr, u);
+#pragma unroll
+    for (int i = 0; i < R; i += 16) tmem_ld16(addr + i, u + i);
   }
   tmem_wait_ld();
 #pragma unroll
@@ -597,35 +609,40 @@ __device__ __forceinline__ int row_of(int lane) {
   return lane * R >> 5;
 }
 
-// The four softmax warps meet; true if any thread passes true.
-__device__ __forceinline__ bool group_any(bool x) {
+// The four warps of a softmax group meet; true if any thread passes true.
+__device__ __forceinline__ bool group_any(int grp, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(static_cast<uint32_t>(x)), "r"(1 + grp)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void group_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int grp) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory"); }
 
 constexpr float kMoveLog2 = 96.f;  // a row's reference moves where a score passes it by this much
 
-template <int D, int R, bool kList>
+template <int D, int kR, bool kList>
 struct Softmax {
-  using L = Layout<D, R>;
+  using L = Layout<D, kR>;
+  static constexpr int R = L::kRows;
   const RowsParams& p;
-  const Smem<D, R>& sm;
+  const Smem<D, kR>& sm;
   const uint32_t tmem;
-  const int lane, w4, key;  // key: of the tile (TMEM lane), and output dim
+  const int grp, lane, w4, key;  // key: of the tile (TMEM lane), and output dim
+  float* const red;
+  float* const row;
+  int* const lim_of;
   float M[R], l[R];
   uint32_t ts = 0, piece = 0;
   bool ok = true;  // this warp's view; all leave together
 
-  __device__ __forceinline__ Softmax(const RowsParams& p_, const Smem<D, R>& sm_, uint32_t tmem_)
-      : p(p_), sm(sm_), tmem(tmem_ + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21)), lane(threadIdx.x & 31),
-        w4((threadIdx.x >> 5) & 3), key(threadIdx.x & 127) {}
+  __device__ __forceinline__ Softmax(const RowsParams& p_, const Smem<D, kR>& sm_, uint32_t tmem_)
+      : p(p_), sm(sm_), tmem(tmem_ + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + ((threadIdx.x >> 7) - 1) * R),
+        grp((threadIdx.x >> 7) - 1), lane(threadIdx.x & 31), w4((threadIdx.x >> 5) & 3), key(threadIdx.x & 127),
+        red(sm_.red + 4 * R * grp), row(sm_.row + 3 * R * grp), lim_of(sm_.lim + R * grp) {}
 
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t site) {
     if (ok) ok = wait_all(bar, parity & 1, sm.abort_flag, site);
@@ -637,19 +654,19 @@ struct Softmax {
     float x[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) x[r] = vis >> r & 1u ? s[r] : -INFINITY;
-    sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(x, [](float a, float b) { return fmaxf(a, b); });
-    group_sync();
+    red[w4 * R + row_of<R>(lane)] = over_warp<R>(x, [](float a, float b) { return fmaxf(a, b); });
+    group_sync(grp);
     // a thread a row: its new reference and the factor of what there is (0 where nothing was seen)
     if (key < R) {
-      const float mx = fmaxf(fmaxf(sm.red[key], sm.red[R + key]), fmaxf(sm.red[2 * R + key], sm.red[3 * R + key]));
-      const float was = first ? -INFINITY : sm.row[key];
+      const float mx = fmaxf(fmaxf(red[key], red[R + key]), fmaxf(red[2 * R + key], red[3 * R + key]));
+      const float was = first ? -INFINITY : row[key];
       const float m = was == -INFINITY || mx - was > 8.f ? fmaxf(was, mx) : was;
-      sm.row[key] = m;
-      sm.red[key] = was == m ? 1.f : ex2_approx(was - m);  // its place was read by this thread
+      row[key] = m;
+      red[key] = was == m ? 1.f : ex2_approx(was - m);  // its place was read by this thread
     }
-    group_sync();
+    group_sync(grp);
 #pragma unroll
-    for (int r = 0; r < R; ++r) M[r] = sm.row[r];
+    for (int r = 0; r < R; ++r) M[r] = row[r];
     if (first) return;
     wait(sm.pvdone + ((ts - 1) & 1), (ts - 1) / 2, 44);
     tc_fence_after();
@@ -658,23 +675,24 @@ struct Softmax {
     tmem_row<R>(at, o);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float f = sm.red[r];
+      const float f = red[r];
       o[r] *= f;
       l[r] *= f;
     }
     tmem_put_row<R>(at, o);
-    group_sync();  // the factors are read
+    group_sync(grp);  // the factors are read
   }
 
   // Outputs of a piece, behind its last product: rows, their factors in row[R + which R ..].
   static constexpr uint32_t kNone = 0xffffffffu;
   struct Ended {
+    bool on;
     int rows, tok0, h, dst;
     uint32_t which, piece;  // piece: number among those with products, kNone without
   };
   __device__ __forceinline__ void write_results(Ended& e) {
-    if (e.rows == 0) return;
-    group_sync();  // the factors are there
+    if (!e.on) return;
+    group_sync(grp);  // the factors are there
     float o[R];
     const bool any = e.piece != kNone;
     if (any) {
@@ -687,19 +705,21 @@ struct Softmax {
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float f = sm.row[R + e.which * R + r];
+      const float f = row[R + e.which * R + r];
       o[r] = any && f != 0.f ? o[r] * f : 0.f;
     }
     if (key < D) {
       if (e.dst >= 0) {
-        float* to = p.o_part + (p.pair_rows + static_cast<long long>(e.dst) * p.unit_rows) * D + key;
+        float* to = p.o_part + (p.pair_rows + static_cast<long long>(e.dst) * p.unit_rows + R * grp) * D + key;
 #pragma unroll
         for (int r = 0; r < R; ++r)
           if (r < e.rows) to[r * D] = o[r];
       } else {
         const int G = p.Hq / p.Hkv;
-        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(e.tok0) * p.Hq + e.h * G) * D + key;
-        int g = 0;
+        const int skip = R * grp / G;  // tokens of the groups before
+        int g = R * grp - skip * G;
+        __nv_bfloat16* to =
+            static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(e.tok0 + skip) * p.Hq + e.h * G + g) * D + key;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           if (r >= e.rows) break;
@@ -712,20 +732,20 @@ struct Softmax {
         }
       }
     }
-    e.rows = 0;
+    e.on = false;
   }
 
   __device__ __forceinline__ void run() {
     const int G = p.Hq / p.Hkv;
     Ended before;
-    before.rows = 0;
+    before.on = false;
     for (uint32_t i = 0;; ++i) {
       const Piece& d = sm.pieces[i % kPieces];
       wait(sm.pieced + i % kPieces, i / kPieces, 41);
-      if (group_any(!ok)) return;
+      if (group_any(grp, !ok)) return;
       const int n = d.n, h = d.h, tok0 = d.tok0, ntok = d.ntok, dst = d.dst;
       if (n < 0) break;
-      const int rows = ntok * G;
+      const int rows = min(max(ntok * G - R * grp, 0), R);  // of this group
       int whole = 0;  // ranges: keys that all rows see
       const bool all = kList || d.all;
       if (!kList) {
@@ -733,16 +753,16 @@ struct Softmax {
         if (!all) {
           int lim = 0x7fffffff;
           if (key < rows) {
-            const int tok = tok0 + key / G, b = tok / p.Nq;
+            const int tok = tok0 + (R * grp + key) / G, b = tok / p.Nq;
             lim = min(whole, clamped_len(p, b) - p.Nq + tok - b * p.Nq + 1 - d.key0);
-            sm.lim[key] = lim;
+            lim_of[key] = lim;
           }
           const int m = __reduce_min_sync(0xffffffffu, lim);
-          if (lane == 0) sm.red[w4] = __int_as_float(m);
-          group_sync();
-          whole = min(min(__float_as_int(sm.red[0]), __float_as_int(sm.red[1])),
-                      min(__float_as_int(sm.red[2]), __float_as_int(sm.red[3])));
-          group_sync();
+          if (lane == 0) red[w4] = __int_as_float(m);
+          group_sync(grp);
+          whole = min(min(__float_as_int(red[0]), __float_as_int(red[1])),
+                      min(__float_as_int(red[2]), __float_as_int(red[3])));
+          group_sync(grp);
         }
       }
 #pragma unroll
@@ -766,7 +786,7 @@ struct Softmax {
           } else {
 #pragma unroll 1
             for (int r = 0; r < rows; ++r)
-              if (128 * j + key >= sm.lim[r]) vis &= ~(1u << r);
+              if (128 * j + key >= lim_of[r]) vis &= ~(1u << r);
           }
         }
         bool over = j == 0;
@@ -775,15 +795,15 @@ struct Softmax {
           s[r] *= p.scale_log2;
           over = over || (r < rows && (vis >> r & 1u) && s[r] - M[r] > kMoveLog2);
         }
-        if (!ok) sm.gone[ts & 1] = 1;
-        if (group_any(over || !ok)) {
-          if (sm.gone[ts & 1]) return;
+        if (!ok) sm.gone[2 * grp + (ts & 1)] = 1;
+        if (group_any(grp, over || !ok)) {
+          if (sm.gone[2 * grp + (ts & 1)]) return;
           move(s, vis, j == 0);
         }
         // p, to its place in the operand: rows of 128 B (64 keys), chunks of 16 B
         // exchanged by the row; the product that read this buffer is done
         if (ts >= 2) wait(sm.pvdone + (ts & 1), ts / 2 - 1, 45);
-        uint8_t* to = sm.ps + (ts & 1) * L::kP + (key >> 6) * (L::kN * 128) + (key & 7) * 2;
+        uint8_t* to = sm.ps + (ts & 1) * L::kP + (key >> 6) * (L::kN * 128) + R * grp * 128 + (key & 7) * 2;
         const int ch = (key & 63) >> 3;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -801,21 +821,21 @@ struct Softmax {
       }
       if (n == 0) write_results(before);
       // sums of the rows: over a warp's keys, then the four warps
-      sm.red[w4 * R + row_of<R>(lane)] = over_warp<R>(l, [](float a, float b) { return a + b; });
-      group_sync();
+      red[w4 * R + row_of<R>(lane)] = over_warp<R>(l, [](float a, float b) { return a + b; });
+      group_sync(grp);
       // a thread a row: the factor of its outputs and its log-sum-exp; l is 0 where nothing was seen, NaN stays NaN
       if (key < rows) {
-        const float sum = (sm.red[key] + sm.red[R + key]) + (sm.red[2 * R + key] + sm.red[3 * R + key]);
-        const float lse2 = sum == 0.f ? -INFINITY : sm.row[key] + __log2f(sum);
-        sm.row[R + (i & 1) * R + key] = sum == 0.f ? 0.f : 1.f / sum;
+        const float sum = (red[key] + red[R + key]) + (red[2 * R + key] + red[3 * R + key]);
+        const float lse2 = sum == 0.f ? -INFINITY : row[key] + __log2f(sum);
+        row[R + (i & 1) * R + key] = sum == 0.f ? 0.f : 1.f / sum;
         if (dst >= 0) {
-          p.lse_part[p.pair_rows + static_cast<long long>(dst) * p.unit_rows + key] = lse2;
+          p.lse_part[p.pair_rows + static_cast<long long>(dst) * p.unit_rows + R * grp + key] = lse2;
         } else {
-          const int tok = tok0 + key / G, b = tok / p.Nq;
-          p.lse[(static_cast<long long>(b) * p.Hq + h * G + key % G) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
+          const int r = R * grp + key, tok = tok0 + r / G, b = tok / p.Nq;
+          p.lse[(static_cast<long long>(b) * p.Hq + h * G + r % G) * p.Nq + tok - b * p.Nq] = lse2 * 0.6931471805599453f;
         }
       }
-      before = {rows, tok0, h, dst, i & 1u, n > 0 ? piece : kNone};
+      before = {true, rows, tok0, h, dst, i & 1u, n > 0 ? piece : kNone};
       if (n > 0) ++piece;
       __syncwarp();
       if (lane == 0) mbar_arrive(sm.unpieced + i % kPieces);
@@ -829,7 +849,7 @@ struct Softmax {
 // still being written, so it takes the SMs as they come free, and only ends
 // after that kernel (the joining kernel waits for this one).
 template <int D, int R, bool kList>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * Layout<D, R>::kWarps, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RowsParams p, int after_pairs) {
   using L = Layout<D, R>;
@@ -849,17 +869,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.sfull + i, 1);
-      mbar_init(sm.pfull + i, 4);
+      mbar_init(sm.pfull + i, 4 * L::kGroups);
       mbar_init(sm.pvdone + i, 1);
       mbar_init(sm.odone + i, 1);
-      mbar_init(sm.ofree + i, 4);
+      mbar_init(sm.ofree + i, 4 * L::kGroups);
       mbar_init(sm.qfull + i, 1);
       mbar_init(sm.qfree + i, 1);
-      sm.gone[i] = 0;
+      sm.gone[i] = sm.gone[2 + i] = 0;
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(sm.pieced + i, 1);
-      mbar_init(sm.unpieced + i, 8);
+      mbar_init(sm.unpieced + i, 4 + 4 * L::kGroups);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(sm.fixset + i, 1);
@@ -878,8 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (!kList)
-    make_plan<kThreads / 32, 1>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
-                                reinterpret_cast<int*>(smem + L::kOffScan + 10 * 8));
+    make_plan<L::kWarps, 1>(p, sm.plan, reinterpret_cast<long long*>(smem + L::kOffScan),
+                            reinterpret_cast<int*>(smem + L::kOffScan + L::kWarps * 8));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -892,11 +912,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Loader<D, R, kList, false> loader(p, &tm_k, &tm_q, sm);
     loader.run();
-  } else if (warp == 8) {
+  } else if (warp == L::kValueWarp) {
     if (lane == 0) tma_prefetch_desc(&tm_v);
     Loader<D, R, kList, true> loader(p, &tm_v, nullptr, sm);
     loader.run();
-  } else if (warp == 9) {
+  } else if (warp == L::kPlanWarp) {
     Planner<D, R, kList> planner(p, sm);
     planner.run();
   } else if (warp == 1) {
@@ -917,8 +937,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (slot < 0) break;
       if (!wait_all(sm.raw + fi, i / 4 & 1, sm.abort_flag, 32)) break;
       uint8_t* base = sm.v + slot * L::kTile;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int v = half ? v1 : v0;
+#pragma unroll 1
         for (int c = lane; c < (64 - v) * (D / 8); c += 32) {
           const int r = v + c / (D / 8), ch = c % (D / 8);
           *reinterpret_cast<uint4*>(base + half * (L::kTile / 2) + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
@@ -954,13 +976,14 @@ cudaError_t launch_r(const RowsParams& p, const CUtensorMap& tm_q, const CUtenso
   auto kern = p.blocks ? few_rows_kernel<D, R, true> : few_rows_kernel<D, R, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(grid), kThreads, L::kAlloc, stream, tm_q, tm_k, tm_v, p, after_pairs ? 1 : 0);
+  return launch_dependent(kern, dim3(grid), 32 * L::kWarps, L::kAlloc, stream, tm_q, tm_k, tm_v, p, after_pairs ? 1 : 0);
 }
 template <int D>
 cudaError_t launch_d(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                      int grid, bool after_pairs, cudaStream_t stream) {
   if (p.unit_rows <= 4) return launch_r<D, 4>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
   if (p.unit_rows <= 8) return launch_r<D, 8>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
+  if (p.unit_rows <= 16) return launch_r<D, 16>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
   return launch_r<D, kFewRows>(p, tm_q, tm_k, tm_v, grid, after_pairs, stream);
 }
 

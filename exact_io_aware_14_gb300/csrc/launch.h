@@ -257,7 +257,7 @@ struct RowsParams {
 cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_qs, const CUtensorMap& tm_k,
                         const CUtensorMap& tm_v, cudaStream_t stream);
 // The lanes' work of units with up to kFewRows rows; after_pairs: the kernel before on the stream is that of the pairs.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 32;
 cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             int grid, bool after_pairs, cudaStream_t stream);
 // Maps of bf16 tensors: a page pool as {64, 8, d / 64, groups of 8 keys, Hkv}, boxes of a head's 64 keys; q's of

@@ -80,35 +80,45 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kThreads = 32 * kWarps;
   const int per = p.Hkv * p.own_rt;  // units of a sequence
-  long long sum = 0;
+  // sums and extremes of all sequences; those of up to kThreads are scanned on the way
+  const bool once = p.B <= kThreads;
+  long long sum = 0, first = 0;
   int longest = 0, shortest = 0x7fffffff;
+#pragma unroll 1
   for (int b = tid; b < p.B; b += kThreads) {
-    sum += static_cast<long long>(own_tiles(p, b)) * per;
-    const int len = clamped_len(p, b);
+    const int raw = p.seqlens[b], len = min(max(raw, 0), p.max_blocks * p.page_size);
+    first = static_cast<long long>(tiles_of(max(0, len - p.shared_len))) * per;
+    sum += first;
     longest = max(longest, len);
     shortest = min(shortest, len);
-    if (blockIdx.x == 0 && (p.seqlens[b] < 0 || p.seqlens[b] > p.max_blocks * p.page_size)) record(1, kDevBadSeqlen);
+    if (blockIdx.x == 0 && raw != len) record(1, kDevBadSeqlen);
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   shortest = __reduce_min_sync(0xffffffffu, shortest);
+  // inclusive over the lanes of the warp: its last lane holds the warp's sum
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) {
     s_sum[warp] = sum;
     s_max[warp] = longest;
     s_max[kWarps + warp] = shortest;
   }
   __syncthreads();
-  sum = 0;
+  long long all = 0, ahead = 0;
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
-    sum += s_sum[w];
+    if (w == warp) ahead = all;
+    all += s_sum[w];
     longest = max(longest, s_max[w]);
     shortest = min(shortest, s_max[kWarps + w]);
   }
   const int end = min(p.shared_len, longest);
   const long long prefix = static_cast<long long>(tiles_of(end)) * p.Hkv;
   const long long solo = p.pairs ? 0 : prefix;
-  const long long total = solo + sum;
+  const long long total = solo + all;
   if (tid == 0) {
     plan->prefix_end = end;
     plan->all_see = max(0, shortest - p.Nq + 1);
@@ -128,7 +138,20 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
       plan->lane_at[s] = x[s];
     }
   }
+  auto place = [&](int b, long long before, long long mine) {
+    if (blockIdx.x == 0) p.sums[b] = before;
+    for (int s = 0; s < kSlots; ++s)
+      if (before <= x[s] && x[s] < before + mine) {
+        plan->lane_b[s] = b;
+        plan->lane_at[s] = x[s] - before;
+      }
+  };
+  if (once) {
+    if (tid < p.B) place(tid, solo + ahead + sum - first, first);
+    return;
+  }
   long long base = solo;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     // the last slot's lane starts last; CTA 0 needs all sums
     if (blockIdx.x != 0 && base > x[kSlots - 1]) break;
@@ -143,18 +166,14 @@ __device__ void make_plan(const RowsParams& p, Plan* plan, long long* s_sum, int
     __syncthreads();
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    long long before = base + incl - mine, all = 0;
+    long long before = base + incl - mine, chunk = 0;
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s_sum[w];
-      all += s_sum[w];
+      chunk += s_sum[w];
     }
-    if (b < p.B && blockIdx.x == 0) p.sums[b] = before;
-    for (int s = 0; s < kSlots; ++s)
-      if (b < p.B && before <= x[s] && x[s] < before + mine) {
-        plan->lane_b[s] = b;
-        plan->lane_at[s] = x[s] - before;
-      }
-    base += all;
+    if (b < p.B) place(b, before, mine);
+    base += chunk;
   }
 }
 

@@ -488,7 +488,9 @@ struct Producer {
     auto drain = [&](uint64_t* bar, uint32_t parity) { mbar_wait(bar, parity & 1, &no_abort, kWaitLimitNs); };
     if (a.rows_n) drain(sm.qfull + 0, a.rows_n - 1);
     if (b.rows_n) drain(sm.qfull + 1, b.rows_n - 1);
+#pragma unroll 1
     for (uint32_t i = 0; i < 4 && i < fix_n; ++i) drain(sm.raw + i, (fix_n - 1 - i) / 4);
+#pragma unroll 1
     for (uint32_t i = 0; i < L::kSlots; ++i) {
       const uint32_t turns = at.turn + (i < at.slot ? 1 : 0);
       if (turns > 0) drain(sm.full + i, turns - 1);
@@ -760,8 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (slot < 0) break;
       if (!wait_all(sm.raw + fi, (i / 4) & 1, abort_flag, 32)) break;
       uint8_t* base = sm.ring + slot * L::kTile;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int v = half ? v1 : v0;
+#pragma unroll 1
         for (int i = lane; i < (64 - v) * (D / 8); i += 32) {
           const int r = v + i / (D / 8), ch = i % (D / 8);
           *reinterpret_cast<uint4*>(base + half * (L::kTile / 2) + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
@@ -952,10 +956,10 @@ __device__ __forceinline__ void join(const RowsParams& p, int count, Place place
     s.l *= a;
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x] *= a;
-    for (int i = 0; i < n; i += 4) {
-      float v[4][kV];
+    for (int i = 0; i < n; i += 8) {
+      float v[8][kV];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const float* o = p.o_part + __shfl_sync(0xffffffffu, at, (i + k) & 31) * D + lane * kV;
         if (i + k < n) {
           if constexpr (kV == 4)
@@ -965,7 +969,7 @@ __device__ __forceinline__ void join(const RowsParams& p, int count, Place place
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const float wi = __shfl_sync(0xffffffffu, w, (i + k) & 31);
         if (i + k < n) {
           s.l += wi;
@@ -994,12 +998,13 @@ __device__ __forceinline__ void write_row(const RowsParams& p, int tok, int hq, 
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_ranges_kernel(const __grid_constant__ RowsParams p, int grid, int lanes) {
-  grid_depends();
+  grid_release();
   const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= p.B * p.Nq * p.Hq) return;
   const int G = p.Hq / p.Hkv;
   const int tok = row / p.Hq, hq = row - tok * p.Hq, h = hq / G, g = hq - h * G;
   const int b = tok / p.Nq, i = tok - b * p.Nq;
+  grid_wait();
+  if (row >= p.B * p.Nq * p.Hq) return;
   const long long total = p.sums[p.B], pair_total = p.sums[p.B + 1];
   const int nt = tiles_of(static_cast<int>(p.sums[p.B + 2]));
   Join s = {-INFINITY, 0.f};
