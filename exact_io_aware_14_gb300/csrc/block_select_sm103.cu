@@ -219,6 +219,214 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p, i
   }
 }
 
+// Scores on the tensor core.  For one sequence and KV head
+//     S^T [128 blocks x N rows] = [lo hi] [q- q+]^T,
+// 2 d deep, rows being tokens with the group's heads: a thread holds a block's
+// scores (TMEM lane), so the largest over a token's heads is taken in its
+// registers and a warp writes 32 neighbouring scores.  Few rows (N = 16): one
+// product for each 128 blocks, bound by reading the bounds.  Many (N = 128): a
+// CTA keeps its 128 blocks and walks the rows, bound by the products.
+// An fp32 sum of 256 terms, truncated at worst, is off by at most 2^-15 of the
+// sum of magnitudes, here bounded by |q| max_j |m_j|, m = max(|lo|, |hi|)
+// (Cauchy and Schwarz): 16 times the bound that `err` stands for.
+template <int D, int N>
+struct MmaLayout {
+  static constexpr int kA = 128 * 2 * D * 2, kB = N * 2 * D * 2;
+  static constexpr int kBufs = N == 128 ? 2 : 1;  // buffers of rows and of scores
+  static constexpr int kOffB = kA;
+  static constexpr int kOffNorm = kOffB + kBufs * kB;  // [kBufs][N] |q|^2, [128] |m|^2
+  static constexpr int kOffBar = kOffNorm + (kBufs * N + 128) * 4;
+  static constexpr int kBytes = kOffBar + kBufs * 8 + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kTmem = N == 128 ? 512 : 32;  // a token's heads are read 8 at a time, past the last one
+};
+__device__ __forceinline__ float sum_squares(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  float s = bf16lo(a) * bf16lo(a);
+  s = fmaf(bf16hi(a), bf16hi(a), s);
+  s = fmaf(bf16lo(b), bf16lo(b), s);
+  s = fmaf(bf16hi(b), bf16hi(b), s);
+  s = fmaf(bf16lo(c), bf16lo(c), s);
+  s = fmaf(bf16hi(c), bf16hi(c), s);
+  s = fmaf(bf16lo(d), bf16lo(d), s);
+  return fmaf(bf16hi(d), bf16hi(d), s);
+}
+__device__ __forceinline__ uint32_t max_abs_nan2(uint32_t a, uint32_t b) {
+  return max_nan2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams p, int token0, int tokens) {
+  using L = MmaLayout<D, N>;
+  constexpr int kC = D / 8;                       // 16-byte chunks of a row of D
+  constexpr int kLoads = (N * kC + kThreads - 1) / kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* s_q = reinterpret_cast<float*>(smem + L::kOffNorm);
+  float* s_m = s_q + L::kBufs * N;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + L::kBufs * 8);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = p.Hq / p.Hkv, h = blockIdx.y;
+  grid_depends();
+  // the launch's tokens of sequence b: n0 .. n1 - 1
+  const int b = token0 / p.Nq + blockIdx.z;
+  const int n0 = max(0, token0 - b * p.Nq), n1 = static_cast<int>(min(static_cast<long long>(p.Nq), token0 + static_cast<long long>(tokens) - static_cast<long long>(b) * p.Nq));
+  const int tile_tokens = N / G, row_tiles = (n1 - n0 + tile_tokens - 1) / tile_tokens;
+  const int block_tiles = (p.n_blocks + 127) / 128;
+  const int part = blockIdx.x / block_tiles, parts = gridDim.x / block_tiles;
+  const int j0 = (blockIdx.x - part * block_tiles) * 128;
+  const int len = clamped_len(p.seqlens, b, p.max_blocks * p.page_size, blockIdx.x == 0 && h == 0 && tid == 0);
+  auto blocks_seen = [&](int n) {  // by token n
+    const int pos = len - p.Nq + n;
+    return pos < 0 ? 0 : pos / kBlock + 1;
+  };
+  const int t0 = static_cast<int>(static_cast<long long>(row_tiles) * part / parts),
+            t1 = static_cast<int>(static_cast<long long>(row_tiles) * (part + 1) / parts);
+  if (t0 >= t1 || blocks_seen(min(n1, n0 + t1 * tile_tokens) - 1) <= j0) return;
+  int first = t0;  // the first tile whose last token sees a block of these
+  while (blocks_seen(min(n1, n0 + (first + 1) * tile_tokens) - 1) <= j0) ++first;
+  if (tid == 0) {
+    for (int i = 0; i < L::kBufs; ++i) mbar_init(bars + i, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, L::kTmem);
+    tmem_relinquish();
+  }
+  // the blocks' bounds: block r, chunk c of lo and of hi
+  const int j_end = (len + kBlock - 1) / kBlock;
+#pragma unroll 4
+  for (int i = 0; i < 128 * kC / kThreads; ++i) {
+    const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+    if (j0 + r < j_end) {
+      const uint4* src = reinterpret_cast<const uint4*>(bounds_at(p, b, j0 + r, h));
+      lo = src[c];
+      hi = src[kC + c];
+    }
+    uint8_t* to = smem + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(to) = lo;
+    *reinterpret_cast<uint4*>(to + (D / 64) * (128 * 128)) = hi;
+    float m = sum_squares(max_abs_nan2(lo.x, hi.x), max_abs_nan2(lo.y, hi.y), max_abs_nan2(lo.z, hi.z), max_abs_nan2(lo.w, hi.w));
+#pragma unroll
+    for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (c == 0) s_m[r] = m;
+  }
+  uint4 held[kLoads];
+  auto fetch = [&](int t) {
+    const int n = n0 + t * tile_tokens, rows = min(tile_tokens, n1 - n) * G;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
+      held[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const int tok = r / G;
+        held[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                 ((static_cast<long long>(b) * p.Nq + n + tok) * p.Hq + h * G + r - tok * G) * D)[c];
+      }
+    }
+  };
+  auto stage = [&](int buf) {
+    uint8_t* base = smem + L::kOffB + buf * L::kB;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
+      const uint4 u = held[i];
+      float m = sum_squares(u.x, u.y, u.z, u.w);
+#pragma unroll
+      for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (r >= N) continue;  // whole rows of lanes
+      if (c == 0) s_q[buf * N + r] = m;
+      uint8_t* to = base + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(to) = make_uint4(min_nan2(u.x, 0u), min_nan2(u.y, 0u), min_nan2(u.z, 0u), min_nan2(u.w, 0u));
+      *reinterpret_cast<uint4*>(to + (D / 64) * (N * 128)) =
+          make_uint4(max_nan2(u.x, 0u), max_nan2(u.y, 0u), max_nan2(u.z, 0u), max_nan2(u.w, 0u));
+    }
+  };
+  fetch(first);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  float m_max = 0.f;
+  for (int r = 0; r < 128; ++r) {
+    const float m = s_m[r];
+    if (!(m <= m_max)) m_max = m == m ? m : INFINITY;
+  }
+  volatile int never = 0;
+  for (int t = first, k = 0; t <= t1; ++t, ++k) {
+    if (t < t1) {
+      const int buf = L::kBufs == 2 ? k & 1 : 0;
+      stage(buf);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+        const uint64_t a = sdesc_sw128(smem_u32(smem), 16, 1024), q = sdesc_sw128(smem_u32(smem + L::kOffB + buf * L::kB), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 2 * D / 16; ++kk)
+          mma_bf16_ss(tmem + buf * N, a + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                      q + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), idesc_bf16_f32(128, N, 0), kk > 0 ? 1u : 0u);
+        mma_commit(bars + buf);
+      }
+      __syncwarp();
+      if (t + 1 < t1) fetch(t + 1);
+    }
+    // results of the tile before, or of this one where there is one buffer
+    if (L::kBufs == 2 && k == 0) continue;
+    if (L::kBufs == 1 && t == t1) break;
+    const int d = L::kBufs == 2 ? t - 1 : t, kd = L::kBufs == 2 ? k - 1 : k, buf = L::kBufs == 2 ? kd & 1 : 0;
+    if (!mbar_wait(bars + buf, (kd / L::kBufs) & 1, &never, 2000000000ull)) record(5, kDevTimeout);
+    tc_fence_after();
+    const int n = n0 + d * tile_tokens, cnt = min(tile_tokens, n1 - n);
+    // warps 0-3 and 4-7 take a half of the tokens each
+    const int half = (cnt + 1) / 2, c0 = warp >= 4 ? half : 0, c1 = warp >= 4 ? cnt : half;
+    const uint32_t at = tmem + buf * N + (static_cast<uint32_t>(warp & 3) << 21);
+    const int j = j0 + (warp & 3) * 32 + lane;
+    const long long lrow0 = (static_cast<long long>(b) * p.Nq + n - token0) * p.Hkv + h;
+    for (int c = c0; c < c1; c += 4) {
+      float best[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) best[x] = -INFINITY;
+      for (int g = 0; g < G; g += 8) {
+        uint32_t u[4][8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld8(at + min(c + x, c1 - 1) * G + g, u[x]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (g + i < G) best[x] = fmaxf(best[x], __uint_as_float(u[x][i]));
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (c + x < c1 && j < blocks_seen(n + c + x)) p.scores[(lrow0 + static_cast<long long>(c + x) * p.Hkv) * p.n_blocks + j] = best[x];
+    }
+    if (tid < cnt) {
+      float q = 0.f;
+      for (int g = 0; g < G; ++g) {
+        const float x = s_q[buf * N + tid * G + g];
+        if (!(x <= q)) q = x == x ? x : INFINITY;
+      }
+      // a little above sqrt(q m); infinite or NaN (0 times inf): looked at in 64 bits
+      float e = 16.1f * sqrtf(q) * sqrtf(m_max);
+      if (!(e <= 3e38f)) e = INFINITY;
+      float* err = p.err + (lrow0 + static_cast<long long>(tid) * p.Hkv) * p.n_chunks + j0 / kChunk;
+      err[0] = e;
+      if (j0 / kChunk + 1 < p.n_chunks) err[1] = e;
+    }
+    tc_fence_before();
+    __syncthreads();  // scores, rows and norms are read
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmem);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Choice.
 __device__ __forceinline__ uint32_t ordered(float x) {  // larger float, larger integer
@@ -489,10 +697,34 @@ cudaError_t launch_key_bounds(const KeyBoundsParams& p, cudaStream_t stream) {
                           0, stream, p, slabs);
 }
 
+template <int D, int N>
+cudaError_t launch_score_mma(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
+  using L = MmaLayout<D, N>;
+  auto kern = score_mma_kernel<D, N>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int seqs = (token0 + tokens - 1) / p.Nq - token0 / p.Nq + 1;
+  const int block_tiles = (p.n_blocks + 127) / 128, tile_tokens = N / (p.Hq / p.Hkv);
+  const long long row_tiles = ((tokens < p.Nq ? tokens : p.Nq) + tile_tokens - 1) / tile_tokens;
+  // the rows in as many parts as give each SM a CTA
+  const long long others = static_cast<long long>(block_tiles) * p.Hkv * seqs;
+  long long parts = others >= 304 ? 1 : (304 + others - 1) / others;
+  if (parts > row_tiles) parts = row_tiles;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(block_tiles * parts), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(seqs)),
+                          kThreads, L::kAlloc, stream, p, token0, tokens);
+}
+
 cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.n_chunks), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(tokens));
-  cudaError_t e = p.d == 64 ? launch_dependent(score_kernel<64>, grid, kThreads, 0, stream, p, token0)
-                            : launch_dependent(score_kernel<128>, grid, kThreads, 0, stream, p, token0);
+  const int G = p.Hq / p.Hkv, rows = p.Nq * G;
+  cudaError_t e;
+  if (rows <= 16)
+    e = p.d == 64 ? launch_score_mma<64, 16>(p, token0, tokens, stream) : launch_score_mma<128, 16>(p, token0, tokens, stream);
+  else if (G <= 128)
+    e = p.d == 64 ? launch_score_mma<64, 128>(p, token0, tokens, stream) : launch_score_mma<128, 128>(p, token0, tokens, stream);
+  else
+    e = p.d == 64 ? launch_dependent(score_kernel<64>, grid, kThreads, 0, stream, p, token0)
+                  : launch_dependent(score_kernel<128>, grid, kThreads, 0, stream, p, token0);
   if (e != cudaSuccess) return e;
   const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
   return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(tokens * p.Hkv)), kThreads,
