@@ -71,7 +71,7 @@ long long select_tokens(int B, int Nq, int Hkv, long long n_blocks) {
   t = t < 1 ? 1 : (t > 65535 ? 65535 : t);
   return t < tokens ? t : tokens;
 }
-long long select_chunks(long long n_blocks) { return (n_blocks + attn::kSelectChunk - 1) / attn::kSelectChunk; }
+long long select_tiles(long long n_blocks) { return (n_blocks + 127) / 128; }
 
 // The arguments that both attention calls share.
 attn_status check_rows_args(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
@@ -248,7 +248,8 @@ attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_bounds, const
 size_t attn_select_blocks_workspace_size(int B, int Nq, int Hkv, int max_seqlen) {
   if (B < 1 || Nq < 1 || Hkv < 1 || max_seqlen < 64) return 0;
   const long long n = max_seqlen / 64;
-  return static_cast<size_t>(select_tokens(B, Nq, Hkv, n)) * Hkv * (n + select_chunks(n)) * sizeof(float);
+  return (static_cast<size_t>(select_tokens(B, Nq, Hkv, n)) * Hkv * (n + 1) + static_cast<size_t>(B) * Hkv * select_tiles(n)) *
+         sizeof(float);
 }
 
 attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const int* block_table, int max_blocks,
@@ -260,6 +261,7 @@ attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const 
   if (st != ATTN_OK) return st;
   if (topk < 1 || sink < 0 || local < 0 || static_cast<long long>(sink) + local > topk) return ATTN_ERR_INVALID_ARG;
   const long long tokens = static_cast<long long>(B) * Nq;
+  if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;  // a token's heads of a group fit one tile of rows
   if (Hkv > 65535 || tokens > kIntMax || tokens * Hkv > kIntMax) return ATTN_ERR_UNSUPPORTED;
   if (!q || !k_bounds || !blocks) return ATTN_ERR_INVALID_ARG;
   if (off(q, 16) || off(k_bounds, 16) || off(blocks, 4)) return ATTN_ERR_MISALIGNED;
@@ -287,10 +289,10 @@ attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const 
   p.sink = sink;
   p.local = local;
   p.n_blocks = static_cast<int>(n);
-  p.n_chunks = static_cast<int>(select_chunks(n));
   const long long step = select_tokens(B, Nq, Hkv, n);
   p.scores = static_cast<float*>(workspace);
-  p.err = p.scores + step * Hkv * n;
+  p.q_norm = p.scores + step * Hkv * n;
+  p.m_norm = p.q_norm + step * Hkv;
   for (long long t = 0; t < tokens; t += step) {
     const int m = static_cast<int>(tokens - t < step ? tokens - t : step);
     if (attn::launch_select(p, static_cast<int>(t), m, static_cast<cudaStream_t>(stream)) != cudaSuccess)

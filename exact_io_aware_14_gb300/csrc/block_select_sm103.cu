@@ -12,11 +12,12 @@
 //
 // Choice: the row's first `sink` and last `local` blocks, then the largest
 // scores, the lower index first among equals; the order is that of the scores
-// in 64 bits.  The scores are formed in fp32 first.  With A = max_j sum |terms|
-// an fp32 score is off by at most E = 2^-19 A (each sum rounds no partial sum
-// more than 32 times, 2^-24 of it each), so a block is in where its score is
-// above the k-th largest T by more than 2 E, out where it is that far below,
-// and only the few in between are scored again in 64 bits.
+// in 64 bits.  The scores are formed in fp32 first, off by at most E, so a block
+// is in where its score is above the k-th largest T by more than 2 E, out where
+// it is that far below, and only the few in between are scored again in 64 bits.
+// An fp32 sum of 256 terms, truncated at worst at each addition, is off by at
+// most 2^-15 of the sum of magnitudes, and that is at most |q| max_j |m_j| with
+// m = max(|lo|, |hi|) (Cauchy and Schwarz).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -150,93 +151,23 @@ __device__ __forceinline__ const __nv_bfloat16* bounds_at(const SelectParams& p,
          ((static_cast<long long>(pg) * per + j % per) * p.Hkv + h) * 2 * p.d;
 }
 
-// fp32 scores.  One CTA for a row and kChunk blocks; 8 threads a block, each
-// with D / 8 channels, and the group's heads four at a time.
-constexpr int kChunk = kSelectChunk;
-
-template <int D>
-__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p, int token0) {
-  grid_depends();
-  constexpr int kPer = D / 8;  // channels of a thread
-  const int G = p.Hq / p.Hkv;
-  const int h = blockIdx.y;
-  const int lrow = blockIdx.z * p.Hkv + h;
-  const int token = token0 + blockIdx.z;
-  const RowSpan r = row_span(p, token, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-  const int j0 = blockIdx.x * kChunk, j1 = min(r.nb, j0 + kChunk);
-  __shared__ float s_a[kThreads / 32];
-  if (j0 >= r.nb) return;
-  const int l = threadIdx.x & 7;
-  float* out = p.scores + static_cast<long long>(lrow) * p.n_blocks;
-  float a_max = 0.f;
-  for (int j = j0 + (threadIdx.x >> 3); j < j0 + kChunk; j += kThreads / 8) {  // same steps for a warp's lanes
-    const bool on = j < j1;
-    float lo[kPer], hi[kPer];
-    {
-      const __nv_bfloat16* src = bounds_at(p, r.b, on ? j : j0, h) + l * kPer;
-#pragma unroll
-      for (int i = 0; i < kPer; i += 8) {
-        unpack8(*reinterpret_cast<const uint4*>(src + i), lo + i);
-        unpack8(*reinterpret_cast<const uint4*>(src + D + i), hi + i);
-      }
-    }
-    float best = -INFINITY;
-    for (int g = 0; g < G; ++g) {
-      const __nv_bfloat16* qs = static_cast<const __nv_bfloat16*>(p.q) +
-                                (static_cast<long long>(token) * p.Hq + h * G + g) * D + l * kPer;
-      float q[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; i += 8) unpack8(*reinterpret_cast<const uint4*>(qs + i), q + i);
-      float2 s = make_float2(0.f, 0.f);
-      float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        s = ffma2(make_float2(fmaxf(q[i], 0.f), fminf(q[i], 0.f)), make_float2(hi[i], lo[i]), s);
-        a = fmaf(fabsf(q[i]), fmaxf(fabsf(hi[i]), fabsf(lo[i])), a);
-        if (q[i] != q[i]) s.x = a = NAN;  // fmaxf, fminf drop it
-      }
-      float v = s.x + s.y;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-      }
-      if (!(v == v)) a = INFINITY;  // looked at in 64 bits
-      best = fmaxf(best, v);
-      if (on) a_max = a > a_max || a != a ? a : a_max;
-    }
-    if (on && l == 0) out[j] = best;
-  }
-  if (a_max != a_max) a_max = INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a_max = fmaxf(a_max, __shfl_xor_sync(0xffffffffu, a_max, o));
-  if ((threadIdx.x & 31) == 0) s_a[threadIdx.x >> 5] = a_max;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) a_max = fmaxf(a_max, s_a[w]);
-    p.err[static_cast<long long>(lrow) * p.n_chunks + blockIdx.x] = a_max;
-  }
-}
-
 // Scores on the tensor core.  For one sequence and KV head
 //     S^T [128 blocks x N rows] = [lo hi] [q- q+]^T,
 // 2 d deep, rows being tokens with the group's heads: a thread holds a block's
 // scores (TMEM lane), so the largest over a token's heads is taken in its
 // registers and a warp writes 32 neighbouring scores.  Few rows (N = 16): one
 // product for each 128 blocks, bound by reading the bounds.  Many (N = 128): a
-// CTA keeps its 128 blocks and walks the rows, bound by the products.
-// An fp32 sum of 256 terms, truncated at worst, is off by at most 2^-15 of the
-// sum of magnitudes, here bounded by |q| max_j |m_j|, m = max(|lo|, |hi|)
-// (Cauchy and Schwarz): 16 times the bound that `err` stands for.
+// CTA keeps its 128 blocks and walks the rows, bound by laying these out.
 template <int D, int N>
 struct MmaLayout {
   static constexpr int kA = 128 * 2 * D * 2, kB = N * 2 * D * 2;
   static constexpr int kBufs = N == 128 ? 2 : 1;  // buffers of rows and of scores
+  static constexpr int kThreads = N == 128 ? 512 : 256;
   static constexpr int kOffB = kA;
   static constexpr int kOffNorm = kOffB + kBufs * kB;  // [kBufs][N] |q|^2, [128] |m|^2
   static constexpr int kOffBar = kOffNorm + (kBufs * N + 128) * 4;
-  static constexpr int kBytes = kOffBar + kBufs * 8 + 16;
+  static constexpr int kOffPage = kOffBar + kBufs * 8 + 16;  // [128] where the blocks' bounds lie
+  static constexpr int kBytes = kOffPage + 128 * 8;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTmem = N == 128 ? 512 : 32;  // a token's heads are read 8 at a time, past the last one
 };
@@ -255,9 +186,10 @@ __device__ __forceinline__ uint32_t max_abs_nan2(uint32_t a, uint32_t b) {
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams p, int token0, int tokens) {
+__global__ void __launch_bounds__(MmaLayout<D, N>::kThreads) score_mma_kernel(const SelectParams p, int token0, int tokens) {
   using L = MmaLayout<D, N>;
-  constexpr int kC = D / 8;                       // 16-byte chunks of a row of D
+  constexpr int kThreads = L::kThreads, kGroups = kThreads / 128;
+  constexpr int kC = D / 8;  // 16-byte chunks of a row of D
   constexpr int kLoads = (N * kC + kThreads - 1) / kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -265,6 +197,7 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
   float* s_m = s_q + L::kBufs * N;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + L::kBufs * 8);
+  const __nv_bfloat16** s_at = reinterpret_cast<const __nv_bfloat16**>(smem + L::kOffPage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.Hkv, h = blockIdx.y;
   grid_depends();
@@ -295,12 +228,14 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
   }
   // the blocks' bounds: block r, chunk c of lo and of hi
   const int j_end = (len + kBlock - 1) / kBlock;
-#pragma unroll 4
+  if (tid < 128) s_at[tid] = j0 + tid < j_end ? bounds_at(p, b, j0 + tid, h) : nullptr;
+  __syncthreads();
+#pragma unroll
   for (int i = 0; i < 128 * kC / kThreads; ++i) {
     const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (j0 + r < j_end) {
-      const uint4* src = reinterpret_cast<const uint4*>(bounds_at(p, b, j0 + r, h));
+    const uint4* src = reinterpret_cast<const uint4*>(s_at[r]);
+    if (src) {
       lo = src[c];
       hi = src[kC + c];
     }
@@ -332,11 +267,13 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
     for (int i = 0; i < kLoads; ++i) {
       const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
       const uint4 u = held[i];
-      float m = sum_squares(u.x, u.y, u.z, u.w);
+      if (j0 == 0) {  // the rows' norms, once
+        float m = sum_squares(u.x, u.y, u.z, u.w);
 #pragma unroll
-      for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (r >= N) continue;  // whole rows of lanes
-      if (c == 0) s_q[buf * N + r] = m;
+        for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        if (c == 0 && r < N) s_q[buf * N + r] = m;
+      }
+      if (r >= N) continue;
       uint8_t* to = base + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
       *reinterpret_cast<uint4*>(to) = make_uint4(min_nan2(u.x, 0u), min_nan2(u.y, 0u), min_nan2(u.z, 0u), min_nan2(u.w, 0u));
       *reinterpret_cast<uint4*>(to + (D / 64) * (N * 128)) =
@@ -348,10 +285,12 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  float m_max = 0.f;
-  for (int r = 0; r < 128; ++r) {
-    const float m = s_m[r];
-    if (!(m <= m_max)) m_max = m == m ? m : INFINITY;
+  if (warp == 0) {  // every part of the rows finds the same
+    float m_max = 0.f;
+    for (int r = lane; r < 128; r += 32) m_max = fmaxf(m_max, s_m[r] == s_m[r] ? s_m[r] : INFINITY);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m_max = fmaxf(m_max, __shfl_xor_sync(0xffffffffu, m_max, o));
+    if (lane == 0) p.m_norm[(static_cast<long long>(b) * p.Hkv + h) * block_tiles + j0 / 128] = m_max;
   }
   volatile int never = 0;
   for (int t = first, k = 0; t <= t1; ++t, ++k) {
@@ -380,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
     if (!mbar_wait(bars + buf, (kd / L::kBufs) & 1, &never, 2000000000ull)) record(5, kDevTimeout);
     tc_fence_after();
     const int n = n0 + d * tile_tokens, cnt = min(tile_tokens, n1 - n);
-    // warps 0-3 and 4-7 take a half of the tokens each
-    const int half = (cnt + 1) / 2, c0 = warp >= 4 ? half : 0, c1 = warp >= 4 ? cnt : half;
+    // each four warps take a part of the tokens
+    const int c0 = cnt * (warp >> 2) / kGroups, c1 = cnt * ((warp >> 2) + 1) / kGroups;
     const uint32_t at = tmem + buf * N + (static_cast<uint32_t>(warp & 3) << 21);
     const int j = j0 + (warp & 3) * 32 + lane;
     const long long lrow0 = (static_cast<long long>(b) * p.Nq + n - token0) * p.Hkv + h;
@@ -404,18 +343,13 @@ __global__ void __launch_bounds__(kThreads) score_mma_kernel(const SelectParams 
       for (int x = 0; x < 4; ++x)
         if (c + x < c1 && j < blocks_seen(n + c + x)) p.scores[(lrow0 + static_cast<long long>(c + x) * p.Hkv) * p.n_blocks + j] = best[x];
     }
-    if (tid < cnt) {
+    if (j0 == 0 && tid < cnt) {
       float q = 0.f;
       for (int g = 0; g < G; ++g) {
         const float x = s_q[buf * N + tid * G + g];
-        if (!(x <= q)) q = x == x ? x : INFINITY;
+        q = fmaxf(q, x == x ? x : INFINITY);
       }
-      // a little above sqrt(q m); infinite or NaN (0 times inf): looked at in 64 bits
-      float e = 16.1f * sqrtf(q) * sqrtf(m_max);
-      if (!(e <= 3e38f)) e = INFINITY;
-      float* err = p.err + (lrow0 + static_cast<long long>(tid) * p.Hkv) * p.n_chunks + j0 / kChunk;
-      err[0] = e;
-      if (j0 / kChunk + 1 < p.n_chunks) err[1] = e;
+      p.q_norm[lrow0 + static_cast<long long>(tid) * p.Hkv] = q;
     }
     tc_fence_before();
     __syncthreads();  // scores, rows and norms are read
@@ -438,7 +372,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 
 // The 64-bit score of block j, formed by a warp; NaN ranks as +inf.
-__device__ double exact_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
+__device__ __noinline__ double exact_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
   const int lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
   const __nv_bfloat16* kb = bounds_at(p, r.b, j, h);
@@ -459,6 +393,61 @@ __device__ double exact_score(const SelectParams& p, const RowSpan& r, int token
   return best;
 }
 
+// The same from pairs of fp32 (products of bf16 are exact in fp32; each addition
+// leaves its error in the second number: Knuth's two-sum), where the row's scores
+// lie well within fp32's range: 2^-46 of the sum of magnitudes, no more than a sum
+// of 256 terms in double precision may be off by, at 60 times its rate here.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
+  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
+  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
+  return {s, __fadd_rn(__fadd_rn(a.l, b.l), e)};
+}
+__device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
+  const int lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  const __nv_bfloat16* kb = bounds_at(p, r.b, j, h);
+  float lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = lane + 32 * i;
+    lo[i] = at < p.d ? __bfloat162float(kb[at]) : 0.f;
+    hi[i] = at < p.d ? __bfloat162float(kb[p.d + at]) : 0.f;
+  }
+  double best = -INFINITY;
+#pragma unroll 2
+  for (int g = 0; g < G; ++g) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(token) * p.Hq + h * G + g) * p.d;
+    Pair s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = lane + 32 * i;
+      const float x = at < p.d ? __bfloat162float(q[at]) : 0.f;
+      s = add_pair(s, {__fmul_rn(x, x > 0.f ? hi[i] : lo[i]), 0.f});
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      s = add_pair(s, {__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
+    best = fmax(best, static_cast<double>(s.h) + static_cast<double>(s.l));
+  }
+  return best;
+}
+
+// Twice the bound on the error of a row's scores (with what products below
+// fp32's range lose); infinite where norms are, and where they are not numbers.
+__device__ __forceinline__ float band_of(const SelectParams& p, const RowSpan& r, int h, int lrow) {
+  const float* m = p.m_norm + (static_cast<long long>(r.b) * p.Hkv + h) * ((p.n_blocks + 127) / 128);
+  float x = 0.f;
+  for (int i = threadIdx.x & 31; i <= (r.nb - 1) / 128; i += 32) x = fmaxf(x, m[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  // 2 * 2^-15, and a little for the roundings of the norms
+  const float band = 6.2e-5f * sqrtf(x) * sqrtf(p.q_norm[lrow]) + 1e-36f;
+  return band <= 3e38f ? band : INFINITY;
+}
+
 constexpr int kHeld = 8192;   // scores kept in shared memory
 constexpr int kBand = 1024;   // blocks scored again at most, else all by passes over 64-bit keys
 
@@ -467,7 +456,153 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 
-// One CTA for a row.
+// A warp for a row of up to 32 K blocks, block 32 m + lane in element m of a lane.
+constexpr int kChooseWarps = 4;
+template <int K>
+__global__ void __launch_bounds__(32 * kChooseWarps) choose_warp_kernel(const SelectParams p, int token0, int rows) {
+  grid_depends();
+  const int lane = threadIdx.x & 31;
+  const int lrow = blockIdx.x * kChooseWarps + (threadIdx.x >> 5);
+  if (lrow >= rows) return;
+  const int h = lrow % p.Hkv, token = token0 + lrow / p.Hkv;
+  const RowSpan r = row_span(p, token, false);
+  int* out = p.blocks + (static_cast<long long>(token) * p.Hkv + h) * p.topk;
+  if (r.nb <= p.topk) {
+    for (int i = lane; i < p.topk; i += 32) out[i] = i < r.nb ? i : -1;
+    return;
+  }
+  const int c0 = p.sink, c1 = r.nb - p.local, k = p.topk - p.sink - p.local;
+  const float* scores = p.scores + static_cast<long long>(lrow) * p.n_blocks;
+  uint32_t key[K];  // 0: no candidate
+#pragma unroll
+  for (int m = 0; m < K; ++m) {
+    const int j = 32 * m + lane;
+    key[m] = j >= c0 && j < c1 ? ordered(scores[j]) : 0u;
+  }
+  uint32_t in = 0, in2 = 0;  // chosen elements of this lane
+  auto take = [&](int m) {
+    if (m < 32)
+      in |= 1u << m;
+    else
+      in2 |= 1u << (m - 32);
+  };
+  if (k > 0) {
+    const float band = band_of(p, r, h, lrow);
+    uint32_t lo = 1u, hi = 0xffffffffu;  // without a bound on the errors all candidates lie between
+    if (band < 1e38f) {
+      // the k-th largest: the largest t with k keys at or above it
+      uint32_t t = 0;
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+        const uint32_t c = t | bit;
+        int n = 0;
+#pragma unroll
+        for (int m = 0; m < K; ++m) n += key[m] >= c ? 1 : 0;
+        if (__reduce_add_sync(0xffffffffu, n) >= k) t = c;
+      }
+      const float x = unordered(t);
+      lo = max(ordered(x - band), 1u);
+      hi = ordered(x + band);
+    }
+    int sure = 0, between = 0;
+#pragma unroll
+    for (int m = 0; m < K; ++m) {
+      sure += key[m] > hi ? 1 : 0;
+      between += key[m] >= lo && key[m] <= hi ? 1 : 0;
+    }
+    sure = __reduce_add_sync(0xffffffffu, sure);
+    between = __reduce_add_sync(0xffffffffu, between);
+    const int left = k - sure;
+#pragma unroll
+    for (int m = 0; m < K; ++m)
+      if (key[m] > hi || (between == left && key[m] >= lo)) take(m);
+    if (between > left) {
+      // those between, by their 64-bit scores (in fp32 pairs where those have the range)
+      const bool pairs = band > 1e-18f && band < 1e18f;
+      auto exact = [&](int j) { return ordered64(pairs ? pair_score(p, r, token, h, j) : exact_score(p, r, token, h, j)); };
+      if (between <= 32) {
+        // a lane each
+        unsigned long long u = 0;
+        int n = 0, id = 0;
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+          uint32_t w = __ballot_sync(0xffffffffu, key[m] >= lo && key[m] <= hi);
+#pragma unroll 1
+          while (w) {
+            const int l = __ffs(w) - 1;
+            w &= w - 1;
+            const unsigned long long v = exact(32 * m + l);
+            if (lane == n) {
+              u = v;
+              id = 32 * m + l;
+            }
+            ++n;
+          }
+        }
+        int rank = 0;  // they are in the order of their indexes
+#pragma unroll 1
+        for (int o = 0; o < n; ++o) {
+          const unsigned long long v = __shfl_sync(0xffffffffu, u, o);
+          rank += v > u || (v == u && o < lane);
+        }
+        const uint32_t won = __ballot_sync(0xffffffffu, lane < n && rank < left);
+#pragma unroll 1
+        for (int o = 0; o < n; ++o) {
+          const int j = __shfl_sync(0xffffffffu, id, o);
+          if ((won >> o & 1u) && (j & 31) == lane) take(j >> 5);
+        }
+      } else {
+        unsigned long long ex[K];  // 0: not between
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+          ex[m] = 0;
+          uint32_t w = __ballot_sync(0xffffffffu, key[m] >= lo && key[m] <= hi);
+#pragma unroll 1
+          while (w) {
+            const int l = __ffs(w) - 1;
+            w &= w - 1;
+            const unsigned long long u = exact(32 * m + l);
+            if (lane == l) ex[m] = u;
+          }
+        }
+        unsigned long long t = 0;  // the largest that `left` of them reach
+        int above = 0;             // those above it
+#pragma unroll 1
+        for (unsigned long long bit = 1ull << 63; bit; bit >>= 1) {
+          int n = 0;
+#pragma unroll
+          for (int m = 0; m < K; ++m) n += ex[m] >= (t | bit) ? 1 : 0;
+          if (__reduce_add_sync(0xffffffffu, n) >= left) t |= bit;
+        }
+#pragma unroll
+        for (int m = 0; m < K; ++m) above += ex[m] > t ? 1 : 0;
+        int equal = left - __reduce_add_sync(0xffffffffu, above);  // of those equal to it the first ones
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+          const uint32_t same = __ballot_sync(0xffffffffu, ex[m] == t);
+          if (ex[m] > t || (ex[m] == t && __popc(same & ((1u << lane) - 1u)) < equal)) take(m);
+          equal -= min(equal, __popc(same));
+        }
+      }
+    }
+  }
+  int at = 0;
+#pragma unroll
+  for (int m = 0; m < K; ++m) {
+    const int j = 32 * m + lane;
+    const bool c = j < r.nb && (j < c0 || j >= c1 || (m < 32 ? in >> m & 1u : in2 >> (m - 32) & 1u));
+    const uint32_t w = __ballot_sync(0xffffffffu, c);
+    if (c) out[at + __popc(w & ((1u << lane) - 1u))] = j;
+    at += __popc(w);
+  }
+}
+template <int K>
+cudaError_t launch_choose_warp(const SelectParams& p, int token0, int rows, cudaStream_t stream) {
+  return launch_dependent(choose_warp_kernel<K>, dim3(static_cast<unsigned>((rows + kChooseWarps - 1) / kChooseWarps)),
+                          32 * kChooseWarps, 0, stream, p, token0, rows);
+}
+
+// One CTA for a row of more.
 __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, int token0) {
   grid_depends();
   extern __shared__ float s_score[];  // [min(n_blocks, kHeld)]
@@ -501,13 +636,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
   unsigned long long cut = 0;              // mode 2: keys above it are in, of those equal the first `left`
   int left = 0;
   if (k > 0) {
-    // error bound of the row
-    float e = 0.f;
-    for (int c = lane; c <= (r.nb - 1) / kChunk; c += 32) e = fmaxf(e, p.err[static_cast<long long>(lrow) * p.n_chunks + c]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
-    const float band = e * 3.814697265625e-6f + 1e-36f;  // 2 E, and what products below fp32's range lose
-    bool all = !(band < 1e38f);
+    const float band = band_of(p, r, h, lrow);
+    const bool all = !(band < 1e38f), pairs = band > 1e-18f && band < 1e18f;
     if (!all) {
       // the k-th largest, a byte of its key at a time
       uint32_t prefix = 0;
@@ -576,7 +706,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
       if (between <= kBand) {
         mode = 1;
         for (int m = warp; m < between; m += kThreads / 32) {
-          const double x = exact_score(p, r, token, h, c0 + s_id[m]);
+          const double x = pairs ? pair_score(p, r, token, h, c0 + s_id[m]) : exact_score(p, r, token, h, c0 + s_id[m]);
           if (lane == 0) s_exact[m] = x;
         }
         __syncthreads();
@@ -706,29 +836,30 @@ cudaError_t launch_score_mma(const SelectParams& p, int token0, int tokens, cuda
   const int seqs = (token0 + tokens - 1) / p.Nq - token0 / p.Nq + 1;
   const int block_tiles = (p.n_blocks + 127) / 128, tile_tokens = N / (p.Hq / p.Hkv);
   const long long row_tiles = ((tokens < p.Nq ? tokens : p.Nq) + tile_tokens - 1) / tile_tokens;
-  // the rows in as many parts as give each SM a CTA
+  // the rows in as many parts as fill the SMs once, not twice
   const long long others = static_cast<long long>(block_tiles) * p.Hkv * seqs;
-  long long parts = others >= 304 ? 1 : (304 + others - 1) / others;
+  long long parts = others >= 152 ? 1 : 152 / others;
   if (parts > row_tiles) parts = row_tiles;
   return launch_dependent(kern, dim3(static_cast<unsigned>(block_tiles * parts), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(seqs)),
-                          kThreads, L::kAlloc, stream, p, token0, tokens);
+                          L::kThreads, L::kAlloc, stream, p, token0, tokens);
 }
 
 cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.n_chunks), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(tokens));
-  const int G = p.Hq / p.Hkv, rows = p.Nq * G;
+  const int rows = p.Nq * (p.Hq / p.Hkv);
   cudaError_t e;
   if (rows <= 16)
     e = p.d == 64 ? launch_score_mma<64, 16>(p, token0, tokens, stream) : launch_score_mma<128, 16>(p, token0, tokens, stream);
-  else if (G <= 128)
-    e = p.d == 64 ? launch_score_mma<64, 128>(p, token0, tokens, stream) : launch_score_mma<128, 128>(p, token0, tokens, stream);
   else
-    e = p.d == 64 ? launch_dependent(score_kernel<64>, grid, kThreads, 0, stream, p, token0)
-                  : launch_dependent(score_kernel<128>, grid, kThreads, 0, stream, p, token0);
+    e = p.d == 64 ? launch_score_mma<64, 128>(p, token0, tokens, stream) : launch_score_mma<128, 128>(p, token0, tokens, stream);
   if (e != cudaSuccess) return e;
+  const int n = tokens * p.Hkv;
+  if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
+  if (p.n_blocks <= 512) return launch_choose_warp<16>(p, token0, n, stream);
+  if (p.n_blocks <= 1024) return launch_choose_warp<32>(p, token0, n, stream);
+  if (p.n_blocks <= 2048) return launch_choose_warp<64>(p, token0, n, stream);
   const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
-  return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(tokens * p.Hkv)), kThreads,
-                          held * static_cast<int>(sizeof(float)), stream, p, token0);
+  return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(n)), kThreads, held * static_cast<int>(sizeof(float)), stream,
+                          p, token0);
 }
 
 cudaError_t status_word_select(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_select_status); }

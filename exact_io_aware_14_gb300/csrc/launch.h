@@ -198,7 +198,6 @@ cudaError_t launch_release(const PagingParams& p, cudaStream_t stream);
 
 // Bounds of the keys of 64-key blocks, and the choice of blocks by them.
 constexpr int kSelectBlock = 64;   // keys of a block
-constexpr int kSelectChunk = 64;   // blocks of a scoring CTA
 struct KeyBoundsParams {
   const void* k_pages;
   void* k_bounds;  // [num_pages, page_size / 64, Hkv, 2, d]
@@ -216,9 +215,10 @@ struct SelectParams {
   const int* seqlens;
   int* blocks;    // [B, Nq, Hkv, topk]
   float* scores;  // [tokens of a launch, Hkv, n_blocks]
-  float* err;     // [tokens of a launch, Hkv, n_chunks]: largest sums of magnitudes
+  float* q_norm;  // [tokens of a launch, Hkv]: largest |q|^2 of the group's heads
+  float* m_norm;  // [B, Hkv, n_blocks / 128]: largest |max(|lo|, |hi|)|^2 of 128 blocks
   int max_blocks, page_size, num_pages, B, Nq, Hq, Hkv, d, topk, sink, local;
-  int n_blocks, n_chunks;  // blocks of a full table, chunks of them
+  int n_blocks;   // of a full table
 };
 cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStream_t stream);
 

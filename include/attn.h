@@ -507,7 +507,7 @@ ATTN_API attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_boun
  * score, the lower index first among equals, topk in all (all of them where
  * there are no more).
  *   blocks: device int32 [B, Nq, Hkv, topk] out, ascending, -1 behind the last;
- *   sink, local >= 0, sink + local <= topk;
+ *   sink, local >= 0, sink + local <= topk; Hq / Hkv is at most 128;
  *   workspace: attn_select_blocks_workspace_size(B, Nq, Hkv, max_blocks *
  *            page_size) bytes, 16-byte aligned, contents ignored; one for each
  *            call that may run at once.
