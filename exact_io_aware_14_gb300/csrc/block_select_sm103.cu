@@ -186,7 +186,7 @@ __device__ __forceinline__ uint32_t max_abs_nan2(uint32_t a, uint32_t b) {
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(MmaLayout<D, N>::kThreads) score_mma_kernel(const SelectParams p, int token0, int tokens) {
+__global__ void __launch_bounds__(MmaLayout<D, N>::kThreads, N == 128 ? 1 : 3) score_mma_kernel(const SelectParams p, int token0, int tokens) {
   using L = MmaLayout<D, N>;
   constexpr int kThreads = L::kThreads, kGroups = kThreads / 128;
   constexpr int kC = D / 8;  // 16-byte chunks of a row of D
@@ -248,18 +248,19 @@ __global__ void __launch_bounds__(MmaLayout<D, N>::kThreads) score_mma_kernel(co
     if (c == 0) s_m[r] = m;
   }
   uint4 held[kLoads];
-  auto fetch = [&](int t) {
-    const int n = n0 + t * tile_tokens, rows = min(tile_tokens, n1 - n) * G;
+  // this thread's chunks of a tile of rows: element offsets from the tile's first token, and their tokens
+  int off[kLoads], tok_of[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
-      held[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        const int tok = r / G;
-        held[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                 ((static_cast<long long>(b) * p.Nq + n + tok) * p.Hq + h * G + r - tok * G) * D)[c];
-      }
-    }
+  for (int i = 0; i < kLoads; ++i) {
+    const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
+    tok_of[i] = r < tile_tokens * G ? r / G : 0x7fffffff;
+    off[i] = r < tile_tokens * G ? (r / G * p.Hq + r % G) * kC + c : 0;
+  }
+  auto fetch = [&](int t) {
+    const int n = n0 + t * tile_tokens, cnt = min(tile_tokens, n1 - n);
+    const uint4* q = static_cast<const uint4*>(p.q) + ((static_cast<long long>(b) * p.Nq + n) * p.Hq + h * G) * kC;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) held[i] = tok_of[i] < cnt ? q[off[i]] : make_uint4(0u, 0u, 0u, 0u);
   };
   auto stage = [&](int buf) {
     uint8_t* base = smem + L::kOffB + buf * L::kB;
@@ -324,24 +325,54 @@ __global__ void __launch_bounds__(MmaLayout<D, N>::kThreads) score_mma_kernel(co
     const uint32_t at = tmem + buf * N + (static_cast<uint32_t>(warp & 3) << 21);
     const int j = j0 + (warp & 3) * 32 + lane;
     const long long lrow0 = (static_cast<long long>(b) * p.Nq + n - token0) * p.Hkv + h;
-    for (int c = c0; c < c1; c += 4) {
-      float best[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) best[x] = -INFINITY;
-      for (int g = 0; g < G; g += 8) {
-        uint32_t u[4][8];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld8(at + min(c + x, c1 - 1) * G + g, u[x]);
+    const int sees = j * kBlock - len + p.Nq - n;  // the first token of the tile that sees this block
+    const long long pitch = static_cast<long long>(p.Hkv) * p.n_blocks;
+    float* to = p.scores + (lrow0 + static_cast<long long>(c0) * p.Hkv) * p.n_blocks + j;
+    auto put = [&](int c, float v) {
+      if (c >= sees) *to = v;
+      to += pitch;
+    };
+    if (G == 4) {
+      int c = c0;
+#pragma unroll 1
+      for (; c + 4 <= c1; c += 4) {
+        uint32_t u[16];
+        tmem_ld16(at + 4 * c, u);
         tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (g + i < G) best[x] = fmaxf(best[x], __uint_as_float(u[x][i]));
+          put(c + x, fmaxf(fmaxf(__uint_as_float(u[4 * x]), __uint_as_float(u[4 * x + 1])),
+                           fmaxf(__uint_as_float(u[4 * x + 2]), __uint_as_float(u[4 * x + 3]))));
       }
+#pragma unroll 1
+      for (; c < c1; ++c) {
+        uint32_t u[8];
+        tmem_ld8(at + 4 * c, u);
+        tmem_wait_ld();
+        put(c, fmaxf(fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1])), fmaxf(__uint_as_float(u[2]), __uint_as_float(u[3]))));
+      }
+    } else {
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 4) {
+        float best[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (c + x < c1 && j < blocks_seen(n + c + x)) p.scores[(lrow0 + static_cast<long long>(c + x) * p.Hkv) * p.n_blocks + j] = best[x];
+        for (int x = 0; x < 4; ++x) best[x] = -INFINITY;
+#pragma unroll 1
+        for (int g = 0; g < G; g += 8) {
+          uint32_t u[4][8];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld8(at + min(c + x, c1 - 1) * G + g, u[x]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (g + i < G) best[x] = fmaxf(best[x], __uint_as_float(u[x][i]));
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (c + x < c1) put(c + x, best[x]);
+      }
     }
     if (j0 == 0 && tid < cnt) {
       float q = 0.f;
@@ -406,33 +437,32 @@ __device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
   return {s, __fadd_rn(__fadd_rn(a.l, b.l), e)};
 }
 __device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
-  const int lane = threadIdx.x & 31;
+  // eight lanes a head, four heads at a time
+  const int lane = threadIdx.x & 31, sub = lane & 7, chunks = p.d >> 6;
   const int G = p.Hq / p.Hkv;
-  const __nv_bfloat16* kb = bounds_at(p, r.b, j, h);
-  float lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = lane + 32 * i;
-    lo[i] = at < p.d ? __bfloat162float(kb[at]) : 0.f;
-    hi[i] = at < p.d ? __bfloat162float(kb[p.d + at]) : 0.f;
-  }
+  const uint4* kb = reinterpret_cast<const uint4*>(bounds_at(p, r.b, j, h));
+  const uint4* qs = static_cast<const uint4*>(p.q) + (static_cast<long long>(token) * p.Hq + h * G) * (p.d >> 3);
   double best = -INFINITY;
-#pragma unroll 2
-  for (int g = 0; g < G; ++g) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<long long>(token) * p.Hq + h * G + g) * p.d;
+#pragma unroll 1
+  for (int g = lane >> 3; g < ((G + 3) & ~3); g += 4) {
     Pair s = {0.f, 0.f};
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int at = c * 8 + sub;
+      float x[8], lo[8], hi[8];
+      unpack8(qs[(g < G ? g : 0) * (p.d >> 3) + at], x);
+      unpack8(kb[at], lo);
+      unpack8(kb[(p.d >> 3) + at], hi);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = lane + 32 * i;
-      const float x = at < p.d ? __bfloat162float(q[at]) : 0.f;
-      s = add_pair(s, {__fmul_rn(x, x > 0.f ? hi[i] : lo[i]), 0.f});
+      for (int i = 0; i < 8; ++i) s = add_pair(s, {__fmul_rn(x[i], x[i] > 0.f ? hi[i] : lo[i]), 0.f});
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1)
       s = add_pair(s, {__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
-    best = fmax(best, static_cast<double>(s.h) + static_cast<double>(s.l));
+    best = fmax(best, static_cast<double>(s.h) + static_cast<double>(s.l));  // (head 0 again past the last one)
   }
-  return best;
+  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
+  return fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
 }
 
 // Twice the bound on the error of a row's scores (with what products below
@@ -490,19 +520,31 @@ __global__ void __launch_bounds__(32 * kChooseWarps) choose_warp_kernel(const Se
     const float band = band_of(p, r, h, lrow);
     uint32_t lo = 1u, hi = 0xffffffffu;  // without a bound on the errors all candidates lie between
     if (band < 1e38f) {
-      // the k-th largest: the largest t with k keys at or above it
-      uint32_t t = 0;
+      // the k-th largest, between t and t + 2^last - 1: the largest t with k keys
+      // at or above it, from the bits that all keys share down to a quarter of the band
+      uint32_t top = 0u, bottom = 0xffffffffu;
+#pragma unroll
+      for (int m = 0; m < K; ++m) {
+        top = max(top, key[m]);
+        bottom = min(bottom, key[m] ? key[m] : 0xffffffffu);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      bottom = __reduce_min_sync(0xffffffffu, bottom);
+      const float large = fmaxf(fabsf(unordered(top)), fabsf(unordered(bottom)));
+      const int last = min(max(static_cast<int>(__float_as_uint(band) >> 23) - 2 - (static_cast<int>(__float_as_uint(large) >> 23) - 23), 0), 24);
+      const int differ = 32 - __clz(top ^ bottom);  // bits from here on down
+      uint32_t t = differ == 32 ? 0u : top >> differ << differ;
 #pragma unroll 1
-      for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
-        const uint32_t c = t | bit;
+      for (int bit = differ - 1; bit >= last; --bit) {
+        const uint32_t c = t | 1u << bit;
         int n = 0;
 #pragma unroll
         for (int m = 0; m < K; ++m) n += key[m] >= c ? 1 : 0;
         if (__reduce_add_sync(0xffffffffu, n) >= k) t = c;
       }
-      const float x = unordered(t);
-      lo = max(ordered(x - band), 1u);
-      hi = ordered(x + band);
+      const uint32_t rest = differ > last ? (1u << last) - 1u : (differ == 32 ? 0xffffffffu : (1u << differ) - 1u);
+      lo = max(ordered(unordered(t) - band), 1u);
+      hi = ordered(unordered(t | rest) + band);
     }
     int sure = 0, between = 0;
 #pragma unroll
@@ -856,7 +898,8 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
   if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
   if (p.n_blocks <= 512) return launch_choose_warp<16>(p, token0, n, stream);
   if (p.n_blocks <= 1024) return launch_choose_warp<32>(p, token0, n, stream);
-  if (p.n_blocks <= 2048) return launch_choose_warp<64>(p, token0, n, stream);
+  // many rows: a warp each; few: a CTA each
+  if (p.n_blocks <= 2048 && n > 2432) return launch_choose_warp<64>(p, token0, n, stream);
   const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
   return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(n)), kThreads, held * static_cast<int>(sizeof(float)), stream,
                           p, token0);
