@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-import _paged as P
+from tests import _paged as P
 from exact_io_aware_14_gb300 import _native as A
 
 pytestmark = pytest.mark.gpu
