@@ -562,60 +562,96 @@ struct Issuer {
     if (s.fin) s.n = 0;
   }
 
-  // One piece of pair work, both slots (told already); slot 1 has rows only if `both`.
-  __device__ __forceinline__ void pair_piece(MmaSlot& a, MmaSlot& b, bool both) {
+  // One piece of pair work (told to both slots), tiles in the ring as K_0, then
+  // V_{j-1}, K_j, and V_{n-1}.  Every instruction of this thread between two
+  // products leaves the tensor core idle, so a step probes the barriers that come
+  // next right behind a batch, while it still runs, and waits only for those that
+  // were not complete.
+  __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, uint32_t site) {
+    return wait_one(bar, parity & 1, sm.abort_flag, site);
+  }
+  __device__ __forceinline__ bool pair_piece(MmaSlot& a, MmaSlot& b) {
     const int n = a.n;
-    wait(sm.qfull + 0, a.rows_n++, 26);
-    if (both) wait(sm.qfull + 1, b.rows_n++, 26);
-    uint32_t vs = 0, vturn = 0;  // where V of the tile before lies
-    bool p0 = false;
-    for (int j = 0; ok && j <= n; ++j) {
-      // ring: (V of j - 1), K of j
-      if (j > 0) {
-        vs = at.slot;
-        vturn = at.turn;
-        at.next();
-        wait(sm.full + vs, vturn, 21);
-        if (!p0) wait(sm.pfull + 0, a.tiles, 22);
-        ++a.tiles;
-        if (j == 1 && a.done > 0) wait(sm.ofree + 0, a.done - 1, 23);
-        if (!ok) break;
-        tc_fence_after();
-        pv<0>(vs, j == 1);
-      }
-      const uint32_t ks = at.slot, kturn = at.turn;
-      if (j < n) {
-        at.next();
-        wait(sm.full + ks, kturn, 25);
-        if (!ok) break;
-        tc_fence_after();
-        qk<0>(ks);
-        if (j == n - 1) mma_commit(sm.qfree + 0);
-      } else {
-        mma_commit(sm.odone + 0);
-      }
-      if (both) {
-        if (j > 0) {
-          wait(sm.pfull + 1, b.tiles++, 22);
-          if (j == 1 && b.done > 0) wait(sm.ofree + 1, b.done - 1, 23);
-          if (!ok) break;
-          tc_fence_after();
-          pv<1>(vs, j == 1);
-        }
-        if (j < n) {
-          qk<1>(ks);
-          if (j == n - 1) mma_commit(sm.qfree + 1);
-        } else {
-          mma_commit(sm.odone + 1);
-        }
-      }
-      if (j > 0) mma_commit(sm.empty + vs);
-      if (j < n) mma_commit(sm.empty + ks);
-      // the next step's first wait, in the shadow of what was issued
-      p0 = mbar_test_wait(sm.pfull + 0, a.tiles & 1);
+    if (!await(sm.qfull + 0, a.rows_n++, 26) || !await(sm.qfull + 1, b.rows_n++, 26) || !await(sm.full + at.slot, at.turn, 25))
+      return false;
+    tc_fence_after();
+    qk<0>(at.slot);
+    qk<1>(at.slot);
+    mma_commit(sm.empty + at.slot);
+    at.next();
+    if (a.done > 0 && !await(sm.ofree + 0, a.done - 1, 23)) return false;
+    if (b.done > 0 && !await(sm.ofree + 1, b.done - 1, 23)) return false;
+    uint32_t p0 = a.tiles & 1, p1 = b.tiles & 1;
+    bool v_ready = false, p0_ready = false;
+#pragma unroll 1
+    for (int j = 1; j < n; ++j) {
+      const uint32_t vs = at.slot, vt = at.turn & 1;
+      at.next();
+      const uint32_t ks = at.slot, kt = at.turn & 1;
+      at.next();
+      if (!v_ready && !await(sm.full + vs, vt, 21)) return false;
+      if (!p0_ready && !await(sm.pfull + 0, p0, 22)) return false;
+      tc_fence_after();
+      pv<0>(vs, j == 1);
+      const bool k_ready = mbar_test_wait(sm.full + ks, kt);
+      if (!k_ready && !await(sm.full + ks, kt, 25)) return false;
+      qk<0>(ks);
+      const bool p1_ready = mbar_test_wait(sm.pfull + 1, p1);
+      if (!p1_ready && !await(sm.pfull + 1, p1, 22)) return false;
+      tc_fence_after();
+      pv<1>(vs, j == 1);
+      qk<1>(ks);
+      mma_commit(sm.empty + vs);
+      mma_commit(sm.empty + ks);
+      p0 ^= 1;
+      p1 ^= 1;
+      v_ready = mbar_test_wait(sm.full + at.slot, at.turn & 1);
+      p0_ready = mbar_test_wait(sm.pfull + 0, p0);
     }
+    mma_commit(sm.qfree + 0);
+    mma_commit(sm.qfree + 1);
+    if (!await(sm.full + at.slot, at.turn, 21) || !await(sm.pfull + 0, p0, 22)) return false;
+    tc_fence_after();
+    pv<0>(at.slot, n == 1);
+    mma_commit(sm.odone + 0);
+    if (!await(sm.pfull + 1, p1, 22)) return false;
+    tc_fence_after();
+    pv<1>(at.slot, n == 1);
+    mma_commit(sm.odone + 1);
+    mma_commit(sm.empty + at.slot);
+    at.next();
+    a.tiles += n;
+    b.tiles += n;
     ++a.done;
-    if (both) ++b.done;
+    ++b.done;
+    return true;
+  }
+  // The same where slot 1 has no rows.
+  __device__ __forceinline__ bool single_piece(MmaSlot& a) {
+    const int n = a.n;
+    if (!await(sm.qfull + 0, a.rows_n++, 26)) return false;
+    if (a.done > 0 && !await(sm.ofree + 0, a.done - 1, 23)) return false;
+#pragma unroll 1
+    for (int j = 0; j <= n; ++j) {
+      if (j > 0) {
+        if (!await(sm.full + at.slot, at.turn, 21) || !await(sm.pfull + 0, a.tiles++, 22)) return false;
+        tc_fence_after();
+        pv<0>(at.slot, j == 1);
+        mma_commit(sm.empty + at.slot);
+        at.next();
+      }
+      if (j < n) {
+        if (!await(sm.full + at.slot, at.turn, 25)) return false;
+        tc_fence_after();
+        qk<0>(at.slot);
+        mma_commit(sm.empty + at.slot);
+        at.next();
+      }
+    }
+    mma_commit(sm.qfree + 0);
+    mma_commit(sm.odone + 0);
+    ++a.done;
+    return true;
   }
 
   template <int S>
@@ -666,7 +702,7 @@ struct Issuer {
       if (!ok || a.fin || share == 0) break;
       int other;
       take<1>(b, &other);
-      if (ok) pair_piece(a, b, share == 1);
+      if (ok) ok = share == 1 ? pair_piece(a, b) : single_piece(a);
       a.n = b.n = a.j = b.j = 0;
     }
 #pragma unroll 1
