@@ -35,6 +35,7 @@ __device__ __forceinline__ void record(uint32_t site, uint32_t code) {
 }
 
 constexpr int kThreads = 256;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: no legitimate wait comes close
 constexpr int kBlock = kSelectBlock;  // keys of a block
 
 __device__ __forceinline__ int clamped_len(const int* seqlens, int b, int cap, bool report) {
@@ -155,21 +156,23 @@ __device__ __forceinline__ const __nv_bfloat16* bounds_at(const SelectParams& p,
 //     S^T [128 blocks x N rows] = [lo hi] [q- q+]^T,
 // 2 d deep, rows being tokens with the group's heads: a thread holds a block's
 // scores (TMEM lane), so the largest over a token's heads is taken in its
-// registers and a warp writes 32 neighbouring scores.  Few rows (N = 16): one
-// product for each 128 blocks, bound by reading the bounds.  Many (N = 128): a
-// CTA keeps its 128 blocks and walks the rows, bound by laying these out.
-template <int D, int N>
+// registers and a warp writes 32 neighbouring scores.  Many rows (N = 128): a CTA
+// keeps its 128 blocks and walks the rows, bound by laying these out.  Few rows
+// (N = 16): a CTA keeps the rows and walks the blocks, the next ones on their way
+// to registers while these are multiplied; bound by reading the bounds.
+template <int D>
 struct MmaLayout {
+  static constexpr int N = 128;
   static constexpr int kA = 128 * 2 * D * 2, kB = N * 2 * D * 2;
-  static constexpr int kBufs = N == 128 ? 2 : 1;  // buffers of rows and of scores
-  static constexpr int kThreads = N == 128 ? 512 : 256;
+  static constexpr int kBufs = 2;  // buffers of rows and of scores
+  static constexpr int kThreads = 512;
   static constexpr int kOffB = kA;
   static constexpr int kOffNorm = kOffB + kBufs * kB;  // [kBufs][N] |q|^2, [128] |m|^2
   static constexpr int kOffBar = kOffNorm + (kBufs * N + 128) * 4;
   static constexpr int kOffPage = kOffBar + kBufs * 8 + 16;  // [128] where the blocks' bounds lie
   static constexpr int kBytes = kOffPage + 128 * 8;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr uint32_t kTmem = N == 128 ? 512 : 32;  // a token's heads are read 8 at a time, past the last one
+  static constexpr uint32_t kTmem = 512;  // a token's heads are read 8 at a time, past the last one
 };
 __device__ __forceinline__ float sum_squares(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   float s = bf16lo(a) * bf16lo(a);
@@ -185,9 +188,10 @@ __device__ __forceinline__ uint32_t max_abs_nan2(uint32_t a, uint32_t b) {
   return max_nan2(a & 0x7fff7fffu, b & 0x7fff7fffu);
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(MmaLayout<D, N>::kThreads, N == 128 ? 1 : 3) score_mma_kernel(const SelectParams p, int token0, int tokens) {
-  using L = MmaLayout<D, N>;
+template <int D>
+__global__ void __launch_bounds__(MmaLayout<D>::kThreads, 1) score_mma_kernel(const SelectParams p, int token0, int tokens) {
+  using L = MmaLayout<D>;
+  constexpr int N = L::N;
   constexpr int kThreads = L::kThreads, kGroups = kThreads / 128;
   constexpr int kC = D / 8;  // 16-byte chunks of a row of D
   constexpr int kLoads = (N * kC + kThreads - 1) / kThreads;
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(MmaLayout<D, N>::kThreads, N == 128 ? 1 : 3) s
   volatile int never = 0;
   for (int t = first, k = 0; t <= t1; ++t, ++k) {
     if (t < t1) {
-      const int buf = L::kBufs == 2 ? k & 1 : 0;
+      const int buf = k & 1;
       stage(buf);
       fence_proxy_async_smem();
       tc_fence_before();
@@ -313,11 +317,10 @@ __global__ void __launch_bounds__(MmaLayout<D, N>::kThreads, N == 128 ? 1 : 3) s
       __syncwarp();
       if (t + 1 < t1) fetch(t + 1);
     }
-    // results of the tile before, or of this one where there is one buffer
-    if (L::kBufs == 2 && k == 0) continue;
-    if (L::kBufs == 1 && t == t1) break;
-    const int d = L::kBufs == 2 ? t - 1 : t, kd = L::kBufs == 2 ? k - 1 : k, buf = L::kBufs == 2 ? kd & 1 : 0;
-    if (!mbar_wait(bars + buf, (kd / L::kBufs) & 1, &never, 2000000000ull)) record(5, kDevTimeout);
+    // results of the tile before
+    if (k == 0) continue;
+    const int d = t - 1, buf = (k - 1) & 1;
+    if (!mbar_wait(bars + buf, ((k - 1) / 2) & 1, &never, kWaitLimitNs)) record(5, kDevTimeout);
     tc_fence_after();
     const int n = n0 + d * tile_tokens, cnt = min(tile_tokens, n1 - n);
     // each four warps take a part of the tokens
@@ -386,6 +389,164 @@ __global__ void __launch_bounds__(MmaLayout<D, N>::kThreads, N == 128 ? 1 : 3) s
     __syncthreads();  // scores, rows and norms are read
   }
   __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmem);
+  }
+}
+
+template <int D>
+struct FewLayout {
+  static constexpr int N = 16;
+  static constexpr int kA = 128 * 2 * D * 2, kB = N * 2 * D * 2;
+  static constexpr int kOffB = kA;
+  static constexpr int kOffNorm = kOffB + kB;             // [128] |m|^2, [N] |q|^2
+  static constexpr int kOffPage = kOffNorm + (128 + N) * 4;  // [2][128] where the blocks' bounds lie
+  static constexpr int kOffBar = kOffPage + 2 * 128 * 8;
+  static constexpr int kBytes = kOffBar + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr uint32_t kTmem = 32;  // a token's heads are read 8 at a time, past the last one
+};
+
+// All rows of a sequence (at most 16); block tiles part, part + parts, ...
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) score_few_kernel(const SelectParams p, int token0, int tokens) {
+  using L = FewLayout<D>;
+  constexpr int N = L::N, kC = D / 8, kLoads = 128 * kC / kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffNorm);
+  float* s_q = s_m + 128;
+  const uint4** s_at = reinterpret_cast<const uint4**>(smem + L::kOffPage);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = p.Hq / p.Hkv, h = blockIdx.y;
+  grid_depends();
+  const int b = token0 / p.Nq + blockIdx.z;
+  const int n0 = max(0, token0 - b * p.Nq), n1 = static_cast<int>(min(static_cast<long long>(p.Nq), token0 + static_cast<long long>(tokens) - static_cast<long long>(b) * p.Nq));
+  const int cnt = n1 - n0;
+  const int len = clamped_len(p.seqlens, b, p.max_blocks * p.page_size, blockIdx.x == 0 && h == 0 && tid == 0);
+  const int pos = len - p.Nq + n1 - 1;                    // of the last token
+  const int nb = pos < 0 ? 0 : pos / kBlock + 1;          // blocks that it sees
+  const int tiles = (nb + 127) / 128, block_tiles = (p.n_blocks + 127) / 128;
+  if (static_cast<int>(blockIdx.x) >= tiles) return;
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, L::kTmem);
+    tmem_relinquish();
+  }
+  auto places = [&](int t, int buf) {  // threads 0 .. 127
+    const int j = 128 * t + tid;
+    s_at[buf * 128 + tid] = t < tiles && j < nb ? reinterpret_cast<const uint4*>(bounds_at(p, b, j, h)) : nullptr;
+  };
+  uint4 lo[kLoads], hi[kLoads];
+  auto fetch = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * kThreads + tid;
+      const uint4* src = s_at[buf * 128 + idx / kC];
+      lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (src) {
+        lo[i] = src[idx % kC];
+        hi[i] = src[kC + idx % kC];
+      }
+    }
+  };
+  if (tid < 128) places(blockIdx.x, 0);
+  // the rows: chunk c of row r
+  if (tid < N * kC) {
+    const int r = tid / kC, c = tid % kC;
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (r < cnt * G)
+      u = (static_cast<const uint4*>(p.q) + ((static_cast<long long>(b) * p.Nq + n0 + r / G) * p.Hq + h * G + r % G) * kC)[c];
+    float m = sum_squares(u.x, u.y, u.z, u.w);
+#pragma unroll
+    for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (c == 0) s_q[r] = m;
+    uint8_t* to = smem + L::kOffB + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(to) = make_uint4(min_nan2(u.x, 0u), min_nan2(u.y, 0u), min_nan2(u.z, 0u), min_nan2(u.w, 0u));
+    *reinterpret_cast<uint4*>(to + (D / 64) * (N * 128)) =
+        make_uint4(max_nan2(u.x, 0u), max_nan2(u.y, 0u), max_nan2(u.z, 0u), max_nan2(u.w, 0u));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long lrow0 = (static_cast<long long>(b) * p.Nq + n0 - token0) * p.Hkv + h;
+  if (blockIdx.x == 0 && tid < cnt) {
+    float q = 0.f;
+    for (int g = 0; g < G; ++g) {
+      const float x = s_q[tid * G + g];
+      q = fmaxf(q, x == x ? x : INFINITY);
+    }
+    p.q_norm[lrow0 + static_cast<long long>(tid) * p.Hkv] = q;
+  }
+  fetch(0);
+  volatile int never = 0;
+#pragma unroll 1
+  for (int t = blockIdx.x, k = 0; t < tiles; t += gridDim.x, ++k) {
+    const int j0 = 128 * t;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
+      uint8_t* to = smem + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(to) = lo[i];
+      *reinterpret_cast<uint4*>(to + (D / 64) * (128 * 128)) = hi[i];
+      float m = sum_squares(max_abs_nan2(lo[i].x, hi[i].x), max_abs_nan2(lo[i].y, hi[i].y), max_abs_nan2(lo[i].z, hi[i].z),
+                            max_abs_nan2(lo[i].w, hi[i].w));
+#pragma unroll
+      for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (c == 0) s_m[r] = m;
+    }
+    if (tid < 128) places(t + gridDim.x, (k + 1) & 1);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const uint64_t a = sdesc_sw128(smem_u32(smem), 16, 1024), q = sdesc_sw128(smem_u32(smem + L::kOffB), 16, 1024);
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 2 * D / 16; ++kk)
+        mma_bf16_ss(tmem, a + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4), q + (((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
+                    idesc_bf16_f32(128, N, 0), kk > 0 ? 1u : 0u);
+      mma_commit(bar);
+    }
+    __syncwarp();
+    if (t + static_cast<int>(gridDim.x) < tiles) fetch((k + 1) & 1);
+    if (warp == 7) {
+      float m = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = fmaxf(m, s_m[32 * r + lane] == s_m[32 * r + lane] ? s_m[32 * r + lane] : INFINITY);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) p.m_norm[(static_cast<long long>(b) * p.Hkv + h) * block_tiles + t] = m;
+    }
+    if (!mbar_wait(bar, k & 1, &never, kWaitLimitNs)) record(5, kDevTimeout);
+    tc_fence_after();
+    if (warp < 4) {
+      const int j = j0 + warp * 32 + lane;
+      const uint32_t at = tmem + (static_cast<uint32_t>(warp) << 21);
+#pragma unroll 1
+      for (int c = 0; c < cnt; ++c) {
+        float best = -INFINITY;
+#pragma unroll 1
+        for (int g = 0; g < G; g += 8) {
+          uint32_t u[8];
+          tmem_ld8(at + c * G + g, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (g + i < G) best = fmaxf(best, __uint_as_float(u[i]));
+        }
+        if (j * kBlock <= len - p.Nq + n0 + c) p.scores[(lrow0 + static_cast<long long>(c) * p.Hkv) * p.n_blocks + j] = best;
+      }
+    }
+    tc_fence_before();
+    __syncthreads();  // scores, bounds and norms are read
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
@@ -869,10 +1030,26 @@ cudaError_t launch_key_bounds(const KeyBoundsParams& p, cudaStream_t stream) {
                           0, stream, p, slabs);
 }
 
-template <int D, int N>
+template <int D>
+cudaError_t launch_score_few(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
+  using L = FewLayout<D>;
+  auto kern = score_few_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int seqs = (token0 + tokens - 1) / p.Nq - token0 / p.Nq + 1, block_tiles = (p.n_blocks + 127) / 128;
+  // two CTAs an SM, twice: sequences differ in their blocks
+  const long long others = static_cast<long long>(p.Hkv) * seqs;
+  long long parts = others >= 608 ? 1 : (608 + others - 1) / others;
+  if (parts > block_tiles) parts = block_tiles;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(p.Hkv), static_cast<unsigned>(seqs)),
+                          kThreads, L::kAlloc, stream, p, token0, tokens);
+}
+
+template <int D>
 cudaError_t launch_score_mma(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
-  using L = MmaLayout<D, N>;
-  auto kern = score_mma_kernel<D, N>;
+  using L = MmaLayout<D>;
+  constexpr int N = L::N;
+  auto kern = score_mma_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   const int seqs = (token0 + tokens - 1) / p.Nq - token0 / p.Nq + 1;
@@ -890,9 +1067,9 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
   const int rows = p.Nq * (p.Hq / p.Hkv);
   cudaError_t e;
   if (rows <= 16)
-    e = p.d == 64 ? launch_score_mma<64, 16>(p, token0, tokens, stream) : launch_score_mma<128, 16>(p, token0, tokens, stream);
+    e = p.d == 64 ? launch_score_few<64>(p, token0, tokens, stream) : launch_score_few<128>(p, token0, tokens, stream);
   else
-    e = p.d == 64 ? launch_score_mma<64, 128>(p, token0, tokens, stream) : launch_score_mma<128, 128>(p, token0, tokens, stream);
+    e = p.d == 64 ? launch_score_mma<64>(p, token0, tokens, stream) : launch_score_mma<128>(p, token0, tokens, stream);
   if (e != cudaSuccess) return e;
   const int n = tokens * p.Hkv;
   if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
