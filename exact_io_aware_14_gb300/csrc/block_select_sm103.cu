@@ -805,12 +805,15 @@ cudaError_t launch_choose_warp(const SelectParams& p, int token0, int rows, cuda
                           32 * kChooseWarps, 0, stream, p, token0, rows);
 }
 
-// One CTA for a row of more.
+// One CTA for a row of more.  K > 0: up to 256 K candidates, whose keys stay in
+// registers; 0: any number.
+template <int K>
 __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, int token0) {
   grid_depends();
   extern __shared__ float s_score[];  // [min(n_blocks, kHeld)]
   __shared__ unsigned s_hist[256];
   __shared__ int s_pick, s_left, s_count[2];
+  __shared__ uint32_t s_turn[2][kThreads / 32];
   __shared__ unsigned s_warp[kThreads / 32];
   __shared__ int s_id[kBand];
   __shared__ double s_exact[kBand];
@@ -842,47 +845,63 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
     const float band = band_of(p, r, h, lrow);
     const bool all = !(band < 1e38f), pairs = band > 1e-18f && band < 1e18f;
     if (!all) {
-      // the k-th largest, a byte of its key at a time
-      uint32_t prefix = 0;
-      int want = k;
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        s_hist[tid] = 0;
-        __syncthreads();
+      // the k-th largest, as in the warps' form: counts of the keys at or above a
+      // value, a bit at a time
+      uint32_t key[K > 0 ? K : 1];
+      uint32_t top = 0u, bottom = 0xffffffffu;
+      if constexpr (K > 0) {
+#pragma unroll
+        for (int m = 0; m < K; ++m) {
+          const int i = m * kThreads + tid;
+          key[m] = i < n ? ordered(s_score[i]) : 0u;
+          top = max(top, key[m]);
+          bottom = min(bottom, i < n ? key[m] : 0xffffffffu);
+        }
+      } else {
         for (int i = tid; i < n; i += kThreads) {
           const uint32_t u = ordered(score(i));
-          if (shift == 24 || (u >> (shift + 8)) == prefix) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
+          top = max(top, u);
+          bottom = min(bottom, u);
         }
-        __syncthreads();
-        if (warp == 0) {
-          // bins from the top, 8 a lane
-          unsigned c[8], sum = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[255 - (lane * 8 + i)];
-          unsigned incl = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-          }
-          unsigned before = incl - sum;
-          if (before < static_cast<unsigned>(want) && static_cast<unsigned>(want) <= incl) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (before < static_cast<unsigned>(want) && static_cast<unsigned>(want) <= before + c[i]) {
-                s_pick = 255 - (lane * 8 + i);
-                s_left = want - static_cast<int>(before);
-              }
-              before += c[i];
-            }
-          }
-        }
-        __syncthreads();
-        prefix = (prefix << 8) | static_cast<uint32_t>(s_pick);
-        want = s_left;
       }
-      const float t = unordered(prefix);
-      t_hi = t + band;
-      t_lo = t - band;
+      top = __reduce_max_sync(0xffffffffu, top);
+      bottom = __reduce_min_sync(0xffffffffu, bottom);
+      if (lane == 0) {
+        s_turn[0][warp] = top;
+        s_turn[1][warp] = bottom;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        top = max(top, s_turn[0][w]);
+        bottom = min(bottom, s_turn[1][w]);
+      }
+      __syncthreads();
+      const float large = fmaxf(fabsf(unordered(top)), fabsf(unordered(bottom)));
+      const int last = min(max(static_cast<int>(__float_as_uint(band) >> 23) - 2 - (static_cast<int>(__float_as_uint(large) >> 23) - 23), 0), 24);
+      const int differ = 32 - __clz(top ^ bottom);  // bits from here on down
+      uint32_t t0 = differ == 32 ? 0u : top >> differ << differ;
+#pragma unroll 1
+      for (int bit = differ - 1; bit >= last; --bit) {
+        const uint32_t c = t0 | 1u << bit;
+        int cnt = 0;
+        if constexpr (K > 0) {
+#pragma unroll
+          for (int m = 0; m < K; ++m) cnt += key[m] >= c ? 1 : 0;
+        } else {
+          for (int i = tid; i < n; i += kThreads) cnt += ordered(score(i)) >= c ? 1 : 0;
+        }
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (lane == 0) s_turn[bit & 1][warp] = static_cast<uint32_t>(cnt);
+        __syncthreads();
+        cnt = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) cnt += static_cast<int>(s_turn[bit & 1][w]);
+        if (cnt >= k) t0 = c;
+      }
+      const uint32_t rest = differ > last ? (1u << last) - 1u : (differ == 32 ? 0xffffffffu : (1u << differ) - 1u);
+      t_hi = unordered(t0 | rest) + band;
+      t_lo = unordered(t0) - band;
     } else {
       t_hi = INFINITY;
       t_lo = -INFINITY;
@@ -956,6 +975,44 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
     }
   }
   // the chosen blocks in ascending order
+  if (mode != 2 && r.nb <= kHeld) {
+    // a bit for each, the words' sums, then each to its place
+    __shared__ uint32_t s_bits[kHeld / 32];
+    __shared__ int s_before[kHeld / 32];
+    const int words = (r.nb + 31) >> 5;
+    for (int base = 0; base < r.nb; base += kThreads) {
+      const int j = base + tid, i = j - c0;
+      bool in = j < r.nb && (j < c0 || j >= c1);
+      if (k > 0 && i >= 0 && i < n) in = mode == 0 ? score(i) >= t_lo : score(i) > t_hi;
+      const unsigned vote = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) s_bits[(base >> 5) + warp] = vote;
+    }
+    __syncthreads();
+    if (mode == 1)
+      for (int m = tid; m < s_count[1]; m += kThreads)
+        if (s_id[m] >= 0) atomicOr(&s_bits[(s_id[m] + c0) >> 5], 1u << ((s_id[m] + c0) & 31));
+    __syncthreads();
+    if (warp == 0) {
+      int sum = 0;
+      for (int w0 = 0; w0 < words; w0 += 32) {
+        const int mine = w0 + lane < words ? __popc(s_bits[w0 + lane]) : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        if (w0 + lane < words) s_before[w0 + lane] = sum + incl - mine;
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+    for (int j = tid; j < r.nb; j += kThreads) {
+      const uint32_t w = s_bits[j >> 5];
+      if (w >> lane & 1u) out[s_before[j >> 5] + __popc(w & ((1u << lane) - 1u))] = j;
+    }
+    return;
+  }
   __shared__ int s_done, s_equal;
   if (tid == 0) s_done = s_equal = 0;
   __syncthreads();
@@ -1078,8 +1135,8 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
   // many rows: a warp each; few: a CTA each
   if (p.n_blocks <= 2048 && n > 2432) return launch_choose_warp<64>(p, token0, n, stream);
   const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
-  return launch_dependent(choose_kernel, dim3(static_cast<unsigned>(n)), kThreads, held * static_cast<int>(sizeof(float)), stream,
-                          p, token0);
+  return launch_dependent(p.n_blocks <= 8 * kThreads ? choose_kernel<8> : choose_kernel<0>, dim3(static_cast<unsigned>(n)), kThreads,
+                          held * static_cast<int>(sizeof(float)), stream, p, token0);
 }
 
 cudaError_t status_word_select(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_select_status); }
