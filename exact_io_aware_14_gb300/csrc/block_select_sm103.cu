@@ -639,6 +639,17 @@ __device__ __forceinline__ float band_of(const SelectParams& p, const RowSpan& r
   return band <= 3e38f ? band : INFINITY;
 }
 
+// Whether all heads of a row are zeros (a padded token): every score is then 0
+// and the lowest indexes win, without 64-bit scores for all.  By a warp.
+__device__ __forceinline__ bool zero_row(const SelectParams& p, int token, int h, int lrow) {
+  if (p.q_norm[lrow] != 0.f) return false;
+  const int chunks = p.Hq / p.Hkv * (p.d >> 3);
+  const uint4* q = static_cast<const uint4*>(p.q) + (static_cast<long long>(token) * p.Hkv + h) * chunks;
+  uint32_t any = 0;
+  for (int i = threadIdx.x & 31; i < chunks; i += 32) any |= (q[i].x | q[i].y | q[i].z | q[i].w) & 0x7fff7fffu;
+  return __any_sync(0xffffffffu, any != 0u) == 0;
+}
+
 constexpr int kHeld = 8192;   // scores kept in shared memory
 constexpr int kBand = 1024;   // blocks scored again at most, else all by passes over 64-bit keys
 
@@ -677,7 +688,11 @@ __global__ void __launch_bounds__(32 * kChooseWarps) choose_warp_kernel(const Se
     else
       in2 |= 1u << (m - 32);
   };
-  if (k > 0) {
+  if (k > 0 && zero_row(p, token, h, lrow) && band_of(p, r, h, lrow) < 1e38f) {
+#pragma unroll
+    for (int m = 0; m < K; ++m)
+      if (32 * m + lane >= c0 && 32 * m + lane < c0 + k) take(m);
+  } else if (k > 0) {
     const float band = band_of(p, r, h, lrow);
     uint32_t lo = 1u, hi = 0xffffffffu;  // without a bound on the errors all candidates lie between
     if (band < 1e38f) {
@@ -828,8 +843,11 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
     for (int i = tid; i < p.topk; i += kThreads) out[i] = i < r.nb ? i : -1;
     return;
   }
-  // candidates [c0, c1), k of them wanted; sink + local <= topk < nb
-  const int c0 = p.sink, c1 = r.nb - p.local, k = p.topk - p.sink - p.local;
+  // candidates [c0, c1), k of them wanted; sink + local <= topk < nb.  Those of a row of zeros are the first ones: k
+  // more at the front, none of the others
+  const bool zeros = zero_row(p, token, h, lrow) && band_of(p, r, h, lrow) < 1e38f;
+  const int all_k = p.topk - p.sink - p.local;
+  const int c0 = p.sink + (zeros ? all_k : 0), c1 = r.nb - p.local, k = zeros ? 0 : all_k;
   const int n = c1 - c0;
   const float* scores = p.scores + static_cast<long long>(lrow) * p.n_blocks + c0;
   const bool held = n <= kHeld;

@@ -56,6 +56,8 @@ SHARED = [
     (5, 1, 16, 16, 64, 64, 640, [641, 700, 1500, 642, 900]),
     (1, 1, 8, 2, 128, 64, 0, [5000]),
     (2, 1, 4, 1, 128, 256, 1536, [2500, 1537]),
+    (700, 1, 2, 1, 64, 64, 64, [65 + i % 70 for i in range(700)]),   # more sequences than threads
+    (400, 1, 40, 1, 64, 64, 0, [1 + i % 90 for i in range(400)]),    # the same, with more rows than few
 ]
 
 

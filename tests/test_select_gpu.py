@@ -125,6 +125,16 @@ def test_values_that_are_not_numbers_and_zeros(what):
         assert 7 in got[0, 0, 0 if what == "nan key" else 1].tolist()
 
 
+@pytest.mark.parametrize("n", [300, 1500, 2500])
+def test_a_padded_token_takes_the_lowest_blocks(n):
+    q, kb, table = case(n, 1, 2, 4, 1, 64, 64, n)
+    q[0, 0] = 0
+    q[0, 0, 1, 3] = -0.0
+    got = run(q, kb, table, [64 * n], 12, 1, 2)
+    assert torch.equal(got, P.select(q, kb, table, 64, [64 * n], 12, 1, 2))
+    assert got[0, 0, 0].tolist() == list(range(10)) + [n - 2, n - 1]
+
+
 def test_products_outside_the_range_of_32_bits():
     n = 24
     for size in (2.0 ** 100, 2.0 ** -100):
