@@ -110,7 +110,7 @@ def _open(path):
     L.attn_select_blocks_paged.restype = i
     L.attn_select_blocks_paged.argtypes = [vp, vp, vp, i, i, i, vp, vp, i, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_fwd_blocks_paged_workspace_size.restype = sz
-    L.attn_fwd_blocks_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_fwd_blocks_paged_workspace_size.argtypes = [i, i, i, i, i, i, i]
     L.attn_fwd_blocks_paged.restype = i
     L.attn_fwd_blocks_paged.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, i, vp, vp, i, i, i, i, i, f, vp, sz, vp]
     L.attn_get_device_status.restype = i
@@ -622,12 +622,12 @@ def _pools(q, k_pages, v_pages, block_table, seqlens, dev):
             _need("v_pages", v_pages, _BF16, pools, dev), bt, max_blocks, pools[1], pools[0], sl), pools[2]
 
 
-def _attend(name, size, q, pools, Hkv, extra, scale, workspace, dev):
+def _attend(name, size, q, pools, Hkv, extra, scale, workspace, dev, *sizes):
     B, Nq, Hq, d = q.shape
     o = torch.empty(q.shape, dtype=_BF16, device=dev)
     lse = torch.empty((B, Hq, Nq), dtype=_F32, device=dev)
     if workspace is None:
-        n = _fn(size)(B, Nq, Hq, Hkv, d)
+        n = _fn(size)(B, Nq, Hq, Hkv, d, *sizes)
         workspace = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
     ws, n = _space(workspace, dev)
     _call(name, dev, None, *pools, *extra, o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d, scale, ws, n)
@@ -695,7 +695,8 @@ def attend_blocks_paged(q, k_pages, v_pages, block_table, seqlens, blocks, scale
     pools, Hkv = _pools(q, k_pages, v_pages, block_table, seqlens, dev)
     n_sel = blocks.shape[-1]
     return _attend("attn_fwd_blocks_paged", "attn_fwd_blocks_paged_workspace_size", q, pools, Hkv,
-                   (_need("blocks", blocks, _I32, q.shape[:2] + (Hkv, n_sel), dev), n_sel), scale, workspace, dev)
+                   (_need("blocks", blocks, _I32, q.shape[:2] + (Hkv, n_sel), dev), n_sel), scale, workspace, dev,
+                   n_sel, min(pools[4] * pools[5], 0x7fffffff))
 
 
 def attn_get_device_status(stream=None):

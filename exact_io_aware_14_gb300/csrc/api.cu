@@ -355,6 +355,7 @@ attn_status attn_get_device_status(void* stream) {
       attn::status_word_select(&words.at[7]) != cudaSuccess ||
       attn::status_word_wide_rows(&words.at[8]) != cudaSuccess ||
       attn::status_word_few_rows(&words.at[9]) != cudaSuccess ||
+      attn::status_word_by_block(&words.at[10]) != cudaSuccess ||
       attn::fetch_status(words, s, &w) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
   switch (w & 0xffu) {

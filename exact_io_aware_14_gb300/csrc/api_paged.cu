@@ -98,14 +98,82 @@ size_t rows_workspace(const attn::RowsSizes& z, int B, int d, bool lists) {
   return 16 + round32(lists ? 0 : (static_cast<size_t>(B) + 3) * sizeof(long long)) + rows * (d + 1) * sizeof(float);
 }
 
+// Attention over listed blocks, block by block: its workspace, laid out from a multiple of 32 bytes on.
+struct ByBlockSpace {
+  size_t o_part, lse_part, tiles, counts, n_tiles, rank, order, end;
+};
+ByBlockSpace by_block_space(const attn::ByBlockSizes& z, int Hkv, int d, long long n_blocks) {
+  ByBlockSpace w;
+  w.o_part = 0;
+  w.tiles = static_cast<size_t>(z.rows) * d * 4;
+  w.lse_part = w.tiles + static_cast<size_t>(z.groups) * z.tile_cap * 16;
+  w.counts = w.lse_part + static_cast<size_t>(z.rows) * 4;
+  w.n_tiles = w.counts + static_cast<size_t>(z.groups) * Hkv * n_blocks * 4;
+  w.rank = w.n_tiles + static_cast<size_t>(z.groups) * 4;
+  w.order = w.rank + static_cast<size_t>(z.entries) * 4;
+  w.end = w.order + static_cast<size_t>(z.entries) * 4;
+  return w;
+}
+size_t lists_workspace(int B, int Nq, int Hq, int Hkv, int d, int n_sel, long long n_blocks) {
+  const attn::ByBlockSizes z = attn::by_block_sizes(B, Nq, Hq, Hkv, d, n_sel, n_blocks);
+  if (z.chunks > 0) return 16 + by_block_space(z, Hkv, d, n_blocks).end;
+  return rows_workspace(attn::rows_sizes(B, Nq, Hq, Hkv, true), B, d, true);
+}
+
 // Both attention calls, behind their checks.  blocks: listed ones, or null.
 attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages, const int* block_table, int max_blocks,
                         int page_size, int num_pages, const int* seqlens, const int* blocks, int n_sel, int shared_len,
                         void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d, float scale, void* workspace,
                         size_t workspace_bytes, void* stream) {
   const attn::RowsSizes z = attn::rows_sizes(B, Nq, Hq, Hkv, blocks != nullptr);
-  if (!workspace || off(workspace, 16) || workspace_bytes < rows_workspace(z, B, d, blocks != nullptr))
+  const long long n_blocks = static_cast<long long>(max_blocks) * (page_size / 64);
+  if (!workspace || off(workspace, 16) ||
+      workspace_bytes < (blocks ? lists_workspace(B, Nq, Hq, Hkv, d, n_sel, n_blocks) : rows_workspace(z, B, d, false)))
     return ATTN_ERR_WORKSPACE;
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  char* ws = reinterpret_cast<char*>(round32(reinterpret_cast<uintptr_t>(workspace)));
+  CUtensorMap tm_q, tm_qs, tm_k, tm_v;
+  if (!attn::make_map_pages(&tm_k, k_pages, num_pages, page_size, Hkv, d) ||
+      !attn::make_map_pages(&tm_v, v_pages, num_pages, page_size, Hkv, d))
+    return ATTN_ERR_LAUNCH;
+  const attn::ByBlockSizes by =
+      blocks ? attn::by_block_sizes(B, Nq, Hq, Hkv, d, n_sel, n_blocks) : attn::ByBlockSizes{};
+  if (by.chunks > 0) {
+    const ByBlockSpace w = by_block_space(by, Hkv, d, n_blocks);
+    attn::ByBlockParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.block_table = block_table;
+    p.seqlens = seqlens;
+    p.blocks = blocks;
+    p.o = o;
+    p.lse = lse;
+    p.o_part = reinterpret_cast<float*>(ws + w.o_part);
+    p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
+    p.tiles = reinterpret_cast<int4*>(ws + w.tiles);
+    p.counts = reinterpret_cast<int*>(ws + w.counts);
+    p.n_tiles = reinterpret_cast<int*>(ws + w.n_tiles);
+    p.rank = reinterpret_cast<int*>(ws + w.rank);
+    p.order = reinterpret_cast<int*>(ws + w.order);
+    p.max_blocks = max_blocks;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.n_sel = n_sel;
+    p.n_blocks = static_cast<int>(n_blocks);
+    p.B = B;
+    p.Nq = Nq;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.d = d;
+    p.chunks = by.chunks;
+    p.chunk_tokens = by.chunk_tokens;
+    p.tile_tokens = by.tile_tokens;
+    p.tile_cap = by.tile_cap;
+    p.scale_log2 = scale_log2;
+    p.list_len = attn::FastDiv(static_cast<uint32_t>(n_sel));
+    return attn::launch_by_block(p, tm_k, tm_v, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                                   : ATTN_ERR_LAUNCH;
+  }
   attn::RowsParams p;
   std::memset(&p, 0, sizeof p);
   p.block_table = block_table;
@@ -123,7 +191,7 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.d = d;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  p.scale_log2 = scale_log2;
   p.tile_tokens = z.tile_tokens;
   p.pairs = z.pairs;
   p.own_tokens = z.own_tokens;
@@ -131,19 +199,15 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
   p.unit_tokens = z.unit_tokens;
   p.unit_rows = z.unit_rows;
   p.pair_rows = z.pair_rows;
-  char* ws = reinterpret_cast<char*>(round32(reinterpret_cast<uintptr_t>(workspace)));
   if (!blocks) {
     p.sums = reinterpret_cast<long long*>(ws);
     ws += round32((static_cast<size_t>(B) + 3) * sizeof(long long));
   }
   p.o_part = reinterpret_cast<float*>(ws);
   p.lse_part = p.o_part + static_cast<size_t>(z.pair_rows + z.lane_pieces * z.unit_rows) * d;
-  CUtensorMap tm_q, tm_qs, tm_k, tm_v;
   const long long tokens = static_cast<long long>(B) * Nq;
   if (!attn::make_map_group(&tm_q, q, tokens, Hkv, Hq / Hkv, d, z.tile_tokens) ||
-      !attn::make_map_group(&tm_qs, q, tokens, Hkv, Hq / Hkv, d, z.unit_tokens) ||
-      !attn::make_map_pages(&tm_k, k_pages, num_pages, page_size, Hkv, d) ||
-      !attn::make_map_pages(&tm_v, v_pages, num_pages, page_size, Hkv, d))
+      !attn::make_map_group(&tm_qs, q, tokens, Hkv, Hq / Hkv, d, z.unit_tokens))
     return ATTN_ERR_LAUNCH;
   return attn::launch_rows(p, tm_q, tm_qs, tm_k, tm_v, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
@@ -301,9 +365,10 @@ attn_status attn_select_blocks_paged(const void* q, const void* k_bounds, const 
   return ATTN_OK;
 }
 
-size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
+size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d, int n_sel, int max_seqlen) {
   if (B < 1 || check_heads(Nq, Hq, Hkv, d) != ATTN_OK || Hq / Hkv > 128) return 0;
-  return rows_workspace(attn::rows_sizes(B, Nq, Hq, Hkv, true), B, d, true);
+  if (n_sel < 1 || n_sel > attn::kMaxListed || max_seqlen < 64) return 0;
+  return lists_workspace(B, Nq, Hq, Hkv, d, n_sel, max_seqlen / 64);
 }
 
 attn_status attn_fwd_blocks_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,

@@ -260,6 +260,42 @@ cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUte
 constexpr int kFewRows = 32;
 cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             int grid, bool after_pairs, cudaStream_t stream);
+// The same over listed blocks, block by block: for many tokens with few heads a group.
+constexpr int kByBlockHeads = 8;                  // heads of a group at most
+constexpr long long kByBlockBytes = 256 << 20;    // outputs of a chunk's pieces at most
+constexpr long long kByBlockEntries = 1 << 16;    // list entries of a chunk at least
+constexpr long long kByBlockShare = 4;            // and of each block of a full table, on average
+struct ByBlockSizes {
+  int chunks;         // of a sequence's tokens; 0: token by token
+  int chunk_tokens, tile_tokens;
+  long long tile_cap;  // tiles of a chunk at most
+  long long groups;    // chunks of all sequences
+  long long rows;      // of a chunk's pieces
+  long long entries;
+};
+ByBlockSizes by_block_sizes(int B, int Nq, int Hq, int Hkv, int d, int n_sel, long long n_blocks);
+struct ByBlockParams {
+  const void* q;
+  const int* block_table;
+  const int* seqlens;
+  const int* blocks;  // [B, Nq, Hkv, n_sel]
+  void* o;
+  float* lse;
+  float* o_part;      // [rows, d]
+  float* lse_part;    // [rows], base 2
+  int4* tiles;        // [groups, tile_cap]: block of (KV head, block), first entry in its order, entries, first group of 8 keys
+  int* counts;        // [groups, Hkv, n_blocks]: entries of a block, then the first one's place
+  int* n_tiles;       // [groups]
+  int* rank;          // [B, Nq, Hkv, n_sel]: place among the block's entries
+  int* order;         // the same size: the entries of a chunk, block by block
+  int max_blocks, page_size, num_pages, n_sel, n_blocks;
+  int B, Nq, Hq, Hkv, d;
+  int chunks, chunk_tokens, tile_tokens;
+  long long tile_cap;
+  float scale_log2;
+  FastDiv list_len;   // n_sel
+};
+cudaError_t launch_by_block(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream);
 // Maps of bf16 tensors: a page pool as {64, 8, d / 64, groups of 8 keys, Hkv}, boxes of a head's 64 keys; q's of
 // `tokens` tokens of a group of heads.
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d);
@@ -276,7 +312,8 @@ cudaError_t status_word_paging(uint32_t** at);
 cudaError_t status_word_select(uint32_t** at);
 cudaError_t status_word_wide_rows(uint32_t** at);
 cudaError_t status_word_few_rows(uint32_t** at);
-constexpr int kStatusUnits = 10;
+cudaError_t status_word_by_block(uint32_t** at);
+constexpr int kStatusUnits = 11;
 struct StatusWords {
   uint32_t* at[kStatusUnits];
 };

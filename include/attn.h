@@ -520,8 +520,10 @@ ATTN_API attn_status attn_select_blocks_paged(const void* q, const void* k_bound
                                               int* blocks, int B, int Nq, int Hq, int Hkv, int d, int topk, int sink,
                                               int local, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace attn_fwd_blocks_paged needs; 0 for invalid arguments. */
-ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+/* Bytes of workspace attn_fwd_blocks_paged needs with n_sel entries a list and
+ * tables of max_seqlen keys (max_blocks * page_size); 0 for invalid arguments. */
+ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d, int n_sel,
+                                                     int max_seqlen);
 
 /*
  * (3) Attention of each new token over the keys of its listed blocks that it
@@ -530,7 +532,9 @@ ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int 
  *            are passed over, as are blocks behind the token's position; a block
  *            listed twice counts twice; n_sel is at most 512; an entry past the table is passed over
  *            and reported as ATTN_ERR_DEVICE_ARG by attn_get_device_status;
- *   workspace: attn_fwd_blocks_paged_workspace_size bytes.
+ *   workspace: attn_fwd_blocks_paged_workspace_size bytes.  Where a block is
+ *            listed by many tokens it holds what each entry gives, up to 256 MB
+ *            at a time, with the entries sorted by their block.
  * The other arguments, limits and results are those of
  * attn_fwd_splitkv_paged_shared.  Nq may be in the thousands (a prompt, or a
  * chunk of one).  Only keys and values that the row sees enter its result; what

@@ -128,17 +128,26 @@ def test_list_and_prefix_checks(L, listed, want, kw):
 
 
 def test_workspace_sizes(L):
-    for f in (L.attn_splitkv_paged_shared_workspace_size, L.attn_fwd_blocks_paged_workspace_size):
+    lists = lambda *a: L.attn_fwd_blocks_paged_workspace_size(*a, 4, 1024)
+    for f in (L.attn_splitkv_paged_shared_workspace_size, lists):
         n = f(4, 2, 8, 2, 64)
         assert 0 < n < 1 << 28
         assert f(0, 2, 8, 2, 64) == f(4, 0, 8, 2, 64) == f(4, 2, 9, 2, 64) == f(4, 2, 8, 2, 65) == f(4, 2, 258, 2, 64) == 0
     assert attend(L, False, wsb=L.attn_splitkv_paged_shared_workspace_size(4, 2, 8, 2, 64) - 1) == 7
-    assert attend(L, True, wsb=L.attn_fwd_blocks_paged_workspace_size(4, 2, 8, 2, 64) - 1) == 7
+    assert attend(L, True, wsb=lists(4, 2, 8, 2, 64) - 1) == 7
     n = L.attn_select_blocks_workspace_size(4, 2, 2, 1024)
     assert n >= 4 * 2 * 2 * 16 * 4 and select(L, wsb=n - 1) == 7
     assert L.attn_select_blocks_workspace_size(0, 2, 2, 1024) == L.attn_select_blocks_workspace_size(4, 2, 2, 63) == 0
-    # a list's workspace does not grow with the tokens
-    assert L.attn_fwd_blocks_paged_workspace_size(1, 4096, 8, 2, 64) == L.attn_fwd_blocks_paged_workspace_size(1, 1, 8, 2, 64)
+    assert L.attn_fwd_blocks_paged_workspace_size(4, 2, 8, 2, 64, 0, 1024) == 0
+    assert L.attn_fwd_blocks_paged_workspace_size(4, 2, 8, 2, 64, 513, 1024) == 0
+    assert L.attn_fwd_blocks_paged_workspace_size(4, 2, 8, 2, 64, 4, 63) == 0
+    # lists of few tokens, and those over many blocks, take the same whatever their number; others are sorted, with
+    # what the entries give held for a chunk of the tokens
+    wide = lambda Nq: L.attn_fwd_blocks_paged_workspace_size(1, Nq, 8, 2, 64, 32, 1 << 24)
+    assert wide(4096) == wide(1)
+    near = lambda Nq: L.attn_fwd_blocks_paged_workspace_size(1, Nq, 8, 2, 64, 32, 16384)
+    assert near(16) == near(1) and near(4096) > 4096 * 8 * 32 * 65 * 4
+    assert near(1 << 16) < (256 << 20) * 1.1 + (1 << 16) * 2 * 32 * 8
 
 
 def test_the_binding_refuses_what_is_not_on_a_gpu_or_of_another_shape():

@@ -126,7 +126,8 @@ def guarded(n, dtype):
 def test_nothing_is_written_outside(kind, B, Nq, Hq, Hkv, d):
     lens = [400 + i % 7 for i in range(B)]
     q, kp, vp, table = (x.cuda() for x in make(5, B, Nq, Hq, Hkv, d, 64, 128, lens))
-    size = A.lib().attn_splitkv_paged_shared_workspace_size if kind == "shared" else A.lib().attn_fwd_blocks_paged_workspace_size
+    shared, lists = A.lib().attn_splitkv_paged_shared_workspace_size, A.lib().attn_fwd_blocks_paged_workspace_size
+    size = shared if kind == "shared" else lambda *a: lists(*a, 4, 64 * table.shape[1])
     ws, ok_ws = guarded(size(B, Nq, Hq, Hkv, d), torch.uint8)
     o, ok_o = guarded(q.numel(), torch.bfloat16)
     lse, ok_lse = guarded(B * Hq * Nq, torch.float32)
@@ -190,6 +191,139 @@ def test_listed_blocks(B, Nq, Hq, Hkv, d, page, lens, n_sel):
     o, lse = A.attend_blocks_paged(*(x.cuda() for x in (q, kp, vp, table)), i32(lens), blocks.cuda(), d ** -0.5)
     assert A.attn_get_device_status() == 0
     P.check(o, lse, P.attend(q, kp, vp, table, page, d ** -0.5, listed(blocks, lens, Nq)))
+
+
+# Many tokens on few blocks: sorted by block, and taken block by block.
+BY_BLOCK = [
+    (1, 900, 8, 2, 128, 64, [2100], 40),
+    (2, 850, 6, 2, 64, 192, [850, 2900], 41),     # three heads: 126 rows a tile; lists that are not full
+    (1, 1024, 8, 1, 128, 128, [1500], 64),
+    (1, 700, 3, 3, 64, 64, [1000], 33),           # one head: tiles of 128 tokens
+    (3, 1400, 5, 1, 128, 256, [5000, 100, 0], 47),  # tokens that see nothing, a sequence without keys
+    (1, 384, 8, 1, 128, 64, [33100], 512),        # chunks of tokens
+]
+
+
+def by_block(Nq, Hq, Hkv, d, n_sel, keys):
+    """Whether such a call is taken block by block: its workspace holds what each entry gives."""
+    size = A.lib().attn_fwd_blocks_paged_workspace_size(1, Nq, Hq, Hkv, d, n_sel, keys)
+    return size > 10 * A.lib().attn_fwd_blocks_paged_workspace_size(1, 1, Hq, Hkv, d, n_sel, keys)
+
+
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,lens,n_sel", BY_BLOCK)
+def test_listed_blocks_of_many_tokens(B, Nq, Hq, Hkv, d, page, lens, n_sel):
+    q, kp, vp, table = make(B + Nq + n_sel, B, Nq, Hq, Hkv, d, page, 0, lens)
+    assert by_block(Nq, Hq, Hkv, d, n_sel, table.shape[1] * page)
+    blocks = random_blocks(torch.Generator().manual_seed(n_sel), B, Nq, Hkv, n_sel, lens)
+    o, lse = A.attend_blocks_paged(*(x.cuda() for x in (q, kp, vp, table)), i32(lens), blocks.cuda(), -0.1)
+    assert A.attn_get_device_status() == 0
+    P.check(o, lse, P.attend(q, kp, vp, table, page, -0.1, listed(blocks, lens, Nq)))
+
+
+def prompt(seed=21, Nq=850, Hkv=2, n_sel=40, stale=True):
+    lens = [1300]
+    q, kp, vp, table = make(seed, 1, Nq, 4 * Hkv, Hkv, 128, 64, 0, lens, stale=stale)
+    assert by_block(Nq, 4 * Hkv, Hkv, 128, n_sel, table.shape[1] * 64)
+    g = torch.Generator().manual_seed(seed)
+    # in any order, with blocks twice, behind the token and passed over
+    blocks = torch.randint(-2, 1300 // 64 + 1, (1, Nq, Hkv, n_sel), generator=g, dtype=torch.int32)
+    blocks[0, :200, :, 1:] = -1
+    blocks[0, 100:120] = -1
+    return lens, q, kp, vp, table, blocks
+
+
+def test_lists_of_a_prompt_as_a_program_may_write_them():
+    lens, q, kp, vp, table, blocks = prompt()
+    for scale in (0.0, 0.1):
+        o, lse = A.attend_blocks_paged(*(x.cuda() for x in (q, kp, vp, table)), i32(lens), blocks.cuda(), scale)
+        assert A.attn_get_device_status() == 0
+        P.check(o, lse, P.attend(q, kp, vp, table, 64, scale, listed(blocks, lens, 850)))
+
+
+def test_values_that_are_not_numbers_behind_a_prompts_tokens():
+    lens, q, kp, vp, table, blocks = prompt(22)
+    blocks[0, 300:] = torch.where(blocks[0, 300:] == 2, 3, blocks[0, 300:])
+    blocks[0, :300] = torch.where(blocks[0, :300] == 2, 1, blocks[0, :300])
+    args = [x.cuda() for x in (q, kp, vp, table)]
+    base = A.attend_blocks_paged(*args, i32(lens), blocks.cuda(), 0.1)
+    P.check(*base, P.attend(q, kp, vp, table, 64, 0.1, listed(blocks, lens, 850)))
+
+    def at(key):
+        return args[3][0, key // 64].long(), key % 64
+    args[1][at(130)[0]], args[2][at(130)[0]] = float("nan"), float("nan")  # a block that nobody lists
+    args[1][at(1299)] = float("nan")
+    args[2][at(1100)[0], at(1100)[1], 1, 77] = float("inf")
+    args[2][at(1111)[0], at(1111)[1], 1, 77] = float("nan")
+    args[2][at(1090)[0], at(1090)[1], 0, 5] = float("-inf")
+    o, lse = A.attend_blocks_paged(*args, i32(lens), blocks.cuda(), 0.1)
+    # what a token sees of them, and nothing else, is spoiled
+    pos = torch.arange(850) + 1300 - 850
+    lists = blocks[0].long()
+    spoiled = torch.zeros((850, 8, 128), dtype=torch.bool)
+    sees = lambda key, h: ((lists[:, h] == key // 64).any(-1) & (pos >= key))[:, None]
+    spoiled[:, 4:, 77] = sees(1100, 1)
+    spoiled[:, :4, 5] = sees(1090, 0)
+    for h in range(2):
+        spoiled[:, 4 * h:4 * h + 4] |= sees(1299, h)[..., None]
+    spoiled = spoiled.cuda()
+    assert spoiled.any(0).any(-1).all() and not spoiled.all(0).any()
+    assert not o[0][spoiled].isfinite().any()
+    assert torch.equal(o[0][~spoiled], base[0][0][~spoiled])
+    assert torch.equal(lse[..., :849], base[1][..., :849])
+
+
+def test_a_prompts_results_repeat_and_stay_inside_their_memory():
+    lens, q, kp, vp, table, blocks = prompt(23)
+    q, kp, vp, table, blocks = (x.cuda() for x in (q, kp, vp, table, blocks))
+    size = A.lib().attn_fwd_blocks_paged_workspace_size(1, 850, 8, 2, 128, 40, 64 * table.shape[1])
+    outs = []
+    for fill in (0, 255, 0x7f):
+        ws, ok_ws = guarded(size, torch.uint8)
+        ws.fill_(fill)
+        outs.append(A.attend_blocks_paged(q, kp, vp, table, i32(lens), blocks, 0.1, workspace=ws))
+        assert A.attn_get_device_status() == 0 and ok_ws()
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+def test_a_captured_prompt_follows_its_inputs():
+    lens, q, kp, vp, table, blocks = prompt(24, stale=False)
+    args = [x.cuda() for x in (q, kp, vp, table)]
+    sl, bl = i32(lens), blocks.cuda()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        A.attend_blocks_paged(*args, sl, bl, 0.1)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = A.attend_blocks_paged(*args, sl, bl, 0.1)
+    for lens in ([1300], [600], [1299]):
+        blocks = blocks.flip(1)
+        sl.copy_(i32(lens))
+        bl.copy_(blocks)
+        graph.replay()
+        torch.cuda.synchronize()
+        P.check(o, lse, P.attend(q, kp, vp, table, 64, 0.1, listed(blocks, lens, 850)))
+    assert A.attn_get_device_status() == 0
+
+
+def test_bad_lengths_pages_and_blocks_of_a_prompt_are_reported():
+    lens, q, kp, vp, table, blocks = prompt(25, stale=False)
+    want = P.attend(q, kp, vp, table, 64, 0.1, listed(blocks, lens, 850))
+    q, kp, vp, table, blocks = (x.cuda() for x in (q, kp, vp, table, blocks))
+    for bad in (-1, 64 * table.shape[1] + 1):
+        A.attend_blocks_paged(q, kp, vp, table, i32([bad]), blocks, 0.1)
+        assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_ARG
+    for bad in (-1, kp.shape[0]):
+        other = table.clone()
+        other[0, 3] = bad
+        A.attend_blocks_paged(q, kp, vp, other, i32(lens), blocks, 0.1)
+        assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_ARG
+    for bad in (table.shape[1], 0x7fffffff):
+        over = torch.where(blocks == -2, bad, blocks)
+        o, lse = A.attend_blocks_paged(q, kp, vp, table, i32(lens), over, 0.1)
+        assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_ARG
+        P.check(o, lse, want)
 
 
 @pytest.mark.parametrize("rows", [
