@@ -100,18 +100,19 @@ size_t rows_workspace(const attn::RowsSizes& z, int B, int d, bool lists) {
 
 // Attention over listed blocks, block by block: its workspace, laid out from a multiple of 32 bytes on.
 struct ByBlockSpace {
-  size_t o_part, lse_part, tiles, counts, n_tiles, rank, order, end;
+  size_t o_part, tiles, starts, lse_part, counts, n_tiles, rank, order, end;
 };
 ByBlockSpace by_block_space(const attn::ByBlockSizes& z, int Hkv, int d, long long n_blocks) {
   ByBlockSpace w;
   w.o_part = 0;
   w.tiles = static_cast<size_t>(z.rows) * d * 4;
-  w.lse_part = w.tiles + static_cast<size_t>(z.groups) * z.tile_cap * 16;
+  w.starts = w.tiles + static_cast<size_t>(z.groups) * z.tile_cap * 16;
+  w.lse_part = w.starts + static_cast<size_t>(z.groups) * Hkv * n_blocks * 8;
   w.counts = w.lse_part + static_cast<size_t>(z.rows) * 4;
   w.n_tiles = w.counts + static_cast<size_t>(z.groups) * Hkv * n_blocks * 4;
   w.rank = w.n_tiles + static_cast<size_t>(z.groups) * 4;
   w.order = w.rank + static_cast<size_t>(z.entries) * 4;
-  w.end = w.order + static_cast<size_t>(z.entries) * 4;
+  w.end = w.order + static_cast<size_t>(z.groups) * z.tile_cap * z.tile_tokens * 4;
   return w;
 }
 size_t lists_workspace(int B, int Nq, int Hq, int Hkv, int d, int n_sel, long long n_blocks) {
@@ -152,6 +153,7 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
     p.lse_part = reinterpret_cast<float*>(ws + w.lse_part);
     p.tiles = reinterpret_cast<int4*>(ws + w.tiles);
     p.counts = reinterpret_cast<int*>(ws + w.counts);
+    p.starts = reinterpret_cast<int2*>(ws + w.starts);
     p.n_tiles = reinterpret_cast<int*>(ws + w.n_tiles);
     p.rank = reinterpret_cast<int*>(ws + w.rank);
     p.order = reinterpret_cast<int*>(ws + w.order);
@@ -170,8 +172,10 @@ attn_status attend_rows(const void* q, const void* k_pages, const void* v_pages,
     p.tile_tokens = by.tile_tokens;
     p.tile_cap = by.tile_cap;
     p.scale_log2 = scale_log2;
-    p.list_len = attn::FastDiv(static_cast<uint32_t>(n_sel));
-    return attn::launch_by_block(p, tm_k, tm_v, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+    p.tile_len = attn::FastDiv(static_cast<uint32_t>(by.tile_tokens));
+    CUtensorMap tm_o;
+    if (!attn::make_map_pieces(&tm_o, p.o_part, by.rows, d)) return ATTN_ERR_LAUNCH;
+    return attn::launch_by_block(p, tm_k, tm_v, tm_o, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
                                                                                                    : ATTN_ERR_LAUNCH;
   }
   attn::RowsParams p;

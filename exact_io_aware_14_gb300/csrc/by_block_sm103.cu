@@ -29,6 +29,10 @@ namespace {
 __device__ __forceinline__ int length_of(const ByBlockParams& p, int b) {
   return min(max(p.seqlens[b], 0), p.max_blocks * p.page_size);
 }
+// Whether one of two bf16 is infinite or not a number.
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
 // Keys that token i of sequence b sees.
 __device__ __forceinline__ int seen_by(const ByBlockParams& p, int b, int i) { return max(0, length_of(p, b) - p.Nq + i + 1); }
 
@@ -40,7 +44,7 @@ struct ListAt {
   int tok, h, b, i, chunk, seen;
   const int* list;
   long long entry;  // first of its entries
-  int* counts;      // of its sequence, chunk and KV head's blocks
+  long long block0;  // first of the blocks of its sequence, chunk and KV head
 };
 __device__ __forceinline__ bool list_at(const ByBlockParams& p, ListAt& l) {
   const long long w = static_cast<long long>(blockIdx.x) * kSortWarps + (threadIdx.x >> 5);
@@ -53,7 +57,7 @@ __device__ __forceinline__ bool list_at(const ByBlockParams& p, ListAt& l) {
   l.seen = seen_by(p, l.b, l.i);
   l.entry = w * p.n_sel;
   l.list = p.blocks + l.entry;
-  l.counts = p.counts + (static_cast<long long>(l.b * p.chunks + l.chunk) * p.Hkv + l.h) * p.n_blocks;
+  l.block0 = (static_cast<long long>(l.b * p.chunks + l.chunk) * p.Hkv + l.h) * p.n_blocks;
   return true;
 }
 
@@ -65,23 +69,39 @@ __global__ void __launch_bounds__(32 * kSortWarps) count_kernel(const __grid_con
   for (int s = lane; s < p.n_sel; s += 32) {
     const int blk = l.list[s];
     if (blk >= p.n_blocks) record(3, kDevBadPage);
-    if (blk >= 0 && blk < p.n_blocks && blk * 64 < l.seen) p.rank[l.entry + s] = atomicAdd(l.counts + blk, 1);
+    if (blk >= 0 && blk < p.n_blocks && blk * 64 < l.seen) p.rank[l.entry + s] = atomicAdd(p.counts + l.block0 + blk, 1);
   }
 }
 
-// Counts to starts, and the tiles: a CTA a sequence and chunk.
+// Counts to starts, and the tiles: a CTA a chunk and KV head, which adds up what the heads before it have.
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ByBlockParams p) {
   grid_depends();
   __shared__ unsigned long long s_sum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.Hkv * p.n_blocks;
-  int* counts = p.counts + static_cast<long long>(blockIdx.x) * n;
-  int4* tiles = p.tiles + static_cast<long long>(blockIdx.x) * p.tile_cap;
-  const int b = blockIdx.x / p.chunks;
-  unsigned long long base = 0;  // entries, and tiles in the upper half
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x / p.Hkv, h = blockIdx.x - group * p.Hkv, b = group / p.chunks;
+  const int n = p.n_blocks, first_j = h * n;
+  const int* counts = p.counts + static_cast<long long>(group) * p.Hkv * n;
+  int2* starts = p.starts + static_cast<long long>(group) * p.Hkv * n;
+  int4* tiles = p.tiles + static_cast<long long>(group) * p.tile_cap;
+  // tiles, and in the upper half 32's of rows: full tiles take 128, the last one what it needs
+  const int G = p.Hq / p.Hkv;
+  auto packed = [&](int c) {
+    const int full = c / p.tile_tokens, rest = c - full * p.tile_tokens;
+    return static_cast<unsigned long long>(4 * full + (rest * G + 31) / 32) << 32 | static_cast<unsigned>(full + (rest > 0 ? 1 : 0));
+  };
+  unsigned long long base = 0;
+  for (int j = tid; j < first_j; j += kPlanThreads) base += packed(counts[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+  if (lane == 0) s_sum[warp] = base;
+  __syncthreads();
+  base = s_sum[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
   for (int j0 = 0; j0 < n; j0 += kPlanThreads) {
-    const int j = j0 + tid, c = j < n ? counts[j] : 0, t = (c + p.tile_tokens - 1) / p.tile_tokens;
-    const unsigned long long mine = static_cast<unsigned long long>(t) << 32 | static_cast<unsigned>(c);
+    const int blk = j0 + tid, j = first_j + blk, c = blk < n ? counts[j] : 0;
+    const unsigned long long mine = packed(c);
     unsigned long long sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -100,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const unsigned long long before = base + sum - mine + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
     base += __shfl_sync(0xffffffffu, w, 31);
     if (c > 0) {
-      const int start = static_cast<int>(before), first = static_cast<int>(before >> 32), blk = j % p.n_blocks;
+      const int first = static_cast<int>(before), rows = static_cast<int>(before >> 32);
       const int at_page = blk * 64 / p.page_size;
       int g = p.block_table[static_cast<long long>(b) * p.max_blocks + at_page];
       if (g < 0 || g >= p.num_pages) {
@@ -108,24 +128,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         g = 0;
       }
       g = g * (p.page_size / 8) + 8 * (blk - at_page * (p.page_size / 64));
-      for (int k = 0; k < t; ++k) tiles[first + k] = make_int4(j, start + k * p.tile_tokens, min(p.tile_tokens, c - k * p.tile_tokens), g);
-      counts[j] = start;
+      starts[j] = make_int2(first, rows);
+      for (int k = 0; k * p.tile_tokens < c; ++k)
+        tiles[first + k] = make_int4(j, rows + 4 * k, min(p.tile_tokens, c - k * p.tile_tokens), g);
     }
   }
-  if (tid == 0) p.n_tiles[blockIdx.x] = static_cast<int>(base >> 32);
+  if (tid == 0 && h == p.Hkv - 1) p.n_tiles[group] = static_cast<int>(base);
 }
 
-// order: (token of the chunk) * n_sel + place in its list, block after block.
+// order: the tokens of the chunk that list a block, tile after tile.
 __global__ void __launch_bounds__(32 * kSortWarps) place_kernel(const __grid_constant__ ByBlockParams p) {
   grid_depends();
   ListAt l;
   if (!list_at(p, l)) return;
   const int i0 = l.chunk * p.chunk_tokens;
-  const long long first = (static_cast<long long>(l.b) * p.Nq + i0) * p.Hkv * p.n_sel;
+  int* order = p.order + static_cast<long long>(l.b * p.chunks + l.chunk) * p.tile_cap * p.tile_tokens;
   for (int s = threadIdx.x & 31; s < p.n_sel; s += 32) {
     const int blk = l.list[s];
     if (blk >= 0 && blk < p.n_blocks && blk * 64 < l.seen)
-      p.order[first + l.counts[blk] + p.rank[l.entry + s]] = (l.i - i0) * p.n_sel + s;
+      order[static_cast<long long>(p.starts[l.block0 + blk].x) * p.tile_tokens + p.rank[l.entry + s]] = l.i - i0;
   }
 }
 
@@ -143,9 +164,11 @@ struct Layout {
   static constexpr int kBlock = 64 * D * 2;   // K or V of a block
   static constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
   static constexpr int kQ = 128 * D * 2;
-  static constexpr int kQs = 3, kKvs = 3;
+  static constexpr int kQs = 2, kKvs = 3;
+  static constexpr int kOut = 32 * 128;       // outputs on their way to memory: 32 columns of a warp's rows, twice
   static constexpr int kOffKv = kQs * kQ;
-  static constexpr int kOffBar = kOffKv + kKvs * 2 * kBlock;
+  static constexpr int kOffOut = kOffKv + kKvs * 2 * kBlock;
+  static constexpr int kOffBar = kOffOut + 8 * 2 * kOut;
   static constexpr int kNumBars = 2 * kQs + 2 * kKvs + 4 * 2 + 2;
   static constexpr int kOffNote = kOffBar + 8 * kNumBars;  // [kNotes][D] first key with a value that is not finite
   static constexpr int kOffNoted = kOffNote + kNotes * D;  // [kNotes]
@@ -159,7 +182,7 @@ static_assert(Layout<128>::kAlloc <= 232448, "shared memory of a CTA");
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     by_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ ByBlockParams p, int group) {
+                    const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ ByBlockParams p, int group) {
   using L = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -213,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.Hq / p.Hkv;
   const int b = group / p.chunks, i0 = (group - b * p.chunks) * p.chunk_tokens;
   const long long tok0 = static_cast<long long>(b) * p.Nq + i0;
-  const int* order = p.order + tok0 * p.Hkv * p.n_sel;
   const long long total = p.n_tiles[group];
   const int x0 = static_cast<int>(run_start(total, gridDim.x, blockIdx.x));
   const int n = static_cast<int>(run_start(total, gridDim.x, blockIdx.x + 1)) - x0;
   const int4* tiles = p.tiles + static_cast<long long>(group) * p.tile_cap + x0;
+  const int* order = p.order + (static_cast<long long>(group) * p.tile_cap + x0) * p.tile_tokens;
   const int len = length_of(p, b), first_seen = len - p.Nq + i0 + 1;  // keys of all, of the first token (below 1: none)
 
   if (warp == 0) {
@@ -259,35 +282,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* mine = note + kv % kNotes * D;
-          for (int c = lane; c < D; c += 32) mine[c] = 64;
-          __syncwarp();
-          bool any = false;
-          // a lane a chunk of 8 columns, keys in falling order: the first one stays
-#pragma unroll 1
-          for (int r = lane < D / 8 ? 63 : -1; r >= 0; --r) {
-            const int ch = lane;
-            uint4* v = reinterpret_cast<uint4*>(at + L::kBlock + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
-                                                (((ch & 7) ^ (r & 7)) << 4));
-            uint4 w = *v;
-            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-            bool changed = key0 + r >= len;
-            if (changed) {
-              w = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t half = x[k >> 1] >> (16 * (k & 1)) & 0x7f80u;
-                if (half == 0x7f80u) {
-                  x[k >> 1] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
-                  changed = any = true;
-                  mine[8 * ch + k] = static_cast<uint8_t>(r);
-                }
-              }
+          uint8_t* v = at + L::kBlock;
+          if (key0 + 64 > len) {
+            for (int c = lane; c < (key0 + 64 - len) * (D / 8); c += 32) {
+              const int r = len - key0 + c / (D / 8), ch = c % (D / 8);
+              *reinterpret_cast<uint4*>(v + (r >> 3) * L::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
             }
-            if (changed) *v = w;
+            __syncwarp();
+          }
+          bool any = false;
+#pragma unroll 8
+          for (int c = lane; c < L::kBlock / 16; c += 32) {
+            const uint4 w = *reinterpret_cast<const uint4*>(v + c * 16);
+            any = any || not_finite(w.x) || not_finite(w.y) || not_finite(w.z) || not_finite(w.w);
           }
           any = __any_sync(0xffffffffu, any);
+          if (any) {
+            // a lane two columns of 64, keys in falling order: the first one stays
+            uint8_t* mine = note + kv % kNotes * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              int first0 = 64, first1 = 64;
+#pragma unroll 1
+              for (int r = 63; r >= 0; --r) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(v + (r >> 3) * L::kGroup + c * 1024 + (r & 7) * 128 +
+                                                          (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                const uint32_t x = *w;
+                if ((x & 0x7f80u) == 0x7f80u) first0 = r;
+                if ((x & 0x7f800000u) == 0x7f800000u) first1 = r;
+                if (not_finite(x))
+                  *w = x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : ~0u) & ((x & 0x7f800000u) == 0x7f800000u ? 0x0000ffffu : ~0u);
+              }
+              mine[64 * c + 2 * lane] = static_cast<uint8_t>(first0);
+              mine[64 * c + 2 * lane + 1] = static_cast<uint8_t>(first1);
+            }
+          }
           if (lane == 0) noted[kv % kNotes] = any;
           fence_proxy_async_smem();
           __syncwarp();
@@ -308,29 +338,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kQk = idesc_bf16_f32(128, 64, 0), kPv = idesc_bf16_f32(128, D, 1);
       const uint64_t dq = sdesc_sw128(smem_u32(sm_q), 16, 1024), dk = sdesc_sw128(smem_u32(sm_kv), 16, L::kGroup);
       const uint64_t dv = sdesc_sw128(smem_u32(sm_kv) + L::kBlock, 1024, L::kGroup);
-      int cur = -1;
-      uint32_t kv = 0, kv_before = 0;  // blocks taken; slot of the tile before
+      // Scores of tile i and the output of tile j, whichever has what it needs.  Scores go over the P of the tile
+      // before the last, whose product was issued before.
+      int i = 0, j = 0, cur = -1;
+      uint32_t kv = 0, slots = 0, last = 0;  // blocks taken; slots and last tiles of a block of tiles j .. i - 1, low bits first
       bool ok = true;
-      int next = n > 0 ? tiles[0].x : 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-        if (ok) ok = wait_one(bar, parity & 1, abort_flag, site);
-      };
+      int next = n > 0 ? tiles[0].x : 0, after = n > 1 ? tiles[1].x : -1;
+      uint64_t since = globaltimer_ns();
 #pragma unroll 1
-      for (int i = 0; i <= n; ++i) {
-        bool fresh = i == n;
-        if (i < n) {
-          fresh = next != cur;
-          cur = next;
-          if (i + 1 < n) next = tiles[i + 1].x;
-          if (fresh) {
-            wait(kvfull + kv % L::kKvs, kv / L::kKvs, 21);
-            ++kv;
-          }
-          const uint32_t slot = (kv - 1) % L::kKvs, q = i % L::kQs;
-          wait(qfull + q, i / L::kQs, 22);
-          if (!ok) break;
+      for (uint32_t idle = 0; j < n;) {
+        if (j < i && mbar_test_wait(pfull + (j & 1), (j / 2) & 1) && (j < 2 || mbar_test_wait(ofree + (j & 1), (j / 2 - 1) & 1))) {
           tc_fence_after();
-          // over the P of the tile before the last, whose product was issued before
+          const uint32_t slot = slots & 0xff;
+          const uint64_t w = dv + static_cast<uint64_t>((slot * 2 * L::kBlock) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(tmem + 128 + (j & 1) * D, tmem + (j & 1) * 64 + kk * 8, w + ((kk * 2 * L::kGroup) >> 4), kPv,
+                        kk > 0 ? 1u : 0u);
+          mma_commit(odone + (j & 1));
+          if (last & 1) mma_commit(kvempty + slot);
+          slots >>= 8;
+          last >>= 1;
+          ++j;
+          idle = 0;
+        }
+        const uint32_t q = i % L::kQs, slot = (next != cur ? kv : kv - 1) % L::kKvs;
+        if (i < n && i < j + 2 && mbar_test_wait(qfull + q, (i / L::kQs) & 1) &&
+            (next == cur || mbar_test_wait(kvfull + slot, (kv / L::kKvs) & 1))) {
+          tc_fence_after();
           const uint64_t a = dq + static_cast<uint64_t>((q * L::kQ) >> 4), w = dk + static_cast<uint64_t>((slot * 2 * L::kBlock) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -340,22 +375,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(sfull + (i & 1));
           mma_commit(qempty + q);
+          if (next != cur) ++kv;
+          cur = next;
+          slots |= slot << (8 * (i - j));
+          last |= (after != cur ? 1u : 0u) << (i - j);
+          ++i;
+          next = after;
+          after = i + 1 < n ? tiles[i + 1].x : -1;
+          idle = 0;
         }
-        if (i > 0) {
-          const int j = i - 1;
-          wait(pfull + (j & 1), j / 2, 23);
-          if (j >= 2) wait(ofree + (j & 1), j / 2 - 1, 24);
+        if (++idle == 1) {
+          since = globaltimer_ns();
+        } else if (idle % 256 == 0) {
+          if (*abort_flag) {
+            ok = false;
+          } else if (globaltimer_ns() - since > kWaitLimitNs) {
+            record(21, kDevTimeout);
+            *abort_flag = 1;
+            ok = false;
+          }
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t w = dv + static_cast<uint64_t>((kv_before * 2 * L::kBlock) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ts(tmem + 128 + (j & 1) * D, tmem + (j & 1) * 64 + kk * 8, w + ((kk * 2 * L::kGroup) >> 4), kPv,
-                        kk > 0 ? 1u : 0u);
-          mma_commit(odone + (j & 1));
-          if (fresh) mma_commit(kvempty + kv_before);
         }
-        if (i < n) kv_before = (kv - 1) % L::kKvs;
       }
       if (!ok) {
         volatile int no_abort = 0;
@@ -364,77 +404,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 4) {
-    // Queries: a token's G rows of a KV head lie in a row of memory, 16 B a thread.
-    const int tid = threadIdx.x - 64, chunks = G * (D / 8), per = chunks < 64 ? 64 / chunks : 1;  // tokens side by side
-    const int side = per > 1 ? tid / chunks : 0, c0 = per > 1 ? tid - side * chunks : tid;
-    const char* q = static_cast<const char*>(p.q) + tok0 * p.Hq * D * 2;
-    const long long tok_bytes = static_cast<long long>(p.Hq) * D * 2;
+    // Queries: 64 rows a warp, 8 lanes for 128 bytes of a row.  Lane l finds rows l and l + 32 in
+    // memory: a tile's description is loaded three tiles ahead, its tokens two.
+    const int w2 = warp - 2, sub = lane >> 3, ch = lane & 7;
+    const char* q = static_cast<const char*>(p.q) + tok0 * p.Hq * D * 2 + ch * 16;
+    const uint32_t tok_step = p.Hq * (D / 8), group_step = G * (D / 8);  // in 16 bytes
+    const int e0 = (64 * w2 + lane) / G, e1 = (64 * w2 + lane + 32) / G;
+    const uint32_t g0 = (64 * w2 + lane - e0 * G) * (D / 8), g1 = (64 * w2 + lane + 32 - e1 * G) * (D / 8);
+    // where a row starts; kNoRow: there is none
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    struct Found {
+      int head, tok0, tok1;  // (KV head, block), tokens
+    };
+    auto find = [&](const int4& t, int i) {
+      const int* at = order + static_cast<long long>(i) * p.tile_tokens;
+      return Found{t.x, e0 < t.z ? at[e0] : -1, e1 < t.z ? at[e1] : -1};
+    };
+    auto place = [&](int head, int tok, uint32_t g) {
+      return tok < 0 ? kNoRow : tok * tok_step + static_cast<uint32_t>(head / p.n_blocks) * group_step + g;
+    };
+    const int4 none = make_int4(0, 0, 0, 0);
+    auto tile = [&](int i) { return i < n ? tiles[i] : none; };
     bool ok = true;
-    int4 t = n > 0 ? tiles[0] : make_int4(0, 0, 0, 0);
+    Found now = find(tile(0), 0), next = find(tile(1), 1);
+    int4 t = tile(2);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const uint32_t slot = i % L::kQs;
-      const int4 next = i + 1 < n ? tiles[i + 1] : t;
-      if (i >= L::kQs) ok = wait_all(qempty + slot, (i / L::kQs - 1) & 1, abort_flag, 31);
-      if (!ok) break;
-      const uint32_t to = smem_u32(sm_q + slot * L::kQ);
-      const char* head = q + static_cast<long long>(t.x / p.n_blocks) * G * D * 2;
-      for (int e0 = 0; e0 < t.z; e0 += 32) {
-        const int m = min(32, t.z - e0);
-        const int mine = lane < m ? static_cast<int>(p.list_len.div(static_cast<uint32_t>(order[t.y + e0 + lane]))) : 0;
-#pragma unroll 4
-        for (int k = 0; k < m; k += per) {
-          const int e = k + side, tok = __shfl_sync(0xffffffffu, mine, e & 31);
-          if (side >= per || e >= m) continue;
-          const char* from = head + tok * tok_bytes;
-          for (int c = c0; c < chunks; c += 64) {
-            const int r = (e0 + e) * G + c / (D / 8), ch = c % (D / 8);
-            cp_async16(to + (ch >> 3) * L::kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), from + c * 16);
-          }
-        }
-      }
-      cp_async_commit();
-      // the tile before has landed
-      if (i > 0) {
+      // the tile before the last has landed
+      if (i > 1) {
         cp_async_wait<1>();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(qfull + (i - 1) % L::kQs);
+        if (lane == 0) mbar_arrive(qfull + (i - 2) % L::kQs);
       }
-      t = next;
+      if (i >= L::kQs) ok = wait_all(qempty + slot, (i / L::kQs - 1) & 1, abort_flag, 31);
+      if (!ok) break;
+      const uint32_t to = smem_u32(sm_q + slot * L::kQ) + (64 * w2 + sub) * 128;
+      const uint32_t at0 = place(now.head, now.tok0, g0), at1 = place(now.head, now.tok1, g1);
+      now = next;
+      next = find(t, i + 2);
+      t = tile(i + 3);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        // row 64 w2 + 4 k + sub
+        const uint32_t at = __shfl_sync(0xffffffffu, k < 8 ? at0 : at1, (4 * k + sub) & 31);
+        if (at != kNoRow) {
+          const char* from = q + static_cast<size_t>(at) * 16;
+          const uint32_t dst = to + k * 512 + ((ch ^ (sub + 4 * (k & 1))) << 4);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) cp_async16(dst + c * L::kHalf, from + c * 128);
+        }
+      }
+      cp_async_commit();
     }
     cp_async_wait<0>();
-    if (ok && n > 0) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qfull + (n - 1) % L::kQs);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (ok && lane == 0) {
+      if (n > 1) mbar_arrive(qfull + (n - 2) % L::kQs);
+      if (n > 0) mbar_arrive(qfull + (n - 1) % L::kQs);
     }
   } else {
     const int which = (warp - 4) >> 2, row = threadIdx.x - 128 - 128 * which, w4 = warp & 3;
-    const int e = row / G, g = row - e * G;
+    const int e = row / G;
     const uint32_t lanes = static_cast<uint32_t>(w4) << 21;  // lane 32 w4 of Tensor Memory
     const uint32_t tS = tmem + lanes + which * 64, tO = tmem + lanes + 128 + which * D;
     const float c = p.scale_log2;
-    uint32_t kv = 0;
+    uint8_t* out = smem + L::kOffOut + (warp - 4) * 2 * L::kOut;
+    const uint32_t to = smem_u32(out) + lane * 128;
+    // tile i and the block of the one before, loaded four tiles ahead, and the row's token of it, two tiles ahead
+    const int4 none = make_int4(-1, 0, 0, 0);
+    auto tile = [&](int i) { return i < n ? tiles[i] : none; };
+    auto token_of = [&](const int4& t, int i) { return e < t.z ? order[static_cast<long long>(i) * p.tile_tokens + e] : 0; };
+    int4 t = tile(which), t_next = tile(which + 2);
+    int before = which > 0 ? tile(0).x : -1, before_next = tile(which + 1).x, tok = token_of(t, which);
+    uint32_t kv = 0;  // blocks up to and with tile i, as the loader numbers them
     int cur = -1;
-    // blocks up to and with tile i, as the loader numbers them
-    auto follow = [&](int bucket) {
-      if (bucket != cur) {
-        cur = bucket;
-        ++kv;
-      }
-    };
 #pragma unroll 1
     for (int i = which; i < n; i += 2) {
-      if (i > 0) follow(tiles[i - 1].x);
-      const int4 t = tiles[i];
-      follow(t.x);
+      const int4 t_after = tile(i + 4);
+      const int before_after = tile(i + 3).x, tok_next = token_of(t_next, i + 2);
+      if (i > 0 && before != cur) ++kv;
+      if (i == 0 || t.x != before) ++kv;
+      cur = t.x;
       const bool live = e < t.z;
-      const int entry = live ? order[t.y + e] : 0;
-      const int tok = static_cast<int>(p.list_len.div(static_cast<uint32_t>(entry)));
       const int h = t.x / p.n_blocks;
       const int lim = live ? min(64, first_seen + tok - 64 * (t.x - h * p.n_blocks)) : 64;
-      const long long out = (static_cast<long long>(tok) * p.Hkv + h) * p.n_sel + (entry - tok * p.n_sel);
       const bool masked = __any_sync(0xffffffffu, lim < 64);
 
       if (!wait_all(sfull + which, (i / 2) & 1, abort_flag, 41)) break;
@@ -482,9 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_all(odone + which, (i / 2) & 1, abort_flag, 42)) break;
       tc_fence_after();
       const bool notes = noted[(kv - 1) % kNotes] != 0;
-      float* o = p.o_part + (out * G + g) * D;
+      // rows of 128 bytes, 16 at a time exchanged by the row: the map's order, and no two lanes on a bank
 #pragma unroll
       for (int s = 0; s < D / 32; ++s) {
+        if (lane == 0) bulk_wait_read<1>();  // this half of the buffer is free
+        __syncwarp();
         tmem_ld32(tO + 32 * s, *reinterpret_cast<uint32_t(*)[32]>(u));
         tmem_wait_ld();
 #pragma unroll
@@ -495,16 +553,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k)
             if (at[k] < lim) u[k] = 0x7fc00000u;
         }
-        if (live) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) st_global_v8(o + 32 * s + 8 * k, u + 8 * k);
+        for (int k = 0; k < 8; ++k)
+          st_shared_v4(to + (s & 1) * L::kOut + ((k ^ (lane & 7)) << 4), u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (32 * w4 < t.z * G) tma_store_2d(&tm_o, out + (s & 1) * L::kOut, 32 * s, 32 * (t.y + w4));
+          bulk_commit();
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree + which);
-      if (live) p.lse_part[out * G + g] = l == 0.f ? -INFINITY : M + __log2f(l);
+      if (live) p.lse_part[32ll * t.y + row] = l == 0.f ? -INFINITY : M + __log2f(l);
+      tok = tok_next;
+      t = t_next;
+      t_next = t_after;
+      before = before_next;
+      before_next = before_after;
     }
+    if (lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
@@ -526,7 +595,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_entries_kernel(const __g
   if (i >= min(p.chunk_tokens, p.Nq - i0)) return;
   const int tok = b * p.Nq + i0 + i, seen = seen_by(p, b, i0 + i);
   const int* list = p.blocks + (static_cast<long long>(tok) * p.Hkv + h) * p.n_sel;
-  const long long first = (static_cast<long long>(i) * p.Hkv + h) * p.n_sel;
+  const int* rank = p.rank + (static_cast<long long>(tok) * p.Hkv + h) * p.n_sel;
+  const int2* starts = p.starts + (static_cast<long long>(group) * p.Hkv + h) * p.n_blocks;
   Join s = {-INFINITY, 0.f};
   float acc[D / 32];
 #pragma unroll
@@ -534,14 +604,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_entries_kernel(const __g
   join<D>(p, p.n_sel,
           [&](int x) {
             const int blk = list[x];
-            return blk >= 0 && blk < p.n_blocks && blk * 64 < seen ? (first + x) * G + hq - h * G : -1ll;
+            if (blk < 0 || blk >= p.n_blocks || blk * 64 >= seen) return -1ll;
+            const int r = rank[x], t = static_cast<int>(p.tile_len.div(static_cast<uint32_t>(r)));
+            return 32ll * starts[blk].y + 128 * t + (r - t * p.tile_tokens) * G + hq - h * G;
           },
           s, acc);
   write_row<D>(p, tok, hq, s, acc);
 }
 
 template <int D>
-cudaError_t launch_d(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
+cudaError_t launch_d(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_o,
+                     cudaStream_t stream) {
   using L = Layout<D>;
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -556,11 +629,11 @@ cudaError_t launch_d(const ByBlockParams& p, const CUtensorMap& tm_k, const CUte
   const dim3 sort(static_cast<unsigned>((lists + kSortWarps - 1) / kSortWarps));
   count_kernel<<<sort, 32 * kSortWarps, 0, stream>>>(p);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_dependent(plan_kernel, dim3(groups), kPlanThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_dependent(plan_kernel, dim3(groups * p.Hkv), kPlanThreads, 0, stream, p);
   if (e == cudaSuccess) e = launch_dependent(place_kernel, sort, 32 * kSortWarps, 0, stream, p);
   const unsigned rows = static_cast<unsigned>((static_cast<long long>(p.chunk_tokens) * p.Hq + kJoinWarps - 1) / kJoinWarps);
   for (int g = 0; g < groups && e == cudaSuccess; ++g) {
-    e = launch_dependent(kern, dim3(n_sm), kThreads, L::kAlloc, stream, tm_k, tm_v, p, g);
+    e = launch_dependent(kern, dim3(n_sm), kThreads, L::kAlloc, stream, tm_k, tm_v, tm_o, p, g);
     if (e == cudaSuccess) e = launch_dependent(join_entries_kernel<D>, dim3(rows), 32 * kJoinWarps, 0, stream, p, g);
   }
   return e;
@@ -573,24 +646,27 @@ ByBlockSizes by_block_sizes(int B, int Nq, int Hq, int Hkv, int d, int n_sel, lo
   const int G = Hq / Hkv;
   const long long lists = static_cast<long long>(B) * Nq * Hkv;
   if (G > kByBlockHeads || lists > (1LL << 30) / n_sel) return z;
-  const long long token_bytes = static_cast<long long>(Hq) * n_sel * d * 4;
-  long long ct = kByBlockBytes / token_bytes;
+  const int T = 128 / G;
+  const long long blocks = Hkv * n_blocks;
+  long long ct = kByBlockBytes / (static_cast<long long>(Hq) * n_sel * d * 4);
   if (ct > Nq) ct = Nq;
   if (ct < 1) return z;
   z.chunks = static_cast<int>((Nq + ct - 1) / ct);
   z.chunk_tokens = (Nq + z.chunks - 1) / z.chunks;
   const long long entries = static_cast<long long>(z.chunk_tokens) * Hkv * n_sel;
-  if (entries < kByBlockEntries || entries < kByBlockShare * Hkv * n_blocks) return ByBlockSizes{};
-  z.tile_tokens = 128 / G;
-  z.tile_cap = entries / z.tile_tokens + (entries < Hkv * n_blocks ? entries : Hkv * n_blocks);
+  if (entries < kByBlockEntries || entries < kByBlockShare * blocks) return ByBlockSizes{};
+  z.tile_tokens = T;
+  z.tile_cap = entries / T + (entries < blocks ? entries : blocks);
+  // full tiles take 128 rows, a block's last one up to 31 more than its entries have
+  z.rows = (entries / T * 128 + (entries % T) * G + 31 * (entries < blocks ? entries : blocks) + 31) / 32 * 32;
   z.groups = static_cast<long long>(B) * z.chunks;
-  z.rows = static_cast<long long>(z.chunk_tokens) * Hq * n_sel;
   z.entries = lists * n_sel;
   return z;
 }
 
-cudaError_t launch_by_block(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
-  return p.d == 64 ? launch_d<64>(p, tm_k, tm_v, stream) : launch_d<128>(p, tm_k, tm_v, stream);
+cudaError_t launch_by_block(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_o,
+                            cudaStream_t stream) {
+  return p.d == 64 ? launch_d<64>(p, tm_k, tm_v, tm_o, stream) : launch_d<128>(p, tm_k, tm_v, tm_o, stream);
 }
 
 cudaError_t status_word_by_block(uint32_t** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_rows_status); }

@@ -262,7 +262,7 @@ cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const 
                             int grid, bool after_pairs, cudaStream_t stream);
 // The same over listed blocks, block by block: for many tokens with few heads a group.
 constexpr int kByBlockHeads = 8;                  // heads of a group at most
-constexpr long long kByBlockBytes = 256 << 20;    // outputs of a chunk's pieces at most
+constexpr long long kByBlockBytes = 1 << 30;    // outputs of a chunk's pieces at most
 constexpr long long kByBlockEntries = 1 << 16;    // list entries of a chunk at least
 constexpr long long kByBlockShare = 4;            // and of each block of a full table, on average
 struct ByBlockSizes {
@@ -283,23 +283,27 @@ struct ByBlockParams {
   float* lse;
   float* o_part;      // [rows, d]
   float* lse_part;    // [rows], base 2
-  int4* tiles;        // [groups, tile_cap]: block of (KV head, block), first entry in its order, entries, first group of 8 keys
-  int* counts;        // [groups, Hkv, n_blocks]: entries of a block, then the first one's place
+  int4* tiles;        // [groups, tile_cap]: (KV head, block), first row / 32, entries, first group of 8 keys
+  int* counts;        // [groups, Hkv, n_blocks]: entries of a block
+  int2* starts;       // the same size: a block's first tile, its first row / 32
   int* n_tiles;       // [groups]
   int* rank;          // [B, Nq, Hkv, n_sel]: place among the block's entries
-  int* order;         // the same size: the entries of a chunk, block by block
+  int* order;         // [groups, tile_cap, tile_tokens]: tokens of the chunk
   int max_blocks, page_size, num_pages, n_sel, n_blocks;
   int B, Nq, Hq, Hkv, d;
   int chunks, chunk_tokens, tile_tokens;
   long long tile_cap;
   float scale_log2;
-  FastDiv list_len;   // n_sel
+  FastDiv tile_len;   // tile_tokens
 };
-cudaError_t launch_by_block(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream);
+// tm_o: o_part in boxes of 32 rows and columns.
+cudaError_t launch_by_block(const ByBlockParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_o,
+                            cudaStream_t stream);
 // Maps of bf16 tensors: a page pool as {64, 8, d / 64, groups of 8 keys, Hkv}, boxes of a head's 64 keys; q's of
-// `tokens` tokens of a group of heads.
+// `tokens` tokens of a group of heads; fp32 rows, boxes of 32 rows and columns.
 bool make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int Hkv, int d);
 bool make_map_group(CUtensorMap* m, const void* base, long long total_tokens, int Hkv, int G, int d, int tokens);
+bool make_map_pieces(CUtensorMap* m, void* base, long long rows, int d);
 
 // Device status words, one a kernel unit, of the current device.
 cudaError_t status_word_prefill(uint32_t** at);
