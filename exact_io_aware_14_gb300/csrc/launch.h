@@ -260,11 +260,18 @@ cudaError_t launch_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUte
 constexpr int kFewRows = 32;
 cudaError_t launch_few_rows(const RowsParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             int grid, bool after_pairs, cudaStream_t stream);
-// The same over listed blocks, block by block: for many tokens with few heads a group.
-constexpr int kByBlockHeads = 8;                  // heads of a group at most
-constexpr long long kByBlockBytes = 1 << 30;    // outputs of a chunk's pieces at most
-constexpr long long kByBlockEntries = 1 << 16;    // list entries of a chunk at least
-constexpr long long kByBlockShare = 4;            // and of each block of a full table, on average
+// The same over listed blocks, block by block: for chunks of 16 K list entries and
+// of 16 for each block of a full table, with at most 8 heads a group.  Measured,
+// us block by block / token by token, d = 128, 8 KV heads:
+//     32 heads, entries (a block)  16 K (16)  40 / 53    8 K (8)  38 / 32    16 K (4)  76 / 50
+//                                  32 K (8)   80 / 84    64 K (16)  105 / 155
+//                                  512 K (128)  476 / 1140    512 K (32)  573 / 1152
+//     64 heads  64 K (16)  153 / 204;  8 heads  64 K (16)  93 / 155
+//     d = 64, 32 heads  64 K (16)  71 / 155
+constexpr int kByBlockHeads = 8;
+constexpr long long kByBlockBytes = 1 << 30;      // outputs of a chunk's pieces at most
+constexpr long long kByBlockEntries = 1 << 14;
+constexpr long long kByBlockShare = 16;
 struct ByBlockSizes {
   int chunks;         // of a sequence's tokens; 0: token by token
   int chunk_tokens, tile_tokens;

@@ -1,22 +1,24 @@
 // Attention of query rows over a paged bf16 cache, for sm_103a: over whole
 // sequences whose first keys the batch shares (attn_fwd_splitkv_paged_shared),
-// or over listed 64-key blocks (attn_fwd_blocks_paged).
+// or over listed 64-key blocks (attn_fwd_blocks_paged); here where more than 32
+// rows read the same keys (few_rows_sm103.cu takes fewer).
 //
 // A row is a query token and one of the heads that read a KV head.  S = Q K^T
 // and O += P V run on tcgen05 with 128 rows and 128 keys a tile.  The rows of a
 // tile are all that read the same keys: for the shared prefix the tokens of the
 // whole batch with the heads of a group, for a sequence's own keys its new
-// tokens with theirs, for listed blocks one token's heads.  Where those are few
-// most of a tile's rows are empty; their products cost what a full tile's do,
-// 1024 cycles for 128 keys of d = 128, less than the 64 KB of K and V take to
-// arrive (1.4 us at this SM's share of memory).
+// tokens with theirs, for listed blocks one token's heads.  A product of 128
+// rows and keys of d = 128 takes 512 cycles whatever part of the rows is there.
 //
 // Work is cut into equal runs of tiles, whatever the lengths.  A CTA has two
 // slots, each with a tile of rows, its scores, its accumulator and a
 // warpgroup for its softmax.
 //   Pair work (a prefix read by more rows than one tile): the slots hold two
 //     tiles of rows and share every K/V tile; each CTA takes an equal run of
-//     (KV head, pair, key tile).
+//     (KV head, pair, key tile).  Bound by the issue of products: 64 sequences
+//     with 32 heads on a prefix of 131072 keys, 8 KV heads of d = 128, take
+//     131 us in all, 137 GFLOP at 1.05 PFLOP/s (2350 of a step's 3500 cycles
+//     the tensor core has a product; the rest goes into waits for P).
 //   Lane work (all else): each slot is a lane of its own with its own K/V
 //     tiles, and each lane takes an equal run of (unit, key tile), a unit being
 //     the rows and keys named above.
@@ -25,6 +27,8 @@
 // order.  A piece of listed blocks that is a whole unit is written as result.
 // Piece numbers need no counters: along the runs either the lane or the unit
 // goes up by one, so lane + unit is a number of its own for each piece.
+//
+// P is rounded to bf16, the tensor core's operand; its sum takes it before.
 //
 // Warps: 0 producer (work, pages, TMA loads into one ring in the order of use),
 // 1 MMA issuer, 2 clears value rows that hold anything, 4-7 and 8-11 softmax
@@ -52,7 +56,7 @@ struct Piece {
   int tok0, ntok;  // first token, tokens
   int key0, keys;  // ranges: position of the first tile's first key, keys from there on
   int dst;    // piece number, -1: the result itself
-  int part;   // keys seen of the blocks marked in part[] (lists)
+  int part;   // keys seen of the blocks marked in some[] (lists)
   uint32_t full[kMaskWords], some[kMaskWords];  // lists: blocks seen whole, seen in part
 };
 template <int D>

@@ -532,9 +532,11 @@ ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int 
  *            are passed over, as are blocks behind the token's position; a block
  *            listed twice counts twice; n_sel is at most 512; an entry past the table is passed over
  *            and reported as ATTN_ERR_DEVICE_ARG by attn_get_device_status;
- *   workspace: attn_fwd_blocks_paged_workspace_size bytes.  Where a block is
- *            listed by many tokens it holds what each entry gives, up to 256 MB
- *            at a time, with the entries sorted by their block.
+ *   workspace: attn_fwd_blocks_paged_workspace_size bytes.  Where the table has
+ *            16 list entries or more for each of its blocks (and 16384 for a
+ *            sequence and KV heads together, at most 8 heads a group), entries are
+ *            sorted by block, and it holds what each gives: 4 (d + 1) bytes a head,
+ *            of as many tokens as 1 GB takes.
  * The other arguments, limits and results are those of
  * attn_fwd_splitkv_paged_shared.  Nq may be in the thousands (a prompt, or a
  * chunk of one).  Only keys and values that the row sees enter its result; what

@@ -200,7 +200,8 @@ BY_BLOCK = [
     (1, 1024, 8, 1, 128, 128, [1500], 64),
     (1, 700, 3, 3, 64, 64, [1000], 33),           # one head: tiles of 128 tokens
     (3, 1400, 5, 1, 128, 256, [5000, 100, 0], 47),  # tokens that see nothing, a sequence without keys
-    (1, 384, 8, 1, 128, 64, [33100], 512),        # chunks of tokens
+    (1, 600, 8, 1, 128, 64, [33100], 512),        # chunks of tokens
+    (2, 256, 4, 1, 128, 64, [256, 700], 64),      # as few as are taken so
 ]
 
 
