@@ -47,7 +47,8 @@ __device__ __forceinline__ int clamped_len(const int* seqlens, int b, int cap, b
 // ---------------------------------------------------------------------------
 // Bounds.  One CTA for each touched block and 64 chunks of 8 channels: four
 // groups of 64 threads take 16 rows each, a thread's loads all in flight at
-// once, and meet in shared memory.  Bound by memory: each key read once.
+// once, and meet in shared memory.  Bound by memory: each key read once (prompts of
+// 8191 tokens padded, 104 MB: 21 us, 5 TB/s; a step's new tokens: 3.2 us, latency).
 __device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -157,9 +158,13 @@ __device__ __forceinline__ const __nv_bfloat16* bounds_at(const SelectParams& p,
 // 2 d deep, rows being tokens with the group's heads: a thread holds a block's
 // scores (TMEM lane), so the largest over a token's heads is taken in its
 // registers and a warp writes 32 neighbouring scores.  Many rows (N = 128): a CTA
-// keeps its 128 blocks and walks the rows, bound by laying these out.  Few rows
-// (N = 16): a CTA keeps the rows and walks the blocks, the next ones on their way
-// to registers while these are multiplied; bound by reading the bounds.
+// keeps its 128 blocks and walks the rows, bound by laying these out (2048 tokens
+// of 32 heads, 512 blocks, 8 KV heads of d = 128: 40 us, 17 GFLOP).  Up to 64 rows
+// (N = 16 or 64): a CTA keeps the rows and walks the blocks, the next ones on their
+// way to registers while these are multiplied; bound by reading the bounds (16
+// sequences of up to 128 K keys, 4 rows each: 75 MB in 24 us).  Measured on these
+// sequences, us of the whole call, walking the blocks / the rows: 4 rows 37 / 84,
+// 20 rows 57 / 100, 32 rows 67 / 104, 64 rows 98 / 127.
 template <int D>
 struct MmaLayout {
   static constexpr int N = 128;
@@ -395,9 +400,9 @@ __global__ void __launch_bounds__(MmaLayout<D>::kThreads, 1) score_mma_kernel(co
   }
 }
 
-template <int D>
+template <int D, int kN>
 struct FewLayout {
-  static constexpr int N = 16;
+  static constexpr int N = kN;
   static constexpr int kA = 128 * 2 * D * 2, kB = N * 2 * D * 2;
   static constexpr int kOffB = kA;
   static constexpr int kOffNorm = kOffB + kB;             // [128] |m|^2, [N] |q|^2
@@ -405,13 +410,13 @@ struct FewLayout {
   static constexpr int kOffBar = kOffPage + 2 * 128 * 8;
   static constexpr int kBytes = kOffBar + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr uint32_t kTmem = 32;  // a token's heads are read 8 at a time, past the last one
+  static constexpr uint32_t kTmem = 2 * N;  // a token's heads are read 8 at a time, past the last one
 };
 
-// All rows of a sequence (at most 16); block tiles part, part + parts, ...
-template <int D>
+// All rows of a sequence (at most N); block tiles part, part + parts, ...
+template <int D, int kN>
 __global__ void __launch_bounds__(kThreads, 2) score_few_kernel(const SelectParams p, int token0, int tokens) {
-  using L = FewLayout<D>;
+  using L = FewLayout<D, kN>;
   constexpr int N = L::N, kC = D / 8, kLoads = 128 * kC / kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -458,8 +463,9 @@ __global__ void __launch_bounds__(kThreads, 2) score_few_kernel(const SelectPara
   };
   if (tid < 128) places(blockIdx.x, 0);
   // the rows: chunk c of row r
-  if (tid < N * kC) {
-    const int r = tid / kC, c = tid % kC;
+#pragma unroll 1
+  for (int idx = tid; idx < N * kC; idx += kThreads) {
+    const int r = idx / kC, c = idx % kC;
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (r < cnt * G)
       u = (static_cast<const uint4*>(p.q) + ((static_cast<long long>(b) * p.Nq + n0 + r / G) * p.Hq + h * G + r % G) * kC)[c];
@@ -526,11 +532,12 @@ __global__ void __launch_bounds__(kThreads, 2) score_few_kernel(const SelectPara
     }
     if (!mbar_wait(bar, k & 1, &never, kWaitLimitNs)) record(5, kDevTimeout);
     tc_fence_after();
-    if (warp < 4) {
-      const int j = j0 + warp * 32 + lane;
-      const uint32_t at = tmem + (static_cast<uint32_t>(warp) << 21);
+    // each four warps take a part of the tokens
+    {
+      const int j = j0 + (warp & 3) * 32 + lane;
+      const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
 #pragma unroll 1
-      for (int c = 0; c < cnt; ++c) {
+      for (int c = warp >> 2; c < cnt; c += 2) {
         float best = -INFINITY;
 #pragma unroll 1
         for (int g = 0; g < G; g += 8) {
@@ -1105,10 +1112,10 @@ cudaError_t launch_key_bounds(const KeyBoundsParams& p, cudaStream_t stream) {
                           0, stream, p, slabs);
 }
 
-template <int D>
+template <int D, int N>
 cudaError_t launch_score_few(const SelectParams& p, int token0, int tokens, cudaStream_t stream) {
-  using L = FewLayout<D>;
-  auto kern = score_few_kernel<D>;
+  using L = FewLayout<D, N>;
+  auto kern = score_few_kernel<D, N>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   const int seqs = (token0 + tokens - 1) / p.Nq - token0 / p.Nq + 1, block_tiles = (p.n_blocks + 127) / 128;
@@ -1142,16 +1149,23 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
   const int rows = p.Nq * (p.Hq / p.Hkv);
   cudaError_t e;
   if (rows <= 16)
-    e = p.d == 64 ? launch_score_few<64>(p, token0, tokens, stream) : launch_score_few<128>(p, token0, tokens, stream);
+    e = p.d == 64 ? launch_score_few<64, 16>(p, token0, tokens, stream) : launch_score_few<128, 16>(p, token0, tokens, stream);
+  else if (rows <= 64)
+    e = p.d == 64 ? launch_score_few<64, 64>(p, token0, tokens, stream) : launch_score_few<128, 64>(p, token0, tokens, stream);
   else
     e = p.d == 64 ? launch_score_mma<64>(p, token0, tokens, stream) : launch_score_mma<128>(p, token0, tokens, stream);
   if (e != cudaSuccess) return e;
   const int n = tokens * p.Hkv;
-  if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
-  if (p.n_blocks <= 512) return launch_choose_warp<16>(p, token0, n, stream);
-  if (p.n_blocks <= 1024) return launch_choose_warp<32>(p, token0, n, stream);
-  // many rows: a warp each; few: a CTA each
-  if (p.n_blocks <= 2048 && n > 2432) return launch_choose_warp<64>(p, token0, n, stream);
+  // More rows than blocks: a warp a row; fewer: a CTA a row.  Measured, us of the whole call, a warp / a CTA:
+  //     512 blocks: 128 rows 27.8 / 24.3, 256 21.3 / 18.9, 512 21.6 / 25.0, 1024 24.2 / 34.4, 16384 114 / 362
+  //     1024: 128 rows 41.9 / 33.8;  2048: 128 rows 50.2 / 36.9, 2048 127 / 126, 16384 566 / 589
+  // (128 rows: 16 sequences, the others one).
+  if (n > p.n_blocks) {
+    if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
+    if (p.n_blocks <= 512) return launch_choose_warp<16>(p, token0, n, stream);
+    if (p.n_blocks <= 1024) return launch_choose_warp<32>(p, token0, n, stream);
+    if (p.n_blocks <= 2048) return launch_choose_warp<64>(p, token0, n, stream);
+  }
   const int held = p.n_blocks < kHeld ? p.n_blocks : kHeld;
   return launch_dependent(p.n_blocks <= 8 * kThreads ? choose_kernel<8> : choose_kernel<0>, dim3(static_cast<unsigned>(n)), kThreads,
                           held * static_cast<int>(sizeof(float)), stream, p, token0);

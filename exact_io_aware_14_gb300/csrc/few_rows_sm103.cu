@@ -6,9 +6,18 @@
 //     S^T [128 keys x N]  = K Q^T            (A: the K tile, B: Q, K-major)
 //     O^T [d x N]        += V^T P^T          (A: the V tile, M-major, B: P^T)
 // Both products of a tile take as long as the tensor core needs to read the
-// tile from shared memory, whatever the rows (128 rows in M, mostly empty, took
-// 1100 cycles and a softmax of 1400 in one warp: 65 us for 16 tokens on 64 listed
-// blocks of 64 keys, 8 KV heads, where this form takes 54).
+// tile from shared memory, whatever the rows: 1024 cycles for 128 keys of d = 128,
+// 1100 with all that is around it, while the tile's 64 KB take 1.4 us to arrive from
+// memory.  Bound by memory: 16 tokens of 32 heads on 64 listed blocks, 8 KV heads of
+// d = 128, read 269 MB in 50.4 us, 5.3 TB/s.  With the rows in M (rows_sm103.cu) that
+// takes 60.4 us.
+//
+// R, the rows that the softmax handles: 4, 8, 16 or 32.  The case above, us by R
+// (by the rows in M):
+//      4 rows   50.4 (4)   51.4 (8)   54.4 (16)   54.8 (32)   60.4
+//      8 rows              52.1       55.1        55.4        60.9
+//     16 rows                         55.8        56.1        61.4
+//     32 rows                                     58.8        63.6
 //
 // The softmax has a thread for each key: its N scores from Tensor Memory, p to
 // shared memory as the next product's operand, a part of each row's sum of p in

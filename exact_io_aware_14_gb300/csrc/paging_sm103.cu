@@ -8,7 +8,8 @@
 // j = 0 .. need - 1, if base + need <= count.  A release counts from the last
 // sequence's last page, so it puts back what the same reserve took, in place.
 //
-// Bound by latency: a few bytes for each sequence, 8 for each slot.  So one
+// Bound by latency: a few bytes for each sequence, 8 for each slot (256 sequences
+// of one new token: 3.2 us a call; 48 prompts of up to 8191 4 us).  So one
 // launch, in which every block forms the sums before its sequences again (B
 // lengths from L2) in place of a second launch or of waiting for a block; the
 // count goes to memory of its own, as blocks that start late still read the

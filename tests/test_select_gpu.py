@@ -72,7 +72,13 @@ def run(q, kb, table, lens, topk, sink=1, local=1):
     (1, 1, 1, 1, 64, 64, [1], 1, 0, 0), (1, 1, 1, 1, 64, 64, [1], 4, 1, 1), (2, 1, 4, 2, 128, 64, [64, 1000], 5, 1, 1),
     (3, 3, 9, 3, 64, 192, [2, 700, 3000], 7, 0, 0), (2, 1, 8, 1, 128, 256, [5000, 4097], 1, 0, 0),
     (2, 70, 10, 2, 128, 64, [75, 2000], 6, 2, 2), (1, 1, 128, 1, 128, 128, [9000], 100, 3, 5), (1, 200, 4, 4, 64, 64, [200], 3, 1, 1),
-    (1, 2, 4, 2, 64, 64, [70000], 64, 1, 2), (2, 1, 2, 2, 64, 64, [900, 0], 2, 1, 1), (1, 1, 7, 1, 64, 64, [2100], 16, 16, 0)])
+    (1, 2, 4, 2, 64, 64, [70000], 64, 1, 2), (2, 1, 2, 2, 64, 64, [900, 0], 2, 1, 1), (1, 1, 7, 1, 64, 64, [2100], 16, 16, 0),
+    # up to 16, up to 64 and more rows of a sequence
+    (1, 16, 1, 1, 64, 64, [9000], 9, 1, 1), (1, 17, 1, 1, 128, 64, [9000], 9, 1, 1), (2, 16, 8, 2, 128, 64, [3000, 9], 5, 1, 1),
+    (3, 3, 10, 1, 64, 192, [700, 20000, 2], 7, 0, 1), (1, 1, 64, 1, 128, 128, [5000], 6, 1, 0), (1, 5, 13, 1, 64, 64, [9000], 8, 1, 1),
+    # more tokens than blocks, and fewer
+    (1, 330, 1, 1, 64, 64, [20100], 9, 1, 1), (1, 300, 1, 1, 64, 64, [20100], 9, 1, 1), (1, 650, 1, 1, 64, 64, [40000], 12, 2, 1),
+    (1, 1110, 1, 1, 64, 64, [70000], 16, 1, 3), (1, 900, 1, 1, 64, 64, [70000], 16, 1, 3)])
 def test_selection(B, Nq, Hq, Hkv, d, page, lens, topk, sink, local):
     q, kb, table = case(Nq + Hq + topk, B, Nq, Hq, Hkv, d, page, -(-max(lens) // page))
     assert torch.equal(run(q, kb, table, lens, topk, sink, local),
