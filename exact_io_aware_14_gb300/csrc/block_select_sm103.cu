@@ -666,9 +666,13 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 }
 
 // A warp for a row of up to 32 K blocks, block 32 m + lane in element m of a lane.
+// Bound by its instructions, one warp's waiting for those before, so by the warps
+// there are: with 64 registers, eight CTAs an SM, 2048 tokens and 8 KV heads take
+// 103 us on 512 blocks (114 with the 108 that the compiler takes by itself), 184
+// (235) on 1024, 446 (566) on 2048.
 constexpr int kChooseWarps = 4;
 template <int K>
-__global__ void __launch_bounds__(32 * kChooseWarps) choose_warp_kernel(const SelectParams p, int token0, int rows) {
+__global__ void __launch_bounds__(32 * kChooseWarps, 8) choose_warp_kernel(const SelectParams p, int token0, int rows) {
   grid_depends();
   const int lane = threadIdx.x & 31;
   const int lrow = blockIdx.x * kChooseWarps + (threadIdx.x >> 5);
@@ -1157,8 +1161,8 @@ cudaError_t launch_select(const SelectParams& p, int token0, int tokens, cudaStr
   if (e != cudaSuccess) return e;
   const int n = tokens * p.Hkv;
   // More rows than blocks: a warp a row; fewer: a CTA a row.  Measured, us of the whole call, a warp / a CTA:
-  //     512 blocks: 128 rows 27.8 / 24.3, 256 21.3 / 18.9, 512 21.6 / 25.0, 1024 24.2 / 34.4, 16384 114 / 362
-  //     1024: 128 rows 41.9 / 33.8;  2048: 128 rows 50.2 / 36.9, 2048 127 / 126, 16384 566 / 589
+  //     512 blocks: 128 rows 27.8 / 24.3, 256 21.3 / 18.9, 512 21.6 / 25.0, 1024 24.2 / 34.4, 16384 103 / 362
+  //     1024: 128 rows 41.9 / 33.8;  2048: 128 rows 50.2 / 36.9, 2048 127 / 126, 16384 446 / 589
   // (128 rows: 16 sequences, the others one).
   if (n > p.n_blocks) {
     if (p.n_blocks <= 256) return launch_choose_warp<8>(p, token0, n, stream);
