@@ -185,7 +185,7 @@ struct Layout {
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTmem = D == 64 ? 256 : 512;  // S twice, O twice
 };
-static_assert(Layout<128>::kAlloc <= 232448, "shared memory of a CTA");
+static_assert(Layout<128>::kAlloc <= 232448 && Layout<64>::kAlloc <= 232448, "shared memory of a CTA");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -462,3 +462,30 @@ def test_a_serving_step_selects_what_it_attends_to():
         P.check(*some, P.attend(*host, page, 0.1, listed(few.cpu(), lens.tolist(), 1)))
     c = A.kvcache_release_paged(table, lens, i32([0] * B), free, count, page)
     assert int(c) == num and sorted(free.tolist()) == list(range(num))
+
+
+def test_a_prompt_selects_what_it_attends_to():
+    """The same for the chunks of a prompt, the second behind the first's keys; then the rejected part is given back."""
+    g = torch.Generator().manual_seed(12)
+    Hq, Hkv, d, page, num = 8, 2, 64, 64, 24
+    kp, vp = (torch.zeros((num, page, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kb = torch.zeros((num, 1, Hkv, 2, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, 20), -1, dtype=torch.int32, device="cuda")
+    free, count = torch.randperm(num, generator=g).to(torch.int32).cuda(), i32([num])
+    lens, n = i32([0]), 600
+    assert by_block(n, Hq, Hkv, d, 16, 20 * page)
+    for chunk in range(2):
+        k, v, q = (torch.randn((1, n, h, d), generator=g).to(torch.bfloat16).cuda() for h in (Hkv, Hkv, Hq))
+        granted, _, count = A.kvcache_reserve_paged(table, lens, i32([n]), free, count, page, n)
+        after = torch.empty_like(lens)
+        A.kvcache_append_paged(k, v, kp, vp, table, lens, new_lens=granted, seqlens_out=after)
+        A.kvcache_bounds_paged(kp, kb, table, after, n, new_lens=granted)
+        lens = after
+        blocks = A.select_blocks_paged(q, kb, table, lens, 16, 1, 2)
+        o, lse = A.attend_blocks_paged(q, kp, vp, table, lens, blocks, 0.125)
+        assert A.attn_get_device_status() == 0
+        host = [x.cpu() for x in (q, kp, vp, table)]
+        assert torch.equal(blocks.cpu(), P.select(host[0], kb.cpu(), host[3], page, lens.tolist(), 16, 1, 2))
+        P.check(o, lse, P.attend(*host, page, 0.125, listed(blocks.cpu(), lens.tolist(), n)))
+    count = A.kvcache_release_paged(table, lens, i32([n]), free, count, page)
+    assert int(count) == num - 10 and A.attn_get_device_status() == 0
