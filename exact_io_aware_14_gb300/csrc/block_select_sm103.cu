@@ -271,13 +271,15 @@ __global__ void __launch_bounds__(MmaLayout<D>::kThreads, 1) score_mma_kernel(co
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) held[i] = tok_of[i] < cnt ? q[off[i]] : make_uint4(0u, 0u, 0u, 0u);
   };
-  auto stage = [&](int buf) {
+  // whether this CTA finds the norms of a tile's rows: those that see the tile take turns
+  auto norms = [&](int t) { return t % ((blocks_seen(min(n1, n0 + (t + 1) * tile_tokens) - 1) - 1) / 128 + 1) == j0 / 128; };
+  auto stage = [&](int buf, bool norm) {
     uint8_t* base = smem + L::kOffB + buf * L::kB;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int idx = i * kThreads + tid, r = idx / kC, c = idx % kC;
       const uint4 u = held[i];
-      if (j0 == 0) {  // the rows' norms, once
+      if (norm) {
         float m = sum_squares(u.x, u.y, u.z, u.w);
 #pragma unroll
         for (int o = kC / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(MmaLayout<D>::kThreads, 1) score_mma_kernel(co
   for (int t = first, k = 0; t <= t1; ++t, ++k) {
     if (t < t1) {
       const int buf = k & 1;
-      stage(buf);
+      stage(buf, norms(t));
       fence_proxy_async_smem();
       tc_fence_before();
       __syncthreads();
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(MmaLayout<D>::kThreads, 1) score_mma_kernel(co
           if (c + x < c1) put(c + x, best[x]);
       }
     }
-    if (j0 == 0 && tid < cnt) {
+    if (tid < cnt && norms(d)) {
       float q = 0.f;
       for (int g = 0; g < G; ++g) {
         const float x = s_q[buf * N + tid * G + g];
