@@ -135,6 +135,8 @@ def test_workspace_sizes(L):
         assert f(0, 2, 8, 2, 64) == f(4, 0, 8, 2, 64) == f(4, 2, 9, 2, 64) == f(4, 2, 8, 2, 65) == f(4, 2, 258, 2, 64) == 0
     assert attend(L, False, wsb=L.attn_splitkv_paged_shared_workspace_size(4, 2, 8, 2, 64) - 1) == 7
     assert attend(L, True, wsb=lists(4, 2, 8, 2, 64) - 1) == 7
+    many = L.attn_fwd_blocks_paged_workspace_size(4, 600, 8, 2, 64, 16, 1024)  # sorted by block
+    assert many > 600 * 8 * 16 * 65 * 4 and attend(L, True, Nq=600, n=16, o=1 << 40, wsb=many - 1) == 7
     n = L.attn_select_blocks_workspace_size(4, 2, 2, 1024)
     assert n >= 4 * 2 * 2 * 16 * 4 and select(L, wsb=n - 1) == 7
     assert L.attn_select_blocks_workspace_size(0, 2, 2, 1024) == L.attn_select_blocks_workspace_size(4, 2, 2, 63) == 0
