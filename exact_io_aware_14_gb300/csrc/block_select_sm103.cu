@@ -17,7 +17,8 @@
 // it is that far below, and only the few in between are scored again in 64 bits.
 // An fp32 sum of 256 terms, truncated at worst at each addition, is off by at
 // most 2^-15 of the sum of magnitudes, and that is at most |q| max_j |m_j| with
-// m = max(|lo|, |hi|) (Cauchy and Schwarz).
+// m = max(|lo|, |hi|) (Cauchy and Schwarz).  Where a norm cannot be told in fp32
+// there is no E, and all blocks are scored again.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -635,16 +636,26 @@ __device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& 
   return fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
 }
 
-// Twice the bound on the error of a row's scores (with what products below
-// fp32's range lose); infinite where norms are, and where they are not numbers.
-__device__ __forceinline__ float band_of(const SelectParams& p, const RowSpan& r, int h, int lrow) {
+// The largest |m|^2 of the blocks that a row sees, by a warp.
+__device__ __forceinline__ float bounds_norm(const SelectParams& p, const RowSpan& r, int h) {
   const float* m = p.m_norm + (static_cast<long long>(r.b) * p.Hkv + h) * ((p.n_blocks + 127) / 128);
   float x = 0.f;
   for (int i = threadIdx.x & 31; i <= (r.nb - 1) / 128; i += 32) x = fmaxf(x, m[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  // 2 * 2^-15, and a little for the roundings of the norms
-  const float band = 6.2e-5f * sqrtf(x) * sqrtf(p.q_norm[lrow]) + 1e-36f;
+  return x;
+}
+
+// Twice the bound on the error of a row's scores: 2 * 2^-15 |q| |m|, a little for
+// the roundings of the norms, and what 256 products below fp32's range lose.
+// Infinite where norms are, and where they are not numbers; and where one's square
+// lies below 2^-100, as then its terms may have passed below that range, while
+// their products with the other side need not: above it 256 terms lost are 2^-18 of
+// the square.
+constexpr float kLeastSquare = 0x1p-100f;
+__device__ __forceinline__ float band_of(float m_norm, float q_norm) {
+  if (!(m_norm >= kLeastSquare && q_norm >= kLeastSquare)) return INFINITY;
+  const float band = 6.2e-5f * sqrtf(m_norm) * sqrtf(q_norm) + 1e-35f;
   return band <= 3e38f ? band : INFINITY;
 }
 
@@ -701,12 +712,13 @@ __global__ void __launch_bounds__(32 * kChooseWarps, 8) choose_warp_kernel(const
     else
       in2 |= 1u << (m - 32);
   };
-  if (k > 0 && zero_row(p, token, h, lrow) && band_of(p, r, h, lrow) < 1e38f) {
+  const float m_norm = k > 0 ? bounds_norm(p, r, h) : 0.f;
+  if (k > 0 && m_norm < INFINITY && zero_row(p, token, h, lrow)) {
 #pragma unroll
     for (int m = 0; m < K; ++m)
       if (32 * m + lane >= c0 && 32 * m + lane < c0 + k) take(m);
   } else if (k > 0) {
-    const float band = band_of(p, r, h, lrow);
+    const float band = band_of(m_norm, p.q_norm[lrow]);
     uint32_t lo = 1u, hi = 0xffffffffu;  // without a bound on the errors all candidates lie between
     if (band < 1e38f) {
       // the k-th largest, between t and t + 2^last - 1: the largest t with k keys
@@ -858,7 +870,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
   }
   // candidates [c0, c1), k of them wanted; sink + local <= topk < nb.  Those of a row of zeros are the first ones: k
   // more at the front, none of the others
-  const bool zeros = zero_row(p, token, h, lrow) && band_of(p, r, h, lrow) < 1e38f;
+  const float m_norm = bounds_norm(p, r, h);
+  const bool zeros = m_norm < INFINITY && zero_row(p, token, h, lrow);
   const int all_k = p.topk - p.sink - p.local;
   const int c0 = p.sink + (zeros ? all_k : 0), c1 = r.nb - p.local, k = zeros ? 0 : all_k;
   const int n = c1 - c0;
@@ -873,7 +886,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
   unsigned long long cut = 0;              // mode 2: keys above it are in, of those equal the first `left`
   int left = 0;
   if (k > 0) {
-    const float band = band_of(p, r, h, lrow);
+    const float band = band_of(m_norm, p.q_norm[lrow]);
     const bool all = !(band < 1e38f), pairs = band > 1e-18f && band < 1e18f;
     if (!all) {
       // the k-th largest, as in the warps' form: counts of the keys at or above a
