@@ -574,7 +574,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 
 // The 64-bit score of block j, formed by a warp; NaN ranks as +inf.
-__device__ __noinline__ double exact_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
+__device__ __forceinline__ double exact_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
   const int lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
   const __nv_bfloat16* kb = bounds_at(p, r.b, j, h);
@@ -595,19 +595,33 @@ __device__ __noinline__ double exact_score(const SelectParams& p, const RowSpan&
   return best;
 }
 
-// The same from pairs of fp32 (products of bf16 are exact in fp32; each addition
-// leaves its error in the second number: Knuth's two-sum), where the row's scores
-// lie well within fp32's range: 2^-46 of the sum of magnitudes, no more than a sum
-// of 256 terms in double precision may be off by, at 60 times its rate here.
-struct Pair {
-  float h, l;
+// The same from sums of three fp32 numbers (products of bf16 are exact in fp32; an
+// addition leaves its error in the second number, and that one's in the third:
+// Knuth's two-sum, cascaded as in Ogita, Rump and Oishi's SumK with K = 3), where
+// the row's scores lie well within fp32's range.  Off by (2 n 2^-24)^3 of the sum of
+// magnitudes, 2^-48 for n = 128 terms, where double precision guarantees 2^-46; at
+// many times its rate here.  (Two numbers lose 2^-43, and blocks that double
+// precision tells apart came out in the wrong order.)
+struct Triple {
+  float h, m, l;
 };
-__device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
-  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
-  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
-  return {s, __fadd_rn(__fadd_rn(a.l, b.l), e)};
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return s;
 }
-__device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
+__device__ __forceinline__ Triple add_to(Triple a, float x) {
+  float e, f;
+  const float h = two_sum(a.h, x, e), m = two_sum(a.m, e, f);
+  return {h, m, __fadd_rn(a.l, f)};
+}
+// the same whichever comes first, so that all lanes of a sum end with the same
+__device__ __forceinline__ Triple add_triples(Triple a, Triple b) {
+  float e, f, g;
+  const float h = two_sum(a.h, b.h, e), ab = two_sum(a.m, b.m, f), m = two_sum(ab, e, g);
+  return {h, m, __fadd_rn(__fadd_rn(a.l, b.l), __fadd_rn(f, g))};
+}
+__device__ __forceinline__ double triple_score(const SelectParams& p, const RowSpan& r, int token, int h, int j) {
   // eight lanes a head, four heads at a time
   const int lane = threadIdx.x & 31, sub = lane & 7, chunks = p.d >> 6;
   const int G = p.Hq / p.Hkv;
@@ -616,7 +630,7 @@ __device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& 
   double best = -INFINITY;
 #pragma unroll 1
   for (int g = lane >> 3; g < ((G + 3) & ~3); g += 4) {
-    Pair s = {0.f, 0.f};
+    Triple s = {0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const int at = c * 8 + sub;
@@ -625,15 +639,25 @@ __device__ __noinline__ double pair_score(const SelectParams& p, const RowSpan& 
       unpack8(kb[at], lo);
       unpack8(kb[(p.d >> 3) + at], hi);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = add_pair(s, {__fmul_rn(x[i], x[i] > 0.f ? hi[i] : lo[i]), 0.f});
+      for (int i = 0; i < 8; ++i) s = add_to(s, __fmul_rn(x[i], x[i] > 0.f ? hi[i] : lo[i]));
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
-      s = add_pair(s, {__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
-    best = fmax(best, static_cast<double>(s.h) + static_cast<double>(s.l));  // (head 0 again past the last one)
+      s = add_triples(s, {__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.m, o),
+                          __shfl_xor_sync(0xffffffffu, s.l, o)});
+    best = fmax(best, static_cast<double>(s.h) + (static_cast<double>(s.m) + static_cast<double>(s.l)));  // (head 0 again past the last one)
   }
   best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
   return fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
+}
+// triples: whether the row's scores have fp32's range; a sum that is very small may
+// all the same be one of products that fp32 does not hold.
+__device__ __noinline__ double score_again(const SelectParams& p, const RowSpan& r, int token, int h, int j, bool triples) {
+  if (triples) {
+    const double s = triple_score(p, r, token, h, j);
+    if (fabs(s) >= 0x1p-80) return s;
+  }
+  return exact_score(p, r, token, h, j);
 }
 
 // The largest |m|^2 of the blocks that a row sees, by a warp.
@@ -760,9 +784,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps, 8) choose_warp_kernel(const
     for (int m = 0; m < K; ++m)
       if (key[m] > hi || (between == left && key[m] >= lo)) take(m);
     if (between > left) {
-      // those between, by their 64-bit scores (in fp32 pairs where those have the range)
-      const bool pairs = band > 1e-18f && band < 1e18f;
-      auto exact = [&](int j) { return ordered64(pairs ? pair_score(p, r, token, h, j) : exact_score(p, r, token, h, j)); };
+      // those between, by their 64-bit scores (in sums of three fp32 where those have the range)
+      const bool triples = band > 1e-18f && band < 1e18f;
+      auto exact = [&](int j) { return ordered64(score_again(p, r, token, h, j, triples)); };
       if (between <= 32) {
         // a lane each
         unsigned long long u = 0;
@@ -887,7 +911,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
   int left = 0;
   if (k > 0) {
     const float band = band_of(m_norm, p.q_norm[lrow]);
-    const bool all = !(band < 1e38f), pairs = band > 1e-18f && band < 1e18f;
+    const bool all = !(band < 1e38f), triples = band > 1e-18f && band < 1e18f;
     if (!all) {
       // the k-th largest, as in the warps' form: counts of the keys at or above a
       // value, a bit at a time
@@ -972,7 +996,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
       if (between <= kBand) {
         mode = 1;
         for (int m = warp; m < between; m += kThreads / 32) {
-          const double x = pairs ? pair_score(p, r, token, h, c0 + s_id[m]) : exact_score(p, r, token, h, c0 + s_id[m]);
+          const double x = score_again(p, r, token, h, c0 + s_id[m], triples);
           if (lane == 0) s_exact[m] = x;
         }
         __syncthreads();
@@ -996,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
           for (int i = warp; i < n; i += kThreads / 32) {
             const float x = score(i);
             if (!all && !(x >= t_lo && x <= t_hi)) continue;
-            const unsigned long long u = ordered64(exact_score(p, r, token, h, c0 + i));
+            const unsigned long long u = ordered64(score_again(p, r, token, h, c0 + i, false));
             if (lane == 0 && (shift == 56 || (u >> (shift + 8)) == cut)) atomicAdd(&s_hist[(u >> shift) & 255u], 1u);
           }
           __syncthreads();
@@ -1091,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const SelectParams p, 
         const float x = score(io);
         const bool certain = t_hi < INFINITY && x > t_hi;
         if (certain || (t_lo > -INFINITY && x < t_lo)) continue;
-        const unsigned long long u = ordered64(exact_score(p, r, token, h, c0 + io));
+        const unsigned long long u = ordered64(score_again(p, r, token, h, c0 + io, false));
         if (u > cut) above |= 1u << o;
         if (u == cut) equal |= 1u << o;
       }

@@ -57,3 +57,39 @@ def test_a_padded_token_beside_small_bounds(power):
     got = run(q, kb, table, [64 * 300], 9, 1, 1)
     assert torch.equal(got, P.select(q, kb, table, 64, [64 * 300], 9, 1, 1))
     assert got[0, 0, 0].tolist() == list(range(8)) + [299]
+
+
+@pytest.mark.parametrize("d,Nq", [(128, 1), (128, 70), (64, 1), (64, 70)])
+def test_scores_that_two_32_bit_numbers_do_not_tell_apart(d, Nq):
+    # 1 + 1.5 2^-25 and, for one block, many numbers of 2^-50, each less than half of what the second of two 32-bit
+    # numbers (2^-25 and up) resolves; for the other one number of 2^-48 that it does resolve.
+    n = 40
+    q, kb, table = case(3, 1, Nq, 1, 1, d, 64, n)
+    q[:] = 1
+    kb[:] = 0
+    many, one = torch.zeros(d), torch.zeros(d)
+    at = [i for i in range(d) if i % 64 < 8]
+    many[at] = 2.0 ** -50  # 6 or 14 of them stay: above 2^-48
+    many[0] = one[0] = 1
+    many[1] = one[1] = 1.5 * 2.0 ** -25
+    one[2] = 2.0 ** -48
+    kb[table[0, 9].long(), 0, 0] = many.to(torch.bfloat16)
+    kb[table[0, 4].long(), 0, 0] = one.to(torch.bfloat16)
+    want = P.select(q, kb, table, 64, [64 * n], 1, 0, 0)
+    assert want.flatten().tolist() == [9] * Nq
+    assert torch.equal(run(q, kb, table, [64 * n], 1, 0, 0), want)
+
+
+@pytest.mark.parametrize("Nq", [1, 60])
+def test_scores_of_products_that_32_bits_do_not_hold_beside_ordinary_norms(Nq):
+    n = 40
+    q, kb, table = case(5, 1, Nq, 1, 1, 64, 64, n)
+    g = torch.Generator().manual_seed(6)
+    q[:] = 0
+    q[..., 0], q[..., 1] = 1, 2.0 ** -72
+    kb[:] = 0
+    kb[:, 0, 0, :, 2] = 1  # the norms' part, which q does not meet
+    kb[:, 0, 0, :, 1] = ((128 + torch.randperm(len(kb), generator=g)) * 2.0 ** -79)[:, None].to(torch.bfloat16)
+    want = P.select(q, kb, table, 64, [64 * n], 9, 0, 0)
+    assert want[0, 0, 0].tolist() != list(range(9))
+    assert torch.equal(run(q, kb, table, [64 * n], 9, 0, 0), want)
