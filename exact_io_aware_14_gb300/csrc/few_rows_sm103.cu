@@ -22,9 +22,10 @@
 // The softmax has a thread for each key: its N scores from Tensor Memory, p to
 // shared memory as the next product's operand, a part of each row's sum of p in
 // its registers until the piece ends.  A row's exponent reference M is the
-// largest score of its first tile; p = 2^(x - M) keeps its relative precision in
-// bf16 and fp32 up to 2^127, so M moves (and O^T is rescaled in Tensor Memory)
-// only where x - M passes 96, on which the four warps vote once a tile.
+// largest score of its first tile; it moves (and O^T is rescaled in Tensor Memory)
+// only where x - M passes 8, on which the four warps vote once a tile, so that
+// p = 2^(x - M) stays below 2^8 and sums of p v have nearly all of fp32's range (with
+// p up to 2^96 values from 2^32 on passed it).
 //
 // The work is that of the lanes of rows_sm103.cu: an equal run of (unit, key
 // tile) for each CTA, pieces joined by the joining kernels there.  Scores, P,
@@ -631,7 +632,7 @@ __device__ __forceinline__ bool group_any(int grp, bool x) {
 }
 __device__ __forceinline__ void group_sync(int grp) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + grp) : "memory"); }
 
-constexpr float kMoveLog2 = 96.f;  // a row's reference moves where a score passes it by this much
+constexpr float kMoveLog2 = 8.f;  // a row's reference moves where a score passes it by this much
 
 template <int D, int kR, bool kList>
 struct Softmax {
@@ -669,7 +670,7 @@ struct Softmax {
     if (key < R) {
       const float mx = fmaxf(fmaxf(red[key], red[R + key]), fmaxf(red[2 * R + key], red[3 * R + key]));
       const float was = first ? -INFINITY : row[key];
-      const float m = was == -INFINITY || mx - was > 8.f ? fmaxf(was, mx) : was;
+      const float m = was == -INFINITY || mx - was > kMoveLog2 ? fmaxf(was, mx) : was;
       row[key] = m;
       red[key] = was == m ? 1.f : ex2_approx(was - m);  // its place was read by this thread
     }

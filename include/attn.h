@@ -471,8 +471,9 @@ ATTN_API size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, 
  *   workspace: attn_splitkv_paged_shared_workspace_size bytes, 16-byte aligned,
  *            contents ignored; one for each call that may run at once.
  * The weights enter the product with V rounded to bf16, as in attn_fwd.  Keys
- * and values that some row sees must be finite; behind a sequence's end there
- * may be anything.  Hq / Hkv is at most 128, B * Nq * Hq below 2^31 - 4096.
+ * and values that some row sees must be finite, and values of magnitude 2^80 at
+ * most, so that no sum of weighted ones passes fp32's range whatever the scores;
+ * behind a sequence's end there may be anything.  Hq / Hkv is at most 128, B * Nq * Hq below 2^31 - 4096.
  */
 ATTN_API attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_pages, const void* v_pages,
                                                    const int* block_table, int max_blocks, int page_size,
