@@ -637,7 +637,8 @@ def _attend(name, size, q, pools, Hkv, extra, scale, workspace, dev, *sizes):
 def decode_paged_shared(q, k_pages, v_pages, block_table, seqlens, shared_len, scale, workspace=None, stream=None):
     """Attention of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over a paged bf16 cache whose first
     shared_len keys (whole pages) all sequences have in common, the pages of row 0 of the block table
-    (attn_fwd_splitkv_paged_shared).  Returns (o, lse [B,Hq,Nq])."""
+    (attn_fwd_splitkv_paged_shared).  Row i is the token at position seqlens - Nq + i: fewer new tokens than Nq are the
+    last rows of q, where kvcache_append_paged takes the first ones.  Returns (o, lse [B,Hq,Nq])."""
     dev = _cuda_device(q)
     if stream is not None:
         with _on(stream, dev):
@@ -662,8 +663,9 @@ def kvcache_bounds_paged(k_pages, k_bounds, block_table, seqlens, max_new, new_l
 
 def select_blocks_paged(q, k_bounds, block_table, seqlens, topk, sink=1, local=1, workspace=None, stream=None):
     """The topk blocks of 64 keys whose bounds allow the largest scores, for each of the last Nq tokens q [B,Nq,Hq,d]
-    of each sequence and each KV head: int32 [B, Nq, Hkv, topk], ascending, -1 behind the last; the first `sink` and
-    the last `local` blocks that a token sees are among them (attn_select_blocks_paged)."""
+    of each sequence (row i at position seqlens - Nq + i) and each KV head: int32 [B, Nq, Hkv, topk], ascending, -1 behind
+    the last; the first `sink` and the last `local` blocks that a token sees are among them
+    (attn_select_blocks_paged)."""
     dev = _cuda_device(q)
     if stream is not None:
         with _on(stream, dev):
@@ -686,8 +688,9 @@ def select_blocks_paged(q, k_bounds, block_table, seqlens, topk, sink=1, local=1
 
 
 def attend_blocks_paged(q, k_pages, v_pages, block_table, seqlens, blocks, scale, workspace=None, stream=None):
-    """Attention of each of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence over the 64-key blocks listed for
-    it and its KV head, blocks int32 [B, Nq, Hkv, n] (attn_fwd_blocks_paged).  Returns (o, lse [B,Hq,Nq])."""
+    """Attention of each of the last Nq tokens q [B,Nq,Hq,d] bf16 of each sequence (row i at position seqlens - Nq + i)
+    over the 64-key blocks listed for it and its KV head, blocks int32 [B, Nq, Hkv, n] (attn_fwd_blocks_paged).  Returns
+    (o, lse [B,Hq,Nq])."""
     dev = _cuda_device(q)
     if stream is not None:
         with _on(stream, dev):

@@ -460,6 +460,9 @@ ATTN_API size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, 
  * for all sequences instead of once for each.  The last Nq tokens of each
  * sequence are the queries, masked causally among themselves: row i sees keys
  * 0 .. seqlens[b] - Nq + i, prefix and own ones alike.
+ * (Where fewer than Nq of a sequence's rows are new tokens they are its last rows,
+ * not its first as in the append; what the rows ahead of them hold is not looked
+ * at by any other row.)
  *   q [B,Nq,Hq,d] bf16, Nq >= 1; o [B,Nq,Hq,d] bf16 and lse [B,Hq,Nq] fp32
  *            out; a row that sees no key gets O = 0 and LSE = -inf; o must not
  *            overlap q;
@@ -485,6 +488,8 @@ ATTN_API attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_
  * Sparse attention over blocks of 64 keys, in three calls.  Block j of a
  * sequence is its keys 64 j .. 64 j + 63; new token n of Nq sits at position
  * seqlens[b] - Nq + n and sees the keys up to its own.
+ * (Of a sequence with fewer than Nq new tokens they are the last rows of q, as
+ * in attn_fwd_splitkv_paged_shared.)
  *
  * (1) Bounds of the keys, kept beside the key pages: k_bounds [num_pages,
  * page_size / 64, Hkv, 2, d] bf16 holds for each block, KV head and channel the
