@@ -1,4 +1,5 @@
-"""Block selection over more blocks than a CTA keeps the scores of, against the definition in 64 bits on the host."""
+"""Block selection over more blocks than a CTA keeps the scores of, and for many tokens with groups of every size that is
+read in its own way, against the definition in 64 bits on the host."""
 import pytest
 import torch
 
@@ -32,3 +33,10 @@ def test_more_blocks_than_are_kept(kind, n, topk, sink, local):
     q, kb, table = many_blocks(kind, n, 2)
     assert torch.equal(run(q, kb, table, [64 * n - 5], topk, sink, local),
                        P.select(q, kb, table, 64, [64 * n - 5], topk, sink, local))
+
+
+@pytest.mark.parametrize("Nq", [131, 129, 257])
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (3, 128), (4, 64), (5, 128), (8, 64), (9, 64)])
+def test_many_tokens_of_small_and_larger_groups(G, d, Nq):
+    q, kb, table = case(G + Nq, 1, Nq, 2 * G, 2, d, 64, 70)
+    assert torch.equal(run(q, kb, table, [4400], 6, 1, 1), P.select(q, kb, table, 64, [4400], 6, 1, 1))
