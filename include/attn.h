@@ -516,7 +516,8 @@ ATTN_API attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_boun
  *   sink, local >= 0, sink + local <= topk; Hq / Hkv is at most 128;
  *   workspace: attn_select_blocks_workspace_size(B, Nq, Hkv, max_blocks *
  *            page_size) bytes, 16-byte aligned, contents ignored; one for each
- *            call that may run at once.
+ *            call that may run at once (a wider table may need a little less:
+ *            each width has a size of its own).
  * The order is that of the scores in 64 bits (the products exact, the sums in
  * double precision); a score that is not a number ranks as +inf.
  */
@@ -527,7 +528,12 @@ ATTN_API attn_status attn_select_blocks_paged(const void* q, const void* k_bound
                                               int local, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace attn_fwd_blocks_paged needs with n_sel entries a list and
- * tables of max_seqlen keys (max_blocks * page_size); 0 for invalid arguments. */
+ * tables of max_seqlen keys (max_blocks * page_size); 0 for invalid arguments.
+ * The size follows the form that the sizes choose, so it does not rise with each
+ * of them: a narrower table may need far more (2048 tokens of 32 heads, 8 KV
+ * heads, d = 128, lists of 32: 1.3 MB with tables of 1 M keys, over 1 GB with
+ * 128 K).  A program that keeps one buffer for calls of several sizes takes the
+ * largest of their own sizes. */
 ATTN_API size_t attn_fwd_blocks_paged_workspace_size(int B, int Nq, int Hq, int Hkv, int d, int n_sel,
                                                      int max_seqlen);
 
