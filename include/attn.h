@@ -445,7 +445,11 @@ ATTN_API attn_status attn_kvcache_reserve_paged(int* block_table, int max_blocks
  * entries *free_count, ... of free_pages, the last sequence's last page first,
  * so that releasing what a reserve took restores the list.  block_table is left
  * as it is.  A keep_lens outside [0, seqlens[b]] (nothing is released) and pages
- * past num_pages of them (dropped) are reported as ATTN_ERR_DEVICE_ARG.
+ * past num_pages of them (dropped) are reported as ATTN_ERR_DEVICE_ARG.  So is an
+ * entry of the table outside [0, num_pages), which goes on the list all the same,
+ * in its place: leaving it out would shift what is behind it, so each sequence
+ * would have to look through the entries of all those released before it.  The
+ * list then has to be built anew; a reserve that takes the entry reports it again.
  */
 ATTN_API attn_status attn_kvcache_release_paged(const int* block_table, int max_blocks, int page_size, int num_pages,
                                                 const int* seqlens, const int* keep_lens, int* free_pages,
@@ -497,7 +501,9 @@ ATTN_API attn_status attn_fwd_splitkv_paged_shared(const void* q, const void* k_
  * them anew, from the pages, for the blocks that hold any of the last
  * new_lens[b] of sequence b's seqlens[b] tokens (NULL: the last Nn, or all of a
  * shorter sequence), each over all its keys before the sequence's end.  A NaN
- * key makes its channel's bounds NaN.  k_bounds must not overlap k_pages.
+ * key makes its channel's bounds NaN.  k_bounds must not overlap k_pages.  A
+ * block that several sequences have in common and that holds new tokens of one of
+ * them must lie before the end of each (whole pages of a common prefix do).
  */
 ATTN_API attn_status attn_kvcache_bounds_paged(const void* k_pages, void* k_bounds, const int* block_table,
                                                int max_blocks, int page_size, int num_pages, const int* seqlens,

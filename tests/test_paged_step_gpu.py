@@ -1,4 +1,5 @@
-"""A serving step over a paged bf16 cache in which the sequences' new tokens differ in number, against 64 bits."""
+"""A serving step over a paged bf16 cache in which the sequences' new tokens differ in number, against 64 bits, and one with
+a bad page in its table."""
 import pytest
 import torch
 
@@ -48,3 +49,16 @@ def test_a_step_of_sequences_with_different_counts_of_new_tokens():
             assert torch.equal(chosen, P.select(qb, kb.cpu(), tb, page, [new[b]], 3, 1, 1))
             P.check(*one(sparse), P.attend(qb, host[0], host[1], tb, page, d ** -0.5, listed(chosen, [new[b]], m)))
         lens = after
+
+
+def test_a_bad_page_that_is_released_is_reported_again_by_the_reserve_that_takes_it():
+    table, free = i32([[3, 99, 5], [6, -1, -1]]), i32([0, 1, 2, -7, -7, -7, -7, -7])
+    count = A.kvcache_release_paged(table, i32([192, 64]), i32([0, 0]), free, i32([3]), 64)
+    assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_ARG
+    assert int(count) == 7 and free.tolist() == [0, 1, 2, 6, 5, 99, 3, -7]
+    fresh = i32([[-1, -1, -1]])
+    granted, slots, count = A.kvcache_reserve_paged(fresh, i32([0]), i32([64]), free, count, 64, 64)
+    assert A.attn_get_device_status() == 0 and int(count) == 6 and fresh.tolist() == [[3, -1, -1]]
+    granted, slots, count = A.kvcache_reserve_paged(fresh, i32([64]), i32([64]), free, count, 64, 64)
+    assert A.attn_get_device_status() == A.ATTN_ERR_DEVICE_ARG
+    assert int(count) == 5 and slots.tolist() == [[-1] * 64]  # no row of the pools is named for its tokens
