@@ -718,10 +718,12 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 }
 
 // A warp for a row of up to 32 K blocks, block 32 m + lane in element m of a lane.
-// Bound by its instructions, one warp's waiting for those before, so by the warps
-// there are: with 64 registers, eight CTAs an SM, 2048 tokens and 8 KV heads take
-// 103 us on 512 blocks (114 with the 108 that the compiler takes by itself), 184
-// (235) on 1024, 446 (566) on 2048.
+// Bound by a warp's chain of instructions, each count of the keys waiting for the one
+// before (512 blocks: 2.0 instructions an SM and cycle of 4), so by the warps there
+// are: with 64 registers, eight CTAs an SM, 2048 tokens and 8 KV heads take 102 us on
+// 512 blocks (115 with the 108 that the compiler takes by itself), 182 (235) on 1024,
+// 445 (549) on 2048, although a thread then spills 0.3, 0.6, 0.9 and 3.4 KB for K = 8,
+// 16, 32 and 64.
 constexpr int kChooseWarps = 4;
 template <int K>
 __global__ void __launch_bounds__(32 * kChooseWarps, 8) choose_warp_kernel(const SelectParams p, int token0, int rows) {

@@ -477,7 +477,8 @@ ATTN_API size_t attn_splitkv_paged_shared_workspace_size(int B, int Nq, int Hq, 
  *            each sequence is read by itself;
  *   workspace: attn_splitkv_paged_shared_workspace_size bytes, 16-byte aligned,
  *            contents ignored; one for each call that may run at once.
- * The weights enter the product with V rounded to bf16, as in attn_fwd.  Keys
+ * The weights enter the product with V rounded to bf16, as in attn_fwd (in
+ * attn_fwd_splitkv_paged, for one token and nothing in common, they keep 32 bits).  Keys
  * and values that some row sees must be finite, and values of magnitude 2^80 at
  * most, so that no sum of weighted ones passes fp32's range whatever the scores;
  * behind a sequence's end there may be anything.  Hq / Hkv is at most 128, B * Nq * Hq below 2^31 - 4096.
